@@ -21,6 +21,8 @@
  * The DFlash-style variant: pe_inject_kv projects the verifier's hidden states
  * straight into the drafter's KV cache.
  *
+ * A KV cache in 4 bits: pe_pack_kv, pe_unpack_kv, pe_attend_packed.
+ *
  * Conventions shared by every entry point:
  *
  * - Memory.  Unless stated otherwise a pointer argument is a DEVICE pointer to
@@ -354,6 +356,86 @@ pe_status pe_step(const pe_config *cfg, const pe_weights *w, const pe_kv *kv, co
                   void *workspace, size_t workspace_bytes, int32_t *draft_tokens, int32_t *num_accepted_out,
                   int32_t *bonus_out, int32_t *next_prev_tokens, int32_t *next_prev_pos, float *logits_dbg,
                   int32_t *err_word, pe_stream_t stream);
+
+/*
+ * The packed KV cache: a paged cache in 4 bits per entry, 0.28 of the bytes of the bf16 one.
+ * The P-EAGLE pages keep the drafter's cache in the model's type; they have no counterpart.
+ *
+ * pool [num_pages][n_kv][18 * head_dim] bytes (pe_packed_page_bytes(cfg) per page), 16-byte
+ * aligned: for each page of 16 positions and each kv head the key codes (16 rows of head_dim/2
+ * bytes, one per position), the value codes, the key scales (16 rows of head_dim/16 bytes) and
+ * the value scales.
+ *
+ * Blocks of 16 consecutive entries of a head's row share one scale byte c,
+ *   s(c) = (1 + (c & 7)/8) * 2^((c >> 3) - 19),
+ * the smallest with 7 s(c) >= the block's largest magnitude (at least c = 0).  Entry x is kept
+ * as the whole number n = sign(x) * min(7, floor(|x| / s + 1/2)) and stands for n * s, which is
+ * exact in bf16.  So an entry is off by at most s/2, and s is at most 9/8 of a seventh of the
+ * block's largest magnitude (blocks whose largest magnitude is below 7 * 2^-19: s = 2^-19).
+ * Codes are stored as the nibble n + 8, as 32-bit words of eight nibbles (nibble i in bits
+ * 4i..4i+3), in this order within a row:
+ *   keys    word t*(hd/32) + u, t < 4: nibbles 0..3 hold entries 16(2u + i/2) + 4t + 2(i%2),
+ *           nibbles 4..7 the entry after each of these;
+ *   values  word g*(hd/64) + h, g < 8: nibble i holds entry 64h + 16(i/2) + g + 8(i%2).
+ * Any byte pattern stands for finite values, so positions that no row sees need not be written.
+ *
+ * These calls read only B, n_q, n_kv, head_dim, page_size, max_pages_per_seq and dtype of
+ * *cfg: B, n_q, n_kv, max_pages_per_seq >= 1, n_kv divides n_q, page_size 16, head_dim 64 or 128.
+ * A slot is page * 16 + position % 16.  Strides are in elements, from one row to the next, at
+ * least the row's length and a multiple of 16 bytes; rows are 16-byte aligned.
+ */
+
+/*
+ * Packs rows as they are written: k and v [n_rows][n_kv * head_dim] of cfg->dtype go to
+ * slots[row] (int64); -1: the row is passed over.  Slots other than -1 must differ: of two
+ * rows with one slot any mixture may be kept.  Device checks: a slot outside the pool
+ * (PE_DEV_BAD_PAGE, the row is passed over); a NaN or infinite entry (PE_DEV_NONFINITE: NaN is
+ * kept as 0, infinity as +-7 of its block's scale, which comes from the finite entries).
+ * Entries beyond 7 * s(255) = 53760 are kept as that.  n_rows = 0: nothing is launched.
+ */
+pe_status pe_pack_kv(const pe_config *cfg, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                     const int64_t *slots, int32_t n_rows, void *pool, int32_t num_pages, int32_t *err_word,
+                     pe_stream_t stream);
+
+/*
+ * Reads entries back as the values they stand for: k_out and v_out [n_rows][n_kv * head_dim]
+ * of cfg->dtype, row by row from slots[row].  A row with slot -1 is left as it is, and so is
+ * one with a slot outside the pool (PE_DEV_BAD_PAGE).  A slot may come more than once.
+ */
+pe_status pe_unpack_kv(const pe_config *cfg, const void *pool, int32_t num_pages, const int64_t *slots,
+                       int32_t n_rows, void *k_out, void *v_out, int64_t k_stride, int64_t v_stride,
+                       int32_t *err_word, pe_stream_t stream);
+
+/*
+ * Causal grouped-query attention over a packed cache.  Sequence b has the query rows
+ * row_start[b] .. row_start[b+1] - 1 (row_start [B+1], none to max_rows each); row r is
+ * q [n_rows][n_q * head_dim] of cfg->dtype and sees the positions 0..positions[r] of its sequence
+ * through block_table [B][max_pages_per_seq]:
+ *   out[r][h] = sum_x w_x v_x / sum_x w_x,   w_x = exp(q[r][h] . k_x / sqrt(head_dim)),
+ * keys and values of kv head h / (n_q / n_kv), as the cache's entries stand for them.
+ * positions[r] = -1: the row sees nothing and gets zeros.  Rows outside
+ * row_start[0] .. row_start[B] - 1 are left as they were.  n_rows (at most 65536) bounds the
+ * rows, max_rows those of one sequence; both bounds choose the kernels, so the closer the better.
+ * fp32: products and sums keep fp32 accuracy.  bf16: the softmax weights are rounded to
+ * bf16 (by at most 2^-8 of each) before the product with the values; scores, statistics and sums are
+ * fp32.  out must not overlap q; rows of both in one buffer, side by side with one stride, do not.
+ * Device checks: rows of a sequence outside [0, n_rows], fewer than none or more than
+ * max_rows (PE_DEV_BAD_ROW: the sequence's rows are left as they were); a position below -1 or beyond
+ * the block table (PE_DEV_BAD_POSITION: the row gets zeros); a page id that a row sees
+ * outside the pool (PE_DEV_BAD_PAGE: its keys and values count as zeros).
+ * workspace: 256-byte aligned, >= pe_attend_workspace_bytes(cfg) bytes (a size that depends on
+ * the GPU, head_dim and dtype alone), contents need not be initialised; not to be used by two
+ * calls, or replays of captured ones, that run concurrently.
+ */
+pe_status pe_attend_packed(const pe_config *cfg, const void *q, int64_t q_stride, const void *pool,
+                           int32_t num_pages, const int32_t *block_table, const int32_t *row_start,
+                           const int32_t *positions, int32_t n_rows, int32_t max_rows, void *out,
+                           int64_t out_stride, void *workspace, size_t workspace_bytes, int32_t *err_word,
+                           pe_stream_t stream);
+
+/* Bytes of one page of a packed pool, and of pe_attend_packed's workspace (0: invalid config). */
+size_t pe_packed_page_bytes(const pe_config *cfg);
+size_t pe_attend_workspace_bytes(const pe_config *cfg);
 
 /*
  * Tracing (optional).  pe_draft_forward and pe_step can record caller-created

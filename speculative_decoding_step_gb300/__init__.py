@@ -19,6 +19,8 @@ from .build import LIB, build
 __all__ = [
     "PeError", "Config", "DeviceWeights", "DeviceKV", "lib", "build", "check_config", "workspace_bytes",
     "prepare_batch", "scatter_hidden", "draft_forward", "verify", "step", "status_str",
+    "pack_kv", "unpack_kv", "attend_packed", "packed_page_bytes", "attend_workspace_bytes", "alloc_packed_pool",
+    "alloc_attend_workspace",
     "PE_OK", "PE_DEV_BAD_TOKEN", "PE_DEV_BAD_ACCEPTED", "PE_DEV_BAD_PAGE", "PE_DEV_BAD_POSITION",
     "PE_DEV_NONFINITE", "PE_DEV_BAD_ROW", "PE_DEV_TIMEOUT", "EXPORTED_SYMBOLS",
 ]
@@ -37,7 +39,8 @@ EXPORTED_SYMBOLS = ["pe_prepare_batch", "pe_scatter_hidden", "pe_draft_forward",
                     "pe_sample_drafts", "pe_verify_sampled",
                     "pe_workspace_bytes", "pe_check_config", "pe_status_str", "pe_set_trace_events",
                     "pe_trace_points", "pe_kernel_launches", "pe_draft_forward_noalloc", "pe_set_wait_limit_ns",
-                    "pe_test_skip_pipeline_stage", "pe_inject_kv"]
+                    "pe_test_skip_pipeline_stage", "pe_inject_kv", "pe_pack_kv", "pe_unpack_kv", "pe_attend_packed",
+                    "pe_packed_page_bytes", "pe_attend_workspace_bytes"]
 
 # Size of the library-owned scratch used by pe_draft_forward_noalloc (PE_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 48 << 20
@@ -159,8 +162,16 @@ def lib():
         L.pe_inject_kv.argtypes = [cp, ctypes.POINTER(_Weights), vp, ctypes.POINTER(_KV), vp, vp, vp, vp, vp,
                                    ctypes.c_size_t, vp, vp]
         L.pe_test_skip_pipeline_stage.argtypes = [i32]
+        i64 = ctypes.c_int64
+        L.pe_pack_kv.argtypes = [cp, vp, vp, i64, i64, vp, i32, vp, i32, vp, vp]
+        L.pe_unpack_kv.argtypes = [cp, vp, i32, vp, i32, vp, vp, i64, i64, vp, vp]
+        L.pe_attend_packed.argtypes = [cp, vp, i64, vp, i32, vp, vp, vp, i32, i32, vp, i64, vp, ctypes.c_size_t, vp, vp]
+        for name in ("pe_packed_page_bytes", "pe_attend_workspace_bytes"):
+            getattr(L, name).restype = ctypes.c_size_t
+            getattr(L, name).argtypes = [cp]
         for name in EXPORTED_SYMBOLS:
-            if name not in ("pe_status_str", "pe_workspace_bytes", "pe_kernel_launches"):
+            if name not in ("pe_status_str", "pe_workspace_bytes", "pe_kernel_launches", "pe_packed_page_bytes",
+                            "pe_attend_workspace_bytes"):
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -297,6 +308,100 @@ def inject_kv(cfg, weights: DeviceWeights, w_inj, kv: DeviceKV, block_table, pre
     _check(st, "pe_inject_kv")
 
 
+def _tensor(t, what: str, device, dtype, shape=None) -> int:
+    """Address of a contiguous tensor of this type (and shape) on this device."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor{'' if shape is None else f' of shape {shape}'} "
+                         f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t, what: str, device, dtype, width: int, n: int):
+    """Address and row stride of n rows of `width` elements ([n][width] or [n][heads][head_dim], each row
+    contiguous)."""
+    if t.dtype != dtype or t.device != device or t.dim() < 2 or t.shape[0] != n:
+        raise ValueError(f"{what}: expected {n} rows of {dtype} on {device}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    inner = 1
+    for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
+        if size != 1 and stride != inner:
+            raise ValueError(f"{what}: the elements of a row have to be contiguous")
+        inner *= size
+    if inner != width:
+        raise ValueError(f"{what}: rows of {inner} elements, expected {width}")
+    return t.data_ptr(), t.stride(0) if n > 1 else width
+
+
+def _current(t) -> torch.device:
+    """The device of a call's tensors, which has to be the current one (its stream is used)."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"expected tensors on the current CUDA device, got {t.device}")
+    return t.device
+
+
+def packed_page_bytes(cfg) -> int:
+    """Bytes of one page (16 positions, every kv head) of a packed cache; 0 for an invalid config."""
+    return int(lib().pe_packed_page_bytes(ctypes.byref(cfg)))
+
+
+def attend_workspace_bytes(cfg) -> int:
+    """Workspace of attend_packed (depends on the GPU, head_dim and dtype alone)."""
+    return int(lib().pe_attend_workspace_bytes(ctypes.byref(cfg)))
+
+
+def _pool(cfg, pool, device):
+    return _tensor(pool, "pool", device, torch.uint8, (pool.shape[0], cfg.n_kv, 18 * cfg.head_dim)), pool.shape[0]
+
+
+def pack_kv(cfg, k, v, slots, pool, err, stream=None):
+    """Round rows k, v ([n][n_kv][head_dim] or [n][n_kv*head_dim], any row stride of whole 16 bytes) to 4 bits
+    and write them to the packed cache ``pool`` (alloc_packed_pool) at ``slots`` (int64; -1: passed over)."""
+    L, dev, n, w = lib(), _current(pool), slots.shape[0], cfg.n_kv * cfg.head_dim
+    dt = cfg.torch_dtype
+    kp, ks = _rows(k, "k", dev, dt, w, n)
+    vp, vs = _rows(v, "v", dev, dt, w, n)
+    pp, pages = _pool(cfg, pool, dev)
+    if n == 0:
+        return
+    st = L.pe_pack_kv(ctypes.byref(cfg), kp, vp, ks, vs, _tensor(slots, "slots", dev, torch.int64, (n,)), n, pp, pages,
+                      _tensor(err, "err", dev, torch.int32), _stream(stream))
+    _check(st, "pe_pack_kv")
+
+
+def unpack_kv(cfg, pool, slots, k_out, v_out, err, stream=None):
+    """Read the entries at ``slots`` back as the values they stand for (-1: the output row stays as it is)."""
+    L, dev, n, w = lib(), _current(pool), slots.shape[0], cfg.n_kv * cfg.head_dim
+    dt = cfg.torch_dtype
+    kp, ks = _rows(k_out, "k_out", dev, dt, w, n)
+    vp, vs = _rows(v_out, "v_out", dev, dt, w, n)
+    pp, pages = _pool(cfg, pool, dev)
+    if n == 0:
+        return
+    st = L.pe_unpack_kv(ctypes.byref(cfg), pp, pages, _tensor(slots, "slots", dev, torch.int64, (n,)), n, kp, vp, ks, vs,
+                        _tensor(err, "err", dev, torch.int32), _stream(stream))
+    _check(st, "pe_unpack_kv")
+
+
+def attend_packed(cfg, q, pool, block_table, row_start, positions, max_rows, out, workspace, err, stream=None):
+    """Causal grouped-query attention over a packed cache: sequence b's rows row_start[b]..row_start[b+1]-1 of
+    q [n][n_q*head_dim], row r seeing positions 0..positions[r] (-1: none, zeros); ``max_rows`` bounds the rows of
+    one sequence.  ``workspace``: alloc_attend_workspace."""
+    L, dev, n, w = lib(), _current(pool), positions.shape[0], cfg.n_q * cfg.head_dim
+    dt, i32 = cfg.torch_dtype, torch.int32
+    qp, qs = _rows(q, "q", dev, dt, w, n)
+    op, os_ = _rows(out, "out", dev, dt, w, n)
+    pp, pages = _pool(cfg, pool, dev)
+    if n == 0:
+        return
+    st = L.pe_attend_packed(ctypes.byref(cfg), qp, qs, pp, pages,
+                            _tensor(block_table, "block_table", dev, i32, (cfg.B, cfg.max_pages_per_seq)),
+                            _tensor(row_start, "row_start", dev, i32, (cfg.B + 1,)),
+                            _tensor(positions, "positions", dev, i32, (n,)), n, max_rows, op, os_,
+                            _tensor(workspace, "workspace", dev, torch.uint8), workspace.shape[0],
+                            _tensor(err, "err", dev, i32), _stream(stream))
+    _check(st, "pe_attend_packed")
+
+
 def step(cfg, weights: DeviceWeights, kv: DeviceKV, block_table, prev_tokens, prev_pos, num_accepted, bonus,
          target_hidden, target_tokens, workspace, out: dict, err, logits_dbg=None, stream=None):
     """One whole round.  ``out`` holds draft_tokens, num_accepted, bonus, next_prev_tokens, next_prev_pos."""
@@ -326,6 +431,20 @@ def alloc_workspace(cfg: Config, device="cuda") -> torch.Tensor:
     n = workspace_bytes(cfg)
     if n == 0:
         raise PeError(check_config(cfg), "pe_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def alloc_packed_pool(cfg: Config, num_pages: int, device="cuda") -> torch.Tensor:
+    """A packed KV cache of ``num_pages`` pages (pack_kv, attend_packed)."""
+    if packed_page_bytes(cfg) == 0:
+        raise PeError(2, "pe_packed_page_bytes")
+    return torch.zeros((num_pages, cfg.n_kv, 18 * cfg.head_dim), dtype=torch.uint8, device=device)
+
+
+def alloc_attend_workspace(cfg: Config, device="cuda") -> torch.Tensor:
+    n = attend_workspace_bytes(cfg)
+    if n == 0:
+        raise PeError(2, "pe_attend_workspace_bytes")
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 

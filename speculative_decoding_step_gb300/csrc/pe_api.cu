@@ -46,6 +46,8 @@ void trace(int point, cudaStream_t s) {
 }
 
 constexpr int kMaxRows = 1 << 16;        // B*2K
+constexpr int kMaxPackedHeads = 1 << 12;  // query heads of a packed-cache call
+constexpr int kMaxPackedPages = 1 << 24;  // block-table row length of a packed-cache call
 constexpr int kAttnItemsPerSlot = 4;     // attention work items aimed for, per resident CTA (load balance)
 constexpr int kAttnMinChunk = 256;       // shortest position chunk of a work item (bounds the chunks to merge)
 constexpr int kTcMaxStages = 12;
@@ -359,6 +361,24 @@ pe_status check_cfg(const pe_config* c) {
   return PE_OK;
 }
 
+// The fields that the packed-cache calls read.
+pe_status check_packed_cfg(const pe_config* c) {
+  if (c == nullptr) return PE_ERR_INVALID_ARG;
+  if (c->dtype != PE_F32 && c->dtype != PE_BF16) return PE_ERR_INVALID_ARG;
+  if (c->B < 1 || c->n_q < 1 || c->n_kv < 1 || c->max_pages_per_seq < 1 || c->n_q % c->n_kv != 0) return PE_ERR_SHAPE;
+  if (c->B > kMaxRows || c->n_q > kMaxPackedHeads || c->max_pages_per_seq > kMaxPackedPages) return PE_ERR_SHAPE;
+  if (c->page_size != 16) return PE_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128) return PE_ERR_UNSUPPORTED;
+  return PE_OK;
+}
+
+// Rows of `width` elements at p, `stride` elements apart.
+pe_status check_rows(const pe_config& c, const void* p, int64_t stride, int64_t width) {
+  if (p == nullptr || !aligned16(p) || stride < width || stride > (int64_t(1) << 40)) return PE_ERR_INVALID_ARG;
+  if ((stride * (int64_t)elem_bytes(c.dtype)) % 16 != 0) return PE_ERR_INVALID_ARG;
+  return PE_OK;
+}
+
 #define PE_TRY_CUDA(expr)                         \
   do {                                            \
     if ((expr) != cudaSuccess) return PE_ERR_CUDA; \
@@ -477,6 +497,20 @@ bool overlaps(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi;
 Span span_of(const void* p, size_t bytes) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
   return Span{lo, lo + bytes};
+}
+// Whether n rows of `width` elements at x and at y share no byte: apart altogether, or side by
+// side in one buffer with the same stride.
+bool rows_disjoint(const pe_config& c, const void* x, int64_t x_stride, const void* y, int64_t y_stride, int64_t width,
+                   int64_t n) {
+  const size_t eb = elem_bytes(c.dtype);
+  if (!overlaps(span_of(x, eb * (size_t)((n - 1) * x_stride + width)),
+                span_of(y, eb * (size_t)((n - 1) * y_stride + width))))
+    return true;
+  if (x_stride != y_stride) return false;
+  const int64_t stride = x_stride * (int64_t)eb, w = width * (int64_t)eb;
+  int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(y) - reinterpret_cast<uintptr_t>(x)) % stride;
+  if (d < 0) d += stride;
+  return d >= w && d + w <= stride;
 }
 bool step_aliasing_ok(const pe_config& c, const int32_t* block_table, const int32_t* prev_tokens,
                       const int32_t* prev_pos, const int32_t* num_accepted, const int32_t* bonus,
@@ -981,6 +1015,78 @@ pe_status pe_inject_kv(const pe_config* cfg, const pe_weights* w, const void* w_
     GemmCall call{EPI_QKV_ROPE, &p.injkv, wkv, y, c.d, c.n_kv * hd, NI, nullptr, 2, (uint64_t)(2 * c.n_kv)};
     if ((st = run_gemm(c, p, ws, call, a, s)) != PE_OK) return st;
   }
+  return PE_OK;
+}
+
+pe_status pe_pack_kv(const pe_config* cfg, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                     const int64_t* slots, int32_t n_rows, void* pool, int32_t num_pages, int32_t* err_word,
+                     pe_stream_t stream) {
+  pe_status st = check_packed_cfg(cfg);
+  if (st != PE_OK) return st;
+  const int64_t width = (int64_t)cfg->n_kv * cfg->head_dim;
+  if ((st = check_rows(*cfg, k, k_stride, width)) != PE_OK || (st = check_rows(*cfg, v, v_stride, width)) != PE_OK)
+    return st;
+  if (!slots || !pool || !err_word || !aligned16(pool)) return PE_ERR_INVALID_ARG;
+  if (n_rows < 0 || num_pages < 1) return PE_ERR_SHAPE;
+  PackArgs a{};
+  a.n_rows = n_rows; a.k = k; a.v = v; a.k_stride = k_stride; a.v_stride = v_stride; a.slots = slots;
+  a.n_kv = cfg->n_kv; a.head_dim = cfg->head_dim; a.pool = static_cast<uint8_t*>(pool); a.num_pages = num_pages;
+  a.err = err_word;
+  PE_TRY_CUDA(launch_pack(a, cfg->dtype, (cudaStream_t)stream));
+  return PE_OK;
+}
+
+pe_status pe_unpack_kv(const pe_config* cfg, const void* pool, int32_t num_pages, const int64_t* slots,
+                       int32_t n_rows, void* k_out, void* v_out, int64_t k_stride, int64_t v_stride,
+                       int32_t* err_word, pe_stream_t stream) {
+  pe_status st = check_packed_cfg(cfg);
+  if (st != PE_OK) return st;
+  const int64_t width = (int64_t)cfg->n_kv * cfg->head_dim;
+  if ((st = check_rows(*cfg, k_out, k_stride, width)) != PE_OK ||
+      (st = check_rows(*cfg, v_out, v_stride, width)) != PE_OK)
+    return st;
+  if (!slots || !pool || !err_word || !aligned16(pool)) return PE_ERR_INVALID_ARG;
+  if (n_rows < 0 || num_pages < 1) return PE_ERR_SHAPE;
+  UnpackArgs a{};
+  a.n_rows = n_rows; a.pool = static_cast<const uint8_t*>(pool); a.num_pages = num_pages; a.slots = slots;
+  a.n_kv = cfg->n_kv; a.head_dim = cfg->head_dim; a.k_out = k_out; a.v_out = v_out; a.k_stride = k_stride;
+  a.v_stride = v_stride; a.err = err_word;
+  PE_TRY_CUDA(launch_unpack(a, cfg->dtype, (cudaStream_t)stream));
+  return PE_OK;
+}
+
+size_t pe_packed_page_bytes(const pe_config* cfg) {
+  return check_packed_cfg(cfg) == PE_OK ? (size_t)cfg->n_kv * 18 * cfg->head_dim : 0;
+}
+
+size_t pe_attend_workspace_bytes(const pe_config* cfg) {
+  return check_packed_cfg(cfg) == PE_OK ? packed_attn_workspace_bytes(cfg->head_dim, cfg->dtype, num_sms()) : 0;
+}
+
+pe_status pe_attend_packed(const pe_config* cfg, const void* q, int64_t q_stride, const void* pool,
+                           int32_t num_pages, const int32_t* block_table, const int32_t* row_start,
+                           const int32_t* positions, int32_t n_rows, int32_t max_rows, void* out,
+                           int64_t out_stride, void* workspace, size_t workspace_bytes, int32_t* err_word,
+                           pe_stream_t stream) {
+  pe_status st = check_packed_cfg(cfg);
+  if (st != PE_OK) return st;
+  const int64_t width = (int64_t)cfg->n_q * cfg->head_dim;
+  if ((st = check_rows(*cfg, q, q_stride, width)) != PE_OK || (st = check_rows(*cfg, out, out_stride, width)) != PE_OK)
+    return st;
+  if (!pool || !block_table || !row_start || !positions || !workspace || !err_word || !aligned16(pool) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return PE_ERR_INVALID_ARG;
+  if (num_pages < 1 || n_rows < 0 || n_rows > kMaxRows || max_rows < (n_rows > 0 ? 1 : 0)) return PE_ERR_SHAPE;
+  const int sms = num_sms();
+  if (workspace_bytes < packed_attn_workspace_bytes(cfg->head_dim, cfg->dtype, sms)) return PE_ERR_SHAPE;
+  if (n_rows > 0 && !rows_disjoint(*cfg, q, q_stride, out, out_stride, width, n_rows)) return PE_ERR_INVALID_ARG;
+  PackedAttnArgs a{};
+  a.B = cfg->B; a.n_q = cfg->n_q; a.n_kv = cfg->n_kv; a.head_dim = cfg->head_dim; a.max_pages = cfg->max_pages_per_seq;
+  a.num_pages = num_pages; a.n_rows = n_rows; a.max_rows = std::min(max_rows, n_rows); a.scale = 1.0f / sqrtf((float)cfg->head_dim);
+  a.q = q; a.q_stride = q_stride; a.pool = static_cast<const uint8_t*>(pool); a.block_table = block_table;
+  a.row_start = row_start; a.positions = positions; a.out = out; a.out_stride = out_stride; a.workspace = workspace;
+  a.wait_ns = wait_limit_ns(); a.err = err_word;
+  PE_TRY_CUDA(launch_attend_packed(a, cfg->dtype, sms, (cudaStream_t)stream));
   return PE_OK;
 }
 

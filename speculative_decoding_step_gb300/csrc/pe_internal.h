@@ -321,4 +321,54 @@ cudaError_t launch_attention_bf16(const CUtensorMap& tmK, const CUtensorMap& tmV
                                   int sms, cudaStream_t s);
 cudaError_t launch_attention_f32(const AttnArgs& a, cudaStream_t s);
 
+// ----------------------------------------------------------------------------- packed (4-bit) KV cache
+
+// Rows k and v ([n_rows][n_kv*hd], strides in elements) rounded to 4 bits and written to the
+// pool at slots[row] (-1: passed over).
+struct PackArgs {
+  int n_rows;             // host upper bound
+  const int32_t* n_dev;   // actual rows (nullable)
+  const void *k, *v;
+  long long k_stride, v_stride;
+  const int64_t* slots;
+  int n_kv, head_dim;
+  uint8_t* pool;
+  int num_pages;
+  int32_t* err;
+};
+cudaError_t launch_pack(const PackArgs& a, pe_dtype dt, cudaStream_t s);
+
+// The entries at slots[row], as the values they stand for (-1: the output row is left as it is).
+struct UnpackArgs {
+  int n_rows;
+  const uint8_t* pool;
+  int num_pages;
+  const int64_t* slots;
+  int n_kv, head_dim;
+  void *k_out, *v_out;
+  long long k_stride, v_stride;
+  int32_t* err;
+};
+cudaError_t launch_unpack(const UnpackArgs& a, pe_dtype dt, cudaStream_t s);
+
+// Attention of ragged query rows over a packed pool; see pe_packed_attn.cu.
+struct PackedAttnArgs {
+  int B, n_q, n_kv, head_dim, max_pages, num_pages;
+  int n_rows, max_rows;          // host upper bounds: rows in all, rows of a sequence
+  float scale;                   // 1/sqrt(head_dim)
+  const void* q;                 // [n_rows][n_q*hd], stride in elements
+  long long q_stride;
+  const uint8_t* pool;
+  const int32_t *block_table, *positions;
+  const int32_t* row_start;      // [B+1], or [B] with row_len
+  const int32_t* row_len;        // nullable: rows of each sequence
+  void* out;                     // [n_rows][n_q*hd]
+  long long out_stride;
+  void* workspace;
+  uint64_t wait_ns;              // limit of every pipeline wait (wait_limit_ns())
+  int32_t* err;
+};
+size_t packed_attn_workspace_bytes(int head_dim, pe_dtype dt, int sms);
+cudaError_t launch_attend_packed(const PackedAttnArgs& a, pe_dtype dt, int sms, cudaStream_t s);
+
 }  // namespace pe

@@ -1,0 +1,49 @@
+// Format of the packed (4-bit) KV cache, shared by the kernels that write and read it.
+//
+// A pool holds [num_pages][n_kv] records of 18 * head_dim bytes, one per page of 16 positions
+// and kv head:
+//
+//   bytes [0, 8 hd)         key codes, one row of hd/2 bytes per position
+//   bytes [8 hd, 16 hd)     value codes, the same
+//   bytes [16 hd, 17 hd)    key scales, one row of hd/16 bytes per position
+//   bytes [17 hd, 18 hd)    value scales
+//
+// 16 consecutive entries of a row share one scale byte c, s(c) = (1 + (c & 7)/8) 2^((c >> 3) - 19):
+// the smallest with 7 s >= the block's largest magnitude.  An entry is kept as the whole number
+// n = sign(x) min(7, floor(|x|/s + 1/2)), stored as the nibble n + 8, and stands for n s.
+// n has three bits and s four significant ones, so n s has seven: exact in bf16, and the
+// tensor cores multiply what the cache stands for without a further rounding.
+//
+// Inside a row the nibbles stand in the order in which the matrix instructions take them,
+// as 32-bit words of eight (nibble i in bits 4i..4i+3):
+//   keys:   word t*(hd/32) + u (t < 4), nibble i < 4: entry 16(2u + i/2) + 4t + 2(i%2); nibble
+//           i + 4: the entry after it.
+//   values: word g*(hd/64) + h (g < 8), nibble i: entry 64h + 16(i/2) + g + 8(i%2).
+// Two nibbles 16 bits apart become one pair of bf16 with three operations (a shift, a
+// mask-and-or, one fused multiply-add): the nibble in the mantissa's upper bits of 1.0 reads
+// 1 + nibble/16, and (1 + nibble/16) S - 1.5 S = (nibble - 8)/16 S, exactly.  The scale byte in
+// the exponent and mantissa bits below a fixed upper exponent reads S = s 2^-12, so a key or
+// value of the matrix products is 2^-16 of what it stands for (kPackedUnit undoes that).
+#pragma once
+
+#include <stdint.h>
+
+#include "pe_device.cuh"
+
+namespace pe {
+
+constexpr int kPackedPage = 16;           // positions per record
+constexpr int kPackedBlock = 16;          // entries per scale
+constexpr float kPackedUnit = 65536.f;    // value of an entry over its bf16 form in the kernels
+
+template <int HD>
+struct PackedLayout {
+  static constexpr int kRow = HD / 2;     // bytes of one position's codes
+  static constexpr int kScaleRow = HD / kPackedBlock;
+  static constexpr int kK = 0, kV = 8 * HD, kKs = 16 * HD, kVs = 17 * HD, kRecord = 18 * HD;
+};
+
+// s(c) as fp32.
+PE_DEV float packed_scale(uint32_t c) { return __uint_as_float((c << 20) + (108u << 23)); }
+
+}  // namespace pe
