@@ -46,4 +46,34 @@ struct PackedLayout {
 // s(c) as fp32.
 PE_DEV float packed_scale(uint32_t c) { return __uint_as_float((c << 20) + (108u << 23)); }
 
+// Four of a word's eight nibbles as bf16 pairs 1 + nibble/16: nibble I in the lower half, I + 4 above.
+template <int I>
+PE_DEV uint32_t packed_pair(uint32_t w) {
+  constexpr int kShift[4] = {3, 1, 5, 9};
+  const uint32_t x = I == 0 ? w << kShift[I] : w >> kShift[I];
+  return (x & 0x00780078u) | 0x3F803F80u;
+}
+
+// Two scale bytes (the first or the second byte of either half of x) as bf16 pairs s 2^-12.
+PE_DEV uint32_t packed_scale_lo(uint32_t x) { return ((x << 4) & 0x0FF00FF0u) | 0x30003000u; }
+PE_DEV uint32_t packed_scale_hi(uint32_t x) { return ((x >> 4) & 0x0FF00FF0u) | 0x30003000u; }
+// Scale byte B of x as fp32 s 2^-12.
+template <int B>
+PE_DEV float packed_scale_f(uint32_t x) {
+  const uint32_t y = B == 3 ? x >> 4 : x << (20 - 8 * (B & 3));
+  return __uint_as_float((y & 0x0FF00000u) | 0x30000000u);
+}
+
+PE_DEV uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+PE_DEV uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+constexpr uint32_t kMinus15 = 0xBFC0BFC0u;  // -1.5 twice
+
 }  // namespace pe

@@ -5,7 +5,18 @@
 // cache positions 0..p of its sequence:
 //   out[r][h] = sum_{x <= p} w_x v_x / sum_{x <= p} w_x,  w_x = exp(q[r][h] . k_x / sqrt(hd) - max)
 // with keys and values of head h / (n_q / n_kv).  A row at position -1 sees nothing: zeros.
+//
+// Work.  The query vectors of a sequence and kv head (rows x G query heads, G = n_q / n_kv) are
+// cut into tiles; a (tile, kv head) pair's range of positions is counted in units of 64.  All units of
+// the launch form one line (tile after tile, head after head, position after position) that
+// N CTAs divide into equal pieces, so ragged lengths leave no CTA idle.  A range that lies in
+// one CTA's piece is finished there; one that is cut leaves a record per CTA (reference maximum,
+// sum, unnormalised output) that the merge kernel joins in CTA order.  Every CTA works the line
+// out for itself from row_start and positions (two dependent loads and a scan, about 2 us,
+// against a launch and a round trip through memory for a kernel that would do it once).
 #include <algorithm>
+#include <climits>
+#include <type_traits>
 
 #include "pe_internal.h"
 #include "pe_packed.cuh"
@@ -14,118 +25,792 @@ namespace pe {
 
 namespace {
 
-// One warp per (row, query head): lanes stride over the positions with an online softmax each,
-// then merge.
-template <typename T, int HD>
-__global__ void __launch_bounds__(256) attend_kernel(const PackedAttnArgs a) {
-  using L = PackedLayout<HD>;
-  pdl_wait();
-  pdl_trigger();
-  const long long gw = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const int row = (int)(gw / a.n_q), h = (int)(gw - (long long)row * a.n_q);
-  if (row >= a.n_rows) return;
-  int lo = 0, hi = a.B;  // the sequence whose rows hold `row`
+constexpr int kUnit = 64;           // positions per unit of work (four pages)
+constexpr int kPlanTiles = 1024;    // tiles per launch (their line is held in shared memory)
+constexpr int kWholePages = 32;     // tables of at most this many pages: no range is cut (and nothing to merge)
+constexpr float kRescaleLog2 = 8.f; // a reference maximum moves when a score exceeds it by more (log2 units)
+
+PE_DEV float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+PE_DEV uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+PE_DEV bool warp_ok(bool ok) { return __all_sync(0xFFFFFFFFu, ok); }
+
+// ----------------------------------------------------------------------------- the line of work
+
+struct Line {
+  int tile0, n_tiles;  // this launch's tiles: b * tps + t
+  int tps;             // tiles per sequence (host bound)
+  int tile_rows;       // query vectors per tile
+  int lanes;           // threads that look through one tile's rows (a power of two, at most 32)
+  int whole;           // every range is one unit
+  int min_units;       // a CTA's piece is at least this long where there are fewer units than that for all
+  int* prefix;         // workspace [n_tiles + 1]: units per head before each tile, for the merge
+  float* part;         // workspace: records of cut ranges, two per CTA
+};
+
+struct TileRows {
+  int r0, m0, M;  // first row of the sequence, first vector of the tile, vectors of the tile (0: none)
+};
+
+PE_DEV TileRows tile_rows(const PackedAttnArgs& a, const Line& ln, int tile) {
+  const int b = tile / ln.tps, t = tile - (tile / ln.tps) * ln.tps;
+  const int G = a.n_q / a.n_kv;
+  const int r0 = __ldcg(a.row_start + b);
+  const int r1 = a.row_len != nullptr ? r0 + __ldcg(a.row_len + b) : __ldcg(a.row_start + b + 1);
+  if (r0 < 0 || r1 < r0 || r1 > a.n_rows || r1 - r0 > a.max_rows) {
+    if (r1 != r0) set_err(a.err, PE_DEV_BAD_ROW);
+    return TileRows{0, 0, 0};
+  }
+  const int m0 = t * ln.tile_rows;
+  return TileRows{r0, m0, max(0, min((r1 - r0) * G - m0, ln.tile_rows))};
+}
+
+// A row's last visible position: -1 when it sees nothing or its position is out of range.
+PE_DEV int row_limit(const PackedAttnArgs& a, int row) {
+  const int p = __ldcg(a.positions + row);
+  if (p < -1 || p / kPackedPage >= a.max_pages) {
+    set_err(a.err, PE_DEV_BAD_POSITION);
+    return -1;
+  }
+  return p;
+}
+
+// prefix[k]: units per head before tile k; last[k]: largest position that tile k sees (-1: none).
+// Every thread of the CTA.
+PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, int* prefix, int* last, int* warp_sums) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int per = ln.lanes, sub = tid & (per - 1), G = a.n_q / a.n_kv;
+  for (int k0 = 0; k0 < ln.n_tiles; k0 += nt / per) {  // the same trip count for every thread
+    const int k = k0 + tid / per;
+    int mx = -1, M = 0;
+    if (k < ln.n_tiles) {
+      const TileRows t = tile_rows(a, ln, ln.tile0 + k);
+      M = t.M;
+      if (M > 0) {
+        const int ra = t.r0 + t.m0 / G, rb = t.r0 + (t.m0 + M - 1) / G;
+#pragma unroll 4
+        for (int r = ra + sub; r <= rb; r += per) mx = max(mx, row_limit(a, r));
+      }
+    }
+    for (int o = per >> 1; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    if (k < ln.n_tiles && sub == 0) {
+      prefix[k + 1] = M == 0 ? 0 : ln.whole ? 1 : max(1, (mx + kUnit) / kUnit);
+      last[k] = mx;
+    }
+  }
+  __syncthreads();
+  // inclusive scan of prefix[1..n]: a run of consecutive tiles per thread, then over threads
+  const int run = (ln.n_tiles + nt - 1) / nt, k0 = tid * run, k1 = min(ln.n_tiles, k0 + run);
+  int sum = 0;
+  for (int k = k0; k < k1; ++k) sum += prefix[k + 1];
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if ((tid & 31) >= o) inc += v;
+  }
+  if ((tid & 31) == 31) warp_sums[tid >> 5] = inc;
+  __syncthreads();
+  int before = inc - sum;
+  for (int w = 0; w < (tid >> 5); ++w) before += warp_sums[w];
+  if (tid == 0) prefix[0] = 0;
+  for (int k = k0; k < k1; ++k) {
+    before += prefix[k + 1];
+    prefix[k + 1] = before;
+  }
+  __syncthreads();
+}
+
+// CTAs that share T units, and the first unit of CTA c.
+PE_DEV int line_ctas(long long T, int grid, int min_units) {
+  return (int)min((long long)grid, max(1LL, T / min_units));
+}
+PE_DEV long long line_cut(long long T, int n, int c) { return T * c / n; }
+
+// The part of a (tile, head) range that a CTA works on.
+struct Segment {
+  int k, g;          // tile (of this launch), kv head
+  int page0, page1;  // its pages
+  bool from_start, to_end;
+  long long next;    // the unit after it
+};
+
+PE_DEV Segment segment_at(const Line& ln, const int* prefix, const int* last, int n_kv, int k, long long u,
+                          long long u1) {
+  Segment s;
+  const int nb = prefix[k + 1] - prefix[k];
+  const long long r = u - (long long)prefix[k] * n_kv;
+  s.k = k;
+  s.g = (int)(r / nb);
+  const int blk = (int)(r - (long long)s.g * nb);
+  const int cnt = (int)min((long long)(nb - blk), u1 - u);
+  s.from_start = blk == 0;
+  s.to_end = blk + cnt == nb;
+  s.next = u + cnt;
+  const int pages = (last[k] + kPackedPage) / kPackedPage;
+  s.page0 = ln.whole ? 0 : blk * (kUnit / kPackedPage);
+  s.page1 = ln.whole ? pages : min(pages, (blk + cnt) * (kUnit / kPackedPage));
+  return s;
+}
+PE_DEV Segment first_segment(const Line& ln, const int* prefix, const int* last, int n_kv, long long u, long long u1) {
+  int lo = 0, hi = ln.n_tiles;  // the last tile that starts at or before u
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldcg(a.row_start + mid) <= row) lo = mid;
+    if ((long long)prefix[mid] * n_kv <= u) lo = mid;
     else hi = mid;
   }
-  const int b = lo, r0 = __ldcg(a.row_start + b), r1 = a.row_len ? r0 + __ldcg(a.row_len + b) : __ldcg(a.row_start + b + 1);
-  if (r0 < 0 || r1 < r0 || r1 > a.n_rows || r1 - r0 > a.max_rows) {
-    if (lane == 0) set_err(a.err, PE_DEV_BAD_ROW);
-    return;
-  }
-  if (row < r0 || row >= r1) return;
-  int p = __ldcg(a.positions + row);
-  if (p < -1 || p >= a.max_pages * kPackedPage) {
-    if (lane == 0) set_err(a.err, PE_DEV_BAD_POSITION);
-    p = -1;
-  }
-  const int G = a.n_q / a.n_kv, g = h / G;
-  const T* q = static_cast<const T*>(a.q) + row * a.q_stride + (long long)h * HD;
-  float qr[HD], o[HD];
+  return segment_at(ln, prefix, last, n_kv, lo, u, u1);
+}
+PE_DEV Segment next_segment(const Line& ln, const int* prefix, const int* last, int n_kv, const Segment& s,
+                            long long u1) {
+  int k = s.k;
+  if (s.next >= (long long)prefix[k + 1] * n_kv)
+    do ++k;
+    while (prefix[k + 1] == prefix[k]);
+  return segment_at(ln, prefix, last, n_kv, k, s.next, u1);
+}
+
+// A record of a cut range: maximum and sum of each vector, then the outputs.
+template <int HD>
+PE_DEV float* part_record(const Line& ln, int cta, bool from_start) {
+  return ln.part + (size_t)(2 * cta + (from_start ? 1 : 0)) * ln.tile_rows * (HD + 2);
+}
+
+// ----------------------------------------------------------------------------- few query vectors: warp MMAs
+//
+// A warp takes whole pages (16 positions), brought into its own ring of shared-memory stages by one bulk
+// copy each, and runs on its own until the segment ends: S^T = K Q^T and O^T += V^T P^T with 16 x 8 x 16
+// warp MMAs, positions (then entries) on the 16 side and 8 query vectors on the other, so one
+// unpacked page serves NQ * 8 vectors and no row is padded beyond 8.
+//   Keys: a product per block of 16 entries over 1 + nibble/16, starting from -1.5 sum(q) (an MMA of
+//   -1.5s at the segment's start), is the block's sum over (nibble - 8)/16; times the scale in fp32.
+//   That saves the scale's multiplication for every pair.
+//   P: rounded to bf16 and transposed by movmatrix into the other product's operand.
+//   Values: two positions' words give pairs of positions; scaled as pairs (exact).
+// fp32: q and P are each split into three bf16 terms (24 bits), three MMAs for one; keys and values
+// are exact in bf16, so the products are those of fp32.
+// The eight warps' statistics and outputs join in shared memory at the end of a segment.
+
+constexpr int kSmallWarps = 8;
+
+template <typename T, int HD, int NQ>
+struct Small {
+  static constexpr int TERMS = sizeof(T) == 4 ? 3 : 1;
+  static constexpr int STAGES = HD == 64 ? 4 : 3;
+  static constexpr int ROWS = 8 * NQ;
+  static constexpr int OROW = HD + 4;  // floats per vector of the joint buffer (no bank conflicts)
+  static constexpr int CTAS = (NQ == 1 && TERMS == 1) || (HD == 64 && TERMS == 1) ? 2 : 1;  // per SM
+  static constexpr int RING = kSmallWarps * STAGES * PackedLayout<HD>::kRecord;
+  static constexpr int JOIN = kSmallWarps * ROWS * (OROW + 2) * 4;
+  static constexpr int FIXED = RING + JOIN + kSmallWarps * STAGES * 8 + 16 * 4 + 16;
+  static size_t smem(int n_tiles) { return 128 + FIXED + 8 * (size_t)(n_tiles + 1); }
+};
+
+PE_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+PE_DEV uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Pairs (x0, x1) as `TERMS` bf16 pairs whose sums are x0 and x1 (one term: rounded to bf16).
+template <int TERMS>
+PE_DEV void split_pair(float x0, float x1, uint32_t (&t)[TERMS]) {
 #pragma unroll
-  for (int e = 0; e < HD; ++e) {
-    qr[e] = to_float<T>(q[e]);
-    o[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int pos = lane; pos <= p; pos += 32) {
-    const int page = __ldcg(a.block_table + (size_t)b * a.max_pages + pos / kPackedPage);
-    const bool ok = page >= 0 && page < a.num_pages;
-    if (!ok) set_err(a.err, PE_DEV_BAD_PAGE);  // such a page's keys and values read as zeros
-    const uint8_t* rec = a.pool + ((size_t)(ok ? page : 0) * a.n_kv + g) * L::kRecord;
-    const int off = pos % kPackedPage;
-    const uint32_t* kw = reinterpret_cast<const uint32_t*>(rec + L::kK + off * L::kRow);
-    const uint32_t* vw = reinterpret_cast<const uint32_t*>(rec + L::kV + off * L::kRow);
-    float dot[HD / 16];
-#pragma unroll
-    for (int j = 0; j < HD / 16; ++j) dot[j] = 0.f;
-#pragma unroll
-    for (int w = 0; w < HD / 8; ++w) {
-      const uint32_t c = __ldg(kw + w);
-      const int t = w / (HD / 32), u = w % (HD / 32);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = 2 * u + (i & 3) / 2, e = 16 * j + 4 * t + 2 * (i & 1) + i / 4;
-        dot[j] += qr[e] * (float)((int)((c >> (4 * i)) & 15u) - 8);
-      }
+  for (int k = 0; k < TERMS; ++k) {
+    t[k] = pack_bf16(x0, x1);
+    if (k + 1 < TERMS) {
+      x0 -= __uint_as_float(t[k] << 16);
+      x1 -= __uint_as_float(t[k] & 0xFFFF0000u);
     }
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < HD / 16; ++j) s += dot[j] * packed_scale(rec[L::kKs + off * L::kScaleRow + j]);
-    s = ok ? s * a.scale : 0.f;
-    const float m_new = fmaxf(m, s);
-    const float c = m == -INFINITY ? 0.f : expf(m - m_new);
-    const float w = expf(s - m_new);
-    l = l * c + w;
-    float ws[HD / 16];
-#pragma unroll
-    for (int j = 0; j < HD / 16; ++j) ws[j] = ok ? w * packed_scale(rec[L::kVs + off * L::kScaleRow + j]) : 0.f;
-#pragma unroll
-    for (int wd = 0; wd < HD / 8; ++wd) {
-      const uint32_t cd = __ldg(vw + wd);
-      const int gg = wd / (HD / 64), hh = wd % (HD / 64);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = 4 * hh + i / 2, e = 16 * j + gg + 8 * (i & 1);
-        o[e] = o[e] * c + ws[j] * (float)((int)((cd >> (4 * i)) & 15u) - 8);
-      }
-    }
-    m = m_new;
-  }
-  float M = m;
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, s));
-  const float f = m == -INFINITY ? 0.f : expf(m - M);
-  float sum = l * f;
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
-  T* out = static_cast<T*>(a.out) + row * a.out_stride + (long long)h * HD;
-#pragma unroll
-  for (int e = 0; e < HD; ++e) {
-    float v = o[e] * f;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, s);
-    if (lane == (e & 31)) out[e] = from_float<T>(sum > 0.f ? v / sum : 0.f);
   }
 }
 
+template <typename T, int HD, int NQ>
+__global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
+    attend_small_kernel(const PackedAttnArgs a, const Line ln) {
+  using S = Small<T, HD, NQ>;
+  using L = PackedLayout<HD>;
+  constexpr int NB = HD / 16, TERMS = S::TERMS;
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 127) & ~uintptr_t(127));
+  uint8_t* ring = sm;
+  float* join_m = reinterpret_cast<float*>(sm + S::RING);          // [warps][ROWS]
+  float* join_l = join_m + kSmallWarps * S::ROWS;                  // [warps][ROWS]
+  float* join_o = join_l + kSmallWarps * S::ROWS;                  // [warps][ROWS][OROW]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::RING + S::JOIN);
+  int* scratch = reinterpret_cast<int*>(bars + kSmallWarps * S::STAGES);  // [16]
+  int* prefix = scratch + 16;
+  int* last = prefix + ln.n_tiles + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
+  uint64_t* bar = bars + warp * S::STAGES;
+  uint8_t* my_ring = ring + warp * S::STAGES * L::kRecord;
+  if (lane == 0) {
+    for (int s = 0; s < S::STAGES; ++s) mbar_init(smem_u32(bar + s), 1);
+    fence_mbar_init();
+  }
+  volatile int* abort_flag = scratch + 15;
+  if (tid == 0) *abort_flag = 0;
+  pdl_wait();
+  pdl_trigger();
+  lay_out(a, ln, prefix, last, scratch);
+  const long long T_ = (long long)prefix[ln.n_tiles] * a.n_kv;
+  const int n_ctas = line_ctas(T_, gridDim.x, ln.min_units);
+  if (blockIdx.x == 0 && !ln.whole)
+    for (int k = tid; k <= ln.n_tiles; k += blockDim.x) ln.prefix[k] = prefix[k];
+  if ((int)blockIdx.x >= n_ctas || T_ == 0) return;
+  const long long u0 = line_cut(T_, n_ctas, blockIdx.x), u1 = line_cut(T_, n_ctas, blockIdx.x + 1);
+  if (u0 == u1) return;
+  const int G = a.n_q / a.n_kv;
+  const float sl2 = a.scale * 1.4426950408889634f * kPackedUnit;
+
+  // Two walks over the segments' pages, the copies `STAGES` pages ahead of the products.  Page i of the
+  // CTA's pages, counted through all its segments, belongs to warp i % 8.
+  Segment ps = first_segment(ln, prefix, last, a.n_kv, u0, u1);
+  int p_rot = 0, p_i = 0;  // pages before the segment (mod 8); this warp's next page of it
+  bool p_done = false;
+  int ids = -1;            // page ids of 32 of this warp's pages, one per lane
+  uint32_t bad = 0;        // bit s: stage s stands for a page outside the pool
+  uint32_t issued = 0, used = 0;
+  auto issue = [&]() {
+    if (p_done) return;
+    int page = ps.page0 + ((warp - p_rot) & 7) + 8 * p_i;
+    while (page >= ps.page1) {
+      if (ps.next >= u1) {
+        p_done = true;
+        return;
+      }
+      p_rot = (p_rot + max(0, ps.page1 - ps.page0)) & 7;
+      ps = next_segment(ln, prefix, last, a.n_kv, ps, u1);
+      p_i = 0;
+      page = ps.page0 + ((warp - p_rot) & 7);
+    }
+    if ((p_i & 31) == 0) {
+      const int x = page + 8 * lane;
+      ids = -1;
+      if (x < ps.page1) {
+        ids = __ldcg(a.block_table + (size_t)((ln.tile0 + ps.k) / ln.tps) * a.max_pages + x);
+        if (ids < 0 || ids >= a.num_pages) {
+          set_err(a.err, PE_DEV_BAD_PAGE);
+          ids = -1;
+        }
+      }
+    }
+    const int id = __shfl_sync(0xFFFFFFFFu, ids, p_i & 31);
+    const int s = issued % S::STAGES;
+    bad = id < 0 ? bad | (1u << s) : bad & ~(1u << s);
+    if (lane == 0) {
+      const uint32_t b = smem_u32(bar + s);
+      if (id >= 0) {
+        mbar_expect_tx(b, L::kRecord);
+        bulk_g2s(smem_u32(my_ring + s * L::kRecord), a.pool + ((size_t)id * a.n_kv + ps.g) * L::kRecord, L::kRecord, b);
+      } else {
+        mbar_arrive(b);
+      }
+    }
+    ++issued;
+    ++p_i;
+  };
+#pragma unroll 1
+  for (int s = 0; s < S::STAGES; ++s) issue();
+
+  bool dead = false;
+  int c_rot = 0;
+  Segment cs = first_segment(ln, prefix, last, a.n_kv, u0, u1);
+  for (;;) {
+    const TileRows tr = tile_rows(a, ln, ln.tile0 + cs.k);
+    // queries: the operand of block j and vector gr is entries 4t..4t+3 of the block
+    uint32_t qf[TERMS][NQ][NB][2];
+    float qc[NQ][NB][4];  // -1.5 times the block's sum of q, for the vectors of this thread's columns
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int m = tr.m0 + n * 8 + gr;
+      const bool live = n * 8 + gr < tr.M;
+      const T* q = static_cast<const T*>(a.q) + (live ? (long long)(tr.r0 + m / G) * a.q_stride + (cs.g * G + m % G) * HD : 0);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        if constexpr (TERMS == 1) {
+          const uint2 v = live ? __ldcg(reinterpret_cast<const uint2*>(q + 16 * j + 4 * t)) : make_uint2(0, 0);
+          qf[0][n][j][0] = v.x;
+          qf[0][n][j][1] = v.y;
+        } else {
+          const float4 v = live ? __ldcg(reinterpret_cast<const float4*>(q + 16 * j + 4 * t)) : make_float4(0, 0, 0, 0);
+          uint32_t x[TERMS], y[TERMS];
+          split_pair<TERMS>(v.x, v.y, x);
+          split_pair<TERMS>(v.z, v.w, y);
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) {
+            qf[k][n][j][0] = x[k];
+            qf[k][n][j][1] = y[k];
+          }
+        }
+      }
+    }
+    const uint32_t minus[4] = {kMinus15, kMinus15, kMinus15, kMinus15};
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816(qc[n][j], minus, qf[TERMS - 1][n][j][0], qf[TERMS - 1][n][j][1], zero);
+#pragma unroll
+        for (int k = TERMS - 2; k >= 0; --k) mma16816(qc[n][j], minus, qf[k][n][j][0], qf[k][n][j][1], qc[n][j]);
+      }
+    int lim[NQ][2], min_lim = INT_MAX;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int v = n * 8 + 2 * t + e;
+        lim[n][e] = v < tr.M ? row_limit(a, tr.r0 + (tr.m0 + v) / G) : INT_MAX;
+        min_lim = min(min_lim, lim[n][e]);
+      }
+    min_lim = min(min_lim, __shfl_xor_sync(0xFFFFFFFFu, min_lim, 1));
+    min_lim = min(min_lim, __shfl_xor_sync(0xFFFFFFFFu, min_lim, 2));
+
+    float o[NB][NQ][4], nm[NQ][2], l[NQ][2];  // outputs, minus the reference maxima (+inf: none yet), sums
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      nm[n][0] = nm[n][1] = INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
+    }
+    const int first = cs.page0 + ((warp - c_rot) & 7);
+    // rows 0..7 of a product stand for positions 0, 4, 1, 5, 2, 6, 3, 7 and rows 8..15 for 8 more, so that
+    // the transposed P pairs positions t and t + 4
+    const int kpos = (gr >> 1) + 4 * (gr & 1);
+#pragma unroll 1
+    for (int page = first; page < cs.page1 && !dead; page += 8) {
+      const int s = used % S::STAGES;
+      if (!warp_ok(mbar_wait(smem_u32(bar + s), (used / S::STAGES) & 1u, a.err, abort_flag, a.wait_ns))) {
+        dead = true;
+        break;
+      }
+      const uint8_t* rec = my_ring + s * L::kRecord;
+      const bool zero = (bad >> s) & 1u;
+      // ---- scores
+      uint32_t kw[2][HD / 32], ks[2][HD / 64];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int pos = kpos + 8 * h;
+        if constexpr (HD == 64) {
+          const uint2 w = *reinterpret_cast<const uint2*>(rec + L::kK + pos * L::kRow + t * 8);
+          kw[h][0] = w.x; kw[h][1] = w.y;
+          ks[h][0] = *reinterpret_cast<const uint32_t*>(rec + L::kKs + pos * 4);
+        } else {
+          const uint4 w = *reinterpret_cast<const uint4*>(rec + L::kK + pos * L::kRow + t * 16);
+          kw[h][0] = w.x; kw[h][1] = w.y; kw[h][2] = w.z; kw[h][3] = w.w;
+          const uint2 c = *reinterpret_cast<const uint2*>(rec + L::kKs + pos * 8);
+          ks[h][0] = c.x; ks[h][1] = c.y;
+        }
+      }
+      float sc[NQ][4];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+      auto block = [&](auto J) {
+        constexpr int j = decltype(J)::value;
+        const uint32_t w0 = kw[0][j / 2], w1 = kw[1][j / 2];
+        const uint32_t af[4] = {packed_pair<2 * (j & 1)>(w0), packed_pair<2 * (j & 1)>(w1),
+                                packed_pair<2 * (j & 1) + 1>(w0), packed_pair<2 * (j & 1) + 1>(w1)};
+        const float s0 = packed_scale_f<(j & 3)>(ks[0][j / 4]), s1 = packed_scale_f<(j & 3)>(ks[1][j / 4]);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          float acc[4];
+          mma16816(acc, af, qf[TERMS - 1][n][j][0], qf[TERMS - 1][n][j][1], qc[n][j]);
+#pragma unroll
+          for (int k = TERMS - 2; k >= 0; --k) mma16816(acc, af, qf[k][n][j][0], qf[k][n][j][1], acc);
+          sc[n][0] = fmaf(acc[0], s0, sc[n][0]);
+          sc[n][1] = fmaf(acc[1], s0, sc[n][1]);
+          sc[n][2] = fmaf(acc[2], s1, sc[n][2]);
+          sc[n][3] = fmaf(acc[3], s1, sc[n][3]);
+        }
+      };
+      block(std::integral_constant<int, 0>{});
+      block(std::integral_constant<int, 1>{});
+      block(std::integral_constant<int, 2>{});
+      block(std::integral_constant<int, 3>{});
+      if constexpr (HD == 128) {
+        block(std::integral_constant<int, 4>{});
+        block(std::integral_constant<int, 5>{});
+        block(std::integral_constant<int, 6>{});
+        block(std::integral_constant<int, 7>{});
+      }
+      if (zero) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+      }
+      // ---- softmax
+      const bool edge = page * kPackedPage + kPackedPage - 1 > min_lim;
+      const int x0 = page * kPackedPage + kpos;
+      float d[NQ][4], top = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          d[n][e] = fmaf(sc[n][e], sl2, nm[n][e & 1]);
+          if (edge && x0 + 8 * (e >> 1) > lim[n][e & 1]) d[n][e] = -INFINITY;
+          top = fmaxf(top, d[n][e]);
+        }
+      if (__any_sync(0xFFFFFFFFu, top > kRescaleLog2)) {
+        // a new reference maximum for every vector: the largest score so far
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int e = c; e < 4; e += 2)
+              if (!(edge && x0 + 8 * (e >> 1) > lim[n][c])) mx = fmaxf(mx, sc[n][e] * sl2);
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
+            mx = fmaxf(mx, -nm[n][c]);
+            const float f = nm[n][c] == INFINITY ? 0.f : ex2_approx(-nm[n][c] - mx);
+            nm[n][c] = -mx;
+            l[n][c] *= f;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+              o[j][n][c] *= f;
+              o[j][n][c + 2] *= f;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            d[n][e] = (edge && x0 + 8 * (e >> 1) > lim[n][e & 1]) ? -INFINITY : fmaf(sc[n][e], sl2, nm[n][e & 1]);
+        }
+      }
+      uint32_t pf[TERMS][NQ][2];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] = ex2_approx(d[n][e]);
+          l[n][e & 1] += p[e];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[TERMS];
+          split_pair<TERMS>(zero ? 0.f : p[2 * h], zero ? 0.f : p[2 * h + 1], x);
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) pf[k][n][h] = transpose8(x[k]);
+        }
+      }
+      // ---- values
+      uint32_t vw[4][HD / 64], vs[4][HD / 64];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int pos = t + 4 * i;
+        if constexpr (HD == 64) {
+          vw[i][0] = *reinterpret_cast<const uint32_t*>(rec + L::kV + pos * L::kRow + gr * 4);
+          vs[i][0] = *reinterpret_cast<const uint32_t*>(rec + L::kVs + pos * 4);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(rec + L::kV + pos * L::kRow + gr * 8);
+          vw[i][0] = w.x; vw[i][1] = w.y;
+          const uint2 c = *reinterpret_cast<const uint2*>(rec + L::kVs + pos * 8);
+          vs[i][0] = c.x; vs[i][1] = c.y;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < HD / 64; ++h) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // blocks 0, 1 and 2, 3 of these 64 entries
+          const uint32_t sel = half == 0 ? 0x5410u : 0x7632u;
+          const uint32_t wa = __byte_perm(vw[0][h], vw[1][h], sel), wb = __byte_perm(vw[2][h], vw[3][h], sel);
+          const uint32_t ca = __byte_perm(vs[0][h], vs[1][h], sel), cb = __byte_perm(vs[2][h], vs[3][h], sel);
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const uint32_t sa = jj == 0 ? packed_scale_lo(ca) : packed_scale_hi(ca);
+            const uint32_t sb = jj == 0 ? packed_scale_lo(cb) : packed_scale_hi(cb);
+            const uint32_t za = bf16x2_mul(sa, kMinus15), zb = bf16x2_mul(sb, kMinus15);
+            uint32_t af[4];
+            if (jj == 0) {
+              af[0] = bf16x2_fma(packed_pair<0>(wa), sa, za);
+              af[1] = bf16x2_fma(packed_pair<1>(wa), sa, za);
+              af[2] = bf16x2_fma(packed_pair<0>(wb), sb, zb);
+              af[3] = bf16x2_fma(packed_pair<1>(wb), sb, zb);
+            } else {
+              af[0] = bf16x2_fma(packed_pair<2>(wa), sa, za);
+              af[1] = bf16x2_fma(packed_pair<3>(wa), sa, za);
+              af[2] = bf16x2_fma(packed_pair<2>(wb), sb, zb);
+              af[3] = bf16x2_fma(packed_pair<3>(wb), sb, zb);
+            }
+            const int j = 4 * h + 2 * half + jj;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+              for (int k = TERMS - 1; k >= 0; --k) mma16816(o[j][n], af, pf[k][n][0], pf[k][n][1], o[j][n]);
+          }
+        }
+      }
+      __syncwarp();  // the stage is read
+      ++used;
+      issue();
+    }
+    // ---- the warps' results join
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float sum = l[n][c];
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, w);
+        const int v = n * 8 + 2 * t + c;
+        if (gr == 0) {
+          join_m[warp * S::ROWS + v] = -nm[n][c];
+          join_l[warp * S::ROWS + v] = sum;
+        }
+        float* dst = join_o + (warp * S::ROWS + v) * S::OROW + gr;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          dst[16 * j] = o[j][n][c];
+          dst[16 * j + 8] = o[j][n][c + 2];
+        }
+      }
+    __syncthreads();
+    {
+      const bool done = cs.from_start && cs.to_end;
+      float* rec = done ? nullptr : part_record<HD>(ln, blockIdx.x, cs.from_start);
+#pragma unroll 1
+      for (int i = tid; i < tr.M * (HD / 4); i += kSmallWarps * 32) {
+        const int v = i / (HD / 4), e = (i - v * (HD / 4)) * 4;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kSmallWarps; ++w) mx = fmaxf(mx, join_m[w * S::ROWS + v]);
+        float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kSmallWarps; ++w) {
+          const float m = join_m[w * S::ROWS + v];
+          const float f = m == -INFINITY ? 0.f : ex2_approx(m - mx);
+          sum = fmaf(f, join_l[w * S::ROWS + v], sum);
+          const float4 y = *reinterpret_cast<const float4*>(join_o + (w * S::ROWS + v) * S::OROW + e);
+          x[0] = fmaf(f, y.x, x[0]); x[1] = fmaf(f, y.y, x[1]); x[2] = fmaf(f, y.z, x[2]); x[3] = fmaf(f, y.w, x[3]);
+        }
+        if (done) {
+          const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
+          const int m = tr.m0 + v;
+          T* out = static_cast<T*>(a.out) + (long long)(tr.r0 + m / G) * a.out_stride + (cs.g * G + m % G) * HD + e;
+          if constexpr (TERMS == 1)
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+          else
+            *reinterpret_cast<float4*>(out) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+        } else {
+          if (e == 0) {
+            rec[v] = mx;
+            rec[S::ROWS + v] = sum;
+          }
+          *reinterpret_cast<float4*>(rec + 2 * S::ROWS + v * HD + e) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+      }
+    }
+    if (cs.next >= u1) break;
+    c_rot = (c_rot + max(0, cs.page1 - cs.page0)) & 7;
+    cs = next_segment(ln, prefix, last, a.n_kv, cs, u1);
+    __syncthreads();  // the joint buffer is read
+  }
+  if (dead)  // leave no copy in flight into this CTA's shared memory
+    for (; used < issued; ++used)
+      mbar_wait(smem_u32(bar + used % S::STAGES), (used / S::STAGES) & 1u, a.err, nullptr, a.wait_ns);
+}
+
+// ----------------------------------------------------------------------------- merge of cut ranges
+
+constexpr int kMergeThreads = 256;
+
+// `split` warps (a power of two, at most 8) per (tile, head, vector) take every split-th record of it;
+// they join in shared memory.  Lanes over the entries.  Every sum runs in CTA order within a warp,
+// then in warp order.
 template <typename T, int HD>
-cudaError_t attend_typed(const PackedAttnArgs& a, cudaStream_t s) {
-  const long long warps = (long long)a.n_rows * a.n_q;
-  return launch_pdl(attend_kernel<T, HD>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, a);
+__global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const PackedAttnArgs a, const Line ln, int grid,
+                                                                     int split) {
+  constexpr int VPL = HD / 32, CB = 4;
+  __shared__ float sh_m[8], sh_l[8], sh_o[8][HD];
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp & (split - 1);
+  const long long task = (long long)blockIdx.x * (8 / split) + warp / split;
+  const long long per_tile = (long long)a.n_kv * ln.tile_rows;
+  const int k = (int)min(task / per_tile, (long long)ln.n_tiles);
+  const int rest = (int)(task - task / per_tile * per_tile);
+  const int g = rest / ln.tile_rows, v = rest - (rest / ln.tile_rows) * ln.tile_rows;
+  const int G = a.n_q / a.n_kv;
+  float mx = -INFINITY, sum = 0.f, x[VPL];
+#pragma unroll
+  for (int e = 0; e < VPL; ++e) x[e] = 0.f;
+  bool live = false;
+  TileRows tr{0, 0, 0};
+  if (k < ln.n_tiles) {
+    const int p0 = __ldcg(ln.prefix + k), p1 = __ldcg(ln.prefix + k + 1);
+    const long long tot = (long long)__ldcg(ln.prefix + ln.n_tiles) * a.n_kv;
+    if (p1 > p0) {
+      const int n = line_ctas(tot, grid, ln.min_units);
+      const long long U0 = (long long)p0 * a.n_kv + (long long)g * (p1 - p0), U1 = U0 + (p1 - p0);
+      int c0 = (int)(U0 * n / tot), c1 = (int)((U1 - 1) * n / tot);
+      while (line_cut(tot, n, c0 + 1) <= U0) ++c0;
+      while (line_cut(tot, n, c1 + 1) <= U1 - 1) ++c1;
+      tr = tile_rows(a, ln, ln.tile0 + k);
+      live = c1 > c0 && v < tr.M;
+      if (live) {
+        for (int c = c0 + sub; c <= c1; c += CB * split) {
+          float m[CB], l[CB], y[CB][VPL];
+#pragma unroll
+          for (int i = 0; i < CB; ++i) {
+            const int cc = c + i * split;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < VPL; ++e) y[i][e] = 0.f;
+            if (cc <= c1) {
+              const float* rec = part_record<HD>(ln, cc, cc == c0);
+              m[i] = __ldcg(rec + v);
+              l[i] = __ldcg(rec + ln.tile_rows + v);
+              const float* src = rec + 2 * ln.tile_rows + (size_t)v * HD + lane * VPL;
+              if constexpr (VPL == 4) {
+                const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
+                y[i][0] = z.x; y[i][1] = z.y; y[i][2] = z.z; y[i][3] = z.w;
+              } else {
+                const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
+                y[i][0] = z.x; y[i][1] = z.y;
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < CB; ++i) {
+            const float nx = fmaxf(mx, m[i]);
+            if (nx == -INFINITY) continue;
+            const float f = ex2_approx(mx - nx), w = ex2_approx(m[i] - nx);
+            sum = sum * f + w * l[i];
+#pragma unroll
+            for (int e = 0; e < VPL; ++e) x[e] = x[e] * f + w * y[i][e];
+            mx = nx;
+          }
+        }
+      }
+    }
+  }
+  if (split > 1) {
+    if (lane == 0) {
+      sh_m[warp] = mx;
+      sh_l[warp] = sum;
+    }
+#pragma unroll
+    for (int e = 0; e < VPL; ++e) sh_o[warp][lane * VPL + e] = x[e];
+    __syncthreads();
+    if (sub != 0) return;
+    for (int w = warp + 1; w < warp + split; ++w) {
+      const float m = sh_m[w], nx = fmaxf(mx, m);
+      if (nx == -INFINITY) continue;
+      const float f = ex2_approx(mx - nx), q = ex2_approx(m - nx);
+      sum = sum * f + q * sh_l[w];
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) x[e] = x[e] * f + q * sh_o[w][lane * VPL + e];
+      mx = nx;
+    }
+  }
+  if (!live) return;
+  const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
+  const int m = tr.m0 + v;
+  T* out = static_cast<T*>(a.out) + (long long)(tr.r0 + m / G) * a.out_stride + (g * G + m % G) * HD + lane * VPL;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < VPL; ++e) out[e] = x[e] * inv;
+  } else if constexpr (VPL == 4) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+  } else {
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16(x[0] * inv, x[1] * inv);
+  }
+}
+
+// ----------------------------------------------------------------------------- launch
+
+constexpr size_t kPrefixBytes = ((size_t)(kPlanTiles + 1) * 4 + 255) / 256 * 256;
+constexpr int kMaxCtasPerSm = 2;
+
+template <auto kernel>
+cudaError_t allow_smem(size_t bytes) {
+  static bool done[64] = {false};  // per kernel
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  return cudaSuccess;
+}
+
+template <typename T, int HD>
+cudaError_t launch_merge(const PackedAttnArgs& a, const Line& ln, int grid, cudaStream_t s) {
+  // few (tile, head) ranges: each may be cut into many records
+  const long long ranges = (long long)ln.n_tiles * a.n_kv;
+  int split = 1;
+  while (split < 8 && ranges * split * 8 < grid) split *= 2;
+  const long long warps = ranges * ln.tile_rows * split;
+  return launch_pdl(attend_merge_kernel<T, HD>, dim3((unsigned)((warps + 7) / 8)), dim3(kMergeThreads), 0, s, a, ln,
+                    grid, split);
+}
+
+template <typename T, int HD, int NQ>
+cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
+  using C = Small<T, HD, NQ>;
+  const int G = a.n_q / a.n_kv;
+  const long long vectors = (long long)a.max_rows * G;
+  Line ln{};
+  ln.tile_rows = C::ROWS;
+  ln.tps = (int)((vectors + C::ROWS - 1) / C::ROWS);
+  ln.whole = a.max_pages <= kWholePages;
+  ln.min_units = ln.whole ? 1 : 2;
+  const int rows = std::min(a.max_rows, C::ROWS / G + 2);
+  ln.lanes = 1;
+  while (ln.lanes < 32 && ln.lanes * 4 < rows) ln.lanes *= 2;
+  ln.prefix = static_cast<int*>(a.workspace);
+  ln.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kPrefixBytes);
+  cudaError_t e = allow_smem<attend_small_kernel<T, HD, NQ>>(C::smem(kPlanTiles));
+  if (e != cudaSuccess) return e;
+  const long long tiles = (long long)a.B * ln.tps;
+  for (long long t0 = 0; t0 < tiles; t0 += kPlanTiles) {
+    ln.tile0 = (int)t0;
+    ln.n_tiles = (int)std::min<long long>(kPlanTiles, tiles - t0);
+    // no more CTAs than the table's positions could keep busy
+    const long long units = (long long)ln.n_tiles * a.n_kv *
+                            (ln.whole ? 1 : ((long long)a.max_pages * kPackedPage + kUnit - 1) / kUnit);
+    const int grid = (int)std::min<long long>((long long)sms * C::CTAS, std::max(1LL, units / ln.min_units));
+    e = launch_pdl(attend_small_kernel<T, HD, NQ>, dim3(grid), dim3(kSmallWarps * 32), C::smem(ln.n_tiles), s, a, ln);
+    if (e != cudaSuccess) return e;
+    if (!ln.whole && grid > 1 && (e = launch_merge<T, HD>(a, ln, grid, s)) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <typename T, int HD>
+cudaError_t launch_attend_typed(const PackedAttnArgs& a, int sms, cudaStream_t s) {
+  const long long vectors = (long long)a.max_rows * (a.n_q / a.n_kv);
+  if (vectors <= 8) return launch_small<T, HD, 1>(a, sms, s);
+  return launch_small<T, HD, 2>(a, sms, s);
 }
 
 }  // namespace
 
-size_t packed_attn_workspace_bytes(int, pe_dtype, int) { return 256; }
+size_t packed_attn_workspace_bytes(int head_dim, pe_dtype, int sms) {
+  return kPrefixBytes + (size_t)sms * kMaxCtasPerSm * 2 * 16 * (head_dim + 2) * 4;
+}
 
-cudaError_t launch_attend_packed(const PackedAttnArgs& a, pe_dtype dt, int, cudaStream_t s) {
+cudaError_t launch_attend_packed(const PackedAttnArgs& a, pe_dtype dt, int sms, cudaStream_t s) {
   if (a.n_rows == 0) return cudaSuccess;
-  if (a.head_dim == 64) return dt == PE_BF16 ? attend_typed<__nv_bfloat16, 64>(a, s) : attend_typed<float, 64>(a, s);
-  return dt == PE_BF16 ? attend_typed<__nv_bfloat16, 128>(a, s) : attend_typed<float, 128>(a, s);
+  if (a.head_dim == 64)
+    return dt == PE_BF16 ? launch_attend_typed<__nv_bfloat16, 64>(a, sms, s) : launch_attend_typed<float, 64>(a, sms, s);
+  return dt == PE_BF16 ? launch_attend_typed<__nv_bfloat16, 128>(a, sms, s) : launch_attend_typed<float, 128>(a, sms, s);
 }
 
 }  // namespace pe
