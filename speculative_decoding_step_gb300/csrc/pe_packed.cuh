@@ -19,11 +19,12 @@
 //   keys:   word t*(hd/32) + u (t < 4), nibble i < 4: entry 16(2u + i/2) + 4t + 2(i%2); nibble
 //           i + 4: the entry after it.
 //   values: word g*(hd/64) + h (g < 8), nibble i: entry 64h + 16(i/2) + g + 8(i%2).
-// Two nibbles 16 bits apart become one pair of bf16 with three operations (a shift, a
-// mask-and-or, one fused multiply-add): the nibble in the mantissa's upper bits of 1.0 reads
-// 1 + nibble/16, and (1 + nibble/16) S - 1.5 S = (nibble - 8)/16 S, exactly.  The scale byte in
-// the exponent and mantissa bits below a fixed upper exponent reads S = s 2^-12, so a key or
-// value of the matrix products is 2^-16 of what it stands for (kPackedUnit undoes that).
+// Two nibbles 16 bits apart become one pair of bf16 with three operations (a shift for three of
+// four, a mask-and-or, one fused multiply-add): the nibble in the lowest mantissa bits of 128
+// reads 128 + nibble, and (128 + nibble) S - 136 S = (nibble - 8) S, exactly: 136 S = 8 * 17 S has at
+// most eight significant bits (17 * 15 = 255).  The scale byte in the exponent and mantissa bits
+// below a fixed upper exponent reads S = s 2^-12, so a key or value of the matrix products is
+// 2^-12 of what it stands for (kPackedUnit undoes that).
 #pragma once
 
 #include <stdint.h>
@@ -34,7 +35,7 @@ namespace pe {
 
 constexpr int kPackedPage = 16;           // positions per record
 constexpr int kPackedBlock = 16;          // entries per scale
-constexpr float kPackedUnit = 65536.f;    // value of an entry over its bf16 form in the kernels
+constexpr float kPackedUnit = 4096.f;     // value of an entry over its bf16 form in the kernels
 
 template <int HD>
 struct PackedLayout {
@@ -46,24 +47,15 @@ struct PackedLayout {
 // s(c) as fp32.
 PE_DEV float packed_scale(uint32_t c) { return __uint_as_float((c << 20) + (108u << 23)); }
 
-// Four of a word's eight nibbles as bf16 pairs 1 + nibble/16: nibble I in the lower half, I + 4 above.
+// Two of a word's eight nibbles as bf16 pairs 128 + nibble: nibble I in the lower half, I + 4 above.
 template <int I>
 PE_DEV uint32_t packed_pair(uint32_t w) {
-  constexpr int kShift[4] = {3, 1, 5, 9};
-  const uint32_t x = I == 0 ? w << kShift[I] : w >> kShift[I];
-  return (x & 0x00780078u) | 0x3F803F80u;
+  return ((I == 0 ? w : w >> (4 * I)) & 0x000F000Fu) | 0x43004300u;
 }
 
 // Two scale bytes (the first or the second byte of either half of x) as bf16 pairs s 2^-12.
 PE_DEV uint32_t packed_scale_lo(uint32_t x) { return ((x << 4) & 0x0FF00FF0u) | 0x30003000u; }
 PE_DEV uint32_t packed_scale_hi(uint32_t x) { return ((x >> 4) & 0x0FF00FF0u) | 0x30003000u; }
-// Scale byte B of x as fp32 s 2^-12.
-template <int B>
-PE_DEV float packed_scale_f(uint32_t x) {
-  const uint32_t y = B == 3 ? x >> 4 : x << (20 - 8 * (B & 3));
-  return __uint_as_float((y & 0x0FF00000u) | 0x30000000u);
-}
-
 PE_DEV uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -74,6 +66,6 @@ PE_DEV uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-constexpr uint32_t kMinus15 = 0xBFC0BFC0u;  // -1.5 twice
+constexpr uint32_t kMinus136 = 0xC308C308u;  // -136 twice
 
 }  // namespace pe

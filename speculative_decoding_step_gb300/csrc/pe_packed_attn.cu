@@ -184,38 +184,45 @@ PE_DEV float* part_record(const Line& ln, int cta, bool from_start) {
 
 // ----------------------------------------------------------------------------- few query vectors: warp MMAs
 //
-// A warp takes whole pages (16 positions), brought into its own ring of shared-memory stages by one bulk
-// copy each, and runs on its own until the segment ends: S^T = K Q^T and O^T += V^T P^T with 16 x 8 x 16
-// warp MMAs, positions (then entries) on the 16 side and 8 query vectors on the other, so one
+// A warp takes pairs of pages (32 positions), brought into its own ring of shared-memory stages by one
+// bulk copy per page, and runs on its own until the segment ends: S^T = K Q^T and O^T += V^T P^T with
+// 16 x 8 x 16 warp MMAs, positions (then entries) on the 16 side and 8 query vectors on the other, so one
 // unpacked page serves NQ * 8 vectors and no row is padded beyond 8.
-//   Keys: a product per block of 16 entries over 1 + nibble/16, starting from -1.5 sum(q) (an MMA of
-//   -1.5s at the segment's start), is the block's sum over (nibble - 8)/16; times the scale in fp32.
-//   That saves the scale's multiplication for every pair.
-//   P: rounded to bf16 and transposed by movmatrix into the other product's operand.
-//   Values: two positions' words give pairs of positions; scaled as pairs (exact).
+//   Scales: each lane turns a few of a page's scale bytes into bf16 pairs, into a small table that the
+//   others read: a lane needs the scales of eight rows, and converting them all itself cost 36 of
+//   400 instructions a page.
+//   Values: two positions' words give pairs of positions; P is rounded to bf16 and transposed by
+//   movmatrix into the other operand.
 // fp32: q and P are each split into three bf16 terms (24 bits), three MMAs for one; keys and values
 // are exact in bf16, so the products are those of fp32.
 // The eight warps' statistics and outputs join in shared memory at the end of a segment.
+//
+// Bound: unpacking.  A page of one head is 1152 bytes at head_dim 64: an SM's share of the HBM rate
+// brings it in about 50 cycles, in which it can issue about 200 instructions, half of them to the
+// integer pipe.
 
 constexpr int kSmallWarps = 8;
 
 template <typename T, int HD, int NQ>
 struct Small {
   static constexpr int TERMS = sizeof(T) == 4 ? 3 : 1;
-  static constexpr int STAGES = HD == 64 ? 4 : 3;
+  static constexpr int STAGES = HD == 64 ? 3 : 2;  // pairs of pages in flight per warp
   static constexpr int ROWS = 8 * NQ;
   static constexpr int OROW = HD + 4;  // floats per vector of the joint buffer (no bank conflicts)
-  static constexpr int CTAS = (NQ == 1 && TERMS == 1) || (HD == 64 && TERMS == 1) ? 2 : 1;  // per SM
-  static constexpr int RING = kSmallWarps * STAGES * PackedLayout<HD>::kRecord;
-  static constexpr int JOIN = kSmallWarps * ROWS * (OROW + 2) * 4;
-  static constexpr int FIXED = RING + JOIN + kSmallWarps * STAGES * 8 + 16 * 4 + 16;
+  static constexpr int CTAS = TERMS == 1 && (NQ == 1 || HD == 64) ? 2 : 1;  // per SM
+  static constexpr int JW = HD == 128 || NQ > 1 ? 4 : 8;  // warps whose results the joint buffer holds
+  static constexpr int STAGE = 2 * PackedLayout<HD>::kRecord;
+  static constexpr int RING = kSmallWarps * STAGES * STAGE;
+  static constexpr int KTAB = HD * 4, VTAB = HD * 2, TAB = 2 * (KTAB + VTAB);  // scale tables of a warp (two pages)
+  static constexpr int JOIN = JW * ROWS * (OROW + 2) * 4;
+  static constexpr int FIXED = RING + kSmallWarps * TAB + JOIN + kSmallWarps * STAGES * 8 + 16 * 4;
   static size_t smem(int n_tiles) { return 128 + FIXED + 8 * (size_t)(n_tiles + 1); }
 };
 
-PE_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+PE_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 PE_DEV uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -236,6 +243,35 @@ PE_DEV void split_pair(float x0, float x1, uint32_t (&t)[TERMS]) {
   }
 }
 
+// The scale tables of one page.  ktab: [16 positions][HD/16 blocks] pairs (S, S); vtab:
+// [position t][t + 8 or not][HD/16 blocks] pairs (S of position t or t + 8, S of the position 4 after it).
+template <int HD>
+PE_DEV void scale_tables(const uint8_t* rec, uint8_t* ktab, uint8_t* vtab, int lane) {
+  using L = PackedLayout<HD>;
+  constexpr int NB = HD / 16;
+  {
+    // NB/2 neighbouring bytes of a row per lane
+    const int pos = lane >> 1, j0 = (lane & 1) * (NB / 2);
+    uint32_t c;
+    if constexpr (NB == 4) c = *reinterpret_cast<const uint16_t*>(rec + L::kKs + pos * NB + j0);
+    else c = *reinterpret_cast<const uint32_t*>(rec + L::kKs + pos * NB + j0);
+    const uint32_t s01[2] = {packed_scale_lo(__byte_perm(c, 0, 0x4040)), packed_scale_lo(__byte_perm(c, 0, 0x4141))};
+    if constexpr (NB == 4) {
+      *reinterpret_cast<uint2*>(ktab + (pos * NB + j0) * 4) = make_uint2(s01[0], s01[1]);
+    } else {
+      const uint32_t s23[2] = {packed_scale_lo(__byte_perm(c, 0, 0x4242)), packed_scale_lo(__byte_perm(c, 0, 0x4343))};
+      *reinterpret_cast<uint4*>(ktab + (pos * NB + j0) * 4) = make_uint4(s01[0], s01[1], s23[0], s23[1]);
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < NB / 4; ++h) {
+    const int row = lane >> 2, j = (lane & 3) + 4 * h;  // row = 2 * t + (8 more)
+    const int pos = (row >> 1) + 8 * (row & 1);
+    const uint32_t c0 = rec[L::kVs + pos * NB + j], c1 = rec[L::kVs + (pos + 4) * NB + j];
+    *reinterpret_cast<uint32_t*>(vtab + (row * NB + j) * 4) = packed_scale_lo(c0 | c1 << 16);
+  }
+}
+
 template <typename T, int HD, int NQ>
 __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
     attend_small_kernel(const PackedAttnArgs a, const Line ln) {
@@ -244,17 +280,18 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   constexpr int NB = HD / 16, TERMS = S::TERMS;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 127) & ~uintptr_t(127));
-  uint8_t* ring = sm;
-  float* join_m = reinterpret_cast<float*>(sm + S::RING);          // [warps][ROWS]
-  float* join_l = join_m + kSmallWarps * S::ROWS;                  // [warps][ROWS]
-  float* join_o = join_l + kSmallWarps * S::ROWS;                  // [warps][ROWS][OROW]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::RING + S::JOIN);
+  uint8_t* tabs = sm + S::RING;
+  float* join_o = reinterpret_cast<float*>(tabs + kSmallWarps * S::TAB);  // [JW][ROWS][OROW]
+  float* join_m = join_o + S::JW * S::ROWS * S::OROW;                      // [JW][ROWS]
+  float* join_l = join_m + S::JW * S::ROWS;                                // [JW][ROWS]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(join_l + S::JW * S::ROWS);
   int* scratch = reinterpret_cast<int*>(bars + kSmallWarps * S::STAGES);  // [16]
   int* prefix = scratch + 16;
   int* last = prefix + ln.n_tiles + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
   uint64_t* bar = bars + warp * S::STAGES;
-  uint8_t* my_ring = ring + warp * S::STAGES * L::kRecord;
+  uint8_t* my_ring = sm + warp * S::STAGES * S::STAGE;
+  uint8_t* my_tab = tabs + warp * S::TAB;
   if (lane == 0) {
     for (int s = 0; s < S::STAGES; ++s) mbar_init(smem_u32(bar + s), 1);
     fence_mbar_init();
@@ -274,29 +311,30 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   const int G = a.n_q / a.n_kv;
   const float sl2 = a.scale * 1.4426950408889634f * kPackedUnit;
 
-  // Two walks over the segments' pages, the copies `STAGES` pages ahead of the products.  Page i of the
-  // CTA's pages, counted through all its segments, belongs to warp i % 8.
+  // Two walks over the segments' pairs of pages, the copies `STAGES` pairs ahead of the products.  Pair i
+  // of the CTA's pairs, counted through all its segments, belongs to warp i % 8.  A cut falls between
+  // units of four pages, so a pair lacks its second page at a range's end only, where every
+  // position of that page is masked.
   Segment ps = first_segment(ln, prefix, last, a.n_kv, u0, u1);
-  int p_rot = 0, p_i = 0;  // pages before the segment (mod 8); this warp's next page of it
+  int p_rot = 0, p_i = 0;  // pairs before the segment (mod 8); this warp's next pair of it
   bool p_done = false;
-  int ids = -1;            // page ids of 32 of this warp's pages, one per lane
-  uint32_t bad = 0;        // bit s: stage s stands for a page outside the pool
+  int ids = -1;            // page ids of 16 of this warp's pairs, one per lane
   uint32_t issued = 0, used = 0;
   auto issue = [&]() {
     if (p_done) return;
-    int page = ps.page0 + ((warp - p_rot) & 7) + 8 * p_i;
+    int page = ps.page0 + 2 * (((warp - p_rot) & 7) + 8 * p_i);
     while (page >= ps.page1) {
       if (ps.next >= u1) {
         p_done = true;
         return;
       }
-      p_rot = (p_rot + max(0, ps.page1 - ps.page0)) & 7;
+      p_rot += (max(0, ps.page1 - ps.page0) + 1) >> 1;
       ps = next_segment(ln, prefix, last, a.n_kv, ps, u1);
       p_i = 0;
-      page = ps.page0 + ((warp - p_rot) & 7);
+      page = ps.page0 + 2 * ((warp - p_rot) & 7);
     }
-    if ((p_i & 31) == 0) {
-      const int x = page + 8 * lane;
+    if ((p_i & 15) == 0) {
+      const int x = page + 16 * (lane >> 1) + (lane & 1);
       ids = -1;
       if (x < ps.page1) {
         ids = __ldcg(a.block_table + (size_t)((ln.tile0 + ps.k) / ln.tps) * a.max_pages + x);
@@ -306,17 +344,25 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
         }
       }
     }
-    const int id = __shfl_sync(0xFFFFFFFFu, ids, p_i & 31);
+    const int id0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (p_i & 15)), id1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (p_i & 15) + 1);
     const int s = issued % S::STAGES;
-    bad = id < 0 ? bad | (1u << s) : bad & ~(1u << s);
+    uint8_t* dst = my_ring + s * S::STAGE;
+    if (id0 < 0 || (id1 < 0 && page + 1 < ps.page1)) {
+      // pages outside the pool stand for zeros: every nibble 8
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h)
+        if ((h == 0 ? id0 : id1) < 0)
+          for (int i = lane; i < L::kRecord / 4; i += 32) reinterpret_cast<uint32_t*>(dst + h * L::kRecord)[i] = 0x88888888u;
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
     if (lane == 0) {
       const uint32_t b = smem_u32(bar + s);
-      if (id >= 0) {
-        mbar_expect_tx(b, L::kRecord);
-        bulk_g2s(smem_u32(my_ring + s * L::kRecord), a.pool + ((size_t)id * a.n_kv + ps.g) * L::kRecord, L::kRecord, b);
-      } else {
-        mbar_arrive(b);
-      }
+      const uint8_t* src = a.pool + (size_t)ps.g * L::kRecord;
+      const size_t step = (size_t)a.n_kv * L::kRecord;
+      mbar_expect_tx(b, (id0 >= 0 ? L::kRecord : 0) + (id1 >= 0 ? L::kRecord : 0));
+      if (id0 >= 0) bulk_g2s(smem_u32(dst), src + (size_t)id0 * step, L::kRecord, b);
+      if (id1 >= 0) bulk_g2s(smem_u32(dst) + L::kRecord, src + (size_t)id1 * step, L::kRecord, b);
     }
     ++issued;
     ++p_i;
@@ -327,11 +373,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   bool dead = false;
   int c_rot = 0;
   Segment cs = first_segment(ln, prefix, last, a.n_kv, u0, u1);
+  // rows 0..7 of a product stand for positions 0, 4, 1, 5, 2, 6, 3, 7 and rows 8..15 for 8 more, so that
+  // the transposed P pairs positions t and t + 4
+  const int kpos = (gr >> 1) + 4 * (gr & 1);
   for (;;) {
     const TileRows tr = tile_rows(a, ln, ln.tile0 + cs.k);
     // queries: the operand of block j and vector gr is entries 4t..4t+3 of the block
     uint32_t qf[TERMS][NQ][NB][2];
-    float qc[NQ][NB][4];  // -1.5 times the block's sum of q, for the vectors of this thread's columns
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       const int m = tr.m0 + n * 8 + gr;
@@ -356,16 +404,6 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
         }
       }
     }
-    const uint32_t minus[4] = {kMinus15, kMinus15, kMinus15, kMinus15};
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816(qc[n][j], minus, qf[TERMS - 1][n][j][0], qf[TERMS - 1][n][j][1], zero);
-#pragma unroll
-        for (int k = TERMS - 2; k >= 0; --k) mma16816(qc[n][j], minus, qf[k][n][j][0], qf[k][n][j][1], qc[n][j]);
-      }
     int lim[NQ][2], min_lim = INT_MAX;
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -386,92 +424,85 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 #pragma unroll
       for (int j = 0; j < NB; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
     }
-    const int first = cs.page0 + ((warp - c_rot) & 7);
-    // rows 0..7 of a product stand for positions 0, 4, 1, 5, 2, 6, 3, 7 and rows 8..15 for 8 more, so that
-    // the transposed P pairs positions t and t + 4
-    const int kpos = (gr >> 1) + 4 * (gr & 1);
 #pragma unroll 1
-    for (int page = first; page < cs.page1 && !dead; page += 8) {
+    for (int page = cs.page0 + 2 * ((warp - c_rot) & 7); page < cs.page1 && !dead; page += 16) {
       const int s = used % S::STAGES;
       if (!warp_ok(mbar_wait(smem_u32(bar + s), (used / S::STAGES) & 1u, a.err, abort_flag, a.wait_ns))) {
         dead = true;
         break;
       }
-      const uint8_t* rec = my_ring + s * L::kRecord;
-      const bool zero = (bad >> s) & 1u;
+      const uint8_t* recs = my_ring + s * S::STAGE;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        scale_tables<HD>(recs + h * L::kRecord, my_tab + h * (S::KTAB + S::VTAB), my_tab + h * (S::KTAB + S::VTAB) + S::KTAB, lane);
+      __syncwarp();
       // ---- scores
-      uint32_t kw[2][HD / 32], ks[2][HD / 64];
+      float sc[2][NQ][4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int pos = kpos + 8 * h;
-        if constexpr (HD == 64) {
-          const uint2 w = *reinterpret_cast<const uint2*>(rec + L::kK + pos * L::kRow + t * 8);
-          kw[h][0] = w.x; kw[h][1] = w.y;
-          ks[h][0] = *reinterpret_cast<const uint32_t*>(rec + L::kKs + pos * 4);
-        } else {
-          const uint4 w = *reinterpret_cast<const uint4*>(rec + L::kK + pos * L::kRow + t * 16);
-          kw[h][0] = w.x; kw[h][1] = w.y; kw[h][2] = w.z; kw[h][3] = w.w;
-          const uint2 c = *reinterpret_cast<const uint2*>(rec + L::kKs + pos * 8);
-          ks[h][0] = c.x; ks[h][1] = c.y;
+        const uint8_t* rec = recs + h * L::kRecord + L::kK;
+        const uint8_t* ktab = my_tab + h * (S::KTAB + S::VTAB);
+        uint32_t kw[2][HD / 32], ks[2][NB];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int pos = kpos + 8 * r;
+          if constexpr (HD == 64) {
+            const uint2 w = *reinterpret_cast<const uint2*>(rec + pos * L::kRow + t * 8);
+            kw[r][0] = w.x; kw[r][1] = w.y;
+          } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(rec + pos * L::kRow + t * 16);
+            kw[r][0] = w.x; kw[r][1] = w.y; kw[r][2] = w.z; kw[r][3] = w.w;
+          }
+#pragma unroll
+          for (int j = 0; j < NB; j += 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(ktab + (pos * NB + j) * 4);
+            ks[r][j] = w.x; ks[r][j + 1] = w.y; ks[r][j + 2] = w.z; ks[r][j + 3] = w.w;
+          }
         }
-      }
-      float sc[NQ][4];
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-      auto block = [&](auto J) {
-        constexpr int j = decltype(J)::value;
-        const uint32_t w0 = kw[0][j / 2], w1 = kw[1][j / 2];
-        const uint32_t af[4] = {packed_pair<2 * (j & 1)>(w0), packed_pair<2 * (j & 1)>(w1),
-                                packed_pair<2 * (j & 1) + 1>(w0), packed_pair<2 * (j & 1) + 1>(w1)};
-        const float s0 = packed_scale_f<(j & 3)>(ks[0][j / 4]), s1 = packed_scale_f<(j & 3)>(ks[1][j / 4]);
+        for (int n = 0; n < NQ; ++n) sc[h][n][0] = sc[h][n][1] = sc[h][n][2] = sc[h][n][3] = 0.f;
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          float acc[4];
-          mma16816(acc, af, qf[TERMS - 1][n][j][0], qf[TERMS - 1][n][j][1], qc[n][j]);
+        for (int j = 0; j < NB; ++j) {
+          const uint32_t w0 = kw[0][j / 2], w1 = kw[1][j / 2], s0 = ks[0][j], s1 = ks[1][j];
+          const uint32_t z0 = bf16x2_mul(s0, kMinus136), z1 = bf16x2_mul(s1, kMinus136);
+          const bool odd = j & 1;
+          const uint32_t af[4] = {bf16x2_fma(odd ? packed_pair<2>(w0) : packed_pair<0>(w0), s0, z0),
+                                  bf16x2_fma(odd ? packed_pair<2>(w1) : packed_pair<0>(w1), s1, z1),
+                                  bf16x2_fma(odd ? packed_pair<3>(w0) : packed_pair<1>(w0), s0, z0),
+                                  bf16x2_fma(odd ? packed_pair<3>(w1) : packed_pair<1>(w1), s1, z1)};
 #pragma unroll
-          for (int k = TERMS - 2; k >= 0; --k) mma16816(acc, af, qf[k][n][j][0], qf[k][n][j][1], acc);
-          sc[n][0] = fmaf(acc[0], s0, sc[n][0]);
-          sc[n][1] = fmaf(acc[1], s0, sc[n][1]);
-          sc[n][2] = fmaf(acc[2], s1, sc[n][2]);
-          sc[n][3] = fmaf(acc[3], s1, sc[n][3]);
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int k = TERMS - 1; k >= 0; --k) mma16816(sc[h][n], af, qf[k][n][j][0], qf[k][n][j][1]);
         }
-      };
-      block(std::integral_constant<int, 0>{});
-      block(std::integral_constant<int, 1>{});
-      block(std::integral_constant<int, 2>{});
-      block(std::integral_constant<int, 3>{});
-      if constexpr (HD == 128) {
-        block(std::integral_constant<int, 4>{});
-        block(std::integral_constant<int, 5>{});
-        block(std::integral_constant<int, 6>{});
-        block(std::integral_constant<int, 7>{});
-      }
-      if (zero) {
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
       }
       // ---- softmax
-      const bool edge = page * kPackedPage + kPackedPage - 1 > min_lim;
-      const int x0 = page * kPackedPage + kpos;
-      float d[NQ][4], top = -INFINITY;
+      const bool edge = (page + 2) * kPackedPage > min_lim + 1;
+      if (edge) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((page + h) * kPackedPage + kpos + 8 * (e >> 1) > lim[n][e & 1]) sc[h][n][e] = -INFINITY;
+      }
+      float top = -INFINITY;
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          d[n][e] = fmaf(sc[n][e], sl2, nm[n][e & 1]);
-          if (edge && x0 + 8 * (e >> 1) > lim[n][e & 1]) d[n][e] = -INFINITY;
-          top = fmaxf(top, d[n][e]);
+        for (int c = 0; c < 2; ++c) {
+          const float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][c + 2]), fmaxf(sc[1][n][c], sc[1][n][c + 2]));
+          // a vector without a reference yet needs one unless all is masked (-inf plus +inf is no number)
+          top = fmaxf(top, mx == -INFINITY ? mx : fmaf(mx, sl2, nm[n][c]));
         }
       if (__any_sync(0xFFFFFFFFu, top > kRescaleLog2)) {
         // a new reference maximum for every vector: the largest score so far
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int e = c; e < 4; e += 2)
-              if (!(edge && x0 + 8 * (e >> 1) > lim[n][c])) mx = fmaxf(mx, sc[n][e] * sl2);
+            float mx = fmaxf(fmaxf(sc[0][n][c], sc[0][n][c + 2]), fmaxf(sc[1][n][c], sc[1][n][c + 2])) * sl2;
 #pragma unroll
             for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
             mx = fmaxf(mx, -nm[n][c]);
@@ -484,76 +515,67 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
               o[j][n][c + 2] *= f;
             }
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            d[n][e] = (edge && x0 + 8 * (e >> 1) > lim[n][e & 1]) ? -INFINITY : fmaf(sc[n][e], sl2, nm[n][e & 1]);
-        }
       }
-      uint32_t pf[TERMS][NQ][2];
+      uint32_t pf[2][TERMS][NQ][2];
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        float p[4];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = ex2_approx(d[n][e]);
-          l[n][e & 1] += p[e];
-        }
+        for (int n = 0; n < NQ; ++n) {
+          float p[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[TERMS];
-          split_pair<TERMS>(zero ? 0.f : p[2 * h], zero ? 0.f : p[2 * h + 1], x);
+          for (int e = 0; e < 4; ++e) {
+            // masked scores are -inf; a vector that has seen nothing takes no offset
+            p[e] = ex2_approx(fmaf(sc[h][n][e], sl2, nm[n][e & 1] == INFINITY ? 0.f : nm[n][e & 1]));
+            l[n][e & 1] += p[e];
+          }
 #pragma unroll
-          for (int k = 0; k < TERMS; ++k) pf[k][n][h] = transpose8(x[k]);
-        }
-      }
-      // ---- values
-      uint32_t vw[4][HD / 64], vs[4][HD / 64];
+          for (int r = 0; r < 2; ++r) {
+            uint32_t x[TERMS];
+            split_pair<TERMS>(p[2 * r], p[2 * r + 1], x);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int pos = t + 4 * i;
-        if constexpr (HD == 64) {
-          vw[i][0] = *reinterpret_cast<const uint32_t*>(rec + L::kV + pos * L::kRow + gr * 4);
-          vs[i][0] = *reinterpret_cast<const uint32_t*>(rec + L::kVs + pos * 4);
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(rec + L::kV + pos * L::kRow + gr * 8);
-          vw[i][0] = w.x; vw[i][1] = w.y;
-          const uint2 c = *reinterpret_cast<const uint2*>(rec + L::kVs + pos * 8);
-          vs[i][0] = c.x; vs[i][1] = c.y;
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < HD / 64; ++h) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {  // blocks 0, 1 and 2, 3 of these 64 entries
-          const uint32_t sel = half == 0 ? 0x5410u : 0x7632u;
-          const uint32_t wa = __byte_perm(vw[0][h], vw[1][h], sel), wb = __byte_perm(vw[2][h], vw[3][h], sel);
-          const uint32_t ca = __byte_perm(vs[0][h], vs[1][h], sel), cb = __byte_perm(vs[2][h], vs[3][h], sel);
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const uint32_t sa = jj == 0 ? packed_scale_lo(ca) : packed_scale_hi(ca);
-            const uint32_t sb = jj == 0 ? packed_scale_lo(cb) : packed_scale_hi(cb);
-            const uint32_t za = bf16x2_mul(sa, kMinus15), zb = bf16x2_mul(sb, kMinus15);
-            uint32_t af[4];
-            if (jj == 0) {
-              af[0] = bf16x2_fma(packed_pair<0>(wa), sa, za);
-              af[1] = bf16x2_fma(packed_pair<1>(wa), sa, za);
-              af[2] = bf16x2_fma(packed_pair<0>(wb), sb, zb);
-              af[3] = bf16x2_fma(packed_pair<1>(wb), sb, zb);
-            } else {
-              af[0] = bf16x2_fma(packed_pair<2>(wa), sa, za);
-              af[1] = bf16x2_fma(packed_pair<3>(wa), sa, za);
-              af[2] = bf16x2_fma(packed_pair<2>(wb), sb, zb);
-              af[3] = bf16x2_fma(packed_pair<3>(wb), sb, zb);
-            }
-            const int j = 4 * h + 2 * half + jj;
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-              for (int k = TERMS - 1; k >= 0; --k) mma16816(o[j][n], af, pf[k][n][0], pf[k][n][1], o[j][n]);
+            for (int k = 0; k < TERMS; ++k) pf[h][k][n][r] = transpose8(x[k]);
           }
         }
+      // ---- values
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* rec = recs + h * L::kRecord + L::kV;
+        const uint8_t* vtab = my_tab + h * (S::KTAB + S::VTAB) + S::KTAB;
+        uint32_t vw[4][HD / 64], vs[2][NB];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (HD == 64) {
+            vw[i][0] = *reinterpret_cast<const uint32_t*>(rec + (t + 4 * i) * L::kRow + gr * 4);
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(rec + (t + 4 * i) * L::kRow + gr * 8);
+            vw[i][0] = w.x; vw[i][1] = w.y;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < NB; j += 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(vtab + ((2 * t + r) * NB + j) * 4);
+            vs[r][j] = w.x; vs[r][j + 1] = w.y; vs[r][j + 2] = w.z; vs[r][j + 3] = w.w;
+          }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const uint32_t sel = (j & 2) ? 0x7632u : 0x5410u;  // blocks 0, 1 of 64 entries in the lower halves
+          const uint32_t wa = __byte_perm(vw[0][j / 4], vw[1][j / 4], sel), wb = __byte_perm(vw[2][j / 4], vw[3][j / 4], sel);
+          const uint32_t sa = vs[0][j], sb = vs[1][j];
+          const uint32_t za = bf16x2_mul(sa, kMinus136), zb = bf16x2_mul(sb, kMinus136);
+          const bool odd = j & 1;
+          const uint32_t af[4] = {bf16x2_fma(odd ? packed_pair<2>(wa) : packed_pair<0>(wa), sa, za),
+                                  bf16x2_fma(odd ? packed_pair<3>(wa) : packed_pair<1>(wa), sa, za),
+                                  bf16x2_fma(odd ? packed_pair<2>(wb) : packed_pair<0>(wb), sb, zb),
+                                  bf16x2_fma(odd ? packed_pair<3>(wb) : packed_pair<1>(wb), sb, zb)};
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int k = TERMS - 1; k >= 0; --k) mma16816(o[j][n], af, pf[h][k][n][0], pf[h][k][n][1]);
+        }
       }
-      __syncwarp();  // the stage is read
+      __syncwarp();  // the stage and the tables are read
       ++used;
       issue();
     }
@@ -561,22 +583,51 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float sum = l[n][c];
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, w);
-        const int v = n * 8 + 2 * t + c;
-        if (gr == 0) {
-          join_m[warp * S::ROWS + v] = -nm[n][c];
-          join_l[warp * S::ROWS + v] = sum;
-        }
-        float* dst = join_o + (warp * S::ROWS + v) * S::OROW + gr;
+        for (int w = 4; w < 32; w <<= 1) l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], w);
+    auto give = [&](int slot) {
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          dst[16 * j] = o[j][n][c];
-          dst[16 * j + 8] = o[j][n][c + 2];
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int v = slot * S::ROWS + n * 8 + 2 * t + c;
+          if (gr == 0) {
+            join_m[v] = -nm[n][c];
+            join_l[v] = l[n][c];
+          }
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            join_o[v * S::OROW + 16 * j + gr] = o[j][n][c];
+            join_o[v * S::OROW + 16 * j + 8 + gr] = o[j][n][c + 2];
+          }
         }
+    };
+    if constexpr (S::JW < kSmallWarps) {  // the upper warps' results first, taken over by the lower ones
+      if (warp >= S::JW) give(warp - S::JW);
+      __syncthreads();
+      if (warp < S::JW) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int v = warp * S::ROWS + n * 8 + 2 * t + c;
+            const float m = join_m[v], mx = fmaxf(m, -nm[n][c]);
+            if (mx != -INFINITY) {
+              const float f = ex2_approx(-nm[n][c] - mx), q = ex2_approx(m - mx);
+              nm[n][c] = -mx;
+              l[n][c] = l[n][c] * f + join_l[v] * q;
+#pragma unroll
+              for (int j = 0; j < NB; ++j) {
+                o[j][n][c] = o[j][n][c] * f + join_o[v * S::OROW + 16 * j + gr] * q;
+                o[j][n][c + 2] = o[j][n][c + 2] * f + join_o[v * S::OROW + 16 * j + 8 + gr] * q;
+              }
+            }
+          }
       }
+      __syncthreads();
+    }
+    if (warp < S::JW) give(warp);
     __syncthreads();
     {
       const bool done = cs.from_start && cs.to_end;
@@ -586,10 +637,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
         const int v = i / (HD / 4), e = (i - v * (HD / 4)) * 4;
         float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kSmallWarps; ++w) mx = fmaxf(mx, join_m[w * S::ROWS + v]);
+        for (int w = 0; w < S::JW; ++w) mx = fmaxf(mx, join_m[w * S::ROWS + v]);
         float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kSmallWarps; ++w) {
+        for (int w = 0; w < S::JW; ++w) {
           const float m = join_m[w * S::ROWS + v];
           const float f = m == -INFINITY ? 0.f : ex2_approx(m - mx);
           sum = fmaf(f, join_l[w * S::ROWS + v], sum);
@@ -614,7 +665,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       }
     }
     if (cs.next >= u1) break;
-    c_rot = (c_rot + max(0, cs.page1 - cs.page0)) & 7;
+    c_rot += (max(0, cs.page1 - cs.page0) + 1) >> 1;
     cs = next_segment(ln, prefix, last, a.n_kv, cs, u1);
     __syncthreads();  // the joint buffer is read
   }
