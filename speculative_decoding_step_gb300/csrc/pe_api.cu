@@ -366,7 +366,9 @@ pe_status check_packed_cfg(const pe_config* c) {
   if (c == nullptr) return PE_ERR_INVALID_ARG;
   if (c->dtype != PE_F32 && c->dtype != PE_BF16) return PE_ERR_INVALID_ARG;
   if (c->B < 1 || c->n_q < 1 || c->n_kv < 1 || c->max_pages_per_seq < 1 || c->n_q % c->n_kv != 0) return PE_ERR_SHAPE;
-  if (c->B > kMaxRows || c->n_q > kMaxPackedHeads || c->max_pages_per_seq > kMaxPackedPages) return PE_ERR_SHAPE;
+  if (c->B > kMaxRows || c->n_q > kMaxPackedHeads || c->max_pages_per_seq > kMaxPackedPages ||
+      (int64_t)c->n_kv * c->max_pages_per_seq > (int64_t(1) << 30))
+    return PE_ERR_SHAPE;
   if (c->page_size != 16) return PE_ERR_UNSUPPORTED;
   if (c->head_dim != 64 && c->head_dim != 128) return PE_ERR_UNSUPPORTED;
   return PE_OK;

@@ -7,13 +7,13 @@
 // with keys and values of head h / (n_q / n_kv).  A row at position -1 sees nothing: zeros.
 //
 // Work.  The query vectors of a sequence and kv head (rows x G query heads, G = n_q / n_kv) are
-// cut into tiles; a (tile, kv head) pair's range of positions is counted in units of 64.  All units of
+// cut into tiles; a (tile, kv head) pair's range of positions is counted in units.  All units of
 // the launch form one line (tile after tile, head after head, position after position) that
 // N CTAs divide into equal pieces, so ragged lengths leave no CTA idle.  A range that lies in
 // one CTA's piece is finished there; one that is cut leaves a record per CTA (reference maximum,
 // sum, unnormalised output) that the merge kernel joins in CTA order.  Every CTA works the line
-// out for itself from row_start and positions (two dependent loads and a scan, about 2 us,
-// against a launch and a round trip through memory for a kernel that would do it once).
+// out for itself from row_start and positions (two dependent loads and a scan), which costs less
+// than a launch and a round trip through memory for a kernel that would do it once.
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -25,9 +25,8 @@ namespace pe {
 
 namespace {
 
-constexpr int kUnit = 64;           // positions per unit of work (four pages)
 constexpr int kPlanTiles = 1024;    // tiles per launch (their line is held in shared memory)
-constexpr int kWholePages = 32;     // tables of at most this many pages: no range is cut (and nothing to merge)
+constexpr int kWholePages = 32;     // tables of at most this many pages: no range is cut between CTAs (no merge)
 constexpr float kRescaleLog2 = 8.f; // a reference maximum moves when a score exceeds it by more (log2 units)
 
 PE_DEV float ex2_approx(float x) {
@@ -47,11 +46,13 @@ struct Line {
   int tile0, n_tiles;  // this launch's tiles: b * tps + t
   int tps;             // tiles per sequence (host bound)
   int tile_rows;       // query vectors per tile
+  int unit_pages;      // pages per unit
   int lanes;           // threads that look through one tile's rows (a power of two, at most 32)
-  int whole;           // every range is one unit
+  int whole;           // CTAs take whole ranges
   int min_units;       // a CTA's piece is at least this long where there are fewer units than that for all
   int* prefix;         // workspace [n_tiles + 1]: units per head before each tile, for the merge
   float* part;         // workspace: records of cut ranges, two per CTA
+  float* spill;        // workspace: a warp's piece of a range that began before it (small kernel)
 };
 
 struct TileRows {
@@ -100,7 +101,8 @@ PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, int* prefix, int* l
     }
     for (int o = per >> 1; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
     if (k < ln.n_tiles && sub == 0) {
-      prefix[k + 1] = M == 0 ? 0 : ln.whole ? 1 : max(1, (mx + kUnit) / kUnit);
+      const int positions = ln.unit_pages * kPackedPage;
+      prefix[k + 1] = M == 0 ? 0 : max(1, (mx + positions) / positions);
       last[k] = mx;
     }
   }
@@ -127,53 +129,83 @@ PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, int* prefix, int* l
   __syncthreads();
 }
 
-// CTAs that share T units, and the first unit of CTA c.
-PE_DEV int line_ctas(long long T, int grid, int min_units) {
-  return (int)min((long long)grid, max(1LL, T / min_units));
+// T units in n equal pieces (the first T % n of them one longer): the first unit of piece c, and the
+// piece that holds unit u.
+struct Cuts {
+  uint32_t n, q, r;
+  PE_DEV Cuts(uint32_t T, uint32_t n_) : n(n_), q(T / n_), r(T - T / n_ * n_) {}
+  PE_DEV uint32_t first(uint32_t c) const { return q * c + min(c, r); }
+  PE_DEV uint32_t piece(uint32_t u) const {
+    const uint32_t longer = r * (q + 1);
+    return u < longer ? u / (q + 1) : r + (u - longer) / q;  // q = 0: every unit lies in a longer piece
+  }
+};
+PE_DEV uint32_t line_ctas(uint32_t T, int grid, int min_units) {
+  return min((uint32_t)grid, max(1u, T / (uint32_t)min_units));
 }
-PE_DEV long long line_cut(long long T, int n, int c) { return T * c / n; }
 
-// The part of a (tile, head) range that a CTA works on.
+// The part of a (tile, head) range that a piece of the line holds.
 struct Segment {
   int k, g;          // tile (of this launch), kv head
   int page0, page1;  // its pages
   bool from_start, to_end;
-  long long next;    // the unit after it
+  uint32_t next;     // the unit after it
 };
 
-PE_DEV Segment segment_at(const Line& ln, const int* prefix, const int* last, int n_kv, int k, long long u,
-                          long long u1) {
-  Segment s;
-  const int nb = prefix[k + 1] - prefix[k];
-  const long long r = u - (long long)prefix[k] * n_kv;
-  s.k = k;
-  s.g = (int)(r / nb);
-  const int blk = (int)(r - (long long)s.g * nb);
-  const int cnt = (int)min((long long)(nb - blk), u1 - u);
-  s.from_start = blk == 0;
-  s.to_end = blk + cnt == nb;
-  s.next = u + cnt;
-  const int pages = (last[k] + kPackedPage) / kPackedPage;
-  s.page0 = ln.whole ? 0 : blk * (kUnit / kPackedPage);
-  s.page1 = ln.whole ? pages : min(pages, (blk + cnt) * (kUnit / kPackedPage));
-  return s;
-}
-PE_DEV Segment first_segment(const Line& ln, const int* prefix, const int* last, int n_kv, long long u, long long u1) {
-  int lo = 0, hi = ln.n_tiles;  // the last tile that starts at or before u
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((long long)prefix[mid] * n_kv <= u) lo = mid;
-    else hi = mid;
+struct Walk {
+  const int *prefix, *last;
+  int n_kv, unit_pages;
+
+  PE_DEV int tile_of(uint32_t u, int n_tiles) const {  // the last tile that starts at or before u and has units
+    int lo = 0, hi = n_tiles;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((uint32_t)prefix[mid] * n_kv <= u) lo = mid;
+      else hi = mid;
+    }
+    return lo;
   }
-  return segment_at(ln, prefix, last, n_kv, lo, u, u1);
-}
-PE_DEV Segment next_segment(const Line& ln, const int* prefix, const int* last, int n_kv, const Segment& s,
-                            long long u1) {
-  int k = s.k;
-  if (s.next >= (long long)prefix[k + 1] * n_kv)
-    do ++k;
-    while (prefix[k + 1] == prefix[k]);
-  return segment_at(ln, prefix, last, n_kv, k, s.next, u1);
+  PE_DEV Segment at(int k, uint32_t u, uint32_t u1) const {
+    Segment s;
+    const uint32_t nb = prefix[k + 1] - prefix[k];
+    const uint32_t r = u - (uint32_t)prefix[k] * n_kv;
+    s.k = k;
+    s.g = (int)(r / nb);
+    const uint32_t blk = r - s.g * nb, cnt = min(nb - blk, u1 - u);
+    s.from_start = blk == 0;
+    s.to_end = blk + cnt == nb;
+    s.next = u + cnt;
+    s.page0 = (int)blk * unit_pages;
+    s.page1 = min((last[k] + kPackedPage) / kPackedPage, (int)(blk + cnt) * unit_pages);
+    return s;
+  }
+  PE_DEV Segment after(const Segment& s, uint32_t u1) const {
+    int k = s.k;
+    if (s.next >= (uint32_t)prefix[k + 1] * n_kv)
+      do ++k;
+      while (prefix[k + 1] == prefix[k]);
+    return at(k, s.next, u1);
+  }
+  // The first unit of the range that holds unit u (u < T).
+  PE_DEV uint32_t range_start(uint32_t u, int n_tiles) const {
+    const int k = tile_of(u, n_tiles);
+    const uint32_t nb = prefix[k + 1] - prefix[k];
+    return u - (u - (uint32_t)prefix[k] * n_kv) % nb;
+  }
+};
+
+// The units of this CTA: [u0, u1) of T.
+PE_DEV void cta_units(const Line& ln, const Walk& w, uint32_t T, uint32_t& u0, uint32_t& u1) {
+  u0 = u1 = 0;
+  const uint32_t n = line_ctas(T, gridDim.x, ln.min_units);
+  if (T == 0 || blockIdx.x >= n) return;
+  const Cuts cuts(T, n);
+  u0 = cuts.first(blockIdx.x);
+  u1 = cuts.first(blockIdx.x + 1);
+  if (ln.whole) {
+    u0 = w.range_start(u0, ln.n_tiles);
+    if (u1 < T) u1 = w.range_start(u1, ln.n_tiles);
+  }
 }
 
 // A record of a cut range: maximum and sum of each vector, then the outputs.
@@ -195,7 +227,11 @@ PE_DEV float* part_record(const Line& ln, int cta, bool from_start) {
 //   movmatrix into the other operand.
 // fp32: q and P are each split into three bf16 terms (24 bits), three MMAs for one; keys and values
 // are exact in bf16, so the products are those of fp32.
-// The eight warps' statistics and outputs join in shared memory at the end of a segment.
+// A CTA's piece of the line is divided once more, evenly, among its eight warps, each of which runs on its
+// own over whole ranges, or parts, of its piece; at the end the parts of ranges that the warps
+// share join in shared memory.  (Dividing every range among the eight warps instead, with a join
+// after each, left SMs with many short ranges behind the others: 94 us for the 84 us here
+// at B = 64 single tokens.)
 //
 // Bound: unpacking.  A page of one head is 1152 bytes at head_dim 64: an SM's share of the HBM rate
 // brings it in about 50 cycles, in which it can issue about 200 instructions, half of them to the
@@ -210,14 +246,23 @@ struct Small {
   static constexpr int ROWS = 8 * NQ;
   static constexpr int OROW = HD + 4;  // floats per vector of the joint buffer (no bank conflicts)
   static constexpr int CTAS = TERMS == 1 && (NQ == 1 || HD == 64) ? 2 : 1;  // per SM
-  static constexpr int JW = HD == 128 || NQ > 1 ? 4 : 8;  // warps whose results the joint buffer holds
   static constexpr int STAGE = 2 * PackedLayout<HD>::kRecord;
   static constexpr int RING = kSmallWarps * STAGES * STAGE;
   static constexpr int KTAB = HD * 4, VTAB = HD * 2, TAB = 2 * (KTAB + VTAB);  // scale tables of a warp (two pages)
-  static constexpr int JOIN = JW * ROWS * (OROW + 2) * 4;
-  static constexpr int FIXED = RING + kSmallWarps * TAB + JOIN + kSmallWarps * STAGES * 8 + 16 * 4;
+  static constexpr int PIECE = ROWS * (OROW + 2);  // floats of a warp's part of a shared range
+  static_assert(PIECE * 4 <= STAGES * STAGE, "it fits the warp's drained ring");
+  static constexpr int FIXED = RING + kSmallWarps * TAB + kSmallWarps * STAGES * 8 + 16 * 4 + 2 * kSmallWarps * 32;
   static size_t smem(int n_tiles) { return 128 + FIXED + 8 * (size_t)(n_tiles + 1); }
 };
+
+// A warp's part of a range that it shares with its neighbours.
+enum PartState : int { kNoPart, kBegins, kGoesOn, kEnds };
+struct Part {
+  const float* data;  // [ROWS][OROW] outputs, then [ROWS] maxima and [ROWS] sums
+  TileRows tr;
+  int g, state;
+};
+static_assert(sizeof(Part) <= 32, "");
 
 PE_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -281,12 +326,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 127) & ~uintptr_t(127));
   uint8_t* tabs = sm + S::RING;
-  float* join_o = reinterpret_cast<float*>(tabs + kSmallWarps * S::TAB);  // [JW][ROWS][OROW]
-  float* join_m = join_o + S::JW * S::ROWS * S::OROW;                      // [JW][ROWS]
-  float* join_l = join_m + S::JW * S::ROWS;                                // [JW][ROWS]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(join_l + S::JW * S::ROWS);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(tabs + kSmallWarps * S::TAB);
   int* scratch = reinterpret_cast<int*>(bars + kSmallWarps * S::STAGES);  // [16]
-  int* prefix = scratch + 16;
+  Part* parts = reinterpret_cast<Part*>(scratch + 16);                    // [warps][2]
+  int* prefix = reinterpret_cast<int*>(parts + 2 * kSmallWarps);
   int* last = prefix + ln.n_tiles + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
   uint64_t* bar = bars + warp * S::STAGES;
@@ -301,40 +344,44 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   pdl_wait();
   pdl_trigger();
   lay_out(a, ln, prefix, last, scratch);
-  const long long T_ = (long long)prefix[ln.n_tiles] * a.n_kv;
-  const int n_ctas = line_ctas(T_, gridDim.x, ln.min_units);
+  const Walk walk{prefix, last, a.n_kv, ln.unit_pages};
+  const uint32_t total = (uint32_t)prefix[ln.n_tiles] * a.n_kv;
   if (blockIdx.x == 0 && !ln.whole)
     for (int k = tid; k <= ln.n_tiles; k += blockDim.x) ln.prefix[k] = prefix[k];
-  if ((int)blockIdx.x >= n_ctas || T_ == 0) return;
-  const long long u0 = line_cut(T_, n_ctas, blockIdx.x), u1 = line_cut(T_, n_ctas, blockIdx.x + 1);
+  uint32_t u0, u1;
+  cta_units(ln, walk, total, u0, u1);
   if (u0 == u1) return;
+  {
+    const Cuts cuts(u1 - u0, kSmallWarps);
+    u1 = u0 + cuts.first(warp + 1);
+    u0 += cuts.first(warp);
+  }
   const int G = a.n_q / a.n_kv;
   const float sl2 = a.scale * 1.4426950408889634f * kPackedUnit;
 
-  // Two walks over the segments' pairs of pages, the copies `STAGES` pairs ahead of the products.  Pair i
-  // of the CTA's pairs, counted through all its segments, belongs to warp i % 8.  A cut falls between
-  // units of four pages, so a pair lacks its second page at a range's end only, where every
+  // Two walks over the pairs of pages of the warp's units, the copies `STAGES` pairs ahead of the
+  // products.  A unit is a pair, so a pair lacks its second page at a range's end only, where every
   // position of that page is masked.
-  Segment ps = first_segment(ln, prefix, last, a.n_kv, u0, u1);
-  int p_rot = 0, p_i = 0;  // pairs before the segment (mod 8); this warp's next pair of it
-  bool p_done = false;
-  int ids = -1;            // page ids of 16 of this warp's pairs, one per lane
+  Segment ps{}, cs{};
+  bool p_done = u0 == u1;
+  if (!p_done) ps = cs = walk.at(walk.tile_of(u0, ln.n_tiles), u0, u1);
+  int p_i = 0;   // the next pair of the segment
+  int ids = -1;  // page ids of 16 pairs, one per lane
   uint32_t issued = 0, used = 0;
   auto issue = [&]() {
     if (p_done) return;
-    int page = ps.page0 + 2 * (((warp - p_rot) & 7) + 8 * p_i);
+    int page = ps.page0 + 2 * p_i;
     while (page >= ps.page1) {
       if (ps.next >= u1) {
         p_done = true;
         return;
       }
-      p_rot += (max(0, ps.page1 - ps.page0) + 1) >> 1;
-      ps = next_segment(ln, prefix, last, a.n_kv, ps, u1);
+      ps = walk.after(ps, u1);
       p_i = 0;
-      page = ps.page0 + 2 * ((warp - p_rot) & 7);
+      page = ps.page0;
     }
     if ((p_i & 15) == 0) {
-      const int x = page + 16 * (lane >> 1) + (lane & 1);
+      const int x = page + lane;
       ids = -1;
       if (x < ps.page1) {
         ids = __ldcg(a.block_table + (size_t)((ln.tile0 + ps.k) / ln.tps) * a.max_pages + x);
@@ -371,12 +418,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   for (int s = 0; s < S::STAGES; ++s) issue();
 
   bool dead = false;
-  int c_rot = 0;
-  Segment cs = first_segment(ln, prefix, last, a.n_kv, u0, u1);
+  if (lane < 2) parts[2 * warp + lane].state = kNoPart;
   // rows 0..7 of a product stand for positions 0, 4, 1, 5, 2, 6, 3, 7 and rows 8..15 for 8 more, so that
   // the transposed P pairs positions t and t + 4
   const int kpos = (gr >> 1) + 4 * (gr & 1);
-  for (;;) {
+  while (u0 != u1) {
     const TileRows tr = tile_rows(a, ln, ln.tile0 + cs.k);
     // queries: the operand of block j and vector gr is entries 4t..4t+3 of the block
     uint32_t qf[TERMS][NQ][NB][2];
@@ -425,7 +471,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       for (int j = 0; j < NB; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
     }
 #pragma unroll 1
-    for (int page = cs.page0 + 2 * ((warp - c_rot) & 7); page < cs.page1 && !dead; page += 16) {
+    for (int page = cs.page0; page < cs.page1 && !dead; page += 2) {
       const int s = used % S::STAGES;
       if (!warp_ok(mbar_wait(smem_u32(bar + s), (used / S::STAGES) & 1u, a.err, abort_flag, a.wait_ns))) {
         dead = true;
@@ -579,99 +625,137 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       ++used;
       issue();
     }
-    // ---- the warps' results join
+    // ---- the segment's end
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], w);
-    auto give = [&](int slot) {
+    const bool ends = cs.next >= u1;
+    if (cs.from_start && cs.to_end) {
+      // a whole range: its rows, through the tables' shared memory (vectors' entries side by side)
+      float* buf = reinterpret_cast<float*>(my_tab);
+      constexpr int COLS = 8;  // entries of all the vectors at a time
+      static_assert(S::ROWS * COLS * 4 <= S::TAB, "");
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int v = slot * S::ROWS + n * 8 + 2 * t + c;
-          if (gr == 0) {
-            join_m[v] = -nm[n][c];
-            join_l[v] = l[n][c];
-          }
+          const float inv = l[n][c] > 0.f ? kPackedUnit / l[n][c] : 0.f;
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
-            join_o[v * S::OROW + 16 * j + gr] = o[j][n][c];
-            join_o[v * S::OROW + 16 * j + 8 + gr] = o[j][n][c + 2];
+            o[j][n][c] *= inv;
+            o[j][n][c + 2] *= inv;
           }
         }
-    };
-    if constexpr (S::JW < kSmallWarps) {  // the upper warps' results first, taken over by the lower ones
-      if (warp >= S::JW) give(warp - S::JW);
-      __syncthreads();
-      if (warp < S::JW) {
+#pragma unroll
+      for (int j8 = 0; j8 < 2 * NB; ++j8) {
+        __syncwarp();
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int v = warp * S::ROWS + n * 8 + 2 * t + c;
-            const float m = join_m[v], mx = fmaxf(m, -nm[n][c]);
-            if (mx != -INFINITY) {
-              const float f = ex2_approx(-nm[n][c] - mx), q = ex2_approx(m - mx);
-              nm[n][c] = -mx;
-              l[n][c] = l[n][c] * f + join_l[v] * q;
+          for (int c = 0; c < 2; ++c) buf[(n * 8 + 2 * t + c) * COLS + gr] = o[j8 / 2][n][c + 2 * (j8 & 1)];
+        __syncwarp();
 #pragma unroll
-              for (int j = 0; j < NB; ++j) {
-                o[j][n][c] = o[j][n][c] * f + join_o[v * S::OROW + 16 * j + gr] * q;
-                o[j][n][c + 2] = o[j][n][c + 2] * f + join_o[v * S::OROW + 16 * j + 8 + gr] * q;
-              }
-            }
+        for (int n = 0; n < NQ; ++n) {
+          const int v = n * 8 + gr;
+          if (v < tr.M) {
+            const float2 x = *reinterpret_cast<const float2*>(buf + v * COLS + 2 * t);
+            const int m = tr.m0 + v;
+            T* out = static_cast<T*>(a.out) + (long long)(tr.r0 + m / G) * a.out_stride + (cs.g * G + m % G) * HD + 8 * j8 + 2 * t;
+            if constexpr (TERMS == 1) *reinterpret_cast<uint32_t*>(out) = pack_bf16(x.x, x.y);
+            else *reinterpret_cast<float2*>(out) = x;
           }
-      }
-      __syncthreads();
-    }
-    if (warp < S::JW) give(warp);
-    __syncthreads();
-    {
-      const bool done = cs.from_start && cs.to_end;
-      float* rec = done ? nullptr : part_record<HD>(ln, blockIdx.x, cs.from_start);
-#pragma unroll 1
-      for (int i = tid; i < tr.M * (HD / 4); i += kSmallWarps * 32) {
-        const int v = i / (HD / 4), e = (i - v * (HD / 4)) * 4;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < S::JW; ++w) mx = fmaxf(mx, join_m[w * S::ROWS + v]);
-        float sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < S::JW; ++w) {
-          const float m = join_m[w * S::ROWS + v];
-          const float f = m == -INFINITY ? 0.f : ex2_approx(m - mx);
-          sum = fmaf(f, join_l[w * S::ROWS + v], sum);
-          const float4 y = *reinterpret_cast<const float4*>(join_o + (w * S::ROWS + v) * S::OROW + e);
-          x[0] = fmaf(f, y.x, x[0]); x[1] = fmaf(f, y.y, x[1]); x[2] = fmaf(f, y.z, x[2]); x[3] = fmaf(f, y.w, x[3]);
-        }
-        if (done) {
-          const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
-          const int m = tr.m0 + v;
-          T* out = static_cast<T*>(a.out) + (long long)(tr.r0 + m / G) * a.out_stride + (cs.g * G + m % G) * HD + e;
-          if constexpr (TERMS == 1)
-            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
-          else
-            *reinterpret_cast<float4*>(out) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-        } else {
-          if (e == 0) {
-            rec[v] = mx;
-            rec[S::ROWS + v] = sum;
-          }
-          *reinterpret_cast<float4*>(rec + 2 * S::ROWS + v * HD + e) = make_float4(x[0], x[1], x[2], x[3]);
         }
       }
+      __syncwarp();
+    } else {
+      // part of a range: kept for the join.  A range that began before this warp's piece comes first; if
+      // more ranges follow, its part waits in the workspace (the ring is still in use)
+      if (dead)  // leave no copy in flight into this CTA's shared memory
+        for (; used < issued; ++used)
+          mbar_wait(smem_u32(bar + used % S::STAGES), (used / S::STAGES) & 1u, a.err, nullptr, a.wait_ns);
+      float* dst = ends ? reinterpret_cast<float*>(my_ring)
+                        : ln.spill + ((size_t)blockIdx.x * kSmallWarps + warp) * S::PIECE;
+      __syncwarp();
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int v = n * 8 + 2 * t + c;
+          if (gr == 0) {
+            dst[S::ROWS * S::OROW + v] = -nm[n][c];
+            dst[S::ROWS * (S::OROW + 1) + v] = l[n][c];
+          }
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            dst[v * S::OROW + 16 * j + gr] = o[j][n][c];
+            dst[v * S::OROW + 16 * j + 8 + gr] = o[j][n][c + 2];
+          }
+        }
+      if (lane == 0) {
+        Part p;
+        p.data = dst;
+        p.tr = tr;
+        p.g = cs.g;
+        p.state = cs.from_start ? kBegins : cs.to_end ? kEnds : kGoesOn;
+        parts[2 * warp + (cs.from_start ? 1 : 0)] = p;
+      }
     }
-    if (cs.next >= u1) break;
-    c_rot += (max(0, cs.page1 - cs.page0) + 1) >> 1;
-    cs = next_segment(ln, prefix, last, a.n_kv, cs, u1);
-    __syncthreads();  // the joint buffer is read
+    if (ends) break;
+    cs = walk.after(cs, u1);
   }
-  if (dead)  // leave no copy in flight into this CTA's shared memory
+  if (dead)
     for (; used < issued; ++used)
       mbar_wait(smem_u32(bar + used % S::STAGES), (used / S::STAGES) & 1u, a.err, nullptr, a.wait_ns);
+  // ---- ranges shared by warps: each is a run of parts, one per warp, the first of which may have
+  // begun before this CTA and the last of which may go on behind it
+  __syncthreads();
+  int run0 = -1;  // index of the run's first part
+#pragma unroll 1
+  for (int i = 0; i <= 2 * kSmallWarps; ++i) {
+    const int state = i < 2 * kSmallWarps ? parts[i].state : kNoPart;
+    if (state != kNoPart && run0 < 0) run0 = i;
+    const bool closed = state == kEnds;
+    if (run0 < 0 || !(closed || i == 2 * kSmallWarps)) continue;
+    const Part head = parts[run0];
+    const int end = min(i + 1, 2 * kSmallWarps);
+    const bool begins = head.state == kBegins, done = begins && closed;
+    float* rec = done ? nullptr : part_record<HD>(ln, blockIdx.x, begins);
+#pragma unroll 1
+    for (int x4 = tid; x4 < head.tr.M * (HD / 4); x4 += kSmallWarps * 32) {
+      const int v = x4 / (HD / 4), e = (x4 - v * (HD / 4)) * 4;
+      float mx = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int w = run0; w < end; ++w)
+        if (parts[w].state != kNoPart) mx = fmaxf(mx, parts[w].data[S::ROWS * S::OROW + v]);
+      for (int w = run0; w < end; ++w) {
+        if (parts[w].state == kNoPart) continue;
+        const float* d = parts[w].data;
+        const float m = d[S::ROWS * S::OROW + v];
+        const float f = m == -INFINITY ? 0.f : ex2_approx(m - mx);
+        sum = fmaf(f, d[S::ROWS * (S::OROW + 1) + v], sum);
+        const float4 y = *reinterpret_cast<const float4*>(d + v * S::OROW + e);
+        x[0] = fmaf(f, y.x, x[0]); x[1] = fmaf(f, y.y, x[1]); x[2] = fmaf(f, y.z, x[2]); x[3] = fmaf(f, y.w, x[3]);
+      }
+      if (done) {
+        const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
+        const int m = head.tr.m0 + v;
+        T* out = static_cast<T*>(a.out) + (long long)(head.tr.r0 + m / G) * a.out_stride + (head.g * G + m % G) * HD + e;
+        if constexpr (TERMS == 1)
+          *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+        else
+          *reinterpret_cast<float4*>(out) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+      } else {
+        if (e == 0) {
+          rec[v] = mx;
+          rec[S::ROWS + v] = sum;
+        }
+        *reinterpret_cast<float4*>(rec + 2 * S::ROWS + v * HD + e) = make_float4(x[0], x[1], x[2], x[3]);
+      }
+    }
+    run0 = -1;
+  }
 }
 
 // ----------------------------------------------------------------------------- merge of cut ranges
@@ -703,13 +787,11 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
   TileRows tr{0, 0, 0};
   if (k < ln.n_tiles) {
     const int p0 = __ldcg(ln.prefix + k), p1 = __ldcg(ln.prefix + k + 1);
-    const long long tot = (long long)__ldcg(ln.prefix + ln.n_tiles) * a.n_kv;
+    const uint32_t tot = (uint32_t)__ldcg(ln.prefix + ln.n_tiles) * a.n_kv;
     if (p1 > p0) {
-      const int n = line_ctas(tot, grid, ln.min_units);
-      const long long U0 = (long long)p0 * a.n_kv + (long long)g * (p1 - p0), U1 = U0 + (p1 - p0);
-      int c0 = (int)(U0 * n / tot), c1 = (int)((U1 - 1) * n / tot);
-      while (line_cut(tot, n, c0 + 1) <= U0) ++c0;
-      while (line_cut(tot, n, c1 + 1) <= U1 - 1) ++c1;
+      const Cuts cuts(tot, line_ctas(tot, grid, ln.min_units));
+      const uint32_t first = (uint32_t)p0 * a.n_kv + (uint32_t)g * (p1 - p0);
+      const int c0 = (int)cuts.piece(first), c1 = (int)cuts.piece(first + (p1 - p0) - 1);
       tr = tile_rows(a, ln, ln.tile0 + k);
       live = c1 > c0 && v < tr.M;
       if (live) {
@@ -812,30 +894,43 @@ cudaError_t launch_merge(const PackedAttnArgs& a, const Line& ln, int grid, cuda
                     grid, split);
 }
 
-template <typename T, int HD, int NQ>
-cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
-  using C = Small<T, HD, NQ>;
+// The launch's line for tiles of `tile_rows` vectors and units of `unit_pages`, and how many of its tiles one
+// launch takes (their units, counted in 32 bits, and kPlanTiles bound it).
+Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_units, int* tiles_per_launch) {
   const int G = a.n_q / a.n_kv;
   const long long vectors = (long long)a.max_rows * G;
   Line ln{};
-  ln.tile_rows = C::ROWS;
-  ln.tps = (int)((vectors + C::ROWS - 1) / C::ROWS);
+  ln.tile_rows = tile_rows;
+  ln.unit_pages = unit_pages;
+  ln.tps = (int)((vectors + tile_rows - 1) / tile_rows);
   ln.whole = a.max_pages <= kWholePages;
-  ln.min_units = ln.whole ? 1 : 2;
-  const int rows = std::min(a.max_rows, C::ROWS / G + 2);
+  ln.min_units = min_units;
+  const int rows = std::min(a.max_rows, tile_rows / G + 2);
   ln.lanes = 1;
   while (ln.lanes < 32 && ln.lanes * 4 < rows) ln.lanes *= 2;
-  ln.prefix = static_cast<int*>(a.workspace);
-  ln.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kPrefixBytes);
+  const long long units = (long long)a.n_kv * ((a.max_pages + unit_pages - 1) / unit_pages);  // of a tile, at most
+  *tiles_per_launch = (int)std::min<long long>(kPlanTiles, std::max(1LL, (1LL << 31) / units));
+  return ln;
+}
+
+template <typename T, int HD, int NQ>
+cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
+  using C = Small<T, HD, NQ>;
+  int per_launch = 0;
+  Line ln = make_line(a, C::ROWS, 2, kSmallWarps, &per_launch);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  ln.prefix = reinterpret_cast<int*>(ws);
+  ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
+  ln.spill = ln.part + (size_t)sms * C::CTAS * 2 * C::ROWS * (HD + 2);
   cudaError_t e = allow_smem<attend_small_kernel<T, HD, NQ>>(C::smem(kPlanTiles));
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)a.B * ln.tps;
-  for (long long t0 = 0; t0 < tiles; t0 += kPlanTiles) {
+  for (long long t0 = 0; t0 < tiles; t0 += per_launch) {
     ln.tile0 = (int)t0;
-    ln.n_tiles = (int)std::min<long long>(kPlanTiles, tiles - t0);
-    // no more CTAs than the table's positions could keep busy
-    const long long units = (long long)ln.n_tiles * a.n_kv *
-                            (ln.whole ? 1 : ((long long)a.max_pages * kPackedPage + kUnit - 1) / kUnit);
+    ln.n_tiles = (int)std::min<long long>(per_launch, tiles - t0);
+    // no more CTAs than the tables' positions could keep busy
+    const long long ranges = (long long)ln.n_tiles * a.n_kv;
+    const long long units = ranges * ((a.max_pages + ln.unit_pages - 1) / ln.unit_pages);
     const int grid = (int)std::min<long long>((long long)sms * C::CTAS, std::max(1LL, units / ln.min_units));
     e = launch_pdl(attend_small_kernel<T, HD, NQ>, dim3(grid), dim3(kSmallWarps * 32), C::smem(ln.n_tiles), s, a, ln);
     if (e != cudaSuccess) return e;
@@ -854,7 +949,9 @@ cudaError_t launch_attend_typed(const PackedAttnArgs& a, int sms, cudaStream_t s
 }  // namespace
 
 size_t packed_attn_workspace_bytes(int head_dim, pe_dtype, int sms) {
-  return kPrefixBytes + (size_t)sms * kMaxCtasPerSm * 2 * 16 * (head_dim + 2) * 4;
+  // two records per CTA, and a part per warp, of up to 16 vectors
+  const size_t rec = (size_t)16 * (head_dim + 2) * 4, part = (size_t)16 * (head_dim + 6) * 4;
+  return kPrefixBytes + (size_t)sms * kMaxCtasPerSm * (2 * rec + kSmallWarps * part);
 }
 
 cudaError_t launch_attend_packed(const PackedAttnArgs& a, pe_dtype dt, int sms, cudaStream_t s) {
