@@ -187,8 +187,9 @@ def _check(status: int, what: str):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle: torch.cuda.current_stream() builds a Stream object each time (2.8 us on a Grace core)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None
+                           else stream.cuda_stream)
 
 
 def set_trace_events(events) -> None:
@@ -308,22 +309,28 @@ def inject_kv(cfg, weights: DeviceWeights, w_inj, kv: DeviceKV, block_table, pre
     _check(st, "pe_inject_kv")
 
 
-def _tensor(t, what: str, device, dtype, shape=None) -> int:
-    """Address of a contiguous tensor of this type (and shape) on this device."""
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor{'' if shape is None else f' of shape {shape}'} "
-                         f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+# The checks of the packed-cache calls.  Small calls take a few microseconds on the GPU, so these go by
+# the cheapest questions a tensor answers (device index, dtype identity) and explain only when one fails.
+
+def _tensor(t, what: str, dev: int, dtype, shape=None) -> int:
+    """Address of a contiguous tensor of this type (and shape) on CUDA device ``dev``."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
+    raise ValueError(f"{what}: expected a contiguous {dtype} tensor{'' if shape is None else f' of shape {shape}'} "
+                     f"on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _rows(t, what: str, device, dtype, width: int, n: int):
+def _rows(t, what: str, dev: int, dtype, width: int, n: int):
     """Address and row stride of n rows of `width` elements ([n][width] or [n][heads][head_dim], each row
     contiguous)."""
-    if t.dtype != dtype or t.device != device or t.dim() < 2 or t.shape[0] != n:
-        raise ValueError(f"{what}: expected {n} rows of {dtype} on {device}, got {t.dtype} {tuple(t.shape)} on "
+    shape = t.shape
+    if t.dtype is not dtype or t.get_device() != dev or len(shape) < 2 or shape[0] != n:
+        raise ValueError(f"{what}: expected {n} rows of {dtype} on cuda:{dev}, got {t.dtype} {tuple(shape)} on "
                          f"{t.device}")
+    if t.is_contiguous() and t.numel() == n * width and n > 0:
+        return t.data_ptr(), width
     inner = 1
-    for size, stride in zip(t.shape[:0:-1], t.stride()[:0:-1]):
+    for size, stride in zip(shape[:0:-1], t.stride()[:0:-1]):
         if size != 1 and stride != inner:
             raise ValueError(f"{what}: the elements of a row have to be contiguous")
         inner *= size
@@ -332,11 +339,19 @@ def _rows(t, what: str, device, dtype, width: int, n: int):
     return t.data_ptr(), t.stride(0) if n > 1 else width
 
 
-def _current(t) -> torch.device:
+def _current(t) -> int:
     """The device of a call's tensors, which has to be the current one (its stream is used)."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"expected tensors on the current CUDA device, got {t.device}")
-    return t.device
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"expected tensors on the current device cuda:{dev}, got {t.device}")
+    return dev
+
+
+def _pool(cfg, pool, dev: int):
+    shape = pool.shape
+    if len(shape) != 3 or shape[1] != cfg.n_kv or shape[2] != 18 * cfg.head_dim:
+        raise ValueError(f"pool: expected [pages][{cfg.n_kv}][{18 * cfg.head_dim}], got {tuple(shape)}")
+    return _tensor(pool, "pool", dev, torch.uint8), shape[0]
 
 
 def packed_page_bytes(cfg) -> int:
@@ -349,14 +364,10 @@ def attend_workspace_bytes(cfg) -> int:
     return int(lib().pe_attend_workspace_bytes(ctypes.byref(cfg)))
 
 
-def _pool(cfg, pool, device):
-    return _tensor(pool, "pool", device, torch.uint8, (pool.shape[0], cfg.n_kv, 18 * cfg.head_dim)), pool.shape[0]
-
-
 def pack_kv(cfg, k, v, slots, pool, err, stream=None):
     """Round rows k, v ([n][n_kv][head_dim] or [n][n_kv*head_dim], any row stride of whole 16 bytes) to 4 bits
     and write them to the packed cache ``pool`` (alloc_packed_pool) at ``slots`` (int64; -1: passed over)."""
-    L, dev, n, w = lib(), _current(pool), slots.shape[0], cfg.n_kv * cfg.head_dim
+    L, dev, n, w = lib(), _current(pool), len(slots), cfg.n_kv * cfg.head_dim
     dt = cfg.torch_dtype
     kp, ks = _rows(k, "k", dev, dt, w, n)
     vp, vs = _rows(v, "v", dev, dt, w, n)
@@ -370,7 +381,7 @@ def pack_kv(cfg, k, v, slots, pool, err, stream=None):
 
 def unpack_kv(cfg, pool, slots, k_out, v_out, err, stream=None):
     """Read the entries at ``slots`` back as the values they stand for (-1: the output row stays as it is)."""
-    L, dev, n, w = lib(), _current(pool), slots.shape[0], cfg.n_kv * cfg.head_dim
+    L, dev, n, w = lib(), _current(pool), len(slots), cfg.n_kv * cfg.head_dim
     dt = cfg.torch_dtype
     kp, ks = _rows(k_out, "k_out", dev, dt, w, n)
     vp, vs = _rows(v_out, "v_out", dev, dt, w, n)
@@ -386,7 +397,7 @@ def attend_packed(cfg, q, pool, block_table, row_start, positions, max_rows, out
     """Causal grouped-query attention over a packed cache: sequence b's rows row_start[b]..row_start[b+1]-1 of
     q [n][n_q*head_dim], row r seeing positions 0..positions[r] (-1: none, zeros); ``max_rows`` bounds the rows of
     one sequence.  ``workspace``: alloc_attend_workspace."""
-    L, dev, n, w = lib(), _current(pool), positions.shape[0], cfg.n_q * cfg.head_dim
+    L, dev, n, w = lib(), _current(pool), len(positions), cfg.n_q * cfg.head_dim
     dt, i32 = cfg.torch_dtype, torch.int32
     qp, qs = _rows(q, "q", dev, dt, w, n)
     op, os_ = _rows(out, "out", dev, dt, w, n)
