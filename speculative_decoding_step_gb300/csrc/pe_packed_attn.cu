@@ -38,18 +38,43 @@ PE_DEV uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-PE_DEV bool warp_ok(bool ok) { return __all_sync(0xFFFFFFFFu, ok); }
+// n / d for n < 2^31 by a multiplication: mul = ceil(2^shift / d), shift = 31 + ceil(log2 d), is at most
+// d 2^-shift above 1/d, which is less than 1/(n d).  (A division by a value that the compiler does not know
+// is a chain of about 150 cycles, several of which stood before the first load.)
+struct Div {
+  uint32_t mul;
+  int shift;
+};
+Div make_div(uint32_t d) {
+  int l = 0;
+  while ((1u << l) < d) ++l;
+  return Div{(uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+PE_DEV uint32_t operator/(uint32_t n, const Div& d) { return (uint32_t)(((uint64_t)n * d.mul) >> d.shift); }
+
+// r / d where the quotient is at most 2^16: the fp32 quotient is off by one at most.
+PE_DEV uint32_t small_quotient(uint32_t r, uint32_t d) {
+  uint32_t q = (uint32_t)__fdividef((float)r, (float)d);
+  if ((uint64_t)q * d > r) --q;
+  else if (r - q * d >= d) ++q;
+  return q;
+}
 
 // ----------------------------------------------------------------------------- the line of work
 
 struct Line {
   int tile0, n_tiles;  // this launch's tiles: b * tps + t
-  int tps;             // tiles per sequence (host bound)
-  int tile_rows;       // query vectors per tile
+  Div tps;             // tiles per sequence (host bound)
+  int n_tps;
+  Div group, heads;    // query heads per kv head, kv heads
+  Div grid;            // CTAs launched
+  int G;
+  int tile_rows;       // query vectors per tile, 2^rows_log2
+  int rows_log2;
   int unit_pages;      // pages per unit
   int lanes;           // threads that look through one tile's rows (a power of two, at most 32)
   int whole;           // CTAs take whole ranges
-  int min_units;       // a CTA's piece is at least this long where there are fewer units than that for all
+  int min_log2;        // a CTA's piece is at least 2^this units long where there are fewer than that for all
   int* prefix;         // workspace [n_tiles + 1]: units per head before each tile, for the merge
   float* part;         // workspace: records of cut ranges, two per CTA
   float* spill;        // workspace: a warp's piece of a range that began before it (small kernel)
@@ -60,8 +85,7 @@ struct TileRows {
 };
 
 PE_DEV TileRows tile_rows(const PackedAttnArgs& a, const Line& ln, int tile) {
-  const int b = tile / ln.tps, t = tile - (tile / ln.tps) * ln.tps;
-  const int G = a.n_q / a.n_kv;
+  const int b = (int)((uint32_t)tile / ln.tps), t = tile - b * ln.n_tps;
   const int r0 = __ldcg(a.row_start + b);
   const int r1 = a.row_len != nullptr ? r0 + __ldcg(a.row_len + b) : __ldcg(a.row_start + b + 1);
   if (r0 < 0 || r1 < r0 || r1 > a.n_rows || r1 - r0 > a.max_rows) {
@@ -69,7 +93,7 @@ PE_DEV TileRows tile_rows(const PackedAttnArgs& a, const Line& ln, int tile) {
     return TileRows{0, 0, 0};
   }
   const int m0 = t * ln.tile_rows;
-  return TileRows{r0, m0, max(0, min((r1 - r0) * G - m0, ln.tile_rows))};
+  return TileRows{r0, m0, max(0, min((r1 - r0) * ln.G - m0, ln.tile_rows))};
 }
 
 // A row's last visible position: -1 when it sees nothing or its position is out of range.
@@ -82,67 +106,144 @@ PE_DEV int row_limit(const PackedAttnArgs& a, int row) {
   return p;
 }
 
-// prefix[k]: units per head before tile k; last[k]: largest position that tile k sees (-1: none).
-// Every thread of the CTA.
-PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, int* prefix, int* last, int* warp_sums) {
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const int per = ln.lanes, sub = tid & (per - 1), G = a.n_q / a.n_kv;
-  for (int k0 = 0; k0 < ln.n_tiles; k0 += nt / per) {  // the same trip count for every thread
+// The line in shared memory, each array of n_tiles (+ 1) entries.
+struct Layout {
+  int* prefix;  // units per head before the tile
+  int* last;    // largest position that the tile sees (-1: none)
+  int* row0;    // its TileRows
+  int* rows;
+  static constexpr int kBytesPerTile = 16;
+  PE_DEV Layout(void* smem, int n) : prefix(static_cast<int*>(smem)), last(prefix + n + 1), row0(last + n), rows(row0 + n) {}
+  PE_DEV TileRows tile(const Line& ln, int k) const {
+    const int tile = ln.tile0 + k;
+    return TileRows{row0[k], (tile - (int)((uint32_t)tile / ln.tps) * ln.n_tps) * ln.tile_rows, rows[k]};
+  }
+};
+
+PE_DEV int tile_units(const Line& ln, const TileRows& t, int mx) {
+  return t.M == 0 ? 0 : max(1, (mx / kPackedPage + ln.unit_pages) >> (ln.unit_pages == 2 ? 1 : 2));
+}
+
+// Fills the line in.  Every thread of the CTA.
+PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, int* warp_sums) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
+  const int n = ln.n_tiles;
+  constexpr int W = 4;  // tiles per lane
+  if (n <= 32 * W && ln.lanes == 1) {
+    // few tiles of few rows: every warp works the whole line out (the same values go to the same places), so
+    // that none waits for another
+    TileRows t[W];
+    int mx[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const int k = lane + 32 * i;
+      t[i] = k < n ? tile_rows(a, ln, ln.tile0 + k) : TileRows{0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      mx[i] = -1;
+      if (t[i].M > 0) {
+        const int ra = t[i].r0 + (int)((uint32_t)t[i].m0 / ln.group);
+        const int rb = t[i].r0 + (int)((uint32_t)(t[i].m0 + t[i].M - 1) / ln.group);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (ra + r <= rb) mx[i] = max(mx[i], row_limit(a, ra + r));
+      }
+    }
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const int k = lane + 32 * i;
+      if (32 * i >= n) break;
+      int inc = tile_units(ln, t[i], mx[i]);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      inc += before;
+      if (k < n) {
+        lo.prefix[k + 1] = inc;
+        lo.last[k] = mx[i];
+        lo.row0[k] = t[i].r0;
+        lo.rows[k] = t[i].M;
+      }
+      before = __shfl_sync(0xFFFFFFFFu, inc, 31);
+    }
+    if (lane == 0) lo.prefix[0] = 0;
+    __syncwarp();
+    return;
+  }
+  const int per = ln.lanes, sub = tid & (per - 1);
+  for (int k0 = 0; k0 < n; k0 += nt / per) {  // the same trip count for every thread
     const int k = k0 + tid / per;
-    int mx = -1, M = 0;
-    if (k < ln.n_tiles) {
-      const TileRows t = tile_rows(a, ln, ln.tile0 + k);
-      M = t.M;
-      if (M > 0) {
-        const int ra = t.r0 + t.m0 / G, rb = t.r0 + (t.m0 + M - 1) / G;
+    int mx = -1;
+    TileRows t{0, 0, 0};
+    if (k < n) {
+      t = tile_rows(a, ln, ln.tile0 + k);
+      if (t.M > 0) {
+        const int ra = t.r0 + (int)((uint32_t)t.m0 / ln.group);
+        const int rb = t.r0 + (int)((uint32_t)(t.m0 + t.M - 1) / ln.group);
 #pragma unroll 4
         for (int r = ra + sub; r <= rb; r += per) mx = max(mx, row_limit(a, r));
       }
     }
     for (int o = per >> 1; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    if (k < ln.n_tiles && sub == 0) {
-      const int positions = ln.unit_pages * kPackedPage;
-      prefix[k + 1] = M == 0 ? 0 : max(1, (mx + positions) / positions);
-      last[k] = mx;
+    if (k < n && sub == 0) {
+      lo.prefix[k + 1] = tile_units(ln, t, mx);
+      lo.last[k] = mx;
+      lo.row0[k] = t.r0;
+      lo.rows[k] = t.M;
     }
   }
   __syncthreads();
   // inclusive scan of prefix[1..n]: a run of consecutive tiles per thread, then over threads
-  const int run = (ln.n_tiles + nt - 1) / nt, k0 = tid * run, k1 = min(ln.n_tiles, k0 + run);
+  const int run = (n + nt - 1) / nt, k0 = tid * run, k1 = min(n, k0 + run);
   int sum = 0;
-  for (int k = k0; k < k1; ++k) sum += prefix[k + 1];
+  for (int k = k0; k < k1; ++k) sum += lo.prefix[k + 1];
   int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-    if ((tid & 31) >= o) inc += v;
+    if (lane >= o) inc += v;
   }
-  if ((tid & 31) == 31) warp_sums[tid >> 5] = inc;
+  if (lane == 31) warp_sums[tid >> 5] = inc;
   __syncthreads();
   int before = inc - sum;
   for (int w = 0; w < (tid >> 5); ++w) before += warp_sums[w];
-  if (tid == 0) prefix[0] = 0;
+  if (tid == 0) lo.prefix[0] = 0;
   for (int k = k0; k < k1; ++k) {
-    before += prefix[k + 1];
-    prefix[k + 1] = before;
+    before += lo.prefix[k + 1];
+    lo.prefix[k + 1] = before;
   }
   __syncthreads();
 }
 
-// T units in n equal pieces (the first T % n of them one longer): the first unit of piece c, and the
-// piece that holds unit u.
+// T units in n equal pieces (the first T % n of them one longer): n is the grid, or less where that would
+// leave a piece shorter than 2^min_log2 units.
 struct Cuts {
   uint32_t n, q, r;
-  PE_DEV Cuts(uint32_t T, uint32_t n_) : n(n_), q(T / n_), r(T - T / n_ * n_) {}
+  PE_DEV Cuts(const Line& ln, int grid, uint32_t T) {
+    n = grid;
+    if ((T >> ln.min_log2) >= n) {
+      q = T / ln.grid;
+      r = T - q * n;
+    } else {
+      n = max(1u, T >> ln.min_log2);
+      q = T >> ln.min_log2 == 0 ? T : 1u << ln.min_log2;
+      r = T - q * n;
+      while (r >= n) {  // r < 2^min_log2
+        r -= n;
+        ++q;
+      }
+    }
+  }
   PE_DEV uint32_t first(uint32_t c) const { return q * c + min(c, r); }
-  PE_DEV uint32_t piece(uint32_t u) const {
+  PE_DEV uint32_t piece(uint32_t u) const {  // the one that holds unit u
     const uint32_t longer = r * (q + 1);
-    return u < longer ? u / (q + 1) : r + (u - longer) / q;  // q = 0: every unit lies in a longer piece
+    return u < longer ? small_quotient(u, q + 1) : r + small_quotient(u - longer, q);
   }
 };
-PE_DEV uint32_t line_ctas(uint32_t T, int grid, int min_units) {
-  return min((uint32_t)grid, max(1u, T / (uint32_t)min_units));
-}
 
 // The part of a (tile, head) range that a piece of the line holds.
 struct Segment {
@@ -153,58 +254,57 @@ struct Segment {
 };
 
 struct Walk {
-  const int *prefix, *last;
-  int n_kv, unit_pages;
+  Layout lo;
+  int n_tiles, n_kv, unit_pages;
 
-  PE_DEV int tile_of(uint32_t u, int n_tiles) const {  // the last tile that starts at or before u and has units
-    int lo = 0, hi = n_tiles;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((uint32_t)prefix[mid] * n_kv <= u) lo = mid;
-      else hi = mid;
+  PE_DEV int tile_of(uint32_t u) const {  // the last tile that starts at or before u (the whole warp)
+    int at = 0;
+    for (int step = 1024; step > 0; step >>= 5) {  // 32 places at a time: the 1024 tiles of a launch in three rounds
+      if (step > n_tiles) continue;
+      const int k = at + (int)(threadIdx.x & 31) * step;
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, k < n_tiles && (uint32_t)lo.prefix[min(k, n_tiles)] * n_kv <= u);
+      at += (31 - __clz(hit)) * step;
     }
-    return lo;
+    return at;
   }
   PE_DEV Segment at(int k, uint32_t u, uint32_t u1) const {
     Segment s;
-    const uint32_t nb = prefix[k + 1] - prefix[k];
-    const uint32_t r = u - (uint32_t)prefix[k] * n_kv;
+    const uint32_t p0 = lo.prefix[k], nb = lo.prefix[k + 1] - p0, r = u - p0 * n_kv;
     s.k = k;
-    s.g = (int)(r / nb);
+    s.g = (int)small_quotient(r, nb);
     const uint32_t blk = r - s.g * nb, cnt = min(nb - blk, u1 - u);
     s.from_start = blk == 0;
     s.to_end = blk + cnt == nb;
     s.next = u + cnt;
     s.page0 = (int)blk * unit_pages;
-    s.page1 = min((last[k] + kPackedPage) / kPackedPage, (int)(blk + cnt) * unit_pages);
+    s.page1 = min((lo.last[k] + kPackedPage) / kPackedPage, (int)(blk + cnt) * unit_pages);
     return s;
   }
   PE_DEV Segment after(const Segment& s, uint32_t u1) const {
     int k = s.k;
-    if (s.next >= (uint32_t)prefix[k + 1] * n_kv)
+    if (s.next >= (uint32_t)lo.prefix[k + 1] * n_kv)
       do ++k;
-      while (prefix[k + 1] == prefix[k]);
+      while (lo.prefix[k + 1] == lo.prefix[k]);
     return at(k, s.next, u1);
   }
   // The first unit of the range that holds unit u (u < T).
-  PE_DEV uint32_t range_start(uint32_t u, int n_tiles) const {
-    const int k = tile_of(u, n_tiles);
-    const uint32_t nb = prefix[k + 1] - prefix[k];
-    return u - (u - (uint32_t)prefix[k] * n_kv) % nb;
+  PE_DEV uint32_t range_start(uint32_t u) const {
+    const int k = tile_of(u);
+    const uint32_t p0 = lo.prefix[k], nb = lo.prefix[k + 1] - p0, r = u - p0 * n_kv;
+    return u - (r - small_quotient(r, nb) * nb);
   }
 };
 
 // The units of this CTA: [u0, u1) of T.
 PE_DEV void cta_units(const Line& ln, const Walk& w, uint32_t T, uint32_t& u0, uint32_t& u1) {
   u0 = u1 = 0;
-  const uint32_t n = line_ctas(T, gridDim.x, ln.min_units);
-  if (T == 0 || blockIdx.x >= n) return;
-  const Cuts cuts(T, n);
+  const Cuts cuts(ln, gridDim.x, T);
+  if (T == 0 || blockIdx.x >= cuts.n) return;
   u0 = cuts.first(blockIdx.x);
   u1 = cuts.first(blockIdx.x + 1);
   if (ln.whole) {
-    u0 = w.range_start(u0, ln.n_tiles);
-    if (u1 < T) u1 = w.range_start(u1, ln.n_tiles);
+    u0 = w.range_start(u0);
+    if (u1 < T) u1 = w.range_start(u1);
   }
 }
 
@@ -216,8 +316,9 @@ PE_DEV float* part_record(const Line& ln, int cta, bool from_start) {
 
 // ----------------------------------------------------------------------------- few query vectors: warp MMAs
 //
-// A warp takes pairs of pages (32 positions), brought into its own ring of shared-memory stages by one
-// bulk copy per page, and runs on its own until the segment ends: S^T = K Q^T and O^T += V^T P^T with
+// A warp takes pairs of pages (32 positions), brought into its own ring of shared-memory stages by
+// 16-byte asynchronous copies of its lanes (a bulk copy per page took longer to issue: the SM's copy
+// unit saw a request per 1152 bytes): S^T = K Q^T and O^T += V^T P^T with
 // 16 x 8 x 16 warp MMAs, positions (then entries) on the 16 side and 8 query vectors on the other, so one
 // unpacked page serves NQ * 8 vectors and no row is padded beyond 8.
 //   Scales: each lane turns a few of a page's scale bytes into bf16 pairs, into a small table that the
@@ -251,18 +352,26 @@ struct Small {
   static constexpr int KTAB = HD * 4, VTAB = HD * 2, TAB = 2 * (KTAB + VTAB);  // scale tables of a warp (two pages)
   static constexpr int PIECE = ROWS * (OROW + 2);  // floats of a warp's part of a shared range
   static_assert(PIECE * 4 <= STAGES * STAGE, "it fits the warp's drained ring");
-  static constexpr int FIXED = RING + kSmallWarps * TAB + kSmallWarps * STAGES * 8 + 16 * 4 + 2 * kSmallWarps * 32;
-  static size_t smem(int n_tiles) { return 128 + FIXED + 8 * (size_t)(n_tiles + 1); }
+  static constexpr int FIXED = RING + kSmallWarps * TAB + 16 * 4 + 2 * kSmallWarps * 16;
+  static size_t smem(int n_tiles) { return 128 + FIXED + Layout::kBytesPerTile * (size_t)n_tiles + 4; }
 };
 
-// A warp's part of a range that it shares with its neighbours.
+// A warp's part of a range that it shares with its neighbours: [ROWS][OROW] outputs, [ROWS] maxima, [ROWS]
+// sums, in its ring or (a part that began before the warp's piece, when more ranges follow) in the
+// workspace.
 enum PartState : int { kNoPart, kBegins, kGoesOn, kEnds };
 struct Part {
-  const float* data;  // [ROWS][OROW] outputs, then [ROWS] maxima and [ROWS] sums
-  TileRows tr;
-  int g, state;
+  int state, k, g, spilled;
 };
-static_assert(sizeof(Part) <= 32, "");
+
+PE_DEV void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+PE_DEV void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+PE_DEV void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 PE_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -326,50 +435,44 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 127) & ~uintptr_t(127));
   uint8_t* tabs = sm + S::RING;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(tabs + kSmallWarps * S::TAB);
-  int* scratch = reinterpret_cast<int*>(bars + kSmallWarps * S::STAGES);  // [16]
-  Part* parts = reinterpret_cast<Part*>(scratch + 16);                    // [warps][2]
-  int* prefix = reinterpret_cast<int*>(parts + 2 * kSmallWarps);
-  int* last = prefix + ln.n_tiles + 1;
+  int* scratch = reinterpret_cast<int*>(tabs + kSmallWarps * S::TAB);  // [16]
+  Part* parts = reinterpret_cast<Part*>(scratch + 16);                 // [warps][2]
+  const Layout lo(parts + 2 * kSmallWarps, ln.n_tiles);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
-  uint64_t* bar = bars + warp * S::STAGES;
   uint8_t* my_ring = sm + warp * S::STAGES * S::STAGE;
   uint8_t* my_tab = tabs + warp * S::TAB;
-  if (lane == 0) {
-    for (int s = 0; s < S::STAGES; ++s) mbar_init(smem_u32(bar + s), 1);
-    fence_mbar_init();
-  }
-  volatile int* abort_flag = scratch + 15;
-  if (tid == 0) *abort_flag = 0;
+  const int G = ln.G;
+  const float sl2 = a.scale * 1.4426950408889634f * kPackedUnit;
+  float* spill = ln.spill + (size_t)blockIdx.x * kSmallWarps * S::PIECE;
+  if (lane < 2) parts[2 * warp + lane].state = kNoPart;
   pdl_wait();
   pdl_trigger();
-  lay_out(a, ln, prefix, last, scratch);
-  const Walk walk{prefix, last, a.n_kv, ln.unit_pages};
-  const uint32_t total = (uint32_t)prefix[ln.n_tiles] * a.n_kv;
+  lay_out(a, ln, lo, scratch);
+  const Walk walk{lo, ln.n_tiles, a.n_kv, ln.unit_pages};
+  const uint32_t total = (uint32_t)lo.prefix[ln.n_tiles] * a.n_kv;
   if (blockIdx.x == 0 && !ln.whole)
-    for (int k = tid; k <= ln.n_tiles; k += blockDim.x) ln.prefix[k] = prefix[k];
+    for (int k = tid; k <= ln.n_tiles; k += blockDim.x) ln.prefix[k] = lo.prefix[k];
   uint32_t u0, u1;
   cta_units(ln, walk, total, u0, u1);
-  if (u0 == u1) return;
+  if (u0 == u1) return;  // the whole CTA
   {
-    const Cuts cuts(u1 - u0, kSmallWarps);
-    u1 = u0 + cuts.first(warp + 1);
-    u0 += cuts.first(warp);
+    const uint32_t n = u1 - u0;
+    const uint32_t c0 = (n >> 3) * warp + min((uint32_t)warp, n & 7), c1 = (n >> 3) * (warp + 1) + min((uint32_t)warp + 1, n & 7);
+    u1 = u0 + c1;
+    u0 += c0;
   }
-  const int G = a.n_q / a.n_kv;
-  const float sl2 = a.scale * 1.4426950408889634f * kPackedUnit;
+  static_assert(kSmallWarps == 8, "");
 
   // Two walks over the pairs of pages of the warp's units, the copies `STAGES` pairs ahead of the
   // products.  A unit is a pair, so a pair lacks its second page at a range's end only, where every
   // position of that page is masked.
   Segment ps{}, cs{};
   bool p_done = u0 == u1;
-  if (!p_done) ps = cs = walk.at(walk.tile_of(u0, ln.n_tiles), u0, u1);
+  if (!p_done) ps = cs = walk.at(walk.tile_of(u0), u0, u1);
   int p_i = 0;   // the next pair of the segment
   int ids = -1;  // page ids of 16 pairs, one per lane
   uint32_t issued = 0, used = 0;
   auto issue = [&]() {
-    if (p_done) return;
     int page = ps.page0 + 2 * p_i;
     while (page >= ps.page1) {
       if (ps.next >= u1) {
@@ -384,7 +487,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       const int x = page + lane;
       ids = -1;
       if (x < ps.page1) {
-        ids = __ldcg(a.block_table + (size_t)((ln.tile0 + ps.k) / ln.tps) * a.max_pages + x);
+        ids = __ldcg(a.block_table + (size_t)((uint32_t)(ln.tile0 + ps.k) / ln.tps) * a.max_pages + x);
         if (ids < 0 || ids >= a.num_pages) {
           set_err(a.err, PE_DEV_BAD_PAGE);
           ids = -1;
@@ -392,45 +495,48 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       }
     }
     const int id0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (p_i & 15)), id1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (p_i & 15) + 1);
-    const int s = issued % S::STAGES;
-    uint8_t* dst = my_ring + s * S::STAGE;
+    uint8_t* dst = my_ring + (issued % S::STAGES) * S::STAGE;
+    const size_t step = (size_t)a.n_kv * L::kRecord;
+    const uint8_t* src0 = a.pool + (size_t)ps.g * L::kRecord + (size_t)max(id0, 0) * step + lane * 16;
+    const uint8_t* src1 = a.pool + (size_t)ps.g * L::kRecord + (size_t)max(id1, 0) * step + lane * 16 - L::kRecord;
+    const uint32_t d = smem_u32(dst) + lane * 16;
+#pragma unroll
+    for (int i = 0; i < (S::STAGE + 511) / 512; ++i) {
+      const int at = i * 512 + lane * 16;  // byte of the two records
+      const bool first = i * 512 + 511 < L::kRecord || at < L::kRecord;
+      if (i * 512 + 511 < S::STAGE || at < S::STAGE) copy16(d + i * 512, (first ? src0 : src1) + i * 512);
+    }
     if (id0 < 0 || (id1 < 0 && page + 1 < ps.page1)) {
-      // pages outside the pool stand for zeros: every nibble 8
+      // pages outside the pool stand for zeros: every nibble 8.  (Page 0 was copied in their place.)
+      copy_commit();
+      copy_wait<0>();
+      __syncwarp();
 #pragma unroll 1
       for (int h = 0; h < 2; ++h)
         if ((h == 0 ? id0 : id1) < 0)
-          for (int i = lane; i < L::kRecord / 4; i += 32) reinterpret_cast<uint32_t*>(dst + h * L::kRecord)[i] = 0x88888888u;
-      fence_proxy_async_smem();
-      __syncwarp();
+          for (int i = lane * 16; i < L::kRecord; i += 512)
+            *reinterpret_cast<uint4*>(dst + h * L::kRecord + i) = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
     }
-    if (lane == 0) {
-      const uint32_t b = smem_u32(bar + s);
-      const uint8_t* src = a.pool + (size_t)ps.g * L::kRecord;
-      const size_t step = (size_t)a.n_kv * L::kRecord;
-      mbar_expect_tx(b, (id0 >= 0 ? L::kRecord : 0) + (id1 >= 0 ? L::kRecord : 0));
-      if (id0 >= 0) bulk_g2s(smem_u32(dst), src + (size_t)id0 * step, L::kRecord, b);
-      if (id1 >= 0) bulk_g2s(smem_u32(dst) + L::kRecord, src + (size_t)id1 * step, L::kRecord, b);
-    }
-    ++issued;
     ++p_i;
   };
-#pragma unroll 1
-  for (int s = 0; s < S::STAGES; ++s) issue();
 
-  bool dead = false;
-  if (lane < 2) parts[2 * warp + lane].state = kNoPart;
   // rows 0..7 of a product stand for positions 0, 4, 1, 5, 2, 6, 3, 7 and rows 8..15 for 8 more, so that
   // the transposed P pairs positions t and t + 4
   const int kpos = (gr >> 1) + 4 * (gr & 1);
   while (u0 != u1) {
-    const TileRows tr = tile_rows(a, ln, ln.tile0 + cs.k);
+    const TileRows tr = lo.tile(ln, cs.k);
+    // offset of vector m of the sequence in the rows of q or out
+    auto row_of = [&](int m, int g, long long stride) {
+      const int r = (int)((uint32_t)m / ln.group);
+      return (tr.r0 + r) * stride + (g * G + m - r * G) * HD;
+    };
     // queries: the operand of block j and vector gr is entries 4t..4t+3 of the block
     uint32_t qf[TERMS][NQ][NB][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       const int m = tr.m0 + n * 8 + gr;
       const bool live = n * 8 + gr < tr.M;
-      const T* q = static_cast<const T*>(a.q) + (live ? (long long)(tr.r0 + m / G) * a.q_stride + (cs.g * G + m % G) * HD : 0);
+      const T* q = static_cast<const T*>(a.q) + (live ? row_of(m, cs.g, a.q_stride) : 0);
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         if constexpr (TERMS == 1) {
@@ -456,7 +562,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int v = n * 8 + 2 * t + e;
-        lim[n][e] = v < tr.M ? row_limit(a, tr.r0 + (tr.m0 + v) / G) : INT_MAX;
+        lim[n][e] = v < tr.M ? row_limit(a, tr.r0 + (int)((uint32_t)(tr.m0 + v) / ln.group)) : INT_MAX;
         min_lim = min(min_lim, lim[n][e]);
       }
     min_lim = min(min_lim, __shfl_xor_sync(0xFFFFFFFFu, min_lim, 1));
@@ -471,12 +577,16 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       for (int j = 0; j < NB; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.f;
     }
 #pragma unroll 1
-    for (int page = cs.page0; page < cs.page1 && !dead; page += 2) {
-      const int s = used % S::STAGES;
-      if (!warp_ok(mbar_wait(smem_u32(bar + s), (used / S::STAGES) & 1u, a.err, abort_flag, a.wait_ns))) {
-        dead = true;
-        break;
+    for (int page = cs.page0; page < cs.page1; page += 2) {
+      // a group of copies per step, empty behind the last pair, so that the oldest of STAGES is this step's
+#pragma unroll 1
+      for (; issued < used + S::STAGES; ++issued) {
+        if (!p_done) issue();
+        copy_commit();
       }
+      copy_wait<S::STAGES - 1>();
+      __syncwarp();
+      const int s = used % S::STAGES;
       const uint8_t* recs = my_ring + s * S::STAGE;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -623,7 +733,6 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       }
       __syncwarp();  // the stage and the tables are read
       ++used;
-      issue();
     }
     // ---- the segment's end
 #pragma unroll
@@ -663,7 +772,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
           if (v < tr.M) {
             const float2 x = *reinterpret_cast<const float2*>(buf + v * COLS + 2 * t);
             const int m = tr.m0 + v;
-            T* out = static_cast<T*>(a.out) + (long long)(tr.r0 + m / G) * a.out_stride + (cs.g * G + m % G) * HD + 8 * j8 + 2 * t;
+            T* out = static_cast<T*>(a.out) + row_of(m, cs.g, a.out_stride) + 8 * j8 + 2 * t;
             if constexpr (TERMS == 1) *reinterpret_cast<uint32_t*>(out) = pack_bf16(x.x, x.y);
             else *reinterpret_cast<float2*>(out) = x;
           }
@@ -671,13 +780,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       }
       __syncwarp();
     } else {
-      // part of a range: kept for the join.  A range that began before this warp's piece comes first; if
-      // more ranges follow, its part waits in the workspace (the ring is still in use)
-      if (dead)  // leave no copy in flight into this CTA's shared memory
-        for (; used < issued; ++used)
-          mbar_wait(smem_u32(bar + used % S::STAGES), (used / S::STAGES) & 1u, a.err, nullptr, a.wait_ns);
-      float* dst = ends ? reinterpret_cast<float*>(my_ring)
-                        : ln.spill + ((size_t)blockIdx.x * kSmallWarps + warp) * S::PIECE;
+      // part of a range: kept for the join
+      float* dst = ends ? reinterpret_cast<float*>(my_ring) : spill + (size_t)warp * S::PIECE;
+      if (ends) copy_wait<0>();
       __syncwarp();
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
@@ -694,67 +799,89 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
             dst[v * S::OROW + 16 * j + 8 + gr] = o[j][n][c + 2];
           }
         }
-      if (lane == 0) {
-        Part p;
-        p.data = dst;
-        p.tr = tr;
-        p.g = cs.g;
-        p.state = cs.from_start ? kBegins : cs.to_end ? kEnds : kGoesOn;
-        parts[2 * warp + (cs.from_start ? 1 : 0)] = p;
-      }
+      if (lane == 0)
+        parts[2 * warp + (cs.from_start ? 1 : 0)] =
+            Part{cs.from_start ? kBegins : cs.to_end ? kEnds : kGoesOn, cs.k, cs.g, ends ? 0 : 1};
     }
     if (ends) break;
     cs = walk.after(cs, u1);
   }
-  if (dead)
-    for (; used < issued; ++used)
-      mbar_wait(smem_u32(bar + used % S::STAGES), (used / S::STAGES) & 1u, a.err, nullptr, a.wait_ns);
   // ---- ranges shared by warps: each is a run of parts, one per warp, the first of which may have
   // begun before this CTA and the last of which may go on behind it
   __syncthreads();
-  int run0 = -1;  // index of the run's first part
+  int st[2 * kSmallWarps];
+#pragma unroll
+  for (int i = 0; i < 2 * kSmallWarps; ++i) st[i] = parts[i].state;
+  int run0 = -1;  // the run's first part
 #pragma unroll 1
-  for (int i = 0; i <= 2 * kSmallWarps; ++i) {
-    const int state = i < 2 * kSmallWarps ? parts[i].state : kNoPart;
-    if (state != kNoPart && run0 < 0) run0 = i;
-    const bool closed = state == kEnds;
-    if (run0 < 0 || !(closed || i == 2 * kSmallWarps)) continue;
-    const Part head = parts[run0];
-    const int end = min(i + 1, 2 * kSmallWarps);
-    const bool begins = head.state == kBegins, done = begins && closed;
-    float* rec = done ? nullptr : part_record<HD>(ln, blockIdx.x, begins);
-#pragma unroll 1
-    for (int x4 = tid; x4 < head.tr.M * (HD / 4); x4 += kSmallWarps * 32) {
-      const int v = x4 / (HD / 4), e = (x4 - v * (HD / 4)) * 4;
-      float mx = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int w = run0; w < end; ++w)
-        if (parts[w].state != kNoPart) mx = fmaxf(mx, parts[w].data[S::ROWS * S::OROW + v]);
-      for (int w = run0; w < end; ++w) {
-        if (parts[w].state == kNoPart) continue;
-        const float* d = parts[w].data;
-        const float m = d[S::ROWS * S::OROW + v];
-        const float f = m == -INFINITY ? 0.f : ex2_approx(m - mx);
-        sum = fmaf(f, d[S::ROWS * (S::OROW + 1) + v], sum);
-        const float4 y = *reinterpret_cast<const float4*>(d + v * S::OROW + e);
-        x[0] = fmaf(f, y.x, x[0]); x[1] = fmaf(f, y.y, x[1]); x[2] = fmaf(f, y.z, x[2]); x[3] = fmaf(f, y.w, x[3]);
+  for (int w1 = 0; w1 < kSmallWarps; ++w1) {
+    // a run ends in a warp's first part (kEnds), or in the last warp
+    int s0 = kNoPart, s1 = kNoPart;
+#pragma unroll
+    for (int w = 0; w < kSmallWarps; ++w)
+      if (w == w1) {
+        s0 = st[2 * w];
+        s1 = st[2 * w + 1];
       }
-      if (done) {
-        const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
-        const int m = head.tr.m0 + v;
-        T* out = static_cast<T*>(a.out) + (long long)(head.tr.r0 + m / G) * a.out_stride + (head.g * G + m % G) * HD + e;
-        if constexpr (TERMS == 1)
-          *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
-        else
-          *reinterpret_cast<float4*>(out) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-      } else {
-        if (e == 0) {
-          rec[v] = mx;
-          rec[S::ROWS + v] = sum;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const int state = half == 0 ? s0 : s1;
+      if (state != kNoPart && run0 < 0) run0 = 2 * w1 + half;
+      const bool closed = state == kEnds;
+      if (run0 < 0 || !(closed || (half == 1 && w1 == kSmallWarps - 1))) continue;
+      const Part head = parts[run0];
+      const bool begins = head.state == kBegins, done = begins && closed;
+      const TileRows tr = lo.tile(ln, head.k);
+      float* rec = done ? nullptr : part_record<HD>(ln, blockIdx.x, begins);
+#pragma unroll 1
+      for (int x4 = tid; x4 < tr.M * (HD / 4); x4 += kSmallWarps * 32) {
+        const int v = x4 / (HD / 4), e = (x4 - v * (HD / 4)) * 4;
+        // at most one part of the run per warp, all of them loaded at once
+        float m[kSmallWarps], l[kSmallWarps];
+        const float* d[kSmallWarps];
+#pragma unroll
+        for (int w = 0; w < kSmallWarps; ++w) {
+          const int i = 2 * w == run0 - 1 ? run0 : 2 * w;
+          const int si = i == run0 ? head.state : st[2 * w];
+          m[w] = -INFINITY;
+          l[w] = 0.f;
+          d[w] = nullptr;
+          if (i >= run0 && w <= w1 && si != kNoPart) {
+            d[w] = parts[i].spilled ? spill + (size_t)w * S::PIECE
+                                    : reinterpret_cast<const float*>(sm + w * S::STAGES * S::STAGE);
+            m[w] = d[w][S::ROWS * S::OROW + v];
+            l[w] = d[w][S::ROWS * (S::OROW + 1) + v];
+          }
         }
-        *reinterpret_cast<float4*>(rec + 2 * S::ROWS + v * HD + e) = make_float4(x[0], x[1], x[2], x[3]);
+        float mx = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kSmallWarps; ++w) mx = fmaxf(mx, m[w]);
+#pragma unroll
+        for (int w = 0; w < kSmallWarps; ++w) {
+          if (m[w] == -INFINITY) continue;
+          const float f = ex2_approx(m[w] - mx);
+          sum = fmaf(f, l[w], sum);
+          const float4 y = *reinterpret_cast<const float4*>(d[w] + v * S::OROW + e);
+          x[0] = fmaf(f, y.x, x[0]); x[1] = fmaf(f, y.y, x[1]); x[2] = fmaf(f, y.z, x[2]); x[3] = fmaf(f, y.w, x[3]);
+        }
+        if (done) {
+          const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
+          const int m_ = tr.m0 + v, r = (int)((uint32_t)m_ / ln.group);
+          T* out = static_cast<T*>(a.out) + (tr.r0 + r) * a.out_stride + (head.g * G + m_ - r * G) * HD + e;
+          if constexpr (TERMS == 1)
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+          else
+            *reinterpret_cast<float4*>(out) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+        } else {
+          if (e == 0) {
+            rec[v] = mx;
+            rec[S::ROWS + v] = sum;
+          }
+          *reinterpret_cast<float4*>(rec + 2 * S::ROWS + v * HD + e) = make_float4(x[0], x[1], x[2], x[3]);
+        }
       }
+      run0 = -1;
     }
-    run0 = -1;
   }
 }
 
@@ -774,12 +901,10 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp & (split - 1);
-  const long long task = (long long)blockIdx.x * (8 / split) + warp / split;
-  const long long per_tile = (long long)a.n_kv * ln.tile_rows;
-  const int k = (int)min(task / per_tile, (long long)ln.n_tiles);
-  const int rest = (int)(task - task / per_tile * per_tile);
-  const int g = rest / ln.tile_rows, v = rest - (rest / ln.tile_rows) * ln.tile_rows;
-  const int G = a.n_q / a.n_kv;
+  const uint32_t task = blockIdx.x * (8 / split) + warp / split;
+  const uint32_t vec = task >> ln.rows_log2;  // (tile, head)
+  const int v = (int)(task - (vec << ln.rows_log2));
+  const int k = min((int)(vec / ln.heads), ln.n_tiles), g = (int)vec - k * a.n_kv;
   float mx = -INFINITY, sum = 0.f, x[VPL];
 #pragma unroll
   for (int e = 0; e < VPL; ++e) x[e] = 0.f;
@@ -788,11 +913,11 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
   if (k < ln.n_tiles) {
     const int p0 = __ldcg(ln.prefix + k), p1 = __ldcg(ln.prefix + k + 1);
     const uint32_t tot = (uint32_t)__ldcg(ln.prefix + ln.n_tiles) * a.n_kv;
+    tr = tile_rows(a, ln, ln.tile0 + k);
     if (p1 > p0) {
-      const Cuts cuts(tot, line_ctas(tot, grid, ln.min_units));
+      const Cuts cuts(ln, grid, tot);
       const uint32_t first = (uint32_t)p0 * a.n_kv + (uint32_t)g * (p1 - p0);
       const int c0 = (int)cuts.piece(first), c1 = (int)cuts.piece(first + (p1 - p0) - 1);
-      tr = tile_rows(a, ln, ln.tile0 + k);
       live = c1 > c0 && v < tr.M;
       if (live) {
         for (int c = c0 + sub; c <= c1; c += CB * split) {
@@ -853,8 +978,8 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
   }
   if (!live) return;
   const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
-  const int m = tr.m0 + v;
-  T* out = static_cast<T*>(a.out) + (long long)(tr.r0 + m / G) * a.out_stride + (g * G + m % G) * HD + lane * VPL;
+  const int m = tr.m0 + v, r = (int)((uint32_t)m / ln.group);
+  T* out = static_cast<T*>(a.out) + (tr.r0 + r) * a.out_stride + (g * ln.G + m - r * ln.G) * HD + lane * VPL;
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int e = 0; e < VPL; ++e) out[e] = x[e] * inv;
@@ -896,20 +1021,25 @@ cudaError_t launch_merge(const PackedAttnArgs& a, const Line& ln, int grid, cuda
 
 // The launch's line for tiles of `tile_rows` vectors and units of `unit_pages`, and how many of its tiles one
 // launch takes (their units, counted in 32 bits, and kPlanTiles bound it).
-Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_units, int* tiles_per_launch) {
+Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_log2, int* tiles_per_launch) {
   const int G = a.n_q / a.n_kv;
   const long long vectors = (long long)a.max_rows * G;
   Line ln{};
   ln.tile_rows = tile_rows;
+  while ((1 << ln.rows_log2) < tile_rows) ++ln.rows_log2;
   ln.unit_pages = unit_pages;
-  ln.tps = (int)((vectors + tile_rows - 1) / tile_rows);
+  ln.n_tps = (int)((vectors + tile_rows - 1) / tile_rows);
+  ln.tps = make_div(ln.n_tps);
+  ln.group = make_div(G);
+  ln.heads = make_div(a.n_kv);
+  ln.G = G;
   ln.whole = a.max_pages <= kWholePages;
-  ln.min_units = min_units;
+  ln.min_log2 = min_log2;
   const int rows = std::min(a.max_rows, tile_rows / G + 2);
   ln.lanes = 1;
   while (ln.lanes < 32 && ln.lanes * 4 < rows) ln.lanes *= 2;
   const long long units = (long long)a.n_kv * ((a.max_pages + unit_pages - 1) / unit_pages);  // of a tile, at most
-  *tiles_per_launch = (int)std::min<long long>(kPlanTiles, std::max(1LL, (1LL << 31) / units));
+  *tiles_per_launch = (int)std::min<long long>(kPlanTiles, std::max(1LL, ((1LL << 31) - 1) / units));
   return ln;
 }
 
@@ -917,21 +1047,22 @@ template <typename T, int HD, int NQ>
 cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Small<T, HD, NQ>;
   int per_launch = 0;
-  Line ln = make_line(a, C::ROWS, 2, kSmallWarps, &per_launch);
+  Line ln = make_line(a, C::ROWS, 2, 3, &per_launch);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ln.prefix = reinterpret_cast<int*>(ws);
   ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
   ln.spill = ln.part + (size_t)sms * C::CTAS * 2 * C::ROWS * (HD + 2);
   cudaError_t e = allow_smem<attend_small_kernel<T, HD, NQ>>(C::smem(kPlanTiles));
   if (e != cudaSuccess) return e;
-  const long long tiles = (long long)a.B * ln.tps;
+  const long long tiles = (long long)a.B * ln.n_tps;
   for (long long t0 = 0; t0 < tiles; t0 += per_launch) {
     ln.tile0 = (int)t0;
     ln.n_tiles = (int)std::min<long long>(per_launch, tiles - t0);
     // no more CTAs than the tables' positions could keep busy
     const long long ranges = (long long)ln.n_tiles * a.n_kv;
     const long long units = ranges * ((a.max_pages + ln.unit_pages - 1) / ln.unit_pages);
-    const int grid = (int)std::min<long long>((long long)sms * C::CTAS, std::max(1LL, units / ln.min_units));
+    const int grid = (int)std::min<long long>((long long)sms * C::CTAS, std::max(1LL, units >> ln.min_log2));
+    ln.grid = make_div(grid);
     e = launch_pdl(attend_small_kernel<T, HD, NQ>, dim3(grid), dim3(kSmallWarps * 32), C::smem(ln.n_tiles), s, a, ln);
     if (e != cudaSuccess) return e;
     if (!ln.whole && grid > 1 && (e = launch_merge<T, HD>(a, ln, grid, s)) != cudaSuccess) return e;
