@@ -84,26 +84,24 @@ struct TileRows {
   int r0, m0, M;  // first row of the sequence, first vector of the tile, vectors of the tile (0: none)
 };
 
-PE_DEV TileRows tile_rows(const PackedAttnArgs& a, const Line& ln, int tile) {
+// The rows of tile `tile`, and whether its sequence's are out of bounds (then none).  Here and in
+// row_limit errors are flagged, not reported: a report would hold the next loads back.
+PE_DEV TileRows tile_rows(const PackedAttnArgs& a, const Line& ln, int tile, bool& bad) {
   const int b = (int)((uint32_t)tile / ln.tps), t = tile - b * ln.n_tps;
   const int r0 = __ldcg(a.row_start + b);
-  const int r1 = a.row_len != nullptr ? r0 + __ldcg(a.row_len + b) : __ldcg(a.row_start + b + 1);
-  if (r0 < 0 || r1 < r0 || r1 > a.n_rows || r1 - r0 > a.max_rows) {
-    if (r1 != r0) set_err(a.err, PE_DEV_BAD_ROW);
-    return TileRows{0, 0, 0};
-  }
+  const int next = __ldcg(a.row_len != nullptr ? a.row_len + b : a.row_start + b + 1);
+  const int r1 = a.row_len != nullptr ? r0 + next : next;
+  const bool out = r0 < 0 || r1 < r0 || r1 > a.n_rows || r1 - r0 > a.max_rows;
+  bad |= out && r1 != r0;
   const int m0 = t * ln.tile_rows;
-  return TileRows{r0, m0, max(0, min((r1 - r0) * ln.G - m0, ln.tile_rows))};
+  return TileRows{out ? 0 : r0, m0, out ? 0 : max(0, min((r1 - r0) * ln.G - m0, ln.tile_rows))};
 }
 
 // A row's last visible position: -1 when it sees nothing or its position is out of range.
-PE_DEV int row_limit(const PackedAttnArgs& a, int row) {
-  const int p = __ldcg(a.positions + row);
-  if (p < -1 || p / kPackedPage >= a.max_pages) {
-    set_err(a.err, PE_DEV_BAD_POSITION);
-    return -1;
-  }
-  return p;
+PE_DEV int row_limit(const PackedAttnArgs& a, int p, bool& bad) {
+  const bool out = p < -1 || p / kPackedPage >= a.max_pages;
+  bad |= out;
+  return out ? -1 : p;
 }
 
 // The line in shared memory, each array of n_tiles (+ 1) entries.
@@ -129,26 +127,30 @@ PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, i
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
   const int n = ln.n_tiles;
   constexpr int W = 4;  // tiles per lane
+  bool bad_rows = false, bad_pos = false;
   if (n <= 32 * W && ln.lanes == 1) {
     // few tiles of few rows: every warp works the whole line out (the same values go to the same places), so
-    // that none waits for another
+    // that none waits for another.  Two round trips: the rows of every tile, then their positions.
     TileRows t[W];
-    int mx[W];
+    int pos[W][4], mx[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       const int k = lane + 32 * i;
-      t[i] = k < n ? tile_rows(a, ln, ln.tile0 + k) : TileRows{0, 0, 0};
+      t[i] = TileRows{0, 0, 0};
+      if (k < n) t[i] = tile_rows(a, ln, ln.tile0 + k, bad_rows);
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const int ra = t[i].r0 + (int)((uint32_t)t[i].m0 / ln.group);
+      const int rb = t[i].r0 + (int)((uint32_t)(t[i].m0 + t[i].M - 1) / ln.group);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) pos[i][r] = t[i].M > 0 && ra + r <= rb ? __ldcg(a.positions + ra + r) : -1;
     }
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       mx[i] = -1;
-      if (t[i].M > 0) {
-        const int ra = t[i].r0 + (int)((uint32_t)t[i].m0 / ln.group);
-        const int rb = t[i].r0 + (int)((uint32_t)(t[i].m0 + t[i].M - 1) / ln.group);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (ra + r <= rb) mx[i] = max(mx[i], row_limit(a, ra + r));
-      }
+      for (int r = 0; r < 4; ++r) mx[i] = max(mx[i], row_limit(a, pos[i][r], bad_pos));
     }
     int before = 0;
 #pragma unroll
@@ -172,6 +174,8 @@ PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, i
     }
     if (lane == 0) lo.prefix[0] = 0;
     __syncwarp();
+    if (bad_rows) set_err(a.err, PE_DEV_BAD_ROW);
+    if (bad_pos) set_err(a.err, PE_DEV_BAD_POSITION);
     return;
   }
   const int per = ln.lanes, sub = tid & (per - 1);
@@ -180,12 +184,17 @@ PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, i
     int mx = -1;
     TileRows t{0, 0, 0};
     if (k < n) {
-      t = tile_rows(a, ln, ln.tile0 + k);
+      t = tile_rows(a, ln, ln.tile0 + k, bad_rows);
       if (t.M > 0) {
         const int ra = t.r0 + (int)((uint32_t)t.m0 / ln.group);
         const int rb = t.r0 + (int)((uint32_t)(t.m0 + t.M - 1) / ln.group);
-#pragma unroll 4
-        for (int r = ra + sub; r <= rb; r += per) mx = max(mx, row_limit(a, r));
+        for (int r = ra + sub; r <= rb; r += 4 * per) {
+          int pos[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pos[i] = r + i * per <= rb ? __ldcg(a.positions + r + i * per) : -1;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx = max(mx, row_limit(a, pos[i], bad_pos));
+        }
       }
     }
     for (int o = per >> 1; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
@@ -196,6 +205,8 @@ PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, i
       lo.rows[k] = t.M;
     }
   }
+  if (bad_rows) set_err(a.err, PE_DEV_BAD_ROW);
+  if (bad_pos) set_err(a.err, PE_DEV_BAD_POSITION);
   __syncthreads();
   // inclusive scan of prefix[1..n]: a run of consecutive tiles per thread, then over threads
   const int run = (n + nt - 1) / nt, k0 = tid * run, k1 = min(n, k0 + run);
@@ -340,6 +351,15 @@ PE_DEV float* part_record(const Line& ln, int cta, bool from_start) {
 
 constexpr int kSmallWarps = 8;
 
+// A warp's part of a range that it shares with its neighbours: [ROWS][OROW] outputs, [ROWS] maxima, [ROWS]
+// sums, in its ring or (a part that began before the warp's piece, when more ranges follow) in the
+// workspace.
+enum : int { kFirst = 1, kFirstEnds = 2, kFirstSpilled = 4, kSecond = 8 };
+struct Parts {
+  int state;             // kFirst: a part of a range that began before the warp; kSecond: of one that begins in it
+  int k[2], g[2], pad[3];  // their tiles and heads
+};
+
 template <typename T, int HD, int NQ>
 struct Small {
   static constexpr int TERMS = sizeof(T) == 4 ? 3 : 1;
@@ -352,16 +372,8 @@ struct Small {
   static constexpr int KTAB = HD * 4, VTAB = HD * 2, TAB = 2 * (KTAB + VTAB);  // scale tables of a warp (two pages)
   static constexpr int PIECE = ROWS * (OROW + 2);  // floats of a warp's part of a shared range
   static_assert(PIECE * 4 <= STAGES * STAGE, "it fits the warp's drained ring");
-  static constexpr int FIXED = RING + kSmallWarps * TAB + 16 * 4 + 2 * kSmallWarps * 16;
+  static constexpr int FIXED = RING + kSmallWarps * TAB + 16 * 4 + kSmallWarps * (int)sizeof(Parts);
   static size_t smem(int n_tiles) { return 128 + FIXED + Layout::kBytesPerTile * (size_t)n_tiles + 4; }
-};
-
-// A warp's part of a range that it shares with its neighbours: [ROWS][OROW] outputs, [ROWS] maxima, [ROWS]
-// sums, in its ring or (a part that began before the warp's piece, when more ranges follow) in the
-// workspace.
-enum PartState : int { kNoPart, kBegins, kGoesOn, kEnds };
-struct Part {
-  int state, k, g, spilled;
 };
 
 PE_DEV void copy16(uint32_t dst, const uint8_t* src) {
@@ -436,15 +448,15 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 127) & ~uintptr_t(127));
   uint8_t* tabs = sm + S::RING;
   int* scratch = reinterpret_cast<int*>(tabs + kSmallWarps * S::TAB);  // [16]
-  Part* parts = reinterpret_cast<Part*>(scratch + 16);                 // [warps][2]
-  const Layout lo(parts + 2 * kSmallWarps, ln.n_tiles);
+  Parts* parts = reinterpret_cast<Parts*>(scratch + 16);               // [warps]
+  const Layout lo(parts + kSmallWarps, ln.n_tiles);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, t = lane & 3;
   uint8_t* my_ring = sm + warp * S::STAGES * S::STAGE;
   uint8_t* my_tab = tabs + warp * S::TAB;
   const int G = ln.G;
   const float sl2 = a.scale * 1.4426950408889634f * kPackedUnit;
   float* spill = ln.spill + (size_t)blockIdx.x * kSmallWarps * S::PIECE;
-  if (lane < 2) parts[2 * warp + lane].state = kNoPart;
+  if (lane == 0) parts[warp].state = 0;
   pdl_wait();
   pdl_trigger();
   lay_out(a, ln, lo, scratch);
@@ -557,12 +569,15 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       }
     }
     int lim[NQ][2], min_lim = INT_MAX;
+    bool bad_pos = false;  // reported by lay_out
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int v = n * 8 + 2 * t + e;
-        lim[n][e] = v < tr.M ? row_limit(a, tr.r0 + (int)((uint32_t)(tr.m0 + v) / ln.group)) : INT_MAX;
+        lim[n][e] = INT_MAX;
+        if (v < tr.M)
+          lim[n][e] = row_limit(a, __ldcg(a.positions + tr.r0 + (int)((uint32_t)(tr.m0 + v) / ln.group)), bad_pos);
         min_lim = min(min_lim, lim[n][e]);
       }
     min_lim = min(min_lim, __shfl_xor_sync(0xFFFFFFFFu, min_lim, 1));
@@ -799,9 +814,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
             dst[v * S::OROW + 16 * j + 8 + gr] = o[j][n][c + 2];
           }
         }
-      if (lane == 0)
-        parts[2 * warp + (cs.from_start ? 1 : 0)] =
-            Part{cs.from_start ? kBegins : cs.to_end ? kEnds : kGoesOn, cs.k, cs.g, ends ? 0 : 1};
+      if (lane == 0) {
+        Parts& p = parts[warp];
+        const int second = cs.from_start ? 1 : 0;
+        p.state |= second ? kSecond : kFirst | (cs.to_end ? kFirstEnds : 0) | (ends ? 0 : kFirstSpilled);
+        p.k[second] = cs.k;
+        p.g[second] = cs.g;
+      }
     }
     if (ends) break;
     cs = walk.after(cs, u1);
@@ -809,79 +828,73 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   // ---- ranges shared by warps: each is a run of parts, one per warp, the first of which may have
   // begun before this CTA and the last of which may go on behind it
   __syncthreads();
-  int st[2 * kSmallWarps];
+  uint32_t firsts = 0, lasts = 0, spilled = 0, seconds = 0;  // bit w: warp w
 #pragma unroll
-  for (int i = 0; i < 2 * kSmallWarps; ++i) st[i] = parts[i].state;
-  int run0 = -1;  // the run's first part
+  for (int w = 0; w < kSmallWarps; ++w) {
+    const int st = parts[w].state;
+    firsts |= (st & kFirst) ? 1u << w : 0;
+    lasts |= (st & kFirstEnds) ? 1u << w : 0;
+    spilled |= (st & kFirstSpilled) ? 1u << w : 0;
+    seconds |= (st & kSecond) ? 1u << w : 0;
+  }
+  // the first run may be a range that began before the CTA: it has first parts alone
+  bool begins = firsts == 0 || (seconds != 0 && __ffs(seconds) < __ffs(firsts));
+  uint32_t heads = seconds;
 #pragma unroll 1
-  for (int w1 = 0; w1 < kSmallWarps; ++w1) {
-    // a run ends in a warp's first part (kEnds), or in the last warp
-    int s0 = kNoPart, s1 = kNoPart;
+  while (!begins || heads != 0) {
+    const int w0 = (begins ? __ffs(heads) : __ffs(firsts)) - 1;
+    const uint32_t later = ~0u << (begins ? w0 + 1 : w0);  // warps whose first parts can be of this run
+    const bool closed = (lasts & later) != 0;
+    const int w1 = closed ? __ffs(lasts & later) - 1 : kSmallWarps - 1;
+    const uint32_t in = firsts & later & ((2u << w1) - 1);
+    const bool done = begins && closed;
+    const TileRows tr = lo.tile(ln, parts[w0].k[begins ? 1 : 0]);
+    const int g = parts[w0].g[begins ? 1 : 0];
+    float* rec = done ? nullptr : part_record<HD>(ln, blockIdx.x, begins);
+#pragma unroll 1
+    for (int x4 = tid; x4 < tr.M * (HD / 4); x4 += kSmallWarps * 32) {
+      const int v = x4 / (HD / 4), e = (x4 - v * (HD / 4)) * 4;
+      // at most one part per warp, all of them loaded at once
+      float m[kSmallWarps], l[kSmallWarps];
+      float4 y[kSmallWarps];
 #pragma unroll
-    for (int w = 0; w < kSmallWarps; ++w)
-      if (w == w1) {
-        s0 = st[2 * w];
-        s1 = st[2 * w + 1];
+      for (int w = 0; w < kSmallWarps; ++w) {
+        const bool second = begins && w == w0, has = second || (in >> w & 1);
+        const float* d = !second && (spilled >> w & 1) ? spill + (size_t)w * S::PIECE
+                                                       : reinterpret_cast<const float*>(sm + w * S::STAGES * S::STAGE);
+        m[w] = has ? d[S::ROWS * S::OROW + v] : -INFINITY;
+        l[w] = has ? d[S::ROWS * (S::OROW + 1) + v] : 0.f;
+        y[w] = has ? *reinterpret_cast<const float4*>(d + v * S::OROW + e) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      const int state = half == 0 ? s0 : s1;
-      if (state != kNoPart && run0 < 0) run0 = 2 * w1 + half;
-      const bool closed = state == kEnds;
-      if (run0 < 0 || !(closed || (half == 1 && w1 == kSmallWarps - 1))) continue;
-      const Part head = parts[run0];
-      const bool begins = head.state == kBegins, done = begins && closed;
-      const TileRows tr = lo.tile(ln, head.k);
-      float* rec = done ? nullptr : part_record<HD>(ln, blockIdx.x, begins);
-#pragma unroll 1
-      for (int x4 = tid; x4 < tr.M * (HD / 4); x4 += kSmallWarps * 32) {
-        const int v = x4 / (HD / 4), e = (x4 - v * (HD / 4)) * 4;
-        // at most one part of the run per warp, all of them loaded at once
-        float m[kSmallWarps], l[kSmallWarps];
-        const float* d[kSmallWarps];
+      float mx = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kSmallWarps; ++w) {
-          const int i = 2 * w == run0 - 1 ? run0 : 2 * w;
-          const int si = i == run0 ? head.state : st[2 * w];
-          m[w] = -INFINITY;
-          l[w] = 0.f;
-          d[w] = nullptr;
-          if (i >= run0 && w <= w1 && si != kNoPart) {
-            d[w] = parts[i].spilled ? spill + (size_t)w * S::PIECE
-                                    : reinterpret_cast<const float*>(sm + w * S::STAGES * S::STAGE);
-            m[w] = d[w][S::ROWS * S::OROW + v];
-            l[w] = d[w][S::ROWS * (S::OROW + 1) + v];
-          }
-        }
-        float mx = -INFINITY, sum = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int w = 0; w < kSmallWarps; ++w) mx = fmaxf(mx, m[w]);
+      const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-        for (int w = 0; w < kSmallWarps; ++w) mx = fmaxf(mx, m[w]);
-#pragma unroll
-        for (int w = 0; w < kSmallWarps; ++w) {
-          if (m[w] == -INFINITY) continue;
-          const float f = ex2_approx(m[w] - mx);
-          sum = fmaf(f, l[w], sum);
-          const float4 y = *reinterpret_cast<const float4*>(d[w] + v * S::OROW + e);
-          x[0] = fmaf(f, y.x, x[0]); x[1] = fmaf(f, y.y, x[1]); x[2] = fmaf(f, y.z, x[2]); x[3] = fmaf(f, y.w, x[3]);
-        }
-        if (done) {
-          const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
-          const int m_ = tr.m0 + v, r = (int)((uint32_t)m_ / ln.group);
-          T* out = static_cast<T*>(a.out) + (tr.r0 + r) * a.out_stride + (head.g * G + m_ - r * G) * HD + e;
-          if constexpr (TERMS == 1)
-            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
-          else
-            *reinterpret_cast<float4*>(out) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-        } else {
-          if (e == 0) {
-            rec[v] = mx;
-            rec[S::ROWS + v] = sum;
-          }
-          *reinterpret_cast<float4*>(rec + 2 * S::ROWS + v * HD + e) = make_float4(x[0], x[1], x[2], x[3]);
-        }
+      for (int w = 0; w < kSmallWarps; ++w) {
+        const float f = ex2_approx(m[w] - ref);
+        sum = fmaf(f, l[w], sum);
+        x[0] = fmaf(f, y[w].x, x[0]); x[1] = fmaf(f, y[w].y, x[1]);
+        x[2] = fmaf(f, y[w].z, x[2]); x[3] = fmaf(f, y[w].w, x[3]);
       }
-      run0 = -1;
+      if (done) {
+        const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
+        const int mv = tr.m0 + v, r = (int)((uint32_t)mv / ln.group);
+        T* out = static_cast<T*>(a.out) + (tr.r0 + r) * a.out_stride + (g * G + mv - r * G) * HD + e;
+        if constexpr (TERMS == 1)
+          *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+        else
+          *reinterpret_cast<float4*>(out) = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+      } else {
+        if (e == 0) {
+          rec[v] = mx;
+          rec[S::ROWS + v] = sum;
+        }
+        *reinterpret_cast<float4*>(rec + 2 * S::ROWS + v * HD + e) = make_float4(x[0], x[1], x[2], x[3]);
+      }
     }
+    if (begins) heads &= heads - 1;
+    begins = true;
   }
 }
 
@@ -913,7 +926,8 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
   if (k < ln.n_tiles) {
     const int p0 = __ldcg(ln.prefix + k), p1 = __ldcg(ln.prefix + k + 1);
     const uint32_t tot = (uint32_t)__ldcg(ln.prefix + ln.n_tiles) * a.n_kv;
-    tr = tile_rows(a, ln, ln.tile0 + k);
+    bool bad = false;  // reported by the kernel before
+    tr = tile_rows(a, ln, ln.tile0 + k, bad);
     if (p1 > p0) {
       const Cuts cuts(ln, grid, tot);
       const uint32_t first = (uint32_t)p0 * a.n_kv + (uint32_t)g * (p1 - p0);
