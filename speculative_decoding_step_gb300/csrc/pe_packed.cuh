@@ -48,10 +48,18 @@ struct PackedLayout {
 PE_DEV float packed_scale(uint32_t c) { return __uint_as_float((c << 20) + (108u << 23)); }
 
 // Two of a word's eight nibbles as bf16 pairs 128 + nibble: nibble I in the lower half, I + 4 above.
-template <int I>
-PE_DEV uint32_t packed_pair(uint32_t w) {
-  return ((I == 0 ? w : w >> (4 * I)) & 0x000F000Fu) | 0x43004300u;
-}
+// (A mask and an exponent are two constants, of which one instruction takes one: the compiler makes two
+// instructions of it unless the other is in a register that it does not look into.)
+struct PairBits {
+  uint32_t exponent;
+  PE_DEV PairBits() { asm("mov.b32 %0, 0x43004300;" : "=r"(exponent)); }
+  template <int I>
+  PE_DEV uint32_t pair(uint32_t w) const {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(d) : "r"(I == 0 ? w : w >> (4 * I)), "r"(exponent));
+    return d;
+  }
+};
 
 // Two scale bytes (the first or the second byte of either half of x) as bf16 pairs s 2^-12.
 PE_DEV uint32_t packed_scale_lo(uint32_t x) { return ((x << 4) & 0x0FF00FF0u) | 0x30003000u; }

@@ -455,6 +455,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   uint8_t* my_tab = tabs + warp * S::TAB;
   const int G = ln.G;
   const float sl2 = a.scale * 1.4426950408889634f * kPackedUnit;
+  const PairBits bits;
   float* spill = ln.spill + (size_t)blockIdx.x * kSmallWarps * S::PIECE;
   if (lane == 0) parts[warp].state = 0;
   pdl_wait();
@@ -481,22 +482,26 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   Segment ps{}, cs{};
   bool p_done = u0 == u1;
   if (!p_done) ps = cs = walk.at(walk.tile_of(u0), u0, u1);
-  int p_i = 0;   // the next pair of the segment
-  int ids = -1;  // page ids of 16 pairs, one per lane
-  uint32_t issued = 0, used = 0;
+  int p_page = ps.page0;  // the next pair of the segment
+  int ids = -1;           // page ids of the 16 pairs from p_page - p_id on, one per lane
+  int p_id = 0;
+  const uint32_t step = (uint32_t)a.n_kv * L::kRecord;
+  const uint8_t* head = a.pool + (size_t)ps.g * L::kRecord + lane * 16;  // of the segment's head, in page 0
+  uint32_t issued = 0, used = 0, stage_in = smem_u32(my_ring) + lane * 16;
+  const uint32_t ring_end = stage_in + S::RING / kSmallWarps;
   auto issue = [&]() {
-    int page = ps.page0 + 2 * p_i;
-    while (page >= ps.page1) {
+    while (p_page >= ps.page1) {
       if (ps.next >= u1) {
         p_done = true;
         return;
       }
       ps = walk.after(ps, u1);
-      p_i = 0;
-      page = ps.page0;
+      p_page = ps.page0;
+      p_id = 0;
+      head = a.pool + (size_t)ps.g * L::kRecord + lane * 16;
     }
-    if ((p_i & 15) == 0) {
-      const int x = page + lane;
+    if (p_id == 0) {
+      const int x = p_page + lane;
       ids = -1;
       if (x < ps.page1) {
         ids = __ldcg(a.block_table + (size_t)((uint32_t)(ln.tile0 + ps.k) / ln.tps) * a.max_pages + x);
@@ -506,31 +511,33 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
         }
       }
     }
-    const int id0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (p_i & 15)), id1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (p_i & 15) + 1);
-    uint8_t* dst = my_ring + (issued % S::STAGES) * S::STAGE;
-    const size_t step = (size_t)a.n_kv * L::kRecord;
-    const uint8_t* src0 = a.pool + (size_t)ps.g * L::kRecord + (size_t)max(id0, 0) * step + lane * 16;
-    const uint8_t* src1 = a.pool + (size_t)ps.g * L::kRecord + (size_t)max(id1, 0) * step + lane * 16 - L::kRecord;
-    const uint32_t d = smem_u32(dst) + lane * 16;
+    const int id0 = __shfl_sync(0xFFFFFFFFu, ids, p_id), id1 = __shfl_sync(0xFFFFFFFFu, ids, p_id + 1);
+    if ((id0 | id1) >= 0) {
+      const uint8_t* src0 = head + (uint64_t)(uint32_t)id0 * step;
+      const uint8_t* src1 = head + (uint64_t)(uint32_t)id1 * step - L::kRecord;
 #pragma unroll
-    for (int i = 0; i < (S::STAGE + 511) / 512; ++i) {
-      const int at = i * 512 + lane * 16;  // byte of the two records
-      const bool first = i * 512 + 511 < L::kRecord || at < L::kRecord;
-      if (i * 512 + 511 < S::STAGE || at < S::STAGE) copy16(d + i * 512, (first ? src0 : src1) + i * 512);
-    }
-    if (id0 < 0 || (id1 < 0 && page + 1 < ps.page1)) {
-      // pages outside the pool stand for zeros: every nibble 8.  (Page 0 was copied in their place.)
-      copy_commit();
-      copy_wait<0>();
-      __syncwarp();
+      for (int i = 0; i < (S::STAGE + 511) / 512; ++i) {
+        const int at = i * 512 + lane * 16;  // byte of the two records
+        const bool first = i * 512 + 511 < L::kRecord || (i * 512 < L::kRecord && at < L::kRecord);
+        if (i * 512 + 511 < S::STAGE || at < S::STAGE) copy16(stage_in + i * 512, (first ? src0 : src1) + i * 512);
+      }
+    } else {
+      // a page outside the pool stands for zeros, every nibble 8; so may the page behind the range
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h)
-        if ((h == 0 ? id0 : id1) < 0)
-          for (int i = lane * 16; i < L::kRecord; i += 512)
-            *reinterpret_cast<uint4*>(dst + h * L::kRecord + i) = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+      for (int h = 0; h < 2; ++h) {
+        const int id = h == 0 ? id0 : id1;
+        for (int i = 0; i + lane * 16 < L::kRecord; i += 512) {
+          const uint32_t d = stage_in + h * L::kRecord + i;
+          if (id >= 0) copy16(d, head + (uint64_t)(uint32_t)id * step + i);
+          else asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(d), "r"(0x88888888u) : "memory");
+        }
+      }
     }
-    ++p_i;
+    stage_in = stage_in + S::STAGE == ring_end ? ring_end - S::RING / kSmallWarps : stage_in + S::STAGE;
+    p_page += 2;
+    p_id = (p_id + 2) & 31;
   };
+  const uint8_t* recs = my_ring;  // the stage to be used next
 
   // rows 0..7 of a product stand for positions 0, 4, 1, 5, 2, 6, 3, 7 and rows 8..15 for 8 more, so that
   // the transposed P pairs positions t and t + 4
@@ -601,8 +608,6 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       }
       copy_wait<S::STAGES - 1>();
       __syncwarp();
-      const int s = used % S::STAGES;
-      const uint8_t* recs = my_ring + s * S::STAGE;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         scale_tables<HD>(recs + h * L::kRecord, my_tab + h * (S::KTAB + S::VTAB), my_tab + h * (S::KTAB + S::VTAB) + S::KTAB, lane);
@@ -637,10 +642,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
           const uint32_t w0 = kw[0][j / 2], w1 = kw[1][j / 2], s0 = ks[0][j], s1 = ks[1][j];
           const uint32_t z0 = bf16x2_mul(s0, kMinus136), z1 = bf16x2_mul(s1, kMinus136);
           const bool odd = j & 1;
-          const uint32_t af[4] = {bf16x2_fma(odd ? packed_pair<2>(w0) : packed_pair<0>(w0), s0, z0),
-                                  bf16x2_fma(odd ? packed_pair<2>(w1) : packed_pair<0>(w1), s1, z1),
-                                  bf16x2_fma(odd ? packed_pair<3>(w0) : packed_pair<1>(w0), s0, z0),
-                                  bf16x2_fma(odd ? packed_pair<3>(w1) : packed_pair<1>(w1), s1, z1)};
+          const uint32_t af[4] = {bf16x2_fma(odd ? bits.pair<2>(w0) : bits.pair<0>(w0), s0, z0),
+                                  bf16x2_fma(odd ? bits.pair<2>(w1) : bits.pair<0>(w1), s1, z1),
+                                  bf16x2_fma(odd ? bits.pair<3>(w0) : bits.pair<1>(w0), s0, z0),
+                                  bf16x2_fma(odd ? bits.pair<3>(w1) : bits.pair<1>(w1), s1, z1)};
 #pragma unroll
           for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -695,8 +700,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            // masked scores are -inf; a vector that has seen nothing takes no offset
-            p[e] = ex2_approx(fmaf(sc[h][n][e], sl2, nm[n][e & 1] == INFINITY ? 0.f : nm[n][e & 1]));
+            p[e] = ex2_approx(fmaf(sc[h][n][e], sl2, nm[n][e & 1]));
+            if (edge && sc[h][n][e] == -INFINITY) p[e] = 0.f;  // no number where a vector has seen nothing yet
             l[n][e & 1] += p[e];
           }
 #pragma unroll
@@ -736,10 +741,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
           const uint32_t sa = vs[0][j], sb = vs[1][j];
           const uint32_t za = bf16x2_mul(sa, kMinus136), zb = bf16x2_mul(sb, kMinus136);
           const bool odd = j & 1;
-          const uint32_t af[4] = {bf16x2_fma(odd ? packed_pair<2>(wa) : packed_pair<0>(wa), sa, za),
-                                  bf16x2_fma(odd ? packed_pair<3>(wa) : packed_pair<1>(wa), sa, za),
-                                  bf16x2_fma(odd ? packed_pair<2>(wb) : packed_pair<0>(wb), sb, zb),
-                                  bf16x2_fma(odd ? packed_pair<3>(wb) : packed_pair<1>(wb), sb, zb)};
+          const uint32_t af[4] = {bf16x2_fma(odd ? bits.pair<2>(wa) : bits.pair<0>(wa), sa, za),
+                                  bf16x2_fma(odd ? bits.pair<3>(wa) : bits.pair<1>(wa), sa, za),
+                                  bf16x2_fma(odd ? bits.pair<2>(wb) : bits.pair<0>(wb), sb, zb),
+                                  bf16x2_fma(odd ? bits.pair<3>(wb) : bits.pair<1>(wb), sb, zb)};
 #pragma unroll
           for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -748,6 +753,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       }
       __syncwarp();  // the stage and the tables are read
       ++used;
+      recs = recs + S::STAGE == my_ring + S::RING / kSmallWarps ? my_ring : recs + S::STAGE;
     }
     // ---- the segment's end
 #pragma unroll
