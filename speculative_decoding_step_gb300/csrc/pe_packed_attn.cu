@@ -38,6 +38,9 @@ PE_DEV uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
+// A wait's outcome, made the same for the whole warp.
+PE_DEV bool warp_ok(bool ok) { return __all_sync(0xFFFFFFFFu, ok); }
+
 // n / d for n < 2^31 by a multiplication: mul = ceil(2^shift / d), shift = 31 + ceil(log2 d), is at most
 // d 2^-shift above 1/d, which is less than 1/(n d).  (A division by a value that the compiler does not know
 // is a chain of about 150 cycles, several of which stood before the first load.)
@@ -904,6 +907,555 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   }
 }
 
+// ----------------------------------------------------------------------------- many query vectors: tcgen05
+//
+// A tile of up to 128 query vectors (bf16) against blocks of 64 positions: S = Q K^T and O += P V on
+// the 5th-generation tensor core, S and O in tensor memory, P written over S as bf16.  One unpacked
+// block serves all 128 vectors.  Roles of a CTA (two CTAs per SM):
+//   warps 0..3  unpack: each takes one page of a block, a row (position) per two lanes, from registers
+//               that were loaded two blocks ahead, into the K and V rings (128-byte swizzle).
+//               Entries stay in the order of the cache's words: K's is a permutation of the
+//               contraction, given to Q as well; V's one of O's columns, undone on output.
+//   warps 4..7  softmax and output: one thread per query vector (TMEM lane).
+//   warp 8      issues the MMAs: S of a block as soon as its keys are there, up to NB - 1 blocks ahead
+//               of the softmax; PV as soon as P and the values are.
+// A vector's reference maximum only moves when a block exceeds it by 2^8; then O is rescaled in TMEM.
+//
+// Bound (head_dim 64): per block of 64 positions about 1300 warp instructions of softmax and 600 of
+// unpacking, 475 issue cycles, beside 256 cycles of MMA and 200 of HBM.
+
+constexpr int kTileRows = 128;
+constexpr int kTileBlk = 64;
+constexpr int kTileThreads = 288;
+constexpr uint32_t kTileTmemCols = 256;
+constexpr uint32_t kTilePollNs = 100;  // longest sleep of the MMA warp on one input
+
+template <int HD>
+struct Tile {
+  static constexpr int SK = HD == 64 ? 3 : 2, SV = SK;  // stages of the K and V rings
+  static constexpr int NB = HD == 64 ? 3 : 2;           // S buffers: NB * 64 columns and O's HD fill the 256
+  static constexpr uint32_t TO = NB * kTileBlk;         // first column of O
+  static constexpr uint32_t Q = kTileRows * HD * 2, KV = kTileBlk * HD * 2;
+  static constexpr uint32_t KRING = Q, VRING = KRING + SK * KV, CTRL = VRING + SV * KV;
+  static constexpr uint32_t FIXED = CTRL + 512;
+  static size_t smem(int n_tiles) { return 1024 + FIXED + Layout::kBytesPerTile * (size_t)n_tiles + 4; }
+};
+
+struct TileCtrl {
+  uint64_t kfull[3], kempty[3], vfull[3], vempty[3];  // full: an arrival per unpacking warp; empty: the MMAs read it
+  uint64_t q_full;                 // the item's query tile is staged
+  uint64_t s_full[3], p_full[3];   // S of a block is in its buffer; P is (and O rescaled where needed)
+  uint64_t pv_item, o_free;        // the item's last PV has completed; its O has been read
+  uint64_t drain;
+  int scratch[12];
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(TileCtrl) <= 512, "");
+
+// 16-byte unit c of row r of a shared-memory tile [HD/64][ROWS][64 bf16], 128-byte swizzle.
+template <int ROWS>
+PE_DEV uint32_t unit_addr(uint32_t base, int row, int c) {
+  return base + (uint32_t)((c >> 3) * ROWS * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+}
+PE_DEV void st_shared16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// What a lane unpacks of a page: half a row of key and of value codes, and the row's scales.
+template <int HD>
+struct RawRow {
+  uint4 k[HD / 64], v[HD / 64];
+  uint32_t ks[HD / 64], vs[HD / 64];
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const PackedAttnArgs a, const Line ln) {
+  using C = Tile<HD>;
+  using L = PackedLayout<HD>;
+  constexpr int H = HD / 64, CH = HD / 8;
+  constexpr int SK = C::SK, SV = C::SV, NB = C::NB;
+  constexpr uint32_t TO = C::TO;
+  static_assert(SV >= NB - 1, "a value stage's release orders the PV product a rescale waits for");
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sQ = smem_u32(sm);
+  TileCtrl* ctl = reinterpret_cast<TileCtrl*>(sm + C::CTRL);
+  const Layout lo(sm + C::FIXED, ln.n_tiles);
+  volatile int* abort_flag = &ctl->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  pdl_wait();
+  pdl_trigger();
+  lay_out(a, ln, lo, ctl->scratch);
+  const Walk walk{lo, ln.n_tiles, a.n_kv, ln.unit_pages};
+  const uint32_t total = (uint32_t)lo.prefix[ln.n_tiles] * a.n_kv;
+  if (blockIdx.x == 0 && !ln.whole)
+    for (int k = tid; k <= ln.n_tiles; k += blockDim.x) ln.prefix[k] = lo.prefix[k];
+  uint32_t u0, u1;
+  cta_units(ln, walk, total, u0, u1);
+  if (u0 == u1) return;  // the whole CTA, before it holds anything
+  if (tid == 0) {
+    for (int s = 0; s < SK; ++s) {
+      mbar_init(smem_u32(&ctl->kfull[s]), 4);
+      mbar_init(smem_u32(&ctl->kempty[s]), 1);
+    }
+    for (int s = 0; s < SV; ++s) {
+      mbar_init(smem_u32(&ctl->vfull[s]), 4);
+      mbar_init(smem_u32(&ctl->vempty[s]), 1);
+    }
+    mbar_init(smem_u32(&ctl->q_full), kTileRows);
+    for (int b = 0; b < NB; ++b) {
+      mbar_init(smem_u32(&ctl->s_full[b]), 1);
+      mbar_init(smem_u32(&ctl->p_full[b]), kTileRows);
+    }
+    mbar_init(smem_u32(&ctl->pv_item), 1);
+    mbar_init(smem_u32(&ctl->o_free), kTileRows);
+    mbar_init(smem_u32(&ctl->drain), 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&ctl->tmem), kTileTmemCols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  auto blocks_of = [](const Segment& s) { return s.page1 > s.page0 ? (s.page1 - s.page0 + 3) >> 2 : 0; };
+  Segment seg = walk.at(walk.tile_of(u0), u0, u1);
+
+  if (warp < 4) {
+    // ------------------------------------------------------------------ unpack
+    const PairBits bits;
+    const int row = lane >> 1, hc = lane & 1, prow = warp * 16 + row;  // the row in the page and in the block
+    const uint32_t step = (uint32_t)a.n_kv * L::kRecord;
+    int blk = 0, ids = -1;
+    bool more = true;
+    // the next block's rows, over the segments; false behind the last
+    auto fetch = [&](RawRow<HD>& r) -> bool {
+      if (!more) return false;
+      while (blk >= blocks_of(seg)) {
+        if (seg.next >= u1) {
+          more = false;
+          return false;
+        }
+        seg = walk.after(seg, u1);
+        blk = 0;
+      }
+      if ((blk & 31) == 0) {  // page ids of 32 blocks, one per lane
+        const int x = seg.page0 + 4 * (blk + lane) + warp;
+        ids = -1;
+        if (x < seg.page1) {
+          ids = __ldcg(a.block_table + (size_t)((uint32_t)(ln.tile0 + seg.k) / ln.tps) * a.max_pages + x);
+          if (ids < 0 || ids >= a.num_pages) {
+            set_err(a.err, PE_DEV_BAD_PAGE);
+            ids = -1;
+          }
+        }
+      }
+      const int id = __shfl_sync(0xFFFFFFFFu, ids, blk & 31);
+      ++blk;
+      if (id >= 0) {
+        const uint8_t* rec = a.pool + (uint64_t)(uint32_t)id * step + (size_t)seg.g * L::kRecord;
+#pragma unroll
+        for (int c = 0; c < H; ++c) {
+          r.k[c] = __ldcg(reinterpret_cast<const uint4*>(rec + L::kK + row * L::kRow + (hc + 2 * c) * 16));
+          r.v[c] = __ldcg(reinterpret_cast<const uint4*>(rec + L::kV + row * L::kRow + (H * hc + c) * 16));
+        }
+#pragma unroll
+        for (int c = 0; c < H; ++c) {
+          r.ks[c] = __ldcg(reinterpret_cast<const uint32_t*>(rec + L::kKs + row * L::kScaleRow) + c);
+          r.vs[c] = __ldcg(reinterpret_cast<const uint32_t*>(rec + L::kVs + row * L::kScaleRow) + c);
+        }
+      } else {  // a page behind the range or outside the pool: zeros
+#pragma unroll
+        for (int c = 0; c < H; ++c) {
+          r.k[c] = r.v[c] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+          r.ks[c] = r.vs[c] = 0;
+        }
+      }
+      return true;
+    };
+    int gi = 0;
+    auto unpack = [&](const RawRow<HD>& r) -> bool {
+      {
+        const int s = gi % SK;
+        if (gi >= SK && !warp_ok(mbar_wait(smem_u32(&ctl->kempty[s]), ((uint32_t)(gi / SK) & 1u) ^ 1u, a.err, abort_flag, a.wait_ns)))
+          return false;
+        const uint32_t base = sQ + C::KRING + (uint32_t)s * C::KV;
+        // word w of the row: entries 4t..4t+3 of blocks 2u and 2u + 1, unit w of the tile's row
+        uint32_t sp[2 * 2 * H], zp[2 * 2 * H];
+#pragma unroll
+        for (int j = 0; j < 4 * H; ++j) {
+          sp[j] = packed_scale_lo(__byte_perm(r.ks[j / 4], 0, 0x4040 + 0x0101 * (j & 3)));
+          zp[j] = bf16x2_mul(sp[j], kMinus136);
+        }
+#pragma unroll
+        for (int c = 0; c < H; ++c) {
+          const uint32_t w4[4] = {r.k[c].x, r.k[c].y, r.k[c].z, r.k[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int u = HD == 64 ? i & 1 : i;  // word 4 (hc + 2c) + i = t * HD/32 + u
+            st_shared16(unit_addr<kTileBlk>(base, prow, 4 * (hc + 2 * c) + i),
+                        bf16x2_fma(bits.pair<0>(w4[i]), sp[2 * u], zp[2 * u]), bf16x2_fma(bits.pair<1>(w4[i]), sp[2 * u], zp[2 * u]),
+                        bf16x2_fma(bits.pair<2>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]),
+                        bf16x2_fma(bits.pair<3>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->kfull[s]));
+      }
+      {
+        const int s = gi % SV;
+        if (gi >= SV && !warp_ok(mbar_wait(smem_u32(&ctl->vempty[s]), ((uint32_t)(gi / SV) & 1u) ^ 1u, a.err, abort_flag, a.wait_ns)))
+          return false;
+        const uint32_t base = sQ + C::VRING + (uint32_t)s * C::KV;
+        // word (g, h): entries g and g + 8 of four blocks, pairs 32 entries apart; unit g of the h-th 64 columns
+        uint32_t sp[H][2], zp[H][2];
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          sp[h][0] = packed_scale_lo(r.vs[h]);
+          sp[h][1] = packed_scale_hi(r.vs[h]);
+          zp[h][0] = bf16x2_mul(sp[h][0], kMinus136);
+          zp[h][1] = bf16x2_mul(sp[h][1], kMinus136);
+        }
+#pragma unroll
+        for (int c = 0; c < H; ++c) {
+          const uint32_t w4[4] = {r.v[c].x, r.v[c].y, r.v[c].z, r.v[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int h = HD == 64 ? 0 : i & 1;  // word 4 (H hc + c) + i = g * H + h
+            const int g = HD == 64 ? 4 * hc + i : 2 * (2 * hc + c) + (i >> 1);
+            st_shared16(unit_addr<kTileBlk>(base, prow, 8 * h + g),
+                        bf16x2_fma(bits.pair<0>(w4[i]), sp[h][0], zp[h][0]), bf16x2_fma(bits.pair<1>(w4[i]), sp[h][0], zp[h][0]),
+                        bf16x2_fma(bits.pair<2>(w4[i]), sp[h][1], zp[h][1]), bf16x2_fma(bits.pair<3>(w4[i]), sp[h][1], zp[h][1]));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->vfull[s]));
+      }
+      ++gi;
+      return true;
+    };
+    RawRow<HD> r0, r1;
+    bool ok0 = fetch(r0), ok1 = fetch(r1);
+#pragma unroll 1
+    while (ok0) {
+      if (!unpack(r0)) break;
+      ok0 = fetch(r0);
+      if (!ok1) break;
+      if (!unpack(r1)) break;
+      ok1 = fetch(r1);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------------ MMA issuer (a converged warp)
+    const uint32_t id_s = idesc_bf16(kTileRows, kTileBlk);               // N = positions
+    const uint32_t id_o = idesc_bf16(kTileRows, HD) | kIdescTransposeB;  // V is MN-major
+    int gi = 0, ii = 0;
+    bool stop = false;
+    for (;;) {
+      const int nblk = blocks_of(seg);
+      if (nblk > 0) {
+        if (!warp_ok(mbar_wait(smem_u32(&ctl->q_full), (uint32_t)ii & 1u, a.err, abort_flag, a.wait_ns))) break;
+        tc_fence_after();
+        // Two streams, issued as their inputs arrive: S of block ns once its keys are there and its
+        // buffer is free (the PV of block ns - NB is issued), and the PV of block np once its P and
+        // its values are (the item's first, which overwrites O, once the last item's O has been read).
+        int ns = 0, np = 0;
+        bool o_ok = ii == 0;
+        uint64_t t_idle = 0;
+        uint32_t n_idle = 0;
+        while (np < nblk) {
+          bool prog = false;
+          if (ns < nblk && ns <= np + NB - 1) {
+            const int x = gi + ns, s = x % SK;
+            if (warp_ok(mbar_test_wait(smem_u32(&ctl->kfull[s]), (uint32_t)(x / SK) & 1u))) {
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t kbase = sQ + C::KRING + (uint32_t)s * C::KV;
+                const uint32_t d = tmem + (uint32_t)((x % NB) * kTileBlk);
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                  const uint64_t ad = sdesc_k_sw128(sQ + (uint32_t)((kk >> 2) * kTileRows * 128)) + 2 * (kk & 3);
+                  const uint64_t bd = sdesc_k_sw128(kbase + (uint32_t)((kk >> 2) * kTileBlk * 128)) + 2 * (kk & 3);
+                  tc_mma_bf16(d, ad, bd, id_s, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(smem_u32(&ctl->s_full[x % NB]));
+                tc_commit(smem_u32(&ctl->kempty[s]));
+              }
+              __syncwarp();
+              ++ns;
+              prog = true;
+            }
+          }
+          if (np < ns) {
+            const int x = gi + np, s = x % SV;
+            if (!o_ok) o_ok = warp_ok(mbar_test_wait(smem_u32(&ctl->o_free), (uint32_t)(ii - 1) & 1u));
+            if (o_ok && warp_ok(mbar_test_wait(smem_u32(&ctl->p_full[x % NB]), (uint32_t)(x / NB) & 1u) &&
+                                mbar_test_wait(smem_u32(&ctl->vfull[s]), (uint32_t)(x / SV) & 1u))) {
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t vbase = sQ + C::VRING + (uint32_t)s * C::KV;
+                const uint32_t pa = tmem + (uint32_t)((x % NB) * kTileBlk);
+#pragma unroll
+                for (int kk = 0; kk < kTileBlk / 16; ++kk)
+                  tc_mma_bf16_tmem_a(tmem + TO, pa + 8u * kk, sdesc_mn_sw128(vbase + (uint32_t)kk * 2048u, kTileBlk * 128),
+                                     id_o, (np > 0 || kk > 0) ? 1u : 0u);
+                if (np == nblk - 1) tc_commit(smem_u32(&ctl->pv_item));
+                tc_commit(smem_u32(&ctl->vempty[s]));
+              }
+              __syncwarp();
+              ++np;
+              prog = true;
+            }
+          }
+          if (prog) {
+            n_idle = 0;
+            continue;
+          }
+          if ((n_idle++ & 7) == 0) {  // a bounded wait: give up when another role did, or after the limit
+            if (*abort_flag) {
+              stop = true;
+              break;
+            }
+            const uint64_t now = global_timer_ns();
+            if (n_idle == 1) {
+              t_idle = now;
+            } else if (now - t_idle > a.wait_ns) {
+              if (elect_one()) {
+                set_err(a.err, PE_DEV_TIMEOUT);
+                *abort_flag = 1;
+              }
+              __syncwarp();
+              stop = true;
+              break;
+            }
+          }
+          // sleep on the input most likely to come next (a hot loop would take issue slots from the others)
+          if (np < ns) {
+            const int x = gi + np;
+            mbar_try_wait_for(smem_u32(&ctl->p_full[x % NB]), (uint32_t)(x / NB) & 1u, kTilePollNs);
+          } else if (ns < nblk) {
+            const int x = gi + ns;
+            mbar_try_wait_for(smem_u32(&ctl->kfull[x % SK]), (uint32_t)(x / SK) & 1u, kTilePollNs);
+          }
+          __syncwarp();
+        }
+        if (stop) break;
+        gi += nblk;
+        ++ii;
+      }
+      if (seg.next >= u1) break;
+      seg = walk.after(seg, u1);
+    }
+    // TMEM is freed only after every MMA issued here has completed
+    if (elect_one()) tc_commit(smem_u32(&ctl->drain));
+    __syncwarp();
+    mbar_wait(smem_u32(&ctl->drain), 0, a.err, nullptr, a.wait_ns);
+  } else {
+    // ------------------------------------------------------------------ softmax and output
+    const int et = tid - 128;
+    const int r = (warp & 3) * 32 + lane;  // query vector of the tile = TMEM lane
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const float sl2 = a.scale * 1.4426950408889634f * kPackedUnit;
+    const __nv_bfloat16* qbuf = static_cast<const __nv_bfloat16*>(a.q);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+    auto row_of = [&](const TileRows& t, int v, int g, long long stride) {
+      const int m = t.m0 + v, rr = (int)((uint32_t)m / ln.group);
+      return (t.r0 + rr) * stride + (g * ln.G + m - rr * ln.G) * HD;
+    };
+    // the query tile, entries in the order of the key words: unit w = t * HD/32 + u holds entries 4t..4t+3 of
+    // blocks 2u and 2u + 1; zeros behind the tile's vectors
+    auto stage_q = [&](const Segment& sg) {
+      const TileRows t = lo.tile(ln, sg.k);
+      constexpr int PER = kTileRows * CH / 128;  // units per thread, eight at a time in flight
+#pragma unroll
+      for (int k0 = 0; k0 < PER; k0 += 8) {
+        uint2 x[8], y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int idx = et + (k0 + k) * 128, m = idx / CH, w = idx % CH;
+          x[k] = y[k] = make_uint2(0, 0);
+          if (m < t.M) {
+            const __nv_bfloat16* src = qbuf + row_of(t, m, sg.g, a.q_stride) + 32 * (w % (HD / 32)) + 4 * (w / (HD / 32));
+            x[k] = __ldcg(reinterpret_cast<const uint2*>(src));
+            y[k] = __ldcg(reinterpret_cast<const uint2*>(src + 16));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int idx = et + (k0 + k) * 128, m = idx / CH, w = idx % CH;
+          st_shared16(unit_addr<kTileRows>(sQ, m, w), x[k].x, x[k].y, y[k].x, y[k].y);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&ctl->q_full));
+    };
+    int gi = 0, ii = 0;
+    bool stop = false, staged = false;
+    for (;;) {
+      const TileRows tr = lo.tile(ln, seg.k);
+      const int nblk = blocks_of(seg);
+      const bool valid = r < tr.M;
+      if (nblk == 0) {  // nothing to see: zeros
+        if (valid) {
+          __nv_bfloat16* dst = out + row_of(tr, r, seg.g, a.out_stride);
+#pragma unroll
+          for (int c = 0; c < CH; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+        }
+        if (seg.next >= u1) break;
+        seg = walk.after(seg, u1);
+        continue;
+      }
+      if (!staged) stage_q(seg);
+      staged = false;
+      // the vector's last visible position within the segment
+      bool bad = false;  // reported by lay_out
+      int lim = -1;
+      if (valid)
+        lim = min(row_limit(a, __ldcg(a.positions + tr.r0 + (int)((uint32_t)(tr.m0 + r) / ln.group)), bad), seg.page1 * kPackedPage - 1);
+      const bool warp_any = __any_sync(0xFFFFFFFFu, valid);
+      int wmin = valid ? lim : INT_MAX;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) wmin = min(wmin, __shfl_xor_sync(0xFFFFFFFFu, wmin, o));
+      float m_ref = -INFINITY, l = 0.f;  // reference maximum (log2 units) and sum
+      for (int j = 0; j < nblk; ++j) {
+        const int x = gi + j;
+        if (!warp_ok(mbar_wait(smem_u32(&ctl->s_full[x % NB]), (uint32_t)(x / NB) & 1u, a.err, abort_flag, a.wait_ns))) {
+          stop = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sbuf = tmem + lane_base + (uint32_t)((x % NB) * kTileBlk);
+        if (warp_any) {
+          float sc[kTileBlk];
+          tmem_load64(sbuf, sc);
+          const int kb0 = seg.page0 * kPackedPage + j * kTileBlk;
+          if (kb0 + kTileBlk - 1 > wmin) {  // some position of the block is masked for some vector of the warp
+#pragma unroll
+            for (int c = 0; c < kTileBlk; ++c) sc[c] = (kb0 + c <= lim) ? sc[c] : -INFINITY;
+          }
+          float mx8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx8[e] = sc[e];
+#pragma unroll
+          for (int c = 8; c < kTileBlk; ++c) mx8[c & 7] = fmaxf(mx8[c & 7], sc[c]);
+          float bm = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                           fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          bm *= sl2;
+          const bool fresh = m_ref == -INFINITY;
+          const bool need = !fresh && bm > m_ref + kRescaleLog2;
+          if (__any_sync(0xFFFFFFFFu, need)) {
+            // O holds the PV products of the blocks before j.  The release of block x - 1's values is
+            // committed after its PV product, and that barrier is at most one phase short of it: S(x)
+            // completing implies that every PV up to block x - NB has, and SV >= NB - 1.
+            const int xp = x - 1;
+            if (!warp_ok(mbar_wait(smem_u32(&ctl->vempty[xp % SV]), (uint32_t)(xp / SV) & 1u, a.err, abort_flag, a.wait_ns))) {
+              stop = true;
+            } else {
+              tc_fence_after();
+              const float f = need ? ex2_approx(m_ref - bm) : 1.f;
+#pragma unroll 1
+              for (int c = 0; c < HD; c += 16) {
+                float ov[16];
+                tmem_load16(tmem + lane_base + TO + (uint32_t)c, ov);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ov[e] *= f;
+                tmem_store16(tmem + lane_base + TO + (uint32_t)c, ov);
+              }
+              if (need) {
+                l *= f;
+                m_ref = bm;
+              }
+            }
+          }
+          if (fresh) m_ref = bm;
+          // masked scores are -inf; a vector with nothing unmasked yet takes offset -inf, so P = 0 there too
+          const float nmr = m_ref == -INFINITY ? -INFINITY : -m_ref;
+          uint32_t pk[kTileBlk / 2];
+          float rs8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) rs8[e] = 0.f;
+#pragma unroll
+          for (int c = 0; c < kTileBlk / 2; ++c) {
+            const float p0 = ex2_approx(fmaf(sc[2 * c], sl2, nmr));
+            const float p1 = ex2_approx(fmaf(sc[2 * c + 1], sl2, nmr));
+            rs8[c & 7] += p0 + p1;
+            pk[c] = pack_bf16(p0, p1);
+          }
+          l += ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
+          tmem_store32(sbuf, pk);
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&ctl->p_full[x % NB]));
+        if (stop) break;
+      }
+      if (stop) break;
+      const Segment done = seg;
+      const bool final = seg.next >= u1;
+      // every S product of this segment has completed: the next one's query tile may go in
+      if (!final) {
+        seg = walk.after(seg, u1);
+        if (blocks_of(seg) > 0) {
+          stage_q(seg);
+          staged = true;
+        }
+      }
+      gi += nblk;
+      if (!warp_ok(mbar_wait(smem_u32(&ctl->pv_item), (uint32_t)ii & 1u, a.err, abort_flag, a.wait_ns))) break;
+      ++ii;
+      tc_fence_after();
+      const bool whole = done.from_start && done.to_end;
+      if (warp_any) {
+        const float inv = whole && l > 0.f ? kPackedUnit / l : whole ? 0.f : 1.f;
+        float* rec = whole ? nullptr : part_record<HD>(ln, blockIdx.x, done.from_start);
+        if (valid && !whole) {
+          rec[r] = m_ref;
+          rec[kTileRows + r] = l;
+        }
+#pragma unroll 1
+        for (int h = 0; h < H; ++h) {
+          float ov[64];
+          tmem_load64(tmem + lane_base + TO + 64u * h, ov);
+          if (valid) {
+            // column 8g + 2i + e holds entry 16 (i/2) + g + 8 (i%2) + 32 e
+            if (whole) {
+              __nv_bfloat16* dst = out + row_of(tr, r, done.g, a.out_stride) + 64 * h;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {  // entries 8c..8c+7: block c/2, its half c%2
+                const int col = 2 * (2 * ((c >> 1) & 1) + (c & 1)) + (c >> 2);
+                reinterpret_cast<uint4*>(dst)[c] =
+                    make_uint4(pack_bf16(ov[col] * inv, ov[8 + col] * inv), pack_bf16(ov[16 + col] * inv, ov[24 + col] * inv),
+                               pack_bf16(ov[32 + col] * inv, ov[40 + col] * inv), pack_bf16(ov[48 + col] * inv, ov[56 + col] * inv));
+              }
+            } else {
+              float* dst = rec + 2 * kTileRows + r * HD + 64 * h;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const int col = 2 * (2 * ((c >> 1) & 1) + (c & 1)) + (c >> 2);
+                const float v[8] = {ov[col], ov[8 + col], ov[16 + col], ov[24 + col], ov[32 + col], ov[40 + col], ov[48 + col], ov[56 + col]};
+                st_global_v8(dst + 8 * c, v);
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(smem_u32(&ctl->o_free));
+      if (final) break;
+    }
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTileTmemCols);
+  }
+}
+
 // ----------------------------------------------------------------------------- merge of cut ranges
 
 constexpr int kMergeThreads = 256;
@@ -1054,13 +1606,20 @@ Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_l
   ln.heads = make_div(a.n_kv);
   ln.G = G;
   ln.whole = a.max_pages <= kWholePages;
-  ln.min_log2 = min_log2;
+  ln.min_log2 = ln.whole ? 0 : min_log2;
   const int rows = std::min(a.max_rows, tile_rows / G + 2);
   ln.lanes = 1;
   while (ln.lanes < 32 && ln.lanes * 4 < rows) ln.lanes *= 2;
   const long long units = (long long)a.n_kv * ((a.max_pages + unit_pages - 1) / unit_pages);  // of a tile, at most
   *tiles_per_launch = (int)std::min<long long>(kPlanTiles, std::max(1LL, ((1LL << 31) - 1) / units));
   return ln;
+}
+
+// CTAs of a launch: no more than the tables' positions could keep busy (whole ranges: one each).
+int line_grid(const PackedAttnArgs& a, const Line& ln, int most) {
+  const long long ranges = (long long)ln.n_tiles * a.n_kv;
+  const long long units = ranges * ((a.max_pages + ln.unit_pages - 1) / ln.unit_pages);
+  return (int)std::min<long long>(most, std::max(1LL, ln.whole ? ranges : units >> ln.min_log2));
 }
 
 template <typename T, int HD, int NQ>
@@ -1078,10 +1637,7 @@ cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   for (long long t0 = 0; t0 < tiles; t0 += per_launch) {
     ln.tile0 = (int)t0;
     ln.n_tiles = (int)std::min<long long>(per_launch, tiles - t0);
-    // no more CTAs than the tables' positions could keep busy
-    const long long ranges = (long long)ln.n_tiles * a.n_kv;
-    const long long units = ranges * ((a.max_pages + ln.unit_pages - 1) / ln.unit_pages);
-    const int grid = (int)std::min<long long>((long long)sms * C::CTAS, std::max(1LL, units >> ln.min_log2));
+    const int grid = line_grid(a, ln, sms * C::CTAS);
     ln.grid = make_div(grid);
     e = launch_pdl(attend_small_kernel<T, HD, NQ>, dim3(grid), dim3(kSmallWarps * 32), C::smem(ln.n_tiles), s, a, ln);
     if (e != cudaSuccess) return e;
@@ -1090,19 +1646,46 @@ cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   return cudaSuccess;
 }
 
+template <int HD>
+cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
+  using C = Tile<HD>;
+  int per_launch = 0;
+  Line ln = make_line(a, kTileRows, 4, 1, &per_launch);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  ln.prefix = reinterpret_cast<int*>(ws);
+  ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
+  cudaError_t e = allow_smem<attend_tile_kernel<HD>>(C::smem(kPlanTiles));
+  if (e != cudaSuccess) return e;
+  const long long tiles = (long long)a.B * ln.n_tps;
+  for (long long t0 = 0; t0 < tiles; t0 += per_launch) {
+    ln.tile0 = (int)t0;
+    ln.n_tiles = (int)std::min<long long>(per_launch, tiles - t0);
+    const int grid = line_grid(a, ln, sms * 2);
+    ln.grid = make_div(grid);
+    e = launch_pdl(attend_tile_kernel<HD>, dim3(grid), dim3(kTileThreads), C::smem(ln.n_tiles), s, a, ln);
+    if (e != cudaSuccess) return e;
+    if (!ln.whole && grid > 1 && (e = launch_merge<__nv_bfloat16, HD>(a, ln, grid, s)) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 template <typename T, int HD>
 cudaError_t launch_attend_typed(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   const long long vectors = (long long)a.max_rows * (a.n_q / a.n_kv);
+  if constexpr (sizeof(T) == 2)
+    if (vectors > 16) return launch_tile<HD>(a, sms, s);
   if (vectors <= 8) return launch_small<T, HD, 1>(a, sms, s);
   return launch_small<T, HD, 2>(a, sms, s);
 }
 
 }  // namespace
 
-size_t packed_attn_workspace_bytes(int head_dim, pe_dtype, int sms) {
-  // two records per CTA, and a part per warp, of up to 16 vectors
+size_t packed_attn_workspace_bytes(int head_dim, pe_dtype dt, int sms) {
+  // small tiles: two records per CTA, and a part per warp, of up to 16 vectors; large ones (bf16): two records
+  // of 128 vectors
   const size_t rec = (size_t)16 * (head_dim + 2) * 4, part = (size_t)16 * (head_dim + 6) * 4;
-  return kPrefixBytes + (size_t)sms * kMaxCtasPerSm * (2 * rec + kSmallWarps * part);
+  const size_t small = 2 * rec + kSmallWarps * part, large = dt == PE_BF16 ? 2 * (size_t)kTileRows * (head_dim + 2) * 4 : 0;
+  return kPrefixBytes + (size_t)sms * kMaxCtasPerSm * std::max(small, large);
 }
 
 cudaError_t launch_attend_packed(const PackedAttnArgs& a, pe_dtype dt, int sms, cudaStream_t s) {
