@@ -969,6 +969,33 @@ struct RawRow {
   uint32_t ks[HD / 64], vs[HD / 64];
 };
 
+// Two fp32 values in one 64-bit register, for the packed fp32 instructions.
+struct F2 {
+  uint64_t v;
+  PE_DEV F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  PE_DEV explicit F2(uint64_t x) : v(x) {}
+  PE_DEV float lo() const {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return a;
+  }
+  PE_DEV float hi() const {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    return b;
+  }
+  static PE_DEV F2 fma(F2 a, F2 b, F2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return F2(d);
+  }
+  static PE_DEV F2 add(F2 a, F2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a.v), "l"(b.v));
+    return F2(d);
+  }
+};
+
 template <int HD>
 __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const PackedAttnArgs a, const Line ln) {
   using C = Tile<HD>;
@@ -1004,13 +1031,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
       mbar_init(smem_u32(&ctl->vfull[s]), 4);
       mbar_init(smem_u32(&ctl->vempty[s]), 1);
     }
-    mbar_init(smem_u32(&ctl->q_full), kTileRows);
+    mbar_init(smem_u32(&ctl->q_full), 4);
     for (int b = 0; b < NB; ++b) {
       mbar_init(smem_u32(&ctl->s_full[b]), 1);
-      mbar_init(smem_u32(&ctl->p_full[b]), kTileRows);
+      mbar_init(smem_u32(&ctl->p_full[b]), 4);
     }
     mbar_init(smem_u32(&ctl->pv_item), 1);
-    mbar_init(smem_u32(&ctl->o_free), kTileRows);
+    mbar_init(smem_u32(&ctl->o_free), 4);
     mbar_init(smem_u32(&ctl->drain), 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -1261,6 +1288,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
     const int et = tid - 128;
     const int r = (warp & 3) * 32 + lane;  // query vector of the tile = TMEM lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    auto arrive = [&](uint64_t* bar) {  // one arrival per warp
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(bar));
+    };
     const float sl2 = a.scale * 1.4426950408889634f * kPackedUnit;
     const __nv_bfloat16* qbuf = static_cast<const __nv_bfloat16*>(a.q);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
@@ -1293,7 +1324,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(smem_u32(&ctl->q_full));
+      arrive(&ctl->q_full);
     };
     int gi = 0, ii = 0;
     bool stop = false, staged = false;
@@ -1339,13 +1370,15 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
 #pragma unroll
             for (int c = 0; c < kTileBlk; ++c) sc[c] = (kb0 + c <= lim) ? sc[c] : -INFINITY;
           }
-          float mx8[8];
+          float mx4[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mx8[e] = sc[e];
+          for (int e = 0; e < 4; ++e) mx4[e] = sc[e];
 #pragma unroll
-          for (int c = 8; c < kTileBlk; ++c) mx8[c & 7] = fmaxf(mx8[c & 7], sc[c]);
-          float bm = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                           fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          for (int c = 4; c < kTileBlk; c += 8)  // (two maxima of three operands each)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx4[e] = c + 4 + e < kTileBlk ? fmaxf(fmaxf(mx4[e], sc[c + e]), sc[c + 4 + e]) : fmaxf(mx4[e], sc[c + e]);
+          float bm = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           bm *= sl2;
           const bool fresh = m_ref == -INFINITY;
           const bool need = !fresh && bm > m_ref + kRescaleLog2;
@@ -1376,22 +1409,22 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
           if (fresh) m_ref = bm;
           // masked scores are -inf; a vector with nothing unmasked yet takes offset -inf, so P = 0 there too
           const float nmr = m_ref == -INFINITY ? -INFINITY : -m_ref;
+          const F2 scale2(sl2, sl2), off2(nmr, nmr);
+          F2 sum2[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
           uint32_t pk[kTileBlk / 2];
-          float rs8[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) rs8[e] = 0.f;
 #pragma unroll
           for (int c = 0; c < kTileBlk / 2; ++c) {
-            const float p0 = ex2_approx(fmaf(sc[2 * c], sl2, nmr));
-            const float p1 = ex2_approx(fmaf(sc[2 * c + 1], sl2, nmr));
-            rs8[c & 7] += p0 + p1;
+            const F2 d = F2::fma(F2(sc[2 * c], sc[2 * c + 1]), scale2, off2);
+            const float p0 = ex2_approx(d.lo()), p1 = ex2_approx(d.hi());
+            sum2[c & 1] = F2::add(sum2[c & 1], F2(p0, p1));
             pk[c] = pack_bf16(p0, p1);
           }
-          l += ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
+          const F2 s2 = F2::add(sum2[0], sum2[1]);
+          l += s2.lo() + s2.hi();
           tmem_store32(sbuf, pk);
         }
         tc_fence_before();
-        mbar_arrive(smem_u32(&ctl->p_full[x % NB]));
+        arrive(&ctl->p_full[x % NB]);
         if (stop) break;
       }
       if (stop) break;
@@ -1445,7 +1478,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
         }
       }
       tc_fence_before();
-      mbar_arrive(smem_u32(&ctl->o_free));
+      arrive(&ctl->o_free);
       if (final) break;
     }
   }
@@ -1460,9 +1493,9 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
 
 constexpr int kMergeThreads = 256;
 
-// `split` warps (a power of two, at most 8) per (tile, head, vector) take every split-th record of it;
-// they join in shared memory.  Lanes over the entries.  Every sum runs in CTA order within a warp,
-// then in warp order.
+// A CTA per (tile, head), or one of `shares` (grid's y) that take its vectors in turn: it finds the CTAs that
+// hold parts of the range, then its warps take the vectors, `split` warps (a power of two, at most 8) for each, every split-th record a warp; these join in
+// shared memory.  Lanes over the entries.  Sums run in CTA order within a warp, then in warp order.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const PackedAttnArgs a, const Line ln, int grid,
                                                                      int split) {
@@ -1470,95 +1503,97 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
   __shared__ float sh_m[8], sh_l[8], sh_o[8][HD];
   pdl_wait();
   pdl_trigger();
+  const int k = (int)(blockIdx.x / ln.heads), g = (int)blockIdx.x - k * a.n_kv;
+  const int p0 = __ldcg(ln.prefix + k), p1 = __ldcg(ln.prefix + k + 1);
+  const uint32_t tot = (uint32_t)__ldcg(ln.prefix + ln.n_tiles) * a.n_kv;
+  bool bad = false;  // reported by the kernel before
+  const TileRows tr = tile_rows(a, ln, ln.tile0 + k, bad);
+  if (p1 == p0) return;
+  const Cuts cuts(ln, grid, tot);
+  const uint32_t first = (uint32_t)p0 * a.n_kv + (uint32_t)g * (p1 - p0);
+  const int c0 = (int)cuts.piece(first), c1 = (int)cuts.piece(first + (p1 - p0) - 1);
+  if (c0 == c1) return;  // finished by its CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = warp & (split - 1);
-  const uint32_t task = blockIdx.x * (8 / split) + warp / split;
-  const uint32_t vec = task >> ln.rows_log2;  // (tile, head)
-  const int v = (int)(task - (vec << ln.rows_log2));
-  const int k = min((int)(vec / ln.heads), ln.n_tiles), g = (int)vec - k * a.n_kv;
-  float mx = -INFINITY, sum = 0.f, x[VPL];
+  const int sub = warp & (split - 1), per = 8 / split;  // vectors at a time
+  for (int v0 = blockIdx.y * per; v0 < tr.M; v0 += gridDim.y * per) {  // the same trip count for every warp
+    const int v = v0 + warp / split;
+    float mx = -INFINITY, sum = 0.f, x[VPL];
 #pragma unroll
-  for (int e = 0; e < VPL; ++e) x[e] = 0.f;
-  bool live = false;
-  TileRows tr{0, 0, 0};
-  if (k < ln.n_tiles) {
-    const int p0 = __ldcg(ln.prefix + k), p1 = __ldcg(ln.prefix + k + 1);
-    const uint32_t tot = (uint32_t)__ldcg(ln.prefix + ln.n_tiles) * a.n_kv;
-    bool bad = false;  // reported by the kernel before
-    tr = tile_rows(a, ln, ln.tile0 + k, bad);
-    if (p1 > p0) {
-      const Cuts cuts(ln, grid, tot);
-      const uint32_t first = (uint32_t)p0 * a.n_kv + (uint32_t)g * (p1 - p0);
-      const int c0 = (int)cuts.piece(first), c1 = (int)cuts.piece(first + (p1 - p0) - 1);
-      live = c1 > c0 && v < tr.M;
-      if (live) {
-        for (int c = c0 + sub; c <= c1; c += CB * split) {
-          float m[CB], l[CB], y[CB][VPL];
+    for (int e = 0; e < VPL; ++e) x[e] = 0.f;
+    if (v < tr.M) {
+      for (int c = c0 + sub; c <= c1; c += CB * split) {
+        float m[CB], l[CB], y[CB][VPL];
 #pragma unroll
-          for (int i = 0; i < CB; ++i) {
-            const int cc = c + i * split;
-            m[i] = -INFINITY;
-            l[i] = 0.f;
+        for (int i = 0; i < CB; ++i) {
+          const int cc = c + i * split;
+          m[i] = -INFINITY;
+          l[i] = 0.f;
 #pragma unroll
-            for (int e = 0; e < VPL; ++e) y[i][e] = 0.f;
-            if (cc <= c1) {
-              const float* rec = part_record<HD>(ln, cc, cc == c0);
-              m[i] = __ldcg(rec + v);
-              l[i] = __ldcg(rec + ln.tile_rows + v);
-              const float* src = rec + 2 * ln.tile_rows + (size_t)v * HD + lane * VPL;
-              if constexpr (VPL == 4) {
-                const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
-                y[i][0] = z.x; y[i][1] = z.y; y[i][2] = z.z; y[i][3] = z.w;
-              } else {
-                const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
-                y[i][0] = z.x; y[i][1] = z.y;
-              }
+          for (int e = 0; e < VPL; ++e) y[i][e] = 0.f;
+          if (cc <= c1) {
+            const float* rec = part_record<HD>(ln, cc, cc == c0);
+            m[i] = __ldcg(rec + v);
+            l[i] = __ldcg(rec + ln.tile_rows + v);
+            const float* src = rec + 2 * ln.tile_rows + (size_t)v * HD + lane * VPL;
+            if constexpr (VPL == 4) {
+              const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
+              y[i][0] = z.x; y[i][1] = z.y; y[i][2] = z.z; y[i][3] = z.w;
+            } else {
+              const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
+              y[i][0] = z.x; y[i][1] = z.y;
             }
           }
-#pragma unroll
-          for (int i = 0; i < CB; ++i) {
-            const float nx = fmaxf(mx, m[i]);
-            if (nx == -INFINITY) continue;
-            const float f = ex2_approx(mx - nx), w = ex2_approx(m[i] - nx);
-            sum = sum * f + w * l[i];
-#pragma unroll
-            for (int e = 0; e < VPL; ++e) x[e] = x[e] * f + w * y[i][e];
-            mx = nx;
-          }
         }
+        float nx = mx;
+#pragma unroll
+        for (int i = 0; i < CB; ++i) nx = fmaxf(nx, m[i]);
+        if (nx == -INFINITY) continue;
+        const float f = ex2_approx(mx - nx);
+        sum *= f;
+#pragma unroll
+        for (int e = 0; e < VPL; ++e) x[e] *= f;
+#pragma unroll
+        for (int i = 0; i < CB; ++i) {
+          const float w = ex2_approx(m[i] - nx);
+          sum = fmaf(w, l[i], sum);
+#pragma unroll
+          for (int e = 0; e < VPL; ++e) x[e] = fmaf(w, y[i][e], x[e]);
+        }
+        mx = nx;
       }
     }
-  }
-  if (split > 1) {
-    if (lane == 0) {
-      sh_m[warp] = mx;
-      sh_l[warp] = sum;
+    if (split > 1) {
+      __syncthreads();  // the last vectors' values have been read
+      if (lane == 0) {
+        sh_m[warp] = mx;
+        sh_l[warp] = sum;
+      }
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) sh_o[warp][lane * VPL + e] = x[e];
+      __syncthreads();
+      if (sub == 0)
+        for (int w = warp + 1; w < warp + split; ++w) {
+          const float m = sh_m[w], nx = fmaxf(mx, m);
+          if (nx == -INFINITY) continue;
+          const float f = ex2_approx(mx - nx), q = ex2_approx(m - nx);
+          sum = sum * f + q * sh_l[w];
+#pragma unroll
+          for (int e = 0; e < VPL; ++e) x[e] = x[e] * f + q * sh_o[w][lane * VPL + e];
+          mx = nx;
+        }
     }
+    if (sub != 0 || v >= tr.M) continue;
+    const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
+    const int m = tr.m0 + v, r = (int)((uint32_t)m / ln.group);
+    T* out = static_cast<T*>(a.out) + (tr.r0 + r) * a.out_stride + (g * ln.G + m - r * ln.G) * HD + lane * VPL;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int e = 0; e < VPL; ++e) sh_o[warp][lane * VPL + e] = x[e];
-    __syncthreads();
-    if (sub != 0) return;
-    for (int w = warp + 1; w < warp + split; ++w) {
-      const float m = sh_m[w], nx = fmaxf(mx, m);
-      if (nx == -INFINITY) continue;
-      const float f = ex2_approx(mx - nx), q = ex2_approx(m - nx);
-      sum = sum * f + q * sh_l[w];
-#pragma unroll
-      for (int e = 0; e < VPL; ++e) x[e] = x[e] * f + q * sh_o[w][lane * VPL + e];
-      mx = nx;
+      for (int e = 0; e < VPL; ++e) out[e] = x[e] * inv;
+    } else if constexpr (VPL == 4) {
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+    } else {
+      *reinterpret_cast<uint32_t*>(out) = pack_bf16(x[0] * inv, x[1] * inv);
     }
-  }
-  if (!live) return;
-  const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
-  const int m = tr.m0 + v, r = (int)((uint32_t)m / ln.group);
-  T* out = static_cast<T*>(a.out) + (tr.r0 + r) * a.out_stride + (g * ln.G + m - r * ln.G) * HD + lane * VPL;
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int e = 0; e < VPL; ++e) out[e] = x[e] * inv;
-  } else if constexpr (VPL == 4) {
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
-  } else {
-    *reinterpret_cast<uint32_t*>(out) = pack_bf16(x[0] * inv, x[1] * inv);
   }
 }
 
@@ -1581,14 +1616,14 @@ cudaError_t allow_smem(size_t bytes) {
 }
 
 template <typename T, int HD>
-cudaError_t launch_merge(const PackedAttnArgs& a, const Line& ln, int grid, cudaStream_t s) {
-  // few (tile, head) ranges: each may be cut into many records
+cudaError_t launch_merge(const PackedAttnArgs& a, const Line& ln, int grid, int sms, cudaStream_t s) {
+  // few ranges: each may be cut into many records
   const long long ranges = (long long)ln.n_tiles * a.n_kv;
   int split = 1;
   while (split < 8 && ranges * split * 8 < grid) split *= 2;
-  const long long warps = ranges * ln.tile_rows * split;
-  return launch_pdl(attend_merge_kernel<T, HD>, dim3((unsigned)((warps + 7) / 8)), dim3(kMergeThreads), 0, s, a, ln,
-                    grid, split);
+  const long long shares = std::min<long long>(ln.tile_rows * split / 8, (8LL * sms + ranges - 1) / ranges);
+  return launch_pdl(attend_merge_kernel<T, HD>, dim3((unsigned)ranges, (unsigned)std::max(1LL, shares)), dim3(kMergeThreads), 0, s,
+                    a, ln, grid, split);
 }
 
 // The launch's line for tiles of `tile_rows` vectors and units of `unit_pages`, and how many of its tiles one
@@ -1641,7 +1676,7 @@ cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
     ln.grid = make_div(grid);
     e = launch_pdl(attend_small_kernel<T, HD, NQ>, dim3(grid), dim3(kSmallWarps * 32), C::smem(ln.n_tiles), s, a, ln);
     if (e != cudaSuccess) return e;
-    if (!ln.whole && grid > 1 && (e = launch_merge<T, HD>(a, ln, grid, s)) != cudaSuccess) return e;
+    if (!ln.whole && grid > 1 && (e = launch_merge<T, HD>(a, ln, grid, sms, s)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
@@ -1664,7 +1699,7 @@ cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
     ln.grid = make_div(grid);
     e = launch_pdl(attend_tile_kernel<HD>, dim3(grid), dim3(kTileThreads), C::smem(ln.n_tiles), s, a, ln);
     if (e != cudaSuccess) return e;
-    if (!ln.whole && grid > 1 && (e = launch_merge<__nv_bfloat16, HD>(a, ln, grid, s)) != cudaSuccess) return e;
+    if (!ln.whole && grid > 1 && (e = launch_merge<__nv_bfloat16, HD>(a, ln, grid, sms, s)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
