@@ -7,9 +7,10 @@
 // with keys and values of head h / (n_q / n_kv).  A row at position -1 sees nothing: zeros.
 //
 // Work.  The query vectors of a sequence and kv head (rows x G query heads, G = n_q / n_kv) are
-// cut into tiles; a (tile, kv head) pair's range of positions is counted in units.  All units of
-// the launch form one line (tile after tile, head after head, position after position) that
-// N CTAs divide into equal pieces, so ragged lengths leave no CTA idle.  A range that lies in
+// cut into tiles; a (tile, kv head) pair's range of positions is counted in units.  All ranges of
+// the launch form one line (tile after tile, head after head, unit after unit), a range as long as it
+// costs: so much at its start and so much per unit.  N CTAs divide the line into equal pieces, so
+// ragged lengths leave no CTA idle; a unit belongs to the piece in which it starts.  A range that lies in
 // one CTA's piece is finished there; one that is cut leaves a record per CTA (reference maximum,
 // sum, unnormalised output) that the merge kernel joins in CTA order.  Every CTA works the line
 // out for itself from row_start and positions (two dependent loads and a scan), which costs less
@@ -77,8 +78,12 @@ struct Line {
   int unit_pages;      // pages per unit
   int lanes;           // threads that look through one tile's rows (a power of two, at most 32)
   int whole;           // CTAs take whole ranges
-  int min_log2;        // a CTA's piece is at least 2^this units long where there are fewer than that for all
-  int* prefix;         // workspace [n_tiles + 1]: units per head before each tile, for the merge
+  int min_log2;        // a CTA's piece is at least 2^this long where there are fewer than that for all
+  int range_cost;      // of a range, beside its units'
+  int by_rows;         // the cost of a unit goes by the tile's vectors: cost[(vectors - 1) / 32]; else cost[0]
+  int cost[4];
+  Div cost_div[4];
+  int* prefix;         // workspace [n_tiles + 1]: cost per head before each tile, for the merge
   float* part;         // workspace: records of cut ranges, two per CTA
   float* spill;        // workspace: a warp's piece of a range that began before it (small kernel)
 };
@@ -109,7 +114,7 @@ PE_DEV int row_limit(const PackedAttnArgs& a, int p, bool& bad) {
 
 // The line in shared memory, each array of n_tiles (+ 1) entries.
 struct Layout {
-  int* prefix;  // units per head before the tile
+  int* prefix;  // cost per head before the tile
   int* last;    // largest position that the tile sees (-1: none)
   int* row0;    // its TileRows
   int* rows;
@@ -121,8 +126,12 @@ struct Layout {
   }
 };
 
-PE_DEV int tile_units(const Line& ln, const TileRows& t, int mx) {
-  return t.M == 0 ? 0 : max(1, (mx / kPackedPage + ln.unit_pages) >> (ln.unit_pages == 2 ? 1 : 2));
+PE_DEV int range_units(const Line& ln, int last) {  // at least one: a range that sees nothing has to be zeroed
+  return max(1, (last / kPackedPage + ln.unit_pages) >> (ln.unit_pages == 2 ? 1 : 2));
+}
+PE_DEV int cost_class(const Line& ln, int vectors) { return ln.by_rows ? (vectors - 1) >> 5 : 0; }
+PE_DEV int tile_cost(const Line& ln, const TileRows& t, int last) {
+  return t.M == 0 ? 0 : range_units(ln, last) * ln.cost[cost_class(ln, t.M)] + ln.range_cost;
 }
 
 // Fills the line in.  Every thread of the CTA.
@@ -160,7 +169,7 @@ PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, i
     for (int i = 0; i < W; ++i) {
       const int k = lane + 32 * i;
       if (32 * i >= n) break;
-      int inc = tile_units(ln, t[i], mx[i]);
+      int inc = tile_cost(ln, t[i], mx[i]);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
@@ -202,7 +211,7 @@ PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, i
     }
     for (int o = per >> 1; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
     if (k < n && sub == 0) {
-      lo.prefix[k + 1] = tile_units(ln, t, mx);
+      lo.prefix[k + 1] = tile_cost(ln, t, mx);
       lo.last[k] = mx;
       lo.row0[k] = t.r0;
       lo.rows[k] = t.M;
@@ -233,8 +242,8 @@ PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, i
   __syncthreads();
 }
 
-// T units in n equal pieces (the first T % n of them one longer): n is the grid, or less where that would
-// leave a piece shorter than 2^min_log2 units.
+// A line of length T in n equal pieces (the first T % n of them one longer): n is the grid, or less where
+// that would leave a piece shorter than 2^min_log2.
 struct Cuts {
   uint32_t n, q, r;
   PE_DEV Cuts(const Line& ln, int grid, uint32_t T) {
@@ -253,7 +262,7 @@ struct Cuts {
     }
   }
   PE_DEV uint32_t first(uint32_t c) const { return q * c + min(c, r); }
-  PE_DEV uint32_t piece(uint32_t u) const {  // the one that holds unit u
+  PE_DEV uint32_t piece(uint32_t u) const {  // the one that holds u
     const uint32_t longer = r * (q + 1);
     return u < longer ? small_quotient(u, q + 1) : r + small_quotient(u - longer, q);
   }
@@ -263,54 +272,78 @@ struct Cuts {
 struct Segment {
   int k, g;          // tile (of this launch), kv head
   int page0, page1;  // its pages
+  bool any;          // a unit starts in the piece
   bool from_start, to_end;
-  uint32_t next;     // the unit after it
+  uint32_t next;     // where the line goes on
 };
 
 struct Walk {
-  Layout lo;
-  int n_tiles, n_kv, unit_pages;
+  const Line& ln;
+  const Layout& lo;
+  int n_kv;
 
   PE_DEV int tile_of(uint32_t u) const {  // the last tile that starts at or before u (the whole warp)
     int at = 0;
     for (int step = 1024; step > 0; step >>= 5) {  // 32 places at a time: the 1024 tiles of a launch in three rounds
-      if (step > n_tiles) continue;
+      if (step > ln.n_tiles) continue;
       const int k = at + (int)(threadIdx.x & 31) * step;
-      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, k < n_tiles && (uint32_t)lo.prefix[min(k, n_tiles)] * n_kv <= u);
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, k < ln.n_tiles && (uint32_t)lo.prefix[min(k, ln.n_tiles)] * n_kv <= u);
       at += (31 - __clz(hit)) * step;
     }
     return at;
   }
   PE_DEV Segment at(int k, uint32_t u, uint32_t u1) const {
     Segment s;
-    const uint32_t p0 = lo.prefix[k], nb = lo.prefix[k + 1] - p0, r = u - p0 * n_kv;
+    const uint32_t p0 = lo.prefix[k], len = lo.prefix[k + 1] - p0;
+    uint32_t r = u - p0 * n_kv;
     s.k = k;
-    s.g = (int)small_quotient(r, nb);
-    const uint32_t blk = r - s.g * nb, cnt = min(nb - blk, u1 - u);
-    s.from_start = blk == 0;
-    s.to_end = blk + cnt == nb;
-    s.next = u + cnt;
-    s.page0 = (int)blk * unit_pages;
-    s.page1 = min((lo.last[k] + kPackedPage) / kPackedPage, (int)(blk + cnt) * unit_pages);
+    s.g = (int)small_quotient(r, len);
+    r -= s.g * len;
+    const uint32_t end = min(len, r + (u1 - u));
+    s.next = u + (end - r);
+    // unit i starts at range_cost + i * cost
+    const int cls = cost_class(ln, lo.rows[k]);
+    const uint32_t base = ln.range_cost, c = ln.cost[cls];
+    const int b0 = r <= base ? 0 : (int)((r - base + c - 1) / ln.cost_div[cls]);
+    const int b1 = end <= base ? 0 : (int)((end - base + c - 1) / ln.cost_div[cls]);
+    s.any = b1 > b0;
+    s.from_start = b0 == 0;
+    s.to_end = end > len - c;  // the last unit starts before `end`
+    s.page0 = b0 * ln.unit_pages;
+    s.page1 = min((lo.last[k] + kPackedPage) / kPackedPage, b1 * ln.unit_pages);
     return s;
   }
-  PE_DEV Segment after(const Segment& s, uint32_t u1) const {
+  // The first segment of [u, u1) with a unit, and the one behind `s`; false where there is none.
+  PE_DEV bool skip_empty(Segment& s, uint32_t u1) const {
+    while (!s.any)
+      if (!step(s, u1)) return false;
+    return true;
+  }
+  PE_DEV bool step(Segment& s, uint32_t u1) const {
+    if (s.next >= u1) return false;
     int k = s.k;
     if (s.next >= (uint32_t)lo.prefix[k + 1] * n_kv)
       do ++k;
       while (lo.prefix[k + 1] == lo.prefix[k]);
-    return at(k, s.next, u1);
+    s = at(k, s.next, u1);
+    return true;
   }
-  // The first unit of the range that holds unit u (u < T).
+  PE_DEV bool first(Segment& s, uint32_t u, uint32_t u1) const {
+    if (u >= u1) return false;
+    s = at(tile_of(u), u, u1);
+    return skip_empty(s, u1);
+  }
+  PE_DEV bool next(Segment& s, uint32_t u1) const { return step(s, u1) && skip_empty(s, u1); }
+  // The start of the range that holds u (u < T).
   PE_DEV uint32_t range_start(uint32_t u) const {
     const int k = tile_of(u);
-    const uint32_t p0 = lo.prefix[k], nb = lo.prefix[k + 1] - p0, r = u - p0 * n_kv;
-    return u - (r - small_quotient(r, nb) * nb);
+    const uint32_t p0 = lo.prefix[k], len = lo.prefix[k + 1] - p0, r = u - p0 * n_kv;
+    return u - (r - small_quotient(r, len) * len);
   }
 };
 
-// The units of this CTA: [u0, u1) of T.
-PE_DEV void cta_units(const Line& ln, const Walk& w, uint32_t T, uint32_t& u0, uint32_t& u1) {
+// The piece of this CTA: [u0, u1) of T.
+PE_DEV void cta_piece(const Line& ln, const Walk& w, uint32_t T, uint32_t& u0, uint32_t& u1) {
   u0 = u1 = 0;
   const Cuts cuts(ln, gridDim.x, T);
   if (T == 0 || blockIdx.x >= cuts.n) return;
@@ -353,6 +386,7 @@ PE_DEV float* part_record(const Line& ln, int cta, bool from_start) {
 // integer pipe.
 
 constexpr int kSmallWarps = 8;
+constexpr int kSmallRangeCost = 1;  // a range's start costs about as much as a pair of pages
 
 // A warp's part of a range that it shares with its neighbours: [ROWS][OROW] outputs, [ROWS] maxima, [ROWS]
 // sums, in its ring or (a part that began before the warp's piece, when more ranges follow) in the
@@ -464,12 +498,12 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   pdl_wait();
   pdl_trigger();
   lay_out(a, ln, lo, scratch);
-  const Walk walk{lo, ln.n_tiles, a.n_kv, ln.unit_pages};
+  const Walk walk{ln, lo, a.n_kv};
   const uint32_t total = (uint32_t)lo.prefix[ln.n_tiles] * a.n_kv;
   if (blockIdx.x == 0 && !ln.whole)
     for (int k = tid; k <= ln.n_tiles; k += blockDim.x) ln.prefix[k] = lo.prefix[k];
   uint32_t u0, u1;
-  cta_units(ln, walk, total, u0, u1);
+  cta_piece(ln, walk, total, u0, u1);
   if (u0 == u1) return;  // the whole CTA
   {
     const uint32_t n = u1 - u0;
@@ -482,9 +516,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   // Two walks over the pairs of pages of the warp's units, the copies `STAGES` pairs ahead of the
   // products.  A unit is a pair, so a pair lacks its second page at a range's end only, where every
   // position of that page is masked.
-  Segment ps{}, cs{};
-  bool p_done = u0 == u1;
-  if (!p_done) ps = cs = walk.at(walk.tile_of(u0), u0, u1);
+  Segment ps{}, cs;
+  const bool some = walk.first(ps, u0, u1);
+  bool p_done = !some;
+  cs = ps;
   int p_page = ps.page0;  // the next pair of the segment
   int ids = -1;           // page ids of the 16 pairs from p_page - p_id on, one per lane
   int p_id = 0;
@@ -494,11 +529,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   const uint32_t ring_end = stage_in + S::RING / kSmallWarps;
   auto issue = [&]() {
     while (p_page >= ps.page1) {
-      if (ps.next >= u1) {
+      if (!walk.next(ps, u1)) {
         p_done = true;
         return;
       }
-      ps = walk.after(ps, u1);
       p_page = ps.page0;
       p_id = 0;
       head = a.pool + (size_t)ps.g * L::kRecord + lane * 16;
@@ -545,7 +579,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   // rows 0..7 of a product stand for positions 0, 4, 1, 5, 2, 6, 3, 7 and rows 8..15 for 8 more, so that
   // the transposed P pairs positions t and t + 4
   const int kpos = (gr >> 1) + 4 * (gr & 1);
-  while (u0 != u1) {
+  while (some) {
     const TileRows tr = lo.tile(ln, cs.k);
     // offset of vector m of the sequence in the rows of q or out
     auto row_of = [&](int m, int g, long long stride) {
@@ -765,8 +799,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], w);
-    const bool ends = cs.next >= u1;
-    if (cs.from_start && cs.to_end) {
+    const Segment at = cs;
+    const bool ends = !walk.next(cs, u1);
+    if (at.from_start && at.to_end) {
       // a whole range: its rows, through the tables' shared memory (vectors' entries side by side)
       float* buf = reinterpret_cast<float*>(my_tab);
       constexpr int COLS = 8;  // entries of all the vectors at a time
@@ -796,7 +831,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
           if (v < tr.M) {
             const float2 x = *reinterpret_cast<const float2*>(buf + v * COLS + 2 * t);
             const int m = tr.m0 + v;
-            T* out = static_cast<T*>(a.out) + row_of(m, cs.g, a.out_stride) + 8 * j8 + 2 * t;
+            T* out = static_cast<T*>(a.out) + row_of(m, at.g, a.out_stride) + 8 * j8 + 2 * t;
             if constexpr (TERMS == 1) *reinterpret_cast<uint32_t*>(out) = pack_bf16(x.x, x.y);
             else *reinterpret_cast<float2*>(out) = x;
           }
@@ -825,14 +860,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
         }
       if (lane == 0) {
         Parts& p = parts[warp];
-        const int second = cs.from_start ? 1 : 0;
-        p.state |= second ? kSecond : kFirst | (cs.to_end ? kFirstEnds : 0) | (ends ? 0 : kFirstSpilled);
-        p.k[second] = cs.k;
-        p.g[second] = cs.g;
+        const int second = at.from_start ? 1 : 0;
+        p.state |= second ? kSecond : kFirst | (at.to_end ? kFirstEnds : 0) | (ends ? 0 : kFirstSpilled);
+        p.k[second] = at.k;
+        p.g[second] = at.g;
       }
     }
     if (ends) break;
-    cs = walk.after(cs, u1);
   }
   // ---- ranges shared by warps: each is a run of parts, one per warp, the first of which may have
   // begun before this CTA and the last of which may go on behind it
@@ -925,6 +959,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 // unpacking, 475 issue cycles, beside 256 cycles of MMA and 200 of HBM.
 
 constexpr int kTileRows = 128;
+// Costs on the line: a block's unpacking as much as the softmax of about 96 vectors, a range's start (queries,
+// filling the pipeline, output) as much as one or two blocks.
+constexpr int kTileUnitCost = 4, kTileRangeCost = 8;
 constexpr int kTileBlk = 64;
 constexpr int kTileThreads = 288;
 constexpr uint32_t kTileTmemCols = 256;
@@ -1015,12 +1052,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
   pdl_wait();
   pdl_trigger();
   lay_out(a, ln, lo, ctl->scratch);
-  const Walk walk{lo, ln.n_tiles, a.n_kv, ln.unit_pages};
+  const Walk walk{ln, lo, a.n_kv};
   const uint32_t total = (uint32_t)lo.prefix[ln.n_tiles] * a.n_kv;
   if (blockIdx.x == 0 && !ln.whole)
     for (int k = tid; k <= ln.n_tiles; k += blockDim.x) ln.prefix[k] = lo.prefix[k];
   uint32_t u0, u1;
-  cta_units(ln, walk, total, u0, u1);
+  cta_piece(ln, walk, total, u0, u1);
   if (u0 == u1) return;  // the whole CTA, before it holds anything
   if (tid == 0) {
     for (int s = 0; s < SK; ++s) {
@@ -1051,9 +1088,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
   auto blocks_of = [](const Segment& s) { return s.page1 > s.page0 ? (s.page1 - s.page0 + 3) >> 2 : 0; };
-  Segment seg = walk.at(walk.tile_of(u0), u0, u1);
+  Segment seg;
+  const bool some = walk.first(seg, u0, u1);
 
-  if (warp < 4) {
+  if (!some) {  // nothing starts here
+  } else if (warp < 4) {
     // ------------------------------------------------------------------ unpack
     const PairBits bits;
     const int row = lane >> 1, hc = lane & 1, prow = warp * 16 + row;  // the row in the page and in the block
@@ -1064,11 +1103,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
     auto fetch = [&](RawRow<HD>& r) -> bool {
       if (!more) return false;
       while (blk >= blocks_of(seg)) {
-        if (seg.next >= u1) {
+        if (!walk.next(seg, u1)) {
           more = false;
           return false;
         }
-        seg = walk.after(seg, u1);
         blk = 0;
       }
       if ((blk & 31) == 0) {  // page ids of 32 blocks, one per lane
@@ -1276,8 +1314,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
         gi += nblk;
         ++ii;
       }
-      if (seg.next >= u1) break;
-      seg = walk.after(seg, u1);
+      if (!walk.next(seg, u1)) break;
     }
     // TMEM is freed only after every MMA issued here has completed
     if (elect_one()) tc_commit(smem_u32(&ctl->drain));
@@ -1338,8 +1375,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
 #pragma unroll
           for (int c = 0; c < CH; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
         }
-        if (seg.next >= u1) break;
-        seg = walk.after(seg, u1);
+        if (!walk.next(seg, u1)) break;
         continue;
       }
       if (!staged) stage_q(seg);
@@ -1429,14 +1465,11 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
       }
       if (stop) break;
       const Segment done = seg;
-      const bool final = seg.next >= u1;
+      const bool final = !walk.next(seg, u1);
       // every S product of this segment has completed: the next one's query tile may go in
-      if (!final) {
-        seg = walk.after(seg, u1);
-        if (blocks_of(seg) > 0) {
-          stage_q(seg);
-          staged = true;
-        }
+      if (!final && blocks_of(seg) > 0) {
+        stage_q(seg);
+        staged = true;
       }
       gi += nblk;
       if (!warp_ok(mbar_wait(smem_u32(&ctl->pv_item), (uint32_t)ii & 1u, a.err, abort_flag, a.wait_ns))) break;
@@ -1510,8 +1543,9 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
   const TileRows tr = tile_rows(a, ln, ln.tile0 + k, bad);
   if (p1 == p0) return;
   const Cuts cuts(ln, grid, tot);
-  const uint32_t first = (uint32_t)p0 * a.n_kv + (uint32_t)g * (p1 - p0);
-  const int c0 = (int)cuts.piece(first), c1 = (int)cuts.piece(first + (p1 - p0) - 1);
+  const uint32_t len = p1 - p0, start = (uint32_t)p0 * a.n_kv + (uint32_t)g * len;
+  // the pieces in which its first and its last unit start
+  const int c0 = (int)cuts.piece(start + ln.range_cost), c1 = (int)cuts.piece(start + len - ln.cost[cost_class(ln, tr.M)]);
   if (c0 == c1) return;  // finished by its CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp & (split - 1), per = 8 / split;  // vectors at a time
@@ -1626,9 +1660,15 @@ cudaError_t launch_merge(const PackedAttnArgs& a, const Line& ln, int grid, int 
                     a, ln, grid, split);
 }
 
+// The longest that a range can be.
+long long line_length(const PackedAttnArgs& a, const Line& ln) {
+  return (long long)((a.max_pages + ln.unit_pages - 1) / ln.unit_pages) * ln.cost[ln.by_rows ? (ln.tile_rows - 1) / 32 : 0] + ln.range_cost;
+}
+
 // The launch's line for tiles of `tile_rows` vectors and units of `unit_pages`, and how many of its tiles one
 // launch takes (their units, counted in 32 bits, and kPlanTiles bound it).
-Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_log2, int* tiles_per_launch) {
+Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_log2, int range_cost, int unit_cost, int by_rows,
+               int* tiles_per_launch) {
   const int G = a.n_q / a.n_kv;
   const long long vectors = (long long)a.max_rows * G;
   Line ln{};
@@ -1645,23 +1685,27 @@ Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_l
   const int rows = std::min(a.max_rows, tile_rows / G + 2);
   ln.lanes = 1;
   while (ln.lanes < 32 && ln.lanes * 4 < rows) ln.lanes *= 2;
-  const long long units = (long long)a.n_kv * ((a.max_pages + unit_pages - 1) / unit_pages);  // of a tile, at most
-  *tiles_per_launch = (int)std::min<long long>(kPlanTiles, std::max(1LL, ((1LL << 31) - 1) / units));
+  ln.range_cost = range_cost;
+  ln.by_rows = by_rows;
+  for (int i = 0; i < 4; ++i) {
+    ln.cost[i] = unit_cost + (by_rows ? i : 0);
+    ln.cost_div[i] = make_div(ln.cost[i]);
+  }
+  *tiles_per_launch = (int)std::min<long long>(kPlanTiles, std::max(1LL, ((1LL << 31) - 1) / (line_length(a, ln) * a.n_kv)));
   return ln;
 }
 
 // CTAs of a launch: no more than the tables' positions could keep busy (whole ranges: one each).
 int line_grid(const PackedAttnArgs& a, const Line& ln, int most) {
   const long long ranges = (long long)ln.n_tiles * a.n_kv;
-  const long long units = ranges * ((a.max_pages + ln.unit_pages - 1) / ln.unit_pages);
-  return (int)std::min<long long>(most, std::max(1LL, ln.whole ? ranges : units >> ln.min_log2));
+  return (int)std::min<long long>(most, std::max(1LL, ln.whole ? ranges : (ranges * line_length(a, ln)) >> ln.min_log2));
 }
 
 template <typename T, int HD, int NQ>
 cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Small<T, HD, NQ>;
   int per_launch = 0;
-  Line ln = make_line(a, C::ROWS, 2, 3, &per_launch);
+  Line ln = make_line(a, C::ROWS, 2, 3, kSmallRangeCost, 1, 0, &per_launch);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ln.prefix = reinterpret_cast<int*>(ws);
   ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
@@ -1685,7 +1729,7 @@ template <int HD>
 cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Tile<HD>;
   int per_launch = 0;
-  Line ln = make_line(a, kTileRows, 4, 1, &per_launch);
+  Line ln = make_line(a, kTileRows, 4, 4, kTileRangeCost, kTileUnitCost, 1, &per_launch);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ln.prefix = reinterpret_cast<int*>(ws);
   ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
