@@ -946,13 +946,13 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 // A tile of up to 128 query vectors (bf16) against blocks of 64 positions: S = Q K^T and O += P V on
 // the 5th-generation tensor core, S and O in tensor memory, P written over S as bf16.  One unpacked
 // block serves all 128 vectors.  Roles of a CTA (two CTAs per SM):
-//   warps 0..3  unpack: each takes one page of a block, a row (position) per two lanes, from registers
+//   warp 0      issues the MMAs: a block's PV once P and the values are there, then the S that reuses its
+//               buffer, NB blocks on.
+//   warps 1..3, 8 unpack: each takes one page of a block, a row (position) per two lanes, from registers
 //               that were loaded two blocks ahead, into the K and V rings (128-byte swizzle).
 //               Entries stay in the order of the cache's words: K's is a permutation of the
 //               contraction, given to Q as well; V's one of O's columns, undone on output.
 //   warps 4..7  softmax and output: one thread per query vector (TMEM lane).
-//   warp 8      issues the MMAs: S of a block as soon as its keys are there, up to NB - 1 blocks ahead
-//               of the softmax; PV as soon as P and the values are.
 // A vector's reference maximum only moves when a block exceeds it by 2^8; then O is rescaled in TMEM.
 //
 // Bound (head_dim 64): per block of 64 positions about 1300 warp instructions of softmax and 600 of
@@ -965,7 +965,6 @@ constexpr int kTileUnitCost = 4, kTileRangeCost = 8;
 constexpr int kTileBlk = 64;
 constexpr int kTileThreads = 288;
 constexpr uint32_t kTileTmemCols = 256;
-constexpr uint32_t kTilePollNs = 100;  // longest sleep of the MMA warp on one input
 
 template <int HD>
 struct Tile {
@@ -979,9 +978,9 @@ struct Tile {
 };
 
 struct TileCtrl {
-  uint64_t kfull[3], kempty[3], vfull[3], vempty[3];  // full: an arrival per unpacking warp; empty: the MMAs read it
+  uint64_t kfull[3], vfull[3], vempty[3];  // full: an arrival per unpacking warp; empty: the PV product has read it
   uint64_t q_full;                 // the item's query tile is staged
-  uint64_t s_full[3], p_full[3];   // S of a block is in its buffer; P is (and O rescaled where needed)
+  uint64_t s_full[3], p_full[3];   // S of a block is in its buffer (its keys are read); P is (O rescaled where needed)
   uint64_t pv_item, o_free;        // the item's last PV has completed; its O has been read
   uint64_t drain;
   int scratch[12];
@@ -1041,6 +1040,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
   constexpr int SK = C::SK, SV = C::SV, NB = C::NB;
   constexpr uint32_t TO = C::TO;
   static_assert(SV >= NB - 1, "a value stage's release orders the PV product a rescale waits for");
+  static_assert(SK == NB, "S in its buffer tells that the stage's keys have been read");
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_u32(sm);
@@ -1062,7 +1062,6 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
   if (tid == 0) {
     for (int s = 0; s < SK; ++s) {
       mbar_init(smem_u32(&ctl->kfull[s]), 4);
-      mbar_init(smem_u32(&ctl->kempty[s]), 1);
     }
     for (int s = 0; s < SV; ++s) {
       mbar_init(smem_u32(&ctl->vfull[s]), 4);
@@ -1079,7 +1078,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
     ctl->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == 0) {
     tmem_alloc(smem_u32(&ctl->tmem), kTileTmemCols);
     tmem_relinquish();
     tc_fence_before();
@@ -1092,10 +1091,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
   const bool some = walk.first(seg, u0, u1);
 
   if (!some) {  // nothing starts here
-  } else if (warp < 4) {
+  } else if (warp == 8 || (warp > 0 && warp < 4)) {
     // ------------------------------------------------------------------ unpack
     const PairBits bits;
-    const int row = lane >> 1, hc = lane & 1, prow = warp * 16 + row;  // the row in the page and in the block
+    const int row = lane >> 1, hc = lane & 1, pw = warp & 3, prow = pw * 16 + row;  // the row in the page and in the block
     const uint32_t step = (uint32_t)a.n_kv * L::kRecord;
     int blk = 0, ids = -1;
     bool more = true;
@@ -1110,7 +1109,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
         blk = 0;
       }
       if ((blk & 31) == 0) {  // page ids of 32 blocks, one per lane
-        const int x = seg.page0 + 4 * (blk + lane) + warp;
+        const int x = seg.page0 + 4 * (blk + lane) + pw;
         ids = -1;
         if (x < seg.page1) {
           ids = __ldcg(a.block_table + (size_t)((uint32_t)(ln.tile0 + seg.k) / ln.tps) * a.max_pages + x);
@@ -1147,7 +1146,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
     auto unpack = [&](const RawRow<HD>& r) -> bool {
       {
         const int s = gi % SK;
-        if (gi >= SK && !warp_ok(mbar_wait(smem_u32(&ctl->kempty[s]), ((uint32_t)(gi / SK) & 1u) ^ 1u, a.err, abort_flag, a.wait_ns)))
+        if (gi >= SK && !warp_ok(mbar_wait(smem_u32(&ctl->s_full[s]), ((uint32_t)(gi / SK) & 1u) ^ 1u, a.err, abort_flag, a.wait_ns)))
           return false;
         const uint32_t base = sQ + C::KRING + (uint32_t)s * C::KV;
         // word w of the row: entries 4t..4t+3 of blocks 2u and 2u + 1, unit w of the tile's row
@@ -1216,106 +1215,64 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
       if (!unpack(r1)) break;
       ok1 = fetch(r1);
     }
-  } else if (warp == 8) {
+  } else if (warp == 0) {
     // ------------------------------------------------------------------ MMA issuer (a converged warp)
-    const uint32_t id_s = idesc_bf16(kTileRows, kTileBlk);               // N = positions
-    const uint32_t id_o = idesc_bf16(kTileRows, HD) | kIdescTransposeB;  // V is MN-major
+    constexpr uint32_t kIdS = idesc_bf16(kTileRows, kTileBlk);               // N = positions
+    constexpr uint32_t kIdO = idesc_bf16(kTileRows, HD) | kIdescTransposeB;  // V is MN-major
+    const uint64_t dq = sdesc_k_sw128(sQ), dk = sdesc_k_sw128(sQ + C::KRING), dv = sdesc_mn_sw128(sQ + C::VRING, kTileBlk * 128);
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      return warp_ok(mbar_wait(smem_u32(bar), phase & 1u, a.err, abort_flag, a.wait_ns));
+    };
+    // The products run in the order of their issue: an S after the PV whose P it overwrites.
+    auto issue_s = [&](int x) -> bool {
+      const int s = x % SK;
+      if (!wait(&ctl->kfull[s], (uint32_t)(x / SK))) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t bk = dk + (uint64_t)((uint32_t)s * (C::KV >> 4));
+        const uint32_t d = tmem + (uint32_t)(s * kTileBlk);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          tc_mma_bf16(d, dq + ((kk >> 2) * (kTileRows * 128 >> 4) + 2 * (kk & 3)),
+                      bk + ((kk >> 2) * (kTileBlk * 128 >> 4) + 2 * (kk & 3)), kIdS, kk > 0 ? 1u : 0u);
+        tc_commit(smem_u32(&ctl->s_full[s]));
+      }
+      __syncwarp();
+      return true;
+    };
     int gi = 0, ii = 0;
     bool stop = false;
-    for (;;) {
+    do {
       const int nblk = blocks_of(seg);
-      if (nblk > 0) {
-        if (!warp_ok(mbar_wait(smem_u32(&ctl->q_full), (uint32_t)ii & 1u, a.err, abort_flag, a.wait_ns))) break;
-        tc_fence_after();
-        // Two streams, issued as their inputs arrive: S of block ns once its keys are there and its
-        // buffer is free (the PV of block ns - NB is issued), and the PV of block np once its P and
-        // its values are (the item's first, which overwrites O, once the last item's O has been read).
-        int ns = 0, np = 0;
-        bool o_ok = ii == 0;
-        uint64_t t_idle = 0;
-        uint32_t n_idle = 0;
-        while (np < nblk) {
-          bool prog = false;
-          if (ns < nblk && ns <= np + NB - 1) {
-            const int x = gi + ns, s = x % SK;
-            if (warp_ok(mbar_test_wait(smem_u32(&ctl->kfull[s]), (uint32_t)(x / SK) & 1u))) {
-              tc_fence_after();
-              if (elect_one()) {
-                const uint32_t kbase = sQ + C::KRING + (uint32_t)s * C::KV;
-                const uint32_t d = tmem + (uint32_t)((x % NB) * kTileBlk);
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                  const uint64_t ad = sdesc_k_sw128(sQ + (uint32_t)((kk >> 2) * kTileRows * 128)) + 2 * (kk & 3);
-                  const uint64_t bd = sdesc_k_sw128(kbase + (uint32_t)((kk >> 2) * kTileBlk * 128)) + 2 * (kk & 3);
-                  tc_mma_bf16(d, ad, bd, id_s, kk > 0 ? 1u : 0u);
-                }
-                tc_commit(smem_u32(&ctl->s_full[x % NB]));
-                tc_commit(smem_u32(&ctl->kempty[s]));
-              }
-              __syncwarp();
-              ++ns;
-              prog = true;
-            }
-          }
-          if (np < ns) {
-            const int x = gi + np, s = x % SV;
-            if (!o_ok) o_ok = warp_ok(mbar_test_wait(smem_u32(&ctl->o_free), (uint32_t)(ii - 1) & 1u));
-            if (o_ok && warp_ok(mbar_test_wait(smem_u32(&ctl->p_full[x % NB]), (uint32_t)(x / NB) & 1u) &&
-                                mbar_test_wait(smem_u32(&ctl->vfull[s]), (uint32_t)(x / SV) & 1u))) {
-              tc_fence_after();
-              if (elect_one()) {
-                const uint32_t vbase = sQ + C::VRING + (uint32_t)s * C::KV;
-                const uint32_t pa = tmem + (uint32_t)((x % NB) * kTileBlk);
-#pragma unroll
-                for (int kk = 0; kk < kTileBlk / 16; ++kk)
-                  tc_mma_bf16_tmem_a(tmem + TO, pa + 8u * kk, sdesc_mn_sw128(vbase + (uint32_t)kk * 2048u, kTileBlk * 128),
-                                     id_o, (np > 0 || kk > 0) ? 1u : 0u);
-                if (np == nblk - 1) tc_commit(smem_u32(&ctl->pv_item));
-                tc_commit(smem_u32(&ctl->vempty[s]));
-              }
-              __syncwarp();
-              ++np;
-              prog = true;
-            }
-          }
-          if (prog) {
-            n_idle = 0;
-            continue;
-          }
-          if ((n_idle++ & 7) == 0) {  // a bounded wait: give up when another role did, or after the limit
-            if (*abort_flag) {
-              stop = true;
-              break;
-            }
-            const uint64_t now = global_timer_ns();
-            if (n_idle == 1) {
-              t_idle = now;
-            } else if (now - t_idle > a.wait_ns) {
-              if (elect_one()) {
-                set_err(a.err, PE_DEV_TIMEOUT);
-                *abort_flag = 1;
-              }
-              __syncwarp();
-              stop = true;
-              break;
-            }
-          }
-          // sleep on the input most likely to come next (a hot loop would take issue slots from the others)
-          if (np < ns) {
-            const int x = gi + np;
-            mbar_try_wait_for(smem_u32(&ctl->p_full[x % NB]), (uint32_t)(x / NB) & 1u, kTilePollNs);
-          } else if (ns < nblk) {
-            const int x = gi + ns;
-            mbar_try_wait_for(smem_u32(&ctl->kfull[x % SK]), (uint32_t)(x / SK) & 1u, kTilePollNs);
-          }
-          __syncwarp();
+      if (nblk == 0) continue;
+      stop = !wait(&ctl->q_full, (uint32_t)ii);
+      tc_fence_after();
+      for (int j = 0; j < NB && j < nblk && !stop; ++j) stop = !issue_s(gi + j);
+#pragma unroll 1
+      for (int j = 0; j < nblk && !stop; ++j) {
+        const int x = gi + j, s = x % SV, b = x % NB;
+        // the item's first PV overwrites O: the last item's has to have been read
+        if (!wait(&ctl->vfull[s], (uint32_t)(x / SV)) || !wait(&ctl->p_full[b], (uint32_t)(x / NB)) ||
+            (j == 0 && ii > 0 && !wait(&ctl->o_free, (uint32_t)(ii - 1)))) {
+          stop = true;
+          break;
         }
-        if (stop) break;
-        gi += nblk;
-        ++ii;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t bv = dv + (uint64_t)((uint32_t)s * (C::KV >> 4));
+          const uint32_t pa = tmem + (uint32_t)(b * kTileBlk);
+#pragma unroll
+          for (int kk = 0; kk < kTileBlk / 16; ++kk)
+            tc_mma_bf16_tmem_a(tmem + TO, pa + 8u * kk, bv + kk * (2048 >> 4), kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+          if (j == nblk - 1) tc_commit(smem_u32(&ctl->pv_item));
+          tc_commit(smem_u32(&ctl->vempty[s]));
+        }
+        __syncwarp();
+        if (j + NB < nblk) stop = !issue_s(x + NB);
       }
-      if (!walk.next(seg, u1)) break;
-    }
+      gi += nblk;
+      ++ii;
+    } while (!stop && walk.next(seg, u1));
     // TMEM is freed only after every MMA issued here has completed
     if (elect_one()) tc_commit(smem_u32(&ctl->drain));
     __syncwarp();
@@ -1516,7 +1473,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
     }
   }
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, kTileTmemCols);
   }
