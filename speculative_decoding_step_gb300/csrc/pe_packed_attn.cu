@@ -946,48 +946,58 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 // A tile of up to 128 query vectors (bf16) against blocks of 64 positions: S = Q K^T and O += P V on
 // the 5th-generation tensor core, S and O in tensor memory, P written over S as bf16.  One unpacked
 // block serves all 128 vectors.  Roles of a CTA (two CTAs per SM):
-//   warp 0      issues the MMAs: a block's PV once P and the values are there, then the S that reuses its
-//               buffer, NB blocks on.
-//   warps 1..3, 8 unpack: each takes one page of a block, a row (position) per two lanes, from registers
-//               that were loaded two blocks ahead, into the K and V rings (128-byte swizzle).
-//               Entries stay in the order of the cache's words: K's is a permutation of the
-//               contraction, given to Q as well; V's one of O's columns, undone on output.
-//   warps 4..7  softmax and output: one thread per query vector (TMEM lane).
+//   one warp     issues the MMAs: a block's PV once P is there, then the S that reuses its buffer, two
+//                blocks on.
+//   four warps   unpack: each takes one page of a block, a row (position) per two lanes, from a ring of its
+//                own that asynchronous copies fill ahead, into the K and V rings (128-byte swizzle).
+//                Entries stay in the order of the cache's words: K's is a permutation of the
+//                contraction, given to Q as well; V's one of O's columns, undone on output.
+//   four warps per stream do the softmax, one thread per query vector (TMEM lane).  head_dim 64: two streams,
+//                the even and the odd blocks, each with its own statistics and its own O, that meet at the
+//                item's end (one stream's softmax alone took 1500 cycles a block, mostly waiting for itself:
+//                two warps of a scheduler do not hide it).  head_dim 128: one, tensor memory holds no second O.
 // A vector's reference maximum only moves when a block exceeds it by 2^8; then O is rescaled in TMEM.
 //
-// Bound (head_dim 64): per block of 64 positions about 1300 warp instructions of softmax and 600 of
-// unpacking, 475 issue cycles, beside 256 cycles of MMA and 200 of HBM.
+// Bound (head_dim 64): per block of 64 positions about 1100 warp instructions of softmax and 900 of
+// unpacking, 500 issue cycles, beside 256 cycles of MMA and 200 of HBM.
 
 constexpr int kTileRows = 128;
 // Costs on the line: a block's unpacking as much as the softmax of about 96 vectors, a range's start (queries,
 // filling the pipeline, output) as much as one or two blocks.
 constexpr int kTileUnitCost = 4, kTileRangeCost = 8;
 constexpr int kTileBlk = 64;
-constexpr int kTileThreads = 288;
-constexpr uint32_t kTileTmemCols = 256;
+constexpr uint32_t kTileTmemCols = 256;  // two S buffers, then O
 
 template <int HD>
 struct Tile {
-  static constexpr int SK = HD == 64 ? 3 : 2, SV = SK;  // stages of the K and V rings
-  static constexpr int NB = HD == 64 ? 3 : 2;           // S buffers: NB * 64 columns and O's HD fill the 256
-  static constexpr uint32_t TO = NB * kTileBlk;         // first column of O
+  static constexpr int STREAMS = HD == 64 ? 2 : 1;
+  static constexpr int SOFTMAX = 128 * STREAMS;       // threads
+  static constexpr int THREADS = 160 + SOFTMAX;       // warp 0: MMA; 1..3 and the last: unpack; 4..: softmax
+  static constexpr int ST = HD == 64 ? 3 : 2;         // stages of keys and values
+  static constexpr int RAW = HD == 64 ? 4 : 1;        // pages ahead of each unpacking warp
+  static constexpr int QB = HD == 64 ? 2 : 1;         // query tiles
+  static constexpr uint32_t TO = 2 * kTileBlk;        // first column of O (of the first stream's)
   static constexpr uint32_t Q = kTileRows * HD * 2, KV = kTileBlk * HD * 2;
-  static constexpr uint32_t KRING = Q, VRING = KRING + SK * KV, CTRL = VRING + SV * KV;
-  static constexpr uint32_t FIXED = CTRL + 512;
+  static constexpr uint32_t KRING = QB * Q, VRING = KRING + ST * KV, RAWS = VRING + ST * KV;
+  static constexpr uint32_t CTRL = RAWS + 4 * RAW * PackedLayout<HD>::kRecord;
+  static constexpr uint32_t STATS = CTRL + 256;       // two streams: [items in turn][streams][maximum, sum][128]
+  static constexpr uint32_t FIXED = STATS + (STREAMS == 2 ? 8 * kTileRows * 4 : 0);
   static size_t smem(int n_tiles) { return 1024 + FIXED + Layout::kBytesPerTile * (size_t)n_tiles + 4; }
 };
 
 struct TileCtrl {
-  uint64_t kfull[3], vfull[3], vempty[3];  // full: an arrival per unpacking warp; empty: the PV product has read it
+  uint64_t kfull[3], vfull[3];     // an arrival per unpacking warp
+  uint64_t vempty[3];              // the block's PV product has completed
+  uint64_t s_full[2], p_full[2];   // S of a block is in its buffer (and its keys are read); P is (O rescaled where needed)
   uint64_t q_full;                 // the item's query tile is staged
-  uint64_t s_full[3], p_full[3];   // S of a block is in its buffer (its keys are read); P is (O rescaled where needed)
   uint64_t pv_item, o_free;        // the item's last PV has completed; its O has been read
+  uint64_t pair[4];                // either stream's warp of 32 vectors has given its statistics
   uint64_t drain;
-  int scratch[12];
+  int scratch[16];
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(TileCtrl) <= 512, "");
+static_assert(sizeof(TileCtrl) <= 256, "");
 
 // 16-byte unit c of row r of a shared-memory tile [HD/64][ROWS][64 bf16], 128-byte swizzle.
 template <int ROWS>
@@ -997,13 +1007,10 @@ PE_DEV uint32_t unit_addr(uint32_t base, int row, int c) {
 PE_DEV void st_shared16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-
-// What a lane unpacks of a page: half a row of key and of value codes, and the row's scales.
-template <int HD>
-struct RawRow {
-  uint4 k[HD / 64], v[HD / 64];
-  uint32_t ks[HD / 64], vs[HD / 64];
-};
+// 8 bytes, or zeros where `bytes` is 0.
+PE_DEV void copy8(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 
 // Two fp32 values in one 64-bit register, for the packed fp32 instructions.
 struct F2 {
@@ -1032,15 +1039,29 @@ struct F2 {
   }
 };
 
+// 32 consecutive fp32 columns of this thread's TMEM lane, waited on.
+PE_DEV void tmem_load32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 template <int HD>
-__global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const PackedAttnArgs a, const Line ln) {
+__global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const PackedAttnArgs a, const Line ln) {
   using C = Tile<HD>;
   using L = PackedLayout<HD>;
-  constexpr int H = HD / 64, CH = HD / 8;
-  constexpr int SK = C::SK, SV = C::SV, NB = C::NB;
-  constexpr uint32_t TO = C::TO;
-  static_assert(SV >= NB - 1, "a value stage's release orders the PV product a rescale waits for");
-  static_assert(SK == NB, "S in its buffer tells that the stage's keys have been read");
+  constexpr int H = HD / 64, CH = HD / 8, ST = C::ST;
+  constexpr bool TWO = C::STREAMS == 2;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_u32(sm);
@@ -1060,20 +1081,19 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
   cta_piece(ln, walk, total, u0, u1);
   if (u0 == u1) return;  // the whole CTA, before it holds anything
   if (tid == 0) {
-    for (int s = 0; s < SK; ++s) {
+    for (int s = 0; s < ST; ++s) {
       mbar_init(smem_u32(&ctl->kfull[s]), 4);
-    }
-    for (int s = 0; s < SV; ++s) {
       mbar_init(smem_u32(&ctl->vfull[s]), 4);
       mbar_init(smem_u32(&ctl->vempty[s]), 1);
     }
-    mbar_init(smem_u32(&ctl->q_full), 4);
-    for (int b = 0; b < NB; ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&ctl->s_full[b]), 1);
       mbar_init(smem_u32(&ctl->p_full[b]), 4);
     }
+    for (int q = 0; q < 4; ++q) mbar_init(smem_u32(&ctl->pair[q]), 2);
+    mbar_init(smem_u32(&ctl->q_full), C::SOFTMAX / 32);
     mbar_init(smem_u32(&ctl->pv_item), 1);
-    mbar_init(smem_u32(&ctl->o_free), 4);
+    mbar_init(smem_u32(&ctl->o_free), C::SOFTMAX / 32);
     mbar_init(smem_u32(&ctl->drain), 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -1087,155 +1107,37 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
   auto blocks_of = [](const Segment& s) { return s.page1 > s.page0 ? (s.page1 - s.page0 + 3) >> 2 : 0; };
+  auto wait = [&](uint64_t* bar, uint32_t phase) {
+    return warp_ok(mbar_wait(smem_u32(bar), phase & 1u, a.err, abort_flag, a.wait_ns));
+  };
+  auto arrive = [&](uint64_t* bar) {  // one arrival per warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(bar));
+  };
+  // Blocks are counted through the CTA's segments: block x uses stage x % ST and S buffer x % 2.
   Segment seg;
   const bool some = walk.first(seg, u0, u1);
 
   if (!some) {  // nothing starts here
-  } else if (warp == 8 || (warp > 0 && warp < 4)) {
-    // ------------------------------------------------------------------ unpack
-    const PairBits bits;
-    const int row = lane >> 1, hc = lane & 1, pw = warp & 3, prow = pw * 16 + row;  // the row in the page and in the block
-    const uint32_t step = (uint32_t)a.n_kv * L::kRecord;
-    int blk = 0, ids = -1;
-    bool more = true;
-    // the next block's rows, over the segments; false behind the last
-    auto fetch = [&](RawRow<HD>& r) -> bool {
-      if (!more) return false;
-      while (blk >= blocks_of(seg)) {
-        if (!walk.next(seg, u1)) {
-          more = false;
-          return false;
-        }
-        blk = 0;
-      }
-      if ((blk & 31) == 0) {  // page ids of 32 blocks, one per lane
-        const int x = seg.page0 + 4 * (blk + lane) + pw;
-        ids = -1;
-        if (x < seg.page1) {
-          ids = __ldcg(a.block_table + (size_t)((uint32_t)(ln.tile0 + seg.k) / ln.tps) * a.max_pages + x);
-          if (ids < 0 || ids >= a.num_pages) {
-            set_err(a.err, PE_DEV_BAD_PAGE);
-            ids = -1;
-          }
-        }
-      }
-      const int id = __shfl_sync(0xFFFFFFFFu, ids, blk & 31);
-      ++blk;
-      if (id >= 0) {
-        const uint8_t* rec = a.pool + (uint64_t)(uint32_t)id * step + (size_t)seg.g * L::kRecord;
-#pragma unroll
-        for (int c = 0; c < H; ++c) {
-          r.k[c] = __ldcg(reinterpret_cast<const uint4*>(rec + L::kK + row * L::kRow + (hc + 2 * c) * 16));
-          r.v[c] = __ldcg(reinterpret_cast<const uint4*>(rec + L::kV + row * L::kRow + (H * hc + c) * 16));
-        }
-#pragma unroll
-        for (int c = 0; c < H; ++c) {
-          r.ks[c] = __ldcg(reinterpret_cast<const uint32_t*>(rec + L::kKs + row * L::kScaleRow) + c);
-          r.vs[c] = __ldcg(reinterpret_cast<const uint32_t*>(rec + L::kVs + row * L::kScaleRow) + c);
-        }
-      } else {  // a page behind the range or outside the pool: zeros
-#pragma unroll
-        for (int c = 0; c < H; ++c) {
-          r.k[c] = r.v[c] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-          r.ks[c] = r.vs[c] = 0;
-        }
-      }
-      return true;
-    };
-    int gi = 0;
-    auto unpack = [&](const RawRow<HD>& r) -> bool {
-      {
-        const int s = gi % SK;
-        if (gi >= SK && !warp_ok(mbar_wait(smem_u32(&ctl->s_full[s]), ((uint32_t)(gi / SK) & 1u) ^ 1u, a.err, abort_flag, a.wait_ns)))
-          return false;
-        const uint32_t base = sQ + C::KRING + (uint32_t)s * C::KV;
-        // word w of the row: entries 4t..4t+3 of blocks 2u and 2u + 1, unit w of the tile's row
-        uint32_t sp[2 * 2 * H], zp[2 * 2 * H];
-#pragma unroll
-        for (int j = 0; j < 4 * H; ++j) {
-          sp[j] = packed_scale_lo(__byte_perm(r.ks[j / 4], 0, 0x4040 + 0x0101 * (j & 3)));
-          zp[j] = bf16x2_mul(sp[j], kMinus136);
-        }
-#pragma unroll
-        for (int c = 0; c < H; ++c) {
-          const uint32_t w4[4] = {r.k[c].x, r.k[c].y, r.k[c].z, r.k[c].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int u = HD == 64 ? i & 1 : i;  // word 4 (hc + 2c) + i = t * HD/32 + u
-            st_shared16(unit_addr<kTileBlk>(base, prow, 4 * (hc + 2 * c) + i),
-                        bf16x2_fma(bits.pair<0>(w4[i]), sp[2 * u], zp[2 * u]), bf16x2_fma(bits.pair<1>(w4[i]), sp[2 * u], zp[2 * u]),
-                        bf16x2_fma(bits.pair<2>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]),
-                        bf16x2_fma(bits.pair<3>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]));
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->kfull[s]));
-      }
-      {
-        const int s = gi % SV;
-        if (gi >= SV && !warp_ok(mbar_wait(smem_u32(&ctl->vempty[s]), ((uint32_t)(gi / SV) & 1u) ^ 1u, a.err, abort_flag, a.wait_ns)))
-          return false;
-        const uint32_t base = sQ + C::VRING + (uint32_t)s * C::KV;
-        // word (g, h): entries g and g + 8 of four blocks, pairs 32 entries apart; unit g of the h-th 64 columns
-        uint32_t sp[H][2], zp[H][2];
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          sp[h][0] = packed_scale_lo(r.vs[h]);
-          sp[h][1] = packed_scale_hi(r.vs[h]);
-          zp[h][0] = bf16x2_mul(sp[h][0], kMinus136);
-          zp[h][1] = bf16x2_mul(sp[h][1], kMinus136);
-        }
-#pragma unroll
-        for (int c = 0; c < H; ++c) {
-          const uint32_t w4[4] = {r.v[c].x, r.v[c].y, r.v[c].z, r.v[c].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int h = HD == 64 ? 0 : i & 1;  // word 4 (H hc + c) + i = g * H + h
-            const int g = HD == 64 ? 4 * hc + i : 2 * (2 * hc + c) + (i >> 1);
-            st_shared16(unit_addr<kTileBlk>(base, prow, 8 * h + g),
-                        bf16x2_fma(bits.pair<0>(w4[i]), sp[h][0], zp[h][0]), bf16x2_fma(bits.pair<1>(w4[i]), sp[h][0], zp[h][0]),
-                        bf16x2_fma(bits.pair<2>(w4[i]), sp[h][1], zp[h][1]), bf16x2_fma(bits.pair<3>(w4[i]), sp[h][1], zp[h][1]));
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->vfull[s]));
-      }
-      ++gi;
-      return true;
-    };
-    RawRow<HD> r0, r1;
-    bool ok0 = fetch(r0), ok1 = fetch(r1);
-#pragma unroll 1
-    while (ok0) {
-      if (!unpack(r0)) break;
-      ok0 = fetch(r0);
-      if (!ok1) break;
-      if (!unpack(r1)) break;
-      ok1 = fetch(r1);
-    }
   } else if (warp == 0) {
     // ------------------------------------------------------------------ MMA issuer (a converged warp)
     constexpr uint32_t kIdS = idesc_bf16(kTileRows, kTileBlk);               // N = positions
     constexpr uint32_t kIdO = idesc_bf16(kTileRows, HD) | kIdescTransposeB;  // V is MN-major
-    const uint64_t dq = sdesc_k_sw128(sQ), dk = sdesc_k_sw128(sQ + C::KRING), dv = sdesc_mn_sw128(sQ + C::VRING, kTileBlk * 128);
-    auto wait = [&](uint64_t* bar, uint32_t phase) {
-      return warp_ok(mbar_wait(smem_u32(bar), phase & 1u, a.err, abort_flag, a.wait_ns));
-    };
+    const uint64_t dk = sdesc_k_sw128(sQ + C::KRING), dv = sdesc_mn_sw128(sQ + C::VRING, kTileBlk * 128);
+    uint64_t dq = 0;
     // The products run in the order of their issue: an S after the PV whose P it overwrites.
     auto issue_s = [&](int x) -> bool {
-      const int s = x % SK;
-      if (!wait(&ctl->kfull[s], (uint32_t)(x / SK))) return false;
+      const int s = x % ST;
+      if (!wait(&ctl->kfull[s], (uint32_t)(x / ST))) return false;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t bk = dk + (uint64_t)((uint32_t)s * (C::KV >> 4));
-        const uint32_t d = tmem + (uint32_t)(s * kTileBlk);
+        const uint32_t d = tmem + (uint32_t)((x & 1) * kTileBlk);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
           tc_mma_bf16(d, dq + ((kk >> 2) * (kTileRows * 128 >> 4) + 2 * (kk & 3)),
                       bk + ((kk >> 2) * (kTileBlk * 128 >> 4) + 2 * (kk & 3)), kIdS, kk > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&ctl->s_full[s]));
+        tc_commit(smem_u32(&ctl->s_full[x & 1]));
       }
       __syncwarp();
       return true;
@@ -1246,13 +1148,13 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
       const int nblk = blocks_of(seg);
       if (nblk == 0) continue;
       stop = !wait(&ctl->q_full, (uint32_t)ii);
-      tc_fence_after();
-      for (int j = 0; j < NB && j < nblk && !stop; ++j) stop = !issue_s(gi + j);
+      dq = sdesc_k_sw128(sQ + (C::QB == 2 && (ii & 1) ? C::Q : 0));
+      for (int j = 0; j < 2 && j < nblk && !stop; ++j) stop = !issue_s(gi + j);
 #pragma unroll 1
       for (int j = 0; j < nblk && !stop; ++j) {
-        const int x = gi + j, s = x % SV, b = x % NB;
-        // the item's first PV overwrites O: the last item's has to have been read
-        if (!wait(&ctl->vfull[s], (uint32_t)(x / SV)) || !wait(&ctl->p_full[b], (uint32_t)(x / NB)) ||
+        const int x = gi + j, s = x % ST;
+        // the item's first products overwrite O: the last item's has to have been read
+        if ((!TWO && !wait(&ctl->vfull[s], (uint32_t)(x / ST))) || !wait(&ctl->p_full[x & 1], (uint32_t)(x >> 1)) ||
             (j == 0 && ii > 0 && !wait(&ctl->o_free, (uint32_t)(ii - 1)))) {
           stop = true;
           break;
@@ -1260,15 +1162,15 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
         tc_fence_after();
         if (elect_one()) {
           const uint64_t bv = dv + (uint64_t)((uint32_t)s * (C::KV >> 4));
-          const uint32_t pa = tmem + (uint32_t)(b * kTileBlk);
+          const uint32_t pa = tmem + (uint32_t)((x & 1) * kTileBlk), d = tmem + C::TO + (TWO ? (uint32_t)((x & 1) * HD) : 0u);
 #pragma unroll
           for (int kk = 0; kk < kTileBlk / 16; ++kk)
-            tc_mma_bf16_tmem_a(tmem + TO, pa + 8u * kk, bv + kk * (2048 >> 4), kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+            tc_mma_bf16_tmem_a(d, pa + 8u * kk, bv + kk * (2048 >> 4), kIdO, (j >= C::STREAMS || kk > 0) ? 1u : 0u);
           if (j == nblk - 1) tc_commit(smem_u32(&ctl->pv_item));
           tc_commit(smem_u32(&ctl->vempty[s]));
         }
         __syncwarp();
-        if (j + NB < nblk) stop = !issue_s(x + NB);
+        if (j + 2 < nblk) stop = !issue_s(x + 2);
       }
       gi += nblk;
       ++ii;
@@ -1277,15 +1179,153 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
     if (elect_one()) tc_commit(smem_u32(&ctl->drain));
     __syncwarp();
     mbar_wait(smem_u32(&ctl->drain), 0, a.err, nullptr, a.wait_ns);
+  } else if (warp < 4 || warp == C::THREADS / 32 - 1) {
+    // ------------------------------------------------------------------ unpack
+    const PairBits bits;
+    const int pw = warp & 3, row = lane >> 1, hc = lane & 1;
+    const uint32_t row_at = (uint32_t)((pw * 16 + row) * 128);
+    uint32_t unit_at[4];  // this lane's units 4hc + i of its row, in 64 columns
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unit_at[i] = row_at + (uint32_t)(((4 * hc + i) ^ (row & 7)) << 4);
+    const uint32_t step = (uint32_t)a.n_kv * L::kRecord;
+    const uint32_t raw0 = sQ + C::RAWS + (uint32_t)pw * (C::RAW * L::kRecord);
+    int blk = 0, ids = -1, slot_in = 0;
+    bool more = true;
+    // copies the page of the next block, over the segments; a group of copies each time, empty behind the last
+    auto fetch = [&]() {
+      if (more) {
+        while (blk >= blocks_of(seg)) {
+          if (!walk.next(seg, u1)) {
+            more = false;
+            break;
+          }
+          blk = 0;
+        }
+      }
+      if (more) {
+        if ((blk & 31) == 0) {  // page ids of 32 blocks, one per lane
+          const int x = seg.page0 + 4 * (blk + lane) + pw;
+          ids = -1;
+          if (x < seg.page1) {
+            ids = __ldcg(a.block_table + (size_t)((uint32_t)(ln.tile0 + seg.k) / ln.tps) * a.max_pages + x);
+            if (ids < 0 || ids >= a.num_pages) {
+              set_err(a.err, PE_DEV_BAD_PAGE);
+              ids = -1;
+            }
+          }
+        }
+        const int id = __shfl_sync(0xFFFFFFFFu, ids, blk & 31);
+        ++blk;
+        const uint32_t dst = raw0 + (uint32_t)slot_in * L::kRecord + lane * 16;
+        const uint8_t* src = a.pool + (uint64_t)(uint32_t)max(id, 0) * step + (size_t)seg.g * L::kRecord + lane * 16;
+#pragma unroll
+        for (int i = 0; i < (L::kRecord + 511) / 512; ++i) {
+          if (i * 512 + 511 < L::kRecord || i * 512 + lane * 16 < L::kRecord) {
+            if (id >= 0) copy16(dst + i * 512, src + i * 512);
+            else st_shared16(dst + i * 512, 0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
+          }
+        }
+        slot_in = slot_in + 1 == C::RAW ? 0 : slot_in + 1;
+      }
+      copy_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < C::RAW; ++i) fetch();
+    // a second walk for the number of blocks
+    Segment cs;
+    walk.first(cs, u0, u1);
+    int gi = 0, s = 0, slot = 0;
+    bool stop = false;
+    do {
+      const int nblk = blocks_of(cs);
+#pragma unroll 1
+      for (int j = 0; j < nblk; ++j) {
+        copy_wait<C::RAW - 1>();
+        __syncwarp();
+        uint4 k[H], v[H];
+        uint32_t ks[H], vs[H];
+        const uint8_t* rec = sm + C::RAWS + (size_t)(pw * C::RAW + slot) * L::kRecord;
+#pragma unroll
+        for (int c = 0; c < H; ++c) {
+          k[c] = *reinterpret_cast<const uint4*>(rec + L::kK + row * L::kRow + (hc + 2 * c) * 16);
+          v[c] = *reinterpret_cast<const uint4*>(rec + L::kV + row * L::kRow + (H * hc + c) * 16);
+          ks[c] = reinterpret_cast<const uint32_t*>(rec + L::kKs + row * L::kScaleRow)[c];
+          vs[c] = reinterpret_cast<const uint32_t*>(rec + L::kVs + row * L::kScaleRow)[c];
+        }
+        slot = slot + 1 == C::RAW ? 0 : slot + 1;
+        __syncwarp();  // the page is in registers
+        fetch();
+        // head_dim 64: the stage is free once its last PV has completed; 128: its keys once S has
+        if (gi >= ST && !(TWO ? wait(&ctl->vempty[s], (uint32_t)(gi / ST) - 1u) : wait(&ctl->s_full[s], (uint32_t)(gi / ST) - 1u))) {
+          stop = true;
+          break;
+        }
+        {
+          const uint32_t base = sQ + C::KRING + (uint32_t)s * C::KV;
+          // word w of the row: entries 4t..4t+3 of blocks 2u and 2u + 1, unit w of the tile's row
+          uint32_t sp[4 * H], zp[4 * H];
+#pragma unroll
+          for (int i = 0; i < 4 * H; ++i) {
+            sp[i] = packed_scale_lo(__byte_perm(ks[i / 4], 0, 0x4040 + 0x0101 * (i & 3)));
+            zp[i] = bf16x2_mul(sp[i], kMinus136);
+          }
+#pragma unroll
+          for (int c = 0; c < H; ++c) {
+            const uint32_t w4[4] = {k[c].x, k[c].y, k[c].z, k[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int u = HD == 64 ? i & 1 : i;  // word 4 (hc + 2c) + i = t * HD/32 + u
+              st_shared16(base + (uint32_t)(c * kTileBlk * 128) + unit_at[i],
+                          bf16x2_fma(bits.pair<0>(w4[i]), sp[2 * u], zp[2 * u]), bf16x2_fma(bits.pair<1>(w4[i]), sp[2 * u], zp[2 * u]),
+                          bf16x2_fma(bits.pair<2>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]),
+                          bf16x2_fma(bits.pair<3>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]));
+            }
+          }
+        }
+        if constexpr (!TWO) {
+          fence_proxy_async_smem();
+          arrive(&ctl->kfull[s]);
+          if (gi >= ST && !wait(&ctl->vempty[s], (uint32_t)(gi / ST) - 1u)) {
+            stop = true;
+            break;
+          }
+        }
+        {
+          const uint32_t base = sQ + C::VRING + (uint32_t)s * C::KV;
+          // word (g, h): entries g and g + 8 of four blocks, pairs 32 entries apart; unit g of the h-th 64 columns
+          uint32_t sp[H][2], zp[H][2];
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            sp[h][0] = packed_scale_lo(vs[h]);
+            sp[h][1] = packed_scale_hi(vs[h]);
+            zp[h][0] = bf16x2_mul(sp[h][0], kMinus136);
+            zp[h][1] = bf16x2_mul(sp[h][1], kMinus136);
+          }
+#pragma unroll
+          for (int c = 0; c < H; ++c) {
+            const uint32_t w4[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int h = HD == 64 ? 0 : i & 1;  // word 4 (H hc + c) + i = g * H + h, g = 4 hc + n
+              const int n = HD == 64 ? i : 2 * c + (i >> 1);
+              st_shared16(base + (uint32_t)(h * kTileBlk * 128) + unit_at[n],
+                          bf16x2_fma(bits.pair<0>(w4[i]), sp[h][0], zp[h][0]), bf16x2_fma(bits.pair<1>(w4[i]), sp[h][0], zp[h][0]),
+                          bf16x2_fma(bits.pair<2>(w4[i]), sp[h][1], zp[h][1]), bf16x2_fma(bits.pair<3>(w4[i]), sp[h][1], zp[h][1]));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        arrive(TWO ? &ctl->kfull[s] : &ctl->vfull[s]);
+        ++gi;
+        s = s + 1 == ST ? 0 : s + 1;
+      }
+    } while (!stop && walk.next(cs, u1));
+    copy_wait<0>();  // leave no copy in flight into this CTA's shared memory
   } else {
     // ------------------------------------------------------------------ softmax and output
-    const int et = tid - 128;
+    const int et = tid - 128, stream = TWO ? (warp - 4) >> 2 : 0;
     const int r = (warp & 3) * 32 + lane;  // query vector of the tile = TMEM lane
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    auto arrive = [&](uint64_t* bar) {  // one arrival per warp
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(bar));
-    };
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float sl2 = a.scale * 1.4426950408889634f * kPackedUnit;
     const __nv_bfloat16* qbuf = static_cast<const __nv_bfloat16*>(a.q);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
@@ -1295,92 +1335,96 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
     };
     // the query tile, entries in the order of the key words: unit w = t * HD/32 + u holds entries 4t..4t+3 of
     // blocks 2u and 2u + 1; zeros behind the tile's vectors
-    auto stage_q = [&](const Segment& sg) {
+    auto stage_q = [&](const Segment& sg, int buf) {
       const TileRows t = lo.tile(ln, sg.k);
-      constexpr int PER = kTileRows * CH / 128;  // units per thread, eight at a time in flight
-#pragma unroll
-      for (int k0 = 0; k0 < PER; k0 += 8) {
-        uint2 x[8], y[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int idx = et + (k0 + k) * 128, m = idx / CH, w = idx % CH;
-          x[k] = y[k] = make_uint2(0, 0);
-          if (m < t.M) {
-            const __nv_bfloat16* src = qbuf + row_of(t, m, sg.g, a.q_stride) + 32 * (w % (HD / 32)) + 4 * (w / (HD / 32));
-            x[k] = __ldcg(reinterpret_cast<const uint2*>(src));
-            y[k] = __ldcg(reinterpret_cast<const uint2*>(src + 16));
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int idx = et + (k0 + k) * 128, m = idx / CH, w = idx % CH;
-          st_shared16(unit_addr<kTileRows>(sQ, m, w), x[k].x, x[k].y, y[k].x, y[k].y);
-        }
+#pragma unroll 1
+      for (int idx = et; idx < kTileRows * CH; idx += C::SOFTMAX) {
+        const int m = idx / CH, w = idx % CH;
+        const __nv_bfloat16* src = qbuf + row_of(t, m < t.M ? m : 0, sg.g, a.q_stride) + 32 * (w % (HD / 32)) + 4 * (w / (HD / 32));
+        const uint32_t dst = unit_addr<kTileRows>(sQ + (uint32_t)buf * C::Q, m, w), bytes = m < t.M ? 8u : 0u;
+        copy8(dst, src, bytes);
+        copy8(dst + 8, src + 16, bytes);
       }
+      copy_commit();
+    };
+    auto q_staged = [&] {
+      copy_wait<0>();
       fence_proxy_async_smem();
       arrive(&ctl->q_full);
     };
-    int gi = 0, ii = 0;
-    bool stop = false, staged = false;
-    for (;;) {
-      const TileRows tr = lo.tile(ln, seg.k);
-      const int nblk = blocks_of(seg);
-      const bool valid = r < tr.M;
-      if (nblk == 0) {  // nothing to see: zeros
-        if (valid) {
-          __nv_bfloat16* dst = out + row_of(tr, r, seg.g, a.out_stride);
+    // the next segment with positions to see; rows of those without get zeros
+    auto advance = [&](Segment& sg) -> bool {
+      for (;;) {
+        if (blocks_of(sg) > 0) return true;
+        const TileRows t = lo.tile(ln, sg.k);
+        if (r < t.M && stream == 0) {
+          __nv_bfloat16* dst = out + row_of(t, r, sg.g, a.out_stride);
 #pragma unroll
           for (int c = 0; c < CH; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
         }
-        if (!walk.next(seg, u1)) break;
-        continue;
+        if (!walk.next(sg, u1)) return false;
       }
-      if (!staged) stage_q(seg);
-      staged = false;
+    };
+    int gi = 0, ii = 0;
+    bool more = advance(seg);
+    if (more) stage_q(seg, 0);
+    while (more) {
+      q_staged();
+      const Segment cur = seg;
+      more = walk.next(seg, u1) && advance(seg);
+      if (C::QB == 2 && more) stage_q(seg, (ii + 1) & 1);
+      const TileRows tr = lo.tile(ln, cur.k);
+      const int nblk = blocks_of(cur);
+      const bool valid = r < tr.M;
       // the vector's last visible position within the segment
       bool bad = false;  // reported by lay_out
       int lim = -1;
       if (valid)
-        lim = min(row_limit(a, __ldcg(a.positions + tr.r0 + (int)((uint32_t)(tr.m0 + r) / ln.group)), bad), seg.page1 * kPackedPage - 1);
+        lim = min(row_limit(a, __ldcg(a.positions + tr.r0 + (int)((uint32_t)(tr.m0 + r) / ln.group)), bad), cur.page1 * kPackedPage - 1);
       const bool warp_any = __any_sync(0xFFFFFFFFu, valid);
       int wmin = valid ? lim : INT_MAX;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) wmin = min(wmin, __shfl_xor_sync(0xFFFFFFFFu, wmin, o));
       float m_ref = -INFINITY, l = 0.f;  // reference maximum (log2 units) and sum
-      for (int j = 0; j < nblk; ++j) {
+      const uint32_t o_at = lanes + C::TO + (TWO ? (uint32_t)(stream * HD) : 0u);
+      bool stop = false;
+#pragma unroll 1
+      for (int j = TWO ? (gi + stream) & 1 : 0; j < nblk; j += C::STREAMS) {  // (two streams: x % 2 = stream)
         const int x = gi + j;
-        if (!warp_ok(mbar_wait(smem_u32(&ctl->s_full[x % NB]), (uint32_t)(x / NB) & 1u, a.err, abort_flag, a.wait_ns))) {
+        if (!wait(&ctl->s_full[x & 1], (uint32_t)(x >> 1))) {
           stop = true;
           break;
         }
         tc_fence_after();
-        const uint32_t sbuf = tmem + lane_base + (uint32_t)((x % NB) * kTileBlk);
         if (warp_any) {
-          float sc[kTileBlk];
-          tmem_load64(sbuf, sc);
-          const int kb0 = seg.page0 * kPackedPage + j * kTileBlk;
-          if (kb0 + kTileBlk - 1 > wmin) {  // some position of the block is masked for some vector of the warp
+          // S twice, 32 columns at a time (the registers do not hold 64 of them): for the maximum, then for P
+          const uint32_t sbuf = lanes + (uint32_t)((x & 1) * kTileBlk);
+          const int kb0 = cur.page0 * kPackedPage + j * kTileBlk;
+          const bool edge = kb0 + kTileBlk - 1 > wmin;  // some position is masked for some vector of the warp
+          float sc[32], mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto load = [&](int h) {
+            tmem_load32(sbuf + 32u * h, sc);
+            if (edge) {
 #pragma unroll
-            for (int c = 0; c < kTileBlk; ++c) sc[c] = (kb0 + c <= lim) ? sc[c] : -INFINITY;
+              for (int c = 0; c < 32; ++c) sc[c] = (kb0 + 32 * h + c <= lim) ? sc[c] : -INFINITY;
+            }
+          };
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            load(h);
+#pragma unroll
+            for (int c = 0; c < 32; c += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(fmaxf(mx4[e], sc[c + e]), sc[c + 4 + e]);
           }
-          float mx4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx4[e] = sc[e];
-#pragma unroll
-          for (int c = 4; c < kTileBlk; c += 8)  // (two maxima of three operands each)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx4[e] = c + 4 + e < kTileBlk ? fmaxf(fmaxf(mx4[e], sc[c + e]), sc[c + 4 + e]) : fmaxf(mx4[e], sc[c + e]);
-          float bm = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          bm *= sl2;
+          const float bm = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
           const bool fresh = m_ref == -INFINITY;
           const bool need = !fresh && bm > m_ref + kRescaleLog2;
           if (__any_sync(0xFFFFFFFFu, need)) {
-            // O holds the PV products of the blocks before j.  The release of block x - 1's values is
-            // committed after its PV product, and that barrier is at most one phase short of it: S(x)
-            // completing implies that every PV up to block x - NB has, and SV >= NB - 1.
-            const int xp = x - 1;
-            if (!warp_ok(mbar_wait(smem_u32(&ctl->vempty[xp % SV]), (uint32_t)(xp / SV) & 1u, a.err, abort_flag, a.wait_ns))) {
+            // O holds the PV products of the stream's blocks before.  Two streams: S(x) was issued behind the
+            // PV of block x - 2, so it has completed.  One: the PV of block x - 1 tells by its stage (at most one
+            // phase short: that of block x - 2 has completed, and there are two stages).
+            if (!TWO && !wait(&ctl->vempty[(x - 1) % ST], (uint32_t)((x - 1) / ST))) {
               stop = true;
             } else {
               tc_fence_after();
@@ -1388,10 +1432,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
 #pragma unroll 1
               for (int c = 0; c < HD; c += 16) {
                 float ov[16];
-                tmem_load16(tmem + lane_base + TO + (uint32_t)c, ov);
+                tmem_load16(o_at + (uint32_t)c, ov);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) ov[e] *= f;
-                tmem_store16(tmem + lane_base + TO + (uint32_t)c, ov);
+                tmem_store16(o_at + (uint32_t)c, ov);
               }
               if (need) {
                 l *= f;
@@ -1404,73 +1448,101 @@ __global__ void __launch_bounds__(kTileThreads, 2) attend_tile_kernel(const Pack
           const float nmr = m_ref == -INFINITY ? -INFINITY : -m_ref;
           const F2 scale2(sl2, sl2), off2(nmr, nmr);
           F2 sum2[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
-          uint32_t pk[kTileBlk / 2];
 #pragma unroll
-          for (int c = 0; c < kTileBlk / 2; ++c) {
-            const F2 d = F2::fma(F2(sc[2 * c], sc[2 * c + 1]), scale2, off2);
-            const float p0 = ex2_approx(d.lo()), p1 = ex2_approx(d.hi());
-            sum2[c & 1] = F2::add(sum2[c & 1], F2(p0, p1));
-            pk[c] = pack_bf16(p0, p1);
+          for (int h = 0; h < 2; ++h) {
+            load(h);
+            float pk[16];  // bf16 pairs
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const F2 d = F2::fma(F2(sc[2 * c], sc[2 * c + 1]), scale2, off2);
+              const float p0 = ex2_approx(d.lo()), p1 = ex2_approx(d.hi());
+              sum2[c & 1] = F2::add(sum2[c & 1], F2(p0, p1));
+              pk[c] = __uint_as_float(pack_bf16(p0, p1));
+            }
+            tmem_store16(sbuf + 16u * h, pk);  // over columns that have been read: 0..15, then 16..31
           }
           const F2 s2 = F2::add(sum2[0], sum2[1]);
           l += s2.lo() + s2.hi();
-          tmem_store32(sbuf, pk);
         }
         tc_fence_before();
-        arrive(&ctl->p_full[x % NB]);
+        arrive(&ctl->p_full[x & 1]);
         if (stop) break;
       }
       if (stop) break;
-      const Segment done = seg;
-      const bool final = !walk.next(seg, u1);
-      // every S product of this segment has completed: the next one's query tile may go in
-      if (!final && blocks_of(seg) > 0) {
-        stage_q(seg);
-        staged = true;
-      }
       gi += nblk;
-      if (!warp_ok(mbar_wait(smem_u32(&ctl->pv_item), (uint32_t)ii & 1u, a.err, abort_flag, a.wait_ns))) break;
-      ++ii;
+      // the other stream's statistics: both end up with the common maximum, and what either's O counts
+      float f_own = 1.f, f_other = 0.f;
+      const bool other_any = TWO && nblk > 1 - ((gi - nblk + stream) & 1);  // the other stream had a block
+      if constexpr (TWO) {
+        // (in alternating places: a warp can be an item ahead of the other)
+        float* stats = reinterpret_cast<float*>(sm + C::STATS) + (ii & 1) * 4 * kTileRows;
+        stats[stream * 2 * kTileRows + r] = m_ref;
+        stats[(stream * 2 + 1) * kTileRows + r] = l;
+        arrive(&ctl->pair[warp & 3]);
+        if (!wait(&ctl->pair[warp & 3], (uint32_t)ii)) break;
+        const float m2 = stats[(stream ^ 1) * 2 * kTileRows + r], l2 = stats[((stream ^ 1) * 2 + 1) * kTileRows + r];
+        const float m = fmaxf(m_ref, m2);
+        f_own = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
+        f_other = m2 == -INFINITY ? 0.f : ex2_approx(m2 - m);
+        l = l * f_own + l2 * f_other;
+        m_ref = m;
+      }
+      const bool own_any = !TWO || nblk > ((gi - nblk + stream) & 1);
+      if (!wait(&ctl->pv_item, (uint32_t)ii)) break;
       tc_fence_after();
-      const bool whole = done.from_start && done.to_end;
+      if (C::QB == 1 && more) stage_q(seg, 0);  // every product of this item has completed
+      const bool whole = cur.from_start && cur.to_end;
       if (warp_any) {
-        const float inv = whole && l > 0.f ? kPackedUnit / l : whole ? 0.f : 1.f;
-        float* rec = whole ? nullptr : part_record<HD>(ln, blockIdx.x, done.from_start);
-        if (valid && !whole) {
+        const float inv = whole ? (l > 0.f ? kPackedUnit / l : 0.f) : 1.f;
+        f_own *= inv;
+        f_other *= inv;
+        float* rec = whole ? nullptr : part_record<HD>(ln, blockIdx.x, cur.from_start);
+        if (valid && !whole && stream == 0) {
           rec[r] = m_ref;
           rec[kTileRows + r] = l;
         }
+        // column 8g + 2i + e of 64 holds entry 16 (i/2) + g + 8 (i%2) + 32 e: four entries (g or g + 4 on) at a time;
+        // two streams: each writes half of the columns
+        __nv_bfloat16* dst = out + row_of(tr, r, cur.g, a.out_stride);
+        float* rdst = rec + 2 * kTileRows + r * HD;
 #pragma unroll 1
-        for (int h = 0; h < H; ++h) {
-          float ov[64];
-          tmem_load64(tmem + lane_base + TO + 64u * h, ov);
+        for (int h = stream; h < 2 * H; h += C::STREAMS) {
+          float ov[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) ov[c] = 0.f;
+          if (own_any) {
+            tmem_load32(o_at + 32u * h, ov);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) ov[c] *= f_own;
+          }
+          if (TWO && other_any) {
+            const uint32_t at = lanes + C::TO + (uint32_t)((stream ^ 1) * HD + 32 * h);
+#pragma unroll
+            for (int c = 0; c < 32; c += 16) {
+              float ot[16];
+              tmem_load16(at + (uint32_t)c, ot);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[c + e] = fmaf(ot[e], f_other, ov[c + e]);
+            }
+          }
           if (valid) {
-            // column 8g + 2i + e holds entry 16 (i/2) + g + 8 (i%2) + 32 e
-            if (whole) {
-              __nv_bfloat16* dst = out + row_of(tr, r, done.g, a.out_stride) + 64 * h;
+            const int at = 64 * (h >> 1) + 4 * (h & 1);
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {  // entries 8c..8c+7: block c/2, its half c%2
-                const int col = 2 * (2 * ((c >> 1) & 1) + (c & 1)) + (c >> 2);
-                reinterpret_cast<uint4*>(dst)[c] =
-                    make_uint4(pack_bf16(ov[col] * inv, ov[8 + col] * inv), pack_bf16(ov[16 + col] * inv, ov[24 + col] * inv),
-                               pack_bf16(ov[32 + col] * inv, ov[40 + col] * inv), pack_bf16(ov[48 + col] * inv, ov[56 + col] * inv));
-              }
-            } else {
-              float* dst = rec + 2 * kTileRows + r * HD + 64 * h;
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const int col = 2 * (2 * ((c >> 1) & 1) + (c & 1)) + (c >> 2);
-                const float v[8] = {ov[col], ov[8 + col], ov[16 + col], ov[24 + col], ov[32 + col], ov[40 + col], ov[48 + col], ov[56 + col]};
-                st_global_v8(dst + 8 * c, v);
-              }
+            for (int c = 0; c < 8; ++c) {  // i = c % 4, e = c / 4
+              const int col = 2 * (c & 3) + (c >> 2), e = at + 16 * ((c >> 1) & 1) + 8 * (c & 1) + 32 * (c >> 2);
+              if (whole)
+                *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16(ov[col], ov[8 + col]), pack_bf16(ov[16 + col], ov[24 + col]));
+              else
+                *reinterpret_cast<float4*>(rdst + e) = make_float4(ov[col], ov[8 + col], ov[16 + col], ov[24 + col]);
             }
           }
         }
       }
       tc_fence_before();
       arrive(&ctl->o_free);
-      if (final) break;
+      ++ii;
     }
+    copy_wait<0>();
   }
   __syncthreads();
   if (warp == 0) {
@@ -1698,7 +1770,7 @@ cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
     ln.n_tiles = (int)std::min<long long>(per_launch, tiles - t0);
     const int grid = line_grid(a, ln, sms * 2);
     ln.grid = make_div(grid);
-    e = launch_pdl(attend_tile_kernel<HD>, dim3(grid), dim3(kTileThreads), C::smem(ln.n_tiles), s, a, ln);
+    e = launch_pdl(attend_tile_kernel<HD>, dim3(grid), dim3(C::THREADS), C::smem(ln.n_tiles), s, a, ln);
     if (e != cudaSuccess) return e;
     if (!ln.whole && grid > 1 && (e = launch_merge<__nv_bfloat16, HD>(a, ln, grid, sms, s)) != cudaSuccess) return e;
   }
