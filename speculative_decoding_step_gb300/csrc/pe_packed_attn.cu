@@ -8,8 +8,8 @@
 //
 // Work.  The query vectors of a sequence and kv head (rows x G query heads, G = n_q / n_kv) are
 // cut into tiles; a (tile, kv head) pair's range of positions is counted in units.  All ranges of
-// the launch form one line (tile after tile, head after head, unit after unit), a range as long as it
-// costs: so much at its start and so much per unit.  N CTAs divide the line into equal pieces, so
+// the launch form one line (tile after tile, head after head, unit after unit), a range a little longer
+// than its units, for what its start costs.  N CTAs divide the line into equal pieces, so
 // ragged lengths leave no CTA idle; a unit belongs to the piece in which it starts.  A range that lies in
 // one CTA's piece is finished there; one that is cut leaves a record per CTA (reference maximum,
 // sum, unnormalised output) that the merge kernel joins in CTA order.  Every CTA works the line
@@ -79,10 +79,7 @@ struct Line {
   int lanes;           // threads that look through one tile's rows (a power of two, at most 32)
   int whole;           // CTAs take whole ranges
   int min_log2;        // a CTA's piece is at least 2^this long where there are fewer than that for all
-  int range_cost;      // of a range, beside its units'
-  int by_rows;         // the cost of a unit goes by the tile's vectors: cost[(vectors - 1) / 32]; else cost[0]
-  int cost[4];
-  Div cost_div[4];
+  int range_cost;      // of a range's start, in units
   int* prefix;         // workspace [n_tiles + 1]: cost per head before each tile, for the merge
   float* part;         // workspace: records of cut ranges, two per CTA
   float* spill;        // workspace: a warp's piece of a range that began before it (small kernel)
@@ -129,10 +126,7 @@ struct Layout {
 PE_DEV int range_units(const Line& ln, int last) {  // at least one: a range that sees nothing has to be zeroed
   return max(1, (last / kPackedPage + ln.unit_pages) >> (ln.unit_pages == 2 ? 1 : 2));
 }
-PE_DEV int cost_class(const Line& ln, int vectors) { return ln.by_rows ? (vectors - 1) >> 5 : 0; }
-PE_DEV int tile_cost(const Line& ln, const TileRows& t, int last) {
-  return t.M == 0 ? 0 : range_units(ln, last) * ln.cost[cost_class(ln, t.M)] + ln.range_cost;
-}
+PE_DEV int tile_cost(const Line& ln, const TileRows& t, int last) { return t.M == 0 ? 0 : range_units(ln, last) + ln.range_cost; }
 
 // Fills the line in.  Every thread of the CTA.
 PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, int* warp_sums) {
@@ -301,14 +295,11 @@ struct Walk {
     r -= s.g * len;
     const uint32_t end = min(len, r + (u1 - u));
     s.next = u + (end - r);
-    // unit i starts at range_cost + i * cost
-    const int cls = cost_class(ln, lo.rows[k]);
-    const uint32_t base = ln.range_cost, c = ln.cost[cls];
-    const int b0 = r <= base ? 0 : (int)((r - base + c - 1) / ln.cost_div[cls]);
-    const int b1 = end <= base ? 0 : (int)((end - base + c - 1) / ln.cost_div[cls]);
+    // unit i starts at range_cost + i
+    const int b0 = max(0, (int)r - ln.range_cost), b1 = max(0, (int)end - ln.range_cost);
     s.any = b1 > b0;
     s.from_start = b0 == 0;
-    s.to_end = end > len - c;  // the last unit starts before `end`
+    s.to_end = end == len;
     s.page0 = b0 * ln.unit_pages;
     s.page1 = min((lo.last[k] + kPackedPage) / kPackedPage, b1 * ln.unit_pages);
     return s;
@@ -962,9 +953,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 // unpacking, 500 issue cycles, beside 256 cycles of MMA and 200 of HBM.
 
 constexpr int kTileRows = 128;
-// Costs on the line: a block's unpacking as much as the softmax of about 96 vectors, a range's start (queries,
-// filling the pipeline, output) as much as one or two blocks.
-constexpr int kTileUnitCost = 4, kTileRangeCost = 8;
+constexpr int kTileRangeCost = 4;  // a range's start (queries, filling the pipeline, output), in blocks
 constexpr int kTileBlk = 64;
 constexpr uint32_t kTileTmemCols = 256;  // two S buffers, then O
 
@@ -1574,7 +1563,7 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
   const Cuts cuts(ln, grid, tot);
   const uint32_t len = p1 - p0, start = (uint32_t)p0 * a.n_kv + (uint32_t)g * len;
   // the pieces in which its first and its last unit start
-  const int c0 = (int)cuts.piece(start + ln.range_cost), c1 = (int)cuts.piece(start + len - ln.cost[cost_class(ln, tr.M)]);
+  const int c0 = (int)cuts.piece(start + ln.range_cost), c1 = (int)cuts.piece(start + len - 1);
   if (c0 == c1) return;  // finished by its CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp & (split - 1), per = 8 / split;  // vectors at a time
@@ -1691,13 +1680,12 @@ cudaError_t launch_merge(const PackedAttnArgs& a, const Line& ln, int grid, int 
 
 // The longest that a range can be.
 long long line_length(const PackedAttnArgs& a, const Line& ln) {
-  return (long long)((a.max_pages + ln.unit_pages - 1) / ln.unit_pages) * ln.cost[ln.by_rows ? (ln.tile_rows - 1) / 32 : 0] + ln.range_cost;
+  return (long long)((a.max_pages + ln.unit_pages - 1) / ln.unit_pages) + ln.range_cost;
 }
 
 // The launch's line for tiles of `tile_rows` vectors and units of `unit_pages`, and how many of its tiles one
 // launch takes (their units, counted in 32 bits, and kPlanTiles bound it).
-Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_log2, int range_cost, int unit_cost, int by_rows,
-               int* tiles_per_launch) {
+Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_log2, int range_cost, int* tiles_per_launch) {
   const int G = a.n_q / a.n_kv;
   const long long vectors = (long long)a.max_rows * G;
   Line ln{};
@@ -1715,11 +1703,6 @@ Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_l
   ln.lanes = 1;
   while (ln.lanes < 32 && ln.lanes * 4 < rows) ln.lanes *= 2;
   ln.range_cost = range_cost;
-  ln.by_rows = by_rows;
-  for (int i = 0; i < 4; ++i) {
-    ln.cost[i] = unit_cost + (by_rows ? i : 0);
-    ln.cost_div[i] = make_div(ln.cost[i]);
-  }
   *tiles_per_launch = (int)std::min<long long>(kPlanTiles, std::max(1LL, ((1LL << 31) - 1) / (line_length(a, ln) * a.n_kv)));
   return ln;
 }
@@ -1734,7 +1717,7 @@ template <typename T, int HD, int NQ>
 cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Small<T, HD, NQ>;
   int per_launch = 0;
-  Line ln = make_line(a, C::ROWS, 2, 3, kSmallRangeCost, 1, 0, &per_launch);
+  Line ln = make_line(a, C::ROWS, 2, 3, kSmallRangeCost, &per_launch);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ln.prefix = reinterpret_cast<int*>(ws);
   ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
@@ -1758,7 +1741,7 @@ template <int HD>
 cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Tile<HD>;
   int per_launch = 0;
-  Line ln = make_line(a, kTileRows, 4, 4, kTileRangeCost, kTileUnitCost, 1, &per_launch);
+  Line ln = make_line(a, kTileRows, 4, 2, kTileRangeCost, &per_launch);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ln.prefix = reinterpret_cast<int*>(ws);
   ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
