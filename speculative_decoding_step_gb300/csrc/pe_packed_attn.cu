@@ -938,49 +938,45 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 // the 5th-generation tensor core, S and O in tensor memory, P written over S as bf16.  One unpacked
 // block serves all 128 vectors.  Roles of a CTA (two CTAs per SM):
 //   one warp     issues the MMAs: a block's PV once P is there, then the S that reuses its buffer, two
-//                blocks on.
-//   four warps   unpack: each takes one page of a block, a row (position) per two lanes, from a ring of its
+//                or three blocks on.
+//   some warps   unpack: each takes a page of a block in turn, a row (position) per two lanes, from a ring of its
 //                own that asynchronous copies fill ahead, into the K and V rings (128-byte swizzle).
 //                Entries stay in the order of the cache's words: K's is a permutation of the
 //                contraction, given to Q as well; V's one of O's columns, undone on output.
-//   four warps per stream do the softmax, one thread per query vector (TMEM lane).  head_dim 64: two streams,
-//                the even and the odd blocks, each with its own statistics and its own O, that meet at the
-//                item's end (one stream's softmax alone took 1500 cycles a block, mostly waiting for itself:
-//                two warps of a scheduler do not hide it).  head_dim 128: one, tensor memory holds no second O.
+//   four warps   do the softmax, one thread per query vector (TMEM lane).
 // A vector's reference maximum only moves when a block exceeds it by 2^8; then O is rescaled in TMEM.
 //
 // Bound (head_dim 64): per block of 64 positions about 1100 warp instructions of softmax and 900 of
 // unpacking, 500 issue cycles, beside 256 cycles of MMA and 200 of HBM.
 
 constexpr int kTileRows = 128;
-constexpr int kTileRangeCost = 4;  // a range's start (queries, filling the pipeline, output), in blocks
+constexpr int kTileRangeCost = 6;  // a range's start (queries, filling the pipeline, output), in blocks
 constexpr int kTileBlk = 64;
-constexpr uint32_t kTileTmemCols = 256;  // two S buffers, then O
+constexpr uint32_t kTileTmemCols = 256;  // S buffers, then O
 
 template <int HD>
 struct Tile {
-  static constexpr int STREAMS = HD == 64 ? 2 : 1;
-  static constexpr int SOFTMAX = 128 * STREAMS;       // threads
-  static constexpr int THREADS = 160 + SOFTMAX;       // warp 0: MMA; 1..3 and the last: unpack; 4..: softmax
-  static constexpr int ST = HD == 64 ? 3 : 2;         // stages of keys and values
-  static constexpr int RAW = HD == 64 ? 4 : 1;        // pages ahead of each unpacking warp
+  static constexpr bool JOINT = HD == 64;             // a block's keys and values are handed over together
+  static constexpr int NB = HD == 64 ? 3 : 2;         // S buffers; O takes the rest of the tensor memory
+  static constexpr int UNPACK = 5;                    // warps
+  static constexpr int THREADS = 32 * (1 + UNPACK) + kTileRows;  // warp 0: MMA; 1..3 and the last ones: unpack; 4..7: softmax
+  static constexpr int ST = NB;                       // stages of keys and values
+  static constexpr int RAW = HD == 64 ? 3 : 1;        // pages ahead of each unpacking warp
   static constexpr int QB = HD == 64 ? 2 : 1;         // query tiles
-  static constexpr uint32_t TO = 2 * kTileBlk;        // first column of O (of the first stream's)
+  static constexpr uint32_t TO = NB * kTileBlk;       // first column of O
   static constexpr uint32_t Q = kTileRows * HD * 2, KV = kTileBlk * HD * 2;
   static constexpr uint32_t KRING = QB * Q, VRING = KRING + ST * KV, RAWS = VRING + ST * KV;
-  static constexpr uint32_t CTRL = RAWS + 4 * RAW * PackedLayout<HD>::kRecord;
-  static constexpr uint32_t STATS = CTRL + 256;       // two streams: [items in turn][streams][maximum, sum][128]
-  static constexpr uint32_t FIXED = STATS + (STREAMS == 2 ? 8 * kTileRows * 4 : 0);
+  static constexpr uint32_t CTRL = (RAWS + UNPACK * RAW * PackedLayout<HD>::kRecord + 127) / 128 * 128;
+  static constexpr uint32_t FIXED = CTRL + 256;
   static size_t smem(int n_tiles) { return 1024 + FIXED + Layout::kBytesPerTile * (size_t)n_tiles + 4; }
 };
 
 struct TileCtrl {
-  uint64_t kfull[3], vfull[3];     // an arrival per unpacking warp
+  uint64_t kfull[3], vfull[3];     // an arrival per page
   uint64_t vempty[3];              // the block's PV product has completed
-  uint64_t s_full[2], p_full[2];   // S of a block is in its buffer (and its keys are read); P is (O rescaled where needed)
+  uint64_t s_full[3], p_full[3];   // S of a block is in its buffer (and its keys are read); P is (O rescaled where needed)
   uint64_t q_full;                 // the item's query tile is staged
   uint64_t pv_item, o_free;        // the item's last PV has completed; its O has been read
-  uint64_t pair[4];                // either stream's warp of 32 vectors has given its statistics
   uint64_t drain;
   int scratch[16];
   uint32_t tmem;
@@ -1050,7 +1046,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
   using C = Tile<HD>;
   using L = PackedLayout<HD>;
   constexpr int H = HD / 64, CH = HD / 8, ST = C::ST;
-  constexpr bool TWO = C::STREAMS == 2;
+  constexpr int NB = C::NB;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sQ = smem_u32(sm);
@@ -1075,14 +1071,13 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       mbar_init(smem_u32(&ctl->vfull[s]), 4);
       mbar_init(smem_u32(&ctl->vempty[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NB; ++b) {
       mbar_init(smem_u32(&ctl->s_full[b]), 1);
       mbar_init(smem_u32(&ctl->p_full[b]), 4);
     }
-    for (int q = 0; q < 4; ++q) mbar_init(smem_u32(&ctl->pair[q]), 2);
-    mbar_init(smem_u32(&ctl->q_full), C::SOFTMAX / 32);
+    mbar_init(smem_u32(&ctl->q_full), 4);
     mbar_init(smem_u32(&ctl->pv_item), 1);
-    mbar_init(smem_u32(&ctl->o_free), C::SOFTMAX / 32);
+    mbar_init(smem_u32(&ctl->o_free), 4);
     mbar_init(smem_u32(&ctl->drain), 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -1103,7 +1098,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(bar));
   };
-  // Blocks are counted through the CTA's segments: block x uses stage x % ST and S buffer x % 2.
+  // Blocks are counted through the CTA's segments: block x uses stage and S buffer x % NB.
   Segment seg;
   const bool some = walk.first(seg, u0, u1);
 
@@ -1121,12 +1116,12 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       tc_fence_after();
       if (elect_one()) {
         const uint64_t bk = dk + (uint64_t)((uint32_t)s * (C::KV >> 4));
-        const uint32_t d = tmem + (uint32_t)((x & 1) * kTileBlk);
+        const uint32_t d = tmem + (uint32_t)(s * kTileBlk);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
           tc_mma_bf16(d, dq + ((kk >> 2) * (kTileRows * 128 >> 4) + 2 * (kk & 3)),
                       bk + ((kk >> 2) * (kTileBlk * 128 >> 4) + 2 * (kk & 3)), kIdS, kk > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&ctl->s_full[x & 1]));
+        tc_commit(smem_u32(&ctl->s_full[s]));
       }
       __syncwarp();
       return true;
@@ -1138,12 +1133,12 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       if (nblk == 0) continue;
       stop = !wait(&ctl->q_full, (uint32_t)ii);
       dq = sdesc_k_sw128(sQ + (C::QB == 2 && (ii & 1) ? C::Q : 0));
-      for (int j = 0; j < 2 && j < nblk && !stop; ++j) stop = !issue_s(gi + j);
+      for (int j = 0; j < NB && j < nblk && !stop; ++j) stop = !issue_s(gi + j);
 #pragma unroll 1
       for (int j = 0; j < nblk && !stop; ++j) {
         const int x = gi + j, s = x % ST;
         // the item's first products overwrite O: the last item's has to have been read
-        if ((!TWO && !wait(&ctl->vfull[s], (uint32_t)(x / ST))) || !wait(&ctl->p_full[x & 1], (uint32_t)(x >> 1)) ||
+        if ((!C::JOINT && !wait(&ctl->vfull[s], (uint32_t)(x / ST))) || !wait(&ctl->p_full[s], (uint32_t)(x / NB)) ||
             (j == 0 && ii > 0 && !wait(&ctl->o_free, (uint32_t)(ii - 1)))) {
           stop = true;
           break;
@@ -1151,15 +1146,15 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
         tc_fence_after();
         if (elect_one()) {
           const uint64_t bv = dv + (uint64_t)((uint32_t)s * (C::KV >> 4));
-          const uint32_t pa = tmem + (uint32_t)((x & 1) * kTileBlk), d = tmem + C::TO + (TWO ? (uint32_t)((x & 1) * HD) : 0u);
+          const uint32_t pa = tmem + (uint32_t)(s * kTileBlk);
 #pragma unroll
           for (int kk = 0; kk < kTileBlk / 16; ++kk)
-            tc_mma_bf16_tmem_a(d, pa + 8u * kk, bv + kk * (2048 >> 4), kIdO, (j >= C::STREAMS || kk > 0) ? 1u : 0u);
+            tc_mma_bf16_tmem_a(tmem + C::TO, pa + 8u * kk, bv + kk * (2048 >> 4), kIdO, (j > 0 || kk > 0) ? 1u : 0u);
           if (j == nblk - 1) tc_commit(smem_u32(&ctl->pv_item));
           tc_commit(smem_u32(&ctl->vempty[s]));
         }
         __syncwarp();
-        if (j + 2 < nblk) stop = !issue_s(x + 2);
+        if (j + NB < nblk) stop = !issue_s(x + NB);
       }
       gi += nblk;
       ++ii;
@@ -1168,32 +1163,33 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
     if (elect_one()) tc_commit(smem_u32(&ctl->drain));
     __syncwarp();
     mbar_wait(smem_u32(&ctl->drain), 0, a.err, nullptr, a.wait_ns);
-  } else if (warp < 4 || warp == C::THREADS / 32 - 1) {
+  } else if (warp < 4 || warp >= 8) {
     // ------------------------------------------------------------------ unpack
     const PairBits bits;
-    const int pw = warp & 3, row = lane >> 1, hc = lane & 1;
-    const uint32_t row_at = (uint32_t)((pw * 16 + row) * 128);
-    uint32_t unit_at[4];  // this lane's units 4hc + i of its row, in 64 columns
+    // pages are counted through the CTA's blocks, four a block; page q belongs to warp q % UNPACK
+    const int uw = warp < 4 ? warp - 1 : warp - 5, row = lane >> 1, hc = lane & 1;
+    uint32_t unit_at[4];  // this lane's units 4hc + i of its row, in a page of 64 columns
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unit_at[i] = row_at + (uint32_t)(((4 * hc + i) ^ (row & 7)) << 4);
+    for (int i = 0; i < 4; ++i) unit_at[i] = (uint32_t)(row * 128 + (((4 * hc + i) ^ (row & 7)) << 4));
     const uint32_t step = (uint32_t)a.n_kv * L::kRecord;
-    const uint32_t raw0 = sQ + C::RAWS + (uint32_t)pw * (C::RAW * L::kRecord);
-    int blk = 0, ids = -1, slot_in = 0;
+    const uint32_t raw0 = sQ + C::RAWS + (uint32_t)uw * (C::RAW * L::kRecord);
+    int page = uw, ids = -1, n_ids = 0, slot_in = 0;  // page: of the segment's blocks (the last may lack some)
     bool more = true;
     // copies the page of the next block, over the segments; a group of copies each time, empty behind the last
     auto fetch = [&]() {
       if (more) {
-        while (blk >= blocks_of(seg)) {
+        for (int n; page >= (n = 4 * blocks_of(seg));) {
           if (!walk.next(seg, u1)) {
             more = false;
             break;
           }
-          blk = 0;
+          page -= n;
+          n_ids = 0;
         }
       }
       if (more) {
-        if ((blk & 31) == 0) {  // page ids of 32 blocks, one per lane
-          const int x = seg.page0 + 4 * (blk + lane) + pw;
+        if (n_ids == 0) {  // the ids of this warp's next 32 pages, one per lane
+          const int x = seg.page0 + page + C::UNPACK * lane;
           ids = -1;
           if (x < seg.page1) {
             ids = __ldcg(a.block_table + (size_t)((uint32_t)(ln.tile0 + seg.k) / ln.tps) * a.max_pages + x);
@@ -1203,8 +1199,9 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
             }
           }
         }
-        const int id = __shfl_sync(0xFFFFFFFFu, ids, blk & 31);
-        ++blk;
+        const int id = __shfl_sync(0xFFFFFFFFu, ids, n_ids);
+        n_ids = (n_ids + 1) & 31;
+        page += C::UNPACK;
         const uint32_t dst = raw0 + (uint32_t)slot_in * L::kRecord + lane * 16;
         const uint8_t* src = a.pool + (uint64_t)(uint32_t)max(id, 0) * step + (size_t)seg.g * L::kRecord + lane * 16;
 #pragma unroll
@@ -1220,20 +1217,23 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
     };
 #pragma unroll 1
     for (int i = 0; i < C::RAW; ++i) fetch();
-    // a second walk for the number of blocks
+    // how many pages there are: a second walk
     Segment cs;
-    walk.first(cs, u0, u1);
-    int gi = 0, s = 0, slot = 0;
-    bool stop = false;
-    do {
-      const int nblk = blocks_of(cs);
+    int pages = 0;
+    if (walk.first(cs, u0, u1))
+      do pages += 4 * blocks_of(cs);
+      while (walk.next(cs, u1));
+    int slot = 0;
 #pragma unroll 1
-      for (int j = 0; j < nblk; ++j) {
+    for (int q = uw; q < pages; q += C::UNPACK) {
+      {
+        const int gi = q >> 2, s = gi % ST;
+        const uint32_t page_at = (uint32_t)((q & 3) * 16 * 128);
         copy_wait<C::RAW - 1>();
         __syncwarp();
         uint4 k[H], v[H];
         uint32_t ks[H], vs[H];
-        const uint8_t* rec = sm + C::RAWS + (size_t)(pw * C::RAW + slot) * L::kRecord;
+        const uint8_t* rec = sm + C::RAWS + (size_t)(uw * C::RAW + slot) * L::kRecord;
 #pragma unroll
         for (int c = 0; c < H; ++c) {
           k[c] = *reinterpret_cast<const uint4*>(rec + L::kK + row * L::kRow + (hc + 2 * c) * 16);
@@ -1245,12 +1245,10 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
         __syncwarp();  // the page is in registers
         fetch();
         // head_dim 64: the stage is free once its last PV has completed; 128: its keys once S has
-        if (gi >= ST && !(TWO ? wait(&ctl->vempty[s], (uint32_t)(gi / ST) - 1u) : wait(&ctl->s_full[s], (uint32_t)(gi / ST) - 1u))) {
-          stop = true;
+        if (gi >= ST && !(C::JOINT ? wait(&ctl->vempty[s], (uint32_t)(gi / ST) - 1u) : wait(&ctl->s_full[s], (uint32_t)(gi / ST) - 1u)))
           break;
-        }
         {
-          const uint32_t base = sQ + C::KRING + (uint32_t)s * C::KV;
+          const uint32_t base = sQ + C::KRING + (uint32_t)s * C::KV + page_at;
           // word w of the row: entries 4t..4t+3 of blocks 2u and 2u + 1, unit w of the tile's row
           uint32_t sp[4 * H], zp[4 * H];
 #pragma unroll
@@ -1271,16 +1269,13 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
             }
           }
         }
-        if constexpr (!TWO) {
+        if constexpr (!C::JOINT) {
           fence_proxy_async_smem();
           arrive(&ctl->kfull[s]);
-          if (gi >= ST && !wait(&ctl->vempty[s], (uint32_t)(gi / ST) - 1u)) {
-            stop = true;
-            break;
-          }
+          if (gi >= ST && !wait(&ctl->vempty[s], (uint32_t)(gi / ST) - 1u)) break;
         }
         {
-          const uint32_t base = sQ + C::VRING + (uint32_t)s * C::KV;
+          const uint32_t base = sQ + C::VRING + (uint32_t)s * C::KV + page_at;
           // word (g, h): entries g and g + 8 of four blocks, pairs 32 entries apart; unit g of the h-th 64 columns
           uint32_t sp[H][2], zp[H][2];
 #pragma unroll
@@ -1304,15 +1299,13 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
           }
         }
         fence_proxy_async_smem();
-        arrive(TWO ? &ctl->kfull[s] : &ctl->vfull[s]);
-        ++gi;
-        s = s + 1 == ST ? 0 : s + 1;
+        arrive(C::JOINT ? &ctl->kfull[s] : &ctl->vfull[s]);
       }
-    } while (!stop && walk.next(cs, u1));
+    }
     copy_wait<0>();  // leave no copy in flight into this CTA's shared memory
   } else {
     // ------------------------------------------------------------------ softmax and output
-    const int et = tid - 128, stream = TWO ? (warp - 4) >> 2 : 0;
+    const int et = tid - 128;
     const int r = (warp & 3) * 32 + lane;  // query vector of the tile = TMEM lane
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float sl2 = a.scale * 1.4426950408889634f * kPackedUnit;
@@ -1327,7 +1320,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
     auto stage_q = [&](const Segment& sg, int buf) {
       const TileRows t = lo.tile(ln, sg.k);
 #pragma unroll 1
-      for (int idx = et; idx < kTileRows * CH; idx += C::SOFTMAX) {
+      for (int idx = et; idx < kTileRows * CH; idx += kTileRows) {
         const int m = idx / CH, w = idx % CH;
         const __nv_bfloat16* src = qbuf + row_of(t, m < t.M ? m : 0, sg.g, a.q_stride) + 32 * (w % (HD / 32)) + 4 * (w / (HD / 32));
         const uint32_t dst = unit_addr<kTileRows>(sQ + (uint32_t)buf * C::Q, m, w), bytes = m < t.M ? 8u : 0u;
@@ -1346,7 +1339,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       for (;;) {
         if (blocks_of(sg) > 0) return true;
         const TileRows t = lo.tile(ln, sg.k);
-        if (r < t.M && stream == 0) {
+        if (r < t.M) {
           __nv_bfloat16* dst = out + row_of(t, r, sg.g, a.out_stride);
 #pragma unroll
           for (int c = 0; c < CH; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
@@ -1375,45 +1368,36 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) wmin = min(wmin, __shfl_xor_sync(0xFFFFFFFFu, wmin, o));
       float m_ref = -INFINITY, l = 0.f;  // reference maximum (log2 units) and sum
-      const uint32_t o_at = lanes + C::TO + (TWO ? (uint32_t)(stream * HD) : 0u);
+      const uint32_t o_at = lanes + C::TO;
       bool stop = false;
 #pragma unroll 1
-      for (int j = TWO ? (gi + stream) & 1 : 0; j < nblk; j += C::STREAMS) {  // (two streams: x % 2 = stream)
-        const int x = gi + j;
-        if (!wait(&ctl->s_full[x & 1], (uint32_t)(x >> 1))) {
+      for (int j = 0; j < nblk; ++j) {
+        const int x = gi + j, b = x % NB;
+        if (!wait(&ctl->s_full[b], (uint32_t)(x / NB))) {
           stop = true;
           break;
         }
         tc_fence_after();
         if (warp_any) {
-          // S twice, 32 columns at a time (the registers do not hold 64 of them): for the maximum, then for P
-          const uint32_t sbuf = lanes + (uint32_t)((x & 1) * kTileBlk);
+          const uint32_t sbuf = lanes + (uint32_t)(b * kTileBlk);
           const int kb0 = cur.page0 * kPackedPage + j * kTileBlk;
-          const bool edge = kb0 + kTileBlk - 1 > wmin;  // some position is masked for some vector of the warp
-          float sc[32], mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto load = [&](int h) {
-            tmem_load32(sbuf + 32u * h, sc);
-            if (edge) {
+          float sc[kTileBlk], mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          tmem_load64(sbuf, sc);
+          if (kb0 + kTileBlk - 1 > wmin) {  // some position is masked for some vector of the warp
 #pragma unroll
-              for (int c = 0; c < 32; ++c) sc[c] = (kb0 + 32 * h + c <= lim) ? sc[c] : -INFINITY;
-            }
-          };
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            load(h);
-#pragma unroll
-            for (int c = 0; c < 32; c += 8)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(fmaxf(mx4[e], sc[c + e]), sc[c + 4 + e]);
+            for (int c = 0; c < kTileBlk; ++c) sc[c] = (kb0 + c <= lim) ? sc[c] : -INFINITY;
           }
+#pragma unroll
+          for (int c = 0; c < kTileBlk; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(fmaxf(mx4[e], sc[c + e]), sc[c + 4 + e]);
           const float bm = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
           const bool fresh = m_ref == -INFINITY;
           const bool need = !fresh && bm > m_ref + kRescaleLog2;
           if (__any_sync(0xFFFFFFFFu, need)) {
-            // O holds the PV products of the stream's blocks before.  Two streams: S(x) was issued behind the
-            // PV of block x - 2, so it has completed.  One: the PV of block x - 1 tells by its stage (at most one
-            // phase short: that of block x - 2 has completed, and there are two stages).
-            if (!TWO && !wait(&ctl->vempty[(x - 1) % ST], (uint32_t)((x - 1) / ST))) {
+            // O holds the PV products of the blocks before.  The PV of block x - 1 tells by its stage (at most one
+            // phase short: S(x) was issued behind the PV of block x - NB, and there are NB stages).
+            if (!wait(&ctl->vempty[(x - 1) % ST], (uint32_t)((x - 1) / ST))) {
               stop = true;
             } else {
               tc_fence_after();
@@ -1437,83 +1421,44 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
           const float nmr = m_ref == -INFINITY ? -INFINITY : -m_ref;
           const F2 scale2(sl2, sl2), off2(nmr, nmr);
           F2 sum2[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
+          uint32_t pk[kTileBlk / 2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            load(h);
-            float pk[16];  // bf16 pairs
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const F2 d = F2::fma(F2(sc[2 * c], sc[2 * c + 1]), scale2, off2);
-              const float p0 = ex2_approx(d.lo()), p1 = ex2_approx(d.hi());
-              sum2[c & 1] = F2::add(sum2[c & 1], F2(p0, p1));
-              pk[c] = __uint_as_float(pack_bf16(p0, p1));
-            }
-            tmem_store16(sbuf + 16u * h, pk);  // over columns that have been read: 0..15, then 16..31
+          for (int c = 0; c < kTileBlk / 2; ++c) {
+            const F2 d = F2::fma(F2(sc[2 * c], sc[2 * c + 1]), scale2, off2);
+            const float p0 = ex2_approx(d.lo()), p1 = ex2_approx(d.hi());
+            sum2[c & 1] = F2::add(sum2[c & 1], F2(p0, p1));
+            pk[c] = pack_bf16(p0, p1);
           }
+          tmem_store32(sbuf, pk);  // over the first half of S's columns
           const F2 s2 = F2::add(sum2[0], sum2[1]);
           l += s2.lo() + s2.hi();
         }
         tc_fence_before();
-        arrive(&ctl->p_full[x & 1]);
+        arrive(&ctl->p_full[b]);
         if (stop) break;
       }
       if (stop) break;
       gi += nblk;
-      // the other stream's statistics: both end up with the common maximum, and what either's O counts
-      float f_own = 1.f, f_other = 0.f;
-      const bool other_any = TWO && nblk > 1 - ((gi - nblk + stream) & 1);  // the other stream had a block
-      if constexpr (TWO) {
-        // (in alternating places: a warp can be an item ahead of the other)
-        float* stats = reinterpret_cast<float*>(sm + C::STATS) + (ii & 1) * 4 * kTileRows;
-        stats[stream * 2 * kTileRows + r] = m_ref;
-        stats[(stream * 2 + 1) * kTileRows + r] = l;
-        arrive(&ctl->pair[warp & 3]);
-        if (!wait(&ctl->pair[warp & 3], (uint32_t)ii)) break;
-        const float m2 = stats[(stream ^ 1) * 2 * kTileRows + r], l2 = stats[((stream ^ 1) * 2 + 1) * kTileRows + r];
-        const float m = fmaxf(m_ref, m2);
-        f_own = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
-        f_other = m2 == -INFINITY ? 0.f : ex2_approx(m2 - m);
-        l = l * f_own + l2 * f_other;
-        m_ref = m;
-      }
-      const bool own_any = !TWO || nblk > ((gi - nblk + stream) & 1);
       if (!wait(&ctl->pv_item, (uint32_t)ii)) break;
       tc_fence_after();
       if (C::QB == 1 && more) stage_q(seg, 0);  // every product of this item has completed
       const bool whole = cur.from_start && cur.to_end;
       if (warp_any) {
         const float inv = whole ? (l > 0.f ? kPackedUnit / l : 0.f) : 1.f;
-        f_own *= inv;
-        f_other *= inv;
         float* rec = whole ? nullptr : part_record<HD>(ln, blockIdx.x, cur.from_start);
-        if (valid && !whole && stream == 0) {
+        if (valid && !whole) {
           rec[r] = m_ref;
           rec[kTileRows + r] = l;
         }
-        // column 8g + 2i + e of 64 holds entry 16 (i/2) + g + 8 (i%2) + 32 e: four entries (g or g + 4 on) at a time;
-        // two streams: each writes half of the columns
+        // column 8g + 2i + e of 64 holds entry 16 (i/2) + g + 8 (i%2) + 32 e: four entries (g or g + 4 on) at a time
         __nv_bfloat16* dst = out + row_of(tr, r, cur.g, a.out_stride);
         float* rdst = rec + 2 * kTileRows + r * HD;
 #pragma unroll 1
-        for (int h = stream; h < 2 * H; h += C::STREAMS) {
+        for (int h = 0; h < 2 * H; ++h) {
           float ov[32];
+          tmem_load32(o_at + 32u * h, ov);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) ov[c] = 0.f;
-          if (own_any) {
-            tmem_load32(o_at + 32u * h, ov);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) ov[c] *= f_own;
-          }
-          if (TWO && other_any) {
-            const uint32_t at = lanes + C::TO + (uint32_t)((stream ^ 1) * HD + 32 * h);
-#pragma unroll
-            for (int c = 0; c < 32; c += 16) {
-              float ot[16];
-              tmem_load16(at + (uint32_t)c, ot);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) ov[c + e] = fmaf(ot[e], f_other, ov[c + e]);
-            }
-          }
+          for (int c = 0; c < 32; ++c) ov[c] *= inv;
           if (valid) {
             const int at = 64 * (h >> 1) + 4 * (h & 1);
 #pragma unroll
@@ -1741,7 +1686,7 @@ template <int HD>
 cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Tile<HD>;
   int per_launch = 0;
-  Line ln = make_line(a, kTileRows, 4, 2, kTileRangeCost, &per_launch);
+  Line ln = make_line(a, kTileRows, 4, 3, kTileRangeCost, &per_launch);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ln.prefix = reinterpret_cast<int*>(ws);
   ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
