@@ -960,9 +960,9 @@ struct Tile {
   static constexpr int NB = HD == 64 ? 3 : 2;         // S buffers; O takes the rest of the tensor memory
   static constexpr int UNPACK = 5;                    // warps
   static constexpr int THREADS = 32 * (1 + UNPACK) + kTileRows;  // warp 0: MMA; 1..3 and the last ones: unpack; 4..7: softmax
-  static constexpr int ST = NB;                       // stages of keys and values
+  static constexpr int ST = HD == 64 ? 4 : 2;         // stages of keys and values
   static constexpr int RAW = HD == 64 ? 3 : 1;        // pages ahead of each unpacking warp
-  static constexpr int QB = HD == 64 ? 2 : 1;         // query tiles
+  static constexpr int QB = 1;                        // query tiles
   static constexpr uint32_t TO = NB * kTileBlk;       // first column of O
   static constexpr uint32_t Q = kTileRows * HD * 2, KV = kTileBlk * HD * 2;
   static constexpr uint32_t KRING = QB * Q, VRING = KRING + ST * KV, RAWS = VRING + ST * KV;
@@ -972,8 +972,8 @@ struct Tile {
 };
 
 struct TileCtrl {
-  uint64_t kfull[3], vfull[3];     // an arrival per page
-  uint64_t vempty[3];              // the block's PV product has completed
+  uint64_t kfull[5], vfull[2];     // an arrival per page
+  uint64_t vempty[5];              // the block's PV product has completed
   uint64_t s_full[3], p_full[3];   // S of a block is in its buffer (and its keys are read); P is (O rescaled where needed)
   uint64_t q_full;                 // the item's query tile is staged
   uint64_t pv_item, o_free;        // the item's last PV has completed; its O has been read
@@ -1068,7 +1068,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(smem_u32(&ctl->kfull[s]), 4);
-      mbar_init(smem_u32(&ctl->vfull[s]), 4);
+      if (!C::JOINT) mbar_init(smem_u32(&ctl->vfull[s]), 4);
       mbar_init(smem_u32(&ctl->vempty[s]), 1);
     }
     for (int b = 0; b < NB; ++b) {
@@ -1098,7 +1098,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(bar));
   };
-  // Blocks are counted through the CTA's segments: block x uses stage and S buffer x % NB.
+  // Blocks are counted through the CTA's segments: block x uses stage x % ST and S buffer x % NB.
   Segment seg;
   const bool some = walk.first(seg, u0, u1);
 
@@ -1116,12 +1116,12 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       tc_fence_after();
       if (elect_one()) {
         const uint64_t bk = dk + (uint64_t)((uint32_t)s * (C::KV >> 4));
-        const uint32_t d = tmem + (uint32_t)(s * kTileBlk);
+        const uint32_t d = tmem + (uint32_t)((x % NB) * kTileBlk);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
           tc_mma_bf16(d, dq + ((kk >> 2) * (kTileRows * 128 >> 4) + 2 * (kk & 3)),
                       bk + ((kk >> 2) * (kTileBlk * 128 >> 4) + 2 * (kk & 3)), kIdS, kk > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&ctl->s_full[s]));
+        tc_commit(smem_u32(&ctl->s_full[x % NB]));
       }
       __syncwarp();
       return true;
@@ -1136,9 +1136,9 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       for (int j = 0; j < NB && j < nblk && !stop; ++j) stop = !issue_s(gi + j);
 #pragma unroll 1
       for (int j = 0; j < nblk && !stop; ++j) {
-        const int x = gi + j, s = x % ST;
+        const int x = gi + j, s = x % ST, b = x % NB;
         // the item's first products overwrite O: the last item's has to have been read
-        if ((!C::JOINT && !wait(&ctl->vfull[s], (uint32_t)(x / ST))) || !wait(&ctl->p_full[s], (uint32_t)(x / NB)) ||
+        if ((!C::JOINT && !wait(&ctl->vfull[s], (uint32_t)(x / ST))) || !wait(&ctl->p_full[b], (uint32_t)(x / NB)) ||
             (j == 0 && ii > 0 && !wait(&ctl->o_free, (uint32_t)(ii - 1)))) {
           stop = true;
           break;
@@ -1146,7 +1146,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
         tc_fence_after();
         if (elect_one()) {
           const uint64_t bv = dv + (uint64_t)((uint32_t)s * (C::KV >> 4));
-          const uint32_t pa = tmem + (uint32_t)(s * kTileBlk);
+          const uint32_t pa = tmem + (uint32_t)(b * kTileBlk);
 #pragma unroll
           for (int kk = 0; kk < kTileBlk / 16; ++kk)
             tc_mma_bf16_tmem_a(tmem + C::TO, pa + 8u * kk, bv + kk * (2048 >> 4), kIdO, (j > 0 || kk > 0) ? 1u : 0u);
@@ -1396,7 +1396,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
           const bool need = !fresh && bm > m_ref + kRescaleLog2;
           if (__any_sync(0xFFFFFFFFu, need)) {
             // O holds the PV products of the blocks before.  The PV of block x - 1 tells by its stage (at most one
-            // phase short: S(x) was issued behind the PV of block x - NB, and there are NB stages).
+            // phase short: S(x) was issued behind the PV of block x - NB, and there are as many stages).
             if (!wait(&ctl->vempty[(x - 1) % ST], (uint32_t)((x - 1) / ST))) {
               stop = true;
             } else {
