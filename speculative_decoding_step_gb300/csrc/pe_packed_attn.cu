@@ -39,6 +39,11 @@ PE_DEV uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
+PE_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // A wait's outcome, made the same for the whole warp.
 PE_DEV bool warp_ok(bool ok) { return __all_sync(0xFFFFFFFFu, ok); }
 
@@ -958,21 +963,23 @@ template <int HD>
 struct Tile {
   static constexpr bool JOINT = HD == 64;             // a block's keys and values are handed over together
   static constexpr int NB = HD == 64 ? 3 : 2;         // S buffers; O takes the rest of the tensor memory
-  static constexpr int UNPACK = 5;                    // warps
+  static constexpr int PAGES = HD == 64 ? 2 : 1;      // pages of a block that an unpacking warp takes at a time
+  static constexpr int UNPACK = HD == 64 ? 3 : 4;     // unpacking warps
   static constexpr int THREADS = 32 * (1 + UNPACK) + kTileRows;  // warp 0: MMA; 1..3 and the last ones: unpack; 4..7: softmax
   static constexpr int ST = HD == 64 ? 4 : 2;         // stages of keys and values
-  static constexpr int RAW = HD == 64 ? 3 : 1;        // pages ahead of each unpacking warp
+  static constexpr int RAW = HD == 64 ? 3 : 1;        // steps that an unpacking warp's copies are ahead
+  static constexpr int STEP = PAGES * PackedLayout<HD>::kRecord;
   static constexpr int QB = 1;                        // query tiles
   static constexpr uint32_t TO = NB * kTileBlk;       // first column of O
   static constexpr uint32_t Q = kTileRows * HD * 2, KV = kTileBlk * HD * 2;
   static constexpr uint32_t KRING = QB * Q, VRING = KRING + ST * KV, RAWS = VRING + ST * KV;
-  static constexpr uint32_t CTRL = (RAWS + UNPACK * RAW * PackedLayout<HD>::kRecord + 127) / 128 * 128;
+  static constexpr uint32_t CTRL = (RAWS + UNPACK * RAW * STEP + 127) / 128 * 128;
   static constexpr uint32_t FIXED = CTRL + 256;
   static size_t smem(int n_tiles) { return 1024 + FIXED + Layout::kBytesPerTile * (size_t)n_tiles + 4; }
 };
 
 struct TileCtrl {
-  uint64_t kfull[5], vfull[2];     // an arrival per page
+  uint64_t kfull[5], vfull[2];     // an arrival per step of the unpacking warps
   uint64_t vempty[5];              // the block's PV product has completed
   uint64_t s_full[3], p_full[3];   // S of a block is in its buffer (and its keys are read); P is (O rescaled where needed)
   uint64_t q_full;                 // the item's query tile is staged
@@ -1067,8 +1074,8 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
   if (u0 == u1) return;  // the whole CTA, before it holds anything
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(smem_u32(&ctl->kfull[s]), 4);
-      if (!C::JOINT) mbar_init(smem_u32(&ctl->vfull[s]), 4);
+      mbar_init(smem_u32(&ctl->kfull[s]), 4 / C::PAGES);
+      if (!C::JOINT) mbar_init(smem_u32(&ctl->vfull[s]), 4 / C::PAGES);
       mbar_init(smem_u32(&ctl->vempty[s]), 1);
     }
     for (int b = 0; b < NB; ++b) {
@@ -1166,16 +1173,17 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
   } else if (warp < 4 || warp >= 8) {
     // ------------------------------------------------------------------ unpack
     const PairBits bits;
-    // pages are counted through the CTA's blocks, four a block; page q belongs to warp q % UNPACK
-    const int uw = warp < 4 ? warp - 1 : warp - 5, row = lane >> 1, hc = lane & 1;
-    uint32_t unit_at[4];  // this lane's units 4hc + i of its row, in a page of 64 columns
-#pragma unroll
-    for (int i = 0; i < 4; ++i) unit_at[i] = (uint32_t)(row * 128 + (((4 * hc + i) ^ (row & 7)) << 4));
+    // Steps of PAGES pages are counted through the CTA's blocks; step q belongs to warp q % UNPACK.  A row (position)
+    // per lane, or two lanes (head_dim 128), which take eight words of its keys and eight of its values.
+    constexpr int PP = C::PAGES, PER = 4 / PP, LPR = 2 / PP;
+    const int uw = warp < 4 ? warp - 1 : warp - 5, row = lane / LPR, hc = lane % LPR;
+    const uint32_t row_x = (uint32_t)(row & 7) << 4;
     const uint32_t step = (uint32_t)a.n_kv * L::kRecord;
-    const uint32_t raw0 = sQ + C::RAWS + (uint32_t)uw * (C::RAW * L::kRecord);
-    int page = uw, ids = -1, n_ids = 0, slot_in = 0;  // page: of the segment's blocks (the last may lack some)
+    const uint32_t raw0 = sQ + C::RAWS + (uint32_t)uw * (C::RAW * C::STEP);
+    int page = uw * PP, ids = -1, n_ids = 0;  // page: of the segment's blocks (the last may lack some)
+    uint32_t raw_in = raw0 + lane * 16;
     bool more = true;
-    // copies the page of the next block, over the segments; a group of copies each time, empty behind the last
+    // copies the pages of the warp's next step, over the segments; a group of copies each time, empty behind the last
     auto fetch = [&]() {
       if (more) {
         for (int n; page >= (n = 4 * blocks_of(seg));) {
@@ -1189,7 +1197,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       }
       if (more) {
         if (n_ids == 0) {  // the ids of this warp's next 32 pages, one per lane
-          const int x = seg.page0 + page + C::UNPACK * lane;
+          const int x = seg.page0 + page + (lane / PP) * (C::UNPACK * PP) + lane % PP;
           ids = -1;
           if (x < seg.page1) {
             ids = __ldcg(a.block_table + (size_t)((uint32_t)(ln.tile0 + seg.k) / ln.tps) * a.max_pages + x);
@@ -1199,108 +1207,125 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
             }
           }
         }
-        const int id = __shfl_sync(0xFFFFFFFFu, ids, n_ids);
-        n_ids = (n_ids + 1) & 31;
-        page += C::UNPACK;
-        const uint32_t dst = raw0 + (uint32_t)slot_in * L::kRecord + lane * 16;
-        const uint8_t* src = a.pool + (uint64_t)(uint32_t)max(id, 0) * step + (size_t)seg.g * L::kRecord + lane * 16;
+        const uint8_t* head = a.pool + (size_t)seg.g * L::kRecord + lane * 16;
+        const int id0 = __shfl_sync(0xFFFFFFFFu, ids, n_ids), id1 = PP == 2 ? __shfl_sync(0xFFFFFFFFu, ids, n_ids + 1) : id0;
+        n_ids = (n_ids + PP) & 31;
+        page += C::UNPACK * PP;
+        const uint8_t* src0 = head + (uint64_t)(uint32_t)id0 * step;
+        const uint8_t* src1 = head + (uint64_t)(uint32_t)id1 * step - L::kRecord;
+        if ((id0 | id1) >= 0) {
 #pragma unroll
-        for (int i = 0; i < (L::kRecord + 511) / 512; ++i) {
-          if (i * 512 + 511 < L::kRecord || i * 512 + lane * 16 < L::kRecord) {
-            if (id >= 0) copy16(dst + i * 512, src + i * 512);
-            else st_shared16(dst + i * 512, 0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros
+          for (int i = 0; i < (C::STEP + 511) / 512; ++i) {
+            const int at = i * 512 + lane * 16;  // byte of the records
+            const bool first = i * 512 + 511 < L::kRecord || (i * 512 < L::kRecord && at < L::kRecord);
+            if (i * 512 + 511 < C::STEP || at < C::STEP) copy16(raw_in + i * 512, (first ? src0 : src1) + i * 512);
+          }
+        } else {
+          // a page behind the range or outside the pool stands for zeros, every nibble 8
+#pragma unroll 1
+          for (int i = 0; i + lane * 16 < C::STEP; i += 512) {
+            const bool first = i + lane * 16 < L::kRecord;
+            if ((first ? id0 : id1) >= 0) copy16(raw_in + i, (first ? src0 : src1) + i);
+            else st_shared16(raw_in + i, 0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
           }
         }
-        slot_in = slot_in + 1 == C::RAW ? 0 : slot_in + 1;
+        raw_in = raw_in + C::STEP == raw0 + lane * 16 + C::RAW * C::STEP ? raw0 + lane * 16 : raw_in + C::STEP;
       }
       copy_commit();
     };
 #pragma unroll 1
     for (int i = 0; i < C::RAW; ++i) fetch();
-    // how many pages there are: a second walk
+    // how many steps there are: a second walk
     Segment cs;
-    int pages = 0;
+    int steps = 0;
     if (walk.first(cs, u0, u1))
-      do pages += 4 * blocks_of(cs);
+      do steps += PER * blocks_of(cs);
       while (walk.next(cs, u1));
+    const uint8_t* raw = sm + C::RAWS + (size_t)uw * (C::RAW * C::STEP);
     int slot = 0;
 #pragma unroll 1
-    for (int q = uw; q < pages; q += C::UNPACK) {
+    for (int q = uw; q < steps; q += C::UNPACK) {
+      const int gi = q / PER, s = gi % ST;
+      const uint32_t at = (uint32_t)(((q % PER) * PP * 16 + row) * 128);
+      copy_wait<C::RAW - 1>();
+      __syncwarp();
+      uint4 k[2], v[2];
+      uint32_t ks[H], vs[H];
       {
-        const int gi = q >> 2, s = gi % ST;
-        const uint32_t page_at = (uint32_t)((q & 3) * 16 * 128);
-        copy_wait<C::RAW - 1>();
-        __syncwarp();
-        uint4 k[H], v[H];
-        uint32_t ks[H], vs[H];
-        const uint8_t* rec = sm + C::RAWS + (size_t)(uw * C::RAW + slot) * L::kRecord;
+        const uint8_t* rec = raw + slot * C::STEP + (row >> 4) * L::kRecord;
+        const int r16 = row & 15;
 #pragma unroll
-        for (int c = 0; c < H; ++c) {
-          k[c] = *reinterpret_cast<const uint4*>(rec + L::kK + row * L::kRow + (hc + 2 * c) * 16);
-          v[c] = *reinterpret_cast<const uint4*>(rec + L::kV + row * L::kRow + (H * hc + c) * 16);
-          ks[c] = reinterpret_cast<const uint32_t*>(rec + L::kKs + row * L::kScaleRow)[c];
-          vs[c] = reinterpret_cast<const uint32_t*>(rec + L::kVs + row * L::kScaleRow)[c];
+        for (int c = 0; c < 2; ++c) {
+          k[c] = *reinterpret_cast<const uint4*>(rec + L::kK + r16 * L::kRow + (LPR * c + hc) * 16);
+          v[c] = *reinterpret_cast<const uint4*>(rec + L::kV + r16 * L::kRow + (2 * hc + c) * 16);
         }
-        slot = slot + 1 == C::RAW ? 0 : slot + 1;
-        __syncwarp();  // the page is in registers
-        fetch();
-        // head_dim 64: the stage is free once its last PV has completed; 128: its keys once S has
-        if (gi >= ST && !(C::JOINT ? wait(&ctl->vempty[s], (uint32_t)(gi / ST) - 1u) : wait(&ctl->s_full[s], (uint32_t)(gi / ST) - 1u)))
-          break;
-        {
-          const uint32_t base = sQ + C::KRING + (uint32_t)s * C::KV + page_at;
-          // word w of the row: entries 4t..4t+3 of blocks 2u and 2u + 1, unit w of the tile's row
-          uint32_t sp[4 * H], zp[4 * H];
 #pragma unroll
-          for (int i = 0; i < 4 * H; ++i) {
-            sp[i] = packed_scale_lo(__byte_perm(ks[i / 4], 0, 0x4040 + 0x0101 * (i & 3)));
-            zp[i] = bf16x2_mul(sp[i], kMinus136);
-          }
-#pragma unroll
-          for (int c = 0; c < H; ++c) {
-            const uint32_t w4[4] = {k[c].x, k[c].y, k[c].z, k[c].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int u = HD == 64 ? i & 1 : i;  // word 4 (hc + 2c) + i = t * HD/32 + u
-              st_shared16(base + (uint32_t)(c * kTileBlk * 128) + unit_at[i],
-                          bf16x2_fma(bits.pair<0>(w4[i]), sp[2 * u], zp[2 * u]), bf16x2_fma(bits.pair<1>(w4[i]), sp[2 * u], zp[2 * u]),
-                          bf16x2_fma(bits.pair<2>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]),
-                          bf16x2_fma(bits.pair<3>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]));
-            }
-          }
+        for (int h = 0; h < H; ++h) {
+          ks[h] = reinterpret_cast<const uint32_t*>(rec + L::kKs + r16 * L::kScaleRow)[h];
+          vs[h] = reinterpret_cast<const uint32_t*>(rec + L::kVs + r16 * L::kScaleRow)[h];
         }
-        if constexpr (!C::JOINT) {
-          fence_proxy_async_smem();
-          arrive(&ctl->kfull[s]);
-          if (gi >= ST && !wait(&ctl->vempty[s], (uint32_t)(gi / ST) - 1u)) break;
-        }
-        {
-          const uint32_t base = sQ + C::VRING + (uint32_t)s * C::KV + page_at;
-          // word (g, h): entries g and g + 8 of four blocks, pairs 32 entries apart; unit g of the h-th 64 columns
-          uint32_t sp[H][2], zp[H][2];
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            sp[h][0] = packed_scale_lo(vs[h]);
-            sp[h][1] = packed_scale_hi(vs[h]);
-            zp[h][0] = bf16x2_mul(sp[h][0], kMinus136);
-            zp[h][1] = bf16x2_mul(sp[h][1], kMinus136);
-          }
-#pragma unroll
-          for (int c = 0; c < H; ++c) {
-            const uint32_t w4[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int h = HD == 64 ? 0 : i & 1;  // word 4 (H hc + c) + i = g * H + h, g = 4 hc + n
-              const int n = HD == 64 ? i : 2 * c + (i >> 1);
-              st_shared16(base + (uint32_t)(h * kTileBlk * 128) + unit_at[n],
-                          bf16x2_fma(bits.pair<0>(w4[i]), sp[h][0], zp[h][0]), bf16x2_fma(bits.pair<1>(w4[i]), sp[h][0], zp[h][0]),
-                          bf16x2_fma(bits.pair<2>(w4[i]), sp[h][1], zp[h][1]), bf16x2_fma(bits.pair<3>(w4[i]), sp[h][1], zp[h][1]));
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        arrive(C::JOINT ? &ctl->kfull[s] : &ctl->vfull[s]);
       }
+      slot = slot + 1 == C::RAW ? 0 : slot + 1;
+      __syncwarp();  // the pages are in registers
+      fetch();
+      // head_dim 64: the stage is free once its last PV has completed; 128: its keys once S has
+      if (gi >= ST && !(C::JOINT ? wait(&ctl->vempty[s], (uint32_t)(gi / ST) - 1u) : wait(&ctl->s_full[s], (uint32_t)(gi / ST) - 1u)))
+        break;
+      {
+        const uint32_t base = sQ + C::KRING + (uint32_t)s * C::KV + at;
+        // word w = t * HD/32 + u of the row: entries 4t..4t+3 of blocks 2u and 2u + 1, unit w of the tile's row
+        uint32_t sp[4 * H], zp[4 * H];
+#pragma unroll
+        for (int i = 0; i < 4 * H; ++i) {
+          sp[i] = packed_scale_lo(__byte_perm(ks[i / 4], 0, 0x4040 + 0x0101 * (i & 3)));
+          zp[i] = bf16x2_mul(sp[i], kMinus136);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t w4[4] = {k[c].x, k[c].y, k[c].z, k[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // head_dim 64: word 4c + i; 128: word 4 (hc + 2c) + i, unit 4 hc + i of the c-th 64 columns
+            const int u = HD == 64 ? i & 1 : i;
+            const uint32_t unit = HD == 64 ? (uint32_t)(4 * c + i) << 4 : (uint32_t)(4 * hc + i) << 4;
+            st_shared16(base + (HD == 64 ? 0u : (uint32_t)(c * kTileBlk * 128)) + (unit ^ row_x),
+                        bf16x2_fma(bits.pair<0>(w4[i]), sp[2 * u], zp[2 * u]), bf16x2_fma(bits.pair<1>(w4[i]), sp[2 * u], zp[2 * u]),
+                        bf16x2_fma(bits.pair<2>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]),
+                        bf16x2_fma(bits.pair<3>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]));
+          }
+        }
+      }
+      if constexpr (!C::JOINT) {
+        fence_proxy_async_smem();
+        arrive(&ctl->kfull[s]);
+        if (gi >= ST && !wait(&ctl->vempty[s], (uint32_t)(gi / ST) - 1u)) break;
+      }
+      {
+        const uint32_t base = sQ + C::VRING + (uint32_t)s * C::KV + at;
+        // word g * H + h: entries g and g + 8 of four blocks, pairs 32 entries apart; unit g of the h-th 64 columns
+        uint32_t sp[H][2], zp[H][2];
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          sp[h][0] = packed_scale_lo(vs[h]);
+          sp[h][1] = packed_scale_hi(vs[h]);
+          zp[h][0] = bf16x2_mul(sp[h][0], kMinus136);
+          zp[h][1] = bf16x2_mul(sp[h][1], kMinus136);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t w4[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int h = HD == 64 ? 0 : i & 1;
+            const uint32_t unit = HD == 64 ? (uint32_t)(4 * c + i) << 4 : (uint32_t)(4 * hc + 2 * c + (i >> 1)) << 4;
+            st_shared16(base + (uint32_t)(h * kTileBlk * 128) + (unit ^ row_x),
+                        bf16x2_fma(bits.pair<0>(w4[i]), sp[h][0], zp[h][0]), bf16x2_fma(bits.pair<1>(w4[i]), sp[h][0], zp[h][0]),
+                        bf16x2_fma(bits.pair<2>(w4[i]), sp[h][1], zp[h][1]), bf16x2_fma(bits.pair<3>(w4[i]), sp[h][1], zp[h][1]));
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      arrive(C::JOINT ? &ctl->kfull[s] : &ctl->vfull[s]);
     }
     copy_wait<0>();  // leave no copy in flight into this CTA's shared memory
   } else {
@@ -1390,7 +1415,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
 #pragma unroll
           for (int c = 0; c < kTileBlk; c += 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(fmaxf(mx4[e], sc[c + e]), sc[c + 4 + e]);
+            for (int e = 0; e < 4; ++e) mx4[e] = max3(mx4[e], sc[c + e], sc[c + 4 + e]);
           const float bm = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
           const bool fresh = m_ref == -INFINITY;
           const bool need = !fresh && bm > m_ref + kRescaleLog2;
