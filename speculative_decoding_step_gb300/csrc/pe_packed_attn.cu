@@ -944,8 +944,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 // block serves all 128 vectors.  Roles of a CTA (two CTAs per SM):
 //   one warp     issues the MMAs: a block's PV once P is there, then the S that reuses its buffer, two
 //                or three blocks on.
-//   some warps   unpack: each takes a page of a block in turn, a row (position) per two lanes, from a ring of its
-//                own that asynchronous copies fill ahead, into the K and V rings (128-byte swizzle).
+//   some warps   unpack: each takes two pages of a block in turn, a row (position) per lane, from a ring of its own
+//                that asynchronous copies fill ahead, into the K and V rings (128-byte swizzle).
 //                Entries stay in the order of the cache's words: K's is a permutation of the
 //                contraction, given to Q as well; V's one of O's columns, undone on output.
 //   four warps   do the softmax, one thread per query vector (TMEM lane).
@@ -963,12 +963,11 @@ template <int HD>
 struct Tile {
   static constexpr bool JOINT = HD == 64;             // a block's keys and values are handed over together
   static constexpr int NB = HD == 64 ? 3 : 2;         // S buffers; O takes the rest of the tensor memory
-  static constexpr int PAGES = HD == 64 ? 2 : 1;      // pages of a block that an unpacking warp takes at a time
-  static constexpr int UNPACK = HD == 64 ? 3 : 4;     // unpacking warps
-  static constexpr int THREADS = 32 * (1 + UNPACK) + kTileRows;  // warp 0: MMA; 1..3 and the last ones: unpack; 4..7: softmax
+  static constexpr int UNPACK = 3;                    // unpacking warps
+  static constexpr int THREADS = 32 * (1 + UNPACK) + kTileRows;  // warp 0: MMA; 1..3: unpack; 4..7: softmax
   static constexpr int ST = HD == 64 ? 4 : 2;         // stages of keys and values
   static constexpr int RAW = HD == 64 ? 3 : 1;        // steps that an unpacking warp's copies are ahead
-  static constexpr int STEP = PAGES * PackedLayout<HD>::kRecord;
+  static constexpr int STEP = 2 * PackedLayout<HD>::kRecord;  // two pages, half a block
   static constexpr int QB = 1;                        // query tiles
   static constexpr uint32_t TO = NB * kTileBlk;       // first column of O
   static constexpr uint32_t Q = kTileRows * HD * 2, KV = kTileBlk * HD * 2;
@@ -1074,8 +1073,8 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
   if (u0 == u1) return;  // the whole CTA, before it holds anything
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(smem_u32(&ctl->kfull[s]), 4 / C::PAGES);
-      if (!C::JOINT) mbar_init(smem_u32(&ctl->vfull[s]), 4 / C::PAGES);
+      mbar_init(smem_u32(&ctl->kfull[s]), 2);
+      if (!C::JOINT) mbar_init(smem_u32(&ctl->vfull[s]), 2);
       mbar_init(smem_u32(&ctl->vempty[s]), 1);
     }
     for (int b = 0; b < NB; ++b) {
@@ -1170,13 +1169,13 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
     if (elect_one()) tc_commit(smem_u32(&ctl->drain));
     __syncwarp();
     mbar_wait(smem_u32(&ctl->drain), 0, a.err, nullptr, a.wait_ns);
-  } else if (warp < 4 || warp >= 8) {
+  } else if (warp < 4) {
     // ------------------------------------------------------------------ unpack
     const PairBits bits;
-    // Steps of PAGES pages are counted through the CTA's blocks; step q belongs to warp q % UNPACK.  A row (position)
-    // per lane, or two lanes (head_dim 128), which take eight words of its keys and eight of its values.
-    constexpr int PP = C::PAGES, PER = 4 / PP, LPR = 2 / PP;
-    const int uw = warp < 4 ? warp - 1 : warp - 5, row = lane / LPR, hc = lane % LPR;
+    // Steps of two pages are counted through the CTA's blocks; step q belongs to warp q % UNPACK.  A row (position)
+    // per lane.
+    constexpr int PP = 2, PER = 2;
+    const int uw = warp - 1, row = lane;
     const uint32_t row_x = (uint32_t)(row & 7) << 4;
     const uint32_t step = (uint32_t)a.n_kv * L::kRecord;
     const uint32_t raw0 = sQ + C::RAWS + (uint32_t)uw * (C::RAW * C::STEP);
@@ -1197,7 +1196,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       }
       if (more) {
         if (n_ids == 0) {  // the ids of this warp's next 32 pages, one per lane
-          const int x = seg.page0 + page + (lane / PP) * (C::UNPACK * PP) + lane % PP;
+          const int x = seg.page0 + page + (lane / PP) * (C::UNPACK * PP) + lane % PP;  // (even lanes: the first of a step's two)
           ids = -1;
           if (x < seg.page1) {
             ids = __ldcg(a.block_table + (size_t)((uint32_t)(ln.tile0 + seg.k) / ln.tps) * a.max_pages + x);
@@ -1208,7 +1207,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
           }
         }
         const uint8_t* head = a.pool + (size_t)seg.g * L::kRecord + lane * 16;
-        const int id0 = __shfl_sync(0xFFFFFFFFu, ids, n_ids), id1 = PP == 2 ? __shfl_sync(0xFFFFFFFFu, ids, n_ids + 1) : id0;
+        const int id0 = __shfl_sync(0xFFFFFFFFu, ids, n_ids), id1 = __shfl_sync(0xFFFFFFFFu, ids, n_ids + 1);
         n_ids = (n_ids + PP) & 31;
         page += C::UNPACK * PP;
         const uint8_t* src0 = head + (uint64_t)(uint32_t)id0 * step;
@@ -1249,15 +1248,15 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       const uint32_t at = (uint32_t)(((q % PER) * PP * 16 + row) * 128);
       copy_wait<C::RAW - 1>();
       __syncwarp();
-      uint4 k[2], v[2];
+      uint4 k[2 * H], v[2 * H];
       uint32_t ks[H], vs[H];
       {
         const uint8_t* rec = raw + slot * C::STEP + (row >> 4) * L::kRecord;
         const int r16 = row & 15;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          k[c] = *reinterpret_cast<const uint4*>(rec + L::kK + r16 * L::kRow + (LPR * c + hc) * 16);
-          v[c] = *reinterpret_cast<const uint4*>(rec + L::kV + r16 * L::kRow + (2 * hc + c) * 16);
+        for (int c = 0; c < 2 * H; ++c) {
+          k[c] = *reinterpret_cast<const uint4*>(rec + L::kK + r16 * L::kRow + c * 16);
+          v[c] = *reinterpret_cast<const uint4*>(rec + L::kV + r16 * L::kRow + c * 16);
         }
 #pragma unroll
         for (int h = 0; h < H; ++h) {
@@ -1281,14 +1280,12 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
           zp[i] = bf16x2_mul(sp[i], kMinus136);
         }
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 2 * H; ++c) {
           const uint32_t w4[4] = {k[c].x, k[c].y, k[c].z, k[c].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            // head_dim 64: word 4c + i; 128: word 4 (hc + 2c) + i, unit 4 hc + i of the c-th 64 columns
-            const int u = HD == 64 ? i & 1 : i;
-            const uint32_t unit = HD == 64 ? (uint32_t)(4 * c + i) << 4 : (uint32_t)(4 * hc + i) << 4;
-            st_shared16(base + (HD == 64 ? 0u : (uint32_t)(c * kTileBlk * 128)) + (unit ^ row_x),
+            const int w = 4 * c + i, u = w % (HD / 32);
+            st_shared16(base + (uint32_t)((w >> 3) * kTileBlk * 128) + (((uint32_t)(w & 7) << 4) ^ row_x),
                         bf16x2_fma(bits.pair<0>(w4[i]), sp[2 * u], zp[2 * u]), bf16x2_fma(bits.pair<1>(w4[i]), sp[2 * u], zp[2 * u]),
                         bf16x2_fma(bits.pair<2>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]),
                         bf16x2_fma(bits.pair<3>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]));
@@ -1312,13 +1309,12 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
           zp[h][1] = bf16x2_mul(sp[h][1], kMinus136);
         }
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 2 * H; ++c) {
           const uint32_t w4[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int h = HD == 64 ? 0 : i & 1;
-            const uint32_t unit = HD == 64 ? (uint32_t)(4 * c + i) << 4 : (uint32_t)(4 * hc + 2 * c + (i >> 1)) << 4;
-            st_shared16(base + (uint32_t)(h * kTileBlk * 128) + (unit ^ row_x),
+            const int w = 4 * c + i, h = w % H;
+            st_shared16(base + (uint32_t)(h * kTileBlk * 128) + (((uint32_t)(w / H) << 4) ^ row_x),
                         bf16x2_fma(bits.pair<0>(w4[i]), sp[h][0], zp[h][0]), bf16x2_fma(bits.pair<1>(w4[i]), sp[h][0], zp[h][0]),
                         bf16x2_fma(bits.pair<2>(w4[i]), sp[h][1], zp[h][1]), bf16x2_fma(bits.pair<3>(w4[i]), sp[h][1], zp[h][1]));
           }
