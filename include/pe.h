@@ -21,7 +21,8 @@
  * The DFlash-style variant: pe_inject_kv projects the verifier's hidden states
  * straight into the drafter's KV cache.
  *
- * A KV cache in 4 bits: pe_pack_kv, pe_unpack_kv, pe_attend_packed.
+ * A KV cache in 4 bits: pe_pack_kv, pe_unpack_kv, pe_attend_packed, and the drafter's
+ * calls over such a cache: pe_draft_forward_packed, pe_step_packed, pe_inject_kv_packed.
  *
  * Conventions shared by every entry point:
  *
@@ -436,6 +437,39 @@ pe_status pe_attend_packed(const pe_config *cfg, const void *q, int64_t q_stride
 /* Bytes of one page of a packed pool, and of pe_attend_packed's workspace (0: invalid config). */
 size_t pe_packed_page_bytes(const pe_config *cfg);
 size_t pe_attend_workspace_bytes(const pe_config *cfg);
+
+/* A packed drafter KV cache: one pool per layer, post-RoPE keys. */
+typedef struct {
+    void *const *pool; /* [L] device pointers (host array) */
+    int32_t num_pages;
+} pe_packed_kv;
+
+/*
+ * pe_draft_forward, pe_step and pe_inject_kv over a packed cache.  Arguments, results and device
+ * checks are theirs, but for three things.  A layer's new k and v rows, rounded to cfg->dtype, are
+ * packed as by pe_pack_kv, and attention is pe_attend_packed's: a row sees every entry, the new
+ * ones too, as the cache keeps it.  The workspace is >= pe_packed_workspace_bytes(cfg) bytes (0:
+ * invalid config; it serves the calls of pe_workspace_bytes as well), of which pe_step_packed
+ * counts all as an output.  And the config has to pass both pe_check_config and the packed calls'
+ * checks.  The trace points are pe_draft_forward's, packing being part of the QKV stage.
+ */
+size_t pe_packed_workspace_bytes(const pe_config *cfg);
+pe_status pe_draft_forward_packed(const pe_config *cfg, const pe_weights *w, const pe_packed_kv *kv,
+                                  const int32_t *block_table, const void *x0, const int32_t *positions,
+                                  const int64_t *slot_mapping, const int32_t *row_list, const int32_t *n_valid,
+                                  const int32_t *draft_rows, void *workspace, size_t workspace_bytes,
+                                  int32_t *draft_tokens, float *logits_dbg, int32_t *err_word, pe_stream_t stream);
+pe_status pe_step_packed(const pe_config *cfg, const pe_weights *w, const pe_packed_kv *kv,
+                         const int32_t *block_table, const int32_t *prev_tokens, const int32_t *prev_pos,
+                         const int32_t *num_accepted, const int32_t *bonus, const void *target_hidden,
+                         const int32_t *target_tokens, void *workspace, size_t workspace_bytes,
+                         int32_t *draft_tokens, int32_t *num_accepted_out, int32_t *bonus_out,
+                         int32_t *next_prev_tokens, int32_t *next_prev_pos, float *logits_dbg, int32_t *err_word,
+                         pe_stream_t stream);
+pe_status pe_inject_kv_packed(const pe_config *cfg, const pe_weights *w, const void *w_inj, const pe_packed_kv *kv,
+                              const int32_t *block_table, const int32_t *prev_pos, const int32_t *num_accepted,
+                              const void *target_hidden, void *workspace, size_t workspace_bytes,
+                              int32_t *err_word, pe_stream_t stream);
 
 /*
  * Tracing (optional).  pe_draft_forward and pe_step can record caller-created

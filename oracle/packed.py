@@ -111,3 +111,44 @@ def attend(q, pool, block_table, row_start, positions, n_q):
             size[r] = np.einsum("ngl,lnd->ngd", w, np.abs(v))
             depth[r] = (np.einsum("ngd,lnd->ngl", np.abs(qd[r]), np.abs(k)).max(-1) / np.sqrt(hd)).reshape(-1)
     return out.reshape(n, -1), size.reshape(n, -1), np.repeat(depth, hd, axis=1)
+
+
+def entry_bytes(shape, slots) -> np.ndarray:
+    """Mask over a pool of this shape: the bytes that hold the entries at slots."""
+    hd = shape[-1] // 18
+    mask = np.zeros(shape, dtype=bool)
+    for slot in slots:
+        page, off = divmod(int(slot), PAGE)
+        for base, row in ((0, hd // 2), (8 * hd, hd // 2), (16 * hd, hd // 16), (17 * hd, hd // 16)):
+            mask[page, :, base + off * row: base + (off + 1) * row] = True
+    return mask
+
+
+def draft_forward(cfg, weights, x0_rows, positions, seqs, block_table, pools, draft_rows) -> dict:
+    """The drafter pass over packed caches that hold the pass's own rows already (as the pass left them).
+
+    The pass of ``oracle.draft_forward`` with every key and value taken from ``pools`` (one per layer), so that
+    the result depends on its inputs without the jumps of rounding to 4 bits.  Rows are in sequence order.
+    Returns logits [n_draft][V] and, per layer, the k (post-RoPE) and v [n][n_kv][hd] of the rows before they are
+    packed."""
+    from . import linear, rmsnorm, rope, widen
+    hd, nq, nkv = cfg.head_dim, cfg.n_q, cfg.n_kv
+    x0 = np.asarray(x0_rows)
+    n = len(positions)
+    row_start = np.searchsorted(np.asarray(seqs), np.arange(len(block_table) + 1))
+    X = linear(x0 if x0.dtype == np.float64 else widen(x0), weights.fc)
+    ks, vs = [], []
+    for l in range(cfg.n_layers):
+        h = linear(rmsnorm(X, weights.norm_attn[l], cfg.rms_eps), weights.wqkv[l]).reshape(n, nq + 2 * nkv, hd)
+        for i in range(n):
+            for g in range(nq + nkv):
+                h[i, g] = rope(h[i, g], positions[i], cfg.rope_theta)
+        ks.append(h[:, nq:nq + nkv])
+        vs.append(h[:, nq + nkv:])
+        out, _, _ = attend(h[:, :nq].reshape(n, -1), pools[l], block_table, row_start, positions, nq)
+        X = X + linear(out, weights.wo[l])
+        gu = linear(rmsnorm(X, weights.norm_mlp[l], cfg.rms_eps), weights.w_gate_up[l])
+        gate, up = gu[:, :cfg.ffn], gu[:, cfg.ffn:]
+        X = X + linear(gate / (1 + np.exp(-gate)) * up, weights.w_down[l])
+    last = rmsnorm(X[np.asarray(draft_rows)], weights.norm_final, cfg.rms_eps)
+    return dict(logits=linear(last, weights.lm_head), new_k=ks, new_v=vs)

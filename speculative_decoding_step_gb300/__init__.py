@@ -17,10 +17,10 @@ import torch
 from .build import LIB, build
 
 __all__ = [
-    "PeError", "Config", "DeviceWeights", "DeviceKV", "lib", "build", "check_config", "workspace_bytes",
+    "PeError", "Config", "DeviceWeights", "DeviceKV", "DevicePackedKV", "lib", "build", "check_config", "workspace_bytes",
     "prepare_batch", "scatter_hidden", "draft_forward", "verify", "step", "status_str",
     "pack_kv", "unpack_kv", "attend_packed", "packed_page_bytes", "attend_workspace_bytes", "alloc_packed_pool",
-    "alloc_attend_workspace",
+    "alloc_attend_workspace", "alloc_packed_workspace", "packed_workspace_bytes",
     "PE_OK", "PE_DEV_BAD_TOKEN", "PE_DEV_BAD_ACCEPTED", "PE_DEV_BAD_PAGE", "PE_DEV_BAD_POSITION",
     "PE_DEV_NONFINITE", "PE_DEV_BAD_ROW", "PE_DEV_TIMEOUT", "EXPORTED_SYMBOLS",
 ]
@@ -40,7 +40,8 @@ EXPORTED_SYMBOLS = ["pe_prepare_batch", "pe_scatter_hidden", "pe_draft_forward",
                     "pe_workspace_bytes", "pe_check_config", "pe_status_str", "pe_set_trace_events",
                     "pe_trace_points", "pe_kernel_launches", "pe_draft_forward_noalloc", "pe_set_wait_limit_ns",
                     "pe_test_skip_pipeline_stage", "pe_inject_kv", "pe_pack_kv", "pe_unpack_kv", "pe_attend_packed",
-                    "pe_packed_page_bytes", "pe_attend_workspace_bytes"]
+                    "pe_packed_page_bytes", "pe_attend_workspace_bytes", "pe_packed_workspace_bytes",
+                    "pe_draft_forward_packed", "pe_step_packed", "pe_inject_kv_packed"]
 
 # Size of the library-owned scratch used by pe_draft_forward_noalloc (PE_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 48 << 20
@@ -84,6 +85,10 @@ class _KV(ctypes.Structure):
                 ("num_pages", ctypes.c_int32)]
 
 
+class _PackedKV(ctypes.Structure):
+    _fields_ = [("pool", ctypes.POINTER(ctypes.c_void_p)), ("num_pages", ctypes.c_int32)]
+
+
 def _ptr(t):
     if t is None:
         return None
@@ -118,6 +123,19 @@ class DeviceKV:
         self.k_cache, self.v_cache = list(k_cache), list(v_cache)
         self._k, self._v = _arr(self.k_cache), _arr(self.v_cache)
         self.struct = _KV(self._k, self._v, self.k_cache[0].shape[0])
+
+
+class DevicePackedKV:
+    """Packed KV cache (alloc_packed_pool per layer) + the pe_packed_kv struct; stands in for a DeviceKV in
+    draft_forward, step, inject_kv and Round."""
+
+    def __init__(self, pools):
+        self.pools = list(pools)
+        for t in self.pools:
+            if not (t.is_cuda and t.dtype is torch.uint8 and t.is_contiguous() and t.shape == self.pools[0].shape):
+                raise ValueError("expected contiguous uint8 CUDA tensors of one shape (alloc_packed_pool)")
+        self._p = _arr(self.pools)
+        self.struct = _PackedKV(self._p, self.pools[0].shape[0])
 
 
 _lib = None
@@ -166,12 +184,18 @@ def lib():
         L.pe_pack_kv.argtypes = [cp, vp, vp, i64, i64, vp, i32, vp, i32, vp, vp]
         L.pe_unpack_kv.argtypes = [cp, vp, i32, vp, i32, vp, vp, i64, i64, vp, vp]
         L.pe_attend_packed.argtypes = [cp, vp, i64, vp, i32, vp, vp, vp, i32, i32, vp, i64, vp, ctypes.c_size_t, vp, vp]
-        for name in ("pe_packed_page_bytes", "pe_attend_workspace_bytes"):
+        L.pe_draft_forward_packed.argtypes = ([cp, ctypes.POINTER(_Weights), ctypes.POINTER(_PackedKV)] + [vp] * 7 +
+                                              [vp, ctypes.c_size_t, vp, vp, vp, vp])
+        L.pe_step_packed.argtypes = ([cp, ctypes.POINTER(_Weights), ctypes.POINTER(_PackedKV)] + [vp] * 7 +
+                                     [vp, ctypes.c_size_t] + [vp] * 8)
+        L.pe_inject_kv_packed.argtypes = [cp, ctypes.POINTER(_Weights), vp, ctypes.POINTER(_PackedKV), vp, vp, vp, vp,
+                                          vp, ctypes.c_size_t, vp, vp]
+        sizes = ("pe_packed_page_bytes", "pe_attend_workspace_bytes", "pe_packed_workspace_bytes")
+        for name in sizes:
             getattr(L, name).restype = ctypes.c_size_t
             getattr(L, name).argtypes = [cp]
         for name in EXPORTED_SYMBOLS:
-            if name not in ("pe_status_str", "pe_workspace_bytes", "pe_kernel_launches", "pe_packed_page_bytes",
-                            "pe_attend_workspace_bytes"):
+            if name not in ("pe_status_str", "pe_workspace_bytes", "pe_kernel_launches") + sizes:
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -249,15 +273,27 @@ def scatter_hidden(cfg, weights: DeviceWeights, target_hidden, meta: dict, x0, e
     _check(st, "pe_scatter_hidden")
 
 
-def draft_forward(cfg, weights: DeviceWeights, kv: DeviceKV, block_table, x0, meta: dict, workspace,
-                  draft_tokens, err, logits_dbg=None, stream=None):
-    """Stages (c)+(d): drafter pass over the valid rows, LM head + argmax -> draft_tokens [B][K]."""
-    st = lib().pe_draft_forward(ctypes.byref(cfg), ctypes.byref(weights.struct), ctypes.byref(kv.struct),
-                                _ptr(block_table), _ptr(x0), _ptr(meta["positions"]), _ptr(meta["slot_mapping"]),
-                                _ptr(meta["row_list"]), _ptr(meta["n_valid"]), _ptr(meta["draft_rows"]),
-                                _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                _ptr(draft_tokens), _ptr(logits_dbg), _ptr(err), _stream(stream))
-    _check(st, "pe_draft_forward")
+def _cache_call(name: str, cfg, kv):
+    """The library's call of this name for a DeviceKV, or its form for a DevicePackedKV, and its name."""
+    if isinstance(kv, DevicePackedKV):
+        name += "_packed"
+        shape = kv.pools[0].shape
+        if len(kv.pools) < cfg.n_layers or shape[1:] != (cfg.n_kv, 18 * cfg.head_dim):
+            raise ValueError(f"kv: expected {cfg.n_layers} pools of [pages][{cfg.n_kv}][{18 * cfg.head_dim}], got "
+                             f"{len(kv.pools)} of {tuple(shape)}")
+    return getattr(lib(), name), name
+
+
+def draft_forward(cfg, weights: DeviceWeights, kv, block_table, x0, meta: dict, workspace, draft_tokens, err,
+                  logits_dbg=None, stream=None):
+    """Stages (c)+(d): drafter pass over the valid rows, LM head + argmax -> draft_tokens [B][K].  ``kv``: a DeviceKV,
+    or a DevicePackedKV with the workspace of alloc_packed_workspace."""
+    call, name = _cache_call("pe_draft_forward", cfg, kv)
+    st = call(ctypes.byref(cfg), ctypes.byref(weights.struct), ctypes.byref(kv.struct), _ptr(block_table), _ptr(x0),
+              _ptr(meta["positions"]), _ptr(meta["slot_mapping"]), _ptr(meta["row_list"]), _ptr(meta["n_valid"]),
+              _ptr(meta["draft_rows"]), _ptr(workspace), workspace.numel() * workspace.element_size(),
+              _ptr(draft_tokens), _ptr(logits_dbg), _ptr(err), _stream(stream))
+    _check(st, name)
 
 
 def draft_forward_noalloc(cfg, weights: DeviceWeights, kv: DeviceKV, block_table, x0, meta: dict, draft_tokens,
@@ -297,16 +333,17 @@ def verify_sampled(cfg, draft_tokens, logits, lse, temperature, target_probs, u_
     _check(st, "pe_verify_sampled")
 
 
-def inject_kv(cfg, weights: DeviceWeights, w_inj, kv: DeviceKV, block_table, prev_pos, num_accepted, target_hidden,
+def inject_kv(cfg, weights: DeviceWeights, w_inj, kv, block_table, prev_pos, num_accepted, target_hidden,
               workspace, err, stream=None):
     """DFlash-style KV injection: the verifier's hidden states of the previous verify batch,
     projected by w_inj [d][d], written as k / v into every layer's cache at the accepted
-    positions (see pe.h)."""
-    st = lib().pe_inject_kv(ctypes.byref(cfg), ctypes.byref(weights.struct), _ptr(w_inj), ctypes.byref(kv.struct),
-                            _ptr(block_table), _ptr(prev_pos), _ptr(num_accepted), _ptr(target_hidden),
-                            _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err),
-                            _stream(stream))
-    _check(st, "pe_inject_kv")
+    positions (see pe.h).  ``kv``: a DeviceKV, or a DevicePackedKV with the workspace of
+    alloc_packed_workspace."""
+    call, name = _cache_call("pe_inject_kv", cfg, kv)
+    st = call(ctypes.byref(cfg), ctypes.byref(weights.struct), _ptr(w_inj), ctypes.byref(kv.struct),
+              _ptr(block_table), _ptr(prev_pos), _ptr(num_accepted), _ptr(target_hidden), _ptr(workspace),
+              workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream))
+    _check(st, name)
 
 
 # The checks of the packed-cache calls.  Small calls take a few microseconds on the GPU, so these go by
@@ -357,6 +394,11 @@ def _pool(cfg, pool, dev: int):
 def packed_page_bytes(cfg) -> int:
     """Bytes of one page (16 positions, every kv head) of a packed cache; 0 for an invalid config."""
     return int(lib().pe_packed_page_bytes(ctypes.byref(cfg)))
+
+
+def packed_workspace_bytes(cfg) -> int:
+    """Workspace of draft_forward, step and inject_kv over a DevicePackedKV (serves the other calls as well)."""
+    return int(lib().pe_packed_workspace_bytes(ctypes.byref(cfg)))
 
 
 def attend_workspace_bytes(cfg) -> int:
@@ -413,16 +455,17 @@ def attend_packed(cfg, q, pool, block_table, row_start, positions, max_rows, out
     _check(st, "pe_attend_packed")
 
 
-def step(cfg, weights: DeviceWeights, kv: DeviceKV, block_table, prev_tokens, prev_pos, num_accepted, bonus,
+def step(cfg, weights: DeviceWeights, kv, block_table, prev_tokens, prev_pos, num_accepted, bonus,
          target_hidden, target_tokens, workspace, out: dict, err, logits_dbg=None, stream=None):
-    """One whole round.  ``out`` holds draft_tokens, num_accepted, bonus, next_prev_tokens, next_prev_pos."""
-    st = lib().pe_step(ctypes.byref(cfg), ctypes.byref(weights.struct), ctypes.byref(kv.struct),
-                       _ptr(block_table), _ptr(prev_tokens), _ptr(prev_pos), _ptr(num_accepted), _ptr(bonus),
-                       _ptr(target_hidden), _ptr(target_tokens), _ptr(workspace),
-                       workspace.numel() * workspace.element_size(), _ptr(out["draft_tokens"]),
-                       _ptr(out["num_accepted"]), _ptr(out["bonus"]), _ptr(out["next_prev_tokens"]),
-                       _ptr(out["next_prev_pos"]), _ptr(logits_dbg), _ptr(err), _stream(stream))
-    _check(st, "pe_step")
+    """One whole round.  ``out`` holds draft_tokens, num_accepted, bonus, next_prev_tokens, next_prev_pos.  ``kv``: a
+    DeviceKV, or a DevicePackedKV with the workspace of alloc_packed_workspace."""
+    call, name = _cache_call("pe_step", cfg, kv)
+    st = call(ctypes.byref(cfg), ctypes.byref(weights.struct), ctypes.byref(kv.struct), _ptr(block_table),
+              _ptr(prev_tokens), _ptr(prev_pos), _ptr(num_accepted), _ptr(bonus), _ptr(target_hidden),
+              _ptr(target_tokens), _ptr(workspace), workspace.numel() * workspace.element_size(),
+              _ptr(out["draft_tokens"]), _ptr(out["num_accepted"]), _ptr(out["bonus"]), _ptr(out["next_prev_tokens"]),
+              _ptr(out["next_prev_pos"]), _ptr(logits_dbg), _ptr(err), _stream(stream))
+    _check(st, name)
 
 
 # ----------------------------------------------------------------------------- buffer helpers
@@ -459,19 +502,27 @@ def alloc_attend_workspace(cfg: Config, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def alloc_packed_workspace(cfg: Config, device="cuda") -> torch.Tensor:
+    n = packed_workspace_bytes(cfg)
+    if n == 0:
+        raise PeError(check_config(cfg) or 2, "pe_packed_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 class Round:
     """Device buffers for one drafter batch plus calls of the five entry points in order.
 
-    ``weights`` / ``kv`` are DeviceWeights / DeviceKV; ``block_table`` an int32 CUDA tensor.
+    ``weights`` is a DeviceWeights, ``kv`` a DeviceKV or DevicePackedKV, ``block_table`` an int32 CUDA tensor.
     Buffers are allocated once here with torch; the library itself allocates nothing.
     """
 
-    def __init__(self, cfg: Config, weights: DeviceWeights, kv: DeviceKV, block_table, device="cuda"):
+    def __init__(self, cfg: Config, weights: DeviceWeights, kv, block_table, device="cuda"):
         self.cfg, self.weights, self.kv, self.block_table = cfg, weights, kv, block_table
         R, T = cfg.B * 2 * cfg.K, cfg.B * cfg.K
         self.meta = alloc_batch(cfg, device)
         self.x0 = torch.empty((R, 2 * cfg.d), dtype=cfg.torch_dtype, device=device)
-        self.workspace = alloc_workspace(cfg, device)
+        packed = isinstance(kv, DevicePackedKV)
+        self.workspace = alloc_packed_workspace(cfg, device) if packed else alloc_workspace(cfg, device)
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
         i32 = dict(dtype=torch.int32, device=device)
         self.draft_tokens = torch.empty((cfg.B, cfg.K), **i32)

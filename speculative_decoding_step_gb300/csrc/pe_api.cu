@@ -175,6 +175,9 @@ struct Plan {
   size_t st_ids, st_pos, st_slot, st_rej, st_mask, st_hmap, st_rows, st_nvalid, st_draft, st_x0;
   size_t samp, samp_acc;
   size_t total = 0;
+  // a packed cache's calls: the layer's new k and v rows before they are packed, attention scratch
+  size_t pk_k = 0, pk_v = 0, pk_attn = 0;
+  size_t packed_total = 0;
 };
 
 Plan make_plan(const pe_config& c) {
@@ -263,8 +266,23 @@ Plan make_plan(const pe_config& c) {
   p.samp = take(sample_stats_bytes(p.T, c.vocab));  // pe_sample_drafts / pe_verify_sampled
   p.samp_acc = take(4 * (size_t)c.B);
   p.total = off;
+  p.pk_k = take(eb * (size_t)p.R * c.n_kv * c.head_dim);
+  p.pk_v = take(eb * (size_t)p.R * c.n_kv * c.head_dim);
+  p.pk_attn = take(packed_attn_workspace_bytes(c.head_dim, c.dtype, p.sms));
+  p.packed_total = off;
   return p;
 }
+
+// The drafter's cache of a call: in the storage type, or packed.
+struct Cache {
+  const pe_kv* kv = nullptr;
+  const pe_packed_kv* packed = nullptr;
+  bool is_packed = false;
+  explicit Cache(const pe_kv* k) : kv(k) {}
+  explicit Cache(const pe_packed_kv* k) : packed(k), is_packed(true) {}
+  int num_pages() const { return is_packed ? packed->num_pages : kv->num_pages; }
+  size_t workspace(const Plan& p) const { return is_packed ? p.packed_total : p.total; }
+};
 
 // ----------------------------------------------------------------------------- TMA descriptors
 
@@ -478,7 +496,17 @@ pe_status check_weights(const pe_config& c, const pe_weights* w) {
   return PE_OK;
 }
 
-pe_status check_kv(const pe_config& c, const pe_kv* kv) {
+pe_status check_cache(const pe_config& c, const Cache& cache) {
+  if (cache.is_packed) {
+    const pe_packed_kv* pk = cache.packed;
+    const pe_status st = check_packed_cfg(&c);
+    if (st != PE_OK) return st;
+    if (pk == nullptr || pk->pool == nullptr || pk->num_pages < 1) return PE_ERR_INVALID_ARG;
+    for (int l = 0; l < c.n_layers; ++l)
+      if (pk->pool[l] == nullptr || !aligned16(pk->pool[l])) return PE_ERR_INVALID_ARG;
+    return PE_OK;
+  }
+  const pe_kv* kv = cache.kv;
   if (kv == nullptr || kv->k_cache == nullptr || kv->v_cache == nullptr || kv->num_pages < 1) return PE_ERR_INVALID_ARG;
   for (int l = 0; l < c.n_layers; ++l)
     if (kv->k_cache[l] == nullptr || kv->v_cache[l] == nullptr || !aligned16(kv->k_cache[l]) ||
@@ -610,7 +638,27 @@ void set_warm_ranges(InitArgs& ia, const pe_config& c, const pe_weights* w) {
   // ~600 pages would make a prologue that finds every translation missing 10-20 us longer
 }
 
-pe_status forward_impl(const pe_config& c, const pe_weights* w, const pe_kv* kv, const int32_t* block_table,
+// Packs the layer's n_rows rows of k and v that its GEMM left in the workspace.
+pe_status pack_layer(const pe_config& c, const Plan& p, void* ws, const pe_packed_kv& pk, int layer, int n_rows,
+                     const int32_t* n_rows_dev, const int64_t* slots, int32_t* err, cudaStream_t s) {
+  PackArgs a{};
+  a.n_rows = n_rows; a.n_dev = n_rows_dev; a.k = at<uint8_t>(ws, p.pk_k); a.v = at<uint8_t>(ws, p.pk_v);
+  a.k_stride = a.v_stride = (long long)c.n_kv * c.head_dim; a.slots = slots; a.n_kv = c.n_kv; a.head_dim = c.head_dim;
+  a.pool = static_cast<uint8_t*>(pk.pool[layer]); a.num_pages = pk.num_pages; a.err = err;
+  PE_TRY_CUDA(launch_pack(a, c.dtype, s));
+  return PE_OK;
+}
+
+// Where a layer's k and v rows go: its cache, or the workspace on their way to a packed one.
+void set_kv_target(GemmArgs& a, const Cache& cache, const Plan& p, void* ws, int layer) {
+  if (cache.is_packed) {
+    a.k_cache = at<uint8_t>(ws, p.pk_k); a.v_cache = at<uint8_t>(ws, p.pk_v); a.tok_slot = nullptr;
+  } else {
+    a.k_cache = cache.kv->k_cache[layer]; a.v_cache = cache.kv->v_cache[layer];
+  }
+}
+
+pe_status forward_impl(const pe_config& c, const pe_weights* w, const Cache& cache, const int32_t* block_table,
                        const void* x0, const int32_t* positions, const int64_t* slot_mapping,
                        const int32_t* row_list, const int32_t* n_valid, const int32_t* draft_rows, void* ws,
                        const Plan& p, int32_t* draft_tokens, float* logits_dbg, int32_t* err, cudaStream_t s,
@@ -670,7 +718,7 @@ pe_status forward_impl(const pe_config& c, const pe_weights* w, const pe_kv* kv,
 
   AttnArgs at_{};
   at_.B = c.B; at_.n_q = c.n_q; at_.n_kv = c.n_kv; at_.head_dim = hd; at_.max_pages = c.max_pages_per_seq;
-  at_.page_size = c.page_size; at_.num_pages = kv->num_pages; at_.scale = 1.0f / sqrtf((float)hd);
+  at_.page_size = c.page_size; at_.num_pages = cache.num_pages(); at_.scale = 1.0f / sqrtf((float)hd);
   at_.q = qb; at_.block_table = block_table; at_.tok_pos = ia.tok_pos; at_.tok_seq = ia.tok_seq;
   at_.seq_start = ia.seq_start; at_.seq_len = ia.seq_len; at_.n_valid = n_valid; at_.items = ia.items;
   at_.seq_minpos = ia.seq_minpos;
@@ -679,6 +727,14 @@ pe_status forward_impl(const pe_config& c, const pe_weights* w, const pe_kv* kv,
   at_.part_l = bf16 ? at<float>(ws, p.part_l) : nullptr;
   at_.part_o = bf16 ? at<float>(ws, p.part_o) : nullptr;
   at_.out = ao; at_.n_rows = p.R; at_.err = err; at_.wait_ns = wait_limit_ns();
+  PackedAttnArgs pa{};
+  if (cache.is_packed) {
+    pa.B = c.B; pa.n_q = c.n_q; pa.n_kv = c.n_kv; pa.head_dim = hd; pa.max_pages = c.max_pages_per_seq;
+    pa.num_pages = cache.num_pages(); pa.n_rows = p.R; pa.max_rows = p.S; pa.scale = at_.scale; pa.q = qb;
+    pa.q_stride = pa.out_stride = (long long)c.n_q * hd; pa.block_table = block_table; pa.positions = ia.tok_pos;
+    pa.row_start = ia.seq_start; pa.row_len = ia.seq_len; pa.out = ao; pa.workspace = at<uint8_t>(ws, p.pk_attn);
+    pa.wait_ns = at_.wait_ns; pa.err = err;
+  }
 
   for (int l = 0; l < c.n_layers; ++l) {
     const int tp = 5 + 7 * l;
@@ -690,18 +746,27 @@ pe_status forward_impl(const pe_config& c, const pe_weights* w, const pe_kv* kv,
     trace(tp + 0, s);
     {
       GemmArgs a = base;
-      a.out_act = qb; a.ld_out = c.n_q * hd; a.k_cache = kv->k_cache[l]; a.v_cache = kv->v_cache[l];
+      a.out_act = qb; a.ld_out = c.n_q * hd;
+      set_kv_target(a, cache, p, ws, l);
       GemmCall call{EPI_QKV_ROPE, &p.qkv, w->wqkv[l], y, c.d, heads * hd / 2, p.R, n_valid, 2, 0};
       pe_status st = run_gemm(c, p, ws, call, a, s);
       if (st != PE_OK) return st;
+      if (cache.is_packed &&
+          (st = pack_layer(c, p, ws, *cache.packed, l, p.R, n_valid, ia.tok_slot, err, s)) != PE_OK)
+        return st;
     }
     trace(tp + 1, s);
-    at_.k_cache = kv->k_cache[l];
-    at_.v_cache = kv->v_cache[l];
+    if (!cache.is_packed) {
+      at_.k_cache = cache.kv->k_cache[l];
+      at_.v_cache = cache.kv->v_cache[l];
+    }
     at_.work_counter = at<int32_t>(ws, p.done) + 1 + l;
-    if (bf16) {
+    if (cache.is_packed) {
+      pa.pool = static_cast<const uint8_t*>(cache.packed->pool[l]);
+      PE_TRY_CUDA(launch_attend_packed(pa, c.dtype, p.sms, s));
+    } else if (bf16) {
       CUtensorMap tk, tv;
-      if (!tmap_kv(&tk, kv->k_cache[l], c, kv->num_pages) || !tmap_kv(&tv, kv->v_cache[l], c, kv->num_pages))
+      if (!tmap_kv(&tk, at_.k_cache, c, at_.num_pages) || !tmap_kv(&tv, at_.v_cache, c, at_.num_pages))
         return PE_ERR_CUDA;
       PE_TRY_CUDA(launch_attention_bf16(tk, tv, at_, p.attn_grid, p.sms, s));
     } else {
@@ -763,6 +828,147 @@ pe_status forward_impl(const pe_config& c, const pe_weights* w, const pe_kv* kv,
   return PE_OK;
 }
 
+pe_status draft_forward_impl(const pe_config* cfg, const pe_weights* w, const Cache& cache,
+                             const int32_t* block_table, const void* x0, const int32_t* positions,
+                             const int64_t* slot_mapping, const int32_t* row_list, const int32_t* n_valid,
+                             const int32_t* draft_rows, void* workspace, size_t workspace_bytes,
+                             int32_t* draft_tokens, float* logits_dbg, int32_t* err_word, cudaStream_t s) {
+  pe_status st = check_cfg(cfg);
+  if (st != PE_OK) return st;
+  if ((st = check_weights(*cfg, w)) != PE_OK) return st;
+  if ((st = check_cache(*cfg, cache)) != PE_OK) return st;
+  if (!block_table || !x0 || !positions || !slot_mapping || !row_list || !n_valid || !draft_rows || !workspace ||
+      !draft_tokens || !err_word)
+    return PE_ERR_INVALID_ARG;
+  if (!aligned16(x0) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PE_ERR_INVALID_ARG;
+  const Plan p = make_plan(*cfg);
+  if (workspace_bytes < cache.workspace(p)) return PE_ERR_SHAPE;
+  for (int i = 0; i < 3; ++i) trace(i, s);
+  return forward_impl(*cfg, w, cache, block_table, x0, positions, slot_mapping, row_list, n_valid, draft_rows,
+                      workspace, p, draft_tokens, logits_dbg, err_word, s);
+}
+
+pe_status step_impl(const pe_config* cfg, const pe_weights* w, const Cache& cache, const int32_t* block_table,
+                    const int32_t* prev_tokens, const int32_t* prev_pos, const int32_t* num_accepted,
+                    const int32_t* bonus, const void* target_hidden, const int32_t* target_tokens, void* workspace,
+                    size_t workspace_bytes, int32_t* draft_tokens, int32_t* num_accepted_out, int32_t* bonus_out,
+                    int32_t* next_prev_tokens, int32_t* next_prev_pos, float* logits_dbg, int32_t* err_word,
+                    cudaStream_t s) {
+  pe_status st = check_cfg(cfg);
+  if (st != PE_OK) return st;
+  if ((st = check_weights(*cfg, w)) != PE_OK) return st;
+  if ((st = check_cache(*cfg, cache)) != PE_OK) return st;
+  if (!block_table || !prev_tokens || !prev_pos || !num_accepted || !bonus || !target_hidden || !target_tokens ||
+      !workspace || !draft_tokens || !num_accepted_out || !bonus_out || !next_prev_tokens || !next_prev_pos ||
+      !err_word)
+    return PE_ERR_INVALID_ARG;
+  if (!aligned16(target_hidden) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PE_ERR_INVALID_ARG;
+  const Plan p = make_plan(*cfg);
+  // the workspace bytes this round would use (a workspace that is too short fails below)
+  if (!step_aliasing_ok(*cfg, block_table, prev_tokens, prev_pos, num_accepted, bonus, target_hidden, target_tokens,
+                        draft_tokens, num_accepted_out, bonus_out, next_prev_tokens, next_prev_pos, logits_dbg,
+                        err_word, workspace, std::min(workspace_bytes, cache.workspace(p))))
+    return PE_ERR_INVALID_ARG;
+  if (workspace_bytes < cache.workspace(p)) return PE_ERR_SHAPE;
+  void* ws = workspace;
+  int32_t* ids = at<int32_t>(ws, p.st_ids);
+  int32_t* pos = at<int32_t>(ws, p.st_pos);
+  int64_t* slot = at<int64_t>(ws, p.st_slot);
+  uint8_t* rej = at<uint8_t>(ws, p.st_rej);
+  uint8_t* msk = at<uint8_t>(ws, p.st_mask);
+  int32_t* hmap = at<int32_t>(ws, p.st_hmap);
+  int32_t* rows = at<int32_t>(ws, p.st_rows);
+  int32_t* nval = at<int32_t>(ws, p.st_nvalid);
+  int32_t* drows = at<int32_t>(ws, p.st_draft);
+  void* x0 = at<uint8_t>(ws, p.st_x0);
+  // the batch rebuild, the input rows and the forward prologue in one launch
+  if (!w->emb || !w->h_shared || !aligned16(w->emb) || !aligned16(w->h_shared)) return PE_ERR_INVALID_ARG;
+  const PrepArgs pa = make_prep_args(*cfg, prev_tokens, prev_pos, num_accepted, bonus, block_table, cache.num_pages(),
+                                     ids, pos, slot, rej, msk, hmap, rows, nval, drows, err_word);
+  const ScatterArgs sa = make_scatter_args(*cfg, w, target_hidden, ids, msk, hmap, rows, nval, x0, err_word);
+  InitArgs ia = make_init_args(*cfg, p, ws, rows, nval, pos, slot, err_word);
+  set_warm_ranges(ia, *cfg, w);
+  trace(0, s);
+  PE_TRY_CUDA(launch_step_prologue(pa, sa, ia, s));
+  trace(1, s);
+  trace(2, s);
+  VerifyArgs va{};
+  va.B = cfg->B; va.K = cfg->K; va.draft = draft_tokens; va.target = target_tokens; va.acc_out = num_accepted_out;
+  va.bonus_out = bonus_out; va.row_list = rows; va.draft_rows = drows; va.positions = pos; va.input_ids = ids;
+  va.next_tokens = next_prev_tokens; va.next_pos = next_prev_pos;
+  const bool bf16 = cfg->dtype == PE_BF16;  // the tensor-core LM head verifies in its finishing CTA
+  st = forward_impl(*cfg, w, cache, block_table, x0, pos, slot, rows, nval, drows, ws, p, draft_tokens, logits_dbg,
+                    err_word, s, true, bf16 ? &va : nullptr);
+  if (st != PE_OK) return st;
+  if (!bf16 && launch_verify(va, s) != cudaSuccess) return PE_ERR_CUDA;
+  trace(7 + 7 * cfg->n_layers, s);
+  return PE_OK;
+}
+
+pe_status inject_kv_impl(const pe_config* cfg, const pe_weights* w, const void* w_inj, const Cache& cache,
+                         const int32_t* block_table, const int32_t* prev_pos, const int32_t* num_accepted,
+                         const void* target_hidden, void* workspace, size_t workspace_bytes, int32_t* err_word,
+                         cudaStream_t s) {
+  pe_status st = check_cfg(cfg);
+  if (st != PE_OK) return st;
+  const pe_config& c = *cfg;
+  if (w == nullptr || w->norm_attn == nullptr || w->wqkv == nullptr) return PE_ERR_INVALID_ARG;
+  for (int l = 0; l < c.n_layers; ++l)
+    if (!w->norm_attn[l] || !w->wqkv[l] || !aligned16(w->norm_attn[l]) || !aligned16(w->wqkv[l]))
+      return PE_ERR_INVALID_ARG;
+  if ((st = check_cache(c, cache)) != PE_OK) return st;
+  if (!w_inj || !block_table || !prev_pos || !num_accepted || !target_hidden || !workspace || !err_word)
+    return PE_ERR_INVALID_ARG;
+  if (!aligned16(w_inj) || !aligned16(target_hidden) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return PE_ERR_INVALID_ARG;
+  const Plan p = make_plan(c);
+  if (workspace_bytes < cache.workspace(p)) return PE_ERR_SHAPE;
+  void* ws = workspace;
+  const bool bf16 = c.dtype == PE_BF16;
+  const int NI = c.B * (c.K + 1);
+  const int hd = c.head_dim;
+  InjectArgs ia{};
+  ia.B = c.B; ia.K = c.K; ia.max_pages = c.max_pages_per_seq; ia.num_pages = cache.num_pages();
+  ia.page_size = c.page_size; ia.prev_pos = prev_pos; ia.num_accepted = num_accepted; ia.block_table = block_table;
+  ia.tok_pos = at<int32_t>(ws, p.tok_pos); ia.tok_slot = at<int64_t>(ws, p.tok_slot); ia.err = err_word;
+  PE_TRY_CUDA(launch_inject_init(ia, s));
+
+  GemmArgs base{};
+  base.n_q = c.n_q; base.n_kv = c.n_kv; base.head_dim = hd; set_rope_table(base, c.rope_theta, hd);
+  base.tok_pos = ia.tok_pos; base.tok_slot = ia.tok_slot; base.err = err_word;
+  float* x = at<float>(ws, p.x);
+  void* y = at<uint8_t>(ws, p.y);
+  // x = H . W_inj^T over every element of the verify batch (the rejected ones are computed but
+  // never written: their slot is -1)
+  {
+    GemmArgs a = base;
+    a.out_f32 = x; a.ld_out = c.d;
+    GemmCall call{EPI_STORE_F32, &p.inj, w_inj, target_hidden, c.d, c.d, NI, nullptr, 0, (uint64_t)c.d};
+    if ((st = run_gemm(c, p, ws, call, a, s)) != PE_OK) return st;
+  }
+  for (int l = 0; l < c.n_layers; ++l) {
+    NormArgs n{};
+    n.x = x; n.d = c.d; n.row_map = nullptr; n.n_rows = NI; n.n_rows_dev = nullptr; n.src_rows = NI;
+    n.g = w->norm_attn[l]; n.eps = c.rms_eps; n.y = y; n.err = err_word;
+    if (bf16 && p.inj.k_splits > 1 && l == 0) {  // the first norm also sums W_inj's split-K partials
+      n.part = at<float>(ws, p.split_part); n.n_splits = p.inj.k_splits; n.bn = p.inj.bn; n.n_t = p.inj.n_t;
+      n.g_ntok = NI; n.g_ntok_dev = nullptr; n.g_ntok_min = NI; n.x = nullptr; n.x_out = x;
+    }
+    PE_TRY_CUDA(launch_rmsnorm(n, c.dtype, s));
+    GemmArgs a = base;
+    a.out_act = at<uint8_t>(ws, p.q); a.ld_out = c.n_q * hd;  // no q heads here: never written
+    set_kv_target(a, cache, p, ws, l);
+    a.head0 = c.n_q;
+    const void* wkv = static_cast<const uint8_t*>(w->wqkv[l]) + (size_t)c.n_q * hd * c.d * elem_bytes(c.dtype);
+    GemmCall call{EPI_QKV_ROPE, &p.injkv, wkv, y, c.d, c.n_kv * hd, NI, nullptr, 2, (uint64_t)(2 * c.n_kv)};
+    if ((st = run_gemm(c, p, ws, call, a, s)) != PE_OK) return st;
+    if (cache.is_packed &&
+        (st = pack_layer(c, p, ws, *cache.packed, l, NI, nullptr, ia.tok_slot, err_word, s)) != PE_OK)
+      return st;
+  }
+  return PE_OK;
+}
+
 }  // namespace
 }  // namespace pe
 
@@ -788,6 +994,11 @@ pe_status pe_check_config(const pe_config* cfg) { return check_cfg(cfg); }
 size_t pe_workspace_bytes(const pe_config* cfg) {
   if (check_cfg(cfg) != PE_OK) return 0;
   return make_plan(*cfg).total;
+}
+
+size_t pe_packed_workspace_bytes(const pe_config* cfg) {
+  if (check_cfg(cfg) != PE_OK || check_packed_cfg(cfg) != PE_OK) return 0;
+  return make_plan(*cfg).packed_total;
 }
 
 pe_status pe_prepare_batch(const pe_config* cfg, const int32_t* prev_tokens, const int32_t* prev_pos,
@@ -830,19 +1041,19 @@ pe_status pe_draft_forward(const pe_config* cfg, const pe_weights* w, const pe_k
                            const int32_t* row_list, const int32_t* n_valid, const int32_t* draft_rows,
                            void* workspace, size_t workspace_bytes, int32_t* draft_tokens, float* logits_dbg,
                            int32_t* err_word, pe_stream_t stream) {
-  pe_status st = check_cfg(cfg);
-  if (st != PE_OK) return st;
-  if ((st = check_weights(*cfg, w)) != PE_OK) return st;
-  if ((st = check_kv(*cfg, kv)) != PE_OK) return st;
-  if (!block_table || !x0 || !positions || !slot_mapping || !row_list || !n_valid || !draft_rows || !workspace ||
-      !draft_tokens || !err_word)
-    return PE_ERR_INVALID_ARG;
-  if (!aligned16(x0) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PE_ERR_INVALID_ARG;
-  const Plan p = make_plan(*cfg);
-  if (workspace_bytes < p.total) return PE_ERR_SHAPE;
-  for (int i = 0; i < 3; ++i) trace(i, (cudaStream_t)stream);
-  return forward_impl(*cfg, w, kv, block_table, x0, positions, slot_mapping, row_list, n_valid, draft_rows,
-                      workspace, p, draft_tokens, logits_dbg, err_word, (cudaStream_t)stream);
+  return draft_forward_impl(cfg, w, Cache(kv), block_table, x0, positions, slot_mapping, row_list, n_valid,
+                            draft_rows, workspace, workspace_bytes, draft_tokens, logits_dbg, err_word,
+                            (cudaStream_t)stream);
+}
+
+pe_status pe_draft_forward_packed(const pe_config* cfg, const pe_weights* w, const pe_packed_kv* kv,
+                                  const int32_t* block_table, const void* x0, const int32_t* positions,
+                                  const int64_t* slot_mapping, const int32_t* row_list, const int32_t* n_valid,
+                                  const int32_t* draft_rows, void* workspace, size_t workspace_bytes,
+                                  int32_t* draft_tokens, float* logits_dbg, int32_t* err_word, pe_stream_t stream) {
+  return draft_forward_impl(cfg, w, Cache(kv), block_table, x0, positions, slot_mapping, row_list, n_valid,
+                            draft_rows, workspace, workspace_bytes, draft_tokens, logits_dbg, err_word,
+                            (cudaStream_t)stream);
 }
 
 pe_status pe_verify(const pe_config* cfg, const int32_t* draft_tokens, const int32_t* target_tokens,
@@ -863,56 +1074,20 @@ pe_status pe_step(const pe_config* cfg, const pe_weights* w, const pe_kv* kv, co
                   size_t workspace_bytes, int32_t* draft_tokens, int32_t* num_accepted_out, int32_t* bonus_out,
                   int32_t* next_prev_tokens, int32_t* next_prev_pos, float* logits_dbg, int32_t* err_word,
                   pe_stream_t stream) {
-  pe_status st = check_cfg(cfg);
-  if (st != PE_OK) return st;
-  if ((st = check_weights(*cfg, w)) != PE_OK) return st;
-  if ((st = check_kv(*cfg, kv)) != PE_OK) return st;
-  if (!block_table || !prev_tokens || !prev_pos || !num_accepted || !bonus || !target_hidden || !target_tokens ||
-      !workspace || !draft_tokens || !num_accepted_out || !bonus_out || !next_prev_tokens || !next_prev_pos ||
-      !err_word)
-    return PE_ERR_INVALID_ARG;
-  if (!aligned16(target_hidden) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PE_ERR_INVALID_ARG;
-  const Plan p = make_plan(*cfg);
-  // the workspace bytes this round would use (a workspace that is too short fails below)
-  if (!step_aliasing_ok(*cfg, block_table, prev_tokens, prev_pos, num_accepted, bonus, target_hidden, target_tokens,
-                        draft_tokens, num_accepted_out, bonus_out, next_prev_tokens, next_prev_pos, logits_dbg,
-                        err_word, workspace, std::min(workspace_bytes, p.total)))
-    return PE_ERR_INVALID_ARG;
-  if (workspace_bytes < p.total) return PE_ERR_SHAPE;
-  cudaStream_t s = (cudaStream_t)stream;
-  void* ws = workspace;
-  int32_t* ids = at<int32_t>(ws, p.st_ids);
-  int32_t* pos = at<int32_t>(ws, p.st_pos);
-  int64_t* slot = at<int64_t>(ws, p.st_slot);
-  uint8_t* rej = at<uint8_t>(ws, p.st_rej);
-  uint8_t* msk = at<uint8_t>(ws, p.st_mask);
-  int32_t* hmap = at<int32_t>(ws, p.st_hmap);
-  int32_t* rows = at<int32_t>(ws, p.st_rows);
-  int32_t* nval = at<int32_t>(ws, p.st_nvalid);
-  int32_t* drows = at<int32_t>(ws, p.st_draft);
-  void* x0 = at<uint8_t>(ws, p.st_x0);
-  // the batch rebuild, the input rows and the forward prologue in one launch
-  if (!w->emb || !w->h_shared || !aligned16(w->emb) || !aligned16(w->h_shared)) return PE_ERR_INVALID_ARG;
-  const PrepArgs pa = make_prep_args(*cfg, prev_tokens, prev_pos, num_accepted, bonus, block_table, kv->num_pages, ids,
-                                     pos, slot, rej, msk, hmap, rows, nval, drows, err_word);
-  const ScatterArgs sa = make_scatter_args(*cfg, w, target_hidden, ids, msk, hmap, rows, nval, x0, err_word);
-  InitArgs ia = make_init_args(*cfg, p, ws, rows, nval, pos, slot, err_word);
-  set_warm_ranges(ia, *cfg, w);
-  trace(0, s);
-  PE_TRY_CUDA(launch_step_prologue(pa, sa, ia, s));
-  trace(1, s);
-  trace(2, s);
-  VerifyArgs va{};
-  va.B = cfg->B; va.K = cfg->K; va.draft = draft_tokens; va.target = target_tokens; va.acc_out = num_accepted_out;
-  va.bonus_out = bonus_out; va.row_list = rows; va.draft_rows = drows; va.positions = pos; va.input_ids = ids;
-  va.next_tokens = next_prev_tokens; va.next_pos = next_prev_pos;
-  const bool bf16 = cfg->dtype == PE_BF16;  // the tensor-core LM head verifies in its finishing CTA
-  st = forward_impl(*cfg, w, kv, block_table, x0, pos, slot, rows, nval, drows, ws, p, draft_tokens, logits_dbg,
-                    err_word, s, true, bf16 ? &va : nullptr);
-  if (st != PE_OK) return st;
-  if (!bf16 && launch_verify(va, s) != cudaSuccess) return PE_ERR_CUDA;
-  trace(7 + 7 * cfg->n_layers, s);
-  return PE_OK;
+  return step_impl(cfg, w, Cache(kv), block_table, prev_tokens, prev_pos, num_accepted, bonus, target_hidden,
+                   target_tokens, workspace, workspace_bytes, draft_tokens, num_accepted_out, bonus_out,
+                   next_prev_tokens, next_prev_pos, logits_dbg, err_word, (cudaStream_t)stream);
+}
+
+pe_status pe_step_packed(const pe_config* cfg, const pe_weights* w, const pe_packed_kv* kv,
+                         const int32_t* block_table, const int32_t* prev_tokens, const int32_t* prev_pos,
+                         const int32_t* num_accepted, const int32_t* bonus, const void* target_hidden,
+                         const int32_t* target_tokens, void* workspace, size_t workspace_bytes, int32_t* draft_tokens,
+                         int32_t* num_accepted_out, int32_t* bonus_out, int32_t* next_prev_tokens,
+                         int32_t* next_prev_pos, float* logits_dbg, int32_t* err_word, pe_stream_t stream) {
+  return step_impl(cfg, w, Cache(kv), block_table, prev_tokens, prev_pos, num_accepted, bonus, target_hidden,
+                   target_tokens, workspace, workspace_bytes, draft_tokens, num_accepted_out, bonus_out,
+                   next_prev_tokens, next_prev_pos, logits_dbg, err_word, (cudaStream_t)stream);
 }
 
 pe_status pe_sample_drafts(const pe_config* cfg, const float* logits, const float* u_draft, float temperature,
@@ -962,62 +1137,16 @@ pe_status pe_inject_kv(const pe_config* cfg, const pe_weights* w, const void* w_
                        const int32_t* block_table, const int32_t* prev_pos, const int32_t* num_accepted,
                        const void* target_hidden, void* workspace, size_t workspace_bytes, int32_t* err_word,
                        pe_stream_t stream) {
-  pe_status st = check_cfg(cfg);
-  if (st != PE_OK) return st;
-  const pe_config& c = *cfg;
-  if (w == nullptr || w->norm_attn == nullptr || w->wqkv == nullptr) return PE_ERR_INVALID_ARG;
-  for (int l = 0; l < c.n_layers; ++l)
-    if (!w->norm_attn[l] || !w->wqkv[l] || !aligned16(w->norm_attn[l]) || !aligned16(w->wqkv[l]))
-      return PE_ERR_INVALID_ARG;
-  if ((st = check_kv(c, kv)) != PE_OK) return st;
-  if (!w_inj || !block_table || !prev_pos || !num_accepted || !target_hidden || !workspace || !err_word)
-    return PE_ERR_INVALID_ARG;
-  if (!aligned16(w_inj) || !aligned16(target_hidden) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-    return PE_ERR_INVALID_ARG;
-  const Plan p = make_plan(c);
-  if (workspace_bytes < p.total) return PE_ERR_SHAPE;
-  cudaStream_t s = (cudaStream_t)stream;
-  void* ws = workspace;
-  const bool bf16 = c.dtype == PE_BF16;
-  const int NI = c.B * (c.K + 1);
-  const int hd = c.head_dim;
-  InjectArgs ia{};
-  ia.B = c.B; ia.K = c.K; ia.max_pages = c.max_pages_per_seq; ia.num_pages = kv->num_pages;
-  ia.page_size = c.page_size; ia.prev_pos = prev_pos; ia.num_accepted = num_accepted; ia.block_table = block_table;
-  ia.tok_pos = at<int32_t>(ws, p.tok_pos); ia.tok_slot = at<int64_t>(ws, p.tok_slot); ia.err = err_word;
-  PE_TRY_CUDA(launch_inject_init(ia, s));
+  return inject_kv_impl(cfg, w, w_inj, Cache(kv), block_table, prev_pos, num_accepted, target_hidden, workspace,
+                        workspace_bytes, err_word, (cudaStream_t)stream);
+}
 
-  GemmArgs base{};
-  base.n_q = c.n_q; base.n_kv = c.n_kv; base.head_dim = hd; set_rope_table(base, c.rope_theta, hd);
-  base.tok_pos = ia.tok_pos; base.tok_slot = ia.tok_slot; base.err = err_word;
-  float* x = at<float>(ws, p.x);
-  void* y = at<uint8_t>(ws, p.y);
-  // x = H . W_inj^T over every element of the verify batch (the rejected ones are computed but
-  // never written: their slot is -1)
-  {
-    GemmArgs a = base;
-    a.out_f32 = x; a.ld_out = c.d;
-    GemmCall call{EPI_STORE_F32, &p.inj, w_inj, target_hidden, c.d, c.d, NI, nullptr, 0, (uint64_t)c.d};
-    if ((st = run_gemm(c, p, ws, call, a, s)) != PE_OK) return st;
-  }
-  for (int l = 0; l < c.n_layers; ++l) {
-    NormArgs n{};
-    n.x = x; n.d = c.d; n.row_map = nullptr; n.n_rows = NI; n.n_rows_dev = nullptr; n.src_rows = NI;
-    n.g = w->norm_attn[l]; n.eps = c.rms_eps; n.y = y; n.err = err_word;
-    if (bf16 && p.inj.k_splits > 1 && l == 0) {  // the first norm also sums W_inj's split-K partials
-      n.part = at<float>(ws, p.split_part); n.n_splits = p.inj.k_splits; n.bn = p.inj.bn; n.n_t = p.inj.n_t;
-      n.g_ntok = NI; n.g_ntok_dev = nullptr; n.g_ntok_min = NI; n.x = nullptr; n.x_out = x;
-    }
-    PE_TRY_CUDA(launch_rmsnorm(n, c.dtype, s));
-    GemmArgs a = base;
-    a.out_act = at<uint8_t>(ws, p.q); a.ld_out = c.n_q * hd;  // no q heads here: never written
-    a.k_cache = kv->k_cache[l]; a.v_cache = kv->v_cache[l];
-    a.head0 = c.n_q;
-    const void* wkv = static_cast<const uint8_t*>(w->wqkv[l]) + (size_t)c.n_q * hd * c.d * elem_bytes(c.dtype);
-    GemmCall call{EPI_QKV_ROPE, &p.injkv, wkv, y, c.d, c.n_kv * hd, NI, nullptr, 2, (uint64_t)(2 * c.n_kv)};
-    if ((st = run_gemm(c, p, ws, call, a, s)) != PE_OK) return st;
-  }
-  return PE_OK;
+pe_status pe_inject_kv_packed(const pe_config* cfg, const pe_weights* w, const void* w_inj, const pe_packed_kv* kv,
+                              const int32_t* block_table, const int32_t* prev_pos, const int32_t* num_accepted,
+                              const void* target_hidden, void* workspace, size_t workspace_bytes, int32_t* err_word,
+                              pe_stream_t stream) {
+  return inject_kv_impl(cfg, w, w_inj, Cache(kv), block_table, prev_pos, num_accepted, target_hidden, workspace,
+                        workspace_bytes, err_word, (cudaStream_t)stream);
 }
 
 pe_status pe_pack_kv(const pe_config* cfg, const void* k, const void* v, int64_t k_stride, int64_t v_stride,

@@ -245,7 +245,7 @@ struct GemmArgs {
   // a float and the float nearest its remainder (i < head_dim / 2 <= 64)
   float rope_tf_hi[64], rope_tf_lo[64];
   const int32_t* tok_pos;
-  const int64_t* tok_slot;
+  const int64_t* tok_slot;   // nullable: row t's k and v go to row t of k_cache and v_cache
   void *k_cache, *v_cache;
   unsigned long long* keys;  // LM head: one key per token (zero before the launch)
   float* logits_dbg;         // nullable [tokens][n_out]
