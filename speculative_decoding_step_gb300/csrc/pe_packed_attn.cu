@@ -1511,13 +1511,16 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
 constexpr int kMergeThreads = 256;
 
 // A CTA per (tile, head), or one of `shares` (grid's y) that take its vectors in turn: it finds the CTAs that
-// hold parts of the range, then its warps take the vectors, `split` warps (a power of two, at most 8) for each, every split-th record a warp; these join in
-// shared memory.  Lanes over the entries.  Sums run in CTA order within a warp, then in warp order.
-template <typename T, int HD>
+// hold parts of the range, then its warps take the vectors, 16 bytes of a vector a lane and U vectors a lane at a
+// time; `split` warps (a power of two, at most 8) share the records of the same vectors and join in shared
+// memory.  Sums run in CTA order within a warp, then in warp order.  It is bound by the time of its loads
+// (each range has few records), so what counts is how many a warp has under way.
+template <typename T, int HD, int U>
 __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const PackedAttnArgs a, const Line ln, int grid,
                                                                      int split) {
-  constexpr int VPL = HD / 32, CB = 4;
-  __shared__ float sh_m[8], sh_l[8], sh_o[8][HD];
+  constexpr int CB = 4 / U, LPV = HD / 4, VW = 32 / LPV;  // records at a time; lanes per vector, vectors per warp
+  __shared__ float sh_m[8][U][VW], sh_l[8][U][VW];
+  __shared__ float4 sh_o[8][U][32];
   pdl_wait();
   pdl_trigger();
   const int k = (int)(blockIdx.x / ln.heads), g = (int)blockIdx.x - k * a.n_kv;
@@ -1532,85 +1535,95 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
   const int c0 = (int)cuts.piece(start + ln.range_cost), c1 = (int)cuts.piece(start + len - 1);
   if (c0 == c1) return;  // finished by its CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = warp & (split - 1), per = 8 / split;  // vectors at a time
+  const int sub = warp & (split - 1), teams = 8 / split;
+  const int vl = lane / LPV, el = lane % LPV * 4;  // the lane's vector of the warp's, its first entry
+  const int per = teams * U * VW;                  // vectors at a time
   for (int v0 = blockIdx.y * per; v0 < tr.M; v0 += gridDim.y * per) {  // the same trip count for every warp
-    const int v = v0 + warp / split;
-    float mx = -INFINITY, sum = 0.f, x[VPL];
+    const int va = v0 + warp / split * U * VW + vl;  // vector u of the lane: va + u * VW
+    float mx[U], sum[U];
+    float4 x[U];
 #pragma unroll
-    for (int e = 0; e < VPL; ++e) x[e] = 0.f;
-    if (v < tr.M) {
-      for (int c = c0 + sub; c <= c1; c += CB * split) {
-        float m[CB], l[CB], y[CB][VPL];
+    for (int u = 0; u < U; ++u) {
+      mx[u] = -INFINITY;
+      sum[u] = 0.f;
+      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int c = c0 + sub; c <= c1; c += CB * split) {
+      float m[U][CB], l[U][CB];
+      float4 y[U][CB];
 #pragma unroll
-        for (int i = 0; i < CB; ++i) {
-          const int cc = c + i * split;
-          m[i] = -INFINITY;
-          l[i] = 0.f;
+      for (int i = 0; i < CB; ++i) {
+        const int cc = c + i * split;
+        const float* rec = part_record<HD>(ln, min(cc, c1), cc == c0);
 #pragma unroll
-          for (int e = 0; e < VPL; ++e) y[i][e] = 0.f;
-          if (cc <= c1) {
-            const float* rec = part_record<HD>(ln, cc, cc == c0);
-            m[i] = __ldcg(rec + v);
-            l[i] = __ldcg(rec + ln.tile_rows + v);
-            const float* src = rec + 2 * ln.tile_rows + (size_t)v * HD + lane * VPL;
-            if constexpr (VPL == 4) {
-              const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
-              y[i][0] = z.x; y[i][1] = z.y; y[i][2] = z.z; y[i][3] = z.w;
-            } else {
-              const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
-              y[i][0] = z.x; y[i][1] = z.y;
-            }
+        for (int u = 0; u < U; ++u) {
+          const int v = va + u * VW;
+          m[u][i] = -INFINITY;
+          l[u][i] = 0.f;
+          y[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (cc <= c1 && v < tr.M) {
+            m[u][i] = __ldcg(rec + v);
+            l[u][i] = __ldcg(rec + ln.tile_rows + v);
+            y[u][i] = __ldcg(reinterpret_cast<const float4*>(rec + 2 * ln.tile_rows + (size_t)v * HD + el));
           }
         }
-        float nx = mx;
+      }
 #pragma unroll
-        for (int i = 0; i < CB; ++i) nx = fmaxf(nx, m[i]);
+      for (int u = 0; u < U; ++u) {
+        float nx = mx[u];
+#pragma unroll
+        for (int i = 0; i < CB; ++i) nx = fmaxf(nx, m[u][i]);
         if (nx == -INFINITY) continue;
-        const float f = ex2_approx(mx - nx);
-        sum *= f;
-#pragma unroll
-        for (int e = 0; e < VPL; ++e) x[e] *= f;
+        const float f = ex2_approx(mx[u] - nx);
+        sum[u] *= f;
+        x[u].x *= f; x[u].y *= f; x[u].z *= f; x[u].w *= f;
 #pragma unroll
         for (int i = 0; i < CB; ++i) {
-          const float w = ex2_approx(m[i] - nx);
-          sum = fmaf(w, l[i], sum);
-#pragma unroll
-          for (int e = 0; e < VPL; ++e) x[e] = fmaf(w, y[i][e], x[e]);
+          const float w = ex2_approx(m[u][i] - nx);
+          sum[u] = fmaf(w, l[u][i], sum[u]);
+          x[u].x = fmaf(w, y[u][i].x, x[u].x); x[u].y = fmaf(w, y[u][i].y, x[u].y);
+          x[u].z = fmaf(w, y[u][i].z, x[u].z); x[u].w = fmaf(w, y[u][i].w, x[u].w);
         }
-        mx = nx;
+        mx[u] = nx;
       }
     }
     if (split > 1) {
       __syncthreads();  // the last vectors' values have been read
-      if (lane == 0) {
-        sh_m[warp] = mx;
-        sh_l[warp] = sum;
-      }
 #pragma unroll
-      for (int e = 0; e < VPL; ++e) sh_o[warp][lane * VPL + e] = x[e];
+      for (int u = 0; u < U; ++u) {
+        if (el == 0) {
+          sh_m[warp][u][vl] = mx[u];
+          sh_l[warp][u][vl] = sum[u];
+        }
+        sh_o[warp][u][lane] = x[u];
+      }
       __syncthreads();
       if (sub == 0)
-        for (int w = warp + 1; w < warp + split; ++w) {
-          const float m = sh_m[w], nx = fmaxf(mx, m);
-          if (nx == -INFINITY) continue;
-          const float f = ex2_approx(mx - nx), q = ex2_approx(m - nx);
-          sum = sum * f + q * sh_l[w];
+        for (int w = warp + 1; w < warp + split; ++w)
 #pragma unroll
-          for (int e = 0; e < VPL; ++e) x[e] = x[e] * f + q * sh_o[w][lane * VPL + e];
-          mx = nx;
-        }
+          for (int u = 0; u < U; ++u) {
+            const float m = sh_m[w][u][vl], nx = fmaxf(mx[u], m);
+            if (nx == -INFINITY) continue;
+            const float f = ex2_approx(mx[u] - nx), q = ex2_approx(m - nx);
+            const float4 y = sh_o[w][u][lane];
+            sum[u] = sum[u] * f + q * sh_l[w][u][vl];
+            x[u].x = x[u].x * f + q * y.x; x[u].y = x[u].y * f + q * y.y;
+            x[u].z = x[u].z * f + q * y.z; x[u].w = x[u].w * f + q * y.w;
+            mx[u] = nx;
+          }
     }
-    if (sub != 0 || v >= tr.M) continue;
-    const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
-    const int m = tr.m0 + v, r = (int)((uint32_t)m / ln.group);
-    T* out = static_cast<T*>(a.out) + (tr.r0 + r) * a.out_stride + (g * ln.G + m - r * ln.G) * HD + lane * VPL;
-    if constexpr (sizeof(T) == 4) {
+    if (sub != 0) continue;
 #pragma unroll
-      for (int e = 0; e < VPL; ++e) out[e] = x[e] * inv;
-    } else if constexpr (VPL == 4) {
-      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
-    } else {
-      *reinterpret_cast<uint32_t*>(out) = pack_bf16(x[0] * inv, x[1] * inv);
+    for (int u = 0; u < U; ++u) {
+      const int v = va + u * VW;
+      if (v >= tr.M) continue;
+      const float inv = sum[u] > 0.f ? kPackedUnit / sum[u] : 0.f;
+      const int m = tr.m0 + v, r = (int)((uint32_t)m / ln.group);
+      T* out = static_cast<T*>(a.out) + (tr.r0 + r) * a.out_stride + (g * ln.G + m - r * ln.G) * HD + el;
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(out) = make_float4(x[u].x * inv, x[u].y * inv, x[u].z * inv, x[u].w * inv);
+      else
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[u].x * inv, x[u].y * inv), pack_bf16(x[u].z * inv, x[u].w * inv));
     }
   }
 }
@@ -1633,15 +1646,16 @@ cudaError_t allow_smem(size_t bytes) {
   return cudaSuccess;
 }
 
-template <typename T, int HD>
+template <typename T, int HD, int U>
 cudaError_t launch_merge(const PackedAttnArgs& a, const Line& ln, int grid, int sms, cudaStream_t s) {
-  // few ranges: each may be cut into many records
+  // warps that the vectors leave idle share records, and so they do where few ranges are cut into many
   const long long ranges = (long long)ln.n_tiles * a.n_kv;
+  const int per = 8 * U * (128 / HD);  // vectors that a CTA's warps take at a time when none share
   int split = 1;
-  while (split < 8 && ranges * split * 8 < grid) split *= 2;
-  const long long shares = std::min<long long>(ln.tile_rows * split / 8, (8LL * sms + ranges - 1) / ranges);
-  return launch_pdl(attend_merge_kernel<T, HD>, dim3((unsigned)ranges, (unsigned)std::max(1LL, shares)), dim3(kMergeThreads), 0, s,
-                    a, ln, grid, split);
+  while (split < 8 && (per / split > ln.tile_rows || ranges * split * 8 < grid)) split *= 2;
+  const long long shares = std::min<long long>(ln.tile_rows * split / per, (8LL * sms + ranges - 1) / ranges);
+  return launch_pdl(attend_merge_kernel<T, HD, U>, dim3((unsigned)ranges, (unsigned)std::max(1LL, shares)),
+                    dim3(kMergeThreads), 0, s, a, ln, grid, split);
 }
 
 // The longest that a range can be.
@@ -1698,7 +1712,7 @@ cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
     ln.grid = make_div(grid);
     e = launch_pdl(attend_small_kernel<T, HD, NQ>, dim3(grid), dim3(kSmallWarps * 32), C::smem(ln.n_tiles), s, a, ln);
     if (e != cudaSuccess) return e;
-    if (!ln.whole && grid > 1 && (e = launch_merge<T, HD>(a, ln, grid, sms, s)) != cudaSuccess) return e;
+    if (!ln.whole && grid > 1 && (e = launch_merge<T, HD, 1>(a, ln, grid, sms, s)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
@@ -1721,7 +1735,7 @@ cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
     ln.grid = make_div(grid);
     e = launch_pdl(attend_tile_kernel<HD>, dim3(grid), dim3(C::THREADS), C::smem(ln.n_tiles), s, a, ln);
     if (e != cudaSuccess) return e;
-    if (!ln.whole && grid > 1 && (e = launch_merge<__nv_bfloat16, HD>(a, ln, grid, sms, s)) != cudaSuccess) return e;
+    if (!ln.whole && grid > 1 && (e = launch_merge<__nv_bfloat16, HD, 2>(a, ln, grid, sms, s)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
