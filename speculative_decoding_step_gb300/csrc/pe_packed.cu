@@ -9,31 +9,88 @@ namespace pe {
 
 namespace {
 
-constexpr int kPackThreads = 256;
+constexpr int kPackThreads = 128;  // (256: 0 to 2 us more for both kernels)
 
-template <typename T>
-PE_DEV void load16(const T* p, float (&x)[16]);
-template <>
-PE_DEV void load16<float>(const float* p, float (&x)[16]) {
+// Eight entries at a 16-byte boundary: their values, and the bits of the largest magnitude as fp32 (at least
+// kInfBits: one is infinite or NaN).  Magnitudes compare as whole numbers, bf16 two at a time.
+constexpr uint32_t kInfBits = 0x7F800000u;
+struct Eight {
+  float x[8];
+  uint32_t top;
+  PE_DEV void load(const float* p) {
+    top = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float4 t = __ldcg(reinterpret_cast<const float4*>(p) + k);
-    x[4 * k] = t.x; x[4 * k + 1] = t.y; x[4 * k + 2] = t.z; x[4 * k + 3] = t.w;
+    for (int k = 0; k < 2; ++k) {
+      const float4 t = __ldcg(reinterpret_cast<const float4*>(p) + k);
+      x[4 * k] = t.x; x[4 * k + 1] = t.y; x[4 * k + 2] = t.z; x[4 * k + 3] = t.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
   }
-}
-template <>
-PE_DEV void load16<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[16]) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint4 t = __ldcg(reinterpret_cast<const uint4*>(p) + k);
+  PE_DEV void load(const __nv_bfloat16* p) {
+    const uint4 t = __ldcg(reinterpret_cast<const uint4*>(p));
     const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+    uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[8 * k + 2 * e] = __uint_as_float(w[e] << 16);
-      x[8 * k + 2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+      asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[e] & 0x7FFF7FFFu));
+      x[2 * e] = __uint_as_float(w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
     }
+    top = max(m << 16, m & 0xFFFF0000u);
   }
+};
+// Eight entries given as bf16 pairs.
+PE_DEV void store8(__nv_bfloat16* p, const uint32_t (&w)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+PE_DEV void store8(float* p, const uint32_t (&w)[4]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    reinterpret_cast<float4*>(p)[k] =
+        make_float4(__uint_as_float(w[2 * k] << 16), __uint_as_float(w[2 * k] & 0xFFFF0000u),
+                    __uint_as_float(w[2 * k + 1] << 16), __uint_as_float(w[2 * k + 1] & 0xFFFF0000u));
+}
+
+// Both kernels give a head's row of keys and of values to HD/8 lanes.  A lane holds word w (its number) of
+// either code row, and the eight entries whose codes come together from the words of a few lanes:
+//   keys    w = t*(HD/32) + u.  Lanes t and t^1 hold, byte by byte, blocks 2u and 2u+1: they exchange half a word, and
+//           lane (t, u) has entries 8(t/2)..+7 of block 2u + t%2.
+//   values  w = g*(HD/64) + h, a nibble for each of eight pieces of eight entries: an 8 x 8 transpose of nibbles
+//           over the lanes g, in three exchanges of half a word; lane (g, h) has entries 64h + 8i..+7, i = g with
+//           its bits 0, 2, 1 as bits 2, 1, 0 (which leaves pairs of entries 16 bits apart, as for the keys).
+template <int HD>
+struct Lane {
+  static constexpr int N = HD / 8, KU = HD / 32, VU = HD / 64;
+  int w, key, value;  // word; first entry of its eight of the keys and of the values
+  PE_DEV explicit Lane(int lane) : w(lane % N) {
+    const int t = w / KU, g = w / VU;
+    key = 16 * (2 * (w % KU) + (t & 1)) + 8 * (t >> 1);
+    value = 64 * (w % VU) + 8 * ((g & 1) << 2 | (g >> 2 & 1) << 1 | (g >> 1 & 1));
+  }
+  // Swaps this lane's half-word fields (`sh` bits, mask) with those of the lane `by` away: the bit of the lane's
+  // number changes places with the bit of the field's.
+  PE_DEV static uint32_t swap(uint32_t x, bool upper, int by, int sh, uint32_t mask) {
+    const uint32_t keep = (upper ? x >> sh : x) & mask, give = (upper ? x : x >> sh) & mask;
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, by);
+    return upper ? (got | keep << sh) : (keep | got << sh);
+  }
+  PE_DEV uint32_t transpose_values(uint32_t x) const {  // its own inverse
+    const int g = w / VU;
+    x = swap(x, g & 1, VU, 16, 0x0000FFFFu);
+    x = swap(x, g & 4, 4 * VU, 8, 0x00FF00FFu);
+    return swap(x, g & 2, 2 * VU, 4, 0x0F0F0F0Fu);
+  }
+  // The word from the codes of the lane's keys (entries 0..3 in bytes 0 and 2, 4..7 in bytes 1 and 3), and back:
+  // entries 0..3 in bytes 0 and 2 of x, 4..7 of y.
+  PE_DEV void keys_of(uint32_t word, uint32_t& x, uint32_t& y) const {
+    const bool odd = (w / KU) & 1;
+    const uint32_t z = swap(word, odd, KU, 8, 0x00FF00FFu);
+    x = z & 0x00FF00FFu;
+    y = (z >> 8) & 0x00FF00FFu;
+  }
+  PE_DEV uint32_t word_of(uint32_t codes) const { return swap(codes, (w / KU) & 1, KU, 8, 0x00FF00FFu); }
+};
 
 // The scale byte of a block whose largest finite magnitude is amax: the smallest c with
 // 7 s(c) >= amax.  amax/7, cut to three mantissa bits, is at most two steps short (the rounding
@@ -48,201 +105,152 @@ PE_DEV uint32_t scale_code(float amax) {
   return (uint32_t)min(max(c, 0), 255);
 }
 
-// Rounds a block of 16 entries: nibbles n[e] = code + 8 and the scale byte.  Returns whether
-// an entry was NaN (kept as 0) or infinite (kept as +-7 s).
+// Rounds eight entries of a block of 16, whose other half the lane `by` away has: the nibbles code + 8 of
+// pairs of entries 16 bits apart (entry 2i in bits 4i, 2i + 1 in bits 16 + 4i), and the block's scale
+// byte.  Returns whether one of the eight was NaN (kept as 0) or infinite (kept as +-7 s).
 template <typename T>
-PE_DEV bool quantise_block(float (&x)[16], uint32_t (&n)[16], uint32_t& code) {
-  float amax = 0.f;
-  bool bad = false;
+PE_DEV bool quantise(Eight& h, int by, uint32_t& nibbles, uint32_t& code) {
+  const bool bad = h.top >= kInfBits;
+  if (bad) {
+    h.top = 0;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const float m = fabsf(x[e]);
-    bad |= !(m < INFINITY);
-    amax = m < INFINITY ? fmaxf(amax, m) : amax;
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t m = __float_as_uint(h.x[e]) & 0x7FFFFFFFu;
+      if (m < kInfBits) h.top = max(h.top, m);
+      if (m > kInfBits) h.x[e] = 0.f;
+    }
   }
+  const float amax = __uint_as_float(max(h.top, __shfl_xor_sync(0xFFFFFFFFu, h.top, by)));
   code = scale_code(amax);
   const float s = packed_scale(code);
   if (bad || amax > 7.f * s) {  // entries beyond the largest scale's range keep its largest code
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = x[e] != x[e] ? 0.f : fminf(fmaxf(x[e], -7.f * s), 7.f * s);
+    for (int e = 0; e < 8; ++e) h.x[e] = fminf(fmaxf(h.x[e], -7.f * s), 7.f * s);
   }
-  // round(x / s), halves away from zero, as x times the float above 1/s plus 1.5 * 2^23 + 8 in one
-  // fused operation: the sum's low mantissa bits are the nibble.  The factor is at most two
+  // round(x / s), halves away from zero, as x times a float above 1/s plus 1.5 * 2^23 + 8 in one
+  // fused operation: the sum's mantissa bits are 2^22 + the nibble.  The factor is at most two
   // rounding steps above 1/s, so an exact half goes away from zero; a bf16 x over a scale of
   // four bits is never nearer to a half than 2^-10 without being one.
-  const float inv = __uint_as_float(__float_as_uint(1.f / s) + 1);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // off by at most one step
+  inv = __uint_as_float(__float_as_uint(inv) + 1);
+  constexpr uint32_t kSum = 0x4B400000u;  // of 1.5 * 2^23; eight of them shifted are taken off at once
+  nibbles = 0u - kSum * 0x11111111u;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    n[e] = __float_as_uint(fmaf(x[e], inv, 12582920.f)) & 15u;
+  for (int e = 0; e < 8; ++e) {
+    uint32_t n = __float_as_uint(fmaf(h.x[e], inv, 12582920.f));
     if (sizeof(T) == 4) {
       // fp32 entries can be nearer to a half than that: the halves themselves decide (exact
       // products of four-bit numbers)
-      const float m = fabsf(x[e]), c = fabsf((float)((int)n[e] - 8));
+      const float m = fabsf(h.x[e]), c = fabsf((float)((int)(n & 15u) - 8));
       const int off = m < (c - 0.5f) * s ? -1 : m >= (c + 0.5f) * s ? 1 : 0;
-      n[e] += x[e] < 0.f ? -off : off;
+      n += h.x[e] < 0.f ? -off : off;
     }
+    nibbles += n << (4 * (e >> 1) + 16 * (e & 1));
   }
   return bad;
 }
 
-// One thread per (row, head, block of 16); blockIdx.y: keys or values.  The four threads of 64
-// entries exchange nibbles so that each stores whole words of the row.
+// HD/8 lanes per (row, head), eight keys and eight values each.
 template <typename T, int HD>
-__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a, const Div heads, int rows) {
   using L = PackedLayout<HD>;
-  constexpr int NB = HD / 16;  // blocks per head row
+  constexpr int N = Lane<HD>::N, GROUPS = kPackThreads / N;
   pdl_wait();
   pdl_trigger();
-  const bool is_v = blockIdx.y != 0;
+  const Lane<HD> ln(threadIdx.x);
+  const long long row0 = (long long)blockIdx.x * rows;
   const int n_rows = a.n_dev != nullptr ? min(max(__ldcg(a.n_dev), 0), a.n_rows) : a.n_rows;
-  const long long per_row = (long long)a.n_kv * NB;
-  const long long idx = (long long)blockIdx.x * kPackThreads + threadIdx.x;
-  const bool live = idx < n_rows * per_row;  // the same for the four threads of 64 entries
-  const long long row = live ? idx / per_row : 0;
-  const int rest = live ? (int)(idx - row * per_row) : 0;
-  const int head = rest / NB, j = rest - (rest / NB) * NB;
-  const int q = threadIdx.x & 3;  // = j & 3
-  long long slot = -1;
-  float x[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = 0.f;
-  if (live) {
-    slot = __ldcg(reinterpret_cast<const long long*>(a.slots) + row);
-    if (slot < -1 || slot >= (long long)a.num_pages * kPackedPage) {
-      set_err(a.err, PE_DEV_BAD_PAGE);
-      slot = -1;
+  const int items = (int)min((long long)rows, n_rows - row0) * a.n_kv;
+  for (int i0 = 0; i0 < items; i0 += GROUPS) {
+    const int item = i0 + threadIdx.x / N;
+    const bool live = item < items;
+    const int r = live ? (int)((uint32_t)item / heads) : 0, head = live ? item - r * a.n_kv : 0;
+    long long slot = -1;
+    Eight k{}, v{};
+    if (live) {
+      slot = __ldcg(reinterpret_cast<const long long*>(a.slots) + row0 + r);
+      k.load(static_cast<const T*>(a.k) + (row0 + r) * a.k_stride + head * HD + ln.key);
+      v.load(static_cast<const T*>(a.v) + (row0 + r) * a.v_stride + head * HD + ln.value);
+      if (slot < -1 || slot >= (long long)a.num_pages * kPackedPage) {
+        set_err(a.err, PE_DEV_BAD_PAGE);
+        slot = -1;
+      }
     }
-    if (slot >= 0) {
-      const T* src = static_cast<const T*>(is_v ? a.v : a.k) + row * (is_v ? a.v_stride : a.k_stride) + head * HD + j * 16;
-      load16<T>(src, x);
-    }
-  }
-  uint32_t n[16], code;
-  if (quantise_block<T>(x, n, code)) set_err(a.err, PE_DEV_NONFINITE);
-  const long long page = slot >= 0 ? slot / kPackedPage : 0;
-  const int off = slot >= 0 ? (int)(slot % kPackedPage) : 0;
-  uint8_t* rec = a.pool + ((size_t)page * a.n_kv + head) * L::kRecord;
-  if (!is_v) {
-    // word (t, u): entries 4t..4t+3 of blocks 2u and 2u+1, a byte of each half from either block
-    uint32_t w[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      w[t] = (n[4 * t] | n[4 * t + 2] << 4 | n[4 * t + 1] << 16 | n[4 * t + 3] << 20) << (8 * (q & 1));
-    const bool hi = q & 1;  // the even block's thread keeps t = 0, 1 and the odd one's t = 2, 3
-    uint32_t o[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t give = hi ? w[k] : w[2 + k];
-      o[k] = (hi ? w[2 + k] : w[k]) | __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-    }
-    if (slot >= 0) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(rec + L::kK + off * L::kRow);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) dst[((hi ? 2 : 0) + k) * (HD / 32) + (j >> 1)] = o[k];
-      rec[L::kKs + off * L::kScaleRow + j] = (uint8_t)code;
-    }
-  } else {
-    // word (g, h): a byte from each of the four blocks of 64 entries (entries g and g + 8 of the block)
-    uint32_t w[8];
-#pragma unroll
-    for (int g = 0; g < 8; ++g) w[g] = (n[g] | n[g + 8] << 4) << (8 * q);
-    const bool b0 = q & 1, b1 = q & 2;
-    uint32_t m[4], o[2];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t give = b0 ? w[k] : w[4 + k];
-      m[k] = (b0 ? w[4 + k] : w[k]) | __shfl_xor_sync(0xFFFFFFFFu, give, 1);
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t give = b1 ? m[k] : m[2 + k];
-      o[k] = (b1 ? m[2 + k] : m[k]) | __shfl_xor_sync(0xFFFFFFFFu, give, 2);
-    }
-    if (slot >= 0) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(rec + L::kV + off * L::kRow);
-      const int g0 = (b0 ? 4 : 0) + (b1 ? 2 : 0);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) dst[(g0 + k) * (HD / 64) + (j >> 2)] = o[k];
-      rec[L::kVs + off * L::kScaleRow + j] = (uint8_t)code;
-    }
+    uint32_t kw, vw, kc, vc;
+    bool bad = quantise<T>(k, 2 * Lane<HD>::KU, kw, kc);
+    bad |= quantise<T>(v, 2 * Lane<HD>::VU, vw, vc);
+    kw = ln.word_of(kw);
+    vw = ln.transpose_values(vw);
+    if (slot < 0) continue;
+    if (bad) set_err(a.err, PE_DEV_NONFINITE);
+    const int off = (int)(slot & (kPackedPage - 1));
+    uint8_t* rec = a.pool + ((size_t)(slot / kPackedPage) * a.n_kv + head) * L::kRecord;
+    reinterpret_cast<uint32_t*>(rec + L::kK + off * L::kRow)[ln.w] = kw;
+    reinterpret_cast<uint32_t*>(rec + L::kV + off * L::kRow)[ln.w] = vw;
+    if ((ln.key & 8) == 0) rec[L::kKs + off * L::kScaleRow + ln.key / kPackedBlock] = (uint8_t)kc;
+    if ((ln.value & 8) == 0) rec[L::kVs + off * L::kScaleRow + ln.value / kPackedBlock] = (uint8_t)vc;
   }
 }
 
-template <typename T>
-PE_DEV void store8(T* p, const float (&x)[8]);
-template <>
-PE_DEV void store8<float>(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-template <>
-PE_DEV void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&x)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-    w[k] = *reinterpret_cast<const uint32_t*>(&t);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// One thread per (row, head, eight entries); blockIdx.y: keys or values.
+// HD/8 lanes per (row, head), eight keys and eight values each.
 template <typename T, int HD>
-__global__ void __launch_bounds__(kPackThreads) unpack_kernel(const UnpackArgs a) {
+__global__ void __launch_bounds__(kPackThreads) unpack_kernel(const UnpackArgs a, const Div heads, int rows) {
   using L = PackedLayout<HD>;
-  constexpr int NE = HD / 8;
+  constexpr int N = Lane<HD>::N, GROUPS = kPackThreads / N;
   pdl_wait();
   pdl_trigger();
-  const bool is_v = blockIdx.y != 0;
-  const long long per_row = (long long)a.n_kv * NE;
-  const long long idx = (long long)blockIdx.x * kPackThreads + threadIdx.x;
-  if (idx >= a.n_rows * per_row) return;
-  const long long row = idx / per_row;
-  const int rest = (int)(idx - row * per_row);
-  const int head = rest / NE, e8 = rest - (rest / NE) * NE;
-  const long long slot = __ldcg(reinterpret_cast<const long long*>(a.slots) + row);
-  if (slot < 0 || slot >= (long long)a.num_pages * kPackedPage) {
-    if (slot != -1) set_err(a.err, PE_DEV_BAD_PAGE);
-    return;
-  }
-  const int off = (int)(slot % kPackedPage);
-  const uint8_t* rec = a.pool + ((size_t)(slot / kPackedPage) * a.n_kv + head) * L::kRecord;
-  const int j = e8 >> 1, h8 = e8 & 1;  // block, and which half of it
-  float x[8];
-  if (!is_v) {
-    const float s = packed_scale(__ldcg(rec + L::kKs + off * L::kScaleRow + j));
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(rec + L::kK + off * L::kRow);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t w = __ldcg(src + (2 * h8 + k) * (HD / 32) + (j >> 1)) >> (8 * (j & 1));
-      x[4 * k] = s * (float)((int)(w & 15u) - 8);
-      x[4 * k + 1] = s * (float)((int)((w >> 16) & 15u) - 8);
-      x[4 * k + 2] = s * (float)((int)((w >> 4) & 15u) - 8);
-      x[4 * k + 3] = s * (float)((int)((w >> 20) & 15u) - 8);
+  const Lane<HD> ln(threadIdx.x);
+  const PairBits bits;
+  const long long row0 = (long long)blockIdx.x * rows;
+  const int items = (int)min((long long)rows, a.n_rows - row0) * a.n_kv;
+  for (int i0 = 0; i0 < items; i0 += GROUPS) {
+    const int item = i0 + threadIdx.x / N;
+    const bool live = item < items;
+    const int r = live ? (int)((uint32_t)item / heads) : 0, head = live ? item - r * a.n_kv : 0;
+    long long slot = live ? __ldcg(reinterpret_cast<const long long*>(a.slots) + row0 + r) : -1;
+    uint32_t kw = 0, vw = 0, ks = 0, vs = 0;
+    if (slot < 0 || slot >= (long long)a.num_pages * kPackedPage) {
+      if (slot != -1) set_err(a.err, PE_DEV_BAD_PAGE);
+      slot = -1;
+    } else {
+      const int off = (int)(slot & (kPackedPage - 1));
+      const uint8_t* rec = a.pool + ((size_t)(slot / kPackedPage) * a.n_kv + head) * L::kRecord;
+      kw = __ldcg(reinterpret_cast<const uint32_t*>(rec + L::kK + off * L::kRow) + ln.w);
+      vw = __ldcg(reinterpret_cast<const uint32_t*>(rec + L::kV + off * L::kRow) + ln.w);
+      ks = __ldcg(rec + L::kKs + off * L::kScaleRow + ln.key / kPackedBlock);
+      vs = __ldcg(rec + L::kVs + off * L::kScaleRow + ln.value / kPackedBlock);
     }
-  } else {
-    const float s = packed_scale(__ldcg(rec + L::kVs + off * L::kScaleRow + j));
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(rec + L::kV + off * L::kRow);
-    const int sh = 8 * (j & 3) + 4 * h8;
-#pragma unroll
-    for (int g = 0; g < 8; ++g)
-      x[g] = s * (float)((int)((__ldcg(src + g * (HD / 64) + (j >> 2)) >> sh) & 15u) - 8);
+    uint32_t x, y;
+    ln.keys_of(kw, x, y);
+    const uint32_t z = ln.transpose_values(vw);
+    if (slot < 0) continue;
+    const uint32_t sk = packed_scale_pair(ks), sv = packed_scale_pair(vs);
+    const uint32_t bk = bf16x2_mul(sk, kMinus136), bv = bf16x2_mul(sv, kMinus136);
+    const uint32_t k4[4] = {bf16x2_fma(bits.pair<0>(x), sk, bk), bf16x2_fma(bits.pair<1>(x), sk, bk),
+                            bf16x2_fma(bits.pair<0>(y), sk, bk), bf16x2_fma(bits.pair<1>(y), sk, bk)};
+    const uint32_t v4[4] = {bf16x2_fma(bits.pair<0>(z), sv, bv), bf16x2_fma(bits.pair<1>(z), sv, bv),
+                            bf16x2_fma(bits.pair<2>(z), sv, bv), bf16x2_fma(bits.pair<3>(z), sv, bv)};
+    store8(static_cast<T*>(a.k_out) + (row0 + r) * a.k_stride + head * HD + ln.key, k4);
+    store8(static_cast<T*>(a.v_out) + (row0 + r) * a.v_stride + head * HD + ln.value, v4);
   }
-  T* dst = static_cast<T*>(is_v ? a.v_out : a.k_out) + row * (is_v ? a.v_stride : a.k_stride) + head * HD + e8 * 8;
-  store8<T>(dst, x);
 }
+
+// A CTA for as many whole rows as its lanes have at once (at least one).
+template <int HD>
+int rows_per_cta(int n_kv) { return std::max(1, kPackThreads / Lane<HD>::N / n_kv); }
 
 template <typename T, int HD>
 cudaError_t pack_typed(const PackArgs& a, cudaStream_t s) {
-  const long long n = (long long)a.n_rows * a.n_kv * (HD / 16);
-  return launch_pdl(pack_kernel<T, HD>, dim3((unsigned)((n + kPackThreads - 1) / kPackThreads), 2), dim3(kPackThreads),
-                    0, s, a);
+  const int rows = rows_per_cta<HD>(a.n_kv);
+  return launch_pdl(pack_kernel<T, HD>, dim3((unsigned)((a.n_rows + (long long)rows - 1) / rows)), dim3(kPackThreads), 0, s,
+                    a, make_div(a.n_kv), rows);
 }
 template <typename T, int HD>
 cudaError_t unpack_typed(const UnpackArgs& a, cudaStream_t s) {
-  const long long n = (long long)a.n_rows * a.n_kv * (HD / 8);
-  return launch_pdl(unpack_kernel<T, HD>, dim3((unsigned)((n + kPackThreads - 1) / kPackThreads), 2),
-                    dim3(kPackThreads), 0, s, a);
+  const int rows = rows_per_cta<HD>(a.n_kv);
+  return launch_pdl(unpack_kernel<T, HD>, dim3((unsigned)((a.n_rows + (long long)rows - 1) / rows)), dim3(kPackThreads), 0,
+                    s, a, make_div(a.n_kv), rows);
 }
 
 }  // namespace

@@ -44,8 +44,25 @@ struct PackedLayout {
   static constexpr int kK = 0, kV = 8 * HD, kKs = 16 * HD, kVs = 17 * HD, kRecord = 18 * HD;
 };
 
+// n / d for n < 2^31 by a multiplication: mul = ceil(2^shift / d), shift = 31 + ceil(log2 d), is at most
+// d 2^-shift above 1/d, which is less than 1/(n d).  (A division by a value that the compiler does not know
+// is a chain of about 150 cycles, several of which stood before the first load.)
+struct Div {
+  uint32_t mul;
+  int shift;
+};
+inline Div make_div(uint32_t d) {
+  int l = 0;
+  while ((1u << l) < d) ++l;
+  return Div{(uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+PE_DEV uint32_t operator/(uint32_t n, const Div& d) { return (uint32_t)(((uint64_t)n * d.mul) >> d.shift); }
+
 // s(c) as fp32.
 PE_DEV float packed_scale(uint32_t c) { return __uint_as_float((c << 20) + (108u << 23)); }
+
+// s(c) as a pair of bf16 (exact: four significant bits).
+PE_DEV uint32_t packed_scale_pair(uint32_t c) { return ((c << 4) + (108u << 7)) * 0x10001u; }
 
 // Two of a word's eight nibbles as bf16 pairs 128 + nibble: nibble I in the lower half, I + 4 above.
 // (A mask and an exponent are two constants, of which one instruction takes one: the compiler makes two

@@ -47,20 +47,6 @@ PE_DEV float max3(float a, float b, float c) {
 // A wait's outcome, made the same for the whole warp.
 PE_DEV bool warp_ok(bool ok) { return __all_sync(0xFFFFFFFFu, ok); }
 
-// n / d for n < 2^31 by a multiplication: mul = ceil(2^shift / d), shift = 31 + ceil(log2 d), is at most
-// d 2^-shift above 1/d, which is less than 1/(n d).  (A division by a value that the compiler does not know
-// is a chain of about 150 cycles, several of which stood before the first load.)
-struct Div {
-  uint32_t mul;
-  int shift;
-};
-Div make_div(uint32_t d) {
-  int l = 0;
-  while ((1u << l) < d) ++l;
-  return Div{(uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
-}
-PE_DEV uint32_t operator/(uint32_t n, const Div& d) { return (uint32_t)(((uint64_t)n * d.mul) >> d.shift); }
-
 // r / d where the quotient is at most 2^16: the fp32 quotient is off by one at most.
 PE_DEV uint32_t small_quotient(uint32_t r, uint32_t d) {
   uint32_t q = (uint32_t)__fdividef((float)r, (float)d);
