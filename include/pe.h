@@ -417,6 +417,8 @@ pe_status pe_unpack_kv(const pe_config *cfg, const void *pool, int32_t num_pages
  * positions[r] = -1: the row sees nothing and gets zeros.  Rows outside
  * row_start[0] .. row_start[B] - 1 are left as they were.  n_rows (at most 65536) bounds the
  * rows, max_rows those of one sequence; both bounds choose the kernels, so the closer the better.
+ * Launches cover B * max_rows rows, 1024 tiles of 128 query vectors each (fp32: 16; a query vector: a row's query
+ * head of one kv head); bounds that would take more than 4096 of them are refused (PE_ERR_SHAPE).
  * fp32: products and sums keep fp32 accuracy.  bf16: the softmax weights are rounded to
  * bf16 (by at most 2^-8 of each) before the product with the values; scores, statistics and sums are
  * fp32.  out must not overlap q; rows of both in one buffer, side by side with one stride, do not.

@@ -48,6 +48,7 @@ void trace(int point, cudaStream_t s) {
 constexpr int kMaxRows = 1 << 16;        // B*2K
 constexpr int kMaxPackedHeads = 1 << 12;  // query heads of a packed-cache call
 constexpr int kMaxPackedPages = 1 << 24;  // block-table row length of a packed-cache call
+constexpr int kMaxPackedLaunches = 4096;  // launches that the bounds of a packed-cache call may ask for
 constexpr int kAttnItemsPerSlot = 4;     // attention work items aimed for, per resident CTA (load balance)
 constexpr int kAttnMinChunk = 256;       // shortest position chunk of a work item (bounds the chunks to merge)
 constexpr int kTcMaxStages = 12;
@@ -1213,10 +1214,12 @@ pe_status pe_attend_packed(const pe_config* cfg, const void* q, int64_t q_stride
   if (n_rows > 0 && !rows_disjoint(*cfg, q, q_stride, out, out_stride, width, n_rows)) return PE_ERR_INVALID_ARG;
   PackedAttnArgs a{};
   a.B = cfg->B; a.n_q = cfg->n_q; a.n_kv = cfg->n_kv; a.head_dim = cfg->head_dim; a.max_pages = cfg->max_pages_per_seq;
-  a.num_pages = num_pages; a.n_rows = n_rows; a.max_rows = std::min(max_rows, n_rows); a.scale = 1.0f / sqrtf((float)cfg->head_dim);
+  a.num_pages = num_pages; a.n_rows = n_rows; a.max_rows = std::min(max_rows, n_rows);
+  a.scale = 1.0f / sqrtf((float)cfg->head_dim);
   a.q = q; a.q_stride = q_stride; a.pool = static_cast<const uint8_t*>(pool); a.block_table = block_table;
   a.row_start = row_start; a.positions = positions; a.out = out; a.out_stride = out_stride; a.workspace = workspace;
   a.wait_ns = wait_limit_ns(); a.err = err_word;
+  if (packed_attn_launches(a, cfg->dtype) > kMaxPackedLaunches) return PE_ERR_SHAPE;
   PE_TRY_CUDA(launch_attend_packed(a, cfg->dtype, sms, (cudaStream_t)stream));
   return PE_OK;
 }

@@ -369,6 +369,8 @@ struct PackedAttnArgs {
   int32_t* err;
 };
 size_t packed_attn_workspace_bytes(int head_dim, pe_dtype dt, int sms);
+// Attention launches of such a call (each with a merge): the tiles that the bounds allow, 1024 or fewer at a time.
+long long packed_attn_launches(const PackedAttnArgs& a, pe_dtype dt);
 cudaError_t launch_attend_packed(const PackedAttnArgs& a, pe_dtype dt, int sms, cudaStream_t s);
 
 }  // namespace pe

@@ -59,38 +59,61 @@ PE_DEV void store8(float* p, const uint32_t (&w)[4]) {
 //   values  w = g*(HD/64) + h, a nibble for each of eight pieces of eight entries: an 8 x 8 transpose of nibbles
 //           over the lanes g, in three exchanges of half a word; lane (g, h) has entries 64h + 8i..+7, i = g with
 //           its bits 0, 2, 1 as bits 2, 1, 0 (which leaves pairs of entries 16 bits apart, as for the keys).
+// An exchange turns a bit of the lane's number into a bit of the place of a field in the word, and that bit into it:
+// the lane keeps one half of its word's fields and swaps the other for its partner's.
+template <int SH, uint32_t MASK>
+struct Exchange {
+  uint32_t keep;
+  int away;  // where the partner's half goes
+  PE_DEV explicit Exchange(bool upper) : keep(upper ? MASK << SH : MASK), away(upper ? 0 : SH) {}
+  PE_DEV uint32_t operator()(uint32_t x, int by) const {
+    return (x & keep) | __shfl_xor_sync(0xFFFFFFFFu, (x >> away) & MASK, by) << away;
+  }
+};
 template <int HD>
 struct Lane {
   static constexpr int N = HD / 8, KU = HD / 32, VU = HD / 64;
   int w, key, value;  // word; first entry of its eight of the keys and of the values
-  PE_DEV explicit Lane(int lane) : w(lane % N) {
+  Exchange<8, 0x00FF00FFu> kx, v1;
+  Exchange<16, 0x0000FFFFu> v0;
+  Exchange<4, 0x0F0F0F0Fu> v2;
+  PE_DEV explicit Lane(int lane)
+      : w(lane % N), kx((w / KU) & 1), v1((w / VU) & 4), v0((w / VU) & 1), v2((w / VU) & 2) {
     const int t = w / KU, g = w / VU;
     key = 16 * (2 * (w % KU) + (t & 1)) + 8 * (t >> 1);
     value = 64 * (w % VU) + 8 * ((g & 1) << 2 | (g >> 2 & 1) << 1 | (g >> 1 & 1));
   }
-  // Swaps this lane's half-word fields (`sh` bits, mask) with those of the lane `by` away: the bit of the lane's
-  // number changes places with the bit of the field's.
-  PE_DEV static uint32_t swap(uint32_t x, bool upper, int by, int sh, uint32_t mask) {
-    const uint32_t keep = (upper ? x >> sh : x) & mask, give = (upper ? x : x >> sh) & mask;
-    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, by);
-    return upper ? (got | keep << sh) : (keep | got << sh);
-  }
-  PE_DEV uint32_t transpose_values(uint32_t x) const {  // its own inverse
-    const int g = w / VU;
-    x = swap(x, g & 1, VU, 16, 0x0000FFFFu);
-    x = swap(x, g & 4, 4 * VU, 8, 0x00FF00FFu);
-    return swap(x, g & 2, 2 * VU, 4, 0x0F0F0F0Fu);
-  }
-  // The word from the codes of the lane's keys (entries 0..3 in bytes 0 and 2, 4..7 in bytes 1 and 3), and back:
-  // entries 0..3 in bytes 0 and 2 of x, 4..7 of y.
-  PE_DEV void keys_of(uint32_t word, uint32_t& x, uint32_t& y) const {
-    const bool odd = (w / KU) & 1;
-    const uint32_t z = swap(word, odd, KU, 8, 0x00FF00FFu);
-    x = z & 0x00FF00FFu;
-    y = (z >> 8) & 0x00FF00FFu;
-  }
-  PE_DEV uint32_t word_of(uint32_t codes) const { return swap(codes, (w / KU) & 1, KU, 8, 0x00FF00FFu); }
+  // Words from codes and codes from words: eight nibbles, the pairs of entries 16 bits apart.  The keys' entries
+  // 0..3 stand in bytes 0 and 2, entries 4..7 in bytes 1 and 3; the values' in nibble order.
+  PE_DEV uint32_t keys(uint32_t x) const { return kx(x, KU); }
+  PE_DEV uint32_t values(uint32_t x) const { return v2(v1(v0(x, VU), 4 * VU), 2 * VU); }
 };
+
+// How a launch deals out rows and heads: a CTA has `heads` groups of lanes side by side for `rows` rows at a
+// time, `steps` times, and again for the heads that are left.  Addresses then advance by additions, and the
+// CTAs are all resident at once, eight an SM (four: a third more time, the loads of a step wait for the
+// one before; sixteen: the same).  With a CTA per 128 lanes' rows, the instructions that found each lane's place
+// were half of all.
+struct Deal {
+  int heads, rows, steps, n_kv;
+  Div by_heads;
+};
+constexpr int kPackCtas = 152 * 8;
+template <int HD>
+Deal deal(int n_rows, int n_kv, unsigned* grid, unsigned* threads) {
+  constexpr int N = Lane<HD>::N, groups = kPackThreads / N;
+  Deal d{};
+  const int passes = (n_kv + groups - 1) / groups;
+  d.heads = (n_kv + passes - 1) / passes;
+  d.rows = groups / d.heads;
+  d.steps = (int)((n_rows + (long long)d.rows * kPackCtas - 1) / ((long long)d.rows * kPackCtas));
+  d.n_kv = n_kv;
+  d.by_heads = make_div(d.heads);
+  const long long per = (long long)d.rows * d.steps;
+  *grid = (unsigned)((n_rows + per - 1) / per);
+  *threads = (unsigned)((d.heads * d.rows * N + 31) / 32 * 32);
+  return d;
+}
 
 // The scale byte of a block whose largest finite magnitude is amax: the smallest c with
 // 7 s(c) >= amax.  amax/7, cut to three mantissa bits, is at most two steps short (the rounding
@@ -151,106 +174,124 @@ PE_DEV bool quantise(Eight& h, int by, uint32_t& nibbles, uint32_t& code) {
   return bad;
 }
 
+// Packing and reading back are bound by memory in principle: bytes of the rows and of their packed form, once
+// each.  Measured, 12,026 rows of 4 heads of 128 entries in bf16 (56 MB both ways) are packed and read back in
+// 21 us, 24,586 rows of 8 heads of 64 read back (65 MB) in 19 us, half of the copy rate: launches this short
+// are a wave of loads, a wave of stores and the way in and out.  Loading a step ahead of its use did not
+// change that (21.6 and 17.7 us), nor did longer rows per lane.
+
 // HD/8 lanes per (row, head), eight keys and eight values each.
 template <typename T, int HD>
-__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a, const Div heads, int rows) {
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a, const Deal d) {
   using L = PackedLayout<HD>;
-  constexpr int N = Lane<HD>::N, GROUPS = kPackThreads / N;
+  const Lane<HD> ln(threadIdx.x);
+  const int group = threadIdx.x / Lane<HD>::N, r = (int)((uint32_t)group / d.by_heads);
+  const uint64_t n_slots = (uint64_t)a.num_pages * kPackedPage;
+  const uint32_t page_bytes = (uint32_t)d.n_kv * L::kRecord;
+  const long long row0 = (long long)blockIdx.x * d.rows * d.steps + r;
   pdl_wait();
   pdl_trigger();
-  const Lane<HD> ln(threadIdx.x);
-  const long long row0 = (long long)blockIdx.x * rows;
   const int n_rows = a.n_dev != nullptr ? min(max(__ldcg(a.n_dev), 0), a.n_rows) : a.n_rows;
-  const int items = (int)min((long long)rows, n_rows - row0) * a.n_kv;
-  for (int i0 = 0; i0 < items; i0 += GROUPS) {
-    const int item = i0 + threadIdx.x / N;
-    const bool live = item < items;
-    const int r = live ? (int)((uint32_t)item / heads) : 0, head = live ? item - r * a.n_kv : 0;
-    long long slot = -1;
-    Eight k{}, v{};
-    if (live) {
-      slot = __ldcg(reinterpret_cast<const long long*>(a.slots) + row0 + r);
-      k.load(static_cast<const T*>(a.k) + (row0 + r) * a.k_stride + head * HD + ln.key);
-      v.load(static_cast<const T*>(a.v) + (row0 + r) * a.v_stride + head * HD + ln.value);
-      if (slot < -1 || slot >= (long long)a.num_pages * kPackedPage) {
-        set_err(a.err, PE_DEV_BAD_PAGE);
-        slot = -1;
+  for (int h0 = 0; h0 < d.n_kv; h0 += d.heads) {
+    const int head = h0 + group - r * d.heads;
+    const bool mine = r < d.rows && head < d.n_kv;
+    const int64_t* slots = a.slots + row0;
+    const T* k_row = static_cast<const T*>(a.k) + row0 * a.k_stride + (long long)head * HD + ln.key;
+    const T* v_row = static_cast<const T*>(a.v) + row0 * a.v_stride + (long long)head * HD + ln.value;
+    uint8_t* pool = a.pool + (size_t)head * L::kRecord;
+    for (int i = 0; i < d.steps; ++i) {
+      int64_t slot = -1;
+      Eight k{}, v{};
+      if (mine && row0 + (long long)i * d.rows < n_rows) {
+        slot = __ldcg(reinterpret_cast<const long long*>(slots));
+        k.load(k_row);
+        v.load(v_row);
       }
+      slots += d.rows;
+      k_row += d.rows * a.k_stride;
+      v_row += d.rows * a.v_stride;
+      uint32_t kw, vw, kc, vc;
+      bool bad = quantise<T>(k, 2 * Lane<HD>::KU, kw, kc);
+      bad |= quantise<T>(v, 2 * Lane<HD>::VU, vw, vc);
+      kw = ln.keys(kw);
+      vw = ln.values(vw);
+      if ((uint64_t)slot >= n_slots) {
+        if (slot != -1) set_err(a.err, PE_DEV_BAD_PAGE);
+        continue;
+      }
+      if (bad) set_err(a.err, PE_DEV_NONFINITE);
+      const int off = (int)slot & (kPackedPage - 1);
+      uint8_t* rec = pool + (uint64_t)(uint32_t)(slot / kPackedPage) * page_bytes;
+      reinterpret_cast<uint32_t*>(rec + L::kK + off * L::kRow)[ln.w] = kw;
+      reinterpret_cast<uint32_t*>(rec + L::kV + off * L::kRow)[ln.w] = vw;
+      if ((ln.key & 8) == 0) rec[L::kKs + off * L::kScaleRow + ln.key / kPackedBlock] = (uint8_t)kc;
+      if ((ln.value & 8) == 0) rec[L::kVs + off * L::kScaleRow + ln.value / kPackedBlock] = (uint8_t)vc;
     }
-    uint32_t kw, vw, kc, vc;
-    bool bad = quantise<T>(k, 2 * Lane<HD>::KU, kw, kc);
-    bad |= quantise<T>(v, 2 * Lane<HD>::VU, vw, vc);
-    kw = ln.word_of(kw);
-    vw = ln.transpose_values(vw);
-    if (slot < 0) continue;
-    if (bad) set_err(a.err, PE_DEV_NONFINITE);
-    const int off = (int)(slot & (kPackedPage - 1));
-    uint8_t* rec = a.pool + ((size_t)(slot / kPackedPage) * a.n_kv + head) * L::kRecord;
-    reinterpret_cast<uint32_t*>(rec + L::kK + off * L::kRow)[ln.w] = kw;
-    reinterpret_cast<uint32_t*>(rec + L::kV + off * L::kRow)[ln.w] = vw;
-    if ((ln.key & 8) == 0) rec[L::kKs + off * L::kScaleRow + ln.key / kPackedBlock] = (uint8_t)kc;
-    if ((ln.value & 8) == 0) rec[L::kVs + off * L::kScaleRow + ln.value / kPackedBlock] = (uint8_t)vc;
   }
 }
 
 // HD/8 lanes per (row, head), eight keys and eight values each.
 template <typename T, int HD>
-__global__ void __launch_bounds__(kPackThreads) unpack_kernel(const UnpackArgs a, const Div heads, int rows) {
+__global__ void __launch_bounds__(kPackThreads) unpack_kernel(const UnpackArgs a, const Deal d) {
   using L = PackedLayout<HD>;
-  constexpr int N = Lane<HD>::N, GROUPS = kPackThreads / N;
-  pdl_wait();
-  pdl_trigger();
   const Lane<HD> ln(threadIdx.x);
   const PairBits bits;
-  const long long row0 = (long long)blockIdx.x * rows;
-  const int items = (int)min((long long)rows, a.n_rows - row0) * a.n_kv;
-  for (int i0 = 0; i0 < items; i0 += GROUPS) {
-    const int item = i0 + threadIdx.x / N;
-    const bool live = item < items;
-    const int r = live ? (int)((uint32_t)item / heads) : 0, head = live ? item - r * a.n_kv : 0;
-    long long slot = live ? __ldcg(reinterpret_cast<const long long*>(a.slots) + row0 + r) : -1;
-    uint32_t kw = 0, vw = 0, ks = 0, vs = 0;
-    if (slot < 0 || slot >= (long long)a.num_pages * kPackedPage) {
-      if (slot != -1) set_err(a.err, PE_DEV_BAD_PAGE);
-      slot = -1;
-    } else {
-      const int off = (int)(slot & (kPackedPage - 1));
-      const uint8_t* rec = a.pool + ((size_t)(slot / kPackedPage) * a.n_kv + head) * L::kRecord;
-      kw = __ldcg(reinterpret_cast<const uint32_t*>(rec + L::kK + off * L::kRow) + ln.w);
-      vw = __ldcg(reinterpret_cast<const uint32_t*>(rec + L::kV + off * L::kRow) + ln.w);
-      ks = __ldcg(rec + L::kKs + off * L::kScaleRow + ln.key / kPackedBlock);
-      vs = __ldcg(rec + L::kVs + off * L::kScaleRow + ln.value / kPackedBlock);
+  const int group = threadIdx.x / Lane<HD>::N, r = (int)((uint32_t)group / d.by_heads);
+  const uint64_t n_slots = (uint64_t)a.num_pages * kPackedPage;
+  const uint32_t page_bytes = (uint32_t)d.n_kv * L::kRecord;
+  const long long row0 = (long long)blockIdx.x * d.rows * d.steps + r;
+  pdl_wait();
+  pdl_trigger();
+  for (int h0 = 0; h0 < d.n_kv; h0 += d.heads) {
+    const int head = h0 + group - r * d.heads;
+    const bool mine = r < d.rows && head < d.n_kv;
+    const int64_t* slots = a.slots + row0;
+    T* k_row = static_cast<T*>(a.k_out) + row0 * a.k_stride + (long long)head * HD + ln.key;
+    T* v_row = static_cast<T*>(a.v_out) + row0 * a.v_stride + (long long)head * HD + ln.value;
+    const uint8_t* pool = a.pool + (size_t)head * L::kRecord;
+    for (int i = 0; i < d.steps; ++i) {
+      const bool live = mine && row0 + (long long)i * d.rows < a.n_rows;
+      const int64_t slot = live ? __ldcg(reinterpret_cast<const long long*>(slots)) : -1;
+      const bool good = (uint64_t)slot < n_slots;
+      if (!good && slot != -1) set_err(a.err, PE_DEV_BAD_PAGE);
+      uint32_t kw = 0, vw = 0, ks = 0, vs = 0;
+      if (good) {
+        const int off = (int)slot & (kPackedPage - 1);
+        const uint8_t* rec = pool + (uint64_t)(uint32_t)(slot / kPackedPage) * page_bytes;
+        kw = __ldcg(reinterpret_cast<const uint32_t*>(rec + L::kK + off * L::kRow) + ln.w);
+        vw = __ldcg(reinterpret_cast<const uint32_t*>(rec + L::kV + off * L::kRow) + ln.w);
+        ks = __ldcg(rec + L::kKs + off * L::kScaleRow + ln.key / kPackedBlock);
+        vs = __ldcg(rec + L::kVs + off * L::kScaleRow + ln.value / kPackedBlock);
+      }
+      const uint32_t x = ln.keys(kw), y = x >> 8, z = ln.values(vw);
+      if (good) {
+        const uint32_t sk = packed_scale_pair(ks), sv = packed_scale_pair(vs);
+        const uint32_t bk = bf16x2_mul(sk, kMinus136), bv = bf16x2_mul(sv, kMinus136);
+        const uint32_t k4[4] = {bf16x2_fma(bits.pair<0>(x), sk, bk), bf16x2_fma(bits.pair<1>(x), sk, bk),
+                                bf16x2_fma(bits.pair<0>(y), sk, bk), bf16x2_fma(bits.pair<1>(y), sk, bk)};
+        const uint32_t v4[4] = {bf16x2_fma(bits.pair<0>(z), sv, bv), bf16x2_fma(bits.pair<1>(z), sv, bv),
+                                bf16x2_fma(bits.pair<2>(z), sv, bv), bf16x2_fma(bits.pair<3>(z), sv, bv)};
+        store8(k_row, k4);
+        store8(v_row, v4);
+      }
+      slots += d.rows;
+      k_row += d.rows * a.k_stride;
+      v_row += d.rows * a.v_stride;
     }
-    uint32_t x, y;
-    ln.keys_of(kw, x, y);
-    const uint32_t z = ln.transpose_values(vw);
-    if (slot < 0) continue;
-    const uint32_t sk = packed_scale_pair(ks), sv = packed_scale_pair(vs);
-    const uint32_t bk = bf16x2_mul(sk, kMinus136), bv = bf16x2_mul(sv, kMinus136);
-    const uint32_t k4[4] = {bf16x2_fma(bits.pair<0>(x), sk, bk), bf16x2_fma(bits.pair<1>(x), sk, bk),
-                            bf16x2_fma(bits.pair<0>(y), sk, bk), bf16x2_fma(bits.pair<1>(y), sk, bk)};
-    const uint32_t v4[4] = {bf16x2_fma(bits.pair<0>(z), sv, bv), bf16x2_fma(bits.pair<1>(z), sv, bv),
-                            bf16x2_fma(bits.pair<2>(z), sv, bv), bf16x2_fma(bits.pair<3>(z), sv, bv)};
-    store8(static_cast<T*>(a.k_out) + (row0 + r) * a.k_stride + head * HD + ln.key, k4);
-    store8(static_cast<T*>(a.v_out) + (row0 + r) * a.v_stride + head * HD + ln.value, v4);
   }
 }
-
-// A CTA for as many whole rows as its lanes have at once (at least one).
-template <int HD>
-int rows_per_cta(int n_kv) { return std::max(1, kPackThreads / Lane<HD>::N / n_kv); }
 
 template <typename T, int HD>
 cudaError_t pack_typed(const PackArgs& a, cudaStream_t s) {
-  const int rows = rows_per_cta<HD>(a.n_kv);
-  return launch_pdl(pack_kernel<T, HD>, dim3((unsigned)((a.n_rows + (long long)rows - 1) / rows)), dim3(kPackThreads), 0, s,
-                    a, make_div(a.n_kv), rows);
+  unsigned grid, threads;
+  const Deal d = deal<HD>(a.n_rows, a.n_kv, &grid, &threads);
+  return launch_pdl(pack_kernel<T, HD>, dim3(grid), dim3(threads), 0, s, a, d);
 }
 template <typename T, int HD>
 cudaError_t unpack_typed(const UnpackArgs& a, cudaStream_t s) {
-  const int rows = rows_per_cta<HD>(a.n_kv);
-  return launch_pdl(unpack_kernel<T, HD>, dim3((unsigned)((a.n_rows + (long long)rows - 1) / rows)), dim3(kPackThreads), 0,
-                    s, a, make_div(a.n_kv), rows);
+  unsigned grid, threads;
+  const Deal d = deal<HD>(a.n_rows, a.n_kv, &grid, &threads);
+  return launch_pdl(unpack_kernel<T, HD>, dim3(grid), dim3(threads), 0, s, a, d);
 }
 
 }  // namespace

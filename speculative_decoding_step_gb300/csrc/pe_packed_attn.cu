@@ -360,8 +360,8 @@ PE_DEV float* part_record(const Line& ln, int cta, bool from_start) {
 // A CTA's piece of the line is divided once more, evenly, among its eight warps, each of which runs on its
 // own over whole ranges, or parts, of its piece; at the end the parts of ranges that the warps
 // share join in shared memory.  (Dividing every range among the eight warps instead, with a join
-// after each, left SMs with many short ranges behind the others: 94 us for the 84 us here
-// at B = 64 single tokens.)
+// after each, left SMs with many short ranges behind the others: an eighth more time at B = 64
+// single tokens.)
 //
 // Bound: unpacking.  A page of one head is 1152 bytes at head_dim 64: an SM's share of the HBM rate
 // brings it in about 50 cycles, in which it can issue about 200 instructions, half of them to the
@@ -930,9 +930,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 // block serves all 128 vectors.  Roles of a CTA (two CTAs per SM):
 //   one warp     issues the MMAs: a block's PV once P is there, then the S that reuses its buffer, two
 //                or three blocks on.
-//   some warps   unpack: each takes two pages of a block in turn, a row (position) per lane, from a ring of its own
-//                that asynchronous copies fill ahead, into the K and V rings (128-byte swizzle).
-//                Entries stay in the order of the cache's words: K's is a permutation of the
+//   three warps  unpack: each takes two pages of a block in turn, a row (position) per lane, from a ring
+//                of its own that asynchronous copies fill ahead, into the K and V rings (128-byte
+//                swizzle).  Entries stay in the order of the cache's words: K's is a permutation of the
 //                contraction, given to Q as well; V's one of O's columns, undone on output.
 //   four warps   do the softmax, one thread per query vector (TMEM lane).
 // A vector's reference maximum only moves when a block exceeds it by 2^8; then O is rescaled in TMEM.
@@ -954,18 +954,17 @@ struct Tile {
   static constexpr int ST = HD == 64 ? 4 : 2;         // stages of keys and values
   static constexpr int RAW = HD == 64 ? 3 : 1;        // steps that an unpacking warp's copies are ahead
   static constexpr int STEP = 2 * PackedLayout<HD>::kRecord;  // two pages, half a block
-  static constexpr int QB = 1;                        // query tiles
   static constexpr uint32_t TO = NB * kTileBlk;       // first column of O
   static constexpr uint32_t Q = kTileRows * HD * 2, KV = kTileBlk * HD * 2;
-  static constexpr uint32_t KRING = QB * Q, VRING = KRING + ST * KV, RAWS = VRING + ST * KV;
+  static constexpr uint32_t KRING = Q, VRING = KRING + ST * KV, RAWS = VRING + ST * KV;
   static constexpr uint32_t CTRL = (RAWS + UNPACK * RAW * STEP + 127) / 128 * 128;
   static constexpr uint32_t FIXED = CTRL + 256;
   static size_t smem(int n_tiles) { return 1024 + FIXED + Layout::kBytesPerTile * (size_t)n_tiles + 4; }
 };
 
 struct TileCtrl {
-  uint64_t kfull[5], vfull[2];     // an arrival per step of the unpacking warps
-  uint64_t vempty[5];              // the block's PV product has completed
+  uint64_t kfull[4], vfull[2];     // an arrival per step of the unpacking warps
+  uint64_t vempty[4];              // the block's PV product has completed
   uint64_t s_full[3], p_full[3];   // S of a block is in its buffer (and its keys are read); P is (O rescaled where needed)
   uint64_t q_full;                 // the item's query tile is staged
   uint64_t pv_item, o_free;        // the item's last PV has completed; its O has been read
@@ -995,14 +994,14 @@ struct F2 {
   PE_DEV F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
   PE_DEV explicit F2(uint64_t x) : v(x) {}
   PE_DEV float lo() const {
-    float a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-    return a;
+    float x;
+    asm("mov.b64 {%0, _}, %1;" : "=f"(x) : "l"(v));
+    return x;
   }
   PE_DEV float hi() const {
-    float a, b;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-    return b;
+    float x;
+    asm("mov.b64 {_, %0}, %1;" : "=f"(x) : "l"(v));
+    return x;
   }
   static PE_DEV F2 fma(F2 a, F2 b, F2 c) {
     uint64_t d;
@@ -1100,7 +1099,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
     constexpr uint32_t kIdS = idesc_bf16(kTileRows, kTileBlk);               // N = positions
     constexpr uint32_t kIdO = idesc_bf16(kTileRows, HD) | kIdescTransposeB;  // V is MN-major
     const uint64_t dk = sdesc_k_sw128(sQ + C::KRING), dv = sdesc_mn_sw128(sQ + C::VRING, kTileBlk * 128);
-    uint64_t dq = 0;
+    const uint64_t dq = sdesc_k_sw128(sQ);
     // The products run in the order of their issue: an S after the PV whose P it overwrites.
     auto issue_s = [&](int x) -> bool {
       const int s = x % ST;
@@ -1124,7 +1123,6 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       const int nblk = blocks_of(seg);
       if (nblk == 0) continue;
       stop = !wait(&ctl->q_full, (uint32_t)ii);
-      dq = sdesc_k_sw128(sQ + (C::QB == 2 && (ii & 1) ? C::Q : 0));
       for (int j = 0; j < NB && j < nblk && !stop; ++j) stop = !issue_s(gi + j);
 #pragma unroll 1
       for (int j = 0; j < nblk && !stop; ++j) {
@@ -1160,7 +1158,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
     const PairBits bits;
     // Steps of two pages are counted through the CTA's blocks; step q belongs to warp q % UNPACK.  A row (position)
     // per lane.
-    constexpr int PP = 2, PER = 2;
+    constexpr int PP = 2, PER = 2;  // pages of a step, steps of a block
     const int uw = warp - 1, row = lane;
     const uint32_t row_x = (uint32_t)(row & 7) << 4;
     const uint32_t step = (uint32_t)a.n_kv * L::kRecord;
@@ -1182,7 +1180,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       }
       if (more) {
         if (n_ids == 0) {  // the ids of this warp's next 32 pages, one per lane
-          const int x = seg.page0 + page + (lane / PP) * (C::UNPACK * PP) + lane % PP;  // (even lanes: the first of a step's two)
+          const int x = seg.page0 + page + (lane / PP) * (C::UNPACK * PP) + lane % PP;
           ids = -1;
           if (x < seg.page1) {
             ids = __ldcg(a.block_table + (size_t)((uint32_t)(ln.tile0 + seg.k) / ln.tps) * a.max_pages + x);
@@ -1324,13 +1322,13 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
     };
     // the query tile, entries in the order of the key words: unit w = t * HD/32 + u holds entries 4t..4t+3 of
     // blocks 2u and 2u + 1; zeros behind the tile's vectors
-    auto stage_q = [&](const Segment& sg, int buf) {
+    auto stage_q = [&](const Segment& sg) {
       const TileRows t = lo.tile(ln, sg.k);
 #pragma unroll 1
       for (int idx = et; idx < kTileRows * CH; idx += kTileRows) {
         const int m = idx / CH, w = idx % CH;
         const __nv_bfloat16* src = qbuf + row_of(t, m < t.M ? m : 0, sg.g, a.q_stride) + 32 * (w % (HD / 32)) + 4 * (w / (HD / 32));
-        const uint32_t dst = unit_addr<kTileRows>(sQ + (uint32_t)buf * C::Q, m, w), bytes = m < t.M ? 8u : 0u;
+        const uint32_t dst = unit_addr<kTileRows>(sQ, m, w), bytes = m < t.M ? 8u : 0u;
         copy8(dst, src, bytes);
         copy8(dst + 8, src + 16, bytes);
       }
@@ -1356,12 +1354,11 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
     };
     int gi = 0, ii = 0;
     bool more = advance(seg);
-    if (more) stage_q(seg, 0);
+    if (more) stage_q(seg);
     while (more) {
       q_staged();
       const Segment cur = seg;
       more = walk.next(seg, u1) && advance(seg);
-      if (C::QB == 2 && more) stage_q(seg, (ii + 1) & 1);
       const TileRows tr = lo.tile(ln, cur.k);
       const int nblk = blocks_of(cur);
       const bool valid = r < tr.M;
@@ -1448,7 +1445,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       gi += nblk;
       if (!wait(&ctl->pv_item, (uint32_t)ii)) break;
       tc_fence_after();
-      if (C::QB == 1 && more) stage_q(seg, 0);  // every product of this item has completed
+      if (more) stage_q(seg);  // every product of this item has completed
       const bool whole = cur.from_start && cur.to_end;
       if (warp_any) {
         const float inv = whole ? (l > 0.f ? kPackedUnit / l : 0.f) : 1.f;
@@ -1680,10 +1677,16 @@ int line_grid(const PackedAttnArgs& a, const Line& ln, int most) {
 }
 
 template <typename T, int HD, int NQ>
+Line small_line(const PackedAttnArgs& a, int* per_launch) {
+  return make_line(a, Small<T, HD, NQ>::ROWS, 2, 3, kSmallRangeCost, per_launch);
+}
+Line tile_line(const PackedAttnArgs& a, int* per_launch) { return make_line(a, kTileRows, 4, 3, kTileRangeCost, per_launch); }
+
+template <typename T, int HD, int NQ>
 cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Small<T, HD, NQ>;
   int per_launch = 0;
-  Line ln = make_line(a, C::ROWS, 2, 3, kSmallRangeCost, &per_launch);
+  Line ln = small_line<T, HD, NQ>(a, &per_launch);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ln.prefix = reinterpret_cast<int*>(ws);
   ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
@@ -1707,7 +1710,7 @@ template <int HD>
 cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Tile<HD>;
   int per_launch = 0;
-  Line ln = make_line(a, kTileRows, 4, 3, kTileRangeCost, &per_launch);
+  Line ln = tile_line(a, &per_launch);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ln.prefix = reinterpret_cast<int*>(ws);
   ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
@@ -1726,13 +1729,17 @@ cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   return cudaSuccess;
 }
 
+// bf16: warp MMAs up to 16 query vectors per sequence and kv head, above them the tensor core's tiles.  B = 64 and
+// 3000 positions, 8 kv heads of 64, 8 query heads each: rows of 16 vectors 59 us (tiles: 80), of 24 vectors
+// 84 us (warp MMAs: 106).  fp32 has no exact form on the tensor core's tiles.
+long long query_vectors(const PackedAttnArgs& a) { return (long long)a.max_rows * (a.n_q / a.n_kv); }
+bool use_tiles(const PackedAttnArgs& a, pe_dtype dt) { return dt == PE_BF16 && query_vectors(a) > 16; }
+
 template <typename T, int HD>
 cudaError_t launch_attend_typed(const PackedAttnArgs& a, int sms, cudaStream_t s) {
-  const long long vectors = (long long)a.max_rows * (a.n_q / a.n_kv);
   if constexpr (sizeof(T) == 2)
-    if (vectors > 16) return launch_tile<HD>(a, sms, s);
-  if (vectors <= 8) return launch_small<T, HD, 1>(a, sms, s);
-  return launch_small<T, HD, 2>(a, sms, s);
+    if (use_tiles(a, PE_BF16)) return launch_tile<HD>(a, sms, s);
+  return query_vectors(a) <= 8 ? launch_small<T, HD, 1>(a, sms, s) : launch_small<T, HD, 2>(a, sms, s);
 }
 
 }  // namespace
@@ -1743,6 +1750,15 @@ size_t packed_attn_workspace_bytes(int head_dim, pe_dtype dt, int sms) {
   const size_t rec = (size_t)16 * (head_dim + 2) * 4, part = (size_t)16 * (head_dim + 6) * 4;
   const size_t small = 2 * rec + kSmallWarps * part, large = dt == PE_BF16 ? 2 * (size_t)kTileRows * (head_dim + 2) * 4 : 0;
   return kPrefixBytes + (size_t)sms * kMaxCtasPerSm * std::max(small, large);
+}
+
+long long packed_attn_launches(const PackedAttnArgs& a, pe_dtype dt) {
+  if (a.n_rows == 0) return 0;
+  int per_launch = 0;
+  const Line ln = use_tiles(a, dt) ? tile_line(a, &per_launch)
+                  : query_vectors(a) <= 8 ? small_line<__nv_bfloat16, 64, 1>(a, &per_launch)
+                                          : small_line<__nv_bfloat16, 64, 2>(a, &per_launch);
+  return ((long long)a.B * ln.n_tps + per_launch - 1) / per_launch;
 }
 
 cudaError_t launch_attend_packed(const PackedAttnArgs& a, pe_dtype dt, int sms, cudaStream_t s) {

@@ -105,6 +105,8 @@ def test_attend_refuses_before_launch():
     assert _attend(c, ws_bytes=full, n=4, most=4, q=_p(q), out=_p(q + 3 * 1024)) == 1
     assert _attend(c, ws_bytes=full, n=4, most=4, q=_p(q), qs=1024, out=_p(q + 1008), os=1024) == 1
     assert pe.attend_workspace_bytes(_cfg(head_dim=96)) == 0 and pe.packed_page_bytes(_cfg(B=0)) == 0
+    # bounds that B * max_rows rows make far too many tiles of
+    assert _attend(_cfg(B=60000), ws_bytes=full, n=65536, most=65536) == 2
     # the sizes that only the drafter reads do not matter here
     assert _attend(_cfg(d=7, ffn=1, K=1, vocab=2, n_layers=1), ws_bytes=full) == 0
 
