@@ -392,3 +392,83 @@ def test_round_of_pack_and_attend_captured_and_replayed(dtype):
         g.replay()
         torch.cuda.synchronize()
         a.check(pos=pos)
+
+
+# ----------------------------------------------------------------------------- more of what the calls allow
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n_kv,hd,n", [(9, 128, 21), (20, 64, 19), (40, 128, 3), (1, 64, 20011), (16, 128, 2500)])
+def test_pack_and_unpack_many_heads_and_rows(dtype, n_kv, hd, n):
+    """More heads than a CTA takes at once, numbers of heads that leave lanes over, several rows a lane."""
+    rng = np.random.default_rng(n)
+    pages = n // 16 + 2
+    cfg = _cfg(1, n_kv, n_kv, hd, dtype, pages)
+    k, v = (torch.randn(n, n_kv, hd, device="cuda").to(_dt(dtype)) for _ in range(2))
+    slots = rng.permutation(pages * 16)[:n].astype(np.int64)
+    slots[::7] = -1
+    s = torch.from_numpy(slots).cuda()
+    pool, err = pe.alloc_packed_pool(cfg, pages), _err()
+    pe.pack_kv(cfg, k, v, s, pool, err)
+    want = np.zeros(tuple(pool.shape), dtype=np.uint8)
+    packed.write(want, _np(k), _np(v), slots)
+    assert np.array_equal(pool.cpu().numpy(), want)
+    ko, vo = torch.full_like(k, 7), torch.full_like(v, 7)
+    pe.unpack_kv(cfg, pool, s, ko, vo, err)
+    wk, wv = packed.read(want, np.maximum(slots, 0))
+    dead = (slots < 0)[:, None, None]
+    assert np.array_equal(_np(ko), np.where(dead, 7, wk)) and np.array_equal(_np(vo), np.where(dead, 7, wv))
+    assert int(err.item()) == 0
+
+
+MORE = {
+    # name: (dtype, hd, n_q, n_kv, rows, ctx, max_rows): more tiles than a launch takes, bounds above the rows
+    "token-1100-sequences": ("bf16", 64, 8, 1, [1] * 1100, [1 + (7 * i) % 90 for i in range(1100)], 1),
+    "f32-1100-sequences": ("f32", 64, 2, 2, [1] * 1100, [1 + (5 * i) % 60 for i in range(1100)], 2),
+    "loose-bound": ("bf16", 64, 16, 2, [1, 2, 1, 3] * 20, [40 + 11 * i for i in range(80)], 600),
+    "f32-loose-bound": ("f32", 64, 8, 2, [1, 2, 1, 3] * 20, [40 + 11 * i for i in range(80)], 300),
+    "chunk-beside-tokens": ("bf16", 128, 8, 2, [1] * 9 + [210] + [1] * 6, [30 + 50 * i for i in range(16)], 210),
+    "draft-hd128-odd-group": ("bf16", 128, 9, 3, [13, 8, 1], [700, 64, 65], 13),
+    "wide-group": ("bf16", 64, 300, 2, [2, 1], [90, 600], 2),
+}
+
+
+@pytest.mark.parametrize("name", list(MORE))
+def test_attend_many_tiles_and_loose_bounds(name):
+    dtype, hd, n_q, n_kv, rows, ctx, most = MORE[name]
+    ctx = [max(c, r) for c, r in zip(ctx, rows)]
+    a = Att(dtype, hd, n_q, n_kv, rows, ctx, seed=len(name))
+    a.run(max_rows=most)
+    a.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hd,n_q,rows", [(64, 8, 1), (64, 16, 15), (128, 8, 33)])
+def test_attend_positions_in_any_order(hd, n_q, rows, dtype):
+    """Rows of a sequence need not be in the order of their positions, nor next to each other."""
+    ctx = [700, 90, 333]
+    a = Att(dtype, hd, n_q, 2 if n_q > 8 else 1, [rows] * 3, ctx, seed=rows)
+    rng = np.random.default_rng(rows)
+    a.pos = np.concatenate([rng.integers(-1, c, rows) for c in ctx]).astype(np.int32)
+    a.d_pos = torch.from_numpy(a.pos).cuda()
+    a.run()
+    a.check()
+
+
+def test_attend_two_calls_at_once_on_streams_of_their_own():
+    """Each call with a workspace of its own: the results are those of one after the other."""
+    calls = [Att("bf16", 64, 64, 8, [1] * 6, [1500, 20, 900, 3000, 1, 640], seed=1),
+             Att("bf16", 64, 64, 8, [14] * 6, [1500, 20, 900, 3000, 16, 640], seed=2),
+             Att("bf16", 128, 32, 4, [90, 100], [1000, 1100], seed=3)]
+    alone = []
+    for a in calls:
+        a.run()
+        alone.append(a.out.clone())
+        a.out.fill_(9.0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        for a, s in zip(calls, streams):
+            pe.attend_packed(a.cfg, a.q, a.d_pool, a.d_table, a.d_start, a.d_pos, a.max_rows, a.out, a.ws, a.err, stream=s)
+    torch.cuda.synchronize()
+    for a, want in zip(calls, alone):
+        assert torch.equal(a.out, want) and int(a.err.item()) == 0
