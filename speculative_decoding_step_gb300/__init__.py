@@ -357,6 +357,14 @@ def _tensor(t, what: str, dev: int, dtype, shape=None) -> int:
                      f"on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _vector(t, what: str, dev: int, dtype) -> int:
+    """Address of a contiguous 1-D tensor of this type on CUDA device ``dev``."""
+    if t.dtype is dtype and t.get_device() == dev and t.dim() == 1 and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what}: expected a contiguous 1-D {dtype} tensor on cuda:{dev}, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}")
+
+
 def _rows(t, what: str, dev: int, dtype, width: int, n: int):
     """Address and row stride of n rows of `width` elements ([n][width] or [n][heads][head_dim], each row
     contiguous)."""
@@ -378,16 +386,20 @@ def _rows(t, what: str, dev: int, dtype, width: int, n: int):
 
 def _current(t) -> int:
     """The device of a call's tensors, which has to be the current one (its stream is used)."""
-    dev = torch.cuda.current_device()
-    if t.get_device() != dev:
-        raise ValueError(f"expected tensors on the current device cuda:{dev}, got {t.device}")
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"expected tensors on the current CUDA device, got {t.device}")
     return dev
 
 
-def _pool(cfg, pool, dev: int):
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _pool(n_kv: int, hd: int, pool, dev: int):
     shape = pool.shape
-    if len(shape) != 3 or shape[1] != cfg.n_kv or shape[2] != 18 * cfg.head_dim:
-        raise ValueError(f"pool: expected [pages][{cfg.n_kv}][{18 * cfg.head_dim}], got {tuple(shape)}")
+    if len(shape) != 3 or shape[1] != n_kv or shape[2] != 18 * hd:
+        raise ValueError(f"pool: expected [pages][{n_kv}][{18 * hd}], got {tuple(shape)}")
     return _tensor(pool, "pool", dev, torch.uint8), shape[0]
 
 
@@ -409,50 +421,51 @@ def attend_workspace_bytes(cfg) -> int:
 def pack_kv(cfg, k, v, slots, pool, err, stream=None):
     """Round rows k, v ([n][n_kv][head_dim] or [n][n_kv*head_dim], any row stride of whole 16 bytes) to 4 bits
     and write them to the packed cache ``pool`` (alloc_packed_pool) at ``slots`` (int64; -1: passed over)."""
-    L, dev, n, w = lib(), _current(pool), len(slots), cfg.n_kv * cfg.head_dim
-    dt = cfg.torch_dtype
-    kp, ks = _rows(k, "k", dev, dt, w, n)
-    vp, vs = _rows(v, "v", dev, dt, w, n)
-    pp, pages = _pool(cfg, pool, dev)
-    if n == 0:
-        return
-    st = L.pe_pack_kv(ctypes.byref(cfg), kp, vp, ks, vs, _tensor(slots, "slots", dev, torch.int64, (n,)), n, pp, pages,
-                      _tensor(err, "err", dev, torch.int32), _stream(stream))
-    _check(st, "pe_pack_kv")
+    dev, n, dt, n_kv, hd = _current(pool), slots.numel(), cfg.torch_dtype, cfg.n_kv, cfg.head_dim
+    sp = _vector(slots, "slots", dev, torch.int64)
+    kp, ks = _rows(k, "k", dev, dt, n_kv * hd, n)
+    vp, vs = _rows(v, "v", dev, dt, n_kv * hd, n)
+    pp, pages = _pool(n_kv, hd, pool, dev)
+    ep = _tensor(err, "err", dev, torch.int32)
+    if n > 0:
+        st = (_lib or lib()).pe_pack_kv(cfg, kp, vp, ks, vs, sp, n, pp, pages, ep, _raw_stream(stream, dev))
+        if st != PE_OK:
+            raise PeError(st, "pe_pack_kv")
 
 
 def unpack_kv(cfg, pool, slots, k_out, v_out, err, stream=None):
     """Read the entries at ``slots`` back as the values they stand for (-1: the output row stays as it is)."""
-    L, dev, n, w = lib(), _current(pool), len(slots), cfg.n_kv * cfg.head_dim
-    dt = cfg.torch_dtype
-    kp, ks = _rows(k_out, "k_out", dev, dt, w, n)
-    vp, vs = _rows(v_out, "v_out", dev, dt, w, n)
-    pp, pages = _pool(cfg, pool, dev)
-    if n == 0:
-        return
-    st = L.pe_unpack_kv(ctypes.byref(cfg), pp, pages, _tensor(slots, "slots", dev, torch.int64, (n,)), n, kp, vp, ks, vs,
-                        _tensor(err, "err", dev, torch.int32), _stream(stream))
-    _check(st, "pe_unpack_kv")
+    dev, n, dt, n_kv, hd = _current(pool), slots.numel(), cfg.torch_dtype, cfg.n_kv, cfg.head_dim
+    sp = _vector(slots, "slots", dev, torch.int64)
+    kp, ks = _rows(k_out, "k_out", dev, dt, n_kv * hd, n)
+    vp, vs = _rows(v_out, "v_out", dev, dt, n_kv * hd, n)
+    pp, pages = _pool(n_kv, hd, pool, dev)
+    ep = _tensor(err, "err", dev, torch.int32)
+    if n > 0:
+        st = (_lib or lib()).pe_unpack_kv(cfg, pp, pages, sp, n, kp, vp, ks, vs, ep, _raw_stream(stream, dev))
+        if st != PE_OK:
+            raise PeError(st, "pe_unpack_kv")
 
 
 def attend_packed(cfg, q, pool, block_table, row_start, positions, max_rows, out, workspace, err, stream=None):
     """Causal grouped-query attention over a packed cache: sequence b's rows row_start[b]..row_start[b+1]-1 of
     q [n][n_q*head_dim], row r seeing positions 0..positions[r] (-1: none, zeros); ``max_rows`` bounds the rows of
     one sequence.  ``workspace``: alloc_attend_workspace."""
-    L, dev, n, w = lib(), _current(pool), len(positions), cfg.n_q * cfg.head_dim
-    dt, i32 = cfg.torch_dtype, torch.int32
-    qp, qs = _rows(q, "q", dev, dt, w, n)
-    op, os_ = _rows(out, "out", dev, dt, w, n)
-    pp, pages = _pool(cfg, pool, dev)
-    if n == 0:
-        return
-    st = L.pe_attend_packed(ctypes.byref(cfg), qp, qs, pp, pages,
-                            _tensor(block_table, "block_table", dev, i32, (cfg.B, cfg.max_pages_per_seq)),
-                            _tensor(row_start, "row_start", dev, i32, (cfg.B + 1,)),
-                            _tensor(positions, "positions", dev, i32, (n,)), n, max_rows, op, os_,
-                            _tensor(workspace, "workspace", dev, torch.uint8), workspace.shape[0],
-                            _tensor(err, "err", dev, i32), _stream(stream))
-    _check(st, "pe_attend_packed")
+    dev, n, dt, i32, n_q, hd = (_current(pool), positions.numel(), cfg.torch_dtype, torch.int32, cfg.n_q,
+                                cfg.head_dim)
+    rp = _vector(positions, "positions", dev, i32)
+    qp, qs = _rows(q, "q", dev, dt, n_q * hd, n)
+    op, os_ = _rows(out, "out", dev, dt, n_q * hd, n)
+    pp, pages = _pool(cfg.n_kv, hd, pool, dev)
+    tp = _tensor(block_table, "block_table", dev, i32, (cfg.B, cfg.max_pages_per_seq))
+    sp = _tensor(row_start, "row_start", dev, i32, (cfg.B + 1,))
+    wp = _vector(workspace, "workspace", dev, torch.uint8)
+    ep = _tensor(err, "err", dev, i32)
+    if n > 0:
+        st = (_lib or lib()).pe_attend_packed(cfg, qp, qs, pp, pages, tp, sp, rp, n, max_rows, op, os_, wp,
+                                              workspace.numel(), ep, _raw_stream(stream, dev))
+        if st != PE_OK:
+            raise PeError(st, "pe_attend_packed")
 
 
 def step(cfg, weights: DeviceWeights, kv, block_table, prev_tokens, prev_pos, num_accepted, bonus,
