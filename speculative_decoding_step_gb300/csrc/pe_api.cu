@@ -176,8 +176,9 @@ struct Plan {
   size_t st_ids, st_pos, st_slot, st_rej, st_mask, st_hmap, st_rows, st_nvalid, st_draft, st_x0;
   size_t samp, samp_acc;
   size_t total = 0;
-  // a packed cache's calls: the layer's new k and v rows before they are packed, attention scratch
-  size_t pk_k = 0, pk_v = 0, pk_attn = 0;
+  // a packed cache's calls: the layer's new k and v rows before they are packed, the slots there (the rows'
+  // own numbers), attention scratch
+  size_t pk_k = 0, pk_v = 0, pk_row = 0, pk_attn = 0;
   size_t packed_total = 0;
 };
 
@@ -269,6 +270,7 @@ Plan make_plan(const pe_config& c) {
   p.total = off;
   p.pk_k = take(eb * (size_t)p.R * c.n_kv * c.head_dim);
   p.pk_v = take(eb * (size_t)p.R * c.n_kv * c.head_dim);
+  p.pk_row = take(8 * (size_t)p.R);
   p.pk_attn = take(packed_attn_workspace_bytes(c.head_dim, c.dtype, p.sms));
   p.packed_total = off;
   return p;
@@ -653,7 +655,7 @@ pe_status pack_layer(const pe_config& c, const Plan& p, void* ws, const pe_packe
 // Where a layer's k and v rows go: its cache, or the workspace on their way to a packed one.
 void set_kv_target(GemmArgs& a, const Cache& cache, const Plan& p, void* ws, int layer) {
   if (cache.is_packed) {
-    a.k_cache = at<uint8_t>(ws, p.pk_k); a.v_cache = at<uint8_t>(ws, p.pk_v); a.tok_slot = nullptr;
+    a.k_cache = at<uint8_t>(ws, p.pk_k); a.v_cache = at<uint8_t>(ws, p.pk_v); a.tok_slot = at<int64_t>(ws, p.pk_row);
   } else {
     a.k_cache = cache.kv->k_cache[layer]; a.v_cache = cache.kv->v_cache[layer];
   }
@@ -668,6 +670,7 @@ pe_status forward_impl(const pe_config& c, const pe_weights* w, const Cache& cac
   const int hd = c.head_dim;
   // prologue (already run by pe_step's fused batch-rebuild kernel when init_done)
   InitArgs ia = make_init_args(c, p, ws, row_list, n_valid, positions, slot_mapping, err);
+  if (cache.is_packed) ia.tok_row = at<int64_t>(ws, p.pk_row);
   set_warm_ranges(ia, c, w);
   if (!init_done) PE_TRY_CUDA(launch_forward_init(ia, s));
   trace(3, s);
@@ -888,6 +891,7 @@ pe_status step_impl(const pe_config* cfg, const pe_weights* w, const Cache& cach
                                      ids, pos, slot, rej, msk, hmap, rows, nval, drows, err_word);
   const ScatterArgs sa = make_scatter_args(*cfg, w, target_hidden, ids, msk, hmap, rows, nval, x0, err_word);
   InitArgs ia = make_init_args(*cfg, p, ws, rows, nval, pos, slot, err_word);
+  if (cache.is_packed) ia.tok_row = at<int64_t>(ws, p.pk_row);
   set_warm_ranges(ia, *cfg, w);
   trace(0, s);
   PE_TRY_CUDA(launch_step_prologue(pa, sa, ia, s));
@@ -932,6 +936,7 @@ pe_status inject_kv_impl(const pe_config* cfg, const pe_weights* w, const void* 
   ia.B = c.B; ia.K = c.K; ia.max_pages = c.max_pages_per_seq; ia.num_pages = cache.num_pages();
   ia.page_size = c.page_size; ia.prev_pos = prev_pos; ia.num_accepted = num_accepted; ia.block_table = block_table;
   ia.tok_pos = at<int32_t>(ws, p.tok_pos); ia.tok_slot = at<int64_t>(ws, p.tok_slot); ia.err = err_word;
+  if (cache.is_packed) ia.tok_row = at<int64_t>(ws, p.pk_row);
   PE_TRY_CUDA(launch_inject_init(ia, s));
 
   GemmArgs base{};

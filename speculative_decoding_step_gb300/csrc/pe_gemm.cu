@@ -64,9 +64,6 @@ PE_DEV void qkv_store(const GemmArgs& a, int unit, int t, float x1, float x2, fl
   c[half] = from_float<T>(x2);
 }
 
-// Where token row t's k and v go (-1: nowhere).
-PE_DEV long long tok_slot(const GemmArgs& a, int t) { return a.tok_slot != nullptr ? a.tok_slot[t] : t; }
-
 template <typename T>
 PE_DEV void epi_qkv(const GemmArgs& a, int unit, int t, float x1, float x2, float2 tf) {
   const int half = a.head_dim >> 1;
@@ -78,7 +75,7 @@ PE_DEV void epi_qkv(const GemmArgs& a, int unit, int t, float x1, float x2, floa
     q[half] = from_float<T>(x2);
     return;
   }
-  const long long slot = tok_slot(a, t);
+  const long long slot = a.tok_slot[t];
   if (slot < 0) return;
   const bool is_k = head < a.n_q + a.n_kv;
   const int g = is_k ? head - a.n_q : head - a.n_q - a.n_kv;
@@ -667,7 +664,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int t = threadIdx.x - 64; t < BN; t += 32 * EW) {
           const int tok = tbase + t;
           pos_s[t] = tok < n_tok ? a.tok_pos[tok] : 0;
-          slot_s[t] = tok < n_tok ? tok_slot(a, tok) : -1;
+          slot_s[t] = tok < n_tok ? a.tok_slot[tok] : -1;
         }
         named_bar_sync(1, 32 * EW);
       }
@@ -929,7 +926,7 @@ __global__ void __launch_bounds__(kFinishThreads) splitk_finish_kernel(const Gem
           }
         if (EPI == EPI_QKV_ROPE) {
           pos[k] = a.tok_pos[t];
-          slot[k] = tok_slot(a, t);
+          slot[k] = a.tok_slot[t];
         }
       }
     }

@@ -146,6 +146,7 @@ struct InitArgs {
   const int64_t* slot_mapping;
   int32_t *tok_pos, *tok_seq;
   int64_t* tok_slot;
+  int64_t* tok_row;          // nullable: every row's own number (slots of k and v kept by row in the workspace)
   int32_t *seq_start, *seq_len, *seq_maxpos;
   int32_t* seq_minpos;       // smallest position of the sequence's valid rows (INT_MAX: none)
   int target_items, max_items, min_chunk;
@@ -169,7 +170,7 @@ struct InjectArgs {
   int B, K, max_pages, num_pages, page_size;
   const int32_t *prev_pos, *num_accepted, *block_table;
   int32_t* tok_pos;
-  int64_t* tok_slot;
+  int64_t *tok_slot, *tok_row;  // tok_row as InitArgs'
   int32_t* err;
 };
 cudaError_t launch_inject_init(const InjectArgs& a, cudaStream_t s);
@@ -245,7 +246,7 @@ struct GemmArgs {
   // a float and the float nearest its remainder (i < head_dim / 2 <= 64)
   float rope_tf_hi[64], rope_tf_lo[64];
   const int32_t* tok_pos;
-  const int64_t* tok_slot;   // nullable: row t's k and v go to row t of k_cache and v_cache
+  const int64_t* tok_slot;
   void *k_cache, *v_cache;
   unsigned long long* keys;  // LM head: one key per token (zero before the launch)
   float* logits_dbg;         // nullable [tokens][n_out]

@@ -178,6 +178,7 @@ __global__ void inject_init_kernel(const InjectArgs a) {
   }
   a.tok_pos[i] = p < 0 ? 0 : p;
   a.tok_slot[i] = slot;
+  if (a.tok_row != nullptr) a.tok_row[i] = i;
 }
 
 cudaError_t launch_inject_init(const InjectArgs& a, cudaStream_t s) {
@@ -207,6 +208,7 @@ PE_DEV void init_body(const InitArgs& a) {
   }
   __syncthreads();
   for (int t = tid; t < a.R; t += blockDim.x) {
+    if (a.tok_row != nullptr) a.tok_row[t] = t;
     if (t < n) {
       const int row = a.row_list[t];
       if (row < 0 || row >= a.R) {
@@ -585,6 +587,7 @@ PE_DEV void step_write_row(const PrepArgs& a, const InitArgs& ia, int row, const
     if (draft_k >= 0) a.draft_rows[bb * K + draft_k] = idx;
     ia.tok_pos[idx] = pos;
     ia.tok_slot[idx] = slot;
+    if (ia.tok_row != nullptr) ia.tok_row[idx] = idx;
     ia.tok_seq[idx] = bb;
   }
 }
