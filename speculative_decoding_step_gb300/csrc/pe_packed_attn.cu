@@ -365,7 +365,9 @@ PE_DEV float* part_record(const Line& ln, int cta, bool from_start) {
 //
 // Bound: unpacking.  A page of one head is 1152 bytes at head_dim 64: an SM's share of the HBM rate
 // brings it in about 50 cycles, in which it can issue about 200 instructions, half of them to the
-// integer pipe.
+// integer pipe; a page takes 267.  B = 64 single tokens of 64 query heads over 8 kv heads of 64, up to 16384
+// positions (163 MB): 60 us, 2.7 TB/s, schedulers busy 60 % of the time and the integer pipe 54 %.  One token over
+// 131,072 positions, 4 kv heads of 128 (75 MB): 33 us, 2.3 TB/s.
 
 constexpr int kSmallWarps = 8;
 constexpr int kSmallRangeCost = 1;  // a range's start costs about as much as a pair of pages
@@ -937,8 +939,15 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 //   four warps   do the softmax, one thread per query vector (TMEM lane).
 // A vector's reference maximum only moves when a block exceeds it by 2^8; then O is rescaled in TMEM.
 //
-// Bound (head_dim 64): per block of 64 positions about 1100 warp instructions of softmax and 900 of
-// unpacking, 500 issue cycles, beside 256 cycles of MMA and 200 of HBM.
+// Bound: the roles' work and its handover.  B = 64 draft blocks (7 to 14 rows of 64 query heads, 8 kv heads of 64,
+// up to 16384 positions: 45,000 blocks, 217 MB) take 141 us, 885 cycles of an SM per block, in which it issues
+// 1770 warp instructions (442 cycles of its four schedulers) and computes 270 cycles of products; HBM is a
+// fifth busy.  In a CTA a block takes the softmax warps 1000 cycles and the unpacking warps 970 of the 1770 that
+// it lasts; the rest they wait for each other's buffers.  Without the softmax the launch takes 126 us, without
+// the unpacking 125, without both 102, with no copies and products either 86: no one part bounds it.
+// Registers end it (eight warps of 128 in two CTAs are all there are): more unpacking warps spill.  Copies of
+// whole pages by the SM's copy engine in place of the lanes' (fewer instructions) took 159 us.
+// head_dim 128, two chunks of 500 to 691 prompt rows: 87 us, 590 TFLOP/s, bound by the same.
 
 constexpr int kTileRows = 128;
 constexpr int kTileRangeCost = 6;  // a range's start (queries, filling the pipeline, output), in blocks
