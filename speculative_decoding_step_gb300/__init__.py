@@ -131,6 +131,8 @@ class DevicePackedKV:
 
     def __init__(self, pools):
         self.pools = list(pools)
+        if not self.pools:
+            raise ValueError("expected a pool per layer")
         for t in self.pools:
             if not (t.is_cuda and t.dtype is torch.uint8 and t.is_contiguous() and t.shape == self.pools[0].shape):
                 raise ValueError("expected contiguous uint8 CUDA tensors of one shape (alloc_packed_pool)")

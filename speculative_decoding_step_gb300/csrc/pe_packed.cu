@@ -153,7 +153,8 @@ PE_DEV bool quantise(Eight& h, int by, uint32_t& nibbles, uint32_t& code) {
   // round(x / s), halves away from zero, as x times a float above 1/s plus 1.5 * 2^23 + 8 in one
   // fused operation: the sum's mantissa bits are 2^22 + the nibble.  The factor is at most two
   // rounding steps above 1/s, so an exact half goes away from zero; a bf16 x over a scale of
-  // four bits is never nearer to a half than 2^-10 without being one.
+  // four bits is never nearer to a half than 2^-10 without being one.  (A scale has
+  // eight mantissas, so the tests have seen every factor that there is.)
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // off by at most one step
   inv = __uint_as_float(__float_as_uint(inv) + 1);

@@ -113,6 +113,24 @@ def test_pack_rounds_halves_and_neighbours_of_halves_away_from_zero():
     assert np.array_equal(pool.cpu().numpy(), want) and int(err.item()) == 0
 
 
+def test_pack_rounds_bf16_halves_away_from_zero():
+    """Every half of every scale that is one in bf16, (2i + 1)/2 * s: four bits times four."""
+    c = np.arange(8, 256)
+    s = packed.SCALES[c]
+    halves = np.concatenate([np.arange(7) + 0.5, -(np.arange(7) + 0.5), [7.0, -7.0]])
+    x = (s[:, None] * halves).reshape(-1, 1, 16)
+    x = np.concatenate([x, np.zeros((-len(x) % 4, 1, 16))]).reshape(-1, 1, 64)
+    t = torch.from_numpy(x).cuda().bfloat16()
+    assert np.array_equal(_np(t), x)  # none is rounded
+    n = len(x)
+    cfg = _cfg(1, 1, 1, 64, "bf16", n // 16 + 1)
+    pool, err = pe.alloc_packed_pool(cfg, n // 16 + 1), _err()
+    pe.pack_kv(cfg, t, -t, torch.arange(n, device="cuda"), pool, err)
+    want = np.zeros(tuple(pool.shape), dtype=np.uint8)
+    packed.write(want, x, -x, np.arange(n))
+    assert np.array_equal(pool.cpu().numpy(), want) and int(err.item()) == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_pack_device_checks(dtype):
     cfg = _cfg(1, 2, 2, 64, dtype, 4)

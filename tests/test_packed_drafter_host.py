@@ -122,3 +122,5 @@ def test_packed_drafter_calls_refuse_before_launch(name):
 def test_device_packed_kv_takes_gpu_pools_only():
     with pytest.raises(ValueError):
         pe.DevicePackedKV([torch.zeros((4, 2, 18 * 64), dtype=torch.uint8)])
+    with pytest.raises(ValueError):
+        pe.DevicePackedKV([])
