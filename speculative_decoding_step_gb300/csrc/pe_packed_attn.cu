@@ -63,6 +63,8 @@ struct Line {
   int n_tps;
   Div group, heads;    // query heads per kv head, kv heads
   Div grid;            // CTAs launched
+  Div half;            // half of it (tile kernel)
+  int older;           // CTAs that take the longer pieces, half the grid, or 0
   int G;
   int tile_rows;       // query vectors per tile, 2^rows_log2
   int rows_log2;
@@ -117,7 +119,9 @@ struct Layout {
 PE_DEV int range_units(const Line& ln, int last) {  // at least one: a range that sees nothing has to be zeroed
   return max(1, (last / kPackedPage + ln.unit_pages) >> (ln.unit_pages == 2 ? 1 : 2));
 }
-PE_DEV int tile_cost(const Line& ln, const TileRows& t, int last) { return t.M == 0 ? 0 : range_units(ln, last) + ln.range_cost; }
+PE_DEV int tile_cost(const Line& ln, const TileRows& t, int last) {
+  return t.M == 0 ? 0 : range_units(ln, last) + ln.range_cost;
+}
 
 // Fills the line in.  Every thread of the CTA.
 PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, int* warp_sums) {
@@ -227,29 +231,48 @@ PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, i
   __syncthreads();
 }
 
-// A line of length T in n equal pieces (the first T % n of them one longer): n is the grid, or less where
-// that would leave a piece shorter than 2^min_log2.
+// A line of length T in n pieces: n is the grid, or less where that would leave a piece shorter than
+// 2^min_log2.  Pieces are equal (the first of them one longer where it does not come out even), except that
+// of the tile kernel's two CTAs an SM the older ones, the first half of the grid, take more than half of the
+// line: schedulers prefer the older warps, and with equal halves the younger CTA ended 13 % later.  36 of 64
+// took draft blocks at B = 64 from 151 to 146 us (34: 148.5, 40: 151).  Single tokens, whose warps fill the
+// SM's instruction slots alone as well as in pairs, gained nothing (66 us, 67 with 34).
+constexpr int kOlderShare = 36;  // of 64
 struct Cuts {
-  uint32_t n, q, r;
+  uint32_t n, h, T1, q1, r1, q2, r2;  // the first h pieces: T1, each q1 and the first r1 of them one longer; the rest
   PE_DEV Cuts(const Line& ln, int grid, uint32_t T) {
     n = grid;
-    if ((T >> ln.min_log2) >= n) {
-      q = T / ln.grid;
-      r = T - q * n;
-    } else {
+    h = (T >> 4) >= n ? ln.older : 0;  // (not for pieces of a few units)
+    if ((T >> ln.min_log2) < n) {
       n = max(1u, T >> ln.min_log2);
-      q = T >> ln.min_log2 == 0 ? T : 1u << ln.min_log2;
-      r = T - q * n;
-      while (r >= n) {  // r < 2^min_log2
-        r -= n;
-        ++q;
+      h = 0;
+      q2 = T >> ln.min_log2 == 0 ? T : 1u << ln.min_log2;
+      r2 = T - q2 * n;
+      while (r2 >= n) {  // r2 < 2^min_log2
+        r2 -= n;
+        ++q2;
       }
+    } else if (h == 0) {
+      q2 = T / ln.grid;
+      r2 = T - q2 * n;
+    }
+    T1 = q1 = r1 = 0;
+    if (h != 0) {  // as many younger as older ones
+      T1 = (T >> 6) * kOlderShare;
+      q1 = T1 / ln.half;
+      r1 = T1 - q1 * h;
+      q2 = (T - T1) / ln.half;
+      r2 = T - T1 - q2 * h;
     }
   }
-  PE_DEV uint32_t first(uint32_t c) const { return q * c + min(c, r); }
+  PE_DEV uint32_t first(uint32_t c) const {
+    return c < h ? q1 * c + min(c, r1) : T1 + q2 * (c - h) + min(c - h, r2);
+  }
   PE_DEV uint32_t piece(uint32_t u) const {  // the one that holds u
-    const uint32_t longer = r * (q + 1);
-    return u < longer ? small_quotient(u, q + 1) : r + small_quotient(u - longer, q);
+    const bool young = u >= T1;
+    const uint32_t q = young ? q2 : q1, r = young ? r2 : r1, longer = r * (q + 1);
+    if (young) u -= T1;
+    return (young ? h : 0) + (u < longer ? small_quotient(u, q + 1) : r + small_quotient(u - longer, q));
   }
 };
 
@@ -491,7 +514,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
   if (u0 == u1) return;  // the whole CTA
   {
     const uint32_t n = u1 - u0;
-    const uint32_t c0 = (n >> 3) * warp + min((uint32_t)warp, n & 7), c1 = (n >> 3) * (warp + 1) + min((uint32_t)warp + 1, n & 7);
+    const uint32_t c0 = (n >> 3) * warp + min((uint32_t)warp, n & 7);
+    const uint32_t c1 = (n >> 3) * (warp + 1) + min((uint32_t)warp + 1, n & 7);
     u1 = u0 + c1;
     u0 += c0;
   }
@@ -630,8 +654,10 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       copy_wait<S::STAGES - 1>();
       __syncwarp();
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        scale_tables<HD>(recs + h * L::kRecord, my_tab + h * (S::KTAB + S::VTAB), my_tab + h * (S::KTAB + S::VTAB) + S::KTAB, lane);
+      for (int h = 0; h < 2; ++h) {
+        uint8_t* tab = my_tab + h * (S::KTAB + S::VTAB);
+        scale_tables<HD>(recs + h * L::kRecord, tab, tab + S::KTAB, lane);
+      }
       __syncwarp();
       // ---- scores
       float sc[2][NQ][4];
@@ -758,7 +784,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
           const uint32_t sel = (j & 2) ? 0x7632u : 0x5410u;  // blocks 0, 1 of 64 entries in the lower halves
-          const uint32_t wa = __byte_perm(vw[0][j / 4], vw[1][j / 4], sel), wb = __byte_perm(vw[2][j / 4], vw[3][j / 4], sel);
+          const uint32_t wa = __byte_perm(vw[0][j / 4], vw[1][j / 4], sel);
+          const uint32_t wb = __byte_perm(vw[2][j / 4], vw[3][j / 4], sel);
           const uint32_t sa = vs[0][j], sb = vs[1][j];
           const uint32_t za = bf16x2_mul(sa, kMinus136), zb = bf16x2_mul(sb, kMinus136);
           const bool odd = j & 1;
@@ -1261,8 +1288,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       __syncwarp();  // the pages are in registers
       fetch();
       // head_dim 64: the stage is free once its last PV has completed; 128: its keys once S has
-      if (gi >= ST && !(C::JOINT ? wait(&ctl->vempty[s], (uint32_t)(gi / ST) - 1u) : wait(&ctl->s_full[s], (uint32_t)(gi / ST) - 1u)))
-        break;
+      if (gi >= ST && !wait(C::JOINT ? &ctl->vempty[s] : &ctl->s_full[s], (uint32_t)(gi / ST) - 1u)) break;
       {
         const uint32_t base = sQ + C::KRING + (uint32_t)s * C::KV + at;
         // word w = t * HD/32 + u of the row: entries 4t..4t+3 of blocks 2u and 2u + 1, unit w of the tile's row
@@ -1279,7 +1305,8 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
           for (int i = 0; i < 4; ++i) {
             const int w = 4 * c + i, u = w % (HD / 32);
             st_shared16(base + (uint32_t)((w >> 3) * kTileBlk * 128) + (((uint32_t)(w & 7) << 4) ^ row_x),
-                        bf16x2_fma(bits.pair<0>(w4[i]), sp[2 * u], zp[2 * u]), bf16x2_fma(bits.pair<1>(w4[i]), sp[2 * u], zp[2 * u]),
+                        bf16x2_fma(bits.pair<0>(w4[i]), sp[2 * u], zp[2 * u]),
+                        bf16x2_fma(bits.pair<1>(w4[i]), sp[2 * u], zp[2 * u]),
                         bf16x2_fma(bits.pair<2>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]),
                         bf16x2_fma(bits.pair<3>(w4[i]), sp[2 * u + 1], zp[2 * u + 1]));
           }
@@ -1308,8 +1335,10 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
           for (int i = 0; i < 4; ++i) {
             const int w = 4 * c + i, h = w % H;
             st_shared16(base + (uint32_t)(h * kTileBlk * 128) + (((uint32_t)(w / H) << 4) ^ row_x),
-                        bf16x2_fma(bits.pair<0>(w4[i]), sp[h][0], zp[h][0]), bf16x2_fma(bits.pair<1>(w4[i]), sp[h][0], zp[h][0]),
-                        bf16x2_fma(bits.pair<2>(w4[i]), sp[h][1], zp[h][1]), bf16x2_fma(bits.pair<3>(w4[i]), sp[h][1], zp[h][1]));
+                        bf16x2_fma(bits.pair<0>(w4[i]), sp[h][0], zp[h][0]),
+                        bf16x2_fma(bits.pair<1>(w4[i]), sp[h][0], zp[h][0]),
+                        bf16x2_fma(bits.pair<2>(w4[i]), sp[h][1], zp[h][1]),
+                        bf16x2_fma(bits.pair<3>(w4[i]), sp[h][1], zp[h][1]));
           }
         }
       }
@@ -1336,7 +1365,8 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
 #pragma unroll 1
       for (int idx = et; idx < kTileRows * CH; idx += kTileRows) {
         const int m = idx / CH, w = idx % CH;
-        const __nv_bfloat16* src = qbuf + row_of(t, m < t.M ? m : 0, sg.g, a.q_stride) + 32 * (w % (HD / 32)) + 4 * (w / (HD / 32));
+        const __nv_bfloat16* src =
+            qbuf + row_of(t, m < t.M ? m : 0, sg.g, a.q_stride) + 32 * (w % (HD / 32)) + 4 * (w / (HD / 32));
         const uint32_t dst = unit_addr<kTileRows>(sQ, m, w), bytes = m < t.M ? 8u : 0u;
         copy8(dst, src, bytes);
         copy8(dst + 8, src + 16, bytes);
@@ -1374,8 +1404,10 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       // the vector's last visible position within the segment
       bool bad = false;  // reported by lay_out
       int lim = -1;
-      if (valid)
-        lim = min(row_limit(a, __ldcg(a.positions + tr.r0 + (int)((uint32_t)(tr.m0 + r) / ln.group)), bad), cur.page1 * kPackedPage - 1);
+      if (valid) {
+        const int pos = __ldcg(a.positions + tr.r0 + (int)((uint32_t)(tr.m0 + r) / ln.group));
+        lim = min(row_limit(a, pos, bad), cur.page1 * kPackedPage - 1);
+      }
       const bool warp_any = __any_sync(0xFFFFFFFFu, valid);
       int wmin = valid ? lim : INT_MAX;
 #pragma unroll
@@ -1478,7 +1510,8 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
             for (int c = 0; c < 8; ++c) {  // i = c % 4, e = c / 4
               const int col = 2 * (c & 3) + (c >> 2), e = at + 16 * ((c >> 1) & 1) + 8 * (c & 1) + 32 * (c >> 2);
               if (whole)
-                *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16(ov[col], ov[8 + col]), pack_bf16(ov[16 + col], ov[24 + col]));
+                *reinterpret_cast<uint2*>(dst + e) =
+                    make_uint2(pack_bf16(ov[col], ov[8 + col]), pack_bf16(ov[16 + col], ov[24 + col]));
               else
                 *reinterpret_cast<float4*>(rdst + e) = make_float4(ov[col], ov[8 + col], ov[16 + col], ov[24 + col]);
             }
@@ -1615,7 +1648,8 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
       if constexpr (sizeof(T) == 4)
         *reinterpret_cast<float4*>(out) = make_float4(x[u].x * inv, x[u].y * inv, x[u].z * inv, x[u].w * inv);
       else
-        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[u].x * inv, x[u].y * inv), pack_bf16(x[u].z * inv, x[u].w * inv));
+        *reinterpret_cast<uint2*>(out) =
+            make_uint2(pack_bf16(x[u].x * inv, x[u].y * inv), pack_bf16(x[u].z * inv, x[u].w * inv));
     }
   }
 }
@@ -1689,7 +1723,9 @@ template <typename T, int HD, int NQ>
 Line small_line(const PackedAttnArgs& a, int* per_launch) {
   return make_line(a, Small<T, HD, NQ>::ROWS, 2, 3, kSmallRangeCost, per_launch);
 }
-Line tile_line(const PackedAttnArgs& a, int* per_launch) { return make_line(a, kTileRows, 4, 3, kTileRangeCost, per_launch); }
+Line tile_line(const PackedAttnArgs& a, int* per_launch) {
+  return make_line(a, kTileRows, 4, 3, kTileRangeCost, per_launch);
+}
 
 template <typename T, int HD, int NQ>
 cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
@@ -1731,6 +1767,8 @@ cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
     ln.n_tiles = (int)std::min<long long>(per_launch, tiles - t0);
     const int grid = line_grid(a, ln, sms * 2);
     ln.grid = make_div(grid);
+    ln.half = make_div(std::max(1, grid / 2));
+    ln.older = grid == 2 * sms ? sms : 0;
     e = launch_pdl(attend_tile_kernel<HD>, dim3(grid), dim3(C::THREADS), C::smem(ln.n_tiles), s, a, ln);
     if (e != cudaSuccess) return e;
     if (!ln.whole && grid > 1 && (e = launch_merge<__nv_bfloat16, HD, 2>(a, ln, grid, sms, s)) != cudaSuccess) return e;
