@@ -27,7 +27,6 @@ namespace pe {
 namespace {
 
 constexpr int kPlanTiles = 1024;    // tiles per launch (their line is held in shared memory)
-constexpr int kWholePages = 32;     // tables of at most this many pages: no range is cut between CTAs (no merge)
 constexpr float kRescaleLog2 = 8.f; // a reference maximum moves when a score exceeds it by more (log2 units)
 
 PE_DEV float ex2_approx(float x) {
@@ -967,13 +966,14 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 // A vector's reference maximum only moves when a block exceeds it by 2^8; then O is rescaled in TMEM.
 //
 // Bound: the roles' work and its handover.  B = 64 draft blocks (7 to 14 rows of 64 query heads, 8 kv heads of 64,
-// up to 16384 positions: 45,000 blocks, 217 MB) take 141 us, 885 cycles of an SM per block, in which it issues
-// 1770 warp instructions (442 cycles of its four schedulers) and computes 270 cycles of products; HBM is a
-// fifth busy.  In a CTA a block takes the softmax warps 1000 cycles and the unpacking warps 970 of the 1770 that
-// it lasts; the rest they wait for each other's buffers.  Without the softmax the launch takes 126 us, without
-// the unpacking 125, without both 102, with no copies and products either 86: no one part bounds it.
-// Registers end it (eight warps of 128 in two CTAs are all there are): more unpacking warps spill.  Copies of
-// whole pages by the SM's copy engine in place of the lanes' (fewer instructions) took 159 us.
+// up to 16384 positions: 45,000 blocks, 217 MB) take 141 us with equal pieces for an SM's CTAs: 885 cycles of an
+// SM per block, in which it issues 1770 warp instructions (442 cycles of its four schedulers) and computes 270
+// cycles of products; HBM is a fifth busy.  In a CTA a block takes the softmax warps 1000 cycles and the
+// unpacking warps 970 of the 1770 that it lasts; the rest they wait for each other's buffers.  Without the
+// softmax call and merge take 126 us of 151, without the unpacking 125, without both 102, with no copies and
+// products either 86: no one part bounds it.  Registers end it (eight warps of 128 in two CTAs are all there are):
+// more unpacking warps spill.  Copies of whole pages by the SM's copy engine in place of the lanes' (fewer
+// instructions) took 159 us of 151.
 // head_dim 128, two chunks of 500 to 691 prompt rows: 87 us, 590 TFLOP/s, bound by the same.
 
 constexpr int kTileRows = 128;
@@ -1689,9 +1689,15 @@ long long line_length(const PackedAttnArgs& a, const Line& ln) {
   return (long long)((a.max_pages + ln.unit_pages - 1) / ln.unit_pages) + ln.range_cost;
 }
 
+// Sequences of several tiles that give every SM a range: these even each other out, and twice as many pages stay
+// whole (2 x 500 rows of 8 heads, 4 kv heads of 128, 1000 positions 48 -> 42 us; 500 rows, 8 kv heads of 64, 1500
+// positions 39 -> 37 us).
+constexpr int kFillingRanges = 152;
+
 // The launch's line for tiles of `tile_rows` vectors and units of `unit_pages`, and how many of its tiles one
 // launch takes (their units, counted in 32 bits, and kPlanTiles bound it).
-Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_log2, int range_cost, int* tiles_per_launch) {
+Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_log2, int range_cost, int whole_pages,
+               int* tiles_per_launch) {
   const int G = a.n_q / a.n_kv;
   const long long vectors = (long long)a.max_rows * G;
   Line ln{};
@@ -1703,7 +1709,8 @@ Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_l
   ln.group = make_div(G);
   ln.heads = make_div(a.n_kv);
   ln.G = G;
-  ln.whole = a.max_pages <= kWholePages;
+  const long long ranges = (long long)a.B * ln.n_tps * a.n_kv;
+  ln.whole = a.max_pages <= (ln.n_tps > 1 && ranges > kFillingRanges ? 2 * whole_pages : whole_pages);
   ln.min_log2 = ln.whole ? 0 : min_log2;
   const int rows = std::min(a.max_rows, tile_rows / G + 2);
   ln.lanes = 1;
@@ -1719,19 +1726,26 @@ int line_grid(const PackedAttnArgs& a, const Line& ln, int most) {
   return (int)std::min<long long>(most, std::max(1LL, ln.whole ? ranges : (ranges * line_length(a, ln)) >> ln.min_log2));
 }
 
-template <typename T, int HD, int NQ>
-Line small_line(const PackedAttnArgs& a, int* per_launch) {
-  return make_line(a, Small<T, HD, NQ>::ROWS, 2, 3, kSmallRangeCost, per_launch);
+// Tables of at most so many pages: no range is cut between CTAs.  A CTA then works longer than its even part, by a
+// range at most, but the merge's launch goes.  Sixteen tokens, 8 kv heads of 64, 700
+// positions 14.2 -> 11.4 us; 32 x 14 rows of 8 heads, 8 kv heads of 64, 760 positions 31.9 -> 22.3 us (28.6 -> 24.0
+// where lengths vary fivefold; 16 x 10 rows of such lengths 16.1 -> 18.0).  Pages take longer in tiles and at
+// head_dim 128, so the limit is lower there: one sequence of 200 rows of 8 heads of 128 over 700 positions takes
+// 23 us cut and 29 us whole.
+constexpr int whole_pages(int head_dim, bool tiles) { return head_dim == 64 ? (tiles ? 48 : 64) : 32; }
+
+Line small_line(const PackedAttnArgs& a, int nq, int* per_launch) {
+  return make_line(a, 8 * nq, 2, 3, kSmallRangeCost, whole_pages(a.head_dim, false), per_launch);
 }
 Line tile_line(const PackedAttnArgs& a, int* per_launch) {
-  return make_line(a, kTileRows, 4, 3, kTileRangeCost, per_launch);
+  return make_line(a, kTileRows, 4, 3, kTileRangeCost, whole_pages(a.head_dim, true), per_launch);
 }
 
 template <typename T, int HD, int NQ>
 cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Small<T, HD, NQ>;
   int per_launch = 0;
-  Line ln = small_line<T, HD, NQ>(a, &per_launch);
+  Line ln = small_line(a, NQ, &per_launch);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ln.prefix = reinterpret_cast<int*>(ws);
   ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
@@ -1803,8 +1817,7 @@ long long packed_attn_launches(const PackedAttnArgs& a, pe_dtype dt) {
   if (a.n_rows == 0) return 0;
   int per_launch = 0;
   const Line ln = use_tiles(a, dt) ? tile_line(a, &per_launch)
-                  : query_vectors(a) <= 8 ? small_line<__nv_bfloat16, 64, 1>(a, &per_launch)
-                                          : small_line<__nv_bfloat16, 64, 2>(a, &per_launch);
+                                     : small_line(a, query_vectors(a) <= 8 ? 1 : 2, &per_launch);
   return ((long long)a.B * ln.n_tps + per_launch - 1) / per_launch;
 }
 
