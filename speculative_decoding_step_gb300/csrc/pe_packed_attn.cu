@@ -70,7 +70,8 @@ struct Line {
   int unit_pages;      // pages per unit
   int lanes;           // threads that look through one tile's rows (a power of two, at most 32)
   int whole;           // CTAs take whole ranges
-  int min_log2;        // a CTA's piece is at least 2^this long where there are fewer than that for all
+  int sms;
+  int pair_log2;       // pieces are at least 2^this long where there are more than SMs
   int range_cost;      // of a range's start, in units
   int* prefix;         // workspace [n_tiles + 1]: cost per head before each tile, for the merge
   float* part;         // workspace: records of cut ranges, two per CTA
@@ -230,27 +231,30 @@ PE_DEV void lay_out(const PackedAttnArgs& a, const Line& ln, const Layout& lo, i
   __syncthreads();
 }
 
-// A line of length T in n pieces: n is the grid, or less where that would leave a piece shorter than
-// 2^min_log2.  Pieces are equal (the first of them one longer where it does not come out even), except that
-// of the tile kernel's two CTAs an SM the older ones, the first half of the grid, take more than half of the
-// line: schedulers prefer the older warps, and with equal halves the younger CTA ended 13 % later.  36 of 64
-// took draft blocks at B = 64 from 151 to 146 us (34: 148.5, 40: 151).  Single tokens, whose warps fill the
-// SM's instruction slots alone as well as in pairs, gained nothing (66 us, 67 with 34).
+// A line of length T in n pieces: n is the grid, or less where that would leave a piece shorter than four units,
+// or than 2^pair_log2 where there are more pieces than SMs (a piece's start and its records cost more than
+// a CTA beside another saves).  Tiles: 14 rows of 8 heads over 4000 positions, 4 kv heads of 128, 16 us (20 with
+// eight units throughout); four sequences of them, 8 kv heads, 25.6 us with 16 units (30.9 with eight).  Single
+// tokens: 16 sequences over 4000 positions, 4 kv heads of 128, 18.6 us with eight units (19.4 with 16).
+//
+// Pieces are equal (the first of them one longer where it does not come out even), except that of the tile
+// kernel's two CTAs an SM the older ones, the first half of the grid, take more than half of the line: schedulers
+// prefer the older warps, and with equal halves the younger CTA ended 13 % later.  36 of 64 took draft blocks
+// at B = 64 from 151 to 146 us (34: 148.5, 40: 151).  Single tokens, whose warps fill the SM's instruction
+// slots alone as well as in pairs, gained nothing (66 us, 67 with 34).
+constexpr int kLoneLog2 = 2;
 constexpr int kOlderShare = 36;  // of 64
 struct Cuts {
   uint32_t n, h, T1, q1, r1, q2, r2;  // the first h pieces: T1, each q1 and the first r1 of them one longer; the rest
   PE_DEV Cuts(const Line& ln, int grid, uint32_t T) {
     n = grid;
     h = (T >> 4) >= n ? ln.older : 0;  // (not for pieces of a few units)
-    if ((T >> ln.min_log2) < n) {
-      n = max(1u, T >> ln.min_log2);
+    const uint32_t busy = ln.whole ? T : max(T >> ln.pair_log2, min(T >> kLoneLog2, (uint32_t)ln.sms));
+    if (busy < n) {
+      n = max(1u, busy);
       h = 0;
-      q2 = T >> ln.min_log2 == 0 ? T : 1u << ln.min_log2;
+      q2 = small_quotient(T, n);
       r2 = T - q2 * n;
-      while (r2 >= n) {  // r2 < 2^min_log2
-        r2 -= n;
-        ++q2;
-      }
     } else if (h == 0) {
       q2 = T / ln.grid;
       r2 = T - q2 * n;
@@ -1696,8 +1700,8 @@ constexpr int kFillingRanges = 152;
 
 // The launch's line for tiles of `tile_rows` vectors and units of `unit_pages`, and how many of its tiles one
 // launch takes (their units, counted in 32 bits, and kPlanTiles bound it).
-Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_log2, int range_cost, int whole_pages,
-               int* tiles_per_launch) {
+Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int pair_log2, int range_cost, int whole_pages,
+               int sms, int* tiles_per_launch) {
   const int G = a.n_q / a.n_kv;
   const long long vectors = (long long)a.max_rows * G;
   Line ln{};
@@ -1711,7 +1715,8 @@ Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_l
   ln.G = G;
   const long long ranges = (long long)a.B * ln.n_tps * a.n_kv;
   ln.whole = a.max_pages <= (ln.n_tps > 1 && ranges > kFillingRanges ? 2 * whole_pages : whole_pages);
-  ln.min_log2 = ln.whole ? 0 : min_log2;
+  ln.sms = sms;
+  ln.pair_log2 = pair_log2;
   const int rows = std::min(a.max_rows, tile_rows / G + 2);
   ln.lanes = 1;
   while (ln.lanes < 32 && ln.lanes * 4 < rows) ln.lanes *= 2;
@@ -1723,7 +1728,7 @@ Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int min_l
 // CTAs of a launch: no more than the tables' positions could keep busy (whole ranges: one each).
 int line_grid(const PackedAttnArgs& a, const Line& ln, int most) {
   const long long ranges = (long long)ln.n_tiles * a.n_kv;
-  return (int)std::min<long long>(most, std::max(1LL, ln.whole ? ranges : (ranges * line_length(a, ln)) >> ln.min_log2));
+  return (int)std::min<long long>(most, std::max(1LL, ln.whole ? ranges : (ranges * line_length(a, ln)) >> kLoneLog2));
 }
 
 // Tables of at most so many pages: no range is cut between CTAs.  A CTA then works longer than its even part, by a
@@ -1734,18 +1739,18 @@ int line_grid(const PackedAttnArgs& a, const Line& ln, int most) {
 // 23 us cut and 29 us whole.
 constexpr int whole_pages(int head_dim, bool tiles) { return head_dim == 64 ? (tiles ? 48 : 64) : 32; }
 
-Line small_line(const PackedAttnArgs& a, int nq, int* per_launch) {
-  return make_line(a, 8 * nq, 2, 3, kSmallRangeCost, whole_pages(a.head_dim, false), per_launch);
+Line small_line(const PackedAttnArgs& a, int nq, int sms, int* per_launch) {
+  return make_line(a, 8 * nq, 2, 3, kSmallRangeCost, whole_pages(a.head_dim, false), sms, per_launch);
 }
-Line tile_line(const PackedAttnArgs& a, int* per_launch) {
-  return make_line(a, kTileRows, 4, 3, kTileRangeCost, whole_pages(a.head_dim, true), per_launch);
+Line tile_line(const PackedAttnArgs& a, int sms, int* per_launch) {
+  return make_line(a, kTileRows, 4, 4, kTileRangeCost, whole_pages(a.head_dim, true), sms, per_launch);
 }
 
 template <typename T, int HD, int NQ>
 cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Small<T, HD, NQ>;
   int per_launch = 0;
-  Line ln = small_line(a, NQ, &per_launch);
+  Line ln = small_line(a, NQ, sms, &per_launch);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ln.prefix = reinterpret_cast<int*>(ws);
   ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
@@ -1769,7 +1774,7 @@ template <int HD>
 cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Tile<HD>;
   int per_launch = 0;
-  Line ln = tile_line(a, &per_launch);
+  Line ln = tile_line(a, sms, &per_launch);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   ln.prefix = reinterpret_cast<int*>(ws);
   ln.part = reinterpret_cast<float*>(ws + kPrefixBytes);
@@ -1816,8 +1821,8 @@ size_t packed_attn_workspace_bytes(int head_dim, pe_dtype dt, int sms) {
 long long packed_attn_launches(const PackedAttnArgs& a, pe_dtype dt) {
   if (a.n_rows == 0) return 0;
   int per_launch = 0;
-  const Line ln = use_tiles(a, dt) ? tile_line(a, &per_launch)
-                                     : small_line(a, query_vectors(a) <= 8 ? 1 : 2, &per_launch);
+  const Line ln =
+      use_tiles(a, dt) ? tile_line(a, 1, &per_launch) : small_line(a, query_vectors(a) <= 8 ? 1 : 2, 1, &per_launch);
   return ((long long)a.B * ln.n_tps + per_launch - 1) / per_launch;
 }
 
