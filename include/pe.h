@@ -401,7 +401,8 @@ pe_status pe_pack_kv(const pe_config *cfg, const void *k, const void *v, int64_t
 /*
  * Reads entries back as the values they stand for: k_out and v_out [n_rows][n_kv * head_dim]
  * of cfg->dtype, row by row from slots[row].  A row with slot -1 is left as it is, and so is
- * one with a slot outside the pool (PE_DEV_BAD_PAGE).  A slot may come more than once.
+ * one with a slot outside the pool (PE_DEV_BAD_PAGE).  A slot may come more than once.  Rows of
+ * k_out and v_out must not overlap; side by side in one buffer with one stride, they do not.
  */
 pe_status pe_unpack_kv(const pe_config *cfg, const void *pool, int32_t num_pages, const int64_t *slots,
                        int32_t n_rows, void *k_out, void *v_out, int64_t k_stride, int64_t v_stride,

@@ -1184,6 +1184,7 @@ pe_status pe_unpack_kv(const pe_config* cfg, const void* pool, int32_t num_pages
     return st;
   if (!slots || !pool || !err_word || !aligned16(pool)) return PE_ERR_INVALID_ARG;
   if (n_rows < 0 || num_pages < 1) return PE_ERR_SHAPE;
+  if (n_rows > 0 && !rows_disjoint(*cfg, k_out, k_stride, v_out, v_stride, width, n_rows)) return PE_ERR_INVALID_ARG;
   UnpackArgs a{};
   a.n_rows = n_rows; a.pool = static_cast<const uint8_t*>(pool); a.num_pages = num_pages; a.slots = slots;
   a.n_kv = cfg->n_kv; a.head_dim = cfg->head_dim; a.k_out = k_out; a.v_out = v_out; a.k_stride = k_stride;

@@ -76,6 +76,14 @@ def test_pack_and_unpack_refuse_before_launch(call):
     assert pe.lib().pe_pack_kv(None, _p(), _p(), 128, 128, _p(), 0, _p(), 4, _p(), NULL) == 1
 
 
+def test_unpack_refuses_outputs_that_overlap():
+    c, at = _cfg(), 1 << 40
+    assert _unpack(c, k=_p(at), v=_p(at), n=3) == 1
+    assert _unpack(c, k=_p(at), v=_p(at + 2 * 128 * 2), n=3) == 1          # the third row of the other
+    assert _unpack(c, k=_p(at), v=_p(at + 240), ks=256, vs=256, n=3) == 1  # side by side, 16 bytes short
+    assert _unpack(c, k=_p(at), v=_p(at + 256), ks=256, vs=264, n=3) == 1
+
+
 def _attend(cfg, q=None, qs=512, pool=None, pages=4, table=None, start=None, pos=None, n=0, most=1, out=None, os=512,
             ws=None, ws_bytes=0, err=None):
     d = lambda x, at: _p((1 << 40) + at * (1 << 32)) if x is None else x  # noqa: E731
