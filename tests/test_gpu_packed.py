@@ -490,3 +490,59 @@ def test_attend_two_calls_at_once_on_streams_of_their_own():
     torch.cuda.synchronize()
     for a, want in zip(calls, alone):
         assert torch.equal(a.out, want) and int(a.err.item()) == 0
+
+
+@pytest.mark.parametrize("rows,dtype", [(1, "bf16"), (9, "bf16"), (2, "f32")])
+def test_pages_beyond_32_bits_of_a_large_pool(rows, dtype):
+    """A cache whose pages lie beyond 4 GiB of its pool: as the same pages in a small pool, bit for bit."""
+    a = Att(dtype, 64, 64, 8, [rows, rows], [900, 333], seed=rows)
+    n, num = 2 * rows, a.pool.shape[0]
+    big_pages = (1 << 32) // (8 * 18 * 64) + 2 * num  # the last `num` pages start beyond 2^32 bytes
+    big = torch.empty((big_pages, 8, 18 * 64), dtype=torch.uint8, device="cuda")
+    base = big_pages - num
+    big[base:].copy_(a.d_pool)
+    k, v = (torch.randn(n, 8, 64, device="cuda").to(_dt(dtype)) for _ in range(2))
+    slots = torch.tensor([int(a.table[r // rows, a.pos[r] // 16]) * 16 + int(a.pos[r]) % 16 for r in range(n)],
+                         dtype=torch.int64, device="cuda")
+    pe.pack_kv(a.cfg, k, v, slots, a.d_pool, a.err)
+    pe.pack_kv(a.cfg, k, v, slots + base * 16, big, a.err)
+    assert torch.equal(big[base:], a.d_pool)
+    a.run()
+    table = torch.where(a.d_table >= 0, a.d_table + base, a.d_table)
+    out = torch.empty_like(a.out)
+    pe.attend_packed(a.cfg, a.q, big, table, a.d_start, a.d_pos, rows, out, a.ws, a.err)
+    assert torch.equal(out, a.out)
+    back = [torch.empty_like(k) for _ in range(4)]
+    pe.unpack_kv(a.cfg, a.d_pool, slots, back[0], back[1], a.err)
+    pe.unpack_kv(a.cfg, big, slots + base * 16, back[2], back[3], a.err)
+    assert torch.equal(back[0], back[2]) and torch.equal(back[1], back[3]) and int(a.err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype,hd,n_q,n_kv,spare", [("bf16", 128, 4096, 1, 1), ("bf16", 64, 300, 300, 1),
+                                                     ("f32", 64, 1024, 1, 1), ("bf16", 64, 16, 2, 1 << 20),
+                                                     ("bf16", 64, 64, 2, 1 << 20)])
+def test_attend_many_heads_and_wide_tables(dtype, hd, n_q, n_kv, spare):
+    """The most query heads, more kv heads than SMs, and a block table far wider than the positions."""
+    a = Att(dtype, hd, n_q, n_kv, [2, 1], [70, 45], seed=n_q, spare=spare)
+    a.run()
+    a.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 2, 14])
+def test_attend_rows_that_are_no_numbers_stay_alone(rows, dtype):
+    """NaN and infinite queries spoil their own rows' outputs and no other's."""
+    a = Att(dtype, 64, 16, 2, [rows] * 4, [200 + rows, 700, 33 + rows, 1200], seed=rows)
+    a.run()
+    clean = _np(a.out)
+    odd = [0, 2 * rows]  # a row each of the first and the third sequence
+    a.q[odd[0], 5] = float("nan")
+    a.q[odd[1], 70] = float("inf")
+    a.run()
+    got = _np(a.out)
+    rest = np.setdiff1d(np.arange(4 * rows), odd)
+    a.q[odd] = 0
+    out, size, depth = a.want()
+    tol = a.tolerance(out, size, depth)
+    assert np.all(np.abs(got - out)[rest] <= tol[rest]) and np.all(np.abs(clean - out)[rest] <= tol[rest])
+    assert int(a.err.item()) == 0
