@@ -9,7 +9,7 @@
 // Work.  The query vectors of a sequence and kv head (rows x G query heads, G = n_q / n_kv) are
 // cut into tiles; a (tile, kv head) pair's range of positions is counted in units.  All ranges of
 // the launch form one line (tile after tile, head after head, unit after unit), a range a little longer
-// than its units, for what its start costs.  N CTAs divide the line into equal pieces, so
+// than its units, for what its start costs.  N CTAs divide the line into pieces of about one length, so
 // ragged lengths leave no CTA idle; a unit belongs to the piece in which it starts.  A range that lies in
 // one CTA's piece is finished there; one that is cut leaves a record per CTA (reference maximum,
 // sum, unnormalised output) that the merge kernel joins in CTA order.  Every CTA works the line
