@@ -1087,7 +1087,6 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   pdl_wait();
-  pdl_trigger();
   lay_out(a, ln, lo, ctl->scratch);
   const Walk walk{ln, lo, a.n_kv};
   const uint32_t total = (uint32_t)lo.prefix[ln.n_tiles] * a.n_kv;
@@ -1121,6 +1120,9 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
+  // The next kernel may be a GEMM, which allocates tensor memory and then waits for this one: it may start once every
+  // CTA here has its own (or, above, has ended).
+  pdl_trigger();
   auto blocks_of = [](const Segment& s) { return s.page1 > s.page0 ? (s.page1 - s.page0 + 3) >> 2 : 0; };
   auto wait = [&](uint64_t* bar, uint32_t phase) {
     return warp_ok(mbar_wait(smem_u32(bar), phase & 1u, a.err, abort_flag, a.wait_ns));
