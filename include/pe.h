@@ -415,7 +415,9 @@ pe_status pe_unpack_kv(const pe_config *cfg, const void *pool, int32_t num_pages
  * through block_table [B][max_pages_per_seq]:
  *   out[r][h] = sum_x w_x v_x / sum_x w_x,   w_x = exp(q[r][h] . k_x / sqrt(head_dim)),
  * keys and values of kv head h / (n_q / n_kv), as the cache's entries stand for them.
- * positions[r] = -1: the row sees nothing and gets zeros.  Rows outside
+ * positions[r] = -1: the row sees nothing and gets zeros.  A query head (of a row that sees something) with a
+ * NaN or infinite entry gets NaN in all its outputs, and other heads and rows what they would without it; scores
+ * beyond the range of fp32 and fp32 entries above the largest bf16 number (3.39e38) may give NaN as well.  Rows outside
  * row_start[0] .. row_start[B] - 1 are left as they were.  n_rows (at most 65536) bounds the
  * rows, max_rows those of one sequence; both bounds choose the kernels, so the closer the better.
  * Launches cover B * max_rows rows, 1024 tiles of 128 query vectors each (fp32: 16; a query vector: a row's query

@@ -54,6 +54,13 @@ PE_DEV uint32_t small_quotient(uint32_t r, uint32_t d) {
   return q;
 }
 
+// The factor of a vector's output.  Without a positive sum of weights its row sees nothing (zeros), or its
+// scores are NaN or infinite (NaN, as the formula gives).  Joins take the sums of parts without a maximum (-inf)
+// as well: NaN where the scores were.
+PE_DEV float normaliser(float sum, bool sees) {
+  return sum > 0.f ? kPackedUnit / sum : sees ? __int_as_float(0x7FFFFFFF) : 0.f;
+}
+
 // ----------------------------------------------------------------------------- the line of work
 
 struct Line {
@@ -100,6 +107,12 @@ PE_DEV int row_limit(const PackedAttnArgs& a, int p, bool& bad) {
   const bool out = p < -1 || p / kPackedPage >= a.max_pages;
   bad |= out;
   return out ? -1 : p;
+}
+
+// Whether a row sees a position (for the few vectors without a sum of weights: a load each).
+PE_DEV bool row_sees(const PackedAttnArgs& a, int row) {
+  bool bad = false;  // reported by lay_out
+  return row_limit(a, __ldcg(a.positions + row), bad) >= 0;
 }
 
 // The line in shared memory, each array of n_tiles (+ 1) entries.
@@ -824,7 +837,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float inv = l[n][c] > 0.f ? kPackedUnit / l[n][c] : 0.f;
+          const float inv = normaliser(l[n][c], lim[n][c] >= 0);
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
             o[j][n][c] *= inv;
@@ -935,8 +948,8 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
         x[2] = fmaf(f, y[w].z, x[2]); x[3] = fmaf(f, y[w].w, x[3]);
       }
       if (done) {
-        const float inv = sum > 0.f ? kPackedUnit / sum : 0.f;
         const int mv = tr.m0 + v, r = (int)((uint32_t)mv / ln.group);
+        const float inv = normaliser(sum, !(sum > 0.f) && row_sees(a, tr.r0 + r));
         T* out = static_cast<T*>(a.out) + (tr.r0 + r) * a.out_stride + (g * G + mv - r * G) * HD + e;
         if constexpr (TERMS == 1)
           *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
@@ -1495,7 +1508,7 @@ __global__ void __launch_bounds__(Tile<HD>::THREADS, 2) attend_tile_kernel(const
       if (more) stage_q(seg);  // every product of this item has completed
       const bool whole = cur.from_start && cur.to_end;
       if (warp_any) {
-        const float inv = whole ? (l > 0.f ? kPackedUnit / l : 0.f) : 1.f;
+        const float inv = whole ? normaliser(l, lim >= 0) : 1.f;
         float* rec = whole ? nullptr : part_record<HD>(ln, blockIdx.x, cur.from_start);
         if (valid && !whole) {
           rec[r] = m_ref;
@@ -1604,7 +1617,11 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
         float nx = mx[u];
 #pragma unroll
         for (int i = 0; i < CB; ++i) nx = fmaxf(nx, m[u][i]);
-        if (nx == -INFINITY) continue;
+        if (nx == -INFINITY) {  // sums of 0, or NaN
+#pragma unroll
+          for (int i = 0; i < CB; ++i) sum[u] += l[u][i];
+          continue;
+        }
         const float f = ex2_approx(mx[u] - nx);
         sum[u] *= f;
         x[u].x *= f; x[u].y *= f; x[u].z *= f; x[u].w *= f;
@@ -1634,7 +1651,10 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const float m = sh_m[w][u][vl], nx = fmaxf(mx[u], m);
-            if (nx == -INFINITY) continue;
+            if (nx == -INFINITY) {
+              sum[u] += sh_l[w][u][vl];
+              continue;
+            }
             const float f = ex2_approx(mx[u] - nx), q = ex2_approx(m - nx);
             const float4 y = sh_o[w][u][lane];
             sum[u] = sum[u] * f + q * sh_l[w][u][vl];
@@ -1648,8 +1668,8 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Packe
     for (int u = 0; u < U; ++u) {
       const int v = va + u * VW;
       if (v >= tr.M) continue;
-      const float inv = sum[u] > 0.f ? kPackedUnit / sum[u] : 0.f;
       const int m = tr.m0 + v, r = (int)((uint32_t)m / ln.group);
+      const float inv = normaliser(sum[u], !(sum[u] > 0.f) && row_sees(a, tr.r0 + r));
       T* out = static_cast<T*>(a.out) + (tr.r0 + r) * a.out_stride + (g * ln.G + m - r * ln.G) * HD + el;
       if constexpr (sizeof(T) == 4)
         *reinterpret_cast<float4*>(out) = make_float4(x[u].x * inv, x[u].y * inv, x[u].z * inv, x[u].w * inv);
