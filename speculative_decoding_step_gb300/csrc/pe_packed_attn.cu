@@ -972,7 +972,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 //
 // A tile of up to 128 query vectors (bf16) against blocks of 64 positions: S = Q K^T and O += P V on
 // the 5th-generation tensor core, S and O in tensor memory, P written over S as bf16.  One unpacked
-// block serves all 128 vectors.  Roles of a CTA (two CTAs per SM):
+// block serves all 128 vectors.  Roles of a CTA (two CTAs per SM where their lines fit, see tile_ctas):
 //   one warp     issues the MMAs: a block's PV once P is there, then the S that reuses its buffer, two
 //                or three blocks on.
 //   three warps  unpack: each takes two pages of a block in turn, a row (position) per lane, from a ring
@@ -1792,6 +1792,13 @@ cudaError_t launch_small(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   return cudaSuccess;
 }
 
+// CTAs of the tile kernel that an SM holds at once: two, until the line takes too much of its shared memory (16 bytes a
+// tile: from 144 tiles a launch on at head_dim 128, 736 at 64).  Then one CTA an SM, and equal pieces: the others would
+// only begin, and lay the line out once more, when the first have ended.  14 rows of 8 heads, 4 kv heads of
+// 128, 1500 to 4000 positions: 143 sequences 153 us, 144 of them 194 us (205 with two CTAs launched for each SM).
+constexpr size_t kSmemPerSm = 228 * 1024, kSmemReserved = 1024;  // of an SM; for each CTA
+int tile_ctas(size_t smem) { return 2 * (smem + kSmemReserved) <= kSmemPerSm ? 2 : 1; }
+
 template <int HD>
 cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   using C = Tile<HD>;
@@ -1806,10 +1813,10 @@ cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
   for (long long t0 = 0; t0 < tiles; t0 += per_launch) {
     ln.tile0 = (int)t0;
     ln.n_tiles = (int)std::min<long long>(per_launch, tiles - t0);
-    const int grid = line_grid(a, ln, sms * 2);
+    const int ctas = tile_ctas(C::smem(ln.n_tiles)), grid = line_grid(a, ln, sms * ctas);
     ln.grid = make_div(grid);
     ln.half = make_div(std::max(1, grid / 2));
-    ln.older = grid == 2 * sms ? sms : 0;
+    ln.older = ctas == 2 && grid == 2 * sms ? sms : 0;
     e = launch_pdl(attend_tile_kernel<HD>, dim3(grid), dim3(C::THREADS), C::smem(ln.n_tiles), s, a, ln);
     if (e != cudaSuccess) return e;
     if (!ln.whole && grid > 1 && (e = launch_merge<__nv_bfloat16, HD, 2>(a, ln, grid, sms, s)) != cudaSuccess) return e;
