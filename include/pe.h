@@ -419,9 +419,12 @@ pe_status pe_unpack_kv(const pe_config *cfg, const void *pool, int32_t num_pages
  * NaN or infinite entry gets NaN in all its outputs, and other heads and rows what they would without it; scores
  * beyond the range of fp32 and fp32 entries above the largest bf16 number (3.39e38) may give NaN as well.  Rows outside
  * row_start[0] .. row_start[B] - 1 are left as they were.  n_rows (at most 65536) bounds the
- * rows, max_rows those of one sequence; both bounds choose the kernels, so the closer the better.
- * Launches cover B * max_rows rows, 1024 tiles of 128 query vectors each (fp32: 16; a query vector: a row's query
- * head of one kv head); bounds that would take more than 4096 of them are refused (PE_ERR_SHAPE).
+ * rows, max_rows those of one sequence; both bounds and max_pages_per_seq choose the kernels, so the closer the better
+ * (tables of at most 32 to 96 pages take no merge).
+ * Of each sequence's max_rows rows the query vectors (a row's query head of one kv head) are cut into tiles of 8
+ * (where they are at most 8), 16 (at most 16, or fp32) or 128.  A launch takes 1024 of all sequences' tiles, or
+ * fewer under very wide tables: (2^31 - 1) / (n_kv * u) with u = ceil(max_pages_per_seq / 2) + 1, for tiles of 128
+ * ceil(max_pages_per_seq / 4) + 6.  Bounds that would take more than 4096 launches are refused (PE_ERR_SHAPE).
  * fp32: products and sums keep fp32 accuracy.  bf16: the softmax weights are rounded to
  * bf16 (by at most 2^-8 of each) before the product with the values; scores, statistics and sums are
  * fp32.  out must not overlap q; rows of both in one buffer, side by side with one stride, do not.
