@@ -394,8 +394,13 @@ PE_DEV float* part_record(const Line& ln, int cta, bool from_start) {
 //   400 instructions a page.
 //   Values: two positions' words give pairs of positions; P is rounded to bf16 and transposed by
 //   movmatrix into the other operand.
+// bf16: P is rounded to bf16, as the queries and outputs are and as in attn_bf16_kernel (half a step, 2^-8 of a
+// weight; a second term would double the products).
 // fp32: q and P are each split into three bf16 terms (24 bits), three MMAs for one; keys and values
-// are exact in bf16, so the products are those of fp32.
+// are exact in bf16, so the products are those of fp32.  The tensor cores cut what they add to an accumulator
+// instead of rounding it, so each page's PV starts at zero and is added to O in fp32: over 16,384 positions outputs
+// are off by 8e-7 of the largest (1.6e-5, all towards zero, through one accumulator, for 3 to 12 % less time).  Against
+// bf16's rounding the cut is nothing (1e-5 there).
 // A CTA's piece of the line is divided once more, evenly, among its eight warps, each of which runs on its
 // own over whole ranges, or parts, of its piece; at the end the parts of ranges that the warps
 // share join in shared memory.  (Dividing every range among the eight warps instead, with a join
@@ -810,9 +815,17 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
                                   bf16x2_fma(odd ? bits.pair<2>(wb) : bits.pair<0>(wb), sb, zb),
                                   bf16x2_fma(odd ? bits.pair<3>(wb) : bits.pair<1>(wb), sb, zb)};
 #pragma unroll
-          for (int n = 0; n < NQ; ++n)
+          for (int n = 0; n < NQ; ++n) {
+            if constexpr (TERMS == 1) {
+              mma16816(o[j][n], af, pf[h][0][n][0], pf[h][0][n][1]);
+            } else {
+              float d[4] = {0.f, 0.f, 0.f, 0.f};  // of this page
 #pragma unroll
-            for (int k = TERMS - 1; k >= 0; --k) mma16816(o[j][n], af, pf[h][k][n][0], pf[h][k][n][1]);
+              for (int k = TERMS - 1; k >= 0; --k) mma16816(d, af, pf[h][k][n][0], pf[h][k][n][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[j][n][e] += d[e];
+            }
+          }
         }
       }
       __syncwarp();  // the stage and the tables are read
