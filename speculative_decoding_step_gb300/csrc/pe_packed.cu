@@ -90,10 +90,10 @@ struct Lane {
 };
 
 // How a launch deals out rows and heads: a CTA has `heads` groups of lanes side by side for `rows` rows at a
-// time, `steps` times, and again for the heads that are left.  Addresses then advance by additions, and the
-// CTAs are all resident at once, eight an SM (four: a third more time, the loads of a step wait for the
-// one before; sixteen: the same).  With a CTA per 128 lanes' rows, the instructions that found each lane's place
-// were half of all.
+// time, `steps` times, and again for the heads that are left.  Addresses then advance by additions, and there
+// are eight CTAs an SM (four: a third more time, the loads of a step wait for the one before; sixteen: the same), all
+// resident at once but for packing fp32, whose registers leave six.  With a CTA per 128 lanes' rows, the
+// instructions that found each lane's place were half of all.
 struct Deal {
   int heads, rows, steps, n_kv;
   Div by_heads;
@@ -177,9 +177,11 @@ PE_DEV bool quantise(Eight& h, int by, uint32_t& nibbles, uint32_t& code) {
 
 // Packing and reading back are bound by memory in principle: bytes of the rows and of their packed form, once
 // each.  Measured, 12,026 rows of 4 heads of 128 entries in bf16 (56 MB both ways) are packed and read back in
-// 21 us, 24,586 rows of 8 heads of 64 read back (65 MB) in 19 us, half of the copy rate: launches this short
-// are a wave of loads, a wave of stores and the way in and out.  Loading a step ahead of its use did not
-// change that (21.6 and 17.7 us), nor did longer rows per lane.
+// 17.4 us (20.7 as a graph), 24,586 rows of 8 heads of 64 read back (65 MB) in 16.1 us (18.6): 3.2 and 4.0 TB/s.  A lane
+// takes five and eleven steps there, one after the other, each a chain of dependent loads (the slot, then, reading
+// back, the entries) and stores; no unit is full (schedulers 45 to 64 % busy, integer pipe 42 to 54 %, DRAM below
+// 27 %).  Loading one step ahead of its use did not change the times (21.6 and 17.7 us against 21 and 18 then), nor did
+// longer rows per lane.
 
 // HD/8 lanes per (row, head), eight keys and eight values each.
 template <typename T, int HD>

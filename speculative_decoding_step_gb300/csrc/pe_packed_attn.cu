@@ -409,9 +409,10 @@ PE_DEV float* part_record(const Line& ln, int cta, bool from_start) {
 //
 // Bound: unpacking.  A page of one head is 1152 bytes at head_dim 64: an SM's share of the HBM rate
 // brings it in about 50 cycles, in which it can issue about 200 instructions, half of them to the
-// integer pipe; a page takes 267.  B = 64 single tokens of 64 query heads over 8 kv heads of 64, up to 16384
-// positions (163 MB): 60 us, 2.7 TB/s, schedulers busy 60 % of the time and the integer pipe 54 %.  One token over
-// 131,072 positions, 4 kv heads of 128 (75 MB): 33 us, 2.3 TB/s.
+// integer pipe; a page takes 267, in a chain (copies, tables, scores, softmax, values) that a warp goes through
+// pair by pair, with 16 warps an SM to fill each other's waits.  B = 64 single tokens of 64 query heads over 8 kv heads of
+// 64, up to 16384 positions (163 MB): 60 to 62 us, 2.7 TB/s, schedulers busy 60 % of the time and the integer pipe
+// 54 %.  One token over 131,072 positions, 4 kv heads of 128 (75 MB): 34 us, 2.2 TB/s, 50 and 47 %.
 
 constexpr int kSmallWarps = 8;
 constexpr int kSmallRangeCost = 1;  // a range's start costs about as much as a pair of pages
@@ -996,15 +997,16 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 // A vector's reference maximum only moves when a block exceeds it by 2^8; then O is rescaled in TMEM.
 //
 // Bound: the roles' work and its handover.  B = 64 draft blocks (7 to 14 rows of 64 query heads, 8 kv heads of 64,
-// up to 16384 positions: 45,000 blocks, 217 MB) take 141 us with equal pieces for an SM's CTAs: 885 cycles of an
-// SM per block, in which it issues 1770 warp instructions (442 cycles of its four schedulers) and computes 270
-// cycles of products; HBM is a fifth busy.  In a CTA a block takes the softmax warps 1000 cycles and the
+// up to 16384 positions: 45,000 blocks, 217 MB) take 134 us, and 141 with equal pieces for an SM's CTAs: then 885 cycles
+// of an SM per block, in which it issues 1770 warp instructions (442 cycles of its four schedulers) and computes 270
+// cycles of products; HBM is a fifth busy, the exponent unit 23 %.  In a CTA a block takes the softmax warps 1000 cycles and the
 // unpacking warps 970 of the 1770 that it lasts; the rest they wait for each other's buffers.  Without the
 // softmax call and merge take 126 us of 151, without the unpacking 125, without both 102, with no copies and
 // products either 86: no one part bounds it.  Registers end it (eight warps of 128 in two CTAs are all there are):
 // more unpacking warps spill.  Copies of whole pages by the SM's copy engine in place of the lanes' (fewer
 // instructions) took 159 us of 151.
-// head_dim 128, two chunks of 500 to 691 prompt rows: 87 us, 590 TFLOP/s, bound by the same.
+// head_dim 128, two chunks of 500 to 691 prompt rows: 85 us, 605 TFLOP/s, bound by the same; every tile unpacks its
+// pages for itself.
 
 constexpr int kTileRows = 128;
 constexpr int kTileRangeCost = 6;  // a range's start (queries, filling the pipeline, output), in blocks
@@ -1731,7 +1733,7 @@ long long line_length(const PackedAttnArgs& a, const Line& ln) {
 // Sequences of several tiles that give every SM a range: these even each other out, and twice as many pages stay
 // whole (2 x 500 rows of 8 heads, 4 kv heads of 128, 1000 positions 48 -> 42 us; 500 rows, 8 kv heads of 64, 1500
 // positions 39 -> 37 us).
-constexpr int kFillingRanges = 152;
+bool filling(const Line& ln, long long ranges, int sms) { return ln.n_tps > 1 && ranges > sms; }
 
 // The launch's line for tiles of `tile_rows` vectors and units of `unit_pages`, and how many of its tiles one
 // launch takes (their units, counted in 32 bits, and kPlanTiles bound it).
@@ -1749,7 +1751,7 @@ Line make_line(const PackedAttnArgs& a, int tile_rows, int unit_pages, int pair_
   ln.heads = make_div(a.n_kv);
   ln.G = G;
   const long long ranges = (long long)a.B * ln.n_tps * a.n_kv;
-  ln.whole = a.max_pages <= (ln.n_tps > 1 && ranges > kFillingRanges ? 2 * whole_pages : whole_pages);
+  ln.whole = a.max_pages <= (filling(ln, ranges, sms) ? 2 : 1) * whole_pages;
   ln.sms = sms;
   ln.pair_log2 = pair_log2;
   const int rows = std::min(a.max_rows, tile_rows / G + 2);
@@ -1771,7 +1773,7 @@ int line_grid(const PackedAttnArgs& a, const Line& ln, int most) {
 // positions 14.2 -> 11.4 us; 32 x 14 rows of 8 heads, 8 kv heads of 64, 760 positions 31.9 -> 22.3 us (28.6 -> 24.0
 // where lengths vary fivefold; 16 x 10 rows of such lengths 16.1 -> 18.0).  Pages take longer in tiles and at
 // head_dim 128, so the limit is lower there: one sequence of 200 rows of 8 heads of 128 over 700 positions takes
-// 23 us cut and 29 us whole.
+// 23 us cut and 29 us whole.  The host knows the tables' width alone, so short contexts under wide tables are cut.
 constexpr int whole_pages(int head_dim, bool tiles) { return head_dim == 64 ? (tiles ? 48 : 64) : 32; }
 
 Line small_line(const PackedAttnArgs& a, int nq, int sms, int* per_launch) {
@@ -1839,7 +1841,9 @@ cudaError_t launch_tile(const PackedAttnArgs& a, int sms, cudaStream_t s) {
 
 // bf16: warp MMAs up to 16 query vectors per sequence and kv head, above them the tensor core's tiles.  B = 64 and
 // 3000 positions, 8 kv heads of 64, 8 query heads each: rows of 16 vectors 59 us (tiles: 80), of 24 vectors
-// 84 us (warp MMAs: 106).  fp32 has no exact form on the tensor core's tiles.
+// 84 us (warp MMAs: 106); 4 kv heads of 128 likewise, 16 vectors 56 us (73) and 24 vectors 76 us (100).  Over a single
+// sequence of 3900 positions the two are within 10 % of each other from 8 to 16 vectors.  fp32 has no exact form on the
+// tensor core's tiles.
 long long query_vectors(const PackedAttnArgs& a) { return (long long)a.max_rows * (a.n_q / a.n_kv); }
 bool use_tiles(const PackedAttnArgs& a, pe_dtype dt) { return dt == PE_BF16 && query_vectors(a) > 16; }
 
