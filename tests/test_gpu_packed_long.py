@@ -1,5 +1,5 @@
 """Packed-cache calls as large as their use: attention whose line of work is divided unevenly between an SM's CTAs, and
-the drafter over contexts whose ranges are cut and merged.
+the drafter over contexts whose ranges are cut and merged, also two rounds at once.
 
 The measures are those of test_gpu_packed.py and test_gpu_packed_drafter.py (tolerances derived there).
 """
@@ -83,3 +83,35 @@ def test_round_over_a_long_packed_cache_against_oracle(name):
 @pytest.mark.parametrize("name", list(LONG))
 def test_step_over_a_long_packed_cache_equals_the_stages_and_its_graph(name):
     drafter.test_step_equals_the_stages_and_its_captured_graph(name)
+
+
+def test_two_rounds_at_once_on_streams_of_their_own():
+    """Rounds of two drafters, each with its caches and workspace: as one after the other."""
+    cases = [drafter._setup(LONG[name])[0] for name in ("bf16-hd64-long", "bf16-hd128-L2-long")]
+    targets = [torch.zeros((c.cfg.B, c.cfg.K + 1), dtype=torch.int32, device="cuda") for c in cases]
+    start = [[p.clone() for p in c.kv.pools] for c in cases]
+
+    def step(c, t):
+        R = c.Rd
+        c.rd.step(R["prev_tokens"], R["prev_pos"], R["num_accepted"], R["bonus"], R["target_hidden"], t, logits=True)
+
+    want = []
+    for c, t in zip(cases, targets):
+        step(c, t)
+        want.append([c.rd.draft_tokens.clone(), c.rd.logits.clone()] + [p.clone() for p in c.kv.pools])
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(4):
+        for c, pools in zip(cases, start):
+            c.rd.logits.zero_()
+            for p, q in zip(c.kv.pools, pools):
+                p.copy_(q)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for c, t, s in zip(cases, targets, streams):
+                with torch.cuda.stream(s):
+                    step(c, t)
+        torch.cuda.synchronize()
+        for c, w in zip(cases, want):
+            assert int(c.rd.err.item()) == 0
+            for x, y in zip([c.rd.draft_tokens, c.rd.logits] + c.kv.pools, w):
+                assert torch.equal(x, y)
