@@ -999,9 +999,9 @@ __global__ void __launch_bounds__(kSmallWarps * 32, (Small<T, HD, NQ>::CTAS))
 // Bound: the roles' work and its handover.  B = 64 draft blocks (7 to 14 rows of 64 query heads, 8 kv heads of 64,
 // up to 16384 positions: 45,000 blocks, 217 MB) take 134 us, and 141 with equal pieces for an SM's CTAs: then 885 cycles
 // of an SM per block, in which it issues 1770 warp instructions (442 cycles of its four schedulers) and computes 270
-// cycles of products; HBM is a fifth busy, the exponent unit 23 %.  In a CTA a block takes the softmax warps 1000 cycles and the
-// unpacking warps 970 of the 1770 that it lasts; the rest they wait for each other's buffers.  Without the
-// softmax call and merge take 126 us of 151, without the unpacking 125, without both 102, with no copies and
+// cycles of products; HBM is a fifth busy, the exponent unit 23 %.  In a CTA a block takes the softmax warps 1000
+// cycles and the unpacking warps 970 of the 1770 that it lasts; the rest they wait for each other's buffers.  Without
+// the softmax call and merge take 126 us of 151, without the unpacking 125, without both 102, with no copies and
 // products either 86: no one part bounds it.  Registers end it (eight warps of 128 in two CTAs are all there are):
 // more unpacking warps spill.  Copies of whole pages by the SM's copy engine in place of the lanes' (fewer
 // instructions) took 159 us of 151.
