@@ -21,6 +21,12 @@
  * The DFlash-style variant: pe_inject_kv projects the verifier's hidden states
  * straight into the drafter's KV cache.
  *
+ * Rows from other products: pe_append_kv rotates query and key rows by their positions and
+ * writes keys and values into the drafter's cache (pe_append_kv_packed: into a packed one).
+ *
+ * Matrices in microscaled 4-bit floating point: pe_quantize_mx, pe_dequantize_mx, and their
+ * product, pe_matmul_mx and pe_linear_mx.
+ *
  * A KV cache in 4 bits: pe_pack_kv, pe_unpack_kv, pe_attend_packed, and the drafter's
  * calls over such a cache: pe_draft_forward_packed, pe_step_packed, pe_inject_kv_packed.
  *
@@ -478,6 +484,93 @@ pe_status pe_inject_kv_packed(const pe_config *cfg, const pe_weights *w, const v
                               const int32_t *block_table, const int32_t *prev_pos, const int32_t *num_accepted,
                               const void *target_hidden, void *workspace, size_t workspace_bytes,
                               int32_t *err_word, pe_stream_t stream);
+
+/*
+ * Rotary positions on the way into a KV cache, for rows that did not come out of the drafter's own
+ * QKV GEMM (a prompt's, or the product of 4-bit matrices).  The P-EAGLE pages have no counterpart.
+ *
+ * Row r of q [n_rows][n_q*head_dim] and k [n_rows][n_kv*head_dim] is rotated head by head: pair i, entries
+ * (x1, x2) = (x[i], x[i + head_dim/2]), becomes
+ *   (x1 cos a - x2 sin a, x2 cos a + x1 sin a),   a = positions[axis][r] * rope_theta^(-2i/head_dim),
+ * axis = axis_of_pair[i] (a host array of head_dim/2 entries, read during the call; null: axis 0 for every pair).
+ * positions [n_axes][n_rows], 1 to 8 axes (time, height, width of pictures and video), any 32-bit value: the angle's
+ * remainder is exact, so far positions lose nothing.  Queries go to q_out (q and q_out both null: no queries),
+ * which may be q itself (the same pointer and stride); keys and the values v, as they are, to
+ *   k_cache, v_cache [num_pages][16][n_kv][head_dim]   at slots[r] = page * 16 + position % 16
+ * (int64; -1: the row's key and value are passed over, its query is not).  Slots other than -1 must differ: of two
+ * rows with one slot any mixture may be kept.  All rows are of cfg->dtype; sums are fp32, rounded once.  A slot outside
+ * the cache sets PE_DEV_BAD_PAGE and the row's key and value are passed over.  Non-finite entries spread to their pair.
+ * Reads n_q, n_kv, head_dim, dtype and rope_theta of *cfg; the fields that the packed calls read have to pass their checks.
+ * Strides as there.  q_out must share no byte with k or v, nor the caches with any of the rows or each other; rows side
+ * by side in one buffer, with one stride, share none.  n_rows = 0: nothing is launched.
+ *
+ * pe_append_kv_packed packs the rotated keys, rounded to cfg->dtype, and the values as pe_pack_kv does, with its
+ * device checks (two launches where there are queries).
+ */
+pe_status pe_append_kv(const pe_config *cfg, const void *q, const void *k, const void *v, int64_t q_stride,
+                       int64_t k_stride, int64_t v_stride, const int32_t *positions, int32_t n_axes,
+                       const uint8_t *axis_of_pair, const int64_t *slots, int32_t n_rows, void *q_out,
+                       int64_t q_out_stride, void *k_cache, void *v_cache, int32_t num_pages, int32_t *err_word,
+                       pe_stream_t stream);
+pe_status pe_append_kv_packed(const pe_config *cfg, const void *q, const void *k, const void *v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, const int32_t *positions, int32_t n_axes,
+                              const uint8_t *axis_of_pair, const int64_t *slots, int32_t n_rows, void *q_out,
+                              int64_t q_out_stride, void *pool, int32_t num_pages, int32_t *err_word,
+                              pe_stream_t stream);
+
+/*
+ * Matrices in microscaled (MX) 4-bit floating point: 4.25 bits an entry.  Drafts are guesses that the target verifies, so
+ * weights and rows in 4 bits cost acceptance, not correctness, and the drafter's time is the bytes of its weights.  The
+ * P-EAGLE pages keep weights in the model's type; they have no counterpart.
+ *
+ * 32 consecutive entries of a row share the scale 2^e, e = floor(log2 m) - 2 with m the block's largest finite magnitude,
+ * between -127 and 127 (-127 for zeros), kept as the byte e + 127.  Entry x is kept as the nearest of
+ * 0, 1/2, 1, 3/2, 2, 3, 4, 6 to |x| 2^-e, of two equally near ones the one whose place in that list is even, 6 beyond 6
+ * (so entries above 6/8 of the next power of two lose up to a quarter), with x's sign.  Every kept value is exact in bf16.
+ *
+ * A matrix of n_rows rows of `width` entries takes pe_mx_bytes(n_rows, width) bytes, 16-byte aligned: for every 128 rows,
+ * one record of 8704 bytes for each 128 entries of the width (the last ones of either filled up).  A record holds
+ *   bytes [0, 512)      the scale bytes: row r (of 128), block b (of 4) at (r % 32)*16 + (r / 32)*4 + b;
+ *   bytes [512, 8704)   the codes: row r, block b at 512 + (r / 8)*512 + b*128 + (r % 8)*16, 16 bytes of two entries each,
+ *                       the first in the lower half: sign in the upper bit, place in the list below it.
+ * So the first n rows of a matrix are a matrix, and so are the rows from a multiple of 128 on.  Rows beyond the last may
+ * hold any bytes; a row's entries beyond the width, to the end of its record, are codes 0 with scale byte 0.
+ * (Bytes made elsewhere: scale byte 255 stands for NaN; values beyond the range of fp32 become infinite.)
+ *
+ * n_rows at most 2^24 (0: nothing is launched), width at most 2^20.  Rows outside these matrices are of either type, at
+ * their element's alignment, strides in elements and at least the row's length; those at 16-byte boundaries are faster.
+ */
+size_t pe_mx_bytes(int32_t n_rows, int32_t width); /* 0: invalid */
+
+/* Rounds rows x [n_rows][width] into mx.  Device check: a NaN (kept as 0) or infinite entry (kept as +-6 of its block's
+ * scale, which comes from the finite entries) sets PE_DEV_NONFINITE. */
+pe_status pe_quantize_mx(pe_dtype dtype, const void *x, int64_t x_stride, int32_t n_rows, int32_t width, void *mx,
+                         int32_t *err_word, pe_stream_t stream);
+
+/* Reads a matrix back into x [n_rows][width] as the values it stands for. */
+pe_status pe_dequantize_mx(pe_dtype dtype, const void *mx, int32_t n_rows, int32_t width, void *x, int64_t x_stride,
+                           pe_stream_t stream);
+
+/*
+ * The product of two such matrices (nn.Linear layout: x has n_rows rows, w n_out rows, both of `width` entries):
+ *   y[r][f] = add[r][f] + sum_k x[r][k] w[f][k]
+ * y [n_rows][n_out] and add (null: nothing is added) of `dtype`; add may be y itself (the same pointer and stride: the
+ * residual add).  Products are exact, sums are fp32, rounded to `dtype` once.  y must share no byte with x or w, nor
+ * with add where that is not y itself.  Only PE_DEV_TIMEOUT can be set in *err_word.
+ */
+pe_status pe_matmul_mx(const void *x, int32_t n_rows, const void *w, int32_t n_out, int32_t width, const void *add,
+                       int64_t add_stride, pe_dtype dtype, void *y, int64_t y_stride, int32_t *err_word,
+                       pe_stream_t stream);
+
+/*
+ * The same from rows x [n_rows][width] of x_dtype, quantised on the way as by pe_quantize_mx (with its device check).
+ * workspace: >= pe_linear_mx_workspace_bytes(n_rows, width) bytes, 256-byte aligned, contents need not be initialised;
+ * not to be used by two calls, or replays of captured ones, that run concurrently.
+ */
+size_t pe_linear_mx_workspace_bytes(int32_t n_rows, int32_t width); /* 0: invalid */
+pe_status pe_linear_mx(pe_dtype x_dtype, const void *x, int64_t x_stride, int32_t n_rows, const void *w, int32_t n_out,
+                       int32_t width, const void *add, int64_t add_stride, pe_dtype y_dtype, void *y, int64_t y_stride,
+                       void *workspace, size_t workspace_bytes, int32_t *err_word, pe_stream_t stream);
 
 /*
  * Tracing (optional).  pe_draft_forward and pe_step can record caller-created

@@ -20,7 +20,8 @@ __all__ = [
     "PeError", "Config", "DeviceWeights", "DeviceKV", "DevicePackedKV", "lib", "build", "check_config", "workspace_bytes",
     "prepare_batch", "scatter_hidden", "draft_forward", "verify", "step", "status_str",
     "pack_kv", "unpack_kv", "attend_packed", "packed_page_bytes", "attend_workspace_bytes", "alloc_packed_pool",
-    "alloc_attend_workspace", "alloc_packed_workspace", "packed_workspace_bytes",
+    "alloc_attend_workspace", "alloc_packed_workspace", "packed_workspace_bytes", "append_kv", "MxMatrix", "quantize_mx",
+    "dequantize_mx", "matmul_mx", "linear_mx", "mx_bytes", "alloc_linear_mx_workspace",
     "PE_OK", "PE_DEV_BAD_TOKEN", "PE_DEV_BAD_ACCEPTED", "PE_DEV_BAD_PAGE", "PE_DEV_BAD_POSITION",
     "PE_DEV_NONFINITE", "PE_DEV_BAD_ROW", "PE_DEV_TIMEOUT", "EXPORTED_SYMBOLS",
 ]
@@ -41,7 +42,9 @@ EXPORTED_SYMBOLS = ["pe_prepare_batch", "pe_scatter_hidden", "pe_draft_forward",
                     "pe_trace_points", "pe_kernel_launches", "pe_draft_forward_noalloc", "pe_set_wait_limit_ns",
                     "pe_test_skip_pipeline_stage", "pe_inject_kv", "pe_pack_kv", "pe_unpack_kv", "pe_attend_packed",
                     "pe_packed_page_bytes", "pe_attend_workspace_bytes", "pe_packed_workspace_bytes",
-                    "pe_draft_forward_packed", "pe_step_packed", "pe_inject_kv_packed"]
+                    "pe_draft_forward_packed", "pe_step_packed", "pe_inject_kv_packed", "pe_append_kv",
+                    "pe_append_kv_packed", "pe_mx_bytes", "pe_quantize_mx", "pe_dequantize_mx", "pe_matmul_mx",
+                    "pe_linear_mx", "pe_linear_mx_workspace_bytes"]
 
 # Size of the library-owned scratch used by pe_draft_forward_noalloc (PE_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 48 << 20
@@ -192,10 +195,19 @@ def lib():
                                      [vp, ctypes.c_size_t] + [vp] * 8)
         L.pe_inject_kv_packed.argtypes = [cp, ctypes.POINTER(_Weights), vp, ctypes.POINTER(_PackedKV), vp, vp, vp, vp,
                                           vp, ctypes.c_size_t, vp, vp]
-        sizes = ("pe_packed_page_bytes", "pe_attend_workspace_bytes", "pe_packed_workspace_bytes")
+        L.pe_append_kv.argtypes = [cp, vp, vp, vp, i64, i64, i64, vp, i32, ctypes.c_char_p, vp, i32, vp, i64, vp, vp, i32,
+                                   vp, vp]
+        L.pe_append_kv_packed.argtypes = [cp, vp, vp, vp, i64, i64, i64, vp, i32, ctypes.c_char_p, vp, i32, vp, i64, vp,
+                                          i32, vp, vp]
+        L.pe_quantize_mx.argtypes = [i32, vp, i64, i32, i32, vp, vp, vp]
+        L.pe_dequantize_mx.argtypes = [i32, vp, i32, i32, vp, i64, vp]
+        L.pe_matmul_mx.argtypes = [vp, i32, vp, i32, i32, vp, i64, i32, vp, i64, vp, vp]
+        L.pe_linear_mx.argtypes = [i32, vp, i64, i32, vp, i32, i32, vp, i64, i32, vp, i64, vp, ctypes.c_size_t, vp, vp]
+        mx_sizes = ("pe_mx_bytes", "pe_linear_mx_workspace_bytes")
+        sizes = ("pe_packed_page_bytes", "pe_attend_workspace_bytes", "pe_packed_workspace_bytes") + mx_sizes
         for name in sizes:
             getattr(L, name).restype = ctypes.c_size_t
-            getattr(L, name).argtypes = [cp]
+            getattr(L, name).argtypes = [i32, i32] if name in mx_sizes else [cp]
         for name in EXPORTED_SYMBOLS:
             if name not in ("pe_status_str", "pe_workspace_bytes", "pe_kernel_launches") + sizes:
                 getattr(L, name).restype = ctypes.c_int
@@ -470,6 +482,146 @@ def attend_packed(cfg, q, pool, block_table, row_start, positions, max_rows, out
             raise PeError(st, "pe_attend_packed")
 
 
+def append_kv(cfg, q, k, v, positions, slots, cache, q_out, err, axes=None, stream=None):
+    """Rotate rows q [n][n_q*head_dim] and k [n][n_kv*head_dim] by their positions and write queries to ``q_out`` (may be
+    q; both None: no queries) and keys and values to one layer's ``cache`` at ``slots`` (int64; -1: passed over): a pair
+    (k_cache, v_cache) of [pages][16][n_kv][head_dim], or a packed pool (alloc_packed_pool).  ``positions``: int32 [n], or
+    [axes][n] with ``axes`` the axis of each of the head_dim/2 pairs, as bytes."""
+    packed = isinstance(cache, torch.Tensor)
+    dev, n, dt, n_kv, hd = _current(slots), slots.numel(), cfg.torch_dtype, cfg.n_kv, cfg.head_dim
+    sp = _vector(slots, "slots", dev, torch.int64)
+    n_axes = positions.shape[0] if positions.dim() == 2 else 1
+    pos = _tensor(positions, "positions", dev, torch.int32, (n,) if positions.dim() == 1 else (n_axes, n))
+    if axes is not None and (type(axes) is not bytes or len(axes) != hd // 2):
+        raise ValueError(f"axes: expected {hd // 2} bytes, one per pair")
+    kp, ks = _rows(k, "k", dev, dt, n_kv * hd, n)
+    vp, vs = _rows(v, "v", dev, dt, n_kv * hd, n)
+    if q is None and q_out is None:
+        qp = qs = op = os_ = 0
+    else:
+        qp, qs = _rows(q, "q", dev, dt, cfg.n_q * hd, n)
+        op, os_ = _rows(q_out, "q_out", dev, dt, cfg.n_q * hd, n)
+    ep = _tensor(err, "err", dev, torch.int32)
+    if packed:
+        pp, pages = _pool(n_kv, hd, cache, dev)
+    else:
+        kc, vc = cache
+        pages = kc.shape[0]
+        kcp = _tensor(kc, "k_cache", dev, dt, (pages, 16, n_kv, hd))
+        vcp = _tensor(vc, "v_cache", dev, dt, (pages, 16, n_kv, hd))
+    if n == 0:
+        return
+    raw = _raw_stream(stream, dev)
+    if packed:
+        st = (_lib or lib()).pe_append_kv_packed(cfg, qp, kp, vp, qs, ks, vs, pos, n_axes, axes, sp, n, op, os_, pp, pages,
+                                                 ep, raw)
+    else:
+        st = (_lib or lib()).pe_append_kv(cfg, qp, kp, vp, qs, ks, vs, pos, n_axes, axes, sp, n, op, os_, kcp, vcp, pages,
+                                          ep, raw)
+    if st != PE_OK:
+        raise PeError(st, "pe_append_kv_packed" if packed else "pe_append_kv")
+
+
+# ----------------------------------------------------------------------------- microscaled (MX) 4-bit matrices
+
+def mx_bytes(n_rows: int, width: int) -> int:
+    """Bytes of a microscaled 4-bit matrix (0: sizes out of range)."""
+    return int(lib().pe_mx_bytes(n_rows, width))
+
+
+class MxMatrix:
+    """A matrix of n_rows x width entries in microscaled 4-bit floating point, resident on the device (see pe.h)."""
+
+    def __init__(self, n_rows: int, width: int, device="cuda", data=None):
+        size = mx_bytes(n_rows, width)
+        if size == 0 and n_rows != 0:
+            raise PeError(2, "pe_mx_bytes")
+        if data is None:
+            data = torch.empty(size, dtype=torch.uint8, device=device)
+        elif not (data.is_cuda and data.dtype is torch.uint8 and data.is_contiguous() and data.numel() >= size):
+            raise ValueError(f"data: expected a contiguous uint8 CUDA tensor of at least {size} bytes")
+        self.n_rows, self.width, self.data = n_rows, width, data
+
+    def first(self, n_rows: int) -> "MxMatrix":
+        """The first n_rows rows, in the same memory."""
+        if not 0 <= n_rows <= self.n_rows:
+            raise ValueError(f"expected 0 to {self.n_rows} rows")
+        return MxMatrix(n_rows, self.width, data=self.data)
+
+
+def _mx(m, what: str, dev: int) -> int:
+    if m.data.get_device() != dev:
+        raise ValueError(f"{what}: expected a matrix on cuda:{dev}, got {m.data.device}")
+    return m.data.data_ptr()
+
+
+def _any_rows(t, what: str, dev: int, n: int, width: int):
+    """Type (as pe_dtype), address and row stride of n rows of ``width`` fp32 or bf16 elements, each row contiguous."""
+    dt = PE_BF16 if t.dtype is torch.bfloat16 else PE_F32 if t.dtype is torch.float32 else None
+    if dt is None or t.get_device() != dev or t.shape != (n, width) or (width > 1 and n > 0 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected {n} rows of {width} contiguous fp32 or bf16 elements on cuda:{dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return dt, t.data_ptr(), t.stride(0) if n > 1 else width
+
+
+def quantize_mx(x, m: MxMatrix, err, stream=None):
+    """Round rows x [n_rows][width] (fp32 or bf16) to 4 bits, into ``m``."""
+    dev = _current(x)
+    dt, xp, xs = _any_rows(x, "x", dev, m.n_rows, m.width)
+    mp, ep = _mx(m, "m", dev), _tensor(err, "err", dev, torch.int32)
+    if m.n_rows > 0:
+        st = (_lib or lib()).pe_quantize_mx(dt, xp, xs, m.n_rows, m.width, mp, ep, _raw_stream(stream, dev))
+        if st != PE_OK:
+            raise PeError(st, "pe_quantize_mx")
+
+
+def dequantize_mx(m: MxMatrix, x, stream=None):
+    """Read a matrix back into rows x [n_rows][width] (fp32 or bf16) as the values it stands for."""
+    dev = _current(x)
+    dt, xp, xs = _any_rows(x, "x", dev, m.n_rows, m.width)
+    mp = _mx(m, "m", dev)
+    if m.n_rows > 0:
+        st = (_lib or lib()).pe_dequantize_mx(dt, mp, m.n_rows, m.width, xp, xs, _raw_stream(stream, dev))
+        if st != PE_OK:
+            raise PeError(st, "pe_dequantize_mx")
+
+
+def _product(y, n: int, w: MxMatrix, add, err, dev: int):
+    """What the two products have in common: type, addresses and strides of y and of what is added."""
+    dt, yp, ys = _any_rows(y, "y", dev, n, w.n_rows)
+    adt, ap, as_ = (dt, None, 0) if add is None else _any_rows(add, "add", dev, n, w.n_rows)
+    if adt != dt:
+        raise ValueError("add: expected y's type")
+    return dt, yp, ys, ap, as_, _mx(w, "w", dev), _tensor(err, "err", dev, torch.int32)
+
+
+def matmul_mx(x: MxMatrix, w: MxMatrix, y, err, add=None, stream=None):
+    """y [x.n_rows][w.n_rows] (fp32 or bf16) = add + x . w^T; ``add`` may be y."""
+    if x.width != w.width:
+        raise ValueError(f"x and w: widths {x.width} and {w.width} differ")
+    dev, n = _current(y), x.n_rows
+    dt, yp, ys, ap, as_, wp, ep = _product(y, n, w, add, err, dev)
+    xp = _mx(x, "x", dev)
+    if n > 0:
+        st = (_lib or lib()).pe_matmul_mx(xp, n, wp, w.n_rows, w.width, ap, as_, dt, yp, ys, ep, _raw_stream(stream, dev))
+        if st != PE_OK:
+            raise PeError(st, "pe_matmul_mx")
+
+
+def linear_mx(x, w: MxMatrix, y, workspace, err, add=None, stream=None):
+    """matmul_mx of rows x [n][w.width] (fp32 or bf16) that are quantised on the way.  ``workspace``:
+    alloc_linear_mx_workspace."""
+    dev, n = _current(y), x.shape[0]
+    xdt, xp, xs = _any_rows(x, "x", dev, n, w.width)
+    dt, yp, ys, ap, as_, wp, ep = _product(y, n, w, add, err, dev)
+    sp = _vector(workspace, "workspace", dev, torch.uint8)
+    if n > 0:
+        st = (_lib or lib()).pe_linear_mx(xdt, xp, xs, n, wp, w.n_rows, w.width, ap, as_, dt, yp, ys, sp,
+                                          workspace.numel(), ep, _raw_stream(stream, dev))
+        if st != PE_OK:
+            raise PeError(st, "pe_linear_mx")
+
+
 def step(cfg, weights: DeviceWeights, kv, block_table, prev_tokens, prev_pos, num_accepted, bonus,
          target_hidden, target_tokens, workspace, out: dict, err, logits_dbg=None, stream=None):
     """One whole round.  ``out`` holds draft_tokens, num_accepted, bonus, next_prev_tokens, next_prev_pos.  ``kv``: a
@@ -521,6 +673,14 @@ def alloc_packed_workspace(cfg: Config, device="cuda") -> torch.Tensor:
     n = packed_workspace_bytes(cfg)
     if n == 0:
         raise PeError(check_config(cfg) or 2, "pe_packed_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def alloc_linear_mx_workspace(n_rows: int, width: int, device="cuda") -> torch.Tensor:
+    """Workspace of linear_mx for up to n_rows rows of this width."""
+    n = int(lib().pe_linear_mx_workspace_bytes(n_rows, width))
+    if n == 0 and n_rows != 0:
+        raise PeError(2, "pe_linear_mx_workspace_bytes")
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 

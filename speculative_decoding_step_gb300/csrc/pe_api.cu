@@ -49,6 +49,7 @@ constexpr int kMaxRows = 1 << 16;        // B*2K
 constexpr int kMaxPackedHeads = 1 << 12;  // query heads of a packed-cache call
 constexpr int kMaxPackedPages = 1 << 24;  // block-table row length of a packed-cache call
 constexpr int kMaxPackedLaunches = 4096;  // launches that the bounds of a packed-cache call may ask for
+constexpr int kMaxAxes = 8;               // position axes of an append call
 constexpr int kAttnItemsPerSlot = 4;     // attention work items aimed for, per resident CTA (load balance)
 constexpr int kAttnMinChunk = 256;       // shortest position chunk of a work item (bounds the chunks to merge)
 constexpr int kTcMaxStages = 12;
@@ -545,6 +546,137 @@ bool rows_disjoint(const pe_config& c, const void* x, int64_t x_stride, const vo
   if (d < 0) d += stride;
   return d >= w && d + w <= stride;
 }
+// Rows of any type: n of them, `row` bytes each, `stride` bytes apart.
+struct ByteRows {
+  const void* p;
+  int64_t stride, row, n;
+  Span span() const { return span_of(p, n > 0 ? (size_t)((n - 1) * stride + row) : 0); }
+};
+// Whether two sets of rows share no byte: apart altogether, or side by side in one buffer with the same stride.
+bool rows_apart(const ByteRows& x, const ByteRows& y) {
+  if (!overlaps(x.span(), y.span())) return true;
+  if (x.stride != y.stride) return false;
+  int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(y.p) - reinterpret_cast<uintptr_t>(x.p)) % x.stride;
+  if (d < 0) d += x.stride;
+  return d >= x.row && d + y.row <= x.stride;
+}
+
+// ----------------------------------------------------------------------------- MX matrices
+
+constexpr int kMaxMxRows = 1 << 24;   // rows of a matrix
+constexpr int kMaxMxWidth = 1 << 20;  // entries of a row
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+
+bool mx_sizes_ok(int32_t n_rows, int32_t width) {
+  return n_rows >= 0 && n_rows <= kMaxMxRows && width >= 1 && width <= kMaxMxWidth;
+}
+size_t mx_bytes(int32_t n_rows, int32_t width) {
+  return (size_t)((n_rows + 127) / 128) * (size_t)((width + 127) / 128) * 8704;
+}
+bool dtype_ok(pe_dtype dt) { return dt == PE_F32 || dt == PE_BF16; }
+// Rows of `width` elements of type dt at p, `stride` elements apart, at the type's own alignment.
+pe_status check_any_rows(pe_dtype dt, const void* p, int64_t stride, int64_t width) {
+  if (p == nullptr || reinterpret_cast<uintptr_t>(p) % elem_bytes(dt) != 0 || stride < width || stride > kMaxStride)
+    return PE_ERR_INVALID_ARG;
+  return PE_OK;
+}
+ByteRows byte_rows(pe_dtype dt, const void* p, int64_t stride, int64_t width, int64_t n) {
+  const int64_t eb = (int64_t)elem_bytes(dt);
+  return ByteRows{p, stride * eb, width * eb, n};
+}
+// Whether every row starts at a 16-byte boundary.
+bool rows_aligned16(pe_dtype dt, const void* p, int64_t stride, int64_t n) {
+  return aligned16(p) && (n <= 1 || stride * (int64_t)elem_bytes(dt) % 16 == 0);
+}
+
+// The operands and outputs that the two product calls share (x apart); y has n_rows > 0 rows.
+pe_status check_product(const void* w, int32_t n_rows, int32_t n_out, int32_t width, const void* add, int64_t add_stride,
+                        pe_dtype dt, const void* y, int64_t y_stride, const int32_t* err_word) {
+  if (!dtype_ok(dt)) return PE_ERR_INVALID_ARG;
+  if (!mx_sizes_ok(n_rows, width) || n_out < 1 || n_out > kMaxMxRows) return PE_ERR_SHAPE;
+  if (!w || !aligned16(w) || !err_word) return PE_ERR_INVALID_ARG;
+  pe_status st = check_any_rows(dt, y, y_stride, n_out);
+  if (st != PE_OK) return st;
+  const ByteRows ys = byte_rows(dt, y, y_stride, n_out, n_rows);
+  if (overlaps(ys.span(), span_of(w, mx_bytes(n_out, width)))) return PE_ERR_INVALID_ARG;
+  if (add != nullptr) {
+    if ((st = check_any_rows(dt, add, add_stride, n_out)) != PE_OK) return st;
+    if (!(add == y && add_stride == y_stride) && !rows_apart(ys, byte_rows(dt, add, add_stride, n_out, n_rows)))
+      return PE_ERR_INVALID_ARG;
+  }
+  return PE_OK;
+}
+
+// ----------------------------------------------------------------------------- appending rotated rows
+
+// Turns per position of each pair, mod 1, in units of 2^-64.
+void set_rope_turns(RopeTable& t, float theta, int hd, const uint8_t* axis_of_pair) {
+  for (int i = 0; i < 64; ++i) {
+    t.turns[i] = 0;
+    t.axis[i] = 0;
+    if (i >= hd / 2) continue;
+    double f = std::pow((double)theta, -2.0 * i / hd) / (2.0 * 3.14159265358979323846);
+    f -= std::floor(f);
+    t.turns[i] = (uint64_t)std::ldexp(f, 64);
+    t.axis[i] = axis_of_pair != nullptr ? axis_of_pair[i] : 0;
+  }
+}
+
+// The rows and positions of an append call; q may be null (with q_out).
+pe_status check_append(const pe_config* cfg, const void* q, const void* k, const void* v, int64_t q_stride,
+                       int64_t k_stride, int64_t v_stride, const int32_t* positions, int32_t n_axes,
+                       const uint8_t* axis_of_pair, const int64_t* slots, int32_t n_rows, const void* q_out,
+                       int64_t q_out_stride, int32_t num_pages, const int32_t* err_word) {
+  pe_status st = check_packed_cfg(cfg);
+  if (st != PE_OK) return st;
+  if (!(cfg->rope_theta > 0.f) || std::isinf(cfg->rope_theta)) return PE_ERR_INVALID_ARG;
+  const int64_t kv_row = (int64_t)cfg->n_kv * cfg->head_dim, q_row = (int64_t)cfg->n_q * cfg->head_dim;
+  if ((st = check_rows(*cfg, k, k_stride, kv_row)) != PE_OK || (st = check_rows(*cfg, v, v_stride, kv_row)) != PE_OK)
+    return st;
+  if ((q == nullptr) != (q_out == nullptr)) return PE_ERR_INVALID_ARG;
+  if (q != nullptr && ((st = check_rows(*cfg, q, q_stride, q_row)) != PE_OK ||
+                       (st = check_rows(*cfg, q_out, q_out_stride, q_row)) != PE_OK))
+    return st;
+  if (!positions || !slots || !err_word) return PE_ERR_INVALID_ARG;
+  if (n_rows < 0 || n_rows > kMaxMxRows || num_pages < 1 || n_axes < 1 || n_axes > kMaxAxes) return PE_ERR_SHAPE;
+  if (axis_of_pair != nullptr)
+    for (int i = 0; i < cfg->head_dim / 2; ++i)
+      if (axis_of_pair[i] >= n_axes) return PE_ERR_INVALID_ARG;
+  if (q != nullptr && n_rows > 0) {
+    const ByteRows out = byte_rows(cfg->dtype, q_out, q_out_stride, q_row, n_rows);
+    if (!(q == q_out && q_stride == q_out_stride) &&
+        !rows_apart(out, byte_rows(cfg->dtype, q, q_stride, q_row, n_rows)))
+      return PE_ERR_INVALID_ARG;
+    if (!rows_apart(out, byte_rows(cfg->dtype, k, k_stride, kv_row, n_rows)) ||
+        !rows_apart(out, byte_rows(cfg->dtype, v, v_stride, kv_row, n_rows)))
+      return PE_ERR_INVALID_ARG;
+  }
+  return PE_OK;
+}
+
+AppendArgs make_append_args(const pe_config& c, const void* q, int64_t q_stride, const int32_t* positions,
+                            const uint8_t* axis_of_pair, const int64_t* slots, int32_t n_rows, void* q_out,
+                            int64_t q_out_stride, int32_t num_pages, int32_t* err) {
+  AppendArgs a{};
+  a.n_rows = n_rows; a.n_q = c.n_q; a.n_kv = c.n_kv; a.q = q; a.q_stride = q_stride; a.positions = positions;
+  a.slots = slots; a.q_out = q_out; a.q_out_stride = q_out_stride; a.num_pages = num_pages; a.err = err;
+  set_rope_turns(a.rope, c.rope_theta, c.head_dim, axis_of_pair);
+  return a;
+}
+
+// Whether none of the byte ranges that a call writes meets one that it reads (rows k and v, positions, slots).
+bool append_cache_apart(const pe_config& c, const Span& cache, const void* q, int64_t q_stride, const void* k,
+                        int64_t k_stride, const void* v, int64_t v_stride, const void* q_out, int64_t q_out_stride,
+                        int32_t n_rows) {
+  const int64_t kv_row = (int64_t)c.n_kv * c.head_dim, q_row = (int64_t)c.n_q * c.head_dim;
+  if (n_rows == 0) return true;
+  if (overlaps(cache, byte_rows(c.dtype, k, k_stride, kv_row, n_rows).span()) ||
+      overlaps(cache, byte_rows(c.dtype, v, v_stride, kv_row, n_rows).span()))
+    return false;
+  return q == nullptr || (!overlaps(cache, byte_rows(c.dtype, q, q_stride, q_row, n_rows).span()) &&
+                          !overlaps(cache, byte_rows(c.dtype, q_out, q_out_stride, q_row, n_rows).span()));
+}
+
 bool step_aliasing_ok(const pe_config& c, const int32_t* block_table, const int32_t* prev_tokens,
                       const int32_t* prev_pos, const int32_t* num_accepted, const int32_t* bonus,
                       const void* target_hidden, const int32_t* target_tokens, const int32_t* draft_tokens,
@@ -1191,6 +1323,128 @@ pe_status pe_unpack_kv(const pe_config* cfg, const void* pool, int32_t num_pages
   a.v_stride = v_stride; a.err = err_word;
   PE_TRY_CUDA(launch_unpack(a, cfg->dtype, (cudaStream_t)stream));
   return PE_OK;
+}
+
+pe_status pe_append_kv(const pe_config* cfg, const void* q, const void* k, const void* v, int64_t q_stride,
+                       int64_t k_stride, int64_t v_stride, const int32_t* positions, int32_t n_axes,
+                       const uint8_t* axis_of_pair, const int64_t* slots, int32_t n_rows, void* q_out,
+                       int64_t q_out_stride, void* k_cache, void* v_cache, int32_t num_pages, int32_t* err_word,
+                       pe_stream_t stream) {
+  pe_status st = check_append(cfg, q, k, v, q_stride, k_stride, v_stride, positions, n_axes, axis_of_pair, slots,
+                              n_rows, q_out, q_out_stride, num_pages, err_word);
+  if (st != PE_OK) return st;
+  if (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return PE_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)num_pages * 16 * cfg->n_kv * cfg->head_dim * elem_bytes(cfg->dtype);
+  const Span kc = span_of(k_cache, bytes), vc = span_of(v_cache, bytes);
+  if (overlaps(kc, vc) ||
+      !append_cache_apart(*cfg, kc, q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, n_rows) ||
+      !append_cache_apart(*cfg, vc, q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, n_rows))
+    return PE_ERR_INVALID_ARG;
+  if (n_rows == 0) return PE_OK;
+  AppendArgs a = make_append_args(*cfg, q, q_stride, positions, axis_of_pair, slots, n_rows, q_out, q_out_stride,
+                                  num_pages, err_word);
+  a.k = k; a.v = v; a.k_stride = k_stride; a.v_stride = v_stride; a.k_cache = k_cache; a.v_cache = v_cache;
+  PE_TRY_CUDA(launch_append(a, cfg->head_dim, cfg->dtype, (cudaStream_t)stream));
+  return PE_OK;
+}
+
+pe_status pe_append_kv_packed(const pe_config* cfg, const void* q, const void* k, const void* v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, const int32_t* positions, int32_t n_axes,
+                              const uint8_t* axis_of_pair, const int64_t* slots, int32_t n_rows, void* q_out,
+                              int64_t q_out_stride, void* pool, int32_t num_pages, int32_t* err_word,
+                              pe_stream_t stream) {
+  pe_status st = check_append(cfg, q, k, v, q_stride, k_stride, v_stride, positions, n_axes, axis_of_pair, slots,
+                              n_rows, q_out, q_out_stride, num_pages, err_word);
+  if (st != PE_OK) return st;
+  if (!pool || !aligned16(pool)) return PE_ERR_INVALID_ARG;
+  const Span ps = span_of(pool, (size_t)num_pages * cfg->n_kv * 18 * cfg->head_dim);
+  if (!append_cache_apart(*cfg, ps, q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, n_rows))
+    return PE_ERR_INVALID_ARG;
+  if (n_rows == 0) return PE_OK;
+  const AppendArgs a = make_append_args(*cfg, q, q_stride, positions, axis_of_pair, slots, n_rows, q_out,
+                                        q_out_stride, num_pages, err_word);
+  if (q != nullptr) PE_TRY_CUDA(launch_append(a, cfg->head_dim, cfg->dtype, (cudaStream_t)stream));
+  PackArgs p{};
+  p.n_rows = n_rows; p.k = k; p.v = v; p.k_stride = k_stride; p.v_stride = v_stride; p.slots = slots;
+  p.n_kv = cfg->n_kv; p.head_dim = cfg->head_dim; p.pool = static_cast<uint8_t*>(pool); p.num_pages = num_pages;
+  p.err = err_word;
+  PE_TRY_CUDA(launch_pack_rope(p, positions, a.rope, cfg->dtype, (cudaStream_t)stream));
+  return PE_OK;
+}
+
+size_t pe_mx_bytes(int32_t n_rows, int32_t width) { return mx_sizes_ok(n_rows, width) ? mx_bytes(n_rows, width) : 0; }
+
+pe_status pe_quantize_mx(pe_dtype dtype, const void* x, int64_t x_stride, int32_t n_rows, int32_t width, void* mx,
+                         int32_t* err_word, pe_stream_t stream) {
+  if (!dtype_ok(dtype)) return PE_ERR_INVALID_ARG;
+  if (!mx_sizes_ok(n_rows, width)) return PE_ERR_SHAPE;
+  const pe_status st = check_any_rows(dtype, x, x_stride, width);
+  if (st != PE_OK) return st;
+  if (!mx || !aligned16(mx) || !err_word) return PE_ERR_INVALID_ARG;
+  if (n_rows == 0) return PE_OK;
+  if (overlaps(byte_rows(dtype, x, x_stride, width, n_rows).span(), span_of(mx, mx_bytes(n_rows, width))))
+    return PE_ERR_INVALID_ARG;
+  MxRowsArgs a{};
+  a.n_rows = n_rows; a.width = width; a.x = x; a.stride = x_stride; a.vec = rows_aligned16(dtype, x, x_stride, n_rows);
+  a.mx = static_cast<uint8_t*>(mx); a.err = err_word;
+  PE_TRY_CUDA(launch_mx_quantize(a, dtype, (cudaStream_t)stream));
+  return PE_OK;
+}
+
+pe_status pe_dequantize_mx(pe_dtype dtype, const void* mx, int32_t n_rows, int32_t width, void* x, int64_t x_stride,
+                           pe_stream_t stream) {
+  if (!dtype_ok(dtype)) return PE_ERR_INVALID_ARG;
+  if (!mx_sizes_ok(n_rows, width)) return PE_ERR_SHAPE;
+  const pe_status st = check_any_rows(dtype, x, x_stride, width);
+  if (st != PE_OK) return st;
+  if (!mx || !aligned16(mx)) return PE_ERR_INVALID_ARG;
+  if (n_rows == 0) return PE_OK;
+  if (overlaps(byte_rows(dtype, x, x_stride, width, n_rows).span(), span_of(mx, mx_bytes(n_rows, width))))
+    return PE_ERR_INVALID_ARG;
+  MxRowsArgs a{};
+  a.n_rows = n_rows; a.width = width; a.out = x; a.stride = x_stride; a.vec = rows_aligned16(dtype, x, x_stride, n_rows);
+  a.mx = const_cast<uint8_t*>(static_cast<const uint8_t*>(mx));
+  PE_TRY_CUDA(launch_mx_dequantize(a, dtype, (cudaStream_t)stream));
+  return PE_OK;
+}
+
+pe_status pe_matmul_mx(const void* x, int32_t n_rows, const void* w, int32_t n_out, int32_t width, const void* add,
+                       int64_t add_stride, pe_dtype dtype, void* y, int64_t y_stride, int32_t* err_word,
+                       pe_stream_t stream) {
+  const pe_status st = check_product(w, n_rows, n_out, width, add, add_stride, dtype, y, y_stride, err_word);
+  if (st != PE_OK) return st;
+  if (!x || !aligned16(x)) return PE_ERR_INVALID_ARG;
+  if (n_rows == 0) return PE_OK;
+  if (overlaps(byte_rows(dtype, y, y_stride, n_out, n_rows).span(), span_of(x, mx_bytes(n_rows, width))))
+    return PE_ERR_INVALID_ARG;
+  MxMatmulArgs a{};
+  a.n_rows = n_rows; a.n_out = n_out; a.width = width; a.x = static_cast<const uint8_t*>(x);
+  a.w = static_cast<const uint8_t*>(w); a.add = add; a.add_stride = add_stride; a.y = y; a.y_stride = y_stride;
+  a.wait_ns = wait_limit_ns(); a.err = err_word;
+  PE_TRY_CUDA(launch_mx_matmul(a, dtype, (cudaStream_t)stream));
+  return PE_OK;
+}
+
+size_t pe_linear_mx_workspace_bytes(int32_t n_rows, int32_t width) { return pe_mx_bytes(n_rows, width); }
+
+pe_status pe_linear_mx(pe_dtype x_dtype, const void* x, int64_t x_stride, int32_t n_rows, const void* w, int32_t n_out,
+                       int32_t width, const void* add, int64_t add_stride, pe_dtype y_dtype, void* y, int64_t y_stride,
+                       void* workspace, size_t workspace_bytes, int32_t* err_word, pe_stream_t stream) {
+  if (!dtype_ok(x_dtype)) return PE_ERR_INVALID_ARG;
+  pe_status st = check_product(w, n_rows, n_out, width, add, add_stride, y_dtype, y, y_stride, err_word);
+  if (st != PE_OK || (st = check_any_rows(x_dtype, x, x_stride, width)) != PE_OK) return st;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PE_ERR_INVALID_ARG;
+  const size_t need = pe_linear_mx_workspace_bytes(n_rows, width);
+  if (workspace_bytes < need) return PE_ERR_SHAPE;
+  if (n_rows == 0) return PE_OK;
+  const ByteRows ys = byte_rows(y_dtype, y, y_stride, n_out, n_rows), xs = byte_rows(x_dtype, x, x_stride, width, n_rows);
+  const Span ws = span_of(workspace, need);
+  if (!rows_apart(ys, xs) || overlaps(ws, ys.span()) || overlaps(ws, xs.span()) ||
+      overlaps(ws, span_of(w, mx_bytes(n_out, width))) ||
+      (add != nullptr && overlaps(ws, byte_rows(y_dtype, add, add_stride, n_out, n_rows).span())))
+    return PE_ERR_INVALID_ARG;
+  if ((st = pe_quantize_mx(x_dtype, x, x_stride, n_rows, width, workspace, err_word, stream)) != PE_OK) return st;
+  return pe_matmul_mx(workspace, n_rows, w, n_out, width, add, add_stride, y_dtype, y, y_stride, err_word, stream);
 }
 
 size_t pe_packed_page_bytes(const pe_config* cfg) {

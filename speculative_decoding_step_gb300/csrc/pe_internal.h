@@ -339,6 +339,32 @@ struct PackArgs {
 };
 cudaError_t launch_pack(const PackArgs& a, pe_dtype dt, cudaStream_t s);
 
+// Turns of each pair of a head per position, mod 1, in units of 2^-64, and the axis whose position it takes.
+struct RopeTable {
+  uint64_t turns[64];
+  uint8_t axis[64];
+};
+
+// Rows of queries, keys and values rotated and written: queries to q_out (q null: none), keys and values to the cache at
+// slots[row] (k null: none; -1: passed over); see pe_append.cu.  Strides in elements.
+struct AppendArgs {
+  int n_rows, n_q, n_kv;
+  const void *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  const int32_t* positions;  // [axes][n_rows]
+  const int64_t* slots;
+  void* q_out;
+  long long q_out_stride;
+  void *k_cache, *v_cache;
+  int num_pages;
+  int32_t* err;
+  RopeTable rope;
+};
+cudaError_t launch_append(const AppendArgs& a, int head_dim, pe_dtype dt, cudaStream_t s);
+// launch_pack of keys rotated first; positions [axes][n_rows].
+cudaError_t launch_pack_rope(const PackArgs& a, const int32_t* positions, const RopeTable& table, pe_dtype dt,
+                             cudaStream_t s);
+
 // The entries at slots[row], as the values they stand for (-1: the output row is left as it is).
 struct UnpackArgs {
   int n_rows;
@@ -373,5 +399,33 @@ size_t packed_attn_workspace_bytes(int head_dim, pe_dtype dt, int sms);
 // Attention launches of such a call (each with a merge): the tiles that the bounds allow, 1024 or fewer at a time.
 long long packed_attn_launches(const PackedAttnArgs& a, pe_dtype dt);
 cudaError_t launch_attend_packed(const PackedAttnArgs& a, pe_dtype dt, int sms, cudaStream_t s);
+
+// ----------------------------------------------------------------------------- microscaled (MX) 4-bit matrices
+
+// Rows and their 4-bit form (format in pe_mx.cuh), one of which a call reads and the other writes.
+struct MxRowsArgs {
+  int n_rows, width;
+  const void* x;       // quantise: rows
+  void* out;           // read back: rows
+  long long stride;    // of the rows, in elements
+  int vec;             // rows start at 16-byte boundaries
+  uint8_t* mx;
+  int32_t* err;
+};
+cudaError_t launch_mx_quantize(const MxRowsArgs& a, pe_dtype dt, cudaStream_t s);
+cudaError_t launch_mx_dequantize(const MxRowsArgs& a, pe_dtype dt, cudaStream_t s);
+
+// y[r][f] = add[r][f] + sum_k x[r][k] w[f][k] of two such matrices.
+struct MxMatmulArgs {
+  int n_rows, n_out, width;
+  const uint8_t *x, *w;
+  const void* add;     // nullable; may be y
+  long long add_stride;
+  void* y;
+  long long y_stride;
+  uint64_t wait_ns;    // limit of every pipeline wait (wait_limit_ns())
+  int32_t* err;
+};
+cudaError_t launch_mx_matmul(const MxMatmulArgs& a, pe_dtype dt, cudaStream_t s);
 
 }  // namespace pe

@@ -2,6 +2,7 @@
 // The format is in pe_packed.cuh.
 #include <algorithm>
 
+#include "pe_append.cuh"
 #include "pe_internal.h"
 #include "pe_packed.cuh"
 
@@ -10,6 +11,15 @@ namespace pe {
 namespace {
 
 constexpr int kPackThreads = 128;  // (256: 0 to 2 us more for both kernels)
+
+// What rotating keys takes besides.
+template <bool ROPE>
+struct PackRope {};
+template <>
+struct PackRope<true> {
+  const int32_t* positions;  // [axes][n_rows]
+  RopeTable table;
+};
 
 // Eight entries at a 16-byte boundary: their values, and the bits of the largest magnitude as fp32 (at least
 // kInfBits: one is infinite or NaN).  Magnitudes compare as whole numbers, bf16 two at a time.
@@ -183,9 +193,28 @@ PE_DEV bool quantise(Eight& h, int by, uint32_t& nibbles, uint32_t& code) {
 // 27 %).  Loading one step ahead of its use did not change the times (21.6 and 17.7 us against 21 and 18 then), nor did
 // longer rows per lane.
 
-// HD/8 lanes per (row, head), eight keys and eight values each.
+// Eight keys of a row, rotated and rounded to T, and their largest magnitude: x and the eight entries half a head on or
+// back.  `at`: the first one's place in its head.
 template <typename T, int HD>
-__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a, const Deal d) {
+PE_DEV void rotate_eight(const RopeTable& rope, const int32_t* positions, int n_rows, long long row, int at, Eight& x,
+                         Eight& other) {
+  const bool upper = at >= HD / 2;
+  x.top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int i = (at & (HD / 2 - 1)) + e;
+    float c, s;
+    rope_angle(rope, __ldcg(positions + (long long)rope.axis[i] * n_rows + row), i, c, s);
+    float x1 = upper ? other.x[e] : x.x[e], x2 = upper ? x.x[e] : other.x[e];
+    rope_turn(x1, x2, c, s);
+    x.x[e] = to_float<T>(from_float<T>(upper ? x2 : x1));
+    x.top = max(x.top, __float_as_uint(x.x[e]) & 0x7FFFFFFFu);
+  }
+}
+
+// HD/8 lanes per (row, head), eight keys and eight values each.  ROPE: keys are rotated first.
+template <typename T, int HD, bool ROPE>
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a, const Deal d, const PackRope<ROPE> rope) {
   using L = PackedLayout<HD>;
   const Lane<HD> ln(threadIdx.x);
   const int group = threadIdx.x / Lane<HD>::N, r = (int)((uint32_t)group / d.by_heads);
@@ -209,6 +238,11 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a, co
         slot = __ldcg(reinterpret_cast<const long long*>(slots));
         k.load(k_row);
         v.load(v_row);
+        if constexpr (ROPE) {
+          Eight other;
+          other.load(k_row + (ln.key < HD / 2 ? HD / 2 : -(HD / 2)));
+          rotate_eight<T, HD>(rope.table, rope.positions, a.n_rows, row0 + (long long)i * d.rows, ln.key, k, other);
+        }
       }
       slots += d.rows;
       k_row += d.rows * a.k_stride;
@@ -284,11 +318,11 @@ __global__ void __launch_bounds__(kPackThreads) unpack_kernel(const UnpackArgs a
   }
 }
 
-template <typename T, int HD>
-cudaError_t pack_typed(const PackArgs& a, cudaStream_t s) {
+template <typename T, int HD, bool ROPE = false>
+cudaError_t pack_typed(const PackArgs& a, cudaStream_t s, const PackRope<ROPE>& rope = PackRope<ROPE>()) {
   unsigned grid, threads;
   const Deal d = deal<HD>(a.n_rows, a.n_kv, &grid, &threads);
-  return launch_pdl(pack_kernel<T, HD>, dim3(grid), dim3(threads), 0, s, a, d);
+  return launch_pdl(pack_kernel<T, HD, ROPE>, dim3(grid), dim3(threads), 0, s, a, d, rope);
 }
 template <typename T, int HD>
 cudaError_t unpack_typed(const UnpackArgs& a, cudaStream_t s) {
@@ -304,6 +338,15 @@ cudaError_t launch_pack(const PackArgs& a, pe_dtype dt, cudaStream_t s) {
   if (a.head_dim == 64)
     return dt == PE_BF16 ? pack_typed<__nv_bfloat16, 64>(a, s) : pack_typed<float, 64>(a, s);
   return dt == PE_BF16 ? pack_typed<__nv_bfloat16, 128>(a, s) : pack_typed<float, 128>(a, s);
+}
+
+cudaError_t launch_pack_rope(const PackArgs& a, const int32_t* positions, const RopeTable& table, pe_dtype dt,
+                             cudaStream_t s) {
+  if (a.n_rows == 0) return cudaSuccess;
+  const PackRope<true> r{positions, table};
+  if (a.head_dim == 64)
+    return dt == PE_BF16 ? pack_typed<__nv_bfloat16, 64, true>(a, s, r) : pack_typed<float, 64, true>(a, s, r);
+  return dt == PE_BF16 ? pack_typed<__nv_bfloat16, 128, true>(a, s, r) : pack_typed<float, 128, true>(a, s, r);
 }
 
 cudaError_t launch_unpack(const UnpackArgs& a, pe_dtype dt, cudaStream_t s) {
