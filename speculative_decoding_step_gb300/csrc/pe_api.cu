@@ -607,6 +607,17 @@ pe_status check_product(const void* w, int32_t n_rows, int32_t n_out, int32_t wi
   return PE_OK;
 }
 
+pe_status run_mx_matmul(const void* x, int32_t n_rows, const void* w, int32_t n_out, int32_t width, const void* add,
+                        int64_t add_stride, pe_dtype dt, void* y, int64_t y_stride, bool w_ready, int32_t* err,
+                        cudaStream_t s) {
+  MxMatmulArgs a{};
+  a.n_rows = n_rows; a.n_out = n_out; a.width = width; a.x = static_cast<const uint8_t*>(x);
+  a.w = static_cast<const uint8_t*>(w); a.add = add; a.add_stride = add_stride; a.y = y; a.y_stride = y_stride;
+  a.w_ready = w_ready; a.wait_ns = wait_limit_ns(); a.drop_stage = take_drop_stage(); a.err = err;
+  if (launch_mx_matmul(a, dt, num_sms(), s) != cudaSuccess) return PE_ERR_CUDA;
+  return PE_OK;
+}
+
 // ----------------------------------------------------------------------------- appending rotated rows
 
 // Turns per position of each pair, mod 1, in units of 2^-64.
@@ -1417,12 +1428,8 @@ pe_status pe_matmul_mx(const void* x, int32_t n_rows, const void* w, int32_t n_o
   if (n_rows == 0) return PE_OK;
   if (overlaps(byte_rows(dtype, y, y_stride, n_out, n_rows).span(), span_of(x, mx_bytes(n_rows, width))))
     return PE_ERR_INVALID_ARG;
-  MxMatmulArgs a{};
-  a.n_rows = n_rows; a.n_out = n_out; a.width = width; a.x = static_cast<const uint8_t*>(x);
-  a.w = static_cast<const uint8_t*>(w); a.add = add; a.add_stride = add_stride; a.y = y; a.y_stride = y_stride;
-  a.wait_ns = wait_limit_ns(); a.err = err_word;
-  PE_TRY_CUDA(launch_mx_matmul(a, dtype, (cudaStream_t)stream));
-  return PE_OK;
+  return run_mx_matmul(x, n_rows, w, n_out, width, add, add_stride, dtype, y, y_stride, false, err_word,
+                       (cudaStream_t)stream);
 }
 
 size_t pe_linear_mx_workspace_bytes(int32_t n_rows, int32_t width) { return pe_mx_bytes(n_rows, width); }
@@ -1444,7 +1451,9 @@ pe_status pe_linear_mx(pe_dtype x_dtype, const void* x, int64_t x_stride, int32_
       (add != nullptr && overlaps(ws, byte_rows(y_dtype, add, add_stride, n_out, n_rows).span())))
     return PE_ERR_INVALID_ARG;
   if ((st = pe_quantize_mx(x_dtype, x, x_stride, n_rows, width, workspace, err_word, stream)) != PE_OK) return st;
-  return pe_matmul_mx(workspace, n_rows, w, n_out, width, add, add_stride, y_dtype, y, y_stride, err_word, stream);
+  // the product starts when every CTA of the quantising kernel is past its own wait: what came before, w too, is done
+  return run_mx_matmul(workspace, n_rows, w, n_out, width, add, add_stride, y_dtype, y, y_stride, true, err_word,
+                       (cudaStream_t)stream);
 }
 
 size_t pe_packed_page_bytes(const pe_config* cfg) {

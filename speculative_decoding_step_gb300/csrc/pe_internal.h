@@ -423,9 +423,11 @@ struct MxMatmulArgs {
   long long add_stride;
   void* y;
   long long y_stride;
+  int w_ready;         // w was written by a kernel that has completed when this one starts
   uint64_t wait_ns;    // limit of every pipeline wait (wait_limit_ns())
+  int drop_stage;      // test of the wait-expiry path: CTA 0 leaves this pipeline stage unarmed (-1: none)
   int32_t* err;
 };
-cudaError_t launch_mx_matmul(const MxMatmulArgs& a, pe_dtype dt, cudaStream_t s);
+cudaError_t launch_mx_matmul(const MxMatmulArgs& a, pe_dtype dt, int sms, cudaStream_t s);
 
 }  // namespace pe

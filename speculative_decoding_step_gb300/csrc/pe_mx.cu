@@ -1,5 +1,4 @@
-// Microscaled (MX) 4-bit matrices: rounding rows, reading them back, and their product.
-// The format is in pe_mx.cuh.
+// Microscaled (MX) 4-bit matrices: rounding rows and reading them back.  The format is in pe_mx.cuh.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -151,61 +150,6 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const MxRowsA
   }
 }
 
-// y[r][f] = add[r][f] + sum_k x[r][k] w[f][k]: a warp per feature and eight rows, lanes over the blocks of 32.
-template <typename T>
-__global__ void __launch_bounds__(kMxThreads) mx_matmul_kernel(const MxMatmulArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const int pieces = (a.width + kMxPiece - 1) / kMxPiece;
-  const int groups = (a.n_rows + 7) / 8;
-  const long long unit = (long long)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5);
-  if (unit >= (long long)groups * a.n_out) return;
-  const int lane = threadIdx.x & 31;
-  const int f = (int)(unit % a.n_out), g = (int)(unit / a.n_out);
-  float acc[8] = {};
-  for (int blk = lane; blk < pieces * 4; blk += 32) {
-    const int piece = blk >> 2, b = blk & 3;
-    const uint8_t* wr = a.w + ((size_t)(f / kMxPiece) * pieces + piece) * kMxRecord;
-    const uint4 wc = __ldcg(reinterpret_cast<const uint4*>(wr + mx_code_at(f % kMxPiece, b)));
-    const float ws = mx_scale(__ldcg(wr + mx_scale_at(f % kMxPiece, b)));
-    const uint32_t ww[4] = {wc.x, wc.y, wc.z, wc.w};
-    for (int j = 0; j < 8; ++j) {
-      const int row = g * 8 + j;
-      if (row >= a.n_rows) break;
-      const uint8_t* xr = a.x + ((size_t)(row / kMxPiece) * pieces + piece) * kMxRecord;
-      const uint4 xc = __ldcg(reinterpret_cast<const uint4*>(xr + mx_code_at(row % kMxPiece, b)));
-      const float xs = mx_scale(__ldcg(xr + mx_scale_at(row % kMxPiece, b)));
-      const uint32_t xw[4] = {xc.x, xc.y, xc.z, xc.w};
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t hw[4], hx[4];
-        mx_decode8(ww[i], hw);
-        mx_decode8(xw[i], hx);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&hw[e]));
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hx[e]));
-          sum = fmaf(u.x, v.x, fmaf(u.y, v.y, sum));
-        }
-      }
-      acc[j] = fmaf(sum * xs, ws, acc[j]);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], o);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const long long row = (long long)g * 8 + j;
-    if (lane != j || row >= a.n_rows) continue;
-    float v = acc[j];
-    if (a.add != nullptr) v += to_float<T>(static_cast<const T*>(a.add)[row * a.add_stride + f]);
-    static_cast<T*>(a.y)[row * a.y_stride + f] = from_float<T>(v);
-  }
-}
-
 }  // namespace
 
 static unsigned mx_grid(long long units) { return (unsigned)((units + kMxThreads / 32 - 1) / (kMxThreads / 32)); }
@@ -222,13 +166,6 @@ cudaError_t launch_mx_dequantize(const MxRowsArgs& a, pe_dtype dt, cudaStream_t 
   const dim3 grid(mx_grid(units)), block(kMxThreads);
   return dt == PE_BF16 ? launch_pdl(mx_dequantize_kernel<__nv_bfloat16>, grid, block, 0, s, a)
                        : launch_pdl(mx_dequantize_kernel<float>, grid, block, 0, s, a);
-}
-
-cudaError_t launch_mx_matmul(const MxMatmulArgs& a, pe_dtype dt, cudaStream_t s) {
-  const long long units = (long long)((a.n_rows + 7) / 8) * a.n_out;
-  const dim3 grid(mx_grid(units)), block(kMxThreads);
-  return dt == PE_BF16 ? launch_pdl(mx_matmul_kernel<__nv_bfloat16>, grid, block, 0, s, a)
-                       : launch_pdl(mx_matmul_kernel<float>, grid, block, 0, s, a);
 }
 
 }  // namespace pe
