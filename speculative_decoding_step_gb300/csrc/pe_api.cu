@@ -607,11 +607,13 @@ pe_status check_product(const void* w, int32_t n_rows, int32_t n_out, int32_t wi
   return PE_OK;
 }
 
-pe_status run_mx_matmul(const void* x, int32_t n_rows, const void* w, int32_t n_out, int32_t width, const void* add,
-                        int64_t add_stride, pe_dtype dt, void* y, int64_t y_stride, bool w_ready, int32_t* err,
-                        cudaStream_t s) {
+// x in 4 bits, or (x null) as rows of x_dtype at 16-byte boundaries that the product quantises itself.
+pe_status run_mx_matmul(const void* x, const void* rows, int64_t rows_stride, pe_dtype rows_type, int32_t n_rows,
+                        const void* w, int32_t n_out, int32_t width, const void* add, int64_t add_stride, pe_dtype dt,
+                        void* y, int64_t y_stride, bool w_ready, int32_t* err, cudaStream_t s) {
   MxMatmulArgs a{};
   a.n_rows = n_rows; a.n_out = n_out; a.width = width; a.x = static_cast<const uint8_t*>(x);
+  a.rows = rows; a.rows_stride = rows_stride; a.rows_type = rows_type;
   a.w = static_cast<const uint8_t*>(w); a.add = add; a.add_stride = add_stride; a.y = y; a.y_stride = y_stride;
   a.w_ready = w_ready; a.wait_ns = wait_limit_ns(); a.drop_stage = take_drop_stage(); a.err = err;
   if (launch_mx_matmul(a, dt, num_sms(), s) != cudaSuccess) return PE_ERR_CUDA;
@@ -1428,8 +1430,8 @@ pe_status pe_matmul_mx(const void* x, int32_t n_rows, const void* w, int32_t n_o
   if (n_rows == 0) return PE_OK;
   if (overlaps(byte_rows(dtype, y, y_stride, n_out, n_rows).span(), span_of(x, mx_bytes(n_rows, width))))
     return PE_ERR_INVALID_ARG;
-  return run_mx_matmul(x, n_rows, w, n_out, width, add, add_stride, dtype, y, y_stride, false, err_word,
-                       (cudaStream_t)stream);
+  return run_mx_matmul(x, nullptr, 0, PE_F32, n_rows, w, n_out, width, add, add_stride, dtype, y, y_stride, false,
+                       err_word, (cudaStream_t)stream);
 }
 
 size_t pe_linear_mx_workspace_bytes(int32_t n_rows, int32_t width) { return pe_mx_bytes(n_rows, width); }
@@ -1450,10 +1452,13 @@ pe_status pe_linear_mx(pe_dtype x_dtype, const void* x, int64_t x_stride, int32_
       overlaps(ws, span_of(w, mx_bytes(n_out, width))) ||
       (add != nullptr && overlaps(ws, byte_rows(y_dtype, add, add_stride, n_out, n_rows).span())))
     return PE_ERR_INVALID_ARG;
+  if (rows_aligned16(x_dtype, x, x_stride, n_rows) && mx_matmul_quantises(n_rows, n_out, width, num_sms()))
+    return run_mx_matmul(nullptr, x, x_stride, x_dtype, n_rows, w, n_out, width, add, add_stride, y_dtype, y, y_stride,
+                         false, err_word, (cudaStream_t)stream);
   if ((st = pe_quantize_mx(x_dtype, x, x_stride, n_rows, width, workspace, err_word, stream)) != PE_OK) return st;
   // the product starts when every CTA of the quantising kernel is past its own wait: what came before, w too, is done
-  return run_mx_matmul(workspace, n_rows, w, n_out, width, add, add_stride, y_dtype, y, y_stride, true, err_word,
-                       (cudaStream_t)stream);
+  return run_mx_matmul(workspace, nullptr, 0, PE_F32, n_rows, w, n_out, width, add, add_stride, y_dtype, y, y_stride,
+                       true, err_word, (cudaStream_t)stream);
 }
 
 size_t pe_packed_page_bytes(const pe_config* cfg) {

@@ -419,6 +419,9 @@ cudaError_t launch_mx_dequantize(const MxRowsArgs& a, pe_dtype dt, cudaStream_t 
 struct MxMatmulArgs {
   int n_rows, n_out, width;
   const uint8_t *x, *w;
+  const void* rows;    // not null: x's rows before they are quantised, at 16-byte boundaries (x is not used then)
+  long long rows_stride;
+  pe_dtype rows_type;
   const void* add;     // nullable; may be y
   long long add_stride;
   void* y;
@@ -429,5 +432,7 @@ struct MxMatmulArgs {
   int32_t* err;
 };
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, pe_dtype dt, int sms, cudaStream_t s);
+// Whether the product of this many rows quantises them itself (rows at 16-byte boundaries), without a launch before it.
+bool mx_matmul_quantises(int n_rows, int n_out, int width, int sms);
 
 }  // namespace pe

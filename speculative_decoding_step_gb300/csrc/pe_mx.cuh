@@ -63,4 +63,55 @@ PE_DEV float mx_scale(uint32_t c) {
   return __uint_as_float(c == 0 ? 0x00400000u : c == 255 ? 0x7FC00000u : c << 23);
 }
 
+// Eight entries at a 16-byte boundary.
+PE_DEV void get8(const float* p, float (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float4 t = __ldcs(reinterpret_cast<const float4*>(p) + k);
+    x[4 * k] = t.x; x[4 * k + 1] = t.y; x[4 * k + 2] = t.z; x[4 * k + 3] = t.w;
+  }
+}
+PE_DEV void get8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 t = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(w[e] << 16);
+    x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  }
+}
+PE_DEV uint32_t max_over_four(uint32_t v) {
+  v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
+  return max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
+}
+
+// Rounds the eight entries that this lane has of a block (the three lanes beside it have the others): their codes, and
+// the block's scale byte.  The scale is 2^(floor(log2 amax) - 2): the exponent field of amax less two.  Returns whether
+// one of the block's entries was NaN (kept as 0) or infinite (kept as +-6 of the scale of the finite ones).
+PE_DEV bool mx_round8(float (&x)[8], uint32_t& codes, uint32_t& scale) {
+  constexpr uint32_t kInf = 0x7F800000u;
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+  top = max_over_four(top);
+  const bool bad = top >= kInf;
+  if (__any_sync(0xFFFFFFFFu, bad)) {
+    uint32_t finite = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t m = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+      if (m < kInf) finite = max(finite, m);
+      if (m > kInf) x[e] = 0.f;
+    }
+    top = max_over_four(finite);
+  }
+  // fields 0 to 2 (below 2^-124) have the smallest scale, 2^-127
+  scale = (uint32_t)max((int)(top >> 23) - 2, 0);
+  const float inv = __uint_as_float((254u - scale) << 23);  // 2^(127 - scale): 2^127 down to 2^-125, exact products
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] *= inv;
+  codes = mx_encode8(x);
+  return bad;
+}
+
 }  // namespace pe

@@ -195,6 +195,26 @@ def test_product_is_exact_where_sums_are(n, m, w):
     assert np.array_equal(mx.kept(x), x) and np.array_equal(_np(y), x @ wt.T) and int(err.item()) == 0
 
 
+# many rows, from one unit of 256 x 256 to a pair of CTAs to several each, with odd numbers of 128-row blocks on either side
+MANY = [(2000, 2000, 257), (1300, 5200, 100), (3000, 3000, 300), (4099, 6000, 200), (2900, 7900, 1000)]
+
+
+@pytest.mark.parametrize("n,m,w", MANY)
+@pytest.mark.parametrize("exact,out,add", [(True, "f32", False), (False, "bf16", False), (False, "f32", True)])
+def test_product_of_many_rows(n, m, w, exact, out, add):
+    rng = np.random.default_rng(n + m + w)
+    x, wt = _product_case(rng, n, m, w, exact)
+    y = _apart(np.full((n, m), np.nan), out, 3 if add else 0)
+    a = torch.randn((n, m), device="cuda").to(DT[out]) if add else None
+    err = _err()
+    pe.matmul_mx(_mx(x), _mx(wt), y, err, add=a)
+    assert int(err.item()) == 0
+    if exact:
+        assert np.array_equal(_np(y), x @ wt.T)
+    else:
+        _compare(_np(y), x, wt, _np(a) if add else None, out)
+
+
 @pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
 @pytest.mark.parametrize("n,m,w,pad", [(1, 129, 33, 0), (7, 768, 256, 8), (14, 640, 2880, 0), (16, 300, 257, 3),
                                        (17, 128, 96, 0), (64, 500, 1000, 24), (200, 300, 640, 0)])
