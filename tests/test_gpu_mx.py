@@ -195,7 +195,7 @@ def test_product_is_exact_where_sums_are(n, m, w):
     assert np.array_equal(mx.kept(x), x) and np.array_equal(_np(y), x @ wt.T) and int(err.item()) == 0
 
 
-# many rows, from one unit of 256 x 256 to a pair of CTAs to several each, with odd numbers of 128-row blocks on either side
+# many rows, from one unit of 128 x 256 a CTA to several each, with odd numbers of 128-row blocks on either side
 MANY = [(2000, 2000, 257), (1300, 5200, 100), (3000, 3000, 300), (4099, 6000, 200), (2900, 7900, 1000)]
 
 
@@ -314,6 +314,32 @@ def test_products_on_another_stream_and_captured():
         torch.cuda.synchronize()
         assert torch.equal(y, want)
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("n, m, w, stage", [(8, 768, 256, 0), (100, 256, 1024, 0), (100, 20000, 2560, 1),
+                                            (1000, 12288, 2048, 0), (1000, 12288, 2048, 3), (1000, 12288, 2048, 6)])
+def test_a_wait_that_runs_out_ends_the_call_and_the_next_one_passes(n, m, w, stage):
+    err = _err()
+    g = torch.Generator(device="cuda").manual_seed(n + m)
+    x = torch.randn(n, w, device="cuda", generator=g)
+    wm = pe.MxMatrix(m, w)
+    pe.quantize_mx(torch.randn(m, w, device="cuda", generator=g), wm, err)
+    ws = pe.alloc_linear_mx_workspace(n, w)
+    want, y = torch.empty((n, m), device="cuda"), torch.empty((n, m), device="cuda")
+    pe.linear_mx(x, wm, want, ws, err)
+    assert int(err.item()) == 0
+    pe.set_wait_limit_ns(1_000_000)
+    try:
+        pe.skip_pipeline_stage_for_test(stage)
+        pe.linear_mx(x, wm, y, ws, err)
+        torch.cuda.synchronize()
+    finally:
+        pe.skip_pipeline_stage_for_test(-1)
+        pe.set_wait_limit_ns(0)
+    assert int(err.item()) == pe.PE_DEV_TIMEOUT
+    err.zero_()
+    pe.linear_mx(x, wm, y, ws, err)
+    assert int(err.item()) == 0 and torch.equal(y, want)
 
 
 def test_python_refusals():
