@@ -388,8 +388,11 @@ def _rows(t, what: str, dev: int, dtype, width: int, n: int):
                          f"{t.device}")
     if t.is_contiguous() and t.numel() == n * width and n > 0:
         return t.data_ptr(), width
+    stride = t.stride()
+    if len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2] and shape[1] * shape[2] == width and n > 1:
+        return t.data_ptr(), stride[0]
     inner = 1
-    for size, stride in zip(shape[:0:-1], t.stride()[:0:-1]):
+    for size, stride in zip(shape[:0:-1], stride[:0:-1]):
         if size != 1 and stride != inner:
             raise ValueError(f"{what}: the elements of a row have to be contiguous")
         inner *= size

@@ -622,17 +622,25 @@ pe_status run_mx_matmul(const void* x, const void* rows, int64_t rows_stride, pe
 
 // ----------------------------------------------------------------------------- appending rotated rows
 
-// Turns per position of each pair, mod 1, in units of 2^-64.
+// Turns per position of each pair, mod 1, in units of 2^-64.  A thread keeps those of the last base and head size that it
+// asked for (64 powers take the host longer than the launch).
 void set_rope_turns(RopeTable& t, float theta, int hd, const uint8_t* axis_of_pair) {
-  for (int i = 0; i < 64; ++i) {
-    t.turns[i] = 0;
-    t.axis[i] = 0;
-    if (i >= hd / 2) continue;
-    double f = std::pow((double)theta, -2.0 * i / hd) / (2.0 * 3.14159265358979323846);
-    f -= std::floor(f);
-    t.turns[i] = (uint64_t)std::ldexp(f, 64);
-    t.axis[i] = axis_of_pair != nullptr ? axis_of_pair[i] : 0;
+  static thread_local struct {
+    float theta;
+    int hd;
+    uint64_t turns[64];
+  } last = {0.f, 0, {}};
+  if (last.theta != theta || last.hd != hd) {
+    for (int i = 0; i < 64; ++i) {
+      double f = i < hd / 2 ? std::pow((double)theta, -2.0 * i / hd) / (2.0 * 3.14159265358979323846) : 0.0;
+      f -= std::floor(f);
+      last.turns[i] = (uint64_t)std::ldexp(f, 64);
+    }
+    last.theta = theta;
+    last.hd = hd;
   }
+  std::copy(last.turns, last.turns + 64, t.turns);
+  for (int i = 0; i < 64; ++i) t.axis[i] = axis_of_pair != nullptr && i < hd / 2 ? axis_of_pair[i] : 0;
 }
 
 // The rows and positions of an append call; q may be null (with q_out).

@@ -14,82 +14,127 @@ namespace pe {
 namespace {
 
 constexpr int kAppendThreads = 128;
+constexpr int kAppendDepth = 3;
 
+// Sixteen entries on their way, as they were read: eight of a head's first half and the eight they are paired with.
 template <typename T>
-PE_DEV void load8(const T* p, float (&x)[8]);
+struct Pairs;
 template <>
-PE_DEV void load8<float>(const float* p, float (&x)[8]) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float4 t = __ldcg(reinterpret_cast<const float4*>(p) + k);
-    x[4 * k] = t.x; x[4 * k + 1] = t.y; x[4 * k + 2] = t.z; x[4 * k + 3] = t.w;
+struct Pairs<__nv_bfloat16> {
+  uint4 a, b;
+  PE_DEV void load(const __nv_bfloat16* p, int half) {
+    a = __ldcg(reinterpret_cast<const uint4*>(p));
+    b = __ldcg(reinterpret_cast<const uint4*>(p + half));
   }
-}
+  PE_DEV void store(__nv_bfloat16* p, int half) const {
+    *reinterpret_cast<uint4*>(p) = a;
+    *reinterpret_cast<uint4*>(p + half) = b;
+  }
+  PE_DEV static void turn(uint32_t& x, uint32_t& y, const float2 (&t)[2]) {
+    float x0 = __uint_as_float(x << 16), x1 = __uint_as_float(x & 0xFFFF0000u);
+    float y0 = __uint_as_float(y << 16), y1 = __uint_as_float(y & 0xFFFF0000u);
+    rope_turn(x0, y0, t[0].x, t[0].y);
+    rope_turn(x1, y1, t[1].x, t[1].y);
+    const __nv_bfloat162 u = __floats2bfloat162_rn(x0, x1), v = __floats2bfloat162_rn(y0, y1);
+    x = *reinterpret_cast<const uint32_t*>(&u);
+    y = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  PE_DEV void turn(const float2 (&t)[4][2]) {
+    turn(a.x, b.x, t[0]);
+    turn(a.y, b.y, t[1]);
+    turn(a.z, b.z, t[2]);
+    turn(a.w, b.w, t[3]);
+  }
+};
 template <>
-PE_DEV void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 t = __ldcg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+struct Pairs<float> {
+  float4 a[2], b[2];
+  PE_DEV void load(const float* p, int half) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[2 * e] = __uint_as_float(w[e] << 16);
-    x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    for (int k = 0; k < 2; ++k) {
+      a[k] = __ldcg(reinterpret_cast<const float4*>(p) + k);
+      b[k] = __ldcg(reinterpret_cast<const float4*>(p + half) + k);
+    }
   }
-}
-PE_DEV void store8(float* p, const float (&x)[8]) {
+  PE_DEV void store(float* p, int half) const {
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    reinterpret_cast<float4*>(p)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-}
-PE_DEV void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-    w[e] = *reinterpret_cast<const uint32_t*>(&t);
+    for (int k = 0; k < 2; ++k) {
+      reinterpret_cast<float4*>(p)[k] = a[k];
+      reinterpret_cast<float4*>(p + half)[k] = b[k];
+    }
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
+  PE_DEV void turn(const float2 (&t)[4][2]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      rope_turn(a[k].x, b[k].x, t[2 * k][0].x, t[2 * k][0].y);
+      rope_turn(a[k].y, b[k].y, t[2 * k][1].x, t[2 * k][1].y);
+      rope_turn(a[k].z, b[k].z, t[2 * k + 1][0].x, t[2 * k + 1][0].y);
+      rope_turn(a[k].w, b[k].w, t[2 * k + 1][1].x, t[2 * k + 1][1].y);
+    }
+  }
+};
 
-// A CTA a row.  A thread has eight pairs of a head (the sines and cosines of one chunk serve every head that it takes);
-// value rows are copied as two eights the same way.
+// A CTA a row.  Its heads' loads go out first (kAppendDepth of each thread at a time); meanwhile a thread a pair finds the
+// sines and cosines, which all heads share.  Bound by memory at many rows.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
-  constexpr int C = HD / 16, HALF = HD / 2;  // chunks of eight pairs
+  constexpr int C = HD / 16, HALF = HD / 2;  // a head's chunks of eight pairs
+  __shared__ __align__(16) float2 turns[HALF];
   pdl_wait();
   pdl_trigger();
   const long long row = blockIdx.x;
-  const int c = threadIdx.x % C;
-  float cs[8], sn[8];
+  const int c = threadIdx.x % C, n_q = a.q != nullptr ? a.n_q : 0, n_kv = a.k != nullptr ? a.n_kv : 0;
+  const int heads = n_q + 2 * n_kv;
+  const T* q = static_cast<const T*>(a.q) + row * a.q_stride;
+  const T* k = static_cast<const T*>(a.k) + row * a.k_stride;
+  const T* v = static_cast<const T*>(a.v) + row * a.v_stride;
+  Pairs<T> x[kAppendDepth];
+  auto load = [&](int h0) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) rope_angle(a.rope, __ldcg(a.positions + (long long)a.rope.axis[8 * c + j] * a.n_rows + row), 8 * c + j, cs[j], sn[j]);
-  int64_t slot = -1;
-  bool put = false;
-  if (a.k != nullptr) {
-    slot = __ldcg(reinterpret_cast<const long long*>(a.slots) + row);
-    put = (uint64_t)slot < (uint64_t)a.num_pages * 16;
-    if (!put && slot != -1 && threadIdx.x == 0) set_err(a.err, PE_DEV_BAD_PAGE);
-  }
-  const int n_q = a.q != nullptr ? a.n_q : 0, n_kv = put ? a.n_kv : 0;
-  for (int h = threadIdx.x / C; h < n_q + 2 * n_kv; h += kAppendThreads / C) {
-    const T* src;
-    T* dst;
-    if (h < n_q) {
-      src = static_cast<const T*>(a.q) + row * a.q_stride + (long long)h * HD;
-      dst = static_cast<T*>(a.q_out) + row * a.q_out_stride + (long long)h * HD;
-    } else {
-      const bool key = h < n_q + n_kv;
-      const int g = h - n_q - (key ? 0 : n_kv);
-      src = static_cast<const T*>(key ? a.k : a.v) + row * (key ? a.k_stride : a.v_stride) + (long long)g * HD;
-      dst = static_cast<T*>(key ? a.k_cache : a.v_cache) + (slot * a.n_kv + g) * HD;
+    for (int j = 0; j < kAppendDepth; ++j) {
+      const int h = h0 + j * (kAppendThreads / C);
+      if (h < n_q)
+        x[j].load(q + (long long)h * HD + 8 * c, HALF);
+      else if (h < n_q + n_kv)
+        x[j].load(k + (long long)(h - n_q) * HD + 8 * c, HALF);
+      else if (h < heads)
+        x[j].load(v + (long long)(h - n_q - n_kv) * HD + 8 * c, HALF);
     }
-    float x1[8], x2[8];
-    load8<T>(src + 8 * c, x1);
-    load8<T>(src + 8 * c + HALF, x2);
-    if (h < n_q + n_kv)
+  };
+  load(threadIdx.x / C);
+  const int64_t slot = n_kv > 0 ? __ldcg(reinterpret_cast<const long long*>(a.slots) + row) : -1;
+  if (threadIdx.x < HALF) {
+    const int i = threadIdx.x;
+    rope_angle(a.rope, __ldcg(a.positions + (long long)a.rope.axis[i] * a.n_rows + row), i, turns[i].x, turns[i].y);
+  }
+  __syncthreads();
+  float2 t[4][2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) rope_turn(x1[j], x2[j], cs[j], sn[j]);
-    store8(dst + 8 * c, x1);
-    store8(dst + 8 * c + HALF, x2);
+  for (int j = 0; j < 4; ++j) {
+    const float4 w = *reinterpret_cast<const float4*>(&turns[8 * c + 2 * j]);
+    t[j][0] = make_float2(w.x, w.y);
+    t[j][1] = make_float2(w.z, w.w);
+  }
+  const bool put = (uint64_t)slot < (uint64_t)a.num_pages * 16;
+  if (!put && slot != -1 && threadIdx.x == 0) set_err(a.err, PE_DEV_BAD_PAGE);
+  T* qo = static_cast<T*>(a.q_out) + row * a.q_out_stride;
+  T* kc = static_cast<T*>(a.k_cache) + (put ? slot * a.n_kv * HD : 0);
+  T* vc = static_cast<T*>(a.v_cache) + (put ? slot * a.n_kv * HD : 0);
+  for (int h0 = threadIdx.x / C;;) {
+#pragma unroll
+    for (int j = 0; j < kAppendDepth; ++j) {
+      const int h = h0 + j * (kAppendThreads / C);
+      if (h < n_q + n_kv) x[j].turn(t);
+      if (h < n_q)
+        x[j].store(qo + (long long)h * HD + 8 * c, HALF);
+      else if (put && h < n_q + n_kv)
+        x[j].store(kc + (long long)(h - n_q) * HD + 8 * c, HALF);
+      else if (put && h < heads)
+        x[j].store(vc + (long long)(h - n_q - n_kv) * HD + 8 * c, HALF);
+    }
+    h0 += kAppendDepth * (kAppendThreads / C);
+    if (h0 >= heads) break;
+    load(h0);
   }
 }
 
