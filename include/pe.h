@@ -25,7 +25,8 @@
  * writes keys and values into the drafter's cache (pe_append_kv_packed: into a packed one).
  *
  * Matrices in microscaled 4-bit floating point: pe_quantize_mx, pe_dequantize_mx, and their
- * product, pe_matmul_mx and pe_linear_mx.
+ * product, pe_matmul_mx and pe_linear_mx; the drafter's calls with such an LM head:
+ * pe_draft_forward_mx_head and pe_step_mx_head.
  *
  * A KV cache in 4 bits: pe_pack_kv, pe_unpack_kv, pe_attend_packed, and the drafter's
  * calls over such a cache: pe_draft_forward_packed, pe_step_packed, pe_inject_kv_packed.
@@ -571,6 +572,29 @@ size_t pe_linear_mx_workspace_bytes(int32_t n_rows, int32_t width); /* 0: invali
 pe_status pe_linear_mx(pe_dtype x_dtype, const void *x, int64_t x_stride, int32_t n_rows, const void *w, int32_t n_out,
                        int32_t width, const void *add, int64_t add_stride, pe_dtype y_dtype, void *y, int64_t y_stride,
                        void *workspace, size_t workspace_bytes, int32_t *err_word, pe_stream_t stream);
+
+/*
+ * pe_draft_forward and pe_step with the LM head in 4 bits: lm_head_mx is a matrix of vocab rows x d (pe_quantize_mx), and
+ * w->lm_head is not read.  The cache is kv, or a packed one (the other of the two is null).  Arguments, results and device
+ * checks are otherwise those of pe_draft_forward and pe_step, or of their packed forms: the final norm's rows, rounded to
+ * cfg->dtype, are quantised as by pe_quantize_mx, the logits are pe_matmul_mx's fp32 sums, and a draft is the lowest index
+ * of the largest.  workspace: >= pe_mx_head_workspace_bytes(cfg) bytes (0: invalid config; it serves the calls of
+ * pe_packed_workspace_bytes as well), of which pe_step_mx_head counts all as an output.
+ */
+size_t pe_mx_head_workspace_bytes(const pe_config *cfg);
+pe_status pe_draft_forward_mx_head(const pe_config *cfg, const pe_weights *w, const void *lm_head_mx, const pe_kv *kv,
+                                   const pe_packed_kv *packed, const int32_t *block_table, const void *x0,
+                                   const int32_t *positions, const int64_t *slot_mapping, const int32_t *row_list,
+                                   const int32_t *n_valid, const int32_t *draft_rows, void *workspace,
+                                   size_t workspace_bytes, int32_t *draft_tokens, float *logits_dbg,
+                                   int32_t *err_word, pe_stream_t stream);
+pe_status pe_step_mx_head(const pe_config *cfg, const pe_weights *w, const void *lm_head_mx, const pe_kv *kv,
+                          const pe_packed_kv *packed, const int32_t *block_table, const int32_t *prev_tokens,
+                          const int32_t *prev_pos, const int32_t *num_accepted, const int32_t *bonus,
+                          const void *target_hidden, const int32_t *target_tokens, void *workspace,
+                          size_t workspace_bytes, int32_t *draft_tokens, int32_t *num_accepted_out,
+                          int32_t *bonus_out, int32_t *next_prev_tokens, int32_t *next_prev_pos, float *logits_dbg,
+                          int32_t *err_word, pe_stream_t stream);
 
 /*
  * Tracing (optional).  pe_draft_forward and pe_step can record caller-created

@@ -22,6 +22,7 @@ __all__ = [
     "pack_kv", "unpack_kv", "attend_packed", "packed_page_bytes", "attend_workspace_bytes", "alloc_packed_pool",
     "alloc_attend_workspace", "alloc_packed_workspace", "packed_workspace_bytes", "append_kv", "MxMatrix", "quantize_mx",
     "dequantize_mx", "matmul_mx", "linear_mx", "mx_bytes", "alloc_linear_mx_workspace",
+    "alloc_mx_head_workspace",
     "PE_OK", "PE_DEV_BAD_TOKEN", "PE_DEV_BAD_ACCEPTED", "PE_DEV_BAD_PAGE", "PE_DEV_BAD_POSITION",
     "PE_DEV_NONFINITE", "PE_DEV_BAD_ROW", "PE_DEV_TIMEOUT", "EXPORTED_SYMBOLS",
 ]
@@ -44,7 +45,8 @@ EXPORTED_SYMBOLS = ["pe_prepare_batch", "pe_scatter_hidden", "pe_draft_forward",
                     "pe_packed_page_bytes", "pe_attend_workspace_bytes", "pe_packed_workspace_bytes",
                     "pe_draft_forward_packed", "pe_step_packed", "pe_inject_kv_packed", "pe_append_kv",
                     "pe_append_kv_packed", "pe_mx_bytes", "pe_quantize_mx", "pe_dequantize_mx", "pe_matmul_mx",
-                    "pe_linear_mx", "pe_linear_mx_workspace_bytes"]
+                    "pe_linear_mx", "pe_linear_mx_workspace_bytes", "pe_draft_forward_mx_head", "pe_step_mx_head",
+                    "pe_mx_head_workspace_bytes"]
 
 # Size of the library-owned scratch used by pe_draft_forward_noalloc (PE_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 48 << 20
@@ -107,16 +109,18 @@ def _arr(ts):
 
 
 class DeviceWeights:
-    """Drafter weights resident on the device (tensors in nn.Linear layout) + the pe_weights struct."""
+    """Drafter weights resident on the device (tensors in nn.Linear layout) + the pe_weights struct.  ``lm_head`` may be
+    an MxMatrix of vocab x d: draft_forward, step and Round then run with the LM head in 4 bits."""
 
     def __init__(self, emb, h_shared, fc, norm_attn, wqkv, wo, norm_mlp, w_gate_up, w_down, norm_final, lm_head):
         self.tensors = dict(emb=emb, h_shared=h_shared, fc=fc, norm_attn=list(norm_attn), wqkv=list(wqkv),
                             wo=list(wo), norm_mlp=list(norm_mlp), w_gate_up=list(w_gate_up),
                             w_down=list(w_down), norm_final=norm_final, lm_head=lm_head)
+        self.mx_head = isinstance(lm_head, MxMatrix)
         self._arrays = [_arr(list(x)) for x in (norm_attn, wqkv, wo, norm_mlp, w_gate_up, w_down)]
         a = self._arrays
         self.struct = _Weights(emb.data_ptr(), h_shared.data_ptr(), fc.data_ptr(), a[0], a[1], a[2], a[3], a[4],
-                               a[5], norm_final.data_ptr(), lm_head.data_ptr())
+                               a[5], norm_final.data_ptr(), None if self.mx_head else lm_head.data_ptr())
 
 
 class DeviceKV:
@@ -195,6 +199,11 @@ def lib():
                                      [vp, ctypes.c_size_t] + [vp] * 8)
         L.pe_inject_kv_packed.argtypes = [cp, ctypes.POINTER(_Weights), vp, ctypes.POINTER(_PackedKV), vp, vp, vp, vp,
                                           vp, ctypes.c_size_t, vp, vp]
+        L.pe_draft_forward_mx_head.argtypes = ([cp, ctypes.POINTER(_Weights), vp, ctypes.POINTER(_KV),
+                                                ctypes.POINTER(_PackedKV)] + [vp] * 7 +
+                                               [vp, ctypes.c_size_t, vp, vp, vp, vp])
+        L.pe_step_mx_head.argtypes = ([cp, ctypes.POINTER(_Weights), vp, ctypes.POINTER(_KV),
+                                       ctypes.POINTER(_PackedKV)] + [vp] * 7 + [vp, ctypes.c_size_t] + [vp] * 8)
         L.pe_append_kv.argtypes = [cp, vp, vp, vp, i64, i64, i64, vp, i32, ctypes.c_char_p, vp, i32, vp, i64, vp, vp, i32,
                                    vp, vp]
         L.pe_append_kv_packed.argtypes = [cp, vp, vp, vp, i64, i64, i64, vp, i32, ctypes.c_char_p, vp, i32, vp, i64, vp,
@@ -204,7 +213,8 @@ def lib():
         L.pe_matmul_mx.argtypes = [vp, i32, vp, i32, i32, vp, i64, i32, vp, i64, vp, vp]
         L.pe_linear_mx.argtypes = [i32, vp, i64, i32, vp, i32, i32, vp, i64, i32, vp, i64, vp, ctypes.c_size_t, vp, vp]
         mx_sizes = ("pe_mx_bytes", "pe_linear_mx_workspace_bytes")
-        sizes = ("pe_packed_page_bytes", "pe_attend_workspace_bytes", "pe_packed_workspace_bytes") + mx_sizes
+        sizes = ("pe_packed_page_bytes", "pe_attend_workspace_bytes", "pe_packed_workspace_bytes",
+                 "pe_mx_head_workspace_bytes") + mx_sizes
         for name in sizes:
             getattr(L, name).restype = ctypes.c_size_t
             getattr(L, name).argtypes = [i32, i32] if name in mx_sizes else [cp]
@@ -298,12 +308,26 @@ def _cache_call(name: str, cfg, kv):
     return getattr(lib(), name), name
 
 
+def _drafter_call(name: str, cfg, weights: DeviceWeights, kv):
+    """The library's call of this name for these weights and this cache, its name, and its arguments for both."""
+    call, cached = _cache_call(name, cfg, kv)
+    w, cache = ctypes.byref(weights.struct), ctypes.byref(kv.struct)
+    if not weights.mx_head:
+        return call, cached, (w, cache)
+    head, name = weights.tensors["lm_head"], name + "_mx_head"
+    if (head.n_rows, head.width) != (cfg.vocab, cfg.d):
+        raise ValueError(f"lm_head: expected a matrix of {cfg.vocab} x {cfg.d}, got {head.n_rows} x {head.width}")
+    packed = isinstance(kv, DevicePackedKV)
+    return getattr(lib(), name), name, (w, _ptr(head.data), None if packed else cache, cache if packed else None)
+
+
 def draft_forward(cfg, weights: DeviceWeights, kv, block_table, x0, meta: dict, workspace, draft_tokens, err,
                   logits_dbg=None, stream=None):
     """Stages (c)+(d): drafter pass over the valid rows, LM head + argmax -> draft_tokens [B][K].  ``kv``: a DeviceKV,
-    or a DevicePackedKV with the workspace of alloc_packed_workspace."""
-    call, name = _cache_call("pe_draft_forward", cfg, kv)
-    st = call(ctypes.byref(cfg), ctypes.byref(weights.struct), ctypes.byref(kv.struct), _ptr(block_table), _ptr(x0),
+    or a DevicePackedKV with the workspace of alloc_packed_workspace; with the LM head in 4 bits, the workspace of
+    alloc_mx_head_workspace."""
+    call, name, args = _drafter_call("pe_draft_forward", cfg, weights, kv)
+    st = call(ctypes.byref(cfg), *args, _ptr(block_table), _ptr(x0),
               _ptr(meta["positions"]), _ptr(meta["slot_mapping"]), _ptr(meta["row_list"]), _ptr(meta["n_valid"]),
               _ptr(meta["draft_rows"]), _ptr(workspace), workspace.numel() * workspace.element_size(),
               _ptr(draft_tokens), _ptr(logits_dbg), _ptr(err), _stream(stream))
@@ -628,9 +652,10 @@ def linear_mx(x, w: MxMatrix, y, workspace, err, add=None, stream=None):
 def step(cfg, weights: DeviceWeights, kv, block_table, prev_tokens, prev_pos, num_accepted, bonus,
          target_hidden, target_tokens, workspace, out: dict, err, logits_dbg=None, stream=None):
     """One whole round.  ``out`` holds draft_tokens, num_accepted, bonus, next_prev_tokens, next_prev_pos.  ``kv``: a
-    DeviceKV, or a DevicePackedKV with the workspace of alloc_packed_workspace."""
-    call, name = _cache_call("pe_step", cfg, kv)
-    st = call(ctypes.byref(cfg), ctypes.byref(weights.struct), ctypes.byref(kv.struct), _ptr(block_table),
+    DeviceKV, or a DevicePackedKV with the workspace of alloc_packed_workspace; with the LM head in 4 bits, the workspace
+    of alloc_mx_head_workspace."""
+    call, name, args = _drafter_call("pe_step", cfg, weights, kv)
+    st = call(ctypes.byref(cfg), *args, _ptr(block_table),
               _ptr(prev_tokens), _ptr(prev_pos), _ptr(num_accepted), _ptr(bonus), _ptr(target_hidden),
               _ptr(target_tokens), _ptr(workspace), workspace.numel() * workspace.element_size(),
               _ptr(out["draft_tokens"]), _ptr(out["num_accepted"]), _ptr(out["bonus"]), _ptr(out["next_prev_tokens"]),
@@ -679,6 +704,14 @@ def alloc_packed_workspace(cfg: Config, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def alloc_mx_head_workspace(cfg: Config, device="cuda") -> torch.Tensor:
+    """Workspace of draft_forward and step with the LM head in 4 bits (serves the other calls as well)."""
+    n = int(lib().pe_mx_head_workspace_bytes(ctypes.byref(cfg)))
+    if n == 0:
+        raise PeError(check_config(cfg), "pe_mx_head_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def alloc_linear_mx_workspace(n_rows: int, width: int, device="cuda") -> torch.Tensor:
     """Workspace of linear_mx for up to n_rows rows of this width."""
     n = int(lib().pe_linear_mx_workspace_bytes(n_rows, width))
@@ -699,8 +732,9 @@ class Round:
         R, T = cfg.B * 2 * cfg.K, cfg.B * cfg.K
         self.meta = alloc_batch(cfg, device)
         self.x0 = torch.empty((R, 2 * cfg.d), dtype=cfg.torch_dtype, device=device)
-        packed = isinstance(kv, DevicePackedKV)
-        self.workspace = alloc_packed_workspace(cfg, device) if packed else alloc_workspace(cfg, device)
+        alloc = (alloc_mx_head_workspace if weights.mx_head else
+                 alloc_packed_workspace if isinstance(kv, DevicePackedKV) else alloc_workspace)
+        self.workspace = alloc(cfg, device)
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
         i32 = dict(dtype=torch.int32, device=device)
         self.draft_tokens = torch.empty((cfg.B, cfg.K), **i32)

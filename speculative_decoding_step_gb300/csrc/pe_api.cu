@@ -181,7 +181,10 @@ struct Plan {
   // own numbers), attention scratch
   size_t pk_k = 0, pk_v = 0, pk_row = 0, pk_attn = 0;
   size_t packed_total = 0;
+  size_t mx_rows = 0, mx_total = 0;  // a 4-bit LM head: the draft rows in 4 bits
 };
+
+size_t mx_bytes(int32_t n_rows, int32_t width);
 
 Plan make_plan(const pe_config& c) {
   Plan p;
@@ -274,6 +277,8 @@ Plan make_plan(const pe_config& c) {
   p.pk_row = take(8 * (size_t)p.R);
   p.pk_attn = take(packed_attn_workspace_bytes(c.head_dim, c.dtype, p.sms));
   p.packed_total = off;
+  p.mx_rows = take(mx_bytes(p.T, c.d));
+  p.mx_total = off;
   return p;
 }
 
@@ -285,7 +290,8 @@ struct Cache {
   explicit Cache(const pe_kv* k) : kv(k) {}
   explicit Cache(const pe_packed_kv* k) : packed(k), is_packed(true) {}
   int num_pages() const { return is_packed ? packed->num_pages : kv->num_pages; }
-  size_t workspace(const Plan& p) const { return is_packed ? p.packed_total : p.total; }
+  // of a call with a 4-bit LM head (mx), or one in the storage type
+  size_t workspace(const Plan& p, bool mx) const { return mx ? p.mx_total : is_packed ? p.packed_total : p.total; }
 };
 
 // ----------------------------------------------------------------------------- TMA descriptors
@@ -484,12 +490,13 @@ pe_status run_gemm(const pe_config& c, const Plan& p, void* ws, const GemmCall& 
   return PE_OK;
 }
 
-pe_status check_weights(const pe_config& c, const pe_weights* w) {
+// head_mx: the LM head in 4 bits, in the place of w->lm_head.
+pe_status check_weights(const pe_config& c, const pe_weights* w, const void* head_mx) {
   if (w == nullptr || w->emb == nullptr || w->h_shared == nullptr || w->fc == nullptr || w->norm_final == nullptr ||
-      w->lm_head == nullptr || w->norm_attn == nullptr || w->wqkv == nullptr || w->wo == nullptr ||
+      (head_mx == nullptr && w->lm_head == nullptr) || w->norm_attn == nullptr || w->wqkv == nullptr || w->wo == nullptr ||
       w->norm_mlp == nullptr || w->w_gate_up == nullptr || w->w_down == nullptr)
     return PE_ERR_INVALID_ARG;
-  const void* ptrs[5] = {w->emb, w->h_shared, w->fc, w->norm_final, w->lm_head};
+  const void* ptrs[5] = {w->emb, w->h_shared, w->fc, w->norm_final, head_mx != nullptr ? head_mx : w->lm_head};
   for (const void* q : ptrs)
     if (!aligned16(q)) return PE_ERR_INVALID_ARG;
   for (int l = 0; l < c.n_layers; ++l) {
@@ -814,7 +821,33 @@ void set_kv_target(GemmArgs& a, const Cache& cache, const Plan& p, void* ws, int
   }
 }
 
-pe_status forward_impl(const pe_config& c, const pe_weights* w, const Cache& cache, const int32_t* block_table,
+// The LM head in 4 bits over the draft rows yl, which are quantised on the way (in the product itself where it has few).
+pe_status run_mx_head(const pe_config& c, const Plan& p, void* ws, const void* head_mx, const void* yl,
+                      unsigned long long* keys, int32_t* draft_tokens, float* logits_dbg, const VerifyArgs* verify,
+                      int32_t* err, cudaStream_t s) {
+  MxMatmulArgs a{};
+  a.n_rows = p.T; a.n_out = c.vocab; a.width = c.d; a.w = static_cast<const uint8_t*>(head_mx);
+  if (mx_matmul_quantises(p.T, c.vocab, c.d, true, p.sms)) {
+    a.rows = yl; a.rows_stride = c.d; a.rows_type = c.dtype;
+  } else {
+    MxRowsArgs q{};
+    q.n_rows = p.T; q.width = c.d; q.x = yl; q.stride = c.d; q.vec = 1; q.mx = at<uint8_t>(ws, p.mx_rows); q.err = err;
+    PE_TRY_CUDA(launch_mx_quantize(q, c.dtype, s));
+    a.x = q.mx;
+  }
+  // what came before the pass has completed (forward_impl), the weights too
+  a.w_ready = 1; a.wait_ns = wait_limit_ns(); a.drop_stage = take_drop_stage(); a.err = err;
+  a.head.keys = keys; a.head.done = at<int32_t>(ws, p.done); a.head.drafts = draft_tokens; a.head.logits = logits_dbg;
+  if (verify != nullptr) {
+    a.head.verify = *verify;
+    a.head.has_verify = 1;
+  }
+  PE_TRY_CUDA(launch_mx_matmul(a, PE_F32, p.sms, s));
+  return PE_OK;
+}
+
+pe_status forward_impl(const pe_config& c, const pe_weights* w, const void* head_mx, const Cache& cache,
+                       const int32_t* block_table,
                        const void* x0, const int32_t* positions, const int64_t* slot_mapping,
                        const int32_t* row_list, const int32_t* n_valid, const int32_t* draft_rows, void* ws,
                        const Plan& p, int32_t* draft_tokens, float* logits_dbg, int32_t* err, cudaStream_t s,
@@ -969,7 +1002,10 @@ pe_status forward_impl(const pe_config& c, const pe_weights* w, const Cache& cac
   norm_after(nf, p.down, true, false);  // the residual after the last layer is needed only here
   PE_TRY_CUDA(launch_rmsnorm(nf, c.dtype, s));
   trace(tf, s);
-  {
+  if (head_mx != nullptr) {
+    const pe_status st = run_mx_head(c, p, ws, head_mx, yl, ia.keys, draft_tokens, logits_dbg, verify, err, s);
+    if (st != PE_OK) return st;
+  } else {
     GemmArgs a = base;
     a.keys = ia.keys; a.logits_dbg = logits_dbg; a.done_counter = at<int32_t>(ws, p.done);
     a.draft_out = draft_tokens;
@@ -985,35 +1021,35 @@ pe_status forward_impl(const pe_config& c, const pe_weights* w, const Cache& cac
   return PE_OK;
 }
 
-pe_status draft_forward_impl(const pe_config* cfg, const pe_weights* w, const Cache& cache,
+pe_status draft_forward_impl(const pe_config* cfg, const pe_weights* w, const void* head_mx, const Cache& cache,
                              const int32_t* block_table, const void* x0, const int32_t* positions,
                              const int64_t* slot_mapping, const int32_t* row_list, const int32_t* n_valid,
                              const int32_t* draft_rows, void* workspace, size_t workspace_bytes,
                              int32_t* draft_tokens, float* logits_dbg, int32_t* err_word, cudaStream_t s) {
   pe_status st = check_cfg(cfg);
   if (st != PE_OK) return st;
-  if ((st = check_weights(*cfg, w)) != PE_OK) return st;
+  if ((st = check_weights(*cfg, w, head_mx)) != PE_OK) return st;
   if ((st = check_cache(*cfg, cache)) != PE_OK) return st;
   if (!block_table || !x0 || !positions || !slot_mapping || !row_list || !n_valid || !draft_rows || !workspace ||
       !draft_tokens || !err_word)
     return PE_ERR_INVALID_ARG;
   if (!aligned16(x0) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PE_ERR_INVALID_ARG;
   const Plan p = make_plan(*cfg);
-  if (workspace_bytes < cache.workspace(p)) return PE_ERR_SHAPE;
+  if (workspace_bytes < cache.workspace(p, head_mx != nullptr)) return PE_ERR_SHAPE;
   for (int i = 0; i < 3; ++i) trace(i, s);
-  return forward_impl(*cfg, w, cache, block_table, x0, positions, slot_mapping, row_list, n_valid, draft_rows,
+  return forward_impl(*cfg, w, head_mx, cache, block_table, x0, positions, slot_mapping, row_list, n_valid, draft_rows,
                       workspace, p, draft_tokens, logits_dbg, err_word, s);
 }
 
-pe_status step_impl(const pe_config* cfg, const pe_weights* w, const Cache& cache, const int32_t* block_table,
-                    const int32_t* prev_tokens, const int32_t* prev_pos, const int32_t* num_accepted,
+pe_status step_impl(const pe_config* cfg, const pe_weights* w, const void* head_mx, const Cache& cache,
+                    const int32_t* block_table, const int32_t* prev_tokens, const int32_t* prev_pos, const int32_t* num_accepted,
                     const int32_t* bonus, const void* target_hidden, const int32_t* target_tokens, void* workspace,
                     size_t workspace_bytes, int32_t* draft_tokens, int32_t* num_accepted_out, int32_t* bonus_out,
                     int32_t* next_prev_tokens, int32_t* next_prev_pos, float* logits_dbg, int32_t* err_word,
                     cudaStream_t s) {
   pe_status st = check_cfg(cfg);
   if (st != PE_OK) return st;
-  if ((st = check_weights(*cfg, w)) != PE_OK) return st;
+  if ((st = check_weights(*cfg, w, head_mx)) != PE_OK) return st;
   if ((st = check_cache(*cfg, cache)) != PE_OK) return st;
   if (!block_table || !prev_tokens || !prev_pos || !num_accepted || !bonus || !target_hidden || !target_tokens ||
       !workspace || !draft_tokens || !num_accepted_out || !bonus_out || !next_prev_tokens || !next_prev_pos ||
@@ -1022,11 +1058,12 @@ pe_status step_impl(const pe_config* cfg, const pe_weights* w, const Cache& cach
   if (!aligned16(target_hidden) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PE_ERR_INVALID_ARG;
   const Plan p = make_plan(*cfg);
   // the workspace bytes this round would use (a workspace that is too short fails below)
+  const size_t need = cache.workspace(p, head_mx != nullptr);
   if (!step_aliasing_ok(*cfg, block_table, prev_tokens, prev_pos, num_accepted, bonus, target_hidden, target_tokens,
                         draft_tokens, num_accepted_out, bonus_out, next_prev_tokens, next_prev_pos, logits_dbg,
-                        err_word, workspace, std::min(workspace_bytes, cache.workspace(p))))
+                        err_word, workspace, std::min(workspace_bytes, need)))
     return PE_ERR_INVALID_ARG;
-  if (workspace_bytes < cache.workspace(p)) return PE_ERR_SHAPE;
+  if (workspace_bytes < need) return PE_ERR_SHAPE;
   void* ws = workspace;
   int32_t* ids = at<int32_t>(ws, p.st_ids);
   int32_t* pos = at<int32_t>(ws, p.st_pos);
@@ -1054,11 +1091,12 @@ pe_status step_impl(const pe_config* cfg, const pe_weights* w, const Cache& cach
   va.B = cfg->B; va.K = cfg->K; va.draft = draft_tokens; va.target = target_tokens; va.acc_out = num_accepted_out;
   va.bonus_out = bonus_out; va.row_list = rows; va.draft_rows = drows; va.positions = pos; va.input_ids = ids;
   va.next_tokens = next_prev_tokens; va.next_pos = next_prev_pos;
-  const bool bf16 = cfg->dtype == PE_BF16;  // the tensor-core LM head verifies in its finishing CTA
-  st = forward_impl(*cfg, w, cache, block_table, x0, pos, slot, rows, nval, drows, ws, p, draft_tokens, logits_dbg,
-                    err_word, s, true, bf16 ? &va : nullptr);
+  // the tensor-core LM heads verify in their finishing CTA
+  const bool fused = cfg->dtype == PE_BF16 || head_mx != nullptr;
+  st = forward_impl(*cfg, w, head_mx, cache, block_table, x0, pos, slot, rows, nval, drows, ws, p, draft_tokens, logits_dbg,
+                    err_word, s, true, fused ? &va : nullptr);
   if (st != PE_OK) return st;
-  if (!bf16 && launch_verify(va, s) != cudaSuccess) return PE_ERR_CUDA;
+  if (!fused && launch_verify(va, s) != cudaSuccess) return PE_ERR_CUDA;
   trace(7 + 7 * cfg->n_layers, s);
   return PE_OK;
 }
@@ -1080,7 +1118,7 @@ pe_status inject_kv_impl(const pe_config* cfg, const pe_weights* w, const void* 
   if (!aligned16(w_inj) || !aligned16(target_hidden) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PE_ERR_INVALID_ARG;
   const Plan p = make_plan(c);
-  if (workspace_bytes < cache.workspace(p)) return PE_ERR_SHAPE;
+  if (workspace_bytes < cache.workspace(p, false)) return PE_ERR_SHAPE;
   void* ws = workspace;
   const bool bf16 = c.dtype == PE_BF16;
   const int NI = c.B * (c.K + 1);
@@ -1200,7 +1238,7 @@ pe_status pe_draft_forward(const pe_config* cfg, const pe_weights* w, const pe_k
                            const int32_t* row_list, const int32_t* n_valid, const int32_t* draft_rows,
                            void* workspace, size_t workspace_bytes, int32_t* draft_tokens, float* logits_dbg,
                            int32_t* err_word, pe_stream_t stream) {
-  return draft_forward_impl(cfg, w, Cache(kv), block_table, x0, positions, slot_mapping, row_list, n_valid,
+  return draft_forward_impl(cfg, w, nullptr, Cache(kv), block_table, x0, positions, slot_mapping, row_list, n_valid,
                             draft_rows, workspace, workspace_bytes, draft_tokens, logits_dbg, err_word,
                             (cudaStream_t)stream);
 }
@@ -1210,7 +1248,7 @@ pe_status pe_draft_forward_packed(const pe_config* cfg, const pe_weights* w, con
                                   const int64_t* slot_mapping, const int32_t* row_list, const int32_t* n_valid,
                                   const int32_t* draft_rows, void* workspace, size_t workspace_bytes,
                                   int32_t* draft_tokens, float* logits_dbg, int32_t* err_word, pe_stream_t stream) {
-  return draft_forward_impl(cfg, w, Cache(kv), block_table, x0, positions, slot_mapping, row_list, n_valid,
+  return draft_forward_impl(cfg, w, nullptr, Cache(kv), block_table, x0, positions, slot_mapping, row_list, n_valid,
                             draft_rows, workspace, workspace_bytes, draft_tokens, logits_dbg, err_word,
                             (cudaStream_t)stream);
 }
@@ -1233,7 +1271,7 @@ pe_status pe_step(const pe_config* cfg, const pe_weights* w, const pe_kv* kv, co
                   size_t workspace_bytes, int32_t* draft_tokens, int32_t* num_accepted_out, int32_t* bonus_out,
                   int32_t* next_prev_tokens, int32_t* next_prev_pos, float* logits_dbg, int32_t* err_word,
                   pe_stream_t stream) {
-  return step_impl(cfg, w, Cache(kv), block_table, prev_tokens, prev_pos, num_accepted, bonus, target_hidden,
+  return step_impl(cfg, w, nullptr, Cache(kv), block_table, prev_tokens, prev_pos, num_accepted, bonus, target_hidden,
                    target_tokens, workspace, workspace_bytes, draft_tokens, num_accepted_out, bonus_out,
                    next_prev_tokens, next_prev_pos, logits_dbg, err_word, (cudaStream_t)stream);
 }
@@ -1244,9 +1282,39 @@ pe_status pe_step_packed(const pe_config* cfg, const pe_weights* w, const pe_pac
                          const int32_t* target_tokens, void* workspace, size_t workspace_bytes, int32_t* draft_tokens,
                          int32_t* num_accepted_out, int32_t* bonus_out, int32_t* next_prev_tokens,
                          int32_t* next_prev_pos, float* logits_dbg, int32_t* err_word, pe_stream_t stream) {
-  return step_impl(cfg, w, Cache(kv), block_table, prev_tokens, prev_pos, num_accepted, bonus, target_hidden,
+  return step_impl(cfg, w, nullptr, Cache(kv), block_table, prev_tokens, prev_pos, num_accepted, bonus, target_hidden,
                    target_tokens, workspace, workspace_bytes, draft_tokens, num_accepted_out, bonus_out,
                    next_prev_tokens, next_prev_pos, logits_dbg, err_word, (cudaStream_t)stream);
+}
+
+size_t pe_mx_head_workspace_bytes(const pe_config* cfg) {
+  return check_cfg(cfg) == PE_OK ? make_plan(*cfg).mx_total : 0;
+}
+
+pe_status pe_draft_forward_mx_head(const pe_config* cfg, const pe_weights* w, const void* lm_head_mx, const pe_kv* kv,
+                                   const pe_packed_kv* packed, const int32_t* block_table, const void* x0,
+                                   const int32_t* positions, const int64_t* slot_mapping, const int32_t* row_list,
+                                   const int32_t* n_valid, const int32_t* draft_rows, void* workspace,
+                                   size_t workspace_bytes, int32_t* draft_tokens, float* logits_dbg, int32_t* err_word,
+                                   pe_stream_t stream) {
+  if (lm_head_mx == nullptr || (kv == nullptr) == (packed == nullptr)) return PE_ERR_INVALID_ARG;
+  return draft_forward_impl(cfg, w, lm_head_mx, kv != nullptr ? Cache(kv) : Cache(packed), block_table, x0, positions,
+                            slot_mapping, row_list, n_valid, draft_rows, workspace, workspace_bytes, draft_tokens,
+                            logits_dbg, err_word, (cudaStream_t)stream);
+}
+
+pe_status pe_step_mx_head(const pe_config* cfg, const pe_weights* w, const void* lm_head_mx, const pe_kv* kv,
+                          const pe_packed_kv* packed, const int32_t* block_table, const int32_t* prev_tokens,
+                          const int32_t* prev_pos, const int32_t* num_accepted, const int32_t* bonus,
+                          const void* target_hidden, const int32_t* target_tokens, void* workspace,
+                          size_t workspace_bytes, int32_t* draft_tokens, int32_t* num_accepted_out, int32_t* bonus_out,
+                          int32_t* next_prev_tokens, int32_t* next_prev_pos, float* logits_dbg, int32_t* err_word,
+                          pe_stream_t stream) {
+  if (lm_head_mx == nullptr || (kv == nullptr) == (packed == nullptr)) return PE_ERR_INVALID_ARG;
+  return step_impl(cfg, w, lm_head_mx, kv != nullptr ? Cache(kv) : Cache(packed), block_table, prev_tokens, prev_pos,
+                   num_accepted, bonus, target_hidden, target_tokens, workspace, workspace_bytes, draft_tokens,
+                   num_accepted_out, bonus_out, next_prev_tokens, next_prev_pos, logits_dbg, err_word,
+                   (cudaStream_t)stream);
 }
 
 pe_status pe_sample_drafts(const pe_config* cfg, const float* logits, const float* u_draft, float temperature,
@@ -1460,7 +1528,7 @@ pe_status pe_linear_mx(pe_dtype x_dtype, const void* x, int64_t x_stride, int32_
       overlaps(ws, span_of(w, mx_bytes(n_out, width))) ||
       (add != nullptr && overlaps(ws, byte_rows(y_dtype, add, add_stride, n_out, n_rows).span())))
     return PE_ERR_INVALID_ARG;
-  if (rows_aligned16(x_dtype, x, x_stride, n_rows) && mx_matmul_quantises(n_rows, n_out, width, num_sms()))
+  if (rows_aligned16(x_dtype, x, x_stride, n_rows) && mx_matmul_quantises(n_rows, n_out, width, false, num_sms()))
     return run_mx_matmul(nullptr, x, x_stride, x_dtype, n_rows, w, n_out, width, add, add_stride, y_dtype, y, y_stride,
                          false, err_word, (cudaStream_t)stream);
   if ((st = pe_quantize_mx(x_dtype, x, x_stride, n_rows, width, workspace, err_word, stream)) != PE_OK) return st;

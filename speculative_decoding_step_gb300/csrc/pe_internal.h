@@ -415,6 +415,16 @@ struct MxRowsArgs {
 cudaError_t launch_mx_quantize(const MxRowsArgs& a, pe_dtype dt, cudaStream_t s);
 cudaError_t launch_mx_dequantize(const MxRowsArgs& a, pe_dtype dt, cudaStream_t s);
 
+// Instead of y: the feature of each row's largest sum (the lowest of equal ones), as the drafter's LM head.
+struct MxHeadArgs {
+  unsigned long long* keys;  // [n_rows], zero before the launch; null: y is written
+  int* done;                 // counter, zero before the launch and after it
+  int32_t* drafts;           // [n_rows]
+  float* logits;             // nullable, [n_rows][n_out]
+  VerifyArgs verify;         // by the CTA that finishes last, if has_verify
+  int has_verify;
+};
+
 // y[r][f] = add[r][f] + sum_k x[r][k] w[f][k] of two such matrices.
 struct MxMatmulArgs {
   int n_rows, n_out, width;
@@ -430,9 +440,10 @@ struct MxMatmulArgs {
   uint64_t wait_ns;    // limit of every pipeline wait (wait_limit_ns())
   int drop_stage;      // test of the wait-expiry path: CTA 0 leaves this pipeline stage unarmed (-1: none)
   int32_t* err;
+  MxHeadArgs head;
 };
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, pe_dtype dt, int sms, cudaStream_t s);
 // Whether the product of this many rows quantises them itself (rows at 16-byte boundaries), without a launch before it.
-bool mx_matmul_quantises(int n_rows, int n_out, int width, int sms);
+bool mx_matmul_quantises(int n_rows, int n_out, int width, bool head, int sms);
 
 }  // namespace pe

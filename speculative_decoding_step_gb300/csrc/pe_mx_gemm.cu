@@ -15,6 +15,7 @@
 // partial sums meet in shared memory over the cluster, each CTA summing its share of the columns in rank order, so the
 // result does not depend on scheduling, and the call needs no workspace and no second kernel.
 #include <algorithm>
+#include <type_traits>
 
 #include "pe_internal.h"
 #include "pe_mx.cuh"
@@ -176,11 +177,38 @@ PE_DEV void mx_store(const MxMatmulArgs& a, int f, int t0, const float (&v)[16])
   }
 }
 
+// Type of the output where the rows' largest sums are looked for instead (MxHeadArgs).
+struct MxArgmax {};
+
+// 16 rows of x (from t0 on) of feature f: the warp's largest keys join the rows' own.
+PE_DEV void mx_argmax(const MxMatmulArgs& a, int f, int t0, const float (&v)[16], int lane) {
+  const int t = t0 + (lane >> 1);
+  const bool mine = (lane & 1) == 0 && t < a.n_rows;
+  // an older key at worst: few of a row's tiles raise its maximum, and the rest need no atomic
+  const unsigned long long seen = mine ? __ldcg(a.head.keys + t) : 0ull;
+  unsigned long long k[16];
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const bool live = f < a.n_out && t0 + j < a.n_rows;
+    bad |= live && !isfinite(v[j]);
+    k[j] = live ? argmax_key(v[j], (uint32_t)f) : 0ull;
+  }
+  if (bad) set_err(a.err, PE_DEV_NONFINITE);
+  if (a.head.logits != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (f < a.n_out && t0 + j < a.n_rows) a.head.logits[(size_t)(t0 + j) * a.n_out + f] = v[j];
+  }
+  const unsigned long long top = argmax_reduce16(k, lane);
+  if (mine && top > seen) atomicMax(a.head.keys + t, top);
+}
+
 // Roles: one thread copies weights (warp 0), one or two x (warps 2 and 3), one issues the MMAs (warp 1); the other warps
 // bring in x where it is kept and write results.
 template <typename T, int SRC>
 __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulArgs a, const MxPlan p) {
-  constexpr bool KEEP = SRC >= SRC_RECORDS, WIDE = SRC == SRC_WIDE;
+  constexpr bool KEEP = SRC >= SRC_RECORDS, WIDE = SRC == SRC_WIDE, ARGMAX = std::is_same<T, MxArgmax>::value;
   constexpr int EW = kMxgThreads / 32 - 4, KA = kMxgKa<SRC>;
   // a stage: weight records, then x: records, or (wide) the codes of both halves of each piece and their scales
   constexpr uint32_t X_OFF = KA * kMxRecord, X_PIECE = WIDE ? 2 * kMxgCodes : kMxRecord;
@@ -201,6 +229,7 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kept + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued_max = abort_flag + 1;  // [4], by warp
+  volatile int* last_flag = issued_max + 4;
   float* recv = reinterpret_cast<float*>(smem);  // clusters, after the MMAs: [rank][columns of this CTA][128]
 
   if (threadIdx.x == 0) {
@@ -412,18 +441,22 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
         constexpr int ALL = WIDE ? 16 : 8, SHARED = kWideShared / 16;
         const int turn = WIDE && !buf ? ALL - SHARED : 0;
         auto row_of = [&](int n) { return w.row0 + ((n + turn) & (ALL - 1)) * 16; };
-        if (a.add != nullptr && f - lane < a.n_out)  // while the MMAs run: what is added comes to L2
-          for (int n = h; n < ALL; n += EW / 4) {
-            const int t = row_of(n) + (lane & 15);
-            if (t < a.n_rows)
-              prefetch_l2(static_cast<const T*>(a.add) + (long long)t * a.add_stride + min(f - lane + (lane & 16), a.n_out - 1));
-          }
+        if constexpr (!ARGMAX) {
+          if (a.add != nullptr && f - lane < a.n_out)  // while the MMAs run: what is added comes to L2
+            for (int n = h; n < ALL; n += EW / 4) {
+              const int t = row_of(n) + (lane & 15);
+              if (t < a.n_rows)
+                prefetch_l2(static_cast<const T*>(a.add) + (long long)t * a.add_stride + min(f - lane + (lane & 16), a.n_out - 1));
+            }
+        }
         const bool ok =
             mbar_wait(smem_u32(tfull + buf), (uint32_t)(i >> 1) & 1u, a.err, abort_flag, a.wait_ns) && !*abort_flag;
         tc_fence_after();
         const uint32_t tl = tmem + (uint32_t)(buf * p.acc_stride) + ((uint32_t)(q * 32) << 16);
         float old[16];
-        if (a.add != nullptr && ok) mx_addend<T>(a, f, row_of(h), old);
+        if constexpr (!ARGMAX) {
+          if (a.add != nullptr && ok) mx_addend<T>(a, f, row_of(h), old);
+        }
         for (int n = h; n < ALL; n += EW / 4) {
           if (WIDE && n >= SHARED && n - EW / 4 < SHARED) {  // this warp's shared chunks have left tensor memory
             tc_fence_before();
@@ -431,23 +464,47 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
             if (lane == 0) mbar_arrive(smem_u32(tempty));
           }
           const int c = (n + turn) & (ALL - 1), t0 = w.row0 + c * 16;
-          float v[16], next[16];
-          if (a.add != nullptr && ok && n + EW / 4 < ALL) mx_addend<T>(a, f, row_of(n + EW / 4), next);
-          if (ok && c < chunks) {
-            tmem_load16(tl + (uint32_t)(c * 16), v);
+          float v[16];
+          if constexpr (ARGMAX) {
+            if (ok && c < chunks) {
+              tmem_load16(tl + (uint32_t)(c * 16), v);
+              mx_argmax(a, f, t0, v, lane);
+            }
+          } else {
+            float next[16];
+            if (a.add != nullptr && ok && n + EW / 4 < ALL) mx_addend<T>(a, f, row_of(n + EW / 4), next);
+            if (ok && c < chunks) {
+              tmem_load16(tl + (uint32_t)(c * 16), v);
+              if (a.add != nullptr)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] += old[j];
+              mx_store<T>(a, f, t0, v);
+            }
             if (a.add != nullptr)
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] += old[j];
-            mx_store<T>(a, f, t0, v);
+              for (int j = 0; j < 16; ++j) old[j] = next[j];
           }
-          if (a.add != nullptr)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) old[j] = next[j];
         }
         if (!WIDE) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(tempty + buf));
+        }
+      }
+      if constexpr (ARGMAX) {
+        const int thread = threadIdx.x - 128;
+        __threadfence();
+        named_bar_sync(1, 32 * EW);
+        if (thread == 0) *last_flag = atomicAdd(a.head.done, 1) == (int)gridDim.x - 1;
+        named_bar_sync(1, 32 * EW);
+        if (*last_flag) {
+          __threadfence();
+          for (int t = thread; t < a.n_rows; t += 32 * EW) a.head.drafts[t] = argmax_key_index(__ldcg(a.head.keys + t));
+          if (thread == 0) *a.head.done = 0;
+          if (a.head.has_verify) {
+            named_bar_sync(1, 32 * EW);
+            for (int b = thread; b < a.head.verify.B; b += 32 * EW) verify_seq(a.head.verify, b);
+          }
         }
       }
     } else {
@@ -456,6 +513,7 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
     }
   }
 
+  if constexpr (!ARGMAX)
   if (p.cluster > 1) {
     // the cluster's one unit: every CTA's MMAs are done (or given up), so the stages' memory takes the partial sums
     const MxUnit w = mx_unit<SRC>(a, p, first);
@@ -543,7 +601,8 @@ MxPlan plan_mx(const MxMatmulArgs& a, int sms) {
   p.bn = std::min(kMxPiece, (a.n_rows + 15) & ~15);
   long long units = (long long)p.n_f * p.n_t;
   p.cluster = 1;
-  while (p.cluster < 8 && units * p.cluster * 2 <= sms && p.pieces >= p.cluster * 4) p.cluster *= 2;
+  // (the LM head's sums are looked at as they are: no shares)
+  while (a.head.keys == nullptr && p.cluster < 8 && units * p.cluster * 2 <= sms && p.pieces >= p.cluster * 4) p.cluster *= 2;
   const int part = (p.pieces + p.cluster - 1) / p.cluster;
   const bool keep = keeps_x(a.n_rows, part);
   // a wide tile takes in 3 records a piece for the 4 of two tiles, and reads its weights from shared memory once: about
@@ -619,14 +678,17 @@ cudaError_t launch_typed(const MxMatmulArgs& a, int sms, cudaStream_t s) {
 
 // Where a CTA has no more than 12,288 entries of x: it rounds them in less than a launch before the product takes (8 rows
 // of 256: 3.7 against 4.6 us; 14 rows of 2880: 12.5 against 9.5 us).
-bool mx_matmul_quantises(int n_rows, int n_out, int width, int sms) {
+bool mx_matmul_quantises(int n_rows, int n_out, int width, bool head, int sms) {
   MxMatmulArgs a{};
+  unsigned long long key;
+  a.head.keys = head ? &key : nullptr;
   a.n_rows = n_rows; a.n_out = n_out; a.width = width;
   const MxPlan p = plan_mx(a, sms);
   return p.src == SRC_RECORDS && (long long)p.bn * ((p.pieces + p.cluster - 1) / p.cluster) * kMxPiece <= 12288;
 }
 
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, pe_dtype dt, int sms, cudaStream_t s) {
+  if (a.head.keys != nullptr) return launch_typed<MxArgmax>(a, sms, s);
   return dt == PE_BF16 ? launch_typed<__nv_bfloat16>(a, sms, s) : launch_typed<float>(a, sms, s);
 }
 

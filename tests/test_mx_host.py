@@ -176,3 +176,30 @@ def test_append_refuses_caches_that_overlap():
     c = _cfg()
     assert _append(c, n=4, vc=1 << 56) == 1 and _append(c, n=4, vc=(1 << 56) + 16) == 1
     assert _append(c, n=4, vc=1 << 50) == 1 and _append(c, n=4, vc=1 << 52) == 1
+
+
+@pytest.mark.parametrize("name", ["pe_draft_forward_mx_head", "pe_step_mx_head"])
+def test_drafter_calls_with_a_4_bit_head_refuse_before_launch(name):
+    c = _cfg(d=128, ffn=128, vocab=300)
+    layer = (ctypes.c_void_p * 1)(1 << 49)
+    w = pe._Weights(AT, AT, AT, layer, layer, layer, layer, layer, layer, AT, None)
+    kv, packed = pe._KV(layer, layer, 40), pe._PackedKV(layer, 40)
+    need = pe.lib().pe_mx_head_workspace_bytes(ctypes.byref(c))
+    assert need >= pe.packed_workspace_bytes(c) + pe.mx_bytes(c.B * c.K, c.d)
+    assert pe.lib().pe_mx_head_workspace_bytes(ctypes.byref(_cfg(d=100))) == 0
+
+    def call(head=1 << 52, kv=ctypes.byref(kv), packed=None, ws=1 << 47, wsb=need, drop=None, weights=w):
+        ptrs = [_p((1 << 40) + i * (1 << 32)) for i in range(7)]
+        outs = [_p((1 << 40) + (20 + i) * (1 << 32)) for i in range(3 if "forward" in name else 7)]
+        if drop is not None:
+            ptrs[drop] = None
+        return getattr(pe.lib(), name)(ctypes.byref(c), ctypes.byref(weights), _p(head), kv, packed, *ptrs, _p(ws),
+                                       ctypes.c_size_t(wsb), *outs, NULL)
+
+    assert call(wsb=need - 1) == 2 and call(wsb=pe.packed_workspace_bytes(c)) == 2
+    assert call(kv=None, packed=ctypes.byref(packed), wsb=need - 1) == 2
+    assert call(head=None) == 1 and call(head=(1 << 52) + 8) == 1 and call(ws=(1 << 47) + 128) == 1
+    assert call(kv=None) == 1 and call(packed=ctypes.byref(packed)) == 1
+    for i in range(7):
+        assert call(drop=i) == 1
+    assert call(weights=pe._Weights(AT, AT, None, layer, layer, layer, layer, layer, layer, AT, None)) == 1
