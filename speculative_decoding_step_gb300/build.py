@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpe.so")
 SOURCES = ["pe_api.cu", "pe_meta.cu", "pe_gemm.cu", "pe_attn.cu", "pe_noalloc.cu", "pe_sample.cu", "pe_packed.cu",
-           "pe_packed_attn.cu", "pe_mx.cu", "pe_mx_gemm.cu", "pe_append.cu"]
+           "pe_packed_attn.cu", "pe_mx.cu", "pe_mx_gemm.cu", "pe_mx_pair.cu", "pe_append.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

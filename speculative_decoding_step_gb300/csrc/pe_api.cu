@@ -1167,6 +1167,16 @@ pe_status inject_kv_impl(const pe_config* cfg, const pe_weights* w, const void* 
 }
 
 }  // namespace
+
+bool tmap_mx(CUtensorMap* m, const uint8_t* base, uint64_t records, uint32_t rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {256, 34, records}, strides[2] = {256, 8704};
+  const cuuint32_t box[3] = {256, rows, 2}, one[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace pe
 
 using namespace pe;

@@ -466,32 +466,6 @@ PE_DEV int32_t argmax_key_index(unsigned long long key) {
   return static_cast<int32_t>(~static_cast<uint32_t>(key & 0xFFFFFFFFull));
 }
 
-// Keys of 16 columns, of a warp's 32 rows each: the largest of column lane / 2, by a transpose-reduce.  Each exchange
-// round halves the columns a lane keeps, so after 4 rounds lane l owns one column (bits 4..1 of l) and a final round
-// joins the lane pair holding it -- 16 exchanges instead of 5 per column.
-PE_DEV unsigned long long umax64(unsigned long long x, unsigned long long y) { return x > y ? x : y; }
-PE_DEV unsigned long long argmax_reduce16(const unsigned long long (&k)[16], int lane) {
-  const bool h1 = (lane >> 4) & 1, h2 = (lane >> 3) & 1, h3 = (lane >> 2) & 1, h4 = (lane >> 1) & 1;
-  unsigned long long k8[8], k4[4], k2[2];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const unsigned long long mine = h1 ? k[8 + i] : k[i], other = h1 ? k[i] : k[8 + i];
-    k8[i] = umax64(mine, __shfl_xor_sync(0xFFFFFFFFu, other, 16));
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned long long mine = h2 ? k8[4 + i] : k8[i], other = h2 ? k8[i] : k8[4 + i];
-    k4[i] = umax64(mine, __shfl_xor_sync(0xFFFFFFFFu, other, 8));
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const unsigned long long mine = h3 ? k4[2 + i] : k4[i], other = h3 ? k4[i] : k4[2 + i];
-    k2[i] = umax64(mine, __shfl_xor_sync(0xFFFFFFFFu, other, 4));
-  }
-  const unsigned long long k1 = umax64(h4 ? k2[1] : k2[0], __shfl_xor_sync(0xFFFFFFFFu, h4 ? k2[0] : k2[1], 2));
-  return umax64(k1, __shfl_xor_sync(0xFFFFFFFFu, k1, 1));
-}
-
 PE_DEV float bf16_bits_to_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 
 template <typename T>

@@ -316,8 +316,13 @@ PE_DEV void apply16(const GemmArgs& a, int unit, int t0, int n_tok, const float 
   epi_chunk<EPI, __nv_bfloat16>(a, unit, t0, max(0, min(16, n_tok - t0)), v, v2, tf, pos_s, slot_s);
 }
 
-// (max, argmax) keys of 16 token columns over the warp's 32 rows.
-// The even lane of the pair that holds a column folds its column into this warp's running keys (no atomics:
+PE_DEV unsigned long long umax64(unsigned long long x, unsigned long long y) { return x > y ? x : y; }
+
+// (max, argmax) keys of 16 token columns over the warp's 32 rows by a
+// transpose-reduce: each exchange round halves the columns a lane keeps, so
+// after 4 rounds lane l owns one column (bits 4..1 of l) and a final round
+// joins the lane pair holding it -- 16 exchanges instead of 5 per column.
+// The even lane folds its column into this warp's running keys (no atomics:
 // every address has one writer).
 PE_DEV void argmax16(const GemmArgs& a, int unit, int t0, int n_tok, const float (&v)[16],
                      unsigned long long* red_w, int lane) {
@@ -338,8 +343,26 @@ PE_DEV void argmax16(const GemmArgs& a, int unit, int t0, int n_tok, const float
     for (int j = 0; j < 16; ++j)
       if (unit < a.n_out && t0 + j < n_tok) a.logits_dbg[(size_t)(t0 + j) * a.n_out + unit] = v[j];
   }
-  const unsigned long long k1 = argmax_reduce16(k, lane);
-  const int col = lane >> 1;
+  const bool h1 = (lane >> 4) & 1, h2 = (lane >> 3) & 1, h3 = (lane >> 2) & 1, h4 = (lane >> 1) & 1;
+  unsigned long long k8[8], k4[4], k2[2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const unsigned long long mine = h1 ? k[8 + i] : k[i], other = h1 ? k[i] : k[8 + i];
+    k8[i] = umax64(mine, __shfl_xor_sync(0xFFFFFFFFu, other, 16));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned long long mine = h2 ? k8[4 + i] : k8[i], other = h2 ? k8[i] : k8[4 + i];
+    k4[i] = umax64(mine, __shfl_xor_sync(0xFFFFFFFFu, other, 8));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const unsigned long long mine = h3 ? k4[2 + i] : k4[i], other = h3 ? k4[i] : k4[2 + i];
+    k2[i] = umax64(mine, __shfl_xor_sync(0xFFFFFFFFu, other, 4));
+  }
+  unsigned long long k1 = umax64(h4 ? k2[1] : k2[0], __shfl_xor_sync(0xFFFFFFFFu, h4 ? k2[0] : k2[1], 2));
+  k1 = umax64(k1, __shfl_xor_sync(0xFFFFFFFFu, k1, 1));
+  const int col = (h1 ? 8 : 0) + (h2 ? 4 : 0) + (h3 ? 2 : 0) + (h4 ? 1 : 0);
   if ((lane & 1) == 0 && k1 > red_w[col]) red_w[col] = k1;
 }
 

@@ -443,6 +443,11 @@ struct MxMatmulArgs {
   MxHeadArgs head;
 };
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, pe_dtype dt, int sms, cudaStream_t s);
+// Its kernel for many rows, on pairs of CTAs, of which mx_pair_clusters() fit on the GPU at once.
+cudaError_t launch_mx_pairs(const MxMatmulArgs& a, pe_dtype dt, int pairs, cudaStream_t s);
+int mx_pair_clusters(int sms);
+// A tensor map of 4-bit records as [records][34][256 bytes]: boxes of `rows` x 256 bytes of two records each.
+bool tmap_mx(CUtensorMap* m, const uint8_t* base, uint64_t records, uint32_t rows);
 // Whether the product of this many rows quantises them itself (rows at 16-byte boundaries), without a launch before it.
 bool mx_matmul_quantises(int n_rows, int n_out, int width, bool head, int sms);
 

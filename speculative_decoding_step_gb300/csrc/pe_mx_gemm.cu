@@ -8,37 +8,31 @@
 // column of eight rows to the next, 512 to the next eight rows) and scales in the order in which tcgen05.cp spreads them
 // over tensor memory (32 lanes x 4 columns for the 128 rows' four blocks each, repeated in every lane quarter).
 //
-// Many rows: tiles of 128 x 256, whose MMAs read a stage's weights from shared memory once for both halves (4099 x 2048 to
-// 12288 features 76.8 -> 52.9 us; pairs of CTAs on 256 x 256 took 66, a stage's hand-over between them half a microsecond).
+// Many rows go to the kernel of pe_mx_pair.cu.
 //
 // With fewer tiles than SMs a cluster of CTAs shares a tile: each takes an equal part of its pieces along k, and the
 // partial sums meet in shared memory over the cluster, each CTA summing its share of the columns in rank order, so the
 // result does not depend on scheduling, and the call needs no workspace and no second kernel.
 #include <algorithm>
-#include <type_traits>
 
 #include "pe_internal.h"
-#include "pe_mx.cuh"
+#include "pe_mx_gemm.cuh"
 
 namespace pe {
 
 namespace {
 
-constexpr uint32_t kMxgCtrl = 1024;  // barriers, tensor-memory slot, flags
 constexpr int kMxgThreads = 32 * 12;
 
-// Where a tile's rows of x come from: with each stage, as records beside the weights' (128 rows or, wide, 256); or once,
-// into shared memory for all of a CTA's tiles, as they are in 4 bits or quantised there from rows of bf16 or fp32.
-enum MxSrc : int { SRC_STAGES = 0, SRC_WIDE = 1, SRC_RECORDS = 2, SRC_BF16 = 3, SRC_F32 = 4 };
+// Where a tile's rows of x come from: with each stage, as records beside the weights' (128 rows); or once, into shared
+// memory for all of a CTA's tiles, as they are in 4 bits or quantised there from rows of bf16 or fp32.
+enum MxSrc : int { SRC_STAGES = 0, SRC_RECORDS = 1, SRC_BF16 = 2, SRC_F32 = 3 };
 
 // Pieces of a stage.  A copy takes the thread that issues it 40 ns and a stage's round trip through the ring about a
-// microsecond, so stages are large and weights, x, and either half of a wide x have a thread each.
-template <int SRC>
-constexpr int kMxgKa = SRC == SRC_WIDE ? 2 : 4;
+// microsecond, so stages are large and weights and x have a thread each.
+constexpr int kMxgKa = 4;
 
 // Tensor memory: two accumulators, the stages' scales, and the scales of x where it is kept (four columns a piece).
-// Wide: two accumulators of 256 columns that share 96, and four stages' scales (12 columns a piece) at the end; the
-// epilogue empties the shared columns first, after which the next unit's MMAs may start.
 struct MxPlan {
   int pieces, n_f, n_t, bn, cluster, stages, grid, src;
   int acc_stride, scale_col, x_col;
@@ -48,39 +42,7 @@ struct MxPlan {
 constexpr int kMxgKeepRows = 64;             // rows of x that are kept at most (accumulators of 64 columns)
 constexpr int kMxgKeepPieces = 64;           // pieces of x that are kept at most (256 columns of scales)
 constexpr uint32_t kMxgKeepBytes = 96 * 1024;
-constexpr uint32_t kMxgCodes = 16 * kMxGroup;  // a record's codes
-constexpr int kWideStages = 4;
-constexpr int kWideShared = kWideStages * 2 * 12;  // columns that wide accumulators share
-constexpr int kWideOdd = 512 - kWideShared - 256;  // first column of odd units' accumulator
-static_assert(kWideOdd + kWideShared == 256 && kWideShared % 16 == 0, "whole chunks are shared");
 
-// Shared-memory descriptor of a K-major operand in core matrices: lbo bytes to the next 16-byte column, sbo to the next
-// eight rows.
-PE_DEV uint64_t sdesc_core(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(sbo >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
-}
-// Instruction descriptor of kind::mxf4: both operands e2m1, K-major, scales ue8m0, fp32 accumulators.  The scales' place in
-// their 32-bit columns (0: the first two blocks, 2: the other two) goes into bits 4 and 29.
-PE_DEV uint32_t idesc_mxf4(int M, int N) {
-  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
-         (static_cast<uint32_t>(M >> 4) << 24);
-}
-constexpr uint32_t kScaleUpper = (2u << 4) | (2u << 29);
-
-PE_DEV void tc_mma_mxf4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t a_scale, uint32_t b_scale,
-                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
-      : "memory");
-}
-// 512 bytes of scales into four columns of all 128 lanes (in order before MMAs issued later by this thread).
-PE_DEV void tc_copy_scales(uint32_t dst, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(dst), "l"(sdesc) : "memory");
-}
 PE_DEV void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -88,12 +50,11 @@ PE_DEV void st_cluster_f32(uint32_t addr, float v) {
 struct MxUnit {
   int tile_f, tile_t, row0, cols;
 };
-template <int SRC>
 PE_DEV MxUnit mx_unit(const MxMatmulArgs& a, const MxPlan& p, int u) {
   MxUnit w;
   w.tile_t = u % p.n_t;  // a weight tile's row tiles run side by side (its records come from L2)
   w.tile_f = u / p.n_t;
-  w.row0 = w.tile_t * (SRC == SRC_WIDE ? 2 : 1) * kMxPiece;
+  w.row0 = w.tile_t * kMxPiece;
   w.cols = min(p.bn, (a.n_rows - w.row0 + 15) & ~15);
   return w;
 }
@@ -154,67 +115,14 @@ PE_DEV void keep_rows(const MxMatmulArgs& a, const MxPlan& p, uint8_t* xs, int p
   if (bad) set_err(a.err, PE_DEV_NONFINITE);
 }
 
-// What is added to 16 columns (rows t0.. of y) of feature f.
-template <typename T>
-PE_DEV void mx_addend(const MxMatmulArgs& a, int f, int t0, float (&old)[16]) {
-  const T* add = static_cast<const T*>(a.add) + (long long)t0 * a.add_stride + f;
-  const int n = f < a.n_out ? a.n_rows - t0 : 0;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) old[j] = j < n ? to_float<T>(add[(long long)j * a.add_stride]) : 0.f;
-}
-template <typename T>
-PE_DEV void mx_store(const MxMatmulArgs& a, int f, int t0, const float (&v)[16]) {
-  if (f >= a.n_out) return;
-  T* y = static_cast<T*>(a.y) + (long long)t0 * a.y_stride + f;
-  const int n = a.n_rows - t0;
-  if (n >= 16) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) y[(long long)j * a.y_stride] = from_float<T>(v[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (j < n) y[(long long)j * a.y_stride] = from_float<T>(v[j]);
-  }
-}
-
-// Type of the output where the rows' largest sums are looked for instead (MxHeadArgs).
-struct MxArgmax {};
-
-// 16 rows of x (from t0 on) of feature f: the warp's largest keys join the rows' own.
-PE_DEV void mx_argmax(const MxMatmulArgs& a, int f, int t0, const float (&v)[16], int lane) {
-  const int t = t0 + (lane >> 1);
-  const bool mine = (lane & 1) == 0 && t < a.n_rows;
-  // an older key at worst: few of a row's tiles raise its maximum, and the rest need no atomic
-  const unsigned long long seen = mine ? __ldcg(a.head.keys + t) : 0ull;
-  unsigned long long k[16];
-  bool bad = false;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const bool live = f < a.n_out && t0 + j < a.n_rows;
-    bad |= live && !isfinite(v[j]);
-    k[j] = live ? argmax_key(v[j], (uint32_t)f) : 0ull;
-  }
-  if (bad) set_err(a.err, PE_DEV_NONFINITE);
-  if (a.head.logits != nullptr) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (f < a.n_out && t0 + j < a.n_rows) a.head.logits[(size_t)(t0 + j) * a.n_out + f] = v[j];
-  }
-  const unsigned long long top = argmax_reduce16(k, lane);
-  if (mine && top > seen) atomicMax(a.head.keys + t, top);
-}
-
-// Roles: one thread copies weights (warp 0), one or two x (warps 2 and 3), one issues the MMAs (warp 1); the other warps
+// Roles: one thread copies weights (warp 0), one x (warp 2), one issues the MMAs (warp 1); the other warps
 // bring in x where it is kept and write results.
 template <typename T, int SRC>
 __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulArgs a, const MxPlan p) {
-  constexpr bool KEEP = SRC >= SRC_RECORDS, WIDE = SRC == SRC_WIDE, ARGMAX = std::is_same<T, MxArgmax>::value;
-  constexpr int EW = kMxgThreads / 32 - 4, KA = kMxgKa<SRC>;
-  // a stage: weight records, then x: records, or (wide) the codes of both halves of each piece and their scales
-  constexpr uint32_t X_OFF = KA * kMxRecord, X_PIECE = WIDE ? 2 * kMxgCodes : kMxRecord;
-  constexpr uint32_t X_SCALES = WIDE ? X_OFF + KA * X_PIECE : X_OFF, X_SCALE_PIECE = WIDE ? 2 * kMxScales : kMxRecord;
-  // columns of a piece's scales, and of a stage's
-  constexpr int PIECE_COLS = KEEP ? 4 : WIDE ? 12 : 8, STAGE_COLS = KA * PIECE_COLS;
+  constexpr bool KEEP = SRC >= SRC_RECORDS, ARGMAX = std::is_same<T, MxArgmax>::value;
+  constexpr int EW = kMxgThreads / 32 - 4, KA = kMxgKa;
+  constexpr uint32_t X_OFF = KA * kMxRecord;  // a stage: weight records, then those of x
+  constexpr int PIECE_COLS = KEEP ? 4 : 8, STAGE_COLS = KA * PIECE_COLS;  // columns of a piece's scales, and of a stage's
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -234,7 +142,7 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(full + s), KEEP ? 1 : WIDE ? 3 : 2);
+      mbar_init(smem_u32(full + s), KEEP ? 1 : 2);
       mbar_init(smem_u32(empty + s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -298,41 +206,25 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
       issued = it;
     }
   } else if (warp == 2 || warp == 3) {
-    if (!KEEP && (warp == 2 || WIDE) && lane == 0) {
+    if (!KEEP && warp == 2 && lane == 0) {
       const uint64_t pol = l2_policy_evict_last();
-      const int half = warp - 2;
       pdl_wait();
       fence_proxy_async_global();
       int s = 0, it = 0;
       uint32_t ph = 0;
       bool stop = false;
       for (int u = first; u < units && !stop; u += step) {
-        const int row0 = mx_unit<SRC>(a, p, u).row0 + half * kMxPiece;
-        const uint8_t* src = a.x + ((size_t)(row0 / kMxPiece) * p.pieces + p0) * kMxRecord;
+        const uint8_t* src = a.x + ((size_t)mx_unit(a, p, u).tile_t * p.pieces + p0) * kMxRecord;
         for (int k = p0; k < p1; k += KA, ++it) {
           if (it >= S && !mbar_wait(smem_u32(empty + s), ph ^ 1u, a.err, abort_flag, a.wait_ns)) {
             stop = true;
             break;
           }
-          const int n = min(KA, p1 - k);
-          const uint32_t fb = smem_u32(full + s), dst = smem_u32(smem + (size_t)s * p.stage_bytes);
-          const uint8_t* rec = src + (size_t)(k - p0) * kMxRecord;
-          if (!WIDE) {
-            // whole records: rows beyond the tile's columns come along unused
-            mbar_expect_tx(fb, (uint32_t)n * kMxRecord);
-            bulk_g2s_hint(dst + X_OFF, rec, (uint32_t)n * kMxRecord, fb, pol);
-          } else if (row0 < a.n_rows) {
-            mbar_expect_tx(fb, (uint32_t)n * kMxRecord);
-#pragma unroll
-            for (int j = 0; j < KA; ++j)
-              if (j < n) {
-                bulk_g2s_hint(dst + X_OFF + (uint32_t)(2 * j + half) * kMxgCodes, rec + j * kMxRecord + kMxScales, kMxgCodes,
-                              fb, pol);
-                bulk_g2s_hint(dst + X_SCALES + (uint32_t)(2 * j + half) * kMxScales, rec + j * kMxRecord, kMxScales, fb, pol);
-              }
-          } else {
-            mbar_arrive(fb);  // no second half: the unit has 128 columns at most
-          }
+          // whole records: rows beyond the tile's columns come along unused
+          const uint32_t bytes = (uint32_t)min(KA, p1 - k) * kMxRecord;
+          mbar_expect_tx(smem_u32(full + s), bytes);
+          bulk_g2s_hint(smem_u32(smem + (size_t)s * p.stage_bytes) + X_OFF, src + (size_t)(k - p0) * kMxRecord, bytes,
+                        smem_u32(full + s), pol);
           if (++s == S) {
             s = 0;
             ph ^= 1u;
@@ -347,15 +239,14 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
     pdl_wait();
     const uint32_t s0 = smem_u32(smem);
     const uint64_t w_codes = sdesc_core(s0 + kMxScales, 128, kMxGroup), w_scales = sdesc_core(s0, 16, 128);
-    const uint64_t x_codes = sdesc_core(KEEP ? smem_u32(xs) + kMxScales : s0 + X_OFF + (WIDE ? 0 : kMxScales), 128, kMxGroup);
-    const uint64_t x_scales = sdesc_core(KEEP ? smem_u32(xs) : s0 + X_SCALES, 16, 128);
-    const uint32_t stage16 = p.stage_bytes >> 4, piece16 = KEEP ? p.x_piece >> 4 : X_PIECE / 16;
+    const uint64_t x_codes = sdesc_core((KEEP ? smem_u32(xs) : s0 + X_OFF) + kMxScales, 128, kMxGroup);
+    const uint64_t x_scales = sdesc_core(KEEP ? smem_u32(xs) : s0 + X_OFF, 16, 128);
+    const uint32_t stage16 = p.stage_bytes >> 4, piece16 = p.x_piece >> 4;
     int s = 0, i = 0;
     uint32_t ph = 0;
     bool stop = false;
     if (KEEP) {
-      const bool ok = mbar_wait(smem_u32(kept), 0, a.err, abort_flag, a.wait_ns);
-      stop = !__shfl_sync(0xFFFFFFFFu, ok, 0);
+      stop = !mbar_wait_warp(smem_u32(kept), 0, a, abort_flag);
       tc_fence_after();
       if (!stop && elect_one())
         for (int k = 0; k < p1 - p0; ++k)
@@ -363,13 +254,11 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
       __syncwarp();
     }
     for (int u = first; u < units && !stop; u += step, ++i) {
-      const int cols = mx_unit<SRC>(a, p, u).cols;
+      const int cols = mx_unit(a, p, u).cols;
       const uint32_t idesc = idesc_mxf4(kMxPiece, cols);
       const int buf = i & 1;
-      if (WIDE ? i >= 1 : i >= 2) {
-        const bool ok = WIDE ? mbar_wait(smem_u32(tempty), (uint32_t)(i - 1) & 1u, a.err, abort_flag, a.wait_ns)
-                             : mbar_wait(smem_u32(tempty + buf), (uint32_t)((i >> 1) - 1) & 1u, a.err, abort_flag, a.wait_ns);
-        if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
+      if (i >= 2) {
+        if (!mbar_wait_warp(smem_u32(tempty + buf), (uint32_t)((i >> 1) - 1) & 1u, a, abort_flag)) {
           stop = true;
           break;
         }
@@ -377,8 +266,7 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
       tc_fence_after();
       const uint32_t d = tmem + (uint32_t)(buf * p.acc_stride);
       for (int k = p0; k < p1; k += KA) {
-        const bool ok = mbar_wait(smem_u32(full + s), ph, a.err, abort_flag, a.wait_ns);
-        if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
+        if (!mbar_wait_warp(smem_u32(full + s), ph, a, abort_flag)) {
           stop = true;
           break;
         }
@@ -395,8 +283,7 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
           for (int j = 0; j < KA; ++j)
             if (j < n) {
               tc_copy_scales(sa + j * PIECE_COLS, ws + j * (kMxRecord / 16));
-              if (!KEEP) tc_copy_scales(sb + j * SB_PIECE, xsc + j * (X_SCALE_PIECE / 16));
-              if (WIDE && cols > kMxPiece) tc_copy_scales(sb + j * SB_PIECE + 4, xsc + (j * X_SCALE_PIECE + kMxScales) / 16);
+              if (!KEEP) tc_copy_scales(sb + j * SB_PIECE, xsc + j * (kMxRecord / 16));
             }
 #pragma unroll
           for (int j = 0; j < KA; ++j)
@@ -435,80 +322,29 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
     if (p.cluster == 1) {
       int i = 0;
       for (int u = first; u < units; u += step, ++i) {
-        const MxUnit w = mx_unit<SRC>(a, p, u);
+        const MxUnit w = mx_unit(a, p, u);
         const int buf = i & 1, f = w.tile_f * kMxPiece + r, chunks = w.cols / 16;
-        // wide: the shared columns first, the last chunks of an even unit, the first of an odd one
-        constexpr int ALL = WIDE ? 16 : 8, SHARED = kWideShared / 16;
-        const int turn = WIDE && !buf ? ALL - SHARED : 0;
-        auto row_of = [&](int n) { return w.row0 + ((n + turn) & (ALL - 1)) * 16; };
-        if constexpr (!ARGMAX) {
-          if (a.add != nullptr && f - lane < a.n_out)  // while the MMAs run: what is added comes to L2
-            for (int n = h; n < ALL; n += EW / 4) {
-              const int t = row_of(n) + (lane & 15);
-              if (t < a.n_rows)
-                prefetch_l2(static_cast<const T*>(a.add) + (long long)t * a.add_stride + min(f - lane + (lane & 16), a.n_out - 1));
-            }
-        }
-        const bool ok =
-            mbar_wait(smem_u32(tfull + buf), (uint32_t)(i >> 1) & 1u, a.err, abort_flag, a.wait_ns) && !*abort_flag;
+        auto row_of = [&](int n) { return w.row0 + n * 16; };
+        if constexpr (!ARGMAX)
+          if (a.add != nullptr) mx_prefetch_addend<T>(a, f - lane, lane, h, 8, EW / 4, row_of);
+        float* seen = reinterpret_cast<float*>(ctrl + kMxgSeen) + buf * 32 * EW;
+        if constexpr (ARGMAX) mx_seen(a, w.row0, seen, threadIdx.x - 128, 32 * EW);
+        MxOut<T> out(a, f, ARGMAX ? w.row0 : row_of(h), seen);
+        const bool ok = mbar_wait_warp(smem_u32(tfull + buf), (uint32_t)(i >> 1) & 1u, a, abort_flag);
         tc_fence_after();
         const uint32_t tl = tmem + (uint32_t)(buf * p.acc_stride) + ((uint32_t)(q * 32) << 16);
-        float old[16];
-        if constexpr (!ARGMAX) {
-          if (a.add != nullptr && ok) mx_addend<T>(a, f, row_of(h), old);
-        }
-        for (int n = h; n < ALL; n += EW / 4) {
-          if (WIDE && n >= SHARED && n - EW / 4 < SHARED) {  // this warp's shared chunks have left tensor memory
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(tempty));
-          }
-          const int c = (n + turn) & (ALL - 1), t0 = w.row0 + c * 16;
+        for (int n = h; n < chunks; n += EW / 4) {
           float v[16];
-          if constexpr (ARGMAX) {
-            if (ok && c < chunks) {
-              tmem_load16(tl + (uint32_t)(c * 16), v);
-              mx_argmax(a, f, t0, v, lane);
-            }
-          } else {
-            float next[16];
-            if (a.add != nullptr && ok && n + EW / 4 < ALL) mx_addend<T>(a, f, row_of(n + EW / 4), next);
-            if (ok && c < chunks) {
-              tmem_load16(tl + (uint32_t)(c * 16), v);
-              if (a.add != nullptr)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] += old[j];
-              mx_store<T>(a, f, t0, v);
-            }
-            if (a.add != nullptr)
-#pragma unroll
-              for (int j = 0; j < 16; ++j) old[j] = next[j];
-          }
+          if (ok) tmem_load16(tl + (uint32_t)(n * 16), v);
+          out.put(row_of(n), n + EW / 4 < chunks ? row_of(n + EW / 4) : -1, ok, v);
         }
-        if (!WIDE) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(tempty + buf));
-        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(tempty + buf));
       }
-      if constexpr (ARGMAX) {
-        const int thread = threadIdx.x - 128;
-        __threadfence();
-        named_bar_sync(1, 32 * EW);
-        if (thread == 0) *last_flag = atomicAdd(a.head.done, 1) == (int)gridDim.x - 1;
-        named_bar_sync(1, 32 * EW);
-        if (*last_flag) {
-          __threadfence();
-          for (int t = thread; t < a.n_rows; t += 32 * EW) a.head.drafts[t] = argmax_key_index(__ldcg(a.head.keys + t));
-          if (thread == 0) *a.head.done = 0;
-          if (a.head.has_verify) {
-            named_bar_sync(1, 32 * EW);
-            for (int b = thread; b < a.head.verify.B; b += 32 * EW) verify_seq(a.head.verify, b);
-          }
-        }
-      }
+      if constexpr (ARGMAX) mx_head_finish(a, last_flag, threadIdx.x - 128, 32 * EW);
     } else {
-      mbar_wait(smem_u32(tfull), 0, a.err, abort_flag, a.wait_ns);
+      mbar_wait_warp(smem_u32(tfull), 0, a, abort_flag);
       tc_fence_after();
     }
   }
@@ -516,7 +352,7 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
   if constexpr (!ARGMAX)
   if (p.cluster > 1) {
     // the cluster's one unit: every CTA's MMAs are done (or given up), so the stages' memory takes the partial sums
-    const MxUnit w = mx_unit<SRC>(a, p, first);
+    const MxUnit w = mx_unit(a, p, first);
     const int share = w.cols / p.cluster;  // columns that each CTA sums
     __syncthreads();
     cluster_sync();
@@ -566,10 +402,10 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
   if (*abort_flag) {
     // After a wait gave up no copy may stay in flight into this CTA's shared memory: threads that stopped earlier than
     // others arrive, without a copy, for the stages they left out, so that every stage begun completes.
-    const bool copier = lane == 0 && (warp == 0 || (!KEEP && (warp == 2 || (WIDE && warp == 3))));
+    const bool copier = lane == 0 && (warp == 0 || (!KEEP && warp == 2));
     if (copier) issued_max[warp] = issued;
     __syncthreads();
-    const int last = KEEP ? issued_max[0] : max(issued_max[0], max(issued_max[2], WIDE ? issued_max[3] : 0));
+    const int last = KEEP ? issued_max[0] : max(issued_max[0], issued_max[2]);
     if (copier) {
       if (warp == 0 && drop >= 0 && drop < issued) mbar_arrive(smem_u32(full + drop % S));
       for (int i = issued; i < last; ++i) mbar_arrive(smem_u32(full + i % S));
@@ -599,33 +435,24 @@ MxPlan plan_mx(const MxMatmulArgs& a, int sms) {
   p.n_f = (a.n_out + kMxPiece - 1) / kMxPiece;
   p.n_t = (a.n_rows + kMxPiece - 1) / kMxPiece;
   p.bn = std::min(kMxPiece, (a.n_rows + 15) & ~15);
-  long long units = (long long)p.n_f * p.n_t;
+  const long long units = (long long)p.n_f * p.n_t;
   p.cluster = 1;
   // (the LM head's sums are looked at as they are: no shares)
-  while (a.head.keys == nullptr && p.cluster < 8 && units * p.cluster * 2 <= sms && p.pieces >= p.cluster * 4) p.cluster *= 2;
+  while (a.head.keys == nullptr && p.cluster < 8 && units * p.cluster * 2 <= sms && p.pieces >= p.cluster * 4)
+    p.cluster *= 2;
   const int part = (p.pieces + p.cluster - 1) / p.cluster;
   const bool keep = keeps_x(a.n_rows, part);
-  // a wide tile takes in 3 records a piece for the 4 of two tiles, and reads its weights from shared memory once: about
-  // three quarters of their time
-  const long long wide_units = (long long)p.n_f * ((p.n_t + 1) / 2);
-  const bool wide = !keep && p.n_t > 1 && (wide_units + sms - 1) / sms * p.pieces * 3 < (units + sms - 1) / sms * part * 2;
-  p.src = wide ? SRC_WIDE : !keep ? SRC_STAGES : a.rows == nullptr ? SRC_RECORDS : a.rows_type == PE_BF16 ? SRC_BF16 : SRC_F32;
-  if (wide) {
-    p.cluster = 1;
-    p.n_t = (p.n_t + 1) / 2;
-    p.bn = 2 * kMxPiece;
-    units = wide_units;
-  }
-  const int ka = wide ? kMxgKa<SRC_WIDE> : kMxgKa<SRC_STAGES>;
+  p.src = !keep ? SRC_STAGES : a.rows == nullptr ? SRC_RECORDS : a.rows_type == PE_BF16 ? SRC_BF16 : SRC_F32;
+  const int ka = kMxgKa;
   p.x_piece = keep ? kMxScales + 64u * (uint32_t)p.bn : kMxRecord;
   p.x_bytes = keep ? (uint32_t)part * p.x_piece : 0;
-  p.stage_bytes = (uint32_t)ka * (keep ? 1 : wide ? 3 : 2) * kMxRecord;
-  p.stages = wide ? kWideStages : (int)((kTcSmemOptIn - 128 - (long long)kMxgCtrl - p.x_bytes) / p.stage_bytes);
+  p.stage_bytes = (uint32_t)ka * (keep ? 1 : 2) * kMxRecord;
+  p.stages = (int)((kTcSmemOptIn - 128 - (long long)kMxgCtrl - p.x_bytes) / p.stage_bytes);
   if (p.cluster > 1) p.stages = std::min(p.stages, (part + ka - 1) / ka);
   p.ring_bytes = (uint32_t)p.stages * p.stage_bytes;
   if (p.cluster > 1) p.ring_bytes = std::max(p.ring_bytes, (uint32_t)p.bn * kMxPiece * 4u);
-  p.acc_stride = wide ? kWideOdd : keep ? kMxgKeepRows : kMxPiece;
-  p.scale_col = wide ? 512 - kWideShared : 2 * p.acc_stride;
+  p.acc_stride = keep ? kMxgKeepRows : kMxPiece;
+  p.scale_col = 2 * p.acc_stride;
   p.x_col = 256;
   p.grid = p.cluster * (int)std::min<long long>(units, p.cluster > 1 ? units : sms);
   p.smem = 128 + (size_t)p.ring_bytes + p.x_bytes + kMxgCtrl;
@@ -666,7 +493,6 @@ cudaError_t launch_typed(const MxMatmulArgs& a, int sms, cudaStream_t s) {
   const MxPlan p = plan_mx(a, sms);
   switch (p.src) {
     case SRC_STAGES: return launch_src<T, SRC_STAGES>(a, p, s);
-    case SRC_WIDE: return launch_src<T, SRC_WIDE>(a, p, s);
     case SRC_RECORDS: return launch_src<T, SRC_RECORDS>(a, p, s);
     case SRC_BF16: return launch_src<T, SRC_BF16>(a, p, s);
     case SRC_F32: return launch_src<T, SRC_F32>(a, p, s);
@@ -681,13 +507,21 @@ cudaError_t launch_typed(const MxMatmulArgs& a, int sms, cudaStream_t s) {
 bool mx_matmul_quantises(int n_rows, int n_out, int width, bool head, int sms) {
   MxMatmulArgs a{};
   unsigned long long key;
-  a.head.keys = head ? &key : nullptr;
-  a.n_rows = n_rows; a.n_out = n_out; a.width = width;
+  a.n_rows = n_rows; a.n_out = n_out; a.width = width; a.head.keys = head ? &key : nullptr;
   const MxPlan p = plan_mx(a, sms);
   return p.src == SRC_RECORDS && (long long)p.bn * ((p.pieces + p.cluster - 1) / p.cluster) * kMxPiece <= 12288;
 }
 
+// Both kernels are bound by what an SM takes in, so the one whose busiest CTA takes in less is chosen (a pair's CTA as
+// much a piece of a 256 x 256 tile as one of a 128 x 128 tile).
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, pe_dtype dt, int sms, cudaStream_t s) {
+  const MxPlan p = plan_mx(a, sms);
+  if (a.n_rows > kMxPiece) {
+    const int pairs = mx_pair_clusters(sms);
+    const long long tiles = (long long)((a.n_out + 255) / 256) * ((a.n_rows + 255) / 256);
+    const long long one = ((long long)p.n_f * p.n_t * p.cluster + sms - 1) / sms * ((p.pieces + p.cluster - 1) / p.cluster);
+    if ((tiles + pairs - 1) / pairs * p.pieces < one) return launch_mx_pairs(a, dt, pairs, s);
+  }
   if (a.head.keys != nullptr) return launch_typed<MxArgmax>(a, sms, s);
   return dt == PE_BF16 ? launch_typed<__nv_bfloat16>(a, sms, s) : launch_typed<float>(a, sms, s);
 }

@@ -195,7 +195,7 @@ def test_product_is_exact_where_sums_are(n, m, w):
     assert np.array_equal(mx.kept(x), x) and np.array_equal(_np(y), x @ wt.T) and int(err.item()) == 0
 
 
-# many rows, from one unit of 128 x 256 a CTA to several each, with odd numbers of 128-row blocks on either side
+# many rows, from one unit of 256 x 256 a pair of CTAs to several each, with odd numbers of 128-row blocks on either side
 MANY = [(2000, 2000, 257), (1300, 5200, 100), (3000, 3000, 300), (4099, 6000, 200), (2900, 7900, 1000)]
 
 
