@@ -410,11 +410,13 @@ def _rows(t, what: str, dev: int, dtype, width: int, n: int):
     if t.dtype is not dtype or t.get_device() != dev or len(shape) < 2 or shape[0] != n:
         raise ValueError(f"{what}: expected {n} rows of {dtype} on cuda:{dev}, got {t.dtype} {tuple(shape)} on "
                          f"{t.device}")
-    if t.is_contiguous() and t.numel() == n * width and n > 0:
-        return t.data_ptr(), width
     stride = t.stride()
-    if len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2] and shape[1] * shape[2] == width and n > 1:
-        return t.data_ptr(), stride[0]
+    if n > 1:
+        if len(shape) == 2:
+            if shape[1] == width and stride[1] == 1:
+                return t.data_ptr(), stride[0]
+        elif len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2] and shape[1] * shape[2] == width:
+            return t.data_ptr(), stride[0]
     inner = 1
     for size, stride in zip(shape[:0:-1], stride[:0:-1]):
         if size != 1 and stride != inner:
@@ -514,39 +516,44 @@ def append_kv(cfg, q, k, v, positions, slots, cache, q_out, err, axes=None, stre
     q; both None: no queries) and keys and values to one layer's ``cache`` at ``slots`` (int64; -1: passed over): a pair
     (k_cache, v_cache) of [pages][16][n_kv][head_dim], or a packed pool (alloc_packed_pool).  ``positions``: int32 [n], or
     [axes][n] with ``axes`` the axis of each of the head_dim/2 pairs, as bytes."""
-    packed = isinstance(cache, torch.Tensor)
     dev, n, dt, n_kv, hd = _current(slots), slots.numel(), cfg.torch_dtype, cfg.n_kv, cfg.head_dim
     sp = _vector(slots, "slots", dev, torch.int64)
-    n_axes = positions.shape[0] if positions.dim() == 2 else 1
-    pos = _tensor(positions, "positions", dev, torch.int32, (n,) if positions.dim() == 1 else (n_axes, n))
+    shape = positions.shape
+    n_axes = shape[0] if len(shape) == 2 else 1
+    if shape[-1:] != (n,) or len(shape) > 2:
+        raise ValueError(f"positions: expected [{n}] or [axes][{n}], got {tuple(shape)}")
+    pos = _tensor(positions, "positions", dev, torch.int32)
     if axes is not None and (type(axes) is not bytes or len(axes) != hd // 2):
         raise ValueError(f"axes: expected {hd // 2} bytes, one per pair")
-    kp, ks = _rows(k, "k", dev, dt, n_kv * hd, n)
-    vp, vs = _rows(v, "v", dev, dt, n_kv * hd, n)
+    width = n_kv * hd
+    kp, ks = _rows(k, "k", dev, dt, width, n)
+    vp, vs = _rows(v, "v", dev, dt, width, n)
     if q is None and q_out is None:
         qp = qs = op = os_ = 0
     else:
-        qp, qs = _rows(q, "q", dev, dt, cfg.n_q * hd, n)
-        op, os_ = _rows(q_out, "q_out", dev, dt, cfg.n_q * hd, n)
+        width = cfg.n_q * hd
+        qp, qs = _rows(q, "q", dev, dt, width, n)
+        op, os_ = _rows(q_out, "q_out", dev, dt, width, n)
     ep = _tensor(err, "err", dev, torch.int32)
-    if packed:
+    if isinstance(cache, torch.Tensor):
         pp, pages = _pool(n_kv, hd, cache, dev)
-    else:
-        kc, vc = cache
-        pages = kc.shape[0]
-        kcp = _tensor(kc, "k_cache", dev, dt, (pages, 16, n_kv, hd))
-        vcp = _tensor(vc, "v_cache", dev, dt, (pages, 16, n_kv, hd))
-    if n == 0:
+        if n > 0:
+            st = (_lib or lib()).pe_append_kv_packed(cfg, qp, kp, vp, qs, ks, vs, pos, n_axes, axes, sp, n, op, os_, pp,
+                                                     pages, ep, _raw_stream(stream, dev))
+            if st != PE_OK:
+                raise PeError(st, "pe_append_kv_packed")
         return
-    raw = _raw_stream(stream, dev)
-    if packed:
-        st = (_lib or lib()).pe_append_kv_packed(cfg, qp, kp, vp, qs, ks, vs, pos, n_axes, axes, sp, n, op, os_, pp, pages,
-                                                 ep, raw)
-    else:
-        st = (_lib or lib()).pe_append_kv(cfg, qp, kp, vp, qs, ks, vs, pos, n_axes, axes, sp, n, op, os_, kcp, vcp, pages,
-                                          ep, raw)
-    if st != PE_OK:
-        raise PeError(st, "pe_append_kv_packed" if packed else "pe_append_kv")
+    kc, vc = cache
+    shape = kc.shape
+    if len(shape) != 4 or shape[1:] != (16, n_kv, hd):
+        raise ValueError(f"k_cache: expected [pages][16][{n_kv}][{hd}], got {tuple(shape)}")
+    kcp = _tensor(kc, "k_cache", dev, dt)
+    vcp = _tensor(vc, "v_cache", dev, dt, shape)
+    if n > 0:
+        st = (_lib or lib()).pe_append_kv(cfg, qp, kp, vp, qs, ks, vs, pos, n_axes, axes, sp, n, op, os_, kcp, vcp,
+                                          shape[0], ep, _raw_stream(stream, dev))
+        if st != PE_OK:
+            raise PeError(st, "pe_append_kv")
 
 
 # ----------------------------------------------------------------------------- microscaled (MX) 4-bit matrices
@@ -557,7 +564,10 @@ def mx_bytes(n_rows: int, width: int) -> int:
 
 
 class MxMatrix:
-    """A matrix of n_rows x width entries in microscaled 4-bit floating point, resident on the device (see pe.h)."""
+    """A matrix of n_rows x width entries in microscaled 4-bit floating point, resident on the device (see pe.h): its
+    bytes are ``data``, which stays the tensor it was made with."""
+
+    __slots__ = ("n_rows", "width", "data", "_ptr", "_dev")
 
     def __init__(self, n_rows: int, width: int, device="cuda", data=None):
         size = mx_bytes(n_rows, width)
@@ -568,6 +578,7 @@ class MxMatrix:
         elif not (data.is_cuda and data.dtype is torch.uint8 and data.is_contiguous() and data.numel() >= size):
             raise ValueError(f"data: expected a contiguous uint8 CUDA tensor of at least {size} bytes")
         self.n_rows, self.width, self.data = n_rows, width, data
+        self._ptr, self._dev = data.data_ptr(), data.get_device()
 
     def first(self, n_rows: int) -> "MxMatrix":
         """The first n_rows rows, in the same memory."""
@@ -577,60 +588,68 @@ class MxMatrix:
 
 
 def _mx(m, what: str, dev: int) -> int:
-    if m.data.get_device() != dev:
+    if m._dev != dev:
         raise ValueError(f"{what}: expected a matrix on cuda:{dev}, got {m.data.device}")
-    return m.data.data_ptr()
+    return m._ptr
+
+
+_ROW_TYPES = {torch.bfloat16: PE_BF16, torch.float32: PE_F32}
 
 
 def _any_rows(t, what: str, dev: int, n: int, width: int):
     """Type (as pe_dtype), address and row stride of n rows of ``width`` fp32 or bf16 elements, each row contiguous."""
-    dt = PE_BF16 if t.dtype is torch.bfloat16 else PE_F32 if t.dtype is torch.float32 else None
-    if dt is None or t.get_device() != dev or t.shape != (n, width) or (width > 1 and n > 0 and t.stride(1) != 1):
-        raise ValueError(f"{what}: expected {n} rows of {width} contiguous fp32 or bf16 elements on cuda:{dev}, got "
-                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    return dt, t.data_ptr(), t.stride(0) if n > 1 else width
+    dt = _ROW_TYPES.get(t.dtype)
+    if dt is not None and t.get_device() == dev and t.shape == (n, width):
+        if t.is_contiguous():
+            return dt, t.data_ptr(), width
+        stride = t.stride()
+        if width <= 1 or n == 0 or stride[1] == 1:
+            return dt, t.data_ptr(), stride[0] if n > 1 else width
+    raise ValueError(f"{what}: expected {n} rows of {width} contiguous fp32 or bf16 elements on cuda:{dev}, got "
+                     f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def quantize_mx(x, m: MxMatrix, err, stream=None):
     """Round rows x [n_rows][width] (fp32 or bf16) to 4 bits, into ``m``."""
-    dev = _current(x)
-    dt, xp, xs = _any_rows(x, "x", dev, m.n_rows, m.width)
+    dev, n, width = _current(x), m.n_rows, m.width
+    dt, xp, xs = _any_rows(x, "x", dev, n, width)
     mp, ep = _mx(m, "m", dev), _tensor(err, "err", dev, torch.int32)
-    if m.n_rows > 0:
-        st = (_lib or lib()).pe_quantize_mx(dt, xp, xs, m.n_rows, m.width, mp, ep, _raw_stream(stream, dev))
+    if n > 0:
+        st = (_lib or lib()).pe_quantize_mx(dt, xp, xs, n, width, mp, ep, _raw_stream(stream, dev))
         if st != PE_OK:
             raise PeError(st, "pe_quantize_mx")
 
 
 def dequantize_mx(m: MxMatrix, x, stream=None):
     """Read a matrix back into rows x [n_rows][width] (fp32 or bf16) as the values it stands for."""
-    dev = _current(x)
-    dt, xp, xs = _any_rows(x, "x", dev, m.n_rows, m.width)
+    dev, n, width = _current(x), m.n_rows, m.width
+    dt, xp, xs = _any_rows(x, "x", dev, n, width)
     mp = _mx(m, "m", dev)
-    if m.n_rows > 0:
-        st = (_lib or lib()).pe_dequantize_mx(dt, mp, m.n_rows, m.width, xp, xs, _raw_stream(stream, dev))
+    if n > 0:
+        st = (_lib or lib()).pe_dequantize_mx(dt, mp, n, width, xp, xs, _raw_stream(stream, dev))
         if st != PE_OK:
             raise PeError(st, "pe_dequantize_mx")
 
 
-def _product(y, n: int, w: MxMatrix, add, err, dev: int):
-    """What the two products have in common: type, addresses and strides of y and of what is added."""
-    dt, yp, ys = _any_rows(y, "y", dev, n, w.n_rows)
-    adt, ap, as_ = (dt, None, 0) if add is None else _any_rows(add, "add", dev, n, w.n_rows)
+def _addend(add, dt: int, dev: int, n: int, n_out: int):
+    if add is None:
+        return None, 0
+    adt, ap, as_ = _any_rows(add, "add", dev, n, n_out)
     if adt != dt:
         raise ValueError("add: expected y's type")
-    return dt, yp, ys, ap, as_, _mx(w, "w", dev), _tensor(err, "err", dev, torch.int32)
+    return ap, as_
 
 
 def matmul_mx(x: MxMatrix, w: MxMatrix, y, err, add=None, stream=None):
     """y [x.n_rows][w.n_rows] (fp32 or bf16) = add + x . w^T; ``add`` may be y."""
-    if x.width != w.width:
-        raise ValueError(f"x and w: widths {x.width} and {w.width} differ")
-    dev, n = _current(y), x.n_rows
-    dt, yp, ys, ap, as_, wp, ep = _product(y, n, w, add, err, dev)
-    xp = _mx(x, "x", dev)
+    dev, n, n_out, width = _current(y), x.n_rows, w.n_rows, w.width
+    if x.width != width:
+        raise ValueError(f"x and w: widths {x.width} and {width} differ")
+    dt, yp, ys = _any_rows(y, "y", dev, n, n_out)
+    ap, as_ = _addend(add, dt, dev, n, n_out)
+    xp, wp, ep = _mx(x, "x", dev), _mx(w, "w", dev), _tensor(err, "err", dev, torch.int32)
     if n > 0:
-        st = (_lib or lib()).pe_matmul_mx(xp, n, wp, w.n_rows, w.width, ap, as_, dt, yp, ys, ep, _raw_stream(stream, dev))
+        st = (_lib or lib()).pe_matmul_mx(xp, n, wp, n_out, width, ap, as_, dt, yp, ys, ep, _raw_stream(stream, dev))
         if st != PE_OK:
             raise PeError(st, "pe_matmul_mx")
 
@@ -638,13 +657,15 @@ def matmul_mx(x: MxMatrix, w: MxMatrix, y, err, add=None, stream=None):
 def linear_mx(x, w: MxMatrix, y, workspace, err, add=None, stream=None):
     """matmul_mx of rows x [n][w.width] (fp32 or bf16) that are quantised on the way.  ``workspace``:
     alloc_linear_mx_workspace."""
-    dev, n = _current(y), x.shape[0]
-    xdt, xp, xs = _any_rows(x, "x", dev, n, w.width)
-    dt, yp, ys, ap, as_, wp, ep = _product(y, n, w, add, err, dev)
+    dev, n, n_out, width = _current(y), x.shape[0], w.n_rows, w.width
+    xdt, xp, xs = _any_rows(x, "x", dev, n, width)
+    dt, yp, ys = _any_rows(y, "y", dev, n, n_out)
+    ap, as_ = _addend(add, dt, dev, n, n_out)
+    wp, ep = _mx(w, "w", dev), _tensor(err, "err", dev, torch.int32)
     sp = _vector(workspace, "workspace", dev, torch.uint8)
     if n > 0:
-        st = (_lib or lib()).pe_linear_mx(xdt, xp, xs, n, wp, w.n_rows, w.width, ap, as_, dt, yp, ys, sp,
-                                          workspace.numel(), ep, _raw_stream(stream, dev))
+        st = (_lib or lib()).pe_linear_mx(xdt, xp, xs, n, wp, n_out, width, ap, as_, dt, yp, ys, sp, workspace.numel(),
+                                          ep, _raw_stream(stream, dev))
         if st != PE_OK:
             raise PeError(st, "pe_linear_mx")
 
