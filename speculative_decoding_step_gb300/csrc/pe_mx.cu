@@ -46,8 +46,10 @@ template <>
 struct BitsOf<__nv_bfloat16> {
   using type = uint16_t;
 };
-PE_DEV float widen(uint32_t b) { return __uint_as_float(b); }
-PE_DEV float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+template <typename T>
+PE_DEV float widen(uint32_t b) {
+  return __uint_as_float(sizeof(T) == 2 ? b << 16 : b);
+}
 
 // Eight entries of each lane of a pair, the odd lane's after the even lane's.  fp32: the lanes exchange halves, so
 // that either store of a pair fills 32 bytes (a lane its own 16 at a time: 75 us instead of 44 for 8209 x 7680).
@@ -115,28 +117,27 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const MxRowsArg
       } else {
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            x[b][e] = live && b * kMxBlock + at.quarter * 8 + e < left ? to_float<T>(p[b * kMxBlock + e]) : 0.f;
+          get8_of(p + b * kMxBlock, live ? left - b * kMxBlock - at.quarter * 8 : 0, x[b]);
       }
     } else {
       using Bits = typename BitsOf<T>::type;
       float* tile = tiles[at.warp];
-      Bits raw[8][4];  // loaded together: each is a trip to memory
+      // Loaded together, each is a trip to memory: what is not there is read from another place, since loads under a
+      // condition wait for each other (16-bit ones: 24.9 us for 2316 x 6919 instead of 12.2).
+      Bits raw[8][4];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const T* p = static_cast<const T*>(a.x) + (at.row0 + j) * a.stride + (size_t)piece * kMxPiece;
+        const long long row = min(at.row0 + j, (long long)a.n_rows - 1);
+        const Bits* p = reinterpret_cast<const Bits*>(static_cast<const T*>(a.x) + row * a.stride + (size_t)piece * kMxPiece);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = e * 32 + lane;
-          raw[j][e] = at.row0 + j < a.n_rows && c < left ? __ldg(reinterpret_cast<const Bits*>(p) + c) : (Bits)0;
-        }
+        for (int e = 0; e < 4; ++e) raw[j][e] = __ldg(p + min(e * 32 + lane, left - 1));
       }
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) tile[j * kMxTileRow + e * 32 + lane] = widen(raw[j][e]);
+        for (int e = 0; e < 4; ++e)
+          tile[j * kMxTileRow + e * 32 + lane] = e * 32 + lane < left ? widen<T>(raw[j][e]) : 0.f;
       __syncwarp();
 #pragma unroll
       for (int b = 0; b < 4; ++b)

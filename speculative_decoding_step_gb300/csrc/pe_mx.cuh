@@ -80,6 +80,24 @@ PE_DEV void get8(const __nv_bfloat16* p, float (&x)[8]) {
     x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
   }
 }
+// The first n of them, then zeros.  (Loads under a condition wait for each other, so the last one there is read again in the
+// place of those that are not.)
+template <typename T>
+PE_DEV void get8_of(const T* p, int n, float (&x)[8]) {
+  if (n >= 8) {
+    get8(p, x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    if (n <= 0) return;
+    T v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = p[min(e, n - 1)];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) x[e] = to_float<T>(v[e]);
+  }
+}
 PE_DEV uint32_t max_over_four(uint32_t v) {
   v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
   return max(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));

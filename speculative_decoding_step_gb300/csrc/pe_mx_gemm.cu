@@ -43,8 +43,8 @@ constexpr int kMxgKeepRows = 64;             // rows of x that are kept at most 
 constexpr int kMxgKeepPieces = 64;           // pieces of x that are kept at most (256 columns of scales)
 constexpr uint32_t kMxgKeepBytes = 96 * 1024;
 
-PE_DEV void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+PE_DEV void st_cluster_v4(uint32_t addr, float x, float y, float z, float w) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
 
 struct MxUnit {
@@ -89,10 +89,7 @@ PE_DEV void keep_rows(const MxMatmulArgs& a, const MxPlan& p, uint8_t* xs, int p
         for (int b = 0; b < 4; ++b) get8(src + b * kMxBlock, x[i][b]);
       } else {
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            x[i][b][e] = live && b * kMxBlock + e < left ? to_float<T>(src[b * kMxBlock + e]) : 0.f;
+        for (int b = 0; b < 4; ++b) get8_of(src + b * kMxBlock, live ? left - b * kMxBlock : 0, x[i][b]);
       }
     }
 #pragma unroll
@@ -138,7 +135,7 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued_max = abort_flag + 1;  // [4], by warp
   volatile int* last_flag = issued_max + 4;
-  float* recv = reinterpret_cast<float*>(smem);  // clusters, after the MMAs: [rank][columns of this CTA][128]
+  float* recv = reinterpret_cast<float*>(smem);  // clusters, after the MMAs: [rank][quads of columns of this CTA][128][4]
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -353,25 +350,22 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
   if (p.cluster > 1) {
     // the cluster's one unit: every CTA's MMAs are done (or given up), so the stages' memory takes the partial sums
     const MxUnit w = mx_unit(a, p, first);
-    const int share = w.cols / p.cluster;  // columns that each CTA sums
+    const int quads = w.cols / 4, share = (quads + p.cluster - 1) / p.cluster;  // quads of columns that each CTA sums
     __syncthreads();
     cluster_sync();
     if (warp >= 4 && !*abort_flag) {
       const int q = warp & 3, h = (warp - 4) >> 2, r = q * 32 + lane;
       const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
+      // to [rank][quad of the owner's][row of w], 16 bytes each
+      const uint32_t mine = smem_u32(recv) + (uint32_t)(rank * share * kMxPiece + r) * 16;
       for (int c = h; c < w.cols / 16; c += EW / 4) {
         float v[16];
         tmem_load16(tl + (uint32_t)(c * 16), v);
-        int owner = c * 16 / share, col = c * 16 - owner * share;  // and on from there column by column
-        uint32_t at = mapa_shared(smem_u32(recv + (size_t)(rank * share) * kMxPiece + r), (uint32_t)owner);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          st_cluster_f32(at + (uint32_t)(col * kMxPiece * 4), v[j]);
-          if (++col == share) {
-            col = 0;
-            if (++owner < p.cluster)
-              at = mapa_shared(smem_u32(recv + (size_t)(rank * share) * kMxPiece + r), (uint32_t)owner);
-          }
+        for (int j = 0; j < 4; ++j) {
+          const int owner = (4 * c + j) / share, at = 4 * c + j - owner * share;
+          st_cluster_v4(mapa_shared(mine + (uint32_t)(at * kMxPiece) * 16, (uint32_t)owner), v[4 * j], v[4 * j + 1],
+                        v[4 * j + 2], v[4 * j + 3]);
         }
       }
       tc_fence_before();
@@ -380,20 +374,34 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
     cluster_sync();  // every partial sum is where it is summed
     if (warp >= 4 && !*abort_flag) {
       const int r = (warp & 3) * 32 + lane, h = (warp - 4) >> 2;
-      const int f = w.tile_f * kMxPiece + r, t0 = w.row0 + rank * share;
+      const int f = w.tile_f * kMxPiece + r, n = min(share, quads - rank * share);
+      const float4* part = reinterpret_cast<const float4*>(recv) + r;
       if (f < a.n_out)
-        for (int c = h; c < share && t0 + c < a.n_rows; c += EW / 4) {
-          float part[8];
+        for (int c = h; c < n; c += EW / 4) {
+          const int t0 = w.row0 + 4 * (rank * share + c);
+          float v[4] = {};
+          float4 x[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            part[k] = k < p.cluster ? recv[(size_t)(k * share + c) * kMxPiece + r] : 0.f;
-          float v = part[0];
+            if (k < p.cluster) x[k] = part[(k * share + c) * kMxPiece];
+          float old[4];
 #pragma unroll
-          for (int k = 1; k < 8; ++k)
-            if (k < p.cluster) v += part[k];
-          if (a.add != nullptr)
-            v += to_float<T>(static_cast<const T*>(a.add)[(long long)(t0 + c) * a.add_stride + f]);
-          static_cast<T*>(a.y)[(long long)(t0 + c) * a.y_stride + f] = from_float<T>(v);
+          for (int j = 0; j < 4; ++j)
+            old[j] = a.add == nullptr ? 0.f
+                                      : to_float<T>(static_cast<const T*>(
+                                            a.add)[(long long)min(t0 + j, a.n_rows - 1) * a.add_stride + f]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < p.cluster) {
+              v[0] += x[k].x;
+              v[1] += x[k].y;
+              v[2] += x[k].z;
+              v[3] += x[k].w;
+            }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (t0 + j < a.n_rows)
+              static_cast<T*>(a.y)[(long long)(t0 + j) * a.y_stride + f] = from_float<T>(v[j] + old[j]);
         }
     }
   }
@@ -429,6 +437,51 @@ bool keeps_x(int n_rows, int pieces) {
          (size_t)pieces * (kMxScales + 64u * (uint32_t)bn) <= kMxgKeepBytes;
 }
 
+// Clusters of so many CTAs that fit on the GPU at once.  Without a device (host-only use of the plan): a quarter less than
+// the SMs would hold.
+int clusters_that_fit(int size, int sms) {
+  static int known[64][9] = {{0}};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sms * 3 / 4 / size;
+  if (known[dev][size] == 0) {
+    int n = 0;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3(kMxgThreads);
+    cfg.dynamicSmemBytes = kTcSmemOptIn;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto* kernel = mx_gemm_kernel<float, SRC_STAGES>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmemOptIn) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      return sms * 3 / 4 / size;
+    }
+    known[dev][size] = n;
+  }
+  return known[dev][size];
+}
+
+// CTAs that share a tile along k.  A CTA takes about 0.107 us a piece where few are at work, and joining the parts 1 us and
+// 0.02 a column (16 rows of 4096 to 128 features 5.8 us alone, 4.4 as eight; of 1024 3.4 and 4.2; 128 rows of 8192 10.1
+// and 7.2, of 2048 5.1 and 6.4).
+int cluster_of(long long units, int pieces, int bn, int sms) {
+  int best = 1, gain = 0;  // ns
+  for (int c = 2; c <= 8; c *= 2) {
+    const int g = (pieces - (pieces + c - 1) / c) * 107 - (1000 + 20 * bn);
+    if (g > gain && units <= clusters_that_fit(c, sms)) {
+      best = c;
+      gain = g;
+    }
+  }
+  return best;
+}
+
 MxPlan plan_mx(const MxMatmulArgs& a, int sms) {
   MxPlan p{};
   p.pieces = (a.width + kMxPiece - 1) / kMxPiece;
@@ -436,10 +489,7 @@ MxPlan plan_mx(const MxMatmulArgs& a, int sms) {
   p.n_t = (a.n_rows + kMxPiece - 1) / kMxPiece;
   p.bn = std::min(kMxPiece, (a.n_rows + 15) & ~15);
   const long long units = (long long)p.n_f * p.n_t;
-  p.cluster = 1;
-  // (the LM head's sums are looked at as they are: no shares)
-  while (a.head.keys == nullptr && p.cluster < 8 && units * p.cluster * 2 <= sms && p.pieces >= p.cluster * 4)
-    p.cluster *= 2;
+  p.cluster = a.head.keys == nullptr ? cluster_of(units, p.pieces, p.bn, sms) : 1;  // (the LM head looks at its sums as they are)
   const int part = (p.pieces + p.cluster - 1) / p.cluster;
   const bool keep = keeps_x(a.n_rows, part);
   p.src = !keep ? SRC_STAGES : a.rows == nullptr ? SRC_RECORDS : a.rows_type == PE_BF16 ? SRC_BF16 : SRC_F32;
@@ -450,7 +500,8 @@ MxPlan plan_mx(const MxMatmulArgs& a, int sms) {
   p.stages = (int)((kTcSmemOptIn - 128 - (long long)kMxgCtrl - p.x_bytes) / p.stage_bytes);
   if (p.cluster > 1) p.stages = std::min(p.stages, (part + ka - 1) / ka);
   p.ring_bytes = (uint32_t)p.stages * p.stage_bytes;
-  if (p.cluster > 1) p.ring_bytes = std::max(p.ring_bytes, (uint32_t)p.bn * kMxPiece * 4u);
+  if (p.cluster > 1)  // the partial sums of a CTA's share
+    p.ring_bytes = std::max(p.ring_bytes, (uint32_t)((p.bn / 4 + p.cluster - 1) / p.cluster * p.cluster) * kMxPiece * 16u);
   p.acc_stride = keep ? kMxgKeepRows : kMxPiece;
   p.scale_col = 2 * p.acc_stride;
   p.x_col = 256;
@@ -512,15 +563,18 @@ bool mx_matmul_quantises(int n_rows, int n_out, int width, bool head, int sms) {
   return p.src == SRC_RECORDS && (long long)p.bn * ((p.pieces + p.cluster - 1) / p.cluster) * kMxPiece <= 12288;
 }
 
-// Both kernels are bound by what an SM takes in, so the one whose busiest CTA takes in less is chosen (a pair's CTA as
-// much a piece of a 256 x 256 tile as one of a 128 x 128 tile).
+// More than 128 rows go to pairs of CTAs where those are expected to take less: about 0.17 us a piece of their 256 x 256
+// tiles against 0.12 of a CTA's 128 x 128 ones, and 1.7 us a call more (640 rows of 7680 to 4096 features: 17.5 us by CTAs,
+// 15.5 by pairs; 256 of 2048 to 4096: 5.6 and 8.0; 1500 of 7680 to 12288: 62 and 48).
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, pe_dtype dt, int sms, cudaStream_t s) {
   const MxPlan p = plan_mx(a, sms);
   if (a.n_rows > kMxPiece) {
     const int pairs = mx_pair_clusters(sms);
     const long long tiles = (long long)((a.n_out + 255) / 256) * ((a.n_rows + 255) / 256);
-    const long long one = ((long long)p.n_f * p.n_t * p.cluster + sms - 1) / sms * ((p.pieces + p.cluster - 1) / p.cluster);
-    if ((tiles + pairs - 1) / pairs * p.pieces < one) return launch_mx_pairs(a, dt, pairs, s);
+    const long long two = (tiles + pairs - 1) / pairs * p.pieces * 170 + 1700;
+    const long long one = p.cluster > 1 ? (p.pieces + p.cluster - 1) / p.cluster * 107 + 1000 + 20 * p.bn
+                                        : ((long long)p.n_f * p.n_t + sms - 1) / sms * p.pieces * 120;
+    if (two < one) return launch_mx_pairs(a, dt, pairs, s);
   }
   if (a.head.keys != nullptr) return launch_typed<MxArgmax>(a, sms, s);
   return dt == PE_BF16 ? launch_typed<__nv_bfloat16>(a, sms, s) : launch_typed<float>(a, sms, s);

@@ -44,13 +44,16 @@ PE_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, const MxMatmulArgs& a,
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, a.err, abort, a.wait_ns) && !*abort);
 }
 
-// What is added to 16 columns (rows t0.. of y) of feature f.
+// What is added to 16 columns (rows t0.. of y) of feature f.  Rows and features beyond the last read the last one's, and do
+// not use it: loads under a condition wait for each other (158 rows to 23494 features, bf16: 21 us instead of 9).
 template <typename T>
 PE_DEV void mx_addend(const MxMatmulArgs& a, int f, int t0, float (&old)[16]) {
-  const T* add = static_cast<const T*>(a.add) + (long long)t0 * a.add_stride + f;
-  const int n = f < a.n_out ? a.n_rows - t0 : 0;
+  const T* add = static_cast<const T*>(a.add) + min(f, a.n_out - 1);
+  T v[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) old[j] = j < n ? to_float<T>(add[(long long)j * a.add_stride]) : 0.f;
+  for (int j = 0; j < 16; ++j) v[j] = add[(long long)min(t0 + j, a.n_rows - 1) * a.add_stride];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) old[j] = to_float<T>(v[j]);
 }
 template <typename T>
 PE_DEV void mx_store(const MxMatmulArgs& a, int f, int t0, const float (&v)[16]) {
