@@ -195,6 +195,25 @@ def test_product_is_exact_where_sums_are(n, m, w):
     assert np.array_equal(mx.kept(x), x) and np.array_equal(_np(y), x @ wt.T) and int(err.item()) == 0
 
 
+# Tiles that two, four or eight CTAs share along k, with columns that do not divide evenly among them; far more rows than
+# anything else, one record of weights
+@pytest.mark.parametrize("n,m,w", [(16, 128, 8192), (7, 5000, 8000), (9, 2100, 5000), (64, 700, 6000), (50, 4500, 8192),
+                                   (100, 130, 8100), (128, 2000, 8192), (33, 129, 4097), (400000, 100, 100)])
+@pytest.mark.parametrize("out,add", [("f32", False), ("f32", True)])
+def test_product_of_shared_tiles_is_exact_where_sums_are(n, m, w, out, add):
+    rng = np.random.default_rng(n + m + w)
+    small = rng.choice([-2.0, -1.0, -0.5, 0.0, 0.5, 1.0, 1.5, 2.0, 4.0], size=(n, w))
+    small[:, ::32] = 4.0                                       # every block's scale is 1
+    wt = rng.choice([-1.0, -0.5, 0.0, 0.5, 1.0, 4.0], size=(m, w))
+    wt[:, ::32] = -4.0
+    y = torch.full((n, m), float("nan"), device="cuda")
+    a = torch.from_numpy(rng.integers(-64, 64, (n, m)).astype(np.float32)).cuda() if add else None
+    err = _err()
+    pe.matmul_mx(_mx(small), _mx(wt), y, err, add=a)
+    want = small.astype(np.float32) @ wt.T.astype(np.float32)  # multiples of 1/4 below 2^18: exact in fp32 in any order
+    assert np.array_equal(y.cpu().numpy(), want + a.cpu().numpy() if add else want) and int(err.item()) == 0
+
+
 # many rows, from one unit of 256 x 256 a pair of CTAs to several each, with odd numbers of 128-row blocks on either side
 MANY = [(2000, 2000, 257), (1300, 5200, 100), (3000, 3000, 300), (4099, 6000, 200), (2900, 7900, 1000)]
 
