@@ -1,8 +1,9 @@
 """P-EAGLE parallel-drafting round on one GB300: Python binding of the C ABI.
 
-Thin ctypes marshalling over ``libpe.so`` (``include/pe.h``): every entry point
-takes torch CUDA tensors (PyTorch supplies device memory and streams only) and
-passes their device pointers and sizes to the library.  All computation runs in
+Thin marshalling over ``libpe.so`` (``include/pe.h``) by ctypes, for the smallest calls by
+``pe_bind.so`` (``csrc/pe_bind.cpp``): every entry point takes torch CUDA tensors (PyTorch
+supplies device memory and streams only) and passes their device pointers and sizes to the
+library.  All computation runs in
 the library's CUDA kernels.  Loading fails loudly when the library has not been
 built; there is no fallback.
 """
@@ -10,11 +11,12 @@ built; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
 
-from .build import LIB, build
+from .build import BIND, LIB, build
 
 __all__ = [
     "PeError", "Config", "DeviceWeights", "DeviceKV", "DevicePackedKV", "lib", "build", "check_config", "workspace_bytes",
@@ -410,15 +412,10 @@ def _rows(t, what: str, dev: int, dtype, width: int, n: int):
     if t.dtype is not dtype or t.get_device() != dev or len(shape) < 2 or shape[0] != n:
         raise ValueError(f"{what}: expected {n} rows of {dtype} on cuda:{dev}, got {t.dtype} {tuple(shape)} on "
                          f"{t.device}")
-    stride = t.stride()
-    if n > 1:
-        if len(shape) == 2:
-            if shape[1] == width and stride[1] == 1:
-                return t.data_ptr(), stride[0]
-        elif len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2] and shape[1] * shape[2] == width:
-            return t.data_ptr(), stride[0]
+    if t.is_contiguous() and t.numel() == n * width and n > 0:
+        return t.data_ptr(), width
     inner = 1
-    for size, stride in zip(shape[:0:-1], stride[:0:-1]):
+    for size, stride in zip(shape[:0:-1], t.stride()[:0:-1]):
         if size != 1 and stride != inner:
             raise ValueError(f"{what}: the elements of a row have to be contiguous")
         inner *= size
@@ -511,49 +508,35 @@ def attend_packed(cfg, q, pool, block_table, row_start, positions, max_rows, out
             raise PeError(st, "pe_attend_packed")
 
 
+# What the following calls ask of their tensors, csrc/pe_bind.cpp asks.
+
+_bind = None
+
+
+def _binding():
+    global _bind
+    if _bind is None:
+        L = lib()
+        if not os.path.exists(BIND):
+            build()
+        spec = importlib.util.spec_from_file_location("pe_bind", BIND)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.use(*[ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in
+                ("pe_quantize_mx", "pe_dequantize_mx", "pe_matmul_mx", "pe_linear_mx", "pe_append_kv",
+                 "pe_append_kv_packed")])
+        _bind = m
+    return _bind
+
+
 def append_kv(cfg, q, k, v, positions, slots, cache, q_out, err, axes=None, stream=None):
     """Rotate rows q [n][n_q*head_dim] and k [n][n_kv*head_dim] by their positions and write queries to ``q_out`` (may be
     q; both None: no queries) and keys and values to one layer's ``cache`` at ``slots`` (int64; -1: passed over): a pair
     (k_cache, v_cache) of [pages][16][n_kv][head_dim], or a packed pool (alloc_packed_pool).  ``positions``: int32 [n], or
     [axes][n] with ``axes`` the axis of each of the head_dim/2 pairs, as bytes."""
-    dev, n, dt, n_kv, hd = _current(slots), slots.numel(), cfg.torch_dtype, cfg.n_kv, cfg.head_dim
-    sp = _vector(slots, "slots", dev, torch.int64)
-    shape = positions.shape
-    n_axes = shape[0] if len(shape) == 2 else 1
-    if shape[-1:] != (n,) or len(shape) > 2:
-        raise ValueError(f"positions: expected [{n}] or [axes][{n}], got {tuple(shape)}")
-    pos = _tensor(positions, "positions", dev, torch.int32)
-    if axes is not None and (type(axes) is not bytes or len(axes) != hd // 2):
-        raise ValueError(f"axes: expected {hd // 2} bytes, one per pair")
-    width = n_kv * hd
-    kp, ks = _rows(k, "k", dev, dt, width, n)
-    vp, vs = _rows(v, "v", dev, dt, width, n)
-    if q is None and q_out is None:
-        qp = qs = op = os_ = 0
-    else:
-        width = cfg.n_q * hd
-        qp, qs = _rows(q, "q", dev, dt, width, n)
-        op, os_ = _rows(q_out, "q_out", dev, dt, width, n)
-    ep = _tensor(err, "err", dev, torch.int32)
-    if isinstance(cache, torch.Tensor):
-        pp, pages = _pool(n_kv, hd, cache, dev)
-        if n > 0:
-            st = (_lib or lib()).pe_append_kv_packed(cfg, qp, kp, vp, qs, ks, vs, pos, n_axes, axes, sp, n, op, os_, pp,
-                                                     pages, ep, _raw_stream(stream, dev))
-            if st != PE_OK:
-                raise PeError(st, "pe_append_kv_packed")
-        return
-    kc, vc = cache
-    shape = kc.shape
-    if len(shape) != 4 or shape[1:] != (16, n_kv, hd):
-        raise ValueError(f"k_cache: expected [pages][16][{n_kv}][{hd}], got {tuple(shape)}")
-    kcp = _tensor(kc, "k_cache", dev, dt)
-    vcp = _tensor(vc, "v_cache", dev, dt, shape)
-    if n > 0:
-        st = (_lib or lib()).pe_append_kv(cfg, qp, kp, vp, qs, ks, vs, pos, n_axes, axes, sp, n, op, os_, kcp, vcp,
-                                          shape[0], ep, _raw_stream(stream, dev))
-        if st != PE_OK:
-            raise PeError(st, "pe_append_kv")
+    st = (_bind or _binding()).append_kv(cfg, q, k, v, positions, slots, cache, q_out, err, axes, stream)
+    if st != PE_OK:
+        raise PeError(st, "pe_append_kv_packed" if isinstance(cache, torch.Tensor) else "pe_append_kv")
 
 
 # ----------------------------------------------------------------------------- microscaled (MX) 4-bit matrices
@@ -564,10 +547,10 @@ def mx_bytes(n_rows: int, width: int) -> int:
 
 
 class MxMatrix:
-    """A matrix of n_rows x width entries in microscaled 4-bit floating point, resident on the device (see pe.h): its
-    bytes are ``data``, which stays the tensor it was made with."""
+    """A matrix of n_rows x width entries in microscaled 4-bit floating point, resident on the device (see pe.h); its
+    bytes are ``data``."""
 
-    __slots__ = ("n_rows", "width", "data", "_ptr", "_dev")
+    __slots__ = ("_arg",)
 
     def __init__(self, n_rows: int, width: int, device="cuda", data=None):
         size = mx_bytes(n_rows, width)
@@ -577,8 +560,11 @@ class MxMatrix:
             data = torch.empty(size, dtype=torch.uint8, device=device)
         elif not (data.is_cuda and data.dtype is torch.uint8 and data.is_contiguous() and data.numel() >= size):
             raise ValueError(f"data: expected a contiguous uint8 CUDA tensor of at least {size} bytes")
-        self.n_rows, self.width, self.data = n_rows, width, data
-        self._ptr, self._dev = data.data_ptr(), data.get_device()
+        self._arg = (n_rows, width, data)
+
+    n_rows = property(lambda self: self._arg[0])
+    width = property(lambda self: self._arg[1])
+    data = property(lambda self: self._arg[2])
 
     def first(self, n_rows: int) -> "MxMatrix":
         """The first n_rows rows, in the same memory."""
@@ -587,87 +573,33 @@ class MxMatrix:
         return MxMatrix(n_rows, self.width, data=self.data)
 
 
-def _mx(m, what: str, dev: int) -> int:
-    if m._dev != dev:
-        raise ValueError(f"{what}: expected a matrix on cuda:{dev}, got {m.data.device}")
-    return m._ptr
-
-
-_ROW_TYPES = {torch.bfloat16: PE_BF16, torch.float32: PE_F32}
-
-
-def _any_rows(t, what: str, dev: int, n: int, width: int):
-    """Type (as pe_dtype), address and row stride of n rows of ``width`` fp32 or bf16 elements, each row contiguous."""
-    dt = _ROW_TYPES.get(t.dtype)
-    if dt is not None and t.get_device() == dev and t.shape == (n, width):
-        if t.is_contiguous():
-            return dt, t.data_ptr(), width
-        stride = t.stride()
-        if width <= 1 or n == 0 or stride[1] == 1:
-            return dt, t.data_ptr(), stride[0] if n > 1 else width
-    raise ValueError(f"{what}: expected {n} rows of {width} contiguous fp32 or bf16 elements on cuda:{dev}, got "
-                     f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-
-
 def quantize_mx(x, m: MxMatrix, err, stream=None):
     """Round rows x [n_rows][width] (fp32 or bf16) to 4 bits, into ``m``."""
-    dev, n, width = _current(x), m.n_rows, m.width
-    dt, xp, xs = _any_rows(x, "x", dev, n, width)
-    mp, ep = _mx(m, "m", dev), _tensor(err, "err", dev, torch.int32)
-    if n > 0:
-        st = (_lib or lib()).pe_quantize_mx(dt, xp, xs, n, width, mp, ep, _raw_stream(stream, dev))
-        if st != PE_OK:
-            raise PeError(st, "pe_quantize_mx")
+    st = (_bind or _binding()).quantize_mx(x, m._arg, err, stream)
+    if st != PE_OK:
+        raise PeError(st, "pe_quantize_mx")
 
 
 def dequantize_mx(m: MxMatrix, x, stream=None):
     """Read a matrix back into rows x [n_rows][width] (fp32 or bf16) as the values it stands for."""
-    dev, n, width = _current(x), m.n_rows, m.width
-    dt, xp, xs = _any_rows(x, "x", dev, n, width)
-    mp = _mx(m, "m", dev)
-    if n > 0:
-        st = (_lib or lib()).pe_dequantize_mx(dt, mp, n, width, xp, xs, _raw_stream(stream, dev))
-        if st != PE_OK:
-            raise PeError(st, "pe_dequantize_mx")
-
-
-def _addend(add, dt: int, dev: int, n: int, n_out: int):
-    if add is None:
-        return None, 0
-    adt, ap, as_ = _any_rows(add, "add", dev, n, n_out)
-    if adt != dt:
-        raise ValueError("add: expected y's type")
-    return ap, as_
+    st = (_bind or _binding()).dequantize_mx(m._arg, x, stream)
+    if st != PE_OK:
+        raise PeError(st, "pe_dequantize_mx")
 
 
 def matmul_mx(x: MxMatrix, w: MxMatrix, y, err, add=None, stream=None):
     """y [x.n_rows][w.n_rows] (fp32 or bf16) = add + x . w^T; ``add`` may be y."""
-    dev, n, n_out, width = _current(y), x.n_rows, w.n_rows, w.width
-    if x.width != width:
-        raise ValueError(f"x and w: widths {x.width} and {width} differ")
-    dt, yp, ys = _any_rows(y, "y", dev, n, n_out)
-    ap, as_ = _addend(add, dt, dev, n, n_out)
-    xp, wp, ep = _mx(x, "x", dev), _mx(w, "w", dev), _tensor(err, "err", dev, torch.int32)
-    if n > 0:
-        st = (_lib or lib()).pe_matmul_mx(xp, n, wp, n_out, width, ap, as_, dt, yp, ys, ep, _raw_stream(stream, dev))
-        if st != PE_OK:
-            raise PeError(st, "pe_matmul_mx")
+    st = (_bind or _binding()).matmul_mx(x._arg, w._arg, y, err, add, stream)
+    if st != PE_OK:
+        raise PeError(st, "pe_matmul_mx")
 
 
 def linear_mx(x, w: MxMatrix, y, workspace, err, add=None, stream=None):
     """matmul_mx of rows x [n][w.width] (fp32 or bf16) that are quantised on the way.  ``workspace``:
     alloc_linear_mx_workspace."""
-    dev, n, n_out, width = _current(y), x.shape[0], w.n_rows, w.width
-    xdt, xp, xs = _any_rows(x, "x", dev, n, width)
-    dt, yp, ys = _any_rows(y, "y", dev, n, n_out)
-    ap, as_ = _addend(add, dt, dev, n, n_out)
-    wp, ep = _mx(w, "w", dev), _tensor(err, "err", dev, torch.int32)
-    sp = _vector(workspace, "workspace", dev, torch.uint8)
-    if n > 0:
-        st = (_lib or lib()).pe_linear_mx(xdt, xp, xs, n, wp, n_out, width, ap, as_, dt, yp, ys, sp, workspace.numel(),
-                                          ep, _raw_stream(stream, dev))
-        if st != PE_OK:
-            raise PeError(st, "pe_linear_mx")
+    st = (_bind or _binding()).linear_mx(x, w._arg, y, workspace, err, add, stream)
+    if st != PE_OK:
+        raise PeError(st, "pe_linear_mx")
 
 
 def step(cfg, weights: DeviceWeights, kv, block_table, prev_tokens, prev_pos, num_accepted, bonus,

@@ -1,21 +1,26 @@
 """Build the CUDA library ``libpe.so`` (sm_103a) in-tree with nvcc.
 
 Each translation unit is compiled in parallel, then linked into one shared
-library exposing the C ABI declared in ``include/pe.h``.
+library exposing the C ABI declared in ``include/pe.h``.  ``pe_bind.so``, the Python
+entry of the calls whose arguments would otherwise take longer than their work, is
+compiled beside it against torch's headers.
 """
 
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpe.so")
+BIND = os.path.join(BUILD, "pe_bind.so")
 SOURCES = ["pe_api.cu", "pe_meta.cu", "pe_gemm.cu", "pe_attn.cu", "pe_noalloc.cu", "pe_sample.cu", "pe_packed.cu",
            "pe_packed_attn.cu", "pe_mx.cu", "pe_mx_gemm.cu", "pe_mx_pair.cu", "pe_append.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -31,6 +36,16 @@ def nvcc() -> str:
 def _flags():
     return ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"),
                    "-Xptxas", "-warn-spills"]
+
+
+def _bind_command(out: str):
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(torch, "include"),
+               os.path.join(cuda, "include")]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared"] + [f"-I{d}" for d in include] +
+            [os.path.join(CSRC, "pe_bind.cpp"), "-o", out, "-L" + os.path.join(torch, "lib"), "-ltorch_python",
+             "-ltorch_cpu", "-lc10", "-lc10_cuda"])
 
 
 def _stale(target: str, deps) -> bool:
@@ -56,14 +71,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"compiling failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    bind_tmp = BIND + f".tmp{os.getpid()}"
+    bind = force or _stale(BIND, [os.path.join(CSRC, "pe_bind.cpp"), os.path.join(ROOT, "include", "pe.h")])
+    if bind:
+        jobs.append(_bind_command(bind_tmp))
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         for log in ex.map(run, jobs):
             if verbose and log:
                 print(log)
-    if force or jobs or _stale(LIB, objs):
+    if bind:
+        os.replace(bind_tmp, BIND)
+    if _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs)
         os.replace(tmp, LIB)
