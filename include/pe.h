@@ -621,7 +621,7 @@ uint64_t pe_kernel_launches(void);
 /*
  * Failure detection.  Inside a CTA the pipeline roles (copy issue, MMA issue,
  * softmax, epilogue) wait on each other through shared-memory barriers; no CTA
- * ever waits for another CTA.  Every such wait gives up after a time limit:
+ * ever waits for one outside its cluster.  Every such wait gives up after a time limit:
  * it records PE_DEV_TIMEOUT in *err_word, raises the CTA's abort flag (the
  * CTA's other roles stop waiting), waits for the CTA's own copies and MMAs in
  * flight, frees its tensor memory and returns; the rest of the call's kernels
@@ -635,7 +635,7 @@ pe_status pe_set_wait_limit_ns(uint64_t ns);
 
 /*
  * Test hook of the wait-expiry path above (for failure-detection tests only).
- * The next tensor-core GEMM launch (bf16 configs), from any thread, leaves
+ * The next tensor-core GEMM launch (bf16 configs, 4-bit products), from any thread, leaves
  * pipeline stage `stage` of its first CTA unarmed: no copy is issued into it
  * and no byte count is expected on its barrier, so the MMA role's wait on it
  * runs out after the wait limit.  One-shot: the launch that applies it clears
