@@ -60,7 +60,7 @@ PE_DEV MxUnit mx_unit(const MxMatmulArgs& a, const MxPlan& p, int u) {
 }
 
 // Rows of x into shared memory in 4 bits: pieces p0..p1 - 1 of all bn rows, x_piece bytes each (a record's scales and its
-// first rows), by `warps` warps of which this is the w-th.  Rows beyond the last become zeros.
+// first rows), by `warps` warps of which this is the w-th.  Rows beyond the last are zeros, or (records) as they are.
 PE_DEV void keep_records(const MxMatmulArgs& a, const MxPlan& p, uint8_t* xs, int p0, int p1, int w, int warps, int lane) {
   const uint32_t chunks = p.x_piece / 16;
   for (int k = p0 + w; k < p1; k += warps) {
@@ -104,6 +104,63 @@ PE_DEV void keep_rows(const MxMatmulArgs& a, const MxPlan& p, uint8_t* xs, int p
   if (bad) set_err(a.err, PE_DEV_NONFINITE);
 }
 
+// A cluster's one unit: its CTAs exchange their partial sums (through `recv`, in the place of the stages) and write their
+// shares of the columns, quad by quad.
+template <typename T>
+PE_DEV void mx_join(const MxMatmulArgs& a, const MxPlan& p, const MxUnit& w, int rank, uint32_t tmem, uint8_t* recv,
+                    volatile int* abort_flag) {
+  constexpr int HALVES = (kMxgThreads / 32 - 4) / 4;  // warps of a lane quarter
+  const int warp = threadIdx.x >> 5, r = threadIdx.x & 127, h = (warp - 4) >> 2;  // row of w, and which columns
+  const int quads = w.cols / 4, share = (quads + p.cluster - 1) / p.cluster;
+  __syncthreads();
+  cluster_sync();
+  if (warp >= 4 && !*abort_flag) {
+    const uint32_t tl = tmem + ((uint32_t)(r & ~31) << 16);
+    // to [rank][quad of the owner's][row of w], 16 bytes each
+    const uint32_t mine = smem_u32(recv) + (uint32_t)(rank * share * kMxPiece + r) * 16;
+    for (int c = h; c < w.cols / 16; c += HALVES) {
+      float v[16];
+      tmem_load16(tl + (uint32_t)(c * 16), v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int owner = (4 * c + j) / share, at = 4 * c + j - owner * share;
+        st_cluster_v4(mapa_shared(mine + (uint32_t)(at * kMxPiece) * 16, (uint32_t)owner), v[4 * j], v[4 * j + 1],
+                      v[4 * j + 2], v[4 * j + 3]);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync();  // every partial sum is where it is summed
+  const int f = w.tile_f * kMxPiece + r, n = min(share, quads - rank * share);
+  if (warp < 4 || *abort_flag || f >= a.n_out) return;
+  const float4* part = reinterpret_cast<const float4*>(recv) + r;
+  for (int c = h; c < n; c += HALVES) {
+    const int t0 = w.row0 + 4 * (rank * share + c);
+    float4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < p.cluster) x[k] = part[(k * share + c) * kMxPiece];
+    float old[4], v[4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      old[j] = a.add == nullptr ? 0.f
+                                : to_float<T>(static_cast<const T*>(
+                                      a.add)[(long long)min(t0 + j, a.n_rows - 1) * a.add_stride + f]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < p.cluster) {
+        v[0] += x[k].x;
+        v[1] += x[k].y;
+        v[2] += x[k].z;
+        v[3] += x[k].w;
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (t0 + j < a.n_rows) static_cast<T*>(a.y)[(long long)(t0 + j) * a.y_stride + f] = from_float<T>(v[j] + old[j]);
+  }
+}
+
 // Roles: one thread copies weights (warp 0), one x (warp 2), one issues the MMAs (warp 1); the other warps
 // bring in x where it is kept and write results.
 template <typename T, int SRC>
@@ -127,7 +184,6 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued_max = abort_flag + 1;  // [4], by warp
   volatile int* last_flag = issued_max + 4;
-  float* recv = reinterpret_cast<float*>(smem);  // clusters, after the MMAs: [rank][quads of columns of this CTA][128][4]
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -339,64 +395,8 @@ __global__ void __launch_bounds__(kMxgThreads, 1) mx_gemm_kernel(const MxMatmulA
   }
 
   if constexpr (!ARGMAX)
-  if (p.cluster > 1) {
-    // the cluster's one unit: every CTA's MMAs are done (or given up), so the stages' memory takes the partial sums
-    const MxUnit w = mx_unit(a, p, first);
-    const int quads = w.cols / 4, share = (quads + p.cluster - 1) / p.cluster;  // quads of columns that each CTA sums
-    __syncthreads();
-    cluster_sync();
-    if (warp >= 4 && !*abort_flag) {
-      const int q = warp & 3, h = (warp - 4) >> 2, r = q * 32 + lane;
-      const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
-      // to [rank][quad of the owner's][row of w], 16 bytes each
-      const uint32_t mine = smem_u32(recv) + (uint32_t)(rank * share * kMxPiece + r) * 16;
-      for (int c = h; c < w.cols / 16; c += EW / 4) {
-        float v[16];
-        tmem_load16(tl + (uint32_t)(c * 16), v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int owner = (4 * c + j) / share, at = 4 * c + j - owner * share;
-          st_cluster_v4(mapa_shared(mine + (uint32_t)(at * kMxPiece) * 16, (uint32_t)owner), v[4 * j], v[4 * j + 1],
-                        v[4 * j + 2], v[4 * j + 3]);
-        }
-      }
-      tc_fence_before();
-    }
-    __syncwarp();
-    cluster_sync();  // every partial sum is where it is summed
-    if (warp >= 4 && !*abort_flag) {
-      const int r = (warp & 3) * 32 + lane, h = (warp - 4) >> 2;
-      const int f = w.tile_f * kMxPiece + r, n = min(share, quads - rank * share);
-      const float4* part = reinterpret_cast<const float4*>(recv) + r;
-      if (f < a.n_out)
-        for (int c = h; c < n; c += EW / 4) {
-          const int t0 = w.row0 + 4 * (rank * share + c);
-          float v[4] = {};
-          float4 x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < p.cluster) x[k] = part[(k * share + c) * kMxPiece];
-          float old[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            old[j] = a.add == nullptr ? 0.f
-                                      : to_float<T>(static_cast<const T*>(
-                                            a.add)[(long long)min(t0 + j, a.n_rows - 1) * a.add_stride + f]);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < p.cluster) {
-              v[0] += x[k].x;
-              v[1] += x[k].y;
-              v[2] += x[k].z;
-              v[3] += x[k].w;
-            }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (t0 + j < a.n_rows)
-              static_cast<T*>(a.y)[(long long)(t0 + j) * a.y_stride + f] = from_float<T>(v[j] + old[j]);
-        }
-    }
-  }
+    if (p.cluster > 1)  // every CTA's MMAs are done (or given up), so the stages' memory takes the partial sums
+      mx_join<T>(a, p, mx_unit(a, p, first), rank, tmem, smem, abort_flag);
 
   __syncthreads();
   if (*abort_flag) {

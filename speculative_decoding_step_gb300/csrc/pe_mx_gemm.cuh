@@ -181,12 +181,12 @@ struct MxOut {
 template <>
 struct MxOut<MxArgmax> {
   const MxMatmulArgs& a;
-  int f, lane;
-  const float* seen;  // mx_seen's, as if from row 0 on
-  PE_DEV MxOut(const MxMatmulArgs& args, int feature, int row0, const float* s)
-      : a(args), f(feature), lane(threadIdx.x & 31), seen(s - row0) {}
+  int f, lane, row0;
+  const float* seen;  // mx_seen's
+  PE_DEV MxOut(const MxMatmulArgs& args, int feature, int first_row, const float* s)
+      : a(args), f(feature), lane(threadIdx.x & 31), row0(first_row), seen(s) {}
   PE_DEV void put(int t0, int, bool some, float (&v)[16]) {
-    if (some) mx_argmax(a, f, t0, v, seen + t0, lane);
+    if (some) mx_argmax(a, f, t0, v, seen + (t0 - row0), lane);
   }
 };
 

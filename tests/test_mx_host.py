@@ -203,3 +203,18 @@ def test_drafter_calls_with_a_4_bit_head_refuse_before_launch(name):
     for i in range(7):
         assert call(drop=i) == 1
     assert call(weights=pe._Weights(AT, AT, None, layer, layer, layer, layer, layer, layer, AT, None)) == 1
+
+
+def test_the_binding_refuses_what_is_no_gpu_tensor_or_no_matrix():
+    m, err = pe.MxMatrix(2, 32, device="cpu"), torch.zeros(1, dtype=torch.int32)
+    x = torch.zeros(2, 32)
+    calls = [lambda: pe.quantize_mx(x, m, err), lambda: pe.dequantize_mx(m, x), lambda: pe.matmul_mx(m, m, x, err),
+             lambda: pe.linear_mx(x, m, x, m.data, err), lambda: pe.quantize_mx(None, m, err),
+             lambda: pe.linear_mx([1.0], m, 3, m.data, err),
+             lambda: pe.append_kv(_cfg(), x, x, x, err, torch.zeros(2, dtype=torch.int64), (x, x), x, err),
+             lambda: pe.append_kv(_cfg(), x, x, x, err, None, (x, x), x, err)]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises((TypeError, ValueError)):
+        pe.append_kv(b"12", x, x, x, err, torch.zeros(2, dtype=torch.int64), (x, x), x, err)
