@@ -363,31 +363,6 @@ PE_DEV void cluster_sync() {
 PE_DEV void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// Wait for phase `parity` of an mbarrier that a thread of another CTA of the cluster arrives on (bounded as mbar_wait).
-PE_DEV bool mbar_wait_cluster(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort, uint64_t limit_ns) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 0;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((i & 63u) == 0) {
-      if (abort != nullptr && *abort) return false;
-      const uint64_t now = global_timer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > limit_ns) {
-        set_err(err, PE_DEV_TIMEOUT);
-        if (abort != nullptr) *abort = 1;
-        return false;
-      }
-    }
-  }
-}
 PE_DEV void tmem_alloc_cg2(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
                : "memory");
