@@ -88,6 +88,24 @@ def test_append_against_the_definition(dtype, axes, theta, n, n_q, n_kv, hd):
     assert np.array_equal(kg[rest], kb[rest]) and np.array_equal(vg[rest], vb[rest])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_largest_number_of_heads_and_axes(dtype):
+    rng = np.random.default_rng(4)
+    n, n_q, n_kv, hd = 3, 4096, 512, 128
+    cfg = _cfg(n_q, n_kv, hd, dtype)
+    _, q, k, v = _rows(rng, n, n_q, n_kv, hd, dtype)
+    positions, axis = rng.integers(0, 5000, (8, n)).astype(np.int32), rng.integers(0, 8, hd // 2)
+    kc, vc = (torch.zeros((1, 16, n_kv, hd), device="cuda", dtype=DT[dtype]) for _ in range(2))
+    out, err = torch.empty((n, n_q * hd), device="cuda", dtype=DT[dtype]), _err()
+    pe.append_kv(cfg, q, k, v, torch.from_numpy(positions).cuda(), torch.arange(n, device="cuda"), (kc, vc), out, err,
+                 axes=bytes(axis.tolist()))
+    assert int(err.item()) == 0 and torch.equal(vc[0, :n].flatten(1), v)
+    for got, x, h in ((out, q, n_q), (kc[0, :n], k, n_kv)):
+        xn = _np(x).reshape(n, h, hd)
+        want = mx.rotated(xn, positions, axis, 1e4)
+        assert (np.abs(_np(got).reshape(n, h, hd) - want) <= _tol(xn, positions, axis, 1e4, dtype, want)).all()
+
+
 @pytest.mark.parametrize("hd", [64, 128])
 def test_far_and_negative_positions(hd):
     rng = np.random.default_rng(hd)

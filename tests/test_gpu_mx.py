@@ -292,6 +292,66 @@ def test_rows_do_not_depend_on_their_neighbours_bytes():
     _compare(_np(z), x, wt[256:], None, "f32")
 
 
+def test_the_largest_sizes():
+    err = _err()
+    rows = 1 << 24                                             # one entry a row: each is kept as the block's largest
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.tensor([0.0, 4.0, -5.0, 6.0, 7.0, 96.0], device="cuda")[torch.randint(0, 6, (rows, 1), device="cuda",
+                                                                                   generator=g)]
+    m = pe.MxMatrix(rows, 1)
+    pe.quantize_mx(x, m, err)
+    back = torch.empty_like(x)
+    pe.dequantize_mx(m, back)
+    kept = torch.where(x == -5.0, -4.0, torch.where(x == 7.0, 6.0, x))  # -5 and 7 lie between 4 and 6, and 6 and 8
+    assert torch.equal(back, kept)
+    y = torch.empty((rows, 1), device="cuda")
+    pe.matmul_mx(m, _mx(np.array([[3.0]])), y, err)
+    assert torch.equal(y, 3 * kept)
+    del m, x, back, kept, y
+    width = 1 << 20
+    rng = np.random.default_rng(9)
+    x, wt = rng.choice([-1.0, 0.0, 1.0], (3, width)), rng.choice([-0.5, 0.5, 1.0], (5, width))
+    x[:, ::32], wt[:, ::32] = 4.0, 4.0
+    y = torch.empty((3, 5), device="cuda")
+    pe.matmul_mx(_mx(x), _mx(wt), y, err)                      # multiples of 1/2 below 2^21: exact in any order
+    assert np.array_equal(_np(y), x @ wt.T) and int(err.item()) == 0
+
+
+def test_a_matrix_times_itself():
+    rng = np.random.default_rng(12)
+    for n, w in ((20, 300), (200, 1000)):
+        x, _ = _product_case(rng, n, 1, w, True)
+        m, y, err = _mx(x), torch.empty((n, n), device="cuda"), _err()
+        pe.matmul_mx(m, m, y, err)
+        assert np.array_equal(_np(y), x @ x.T) and int(err.item()) == 0
+
+
+def test_products_on_two_streams_at_once():
+    """Kept rows, tiles of a CTA, of a cluster and of a pair, each beside the others, on the same matrices."""
+    err = _err()
+    g = torch.Generator(device="cuda").manual_seed(8)
+    cases = []
+    for n, m, w in ((8, 20000, 2880), (128, 4000, 2000), (100, 300, 8192), (1000, 8192, 2048)):
+        x, wm = pe.MxMatrix(n, w), pe.MxMatrix(m, w)
+        pe.quantize_mx(torch.randn(n, w, device="cuda", generator=g), x, err)
+        pe.quantize_mx(torch.randn(m, w, device="cuda", generator=g), wm, err)
+        want = torch.empty((n, m), device="cuda")
+        pe.matmul_mx(x, wm, want, err)
+        cases.append((x, wm, want))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(24):
+        for k, s in enumerate(streams):
+            x, wm, want = cases[(i + k) % len(cases)]
+            with torch.cuda.stream(s):
+                y = torch.empty_like(want)
+            pe.matmul_mx(x, wm, y, err, stream=s)
+            got.append((y, want))
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and all(torch.equal(y, want) for y, want in got)
+
+
 def test_scale_bytes_that_stand_for_nan_and_extremes():
     rng = np.random.default_rng(8)
     x, wt = _product_case(rng, 3, 130, 160, True)
