@@ -146,7 +146,8 @@ def test_in_place_without_queries_and_bad_slots(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("n,n_q,n_kv,hd", [(1, 2, 1, 64), (37, 64, 8, 64), (130, 12, 3, 128), (300, 5, 5, 64)])
+@pytest.mark.parametrize("n,n_q,n_kv,hd", [(1, 2, 1, 64), (37, 64, 8, 64), (130, 12, 3, 128), (300, 5, 5, 64), (4100, 20, 20, 128),
+                                          (9000, 40, 40, 64)])
 def test_packed_append_is_append_then_pack(dtype, n, n_q, n_kv, hd):
     rng = np.random.default_rng(n + hd)
     cfg = _cfg(n_q, n_kv, hd, dtype)
