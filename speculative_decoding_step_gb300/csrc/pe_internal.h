@@ -450,5 +450,7 @@ int mx_pair_clusters(int sms);
 bool tmap_mx(CUtensorMap* m, const uint8_t* base, uint64_t records, uint32_t rows);
 // Whether the product of this many rows quantises them itself (rows at 16-byte boundaries), without a launch before it.
 bool mx_matmul_quantises(int n_rows, int n_out, int width, bool head, int sms);
+// Dynamic shared memory of a CTA of the product's kernel for few rows, and the CTAs that share a tile (the tests ask for it).
+size_t mx_matmul_smem(int n_rows, int n_out, int width, int sms, int* cluster);
 
 }  // namespace pe

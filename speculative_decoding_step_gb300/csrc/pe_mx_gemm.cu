@@ -43,6 +43,13 @@ constexpr int kMxgKeepRows = 64;             // rows of x that are kept at most 
 constexpr int kMxgKeepPieces = 64;           // pieces of x that are kept at most (256 columns of scales)
 constexpr uint32_t kMxgKeepBytes = 96 * 1024;
 
+// Shared memory that a CTA of a cluster asks for at least: more than half of an SM's (228 KB, a CTA's own 1 KB of it
+// included), so that no SM has two of them.  A CTA holds all of its SM's tensor memory while it waits for its cluster; two
+// clusters (calls on two streams) that each have a CTA waiting for tensor memory which the other's holds would never end.
+// (Pairs of CTAs, here and of the drafter's GEMMs, take nearly all of an SM's shared memory, so none fits beside it either.)
+constexpr size_t kMxgClusterSmem = 116 * 1024;
+static_assert(2 * (kMxgClusterSmem + 1024) > 228 * 1024, "two CTAs do not fit an SM");
+
 PE_DEV void st_cluster_v4(uint32_t addr, float x, float y, float z, float w) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
@@ -499,6 +506,7 @@ MxPlan plan_mx(const MxMatmulArgs& a, int sms) {
   p.x_col = 256;
   p.grid = p.cluster * (int)std::min<long long>(units, p.cluster > 1 ? units : sms);
   p.smem = 128 + (size_t)p.ring_bytes + p.x_bytes + kMxgCtrl;
+  if (p.cluster > 1) p.smem = std::max(p.smem, kMxgClusterSmem);
   return p;
 }
 
@@ -553,6 +561,14 @@ bool mx_matmul_quantises(int n_rows, int n_out, int width, bool head, int sms) {
   a.n_rows = n_rows; a.n_out = n_out; a.width = width; a.head.keys = head ? &key : nullptr;
   const MxPlan p = plan_mx(a, sms);
   return p.src == SRC_RECORDS && (long long)p.bn * ((p.pieces + p.cluster - 1) / p.cluster) * kMxPiece <= 12288;
+}
+
+size_t mx_matmul_smem(int n_rows, int n_out, int width, int sms, int* cluster) {
+  MxMatmulArgs a{};
+  a.n_rows = n_rows; a.n_out = n_out; a.width = width;
+  const MxPlan p = plan_mx(a, sms);
+  *cluster = p.cluster;
+  return p.smem;
 }
 
 // More than 128 rows go to pairs of CTAs where those are expected to take less: about 0.17 us a piece of their 256 x 256
