@@ -503,7 +503,8 @@ pe_status pe_inject_kv_packed(const pe_config *cfg, const pe_weights *w, const v
  * the cache sets PE_DEV_BAD_PAGE and the row's key and value are passed over.  Non-finite entries spread to their pair.
  * Reads n_q, n_kv, head_dim, dtype and rope_theta of *cfg; the fields that the packed calls read have to pass their checks.
  * Strides as there.  q_out must share no byte with k or v, nor the caches with any of the rows or each other; rows side
- * by side in one buffer, with one stride, share none.  n_rows = 0: nothing is launched.
+ * by side in one buffer, with one stride, share none.  Neither q_out nor a cache may share a byte with positions or slots.
+ * n_rows = 0: nothing is launched.
  *
  * pe_append_kv_packed packs the rotated keys, rounded to cfg->dtype, and the values as pe_pack_kv does, with its
  * device checks (two launches where there are queries).

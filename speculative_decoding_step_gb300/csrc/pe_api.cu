@@ -568,6 +568,15 @@ bool rows_apart(const ByteRows& x, const ByteRows& y) {
   return d >= x.row && d + y.row <= x.stride;
 }
 
+// Whether a byte range meets one of the rows (one that lies between two rows does not).
+bool meets_rows(const Span& s, const ByteRows& r) {
+  if (!overlaps(s, r.span())) return false;
+  const uintptr_t base = reinterpret_cast<uintptr_t>(r.p);
+  const int64_t i = s.lo < base ? 0 : (int64_t)(s.lo - base) / r.stride;  // the row at or before the range's start
+  const uintptr_t at = base + (uintptr_t)(i * r.stride);
+  return overlaps(s, Span{at, at + (uintptr_t)r.row}) || (i + 1 < r.n && at + (uintptr_t)r.stride < s.hi);
+}
+
 // ----------------------------------------------------------------------------- MX matrices
 
 constexpr int kMaxMxRows = 1 << 24;   // rows of a matrix
@@ -682,6 +691,19 @@ pe_status check_append(const pe_config* cfg, const void* q, const void* k, const
   return PE_OK;
 }
 
+// Rows are turned and placed by CTAs that do not wait for one another, so no output may lie over positions or slots.
+pe_status check_append_indices(const pe_config& c, const int32_t* positions, int32_t n_axes, const int64_t* slots,
+                               int32_t n_rows, const void* q_out, int64_t q_out_stride, const Span& cache) {
+  if (n_rows == 0) return PE_OK;
+  const Span in[2] = {span_of(positions, (size_t)n_axes * n_rows * sizeof(int32_t)),
+                      span_of(slots, (size_t)n_rows * sizeof(int64_t))};
+  for (const Span& s : in)
+    if (overlaps(cache, s) ||
+        (q_out != nullptr && meets_rows(s, byte_rows(c.dtype, q_out, q_out_stride, (int64_t)c.n_q * c.head_dim, n_rows))))
+      return PE_ERR_INVALID_ARG;
+  return PE_OK;
+}
+
 AppendArgs make_append_args(const pe_config& c, const void* q, int64_t q_stride, const int32_t* positions,
                             const uint8_t* axis_of_pair, const int64_t* slots, int32_t n_rows, void* q_out,
                             int64_t q_out_stride, int32_t num_pages, int32_t* err) {
@@ -692,7 +714,7 @@ AppendArgs make_append_args(const pe_config& c, const void* q, int64_t q_stride,
   return a;
 }
 
-// Whether none of the byte ranges that a call writes meets one that it reads (rows k and v, positions, slots).
+// Whether a cache that a call writes shares no byte with its rows (positions and slots: check_append_indices).
 bool append_cache_apart(const pe_config& c, const Span& cache, const void* q, int64_t q_stride, const void* k,
                         int64_t k_stride, const void* v, int64_t v_stride, const void* q_out, int64_t q_out_stride,
                         int32_t n_rows) {
@@ -1439,6 +1461,8 @@ pe_status pe_append_kv(const pe_config* cfg, const void* q, const void* k, const
       !append_cache_apart(*cfg, kc, q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, n_rows) ||
       !append_cache_apart(*cfg, vc, q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, n_rows))
     return PE_ERR_INVALID_ARG;
+  for (const Span& cache : {kc, vc})
+    if ((st = check_append_indices(*cfg, positions, n_axes, slots, n_rows, q_out, q_out_stride, cache)) != PE_OK) return st;
   if (n_rows == 0) return PE_OK;
   AppendArgs a = make_append_args(*cfg, q, q_stride, positions, axis_of_pair, slots, n_rows, q_out, q_out_stride,
                                   num_pages, err_word);
@@ -1459,6 +1483,7 @@ pe_status pe_append_kv_packed(const pe_config* cfg, const void* q, const void* k
   const Span ps = span_of(pool, (size_t)num_pages * cfg->n_kv * 18 * cfg->head_dim);
   if (!append_cache_apart(*cfg, ps, q, q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, n_rows))
     return PE_ERR_INVALID_ARG;
+  if ((st = check_append_indices(*cfg, positions, n_axes, slots, n_rows, q_out, q_out_stride, ps)) != PE_OK) return st;
   if (n_rows == 0) return PE_OK;
   const AppendArgs a = make_append_args(*cfg, q, q_stride, positions, axis_of_pair, slots, n_rows, q_out,
                                         q_out_stride, num_pages, err_word);
