@@ -541,9 +541,16 @@ def append_kv(cfg, q, k, v, positions, slots, cache, q_out, err, axes=None, stre
 
 # ----------------------------------------------------------------------------- microscaled (MX) 4-bit matrices
 
+def _mx_size(call: str, n_rows: int, width: int) -> int:
+    # ctypes keeps the lower 32 bits of a number
+    if not (0 <= n_rows < 1 << 31 and 0 <= width < 1 << 31):
+        return 0
+    return int(getattr(lib(), call)(n_rows, width))
+
+
 def mx_bytes(n_rows: int, width: int) -> int:
     """Bytes of a microscaled 4-bit matrix (0: sizes out of range)."""
-    return int(lib().pe_mx_bytes(n_rows, width))
+    return _mx_size("pe_mx_bytes", n_rows, width)
 
 
 class MxMatrix:
@@ -667,7 +674,7 @@ def alloc_mx_head_workspace(cfg: Config, device="cuda") -> torch.Tensor:
 
 def alloc_linear_mx_workspace(n_rows: int, width: int, device="cuda") -> torch.Tensor:
     """Workspace of linear_mx for up to n_rows rows of this width."""
-    n = int(lib().pe_linear_mx_workspace_bytes(n_rows, width))
+    n = _mx_size("pe_linear_mx_workspace_bytes", n_rows, width)
     if n == 0 and n_rows != 0:
         raise PeError(2, "pe_linear_mx_workspace_bytes")
     return torch.empty(n, dtype=torch.uint8, device=device)
