@@ -123,14 +123,15 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const MxRowsArg
       using Bits = typename BitsOf<T>::type;
       float* tile = tiles[at.warp];
       // Loaded together, each is a trip to memory: what is not there is read from another place, since loads under a
-      // condition wait for each other (16-bit ones: 24.9 us for 2316 x 6919 instead of 12.2).
+      // condition wait for each other (16-bit ones: 24.9 us for 2316 x 6919 instead of 12.2).  Plain loads: the kernel before
+      // this one may still write x when this one starts, which the read-only path does not allow.
       Bits raw[8][4];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const long long row = min(at.row0 + j, (long long)a.n_rows - 1);
         const Bits* p = reinterpret_cast<const Bits*>(static_cast<const T*>(a.x) + row * a.stride + (size_t)piece * kMxPiece);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) raw[j][e] = __ldg(p + min(e * 32 + lane, left - 1));
+        for (int e = 0; e < 4; ++e) raw[j][e] = p[min(e * 32 + lane, left - 1)];
       }
       __syncwarp();
 #pragma unroll
