@@ -248,6 +248,15 @@ PyObject* linear_mx(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+struct Ref {  // a reference of this call's own
+  PyObject* o;
+  explicit Ref(PyObject* p) : o(p) {
+    if (p == nullptr) throw Refused();
+  }
+  Ref(const Ref&) = delete;
+  ~Ref() { Py_DECREF(o); }
+};
+
 // append_kv(cfg, q, k, v, positions, slots, cache, q_out, err, axes, stream)
 struct ConfigView {  // the pe_config that a ctypes structure holds
   Py_buffer b;
@@ -303,14 +312,13 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       });
     }
     if (!PySequence_Check(a[6]) || PySequence_Size(a[6]) != 2) refuse("cache", "a pool, or keys and values");
+    // (a sequence may make its items when it is asked for them, and keep none)
+    const Ref items[2] = {Ref(PySequence_GetItem(a[6], 0)), Ref(PySequence_GetItem(a[6], 1))};
     void* at_[2];
     int32_t pages = 0;
     for (int i = 0; i < 2; ++i) {
-      PyObject* item = PySequence_GetItem(a[6], i);  // (the sequence keeps it)
-      if (item == nullptr) throw Refused();
-      Py_DECREF(item);
       const char* what = i == 0 ? "k_cache" : "v_cache";
-      const at::Tensor& t = whole(item, what, dev, type);
+      const at::Tensor& t = whole(items[i].o, what, dev, type);
       if (t.dim() != 4 || t.size(1) != 16 || t.size(2) != c.n_kv || t.size(3) != c.head_dim || t.size(0) > INT32_MAX ||
           (i == 1 && t.size(0) != pages))
         refuse(what, "[pages][16][" + std::to_string(c.n_kv) + "][" + std::to_string(c.head_dim) + "]", t);
