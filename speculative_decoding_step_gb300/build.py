@@ -3,7 +3,7 @@
 Each translation unit is compiled in parallel, then linked into one shared
 library exposing the C ABI declared in ``include/pe.h``.  ``pe_bind.so``, the Python
 entry of the calls whose arguments would otherwise take longer than their work, is
-compiled beside it against torch's headers.
+compiled beside it against torch's headers (without torch the library is built alone).
 """
 
 from __future__ import annotations
@@ -38,8 +38,13 @@ def _flags():
                    "-Xptxas", "-warn-spills"]
 
 
-def _bind_command(out: str):
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+def _torch():
+    """Where torch is installed; None where it is not."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec is not None else None
+
+
+def _bind_command(torch: str, out: str):
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     include = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(torch, "include"),
                os.path.join(cuda, "include")]
@@ -74,10 +79,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"compiling failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    bind_tmp = BIND + f".tmp{os.getpid()}"
-    bind = force or _stale(BIND, [os.path.join(CSRC, "pe_bind.cpp"), os.path.join(ROOT, "include", "pe.h")])
+    bind_tmp, torch = BIND + f".tmp{os.getpid()}", _torch()
+    # (a C caller needs libpe.so alone, and no torch)
+    bind = torch is not None and (force or _stale(BIND, [os.path.join(CSRC, "pe_bind.cpp"),
+                                                         os.path.join(ROOT, "include", "pe.h")]))
     if bind:
-        jobs.append(_bind_command(bind_tmp))
+        jobs.append(_bind_command(torch, bind_tmp))
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         for log in ex.map(run, jobs):
             if verbose and log:
