@@ -16,7 +16,7 @@ import os
 
 import torch
 
-from .build import BIND, LIB, build
+from .build import BIND, LIB, bind_is_current, build
 
 __all__ = [
     "PeError", "Config", "DeviceWeights", "DeviceKV", "DevicePackedKV", "lib", "build", "check_config", "workspace_bytes",
@@ -517,7 +517,7 @@ def _binding():
     global _bind
     if _bind is None:
         L = lib()
-        if not os.path.exists(BIND):
+        if not bind_is_current():
             build()
         spec = importlib.util.spec_from_file_location("pe_bind", BIND)
         m = importlib.util.module_from_spec(spec)

@@ -9,6 +9,7 @@ compiled beside it against torch's headers (without torch the library is built a
 from __future__ import annotations
 
 import concurrent.futures
+import contextlib
 import importlib.util
 import os
 import shutil
@@ -21,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpe.so")
 BIND = os.path.join(BUILD, "pe_bind.so")
+BIND_FOR = os.path.join(BUILD, "pe_bind.for")  # the torch and the Python that it was compiled against
 SOURCES = ["pe_api.cu", "pe_meta.cu", "pe_gemm.cu", "pe_attn.cu", "pe_noalloc.cu", "pe_sample.cu", "pe_packed.cu",
            "pe_packed_attn.cu", "pe_mx.cu", "pe_mx_gemm.cu", "pe_mx_pair.cu", "pe_append.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -53,6 +55,21 @@ def _bind_command(torch: str, out: str):
              "-ltorch_cpu", "-lc10", "-lc10_cuda"])
 
 
+def _bind_for(torch: str) -> str:
+    """What pe_bind.so is good for: it reads tensors' fields at the places that these headers give them."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return "\n".join([torch, sysconfig.get_config_var("SOABI") or "", f.read()])
+
+
+def bind_is_current() -> bool:
+    """Whether pe_bind.so is there and was compiled against this torch and this Python."""
+    torch = _torch()
+    if torch is None or not os.path.exists(BIND) or not os.path.exists(BIND_FOR):
+        return False
+    with open(BIND_FOR) as f:
+        return f.read() == _bind_for(torch)
+
+
 def _stale(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -81,8 +98,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     bind_tmp, torch = BIND + f".tmp{os.getpid()}", _torch()
     # (a C caller needs libpe.so alone, and no torch)
-    bind = torch is not None and (force or _stale(BIND, [os.path.join(CSRC, "pe_bind.cpp"),
-                                                         os.path.join(ROOT, "include", "pe.h")]))
+    bind = torch is not None and (force or not bind_is_current() or
+                                  _stale(BIND, [os.path.join(CSRC, "pe_bind.cpp"), os.path.join(ROOT, "include", "pe.h")]))
     if bind:
         jobs.append(_bind_command(torch, bind_tmp))
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
@@ -90,7 +107,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if verbose and log:
                 print(log)
     if bind:
+        # (a build that ends between these two compiles it again)
+        with contextlib.suppress(FileNotFoundError):
+            os.remove(BIND_FOR)
         os.replace(bind_tmp, BIND)
+        with open(bind_tmp, "w") as f:
+            f.write(_bind_for(torch))
+        os.replace(bind_tmp, BIND_FOR)
     if _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs)
