@@ -494,8 +494,9 @@ pe_status pe_inject_kv_packed(const pe_config *cfg, const pe_weights *w, const v
  * (x1, x2) = (x[i], x[i + head_dim/2]), becomes
  *   (x1 cos a - x2 sin a, x2 cos a + x1 sin a),   a = positions[axis][r] * rope_theta^(-2i/head_dim),
  * axis = axis_of_pair[i] (a host array of head_dim/2 entries, read during the call; null: axis 0 for every pair).
- * positions [n_axes][n_rows], 1 to 8 axes (time, height, width of pictures and video), any 32-bit value: the angle's
- * remainder is exact, so far positions lose nothing.  Queries go to q_out (q and q_out both null: no queries),
+ * positions [n_axes][n_rows], 1 to 8 axes (time, height, width of pictures and video), any 32-bit value: an angle is off by
+ * at most 2^-51 of positions * rope_theta^(-2i/head_dim) (10^-6 at the farthest), besides fp32's rounding of its remainder.
+ * Queries go to q_out (q and q_out both null: no queries),
  * which may be q itself (the same pointer and stride); keys and the values v, as they are, to
  *   k_cache, v_cache [num_pages][16][n_kv][head_dim]   at slots[r] = page * 16 + position % 16
  * (int64; -1: the row's key and value are passed over, its query is not).  Slots other than -1 must differ: of two

@@ -43,10 +43,11 @@ constexpr int kMxgKeepRows = 64;             // rows of x that are kept at most 
 constexpr int kMxgKeepPieces = 64;           // pieces of x that are kept at most (256 columns of scales)
 constexpr uint32_t kMxgKeepBytes = 96 * 1024;
 
-// Shared memory that a CTA of a cluster asks for at least: more than half of an SM's (228 KB, a CTA's own 1 KB of it
-// included), so that no SM has two of them.  A CTA holds all of its SM's tensor memory while it waits for its cluster; two
-// clusters (calls on two streams) that each have a CTA waiting for tensor memory which the other's holds would never end.
-// (Pairs of CTAs, here and of the drafter's GEMMs, take nearly all of an SM's shared memory, so none fits beside it either.)
+// Shared memory that a CTA of a cluster asks for at least: more than half of an SM's (228 KB, with 1 KB of its own for every
+// CTA), so that no SM has two of them.  Such a CTA holds all of its SM's tensor memory until its cluster has joined its
+// parts, and an allocation waits without a limit: of two clusters (calls on two streams), each with a CTA that waits for
+// tensor memory which a CTA of the other holds, neither would end.  (Pairs of CTAs, here and in the drafter's GEMMs, take
+// nearly all of an SM's shared memory, so none fits beside one either.)
 constexpr size_t kMxgClusterSmem = 116 * 1024;
 static_assert(2 * (kMxgClusterSmem + 1024) > 228 * 1024, "two CTAs do not fit an SM");
 
@@ -573,7 +574,9 @@ size_t mx_matmul_smem(int n_rows, int n_out, int width, int sms, int* cluster) {
 
 // More than 128 rows go to pairs of CTAs where those are expected to take less: about 0.17 us a piece of their 256 x 256
 // tiles against 0.12 of a CTA's 128 x 128 ones, and 1.7 us a call more (640 rows of 7680 to 4096 features: 17.5 us by CTAs,
-// 15.5 by pairs; 256 of 2048 to 4096: 5.6 and 8.0; 1500 of 7680 to 12288: 62 and 48).
+// 15.5 by pairs; 256 of 2048 to 4096: 5.4 and 8.2; 1500 of 7680 to 12288: 62 and 48; 640 of 2880 to 5120: 9.7 and 9.8).  The
+// results' way out, which nothing hides at one tile a pair, is in neither side: 896 rows of 7680 to 2880 features with fp32
+// addends take 19.2 us by CTAs and 17.1 by pairs, where 14.4 and 11.9 are expected.
 cudaError_t launch_mx_matmul(const MxMatmulArgs& a, pe_dtype dt, int sms, cudaStream_t s) {
   const MxPlan p = plan_mx(a, sms);
   if (a.n_rows > kMxPiece) {
